@@ -237,6 +237,107 @@ int moe_route_qb_noalloc(int T, int n, int k, int qb_sweeps,
 
 /*
  * ---------------------------------------------------------------------------
+ * Router training: balance loss, per-expert counts and the logits' gradient.
+ *
+ * A batch of T tokens is cut into S sequences, seq_offsets [S + 1] (int32
+ * device, non-decreasing from 0 to T; NULL = one sequence of all T tokens).
+ * token_mask [T] (device bytes, 0 = padding, not counted; NULL = all valid).
+ * idx [T, k] int32 device: the experts each token was routed to, distinct; an
+ * entry outside [0, n) stands for no route.  logits [T, n], row stride ld >= n
+ * elements, QBMOE_F32 or QBMOE_BF16 (logit_dtype).
+ *
+ * With s = sigmoid(logit clamped to [-80, 80]) (the router's score), the share
+ * p[t][j] = s[t][j] / sum_l s[t][l], and over the valid tokens V_q of sequence q
+ * (T_q of them):
+ *   counts[q][j] = routes of V_q to expert j
+ *   probs[q][j]  = mean over V_q of p[t][j]
+ *   loss[q]      = n / (k T_q) * sum_j counts[q][j] probs[q][j]
+ * loss[q] is 1 when every expert has the same count or the same mean share;
+ * a sequence without valid tokens has zeros throughout.  (The auxiliary loss
+ * of sigmoid routers, per sequence; the caller weighs and sums loss[q].)
+ *
+ * moe_balance_loss writes loss [S] fp32, counts [S, n] int32, probs [S, n]
+ * fp32 and tokens [S] int32 (T_q).  workspace: device, 256-byte aligned,
+ * >= qbmoe_balance_workspace_bytes(T, n, S) bytes.  Sums are fp32 in a fixed
+ * order: bit-reproducible.
+ *
+ * moe_router_backward writes dlogits [T, n] (row stride ldg, of logit_dtype),
+ * the gradient of
+ *   sum_t sum_i dw[t][i] w[t][i] + sum_q dloss[q] loss[q]
+ * where w[t][i] = s[t][idx_i] / sum_l s[t][idx_l] are the mixture weights and
+ * the routes (idx, counts) are constants.  dw [T, k] fp32 or NULL (no such
+ * term); dloss [S] fp32 with counts and tokens as moe_balance_loss wrote them,
+ * or all three NULL.  Padding tokens, and logits outside [-80, 80], get 0.
+ * dlogits may equal logits (same stride).
+ *
+ * 1 <= T, 2 <= n <= QBMOE_MAX_EXPERTS, 1 <= k <= min(n, QBMOE_MAX_TOPK),
+ * 1 <= S.  Device pointers are aligned to their element type only: rows of a
+ * 16-byte-aligned base and stride are read as vectors.
+ */
+size_t qbmoe_balance_workspace_bytes(int T, int n, int S);
+int moe_balance_loss(int T, int n, int k, int S, int logit_dtype, const void* logits, long long ld,
+                     const int32_t* idx, const int32_t* seq_offsets, const uint8_t* token_mask,
+                     float* loss, int32_t* counts, float* probs, int32_t* tokens,
+                     void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void* logits, long long ld,
+                        const int32_t* idx, const int32_t* seq_offsets, const uint8_t* token_mask,
+                        const float* dw, const float* dloss, const int32_t* counts, const int32_t* tokens,
+                        void* dlogits, long long ldg, qbmoe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * MXFP4 tensors: quantisation, product and its gradients.
+ *
+ * An MXFP4 tensor [rows, K] is codes [rows, K/2] u8 (E2M1, element 2i in the
+ * low nibble) and scales [rows, K/32] u8 (E8M0: 2^(byte - 127)), both
+ * contiguous: the layout of the layer's routed-expert weights (qbmoe_weights).
+ * K is a multiple of 32.
+ *
+ * moe_mxfp4_quantize: x [rows, K] (QBMOE_F32 or QBMOE_BF16, row stride ldx
+ * elements) to codes and scales.  Per 32 elements, e = floor(log2 max|x|) - 2
+ * (at least -127; -127 for a block of zeros), code = x * 2^-e rounded to
+ * nearest, ties to even, magnitudes above 6 to 6; the sign of zero is kept.  A block that
+ * holds an infinity or a NaN gets the scale byte 0xFF (NaN) and zero codes.
+ * values (NULL if not wanted): [rows, K] contiguous, of x's type, what the codes
+ * stand for, exact in either type (NaN throughout a 0xFF block).
+ * x, codes and values 16-byte aligned, ldx * element size a multiple of 16.
+ *
+ * Grouped rows: R rows in expert order, offsets [E + 1] int32 device,
+ * non-decreasing from 0 to R: rows offsets[e] .. offsets[e+1] - 1 belong to
+ * expert e (an expert may have none).  offsets NULL: E = 1, all rows.
+ * Rows that no expert owns are not written.  0 <= R, 1 <= E <=
+ * QBMOE_MAX_EXPERTS, N a multiple of 8.
+ *
+ * moe_mxfp4_matmul:  y[r][f] = sum_k x[r][k] w[e(r)][f][k], x and w MXFP4
+ *   ([R, K] and [E, N, K]), y [R, N] bf16, row stride ldy elements.
+ * moe_mxfp4_dgrad:   dx[r][k] = sum_f dy[r][f] w[e(r)][f][k], dy [R, N] bf16
+ *   (row stride lddy), dx [R, K] bf16 (row stride lddx).
+ * moe_mxfp4_wgrad:   dw[e][f][k] = sum over e's rows of dy[r][f] x[r][k],
+ *   dw [E, N, K] contiguous, QBMOE_F32 or QBMOE_BF16; zeros for an expert
+ *   without rows.
+ * The gradients are those of the product for the values x and w stand for; a
+ * trainer that quantises its own activations and weights passes them straight
+ * through the rounding.  Products are exact, sums fp32, each output rounded
+ * once.  All pointers 16-byte aligned, strides multiples of 8 elements.
+ * workspace: device, 256-byte aligned, >= qbmoe_mxfp4_workspace_bytes(R, E, N,
+ * K) bytes (one size serves the three calls).  A bounded wait that expires is
+ * reported by qbmoe_status(NULL, stream).
+ */
+int moe_mxfp4_quantize(long long rows, int K, int x_dtype, const void* x, long long ldx, uint8_t* codes,
+                       uint8_t* scales, void* values, qbmoe_stream_t stream);
+size_t qbmoe_mxfp4_workspace_bytes(int R, int E, int N, int K);
+int moe_mxfp4_matmul(int R, int E, int N, int K, const uint8_t* x_codes, const uint8_t* x_scales,
+                     const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets, void* y, long long ldy,
+                     void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,
+                    const uint8_t* w_scales, const int32_t* offsets, void* dx, long long lddx,
+                    void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
+                    const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
+                    void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Layer context.
  */
 typedef struct {

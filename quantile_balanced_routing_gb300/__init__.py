@@ -5,12 +5,15 @@ kernels.  PyTorch provides device memory and streams.  There is no CPU
 fallback: if ``libqbmoe.so`` is missing, loading it raises.
 
 The C entry points are exposed under their C names (``moe_route_qb``,
-``moe_latent_forward``, ``qbmoe_*``) taking plain integers/pointers, plus two
-torch conveniences, :func:`route_qb` and :class:`LatentMoE`, that allocate
-outputs with torch and call them.
+``moe_latent_forward``, ``qbmoe_*``) taking plain integers/pointers, plus
+torch conveniences that allocate outputs with torch and call them:
+:func:`route_qb` and :class:`LatentMoE`, the router's training side
+(:func:`balance_loss`, :func:`router_backward`) and MXFP4 tensors
+(:func:`mxfp4_quantize`, :func:`mxfp4_matmul`, :func:`mxfp4_matmul_backward`).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -122,6 +125,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qbmoe_uses_tensor_cores.restype = i
     lib.qbmoe_mma_probe.argtypes = [i, i, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_double)]
     lib.qbmoe_mma_probe.restype = i
+    ll = ctypes.c_longlong
+    lib.qbmoe_balance_workspace_bytes.argtypes = [i, i, i]
+    lib.qbmoe_balance_workspace_bytes.restype = sz
+    lib.moe_balance_loss.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_router_backward.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, ll, vp]
+    lib.moe_mxfp4_quantize.argtypes = [ll, i, i, vp, ll, vp, vp, vp, vp]
+    lib.qbmoe_mxfp4_workspace_bytes.argtypes = [i, i, i, i]
+    lib.qbmoe_mxfp4_workspace_bytes.restype = sz
+    lib.moe_mxfp4_matmul.argtypes = [i, i, i, i, vp, vp, vp, vp, vp, vp, ll, vp, sz, vp]
+    lib.moe_mxfp4_dgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, vp, ll, vp, sz, vp]
+    lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp, sz, vp]
+    for nm in ("moe_balance_loss", "moe_router_backward", "moe_mxfp4_quantize", "moe_mxfp4_matmul",
+               "moe_mxfp4_dgrad", "moe_mxfp4_wgrad"):
+        getattr(lib, nm).restype = i
     lib.qbmoe_strerror.argtypes = [i]
     lib.qbmoe_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -148,6 +165,21 @@ def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream or None
+
+
+def _allocating_on(stream):
+    """Allocate on the stream a call runs on, so that the memory is not reused
+    before that stream is done with it."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _check_device(what, *tensors):
+    """Every given tensor lives on the current CUDA device."""
+    import torch
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+            raise QbmoeError(QBMOE_EINVAL, f"{what}: tensors are on the current CUDA device (got {t.device})")
 
 
 # ---------------------------------------------------------------------------
@@ -375,3 +407,7 @@ class LatentMoE:
     @property
     def uses_tensor_cores(self) -> bool:
         return bool(self.lib.qbmoe_uses_tensor_cores(self.ctx))
+
+
+from .balance import BalanceLoss, balance_loss, router_backward  # noqa: E402
+from .mxfp4 import Mxfp4, mxfp4_matmul, mxfp4_matmul_backward, mxfp4_quantize  # noqa: E402

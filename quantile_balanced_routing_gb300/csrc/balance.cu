@@ -1,0 +1,464 @@
+// Router training (C ABI: moe_balance_loss, moe_router_backward): the balance
+// loss of a routed batch with its per-expert counts, and the gradient of the
+// router logits from the mixture weights and from that loss.
+//
+// Notation: s = sigmoid(x), c = 1 - s, S_t = sum_j s_tj, p_tj = s_tj / S_t.
+// Both kernels make one pass over the [T, n] logits with one warp per token:
+// a lane keeps n / 32 of the row's scores in registers, so S_t (and, in the
+// backward pass, sum_j f_j p_tj) is a warp reduction and no row is read twice.
+#include "common.cuh"
+
+#include <climits>
+
+namespace {
+
+using namespace qb;
+
+constexpr int kBalWarps = 8;
+constexpr int kBalThreads = 32 * kBalWarps;
+constexpr int kMaxPerLane = QBMOE_MAX_EXPERTS / 32;   // 32 logits of a row per lane
+constexpr float kLogitLimit = 80.0f;
+
+// s = sigmoid(x) and c = 1 - s for x clamped to [-80, 80]; c = e^-x s keeps
+// its relative precision where s rounds to 1.  The hardware exponential and
+// reciprocal: relative error about 2^-22, far below the gradients' use.
+QB_DEV void score_pair(float x, float& s, float& c) {
+    x = x < -kLogitLimit ? -kLogitLimit : x > kLogitLimit ? kLogitLimit : x;   // a NaN stays one
+    const float e = __expf(-x);
+    s = __frcp_rn(1.0f + e);
+    c = e * s;
+}
+
+template <typename T> struct Vec;   // elements of T in 16 bytes
+template <> struct Vec<float> { static constexpr int n = 4; };
+template <> struct Vec<__nv_bfloat16> { static constexpr int n = 8; };
+
+// This lane's elements of a row: element v of group i is column (32 i + lane) V + v.
+template <typename T, int V>
+QB_DEV void load_row(const T* __restrict__ row, int n, int lane, float (&x)[kMaxPerLane]) {
+#pragma unroll
+    for (int i = 0; i < kMaxPerLane / V; ++i) {
+        const int j = (32 * i + lane) * V;
+        if (V == 1) {
+            x[i] = j < n ? to_f32<T>(row[j]) : 0.0f;
+        } else if (j < n) {   // n is a multiple of V here
+            const uint4 u = *reinterpret_cast<const uint4*>(row + j);
+            const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[i * V + v] = to_f32<T>(e[v]);
+        }
+    }
+}
+
+QB_DEV float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Largest q with off[q] <= t (off[0] <= t assumed).
+QB_DEV int find_seq(const int32_t* off, int S, int t) {
+    int lo = 0, hi = S;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(off + mid) <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  Chunk c of `chunk` tokens is one CTA's; the part of it that lies
+// in sequence q is summed into slot c + q (along the chunks and sequences that
+// overlap, c + q takes each value once), so no sum needs an atomic and the
+// order is fixed.
+// ---------------------------------------------------------------------------
+struct BalanceArgs {
+    int T, n, k, S, chunk, nchunk;
+    long long ld;
+    const void* logits;
+    const int32_t* idx;
+    const int32_t* seq;
+    const uint8_t* mask;
+    float* part_p;     // [nchunk + S, n] sums of p
+    int32_t* part_c;   // [nchunk + S, n] routes
+    int32_t* part_t;   // [nchunk + S] valid tokens
+    unsigned* ticket;  // [S]
+    float* loss_part;  // [S, ceil(n / 32)]
+    float* loss;
+    int32_t* counts;
+    float* probs;
+    int32_t* tokens;
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kBalThreads) k_balance_partial(const BalanceArgs a) {
+    extern __shared__ float sm[];
+    float* red = sm;                                              // [kBalWarps][n]
+    int* cnt = reinterpret_cast<int*>(sm + kBalWarps * a.n);      // [n]
+    __shared__ int valid[kBalWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T* logits = static_cast<const T*>(a.logits);
+    const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
+    if (blockIdx.x == 0)
+        for (int q = threadIdx.x; q < a.S; q += kBalThreads) a.ticket[q] = 0;
+    int q = a.seq ? find_seq(a.seq, a.S, c0) : 0;
+    for (int t0 = c0; t0 < c1; ++q) {
+        const int t1 = a.seq && q + 1 < a.S ? min(c1, max(t0, __ldg(a.seq + q + 1))) : c1;
+        for (int j = threadIdx.x; j < a.n; j += kBalThreads) cnt[j] = 0;
+        __syncthreads();
+        float acc[kMaxPerLane] = {};
+        int nv = 0;
+        for (int t = t0 + warp; t < t1; t += kBalWarps) {
+            if (a.mask && !__ldg(a.mask + t)) continue;
+            ++nv;
+            float x[kMaxPerLane];
+            load_row<T, V>(logits + (long long)t * a.ld, a.n, lane, x);
+            if (lane < a.k) {
+                const int id = __ldg(a.idx + (long long)t * a.k + lane);
+                if ((unsigned)id < (unsigned)a.n) atomicAdd(cnt + id, 1);
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kMaxPerLane / V; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float s = 0.0f, c;
+                    if ((32 * i + lane) * V < a.n) score_pair(x[i * V + v], s, c);
+                    x[i * V + v] = s;
+                    sum += s;
+                }
+            const float inv = 1.0f / warp_sum(sum);
+#pragma unroll
+            for (int i = 0; i < kMaxPerLane; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxPerLane / V; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j = (32 * i + lane) * V + v;
+                if (j < a.n) red[warp * a.n + j] = acc[i * V + v];
+            }
+        if (lane == 0) valid[warp] = nv;
+        __syncthreads();
+        const long long slot = blockIdx.x + q;
+        for (int j = threadIdx.x; j < a.n; j += kBalThreads) {
+            float p = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kBalWarps; ++w) p += red[w * a.n + j];
+            a.part_p[slot * a.n + j] = p;
+            a.part_c[slot * a.n + j] = cnt[j];
+        }
+        if (threadIdx.x == 0) {
+            int tv = 0;
+            for (int w = 0; w < kBalWarps; ++w) tv += valid[w];
+            a.part_t[slot] = tv;
+        }
+        __syncthreads();
+        t0 = t1;
+    }
+}
+
+// CTA (b, q): experts 32 b .. 32 b + 31 of sequence q over its slots; the
+// sequence's last CTA adds up its loss.
+__global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArgs a) {
+    __shared__ float sp[kBalWarps][33];
+    __shared__ int sc[kBalWarps][33];
+    __shared__ int st[kBalWarps];
+    __shared__ bool last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = blockIdx.y, j = blockIdx.x * 32 + lane;
+    const int o0 = a.seq ? min(max(__ldg(a.seq + q), 0), a.T) : 0;
+    const int o1 = a.seq ? min(max(__ldg(a.seq + q + 1), o0), a.T) : a.T;
+    const int f = o0 / a.chunk, g = o1 > o0 ? (o1 - 1) / a.chunk + 1 : f;   // chunks [f, g)
+    float p = 0.0f;
+    int c = 0, t = 0;
+    for (int u = f + warp; u < g; u += kBalWarps) {
+        const long long slot = u + q;
+        if (j < a.n) {
+            p += a.part_p[slot * a.n + j];
+            c += a.part_c[slot * a.n + j];
+        }
+        t += a.part_t[slot];
+    }
+    sp[warp][lane] = p;
+    sc[warp][lane] = c;
+    if (lane == 0) st[warp] = t;
+    __syncthreads();
+    if (warp == 0) {
+        p = 0.0f, c = 0, t = 0;
+        for (int w = 0; w < kBalWarps; ++w) p += sp[w][lane], c += sc[w][lane], t += st[w];
+        const float inv_t = 1.0f / fmaxf((float)t, 1.0f);
+        p *= inv_t;
+        if (j < a.n) {
+            a.probs[(long long)q * a.n + j] = p;
+            a.counts[(long long)q * a.n + j] = c;
+        }
+        const float l = warp_sum(j < a.n ? (float)c * p : 0.0f) * ((float)a.n * inv_t / (float)a.k);
+        if (lane == 0) {
+            if (blockIdx.x == 0) a.tokens[q] = t;
+            a.loss_part[(long long)q * gridDim.x + blockIdx.x] = l;
+            __threadfence();
+            last = atomicAdd(a.ticket + q, 1u) == gridDim.x - 1;
+        }
+        __syncwarp();
+        if (last) {
+            __threadfence();
+            const float v = lane < (int)gridDim.x
+                                ? *(volatile float*)(a.loss_part + (long long)q * gridDim.x + lane) : 0.0f;
+            const float total = warp_sum(v);   // at most 32 CTAs a sequence
+            if (lane == 0) a.loss[q] = total;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  With f_j = dloss n counts_j / (k T_q^2) and D = sum_j f_j p_j:
+//   dx_j = p_j c_j (f_j - D)                             balance loss
+//        + w_i c_j (dw_i - sum_l dw_l w_l)  for j = idx_i   mixture weights
+// ---------------------------------------------------------------------------
+struct RouterGradArgs {
+    int T, n, k, S, per_warp;
+    long long ld, ldg;
+    const void* logits;
+    const int32_t* idx;
+    const int32_t* seq;
+    const uint8_t* mask;
+    const float* dw;
+    const float* dloss;
+    const int32_t* counts;
+    const int32_t* tokens;
+    void* out;
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kBalThreads) k_router_backward(const RouterGradArgs a) {
+    extern __shared__ float sm[];   // [kBalWarps][n]: the row's mixture-weight terms, zero between tokens
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* sp = sm + warp * a.n;
+    for (int j = lane; j < a.n; j += 32) sp[j] = 0.0f;
+    __syncwarp();
+    const long long first = ((long long)blockIdx.x * kBalWarps + warp) * a.per_warp;
+    const int t1 = (int)min((long long)a.T, first + a.per_warp);
+    float f[kMaxPerLane] = {};
+    int q = -1, q_end = INT_MIN;
+    for (int t = (int)min(first, (long long)a.T); t < t1; ++t) {
+        const T* row = static_cast<const T*>(a.logits) + (long long)t * a.ld;
+        T* out = static_cast<T*>(a.out) + (long long)t * a.ldg;
+        const bool live = !a.mask || __ldg(a.mask + t);
+        float x[kMaxPerLane];
+        if (live) {
+            if (a.dloss && t >= q_end) {   // the next sequence's frequencies
+                q = a.seq ? find_seq(a.seq, a.S, t) : 0;
+                q_end = a.seq && q + 1 < a.S ? __ldg(a.seq + q + 1) : INT_MAX;
+                const float tq = fmaxf((float)__ldg(a.tokens + q), 1.0f);
+                const float scale = __ldg(a.dloss + q) * ((float)a.n / ((float)a.k * tq)) / tq;
+#pragma unroll
+                for (int i = 0; i < kMaxPerLane / V; ++i)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int j = (32 * i + lane) * V + v;
+                        f[i * V + v] = j < a.n ? scale * (float)__ldg(a.counts + (long long)q * a.n + j) : 0.0f;
+                    }
+            }
+            load_row<T, V>(row, a.n, lane, x);
+            if (a.dw) {
+                float s = 0.0f, c = 0.0f, d = 0.0f;
+                int id = -1;
+                if (lane < a.k) {
+                    id = __ldg(a.idx + (long long)t * a.k + lane);
+                    if ((unsigned)id < (unsigned)a.n) {
+                        score_pair(to_f32<T>(row[id]), s, c);
+                        d = __ldg(a.dw + (long long)t * a.k + lane);
+                    } else {
+                        id = -1;
+                    }
+                }
+                const float sum = warp_sum(s);
+                const float w = sum > 0.0f ? s / sum : 0.0f;
+                const float dot = warp_sum(d * w);
+                if (id >= 0) atomicAdd(sp + id, w * c * (d - dot));
+                __syncwarp();
+            }
+        }
+        float sum = 0.0f, dot = 0.0f;
+        float g[kMaxPerLane];   // c, then the gradient
+#pragma unroll
+        for (int i = 0; i < kMaxPerLane / V; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = i * V + v;
+                float s = 0.0f, c = 0.0f;
+                if (live && (32 * i + lane) * V < a.n) {
+                    score_pair(x[e], s, c);
+                    if (fabsf(x[e]) > kLogitLimit) c = 0.0f;   // clamped: no slope
+                }
+                x[e] = s;
+                g[e] = c;
+                sum += s;
+                dot = fmaf(f[e], s, dot);
+            }
+        if (live) {
+            const float inv = 1.0f / warp_sum(sum);
+            const float D = warp_sum(dot) * inv;
+#pragma unroll
+            for (int i = 0; i < kMaxPerLane / V; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int e = i * V + v, j = (32 * i + lane) * V + v;
+                    // a clamped logit gets 0 from the mixture weights too
+                    const float m = a.dw && j < a.n ? (g[e] == 0.0f ? 0.0f : sp[j]) : 0.0f;
+                    g[e] = fmaf(x[e] * inv * g[e], f[e] - D, m);
+                }
+            if (a.dw) {
+                __syncwarp();
+                if (lane < a.k) {
+                    const int id = __ldg(a.idx + (long long)t * a.k + lane);
+                    if ((unsigned)id < (unsigned)a.n) sp[id] = 0.0f;
+                }
+                __syncwarp();
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxPerLane / V; ++i) {
+            const int j = (32 * i + lane) * V;
+            if (j >= a.n) continue;
+            if (V == 1) {
+                out[j] = from_f32<T>(g[i]);
+            } else {
+                uint4 u;
+                T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] = from_f32<T>(g[i * V + v]);
+                *reinterpret_cast<uint4*>(out + j) = u;
+            }
+        }
+    }
+}
+
+// Tokens per forward CTA: about two CTAs a SM at full size, one token a warp at least.
+int balance_chunk(int T) {
+    const int per = (T + 303) / 304;
+    return ((per + kBalWarps - 1) / kBalWarps) * kBalWarps;
+}
+
+struct BalanceLayout {
+    size_t part_p, part_c, part_t, ticket, loss_part, total;
+};
+BalanceLayout balance_layout(int T, int n, int S) {
+    const size_t slots = (size_t)((T + balance_chunk(T) - 1) / balance_chunk(T)) + S;
+    BalanceLayout l;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = qbh::align_up(off + bytes, 256);
+        return o;
+    };
+    l.part_p = take(slots * n * 4);
+    l.part_c = take(slots * n * 4);
+    l.part_t = take(slots * 4);
+    l.ticket = take((size_t)S * 4);
+    l.loss_part = take((size_t)S * ((n + 31) / 32) * 4);
+    l.total = off;
+    return l;
+}
+
+bool router_sizes_ok(int T, int n, int k, int S, int dtype, long long ld) {
+    return T >= 1 && n >= 2 && n <= QBMOE_MAX_EXPERTS && k >= 1 && k <= n && k <= QBMOE_MAX_TOPK && S >= 1 &&
+           S <= 65535 && (dtype == QBMOE_F32 || dtype == QBMOE_BF16) && ld >= n;
+}
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Rows are read as 16-byte vectors when every row starts on one.
+template <typename T>
+bool vector_rows(int n, const void* p, long long ld) {
+    return n % Vec<T>::n == 0 && ld % Vec<T>::n == 0 && qbh::aligned16(p);
+}
+
+}  // namespace
+
+extern "C" size_t qbmoe_balance_workspace_bytes(int T, int n, int S) {
+    if (T < 1 || n < 2 || n > QBMOE_MAX_EXPERTS || S < 1 || S > 65535) return 0;
+    return balance_layout(T, n, S).total;
+}
+
+extern "C" int moe_balance_loss(int T, int n, int k, int S, int logit_dtype, const void* logits, long long ld,
+                                const int32_t* idx, const int32_t* seq_offsets, const uint8_t* token_mask,
+                                float* loss, int32_t* counts, float* probs, int32_t* tokens, void* workspace,
+                                size_t workspace_bytes, qbmoe_stream_t stream) {
+    if (!router_sizes_ok(T, n, k, S, logit_dtype, ld)) return QBMOE_EINVAL;
+    if (!logits || !idx || !loss || !counts || !probs || !tokens || !workspace) return QBMOE_EINVAL;
+    if (!seq_offsets && S != 1) return QBMOE_EINVAL;
+    const size_t es = logit_dtype == QBMOE_BF16 ? 2 : 4;
+    if (!aligned_to(logits, es)) return QBMOE_EINVAL;
+    for (const void* p : {(const void*)idx, (const void*)seq_offsets, (const void*)loss, (const void*)counts,
+                          (const void*)probs, (const void*)tokens})
+        if (p && !aligned_to(p, 4)) return QBMOE_EINVAL;
+    if (!aligned_to(workspace, 256)) return QBMOE_EINVAL;
+    const BalanceLayout l = balance_layout(T, n, S);
+    if (workspace_bytes < l.total) return QBMOE_EWORKSPACE;
+    int rc = qbh::device_init();
+    if (rc) return rc;
+    char* ws = static_cast<char*>(workspace);
+    BalanceArgs a{};
+    a.T = T; a.n = n; a.k = k; a.S = S; a.ld = ld;
+    a.chunk = balance_chunk(T);
+    a.nchunk = (T + a.chunk - 1) / a.chunk;
+    a.logits = logits; a.idx = idx; a.seq = seq_offsets; a.mask = token_mask;
+    a.part_p = reinterpret_cast<float*>(ws + l.part_p);
+    a.part_c = reinterpret_cast<int32_t*>(ws + l.part_c);
+    a.part_t = reinterpret_cast<int32_t*>(ws + l.part_t);
+    a.ticket = reinterpret_cast<unsigned*>(ws + l.ticket);
+    a.loss_part = reinterpret_cast<float*>(ws + l.loss_part);
+    a.loss = loss; a.counts = counts; a.probs = probs; a.tokens = tokens;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t smem = (size_t)(kBalWarps + 1) * n * 4;   // at most 36 KB
+    if (logit_dtype == QBMOE_F32) {
+        if (vector_rows<float>(n, logits, ld)) k_balance_partial<float, 4><<<a.nchunk, kBalThreads, smem, s>>>(a);
+        else k_balance_partial<float, 1><<<a.nchunk, kBalThreads, smem, s>>>(a);
+    } else {
+        if (vector_rows<__nv_bfloat16>(n, logits, ld))
+            k_balance_partial<__nv_bfloat16, 8><<<a.nchunk, kBalThreads, smem, s>>>(a);
+        else k_balance_partial<__nv_bfloat16, 1><<<a.nchunk, kBalThreads, smem, s>>>(a);
+    }
+    if ((rc = qbh::cuda_err(cudaGetLastError()))) return rc;
+    k_balance_finish<<<dim3((n + 31) / 32, S), kBalThreads, 0, s>>>(a);
+    return qbh::cuda_err(cudaGetLastError());
+}
+
+extern "C" int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void* logits, long long ld,
+                                   const int32_t* idx, const int32_t* seq_offsets, const uint8_t* token_mask,
+                                   const float* dw, const float* dloss, const int32_t* counts,
+                                   const int32_t* tokens, void* dlogits, long long ldg, qbmoe_stream_t stream) {
+    if (!router_sizes_ok(T, n, k, S, logit_dtype, ld) || ldg < n) return QBMOE_EINVAL;
+    if (!logits || !idx || !dlogits || (!dw && !dloss)) return QBMOE_EINVAL;
+    if (dloss ? (!counts || !tokens) : (counts || tokens)) return QBMOE_EINVAL;
+    if (!seq_offsets && S != 1) return QBMOE_EINVAL;
+    if (dlogits == logits && ldg != ld) return QBMOE_EINVAL;
+    const size_t es = logit_dtype == QBMOE_BF16 ? 2 : 4;
+    if (!aligned_to(logits, es) || !aligned_to(dlogits, es)) return QBMOE_EINVAL;
+    for (const void* p : {(const void*)idx, (const void*)seq_offsets, (const void*)dw, (const void*)dloss,
+                          (const void*)counts, (const void*)tokens})
+        if (p && !aligned_to(p, 4)) return QBMOE_EINVAL;
+    int rc = qbh::device_init();
+    if (rc) return rc;
+    RouterGradArgs a{};
+    a.T = T; a.n = n; a.k = k; a.S = S; a.ld = ld; a.ldg = ldg;
+    a.logits = logits; a.idx = idx; a.seq = seq_offsets; a.mask = token_mask;
+    a.dw = dw; a.dloss = dloss; a.counts = counts; a.tokens = tokens; a.out = dlogits;
+    // consecutive tokens per warp, so that a sequence's frequencies stay in
+    // registers: about two CTAs a SM
+    a.per_warp = (T + 304 * kBalWarps - 1) / (304 * kBalWarps);
+    const int grid = (int)(((long long)T + (long long)a.per_warp * kBalWarps - 1) / ((long long)a.per_warp * kBalWarps));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t smem = (size_t)kBalWarps * n * 4;
+    if (logit_dtype == QBMOE_F32) {
+        if (vector_rows<float>(n, logits, ld) && vector_rows<float>(n, dlogits, ldg))
+            k_router_backward<float, 4><<<grid, kBalThreads, smem, s>>>(a);
+        else k_router_backward<float, 1><<<grid, kBalThreads, smem, s>>>(a);
+    } else {
+        if (vector_rows<__nv_bfloat16>(n, logits, ld) && vector_rows<__nv_bfloat16>(n, dlogits, ldg))
+            k_router_backward<__nv_bfloat16, 8><<<grid, kBalThreads, smem, s>>>(a);
+        else k_router_backward<__nv_bfloat16, 1><<<grid, kBalThreads, smem, s>>>(a);
+    }
+    return qbh::cuda_err(cudaGetLastError());
+}

@@ -1,0 +1,329 @@
+// MXFP4 tensors (C ABI: moe_mxfp4_*): quantisation of rows, the product of
+// MXFP4 rows with MXFP4 weights, and the product's gradients.
+//
+// [K3-width] 延伸解读 on deployment: routed-expert weights in MXFP4 with
+// quantisation-aware post-training.  OCP MX: E2M1 elements, one E8M0 scale per
+// 32 along K.
+#include "common.cuh"
+
+namespace {
+
+using namespace qb;
+
+// ---------------------------------------------------------------------------
+// Quantisation.  Four consecutive lanes hold one block of 32 (8 elements each);
+// the block's largest magnitude is two shuffles away.
+// ---------------------------------------------------------------------------
+constexpr int kQThreads = 256;
+
+// 8 elements of a row from 16-byte loads.
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    static QB_DEV void load(const float* p, float (&x)[8]) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    static QB_DEV void store(float* p, const float (&x)[8]) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+template <> struct Eight<__nv_bfloat16> {
+    static QB_DEV void load(const __nv_bfloat16* p, float (&x)[8]) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static QB_DEV void store(__nv_bfloat16* p, const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // exact: at most two significant bits
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Two floats to a byte of E2M1 codes (lo in the low nibble): round to nearest,
+// ties to even, magnitudes above 6 to 6.
+QB_DEV uint32_t e2m1_pair(float lo, float hi) {
+    uint16_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
+        : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// E2M1 code -> value.
+QB_DEV float e2m1_value(uint32_t code) {
+    const uint32_t m = code & 7u;
+    const float v = m < 4u ? 0.5f * (float)m : (m < 6u ? (float)m - 2.0f : 2.0f * (float)m - 8.0f);
+    return (code & 8u) ? -v : v;
+}
+
+// E8M0 byte -> scale (0xFF: NaN).
+QB_DEV float e8m0_value(uint32_t b) {
+    return b == 0xffu ? __int_as_float(0x7fffffff) : __int_as_float(b ? (int)(b << 23) : 0x00400000);
+}
+
+template <typename T, bool kValues>
+__global__ void __launch_bounds__(kQThreads) k_mxfp4_quantize(long long rows, int K, const T* __restrict__ x,
+                                                              long long ldx, uint8_t* __restrict__ codes,
+                                                              uint8_t* __restrict__ scales, T* __restrict__ values) {
+    const int per_row = K / 8;   // a multiple of 4: the lanes of a block share its fate
+    const long long items = rows * per_row;
+    for (long long it = (long long)blockIdx.x * kQThreads + threadIdx.x; it < items;
+         it += (long long)gridDim.x * kQThreads) {
+        const long long r = it / per_row;
+        const int k = (int)(it - r * per_row) * 8;
+        float v[8];
+        Eight<T>::load(x + r * ldx + k, v);
+        uint32_t m = 0;   // largest magnitude as bits: an infinity or a NaN is above every finite number
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        const uint32_t group = 0xfu << (threadIdx.x & 28);
+        m = max(m, __shfl_xor_sync(group, m, 1));
+        m = max(m, __shfl_xor_sync(group, m, 2));
+        // a subnormal maximum has exponent field 0: below 2^-126, so e < -127 and the clamp holds
+        const int e = max((int)(m >> 23) - 127 - 2, -127);
+        const bool bad = m >= 0x7f800000u;
+        const float inv = __int_as_float((127 - e) << 23);   // 2^-e: -127 <= e <= 125 (not used when bad)
+        uint32_t q = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q |= e2m1_pair(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+        if (bad) q = 0;
+        reinterpret_cast<uint32_t*>(codes)[it] = q;
+        const uint32_t sb = bad ? 0xffu : (uint32_t)(e + 127);
+        if ((threadIdx.x & 3) == 0) scales[it >> 2] = (uint8_t)sb;
+        if (kValues) {
+            const float sc = e8m0_value(sb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = e2m1_value(q >> (4 * i)) * sc;
+            Eight<T>::store(values + r * K + k, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Products on CUDA cores, 64 x 64 output tiles.  A grouped tile belongs to one
+// expert; its place is found by walking the offsets.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 64, kStep = 32, kThreads = 256;
+
+struct Group {
+    int e, row0, row1;   // expert, tile rows [row0, row1)
+};
+QB_DEV bool find_tile(const int32_t* offsets, int E, int R, int tile, Group& g) {
+    int seen = 0;
+    for (int e = 0; e < E; ++e) {
+        const int a = offsets ? min(max(__ldg(offsets + e), 0), R) : 0;
+        const int b = offsets ? min(max(__ldg(offsets + e + 1), a), R) : R;
+        const int nt = (b - a + kTile - 1) / kTile;
+        if (tile < seen + nt) {
+            g.e = e;
+            g.row0 = a + (tile - seen) * kTile;
+            g.row1 = min(b, g.row0 + kTile);
+            return true;
+        }
+        seen += nt;
+    }
+    return false;
+}
+
+QB_DEV float mx_at(const uint8_t* codes, const uint8_t* scales, long long row, int K, int k) {
+    const uint32_t b = __ldg(codes + row * (K / 2) + k / 2);
+    return e2m1_value(k & 1 ? b >> 4 : b) * e8m0_value(__ldg(scales + row * (K / 32) + k / 32));
+}
+
+// acc[i][j] += sum_c a[c][ty + 16 i] b[c][tx + 16 j] over a staged step.
+QB_DEV void step_product(const float (&a)[kStep][kTile + 1], const float (&b)[kStep][kTile + 1], int n,
+                         float (&acc)[4][4]) {
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    for (int c = 0; c < n; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[c][ty + 16 * i], b[c][tx + 16 * j], acc[i][j]);
+}
+
+__global__ void __launch_bounds__(kThreads) k_matmul(int R, int E, int N, int K, const uint8_t* xc, const uint8_t* xs,
+                                                     const uint8_t* wc, const uint8_t* ws, const int32_t* offsets,
+                                                     __nv_bfloat16* y, long long ldy) {
+    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
+    Group g;
+    if (!find_tile(offsets, E, R, blockIdx.y, g)) return;
+    const int f0 = blockIdx.x * kTile;
+    float acc[4][4] = {};
+    for (int k0 = 0; k0 < K; k0 += kStep) {
+        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
+            const int r = i / kStep, c = i % kStep;
+            sa[c][r] = g.row0 + r < g.row1 ? mx_at(xc, xs, g.row0 + r, K, k0 + c) : 0.0f;
+            sb[c][r] = f0 + r < N ? mx_at(wc, ws, (long long)g.e * N + f0 + r, K, k0 + c) : 0.0f;
+        }
+        __syncthreads();
+        step_product(sa, sb, kStep, acc);
+        __syncthreads();
+    }
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int r = g.row0 + ty + 16 * i, f = f0 + tx + 16 * j;
+            if (r < g.row1 && f < N) y[(long long)r * ldy + f] = __float2bfloat16_rn(acc[i][j]);
+        }
+}
+
+__global__ void __launch_bounds__(kThreads) k_dgrad(int R, int E, int N, int K, const __nv_bfloat16* dy,
+                                                    long long lddy, const uint8_t* wc, const uint8_t* ws,
+                                                    const int32_t* offsets, __nv_bfloat16* dx, long long lddx) {
+    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
+    Group g;
+    if (!find_tile(offsets, E, R, blockIdx.y, g)) return;
+    const int k0 = blockIdx.x * kTile;
+    float acc[4][4] = {};
+    for (int f0 = 0; f0 < N; f0 += kStep) {
+        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
+            const int r = i / kStep, c = i % kStep;
+            sa[c][r] = g.row0 + r < g.row1 && f0 + c < N ? __bfloat162float(dy[(long long)(g.row0 + r) * lddy + f0 + c])
+                                                         : 0.0f;
+            const int c2 = i / kTile, kk = i % kTile;
+            sb[c2][kk] = f0 + c2 < N && k0 + kk < K ? mx_at(wc, ws, (long long)g.e * N + f0 + c2, K, k0 + kk) : 0.0f;
+        }
+        __syncthreads();
+        step_product(sa, sb, kStep, acc);
+        __syncthreads();
+    }
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int r = g.row0 + ty + 16 * i, k = k0 + tx + 16 * j;
+            if (r < g.row1 && k < K) dx[(long long)r * lddx + k] = __float2bfloat16_rn(acc[i][j]);
+        }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_wgrad(int R, int N, int K, const __nv_bfloat16* dy, long long lddy,
+                                                    const uint8_t* xc, const uint8_t* xs, const int32_t* offsets,
+                                                    T* dw) {
+    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
+    const int e = blockIdx.z, f0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
+    const int a = offsets ? min(max(__ldg(offsets + e), 0), R) : 0;
+    const int b = offsets ? min(max(__ldg(offsets + e + 1), a), R) : R;
+    float acc[4][4] = {};
+    for (int r0 = a; r0 < b; r0 += kStep) {
+        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
+            const int c = i / kTile, j = i % kTile;
+            sa[c][j] = r0 + c < b && f0 + j < N ? __bfloat162float(dy[(long long)(r0 + c) * lddy + f0 + j]) : 0.0f;
+            sb[c][j] = r0 + c < b && k0 + j < K ? mx_at(xc, xs, r0 + c, K, k0 + j) : 0.0f;
+        }
+        __syncthreads();
+        step_product(sa, sb, kStep, acc);
+        __syncthreads();
+    }
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int f = f0 + ty + 16 * i, k = k0 + tx + 16 * j;
+            if (f < N && k < K) dw[((long long)e * N + f) * K + k] = from_f32<T>(acc[i][j]);
+        }
+}
+
+bool product_sizes_ok(int R, int E, int N, int K, const int32_t* offsets) {
+    return R >= 0 && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && K >= 32 && K % 32 == 0 &&
+           (offsets || E == 1);
+}
+int check_workspace(const void* ws, size_t bytes, int R, int E, int N, int K) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return QBMOE_EINVAL;
+    return bytes < qbmoe_mxfp4_workspace_bytes(R, E, N, K) ? QBMOE_EWORKSPACE : QBMOE_OK;
+}
+template <typename... P>
+bool all_aligned16(const P*... p) { return ((p != nullptr && qbh::aligned16(p)) && ...); }
+
+}  // namespace
+
+extern "C" int moe_mxfp4_quantize(long long rows, int K, int x_dtype, const void* x, long long ldx, uint8_t* codes,
+                                  uint8_t* scales, void* values, qbmoe_stream_t stream) {
+    if (K < 32 || K % 32 || ldx < K || rows < 0 || rows > (1LL << 40) / K) return QBMOE_EINVAL;
+    if (x_dtype != QBMOE_F32 && x_dtype != QBMOE_BF16) return QBMOE_EINVAL;
+    if (ldx % (x_dtype == QBMOE_BF16 ? 8 : 4)) return QBMOE_EINVAL;
+    if (rows == 0) return QBMOE_OK;
+    if (!all_aligned16(x, codes) || !scales || !qbh::aligned16(values)) return QBMOE_EINVAL;
+    int rc = qbh::device_init();
+    if (rc) return rc;
+    const long long items = rows * (K / 8);
+    const int grid = (int)min((items + kQThreads - 1) / kQThreads, 152LL * 8);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (x_dtype == QBMOE_F32) {
+        const float* p = static_cast<const float*>(x);
+        if (values) k_mxfp4_quantize<float, true><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, static_cast<float*>(values));
+        else k_mxfp4_quantize<float, false><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, nullptr);
+    } else {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x);
+        if (values) k_mxfp4_quantize<__nv_bfloat16, true><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, static_cast<__nv_bfloat16*>(values));
+        else k_mxfp4_quantize<__nv_bfloat16, false><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, nullptr);
+    }
+    return qbh::cuda_err(cudaGetLastError());
+}
+
+extern "C" size_t qbmoe_mxfp4_workspace_bytes(int R, int E, int N, int K) {
+    if (R < 0 || E < 1 || E > QBMOE_MAX_EXPERTS || N < 8 || N % 8 || K < 32 || K % 32) return 0;
+    return 256;
+}
+
+extern "C" int moe_mxfp4_matmul(int R, int E, int N, int K, const uint8_t* x_codes, const uint8_t* x_scales,
+                                const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets, void* y,
+                                long long ldy, void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
+    if (!product_sizes_ok(R, E, N, K, offsets) || ldy < N || ldy % 8) return QBMOE_EINVAL;
+    int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
+    if (rc) return rc;
+    if (R == 0) return QBMOE_OK;
+    if (!all_aligned16(x_codes, x_scales, w_codes, w_scales, static_cast<const uint8_t*>(y)) || !qbh::aligned16(offsets))
+        return QBMOE_EINVAL;
+    if ((rc = qbh::device_init())) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    k_matmul<<<dim3((N + kTile - 1) / kTile, (R + kTile - 1) / kTile + E), kThreads, 0, s>>>(
+        R, E, N, K, x_codes, x_scales, w_codes, w_scales, offsets, static_cast<__nv_bfloat16*>(y), ldy);
+    return qbh::cuda_err(cudaGetLastError());
+}
+
+extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const int32_t* offsets, void* dx, long long lddx,
+                               void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
+    if (!product_sizes_ok(R, E, N, K, offsets) || lddy < N || lddy % 8 || lddx < K || lddx % 8) return QBMOE_EINVAL;
+    int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
+    if (rc) return rc;
+    if (R == 0) return QBMOE_OK;
+    if (!all_aligned16(static_cast<const uint8_t*>(dy), w_codes, w_scales, static_cast<const uint8_t*>(dx)) ||
+        !qbh::aligned16(offsets))
+        return QBMOE_EINVAL;
+    if ((rc = qbh::device_init())) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    k_dgrad<<<dim3((K + kTile - 1) / kTile, (R + kTile - 1) / kTile + E), kThreads, 0, s>>>(
+        R, E, N, K, static_cast<const __nv_bfloat16*>(dy), lddy, w_codes, w_scales, offsets,
+        static_cast<__nv_bfloat16*>(dx), lddx);
+    return qbh::cuda_err(cudaGetLastError());
+}
+
+extern "C" int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
+                               const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
+                               void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
+    if (!product_sizes_ok(R, E, N, K, offsets) || lddy < N || lddy % 8) return QBMOE_EINVAL;
+    if (dw_dtype != QBMOE_F32 && dw_dtype != QBMOE_BF16) return QBMOE_EINVAL;
+    int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
+    if (rc) return rc;
+    if (!dw || !qbh::aligned16(dw) || !qbh::aligned16(offsets)) return QBMOE_EINVAL;
+    if (R > 0 && !all_aligned16(static_cast<const uint8_t*>(dy), x_codes, x_scales)) return QBMOE_EINVAL;
+    if ((rc = qbh::device_init())) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const dim3 grid((K + kTile - 1) / kTile, (N + kTile - 1) / kTile, E);
+    const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(dy);
+    if (dw_dtype == QBMOE_F32)
+        k_wgrad<float><<<grid, kThreads, 0, s>>>(R, N, K, d, lddy, x_codes, x_scales, offsets, static_cast<float*>(dw));
+    else
+        k_wgrad<__nv_bfloat16><<<grid, kThreads, 0, s>>>(R, N, K, d, lddy, x_codes, x_scales, offsets,
+                                                         static_cast<__nv_bfloat16*>(dw));
+    return qbh::cuda_err(cudaGetLastError());
+}
