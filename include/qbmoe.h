@@ -48,7 +48,7 @@ typedef enum {
 } qbmoe_status_t;
 
 /* Storage types. */
-enum { QBMOE_F32 = 0, QBMOE_BF16 = 1 };
+enum { QBMOE_F32 = 0, QBMOE_BF16 = 1, QBMOE_MXFP4 = 2 /* moe_mxfp4_matmul's rows only */ };
 /* Routed-expert weight formats. */
 enum { QBMOE_W_F32 = 0, QBMOE_W_BF16 = 1, QBMOE_W_MXFP4 = 2 };
 /* QB sweep forms: every expert from the same biases (the default, one
@@ -309,7 +309,10 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  * QBMOE_MAX_EXPERTS, N a multiple of 8.
  *
  * moe_mxfp4_matmul:  y[r][f] = sum_k x[r][k] w[e(r)][f][k], x and w MXFP4
- *   ([R, K] and [E, N, K]), y [R, N] bf16, row stride ldy elements.
+ *   ([R, K] and [E, N, K]), y [R, N] bf16, row stride ldy elements.  x_type
+ *   QBMOE_MXFP4: x the codes, x_scales the scales, ldx = K.  x_type QBMOE_F32
+ *   or QBMOE_BF16: x [R, K] of that type, row stride ldx elements, quantised
+ *   into the workspace first as moe_mxfp4_quantize does; x_scales is not used.
  * moe_mxfp4_dgrad:   dx[r][k] = sum_f dy[r][f] w[e(r)][f][k], dy [R, N] bf16
  *   (row stride lddy), dx [R, K] bf16 (row stride lddx).
  * moe_mxfp4_wgrad:   dw[e][f][k] = sum over e's rows of dy[r][f] x[r][k],
@@ -323,10 +326,10 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  * K) bytes (one size serves the three calls).  A bounded wait that expires is
  * reported by qbmoe_status(NULL, stream).
  */
-int moe_mxfp4_quantize(long long rows, int K, int x_dtype, const void* x, long long ldx, uint8_t* codes,
+int moe_mxfp4_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes,
                        uint8_t* scales, void* values, qbmoe_stream_t stream);
 size_t qbmoe_mxfp4_workspace_bytes(int R, int E, int N, int K);
-int moe_mxfp4_matmul(int R, int E, int N, int K, const uint8_t* x_codes, const uint8_t* x_scales,
+int moe_mxfp4_matmul(int R, int E, int N, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales,
                      const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets, void* y, long long ldy,
                      void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
 int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,
@@ -450,7 +453,8 @@ int moe_latent_forward(qbmoe_ctx* ctx, int T, const void* x, const float* logits
  * Synchronise `stream`, then return and clear the context's device status
  * word: QBMOE_OK, QBMOE_ETIMEOUT (a bounded wait expired; the kernel
  * returned early and its outputs are undefined) or QBMOE_EDEVICE.
- * ctx may be NULL (then only the stream's CUDA error state is checked).
+ * ctx may be NULL: the status word of the calls that take no context
+ * (moe_mxfp4_*, one word per device) instead.
  */
 int qbmoe_status(qbmoe_ctx* ctx, qbmoe_stream_t stream);
 
@@ -471,14 +475,15 @@ int qbmoe_route_last_launch_count(void);
 
 /* Test hook: cap on bounded device waits, in polls of at most 20 us each
  * (<= 0 restores the default of 2^17).  Applies to launches made after the
- * call. */
+ * call.  ctx NULL: the moe_mxfp4_* calls. */
 int qbmoe_set_wait_limit(qbmoe_ctx* ctx, long long iterations);
 
 /* Test hook: while enabled, the tensor-core GEMM kernels withhold their first
  * accumulator hand-off, so the epilogue's bounded wait expires and the next
  * qbmoe_status reports QBMOE_ETIMEOUT (outputs undefined).  The kernels then
  * drain their own copies and MMAs, free TMEM and return; the context stays
- * usable.  No effect when the layer runs on CUDA cores. */
+ * usable.  No effect when the layer runs on CUDA cores.  ctx NULL: the
+ * moe_mxfp4_* products. */
 int qbmoe_debug_stall(qbmoe_ctx* ctx, int enable);
 
 /* 1 when the context's bf16 GEMMs run on the tcgen05 tensor-core kernels, 0

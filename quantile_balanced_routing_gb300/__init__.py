@@ -25,7 +25,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "qbmoe.h")
 
 QBMOE_OK, QBMOE_EINVAL, QBMOE_ENOMEM, QBMOE_ECUDA = 0, -1, -2, -3
 QBMOE_EARCH, QBMOE_EWORKSPACE, QBMOE_ETIMEOUT, QBMOE_EDEVICE = -4, -5, -6, -7
-QBMOE_F32, QBMOE_BF16 = 0, 1
+QBMOE_F32, QBMOE_BF16, QBMOE_MXFP4 = 0, 1, 2
 QBMOE_W_F32, QBMOE_W_BF16, QBMOE_W_MXFP4 = 0, 1, 2
 QBMOE_QB_JACOBI, QBMOE_QB_GAUSS_SEIDEL = 0, 1
 MAX_EXPERTS, MAX_TOPK = 1024, 32
@@ -133,7 +133,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_mxfp4_quantize.argtypes = [ll, i, i, vp, ll, vp, vp, vp, vp]
     lib.qbmoe_mxfp4_workspace_bytes.argtypes = [i, i, i, i]
     lib.qbmoe_mxfp4_workspace_bytes.restype = sz
-    lib.moe_mxfp4_matmul.argtypes = [i, i, i, i, vp, vp, vp, vp, vp, vp, ll, vp, sz, vp]
+    lib.moe_mxfp4_matmul.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, ll, vp, sz, vp]
     lib.moe_mxfp4_dgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, vp, ll, vp, sz, vp]
     lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp, sz, vp]
     for nm in ("moe_balance_loss", "moe_router_backward", "moe_mxfp4_quantize", "moe_mxfp4_matmul",

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "dispatch.cuh"
 #include "gemm_tc.cuh"
+#include "mxfp4.cuh"
 
 #include <cstdio>
 #include <cstring>
@@ -40,6 +41,7 @@ int qbh::device_init() {
     int rc = check_device_arch(dev);
     if (!rc) rc = qbh::route_init_attributes();
     if (!rc) rc = qbh::tc_init_attributes();
+    if (!rc) rc = qbh::mx_product_init();
     if (rc) {
         cudaGetLastError();
         return rc;
@@ -402,14 +404,20 @@ extern "C" int qbmoe_stage_times(qbmoe_ctx* c, float* ms, const char** names, in
 extern "C" int qbmoe_last_launch_count(qbmoe_ctx* c) { return c ? c->launches : 0; }
 
 extern "C" int qbmoe_set_wait_limit(qbmoe_ctx* c, long long iterations) {
-    if (!c) return QBMOE_EINVAL;
+    if (!c) {
+        qbh::mx_set_wait_limit(iterations);
+        return QBMOE_OK;
+    }
     c->wait_limit = iterations > 0 ? iterations : 0;
     qbh::tc_set_wait_limit(c->tc, c->wait_limit);
     return QBMOE_OK;
 }
 
 extern "C" int qbmoe_debug_stall(qbmoe_ctx* c, int enable) {
-    if (!c) return QBMOE_EINVAL;
+    if (!c) {
+        qbh::mx_set_stall(enable != 0);
+        return QBMOE_OK;
+    }
     qbh::tc_set_stall(c->tc, enable != 0);
     return QBMOE_OK;
 }
@@ -420,7 +428,7 @@ extern "C" int qbmoe_status(qbmoe_ctx* c, qbmoe_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return QBMOE_ECUDA;
     if (cudaGetLastError() != cudaSuccess) return QBMOE_ECUDA;
-    if (!c) return QBMOE_OK;
+    if (!c) return qbh::mx_status_take();
     int v = 0;
     if (cudaMemcpy(&v, c->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return QBMOE_ECUDA;
     if (v != 0 && cudaMemset(c->status, 0, 4) != cudaSuccess) return QBMOE_ECUDA;

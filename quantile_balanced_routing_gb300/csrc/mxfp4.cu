@@ -4,7 +4,9 @@
 // [K3-width] 延伸解读 on deployment: routed-expert weights in MXFP4 with
 // quantisation-aware post-training.  OCP MX: E2M1 elements, one E8M0 scale per
 // 32 along K.
-#include "common.cuh"
+#include "mxfp4.cuh"
+
+#include <type_traits>
 
 namespace {
 
@@ -74,6 +76,7 @@ template <typename T, bool kValues>
 __global__ void __launch_bounds__(kQThreads) k_mxfp4_quantize(long long rows, int K, const T* __restrict__ x,
                                                               long long ldx, uint8_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales, T* __restrict__ values) {
+    pdl_trigger();   // a product of these rows may set itself up meanwhile
     const int per_row = K / 8;   // a multiple of 4: the lanes of a block share its fate
     const long long items = rows * per_row;
     for (long long it = (long long)blockIdx.x * kQThreads + threadIdx.x; it < items;
@@ -150,32 +153,6 @@ QB_DEV void step_product(const float (&a)[kStep][kTile + 1], const float (&b)[kS
             for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[c][ty + 16 * i], b[c][tx + 16 * j], acc[i][j]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_matmul(int R, int E, int N, int K, const uint8_t* xc, const uint8_t* xs,
-                                                     const uint8_t* wc, const uint8_t* ws, const int32_t* offsets,
-                                                     __nv_bfloat16* y, long long ldy) {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-    Group g;
-    if (!find_tile(offsets, E, R, blockIdx.y, g)) return;
-    const int f0 = blockIdx.x * kTile;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int r = i / kStep, c = i % kStep;
-            sa[c][r] = g.row0 + r < g.row1 ? mx_at(xc, xs, g.row0 + r, K, k0 + c) : 0.0f;
-            sb[c][r] = f0 + r < N ? mx_at(wc, ws, (long long)g.e * N + f0 + r, K, k0 + c) : 0.0f;
-        }
-        __syncthreads();
-        step_product(sa, sb, kStep, acc);
-        __syncthreads();
-    }
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = g.row0 + ty + 16 * i, f = f0 + tx + 16 * j;
-            if (r < g.row1 && f < N) y[(long long)r * ldy + f] = __float2bfloat16_rn(acc[i][j]);
-        }
-}
-
 __global__ void __launch_bounds__(kThreads) k_dgrad(int R, int E, int N, int K, const __nv_bfloat16* dy,
                                                     long long lddy, const uint8_t* wc, const uint8_t* ws,
                                                     const int32_t* offsets, __nv_bfloat16* dx, long long lddx) {
@@ -231,6 +208,10 @@ __global__ void __launch_bounds__(kThreads) k_wgrad(int R, int N, int K, const _
         }
 }
 
+bool rows_ok(int K, int x_type, long long ldx) {
+    return (x_type == QBMOE_F32 || x_type == QBMOE_BF16) && ldx >= K && ldx % (x_type == QBMOE_BF16 ? 8 : 4) == 0;
+}
+
 bool product_sizes_ok(int R, int E, int N, int K, const int32_t* offsets) {
     return R >= 0 && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && K >= 32 && K % 32 == 0 &&
            (offsets || E == 1);
@@ -244,49 +225,64 @@ bool all_aligned16(const P*... p) { return ((p != nullptr && qbh::aligned16(p)) 
 
 }  // namespace
 
-extern "C" int moe_mxfp4_quantize(long long rows, int K, int x_dtype, const void* x, long long ldx, uint8_t* codes,
+namespace qbh {
+
+int mx_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes, uint8_t* scales,
+                void* values, cudaStream_t s) {
+    const long long items = rows * (K / 8);
+    const int grid = (int)min((items + kQThreads - 1) / kQThreads, 8LL * sm_count());
+    auto go = [&](auto tag, auto with) {
+        using T = decltype(tag);
+        k_mxfp4_quantize<T, decltype(with)::value><<<grid, kQThreads, 0, s>>>(
+            rows, K, static_cast<const T*>(x), ldx, codes, scales, static_cast<T*>(values));
+    };
+    if (x_type == QBMOE_F32) values ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
+    else values ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});
+    return cuda_err(cudaGetLastError());
+}
+
+}  // namespace qbh
+
+extern "C" int moe_mxfp4_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes,
                                   uint8_t* scales, void* values, qbmoe_stream_t stream) {
-    if (K < 32 || K % 32 || ldx < K || rows < 0 || rows > (1LL << 40) / K) return QBMOE_EINVAL;
-    if (x_dtype != QBMOE_F32 && x_dtype != QBMOE_BF16) return QBMOE_EINVAL;
-    if (ldx % (x_dtype == QBMOE_BF16 ? 8 : 4)) return QBMOE_EINVAL;
+    if (K < 32 || K % 32 || rows < 0 || rows > (1LL << 40) / K || !rows_ok(K, x_type, ldx)) return QBMOE_EINVAL;
     if (rows == 0) return QBMOE_OK;
     if (!all_aligned16(x, codes) || !scales || !qbh::aligned16(values)) return QBMOE_EINVAL;
     int rc = qbh::device_init();
     if (rc) return rc;
-    const long long items = rows * (K / 8);
-    const int grid = (int)min((items + kQThreads - 1) / kQThreads, 152LL * 8);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (x_dtype == QBMOE_F32) {
-        const float* p = static_cast<const float*>(x);
-        if (values) k_mxfp4_quantize<float, true><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, static_cast<float*>(values));
-        else k_mxfp4_quantize<float, false><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, nullptr);
-    } else {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x);
-        if (values) k_mxfp4_quantize<__nv_bfloat16, true><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, static_cast<__nv_bfloat16*>(values));
-        else k_mxfp4_quantize<__nv_bfloat16, false><<<grid, kQThreads, 0, s>>>(rows, K, p, ldx, codes, scales, nullptr);
-    }
-    return qbh::cuda_err(cudaGetLastError());
+    return qbh::mx_quantize(rows, K, x_type, x, ldx, codes, scales, values, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t qbmoe_mxfp4_workspace_bytes(int R, int E, int N, int K) {
     if (R < 0 || E < 1 || E > QBMOE_MAX_EXPERTS || N < 8 || N % 8 || K < 32 || K % 32) return 0;
-    return 256;
+    // codes and scales of rows that come in another type
+    return 256 + qbh::align_up((size_t)R * (K / 2), 256) + qbh::align_up((size_t)R * (K / 32), 256);
 }
 
-extern "C" int moe_mxfp4_matmul(int R, int E, int N, int K, const uint8_t* x_codes, const uint8_t* x_scales,
-                                const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets, void* y,
-                                long long ldy, void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
+extern "C" int moe_mxfp4_matmul(int R, int E, int N, int K, int x_type, const void* x, long long ldx,
+                                const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                                const int32_t* offsets, void* y, long long ldy, void* workspace,
+                                size_t workspace_bytes, qbmoe_stream_t stream) {
     if (!product_sizes_ok(R, E, N, K, offsets) || ldy < N || ldy % 8) return QBMOE_EINVAL;
+    if (x_type == QBMOE_MXFP4 ? ldx != K : !rows_ok(K, x_type, ldx)) return QBMOE_EINVAL;
     int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
     if (rc) return rc;
     if (R == 0) return QBMOE_OK;
-    if (!all_aligned16(x_codes, x_scales, w_codes, w_scales, static_cast<const uint8_t*>(y)) || !qbh::aligned16(offsets))
+    if (!all_aligned16(static_cast<const uint8_t*>(x), w_codes, w_scales, static_cast<const uint8_t*>(y)) ||
+        !qbh::aligned16(offsets) || (x_type == QBMOE_MXFP4 && !all_aligned16(x_scales)))
         return QBMOE_EINVAL;
     if ((rc = qbh::device_init())) return rc;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    k_matmul<<<dim3((N + kTile - 1) / kTile, (R + kTile - 1) / kTile + E), kThreads, 0, s>>>(
-        R, E, N, K, x_codes, x_scales, w_codes, w_scales, offsets, static_cast<__nv_bfloat16*>(y), ldy);
-    return qbh::cuda_err(cudaGetLastError());
+    uint8_t* codes = static_cast<uint8_t*>(workspace);
+    uint8_t* scales = codes + qbh::align_up((size_t)R * (K / 2), 256);
+    const bool raw = x_type != QBMOE_MXFP4;
+    qbh::MxProduct p{};
+    p.R = R; p.E = E; p.N = N; p.K = K;
+    p.x_codes = raw ? codes : static_cast<uint8_t*>(const_cast<void*>(x));
+    p.x_scales = raw ? scales : const_cast<uint8_t*>(x_scales);
+    p.w_codes = w_codes; p.w_scales = w_scales; p.offsets = offsets;
+    p.y = y; p.ldy = ldy;
+    p.raw = raw ? x : nullptr; p.raw_type = x_type; p.raw_ld = ldx;
+    return qbh::mx_product(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,

@@ -1,0 +1,127 @@
+// What the MXFP4 products share: grouped tiles, tensor maps, the status word.
+#pragma once
+
+#include "common.cuh"
+
+#include <cuda.h>
+
+namespace qbh {
+
+int mx_product_init();   // mxfp4_product.cu: kernel attributes, once per device (device_init)
+
+// Status word of the calls that take no context (one per device): the first
+// code a kernel recorded since it was last taken, then cleared.
+int* mx_status();
+int mx_status_take();
+// Test hooks of those calls (qbmoe_set_wait_limit / qbmoe_debug_stall without a context).
+long long mx_wait_limit();
+void mx_set_wait_limit(long long polls);
+int mx_stall();
+void mx_set_stall(int on);
+
+int sm_count();
+// 2-D row-major tensor map: cols elements a row (row stride ld bytes), box
+// {box_cols, box_rows}, 128-byte swizzle, zeros outside.
+bool encode_rows(CUtensorMap* m, CUtensorMapDataType type, const void* base, long long rows, long long cols,
+                 long long ld_bytes, int box_cols, int box_rows);
+
+// Rows of fp32 or bf16 (x_type) to codes and scales, and the values if wanted (mxfp4.cu).
+int mx_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes, uint8_t* scales,
+                void* values, cudaStream_t s);
+
+// Sizes and alignment are checked by the caller.  raw: rows of another type
+// that are quantised into x_codes and x_scales first (NULL: they hold the rows).
+struct MxProduct {
+    int R, E, N, K;
+    uint8_t *x_codes, *x_scales;
+    const uint8_t *w_codes, *w_scales;
+    const int32_t* offsets;
+    void* y;
+    long long ldy;
+    const void* raw;
+    int raw_type;
+    long long raw_ld;
+};
+int mx_product(const MxProduct& p, cudaStream_t s);
+
+}  // namespace qbh
+
+namespace qb {
+
+// Expert-ordered rows as tiles of at most BN rows: seg [E + 1] and toff [E + 1]
+// (first tile of each expert) in shared memory.  Offsets out of order or out
+// of range are clamped, so that every tile lies inside [0, R).
+struct Groups {
+    int* seg;
+    int* toff;
+};
+
+// Whole CTA: read the offsets and count each expert's tiles.  NULL offsets: one
+// group of R rows.  Ends with a __syncthreads.
+template <int BN, int kThreads>
+QB_DEV void load_groups(const Groups& g, const int32_t* offsets, int E, int R, int* scratch /* [kThreads / 32] */) {
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e <= E; e += kThreads)
+        g.seg[e] = offsets ? min(max(__ldg(offsets + e), 0), R) : (e ? R : 0);
+    __syncthreads();
+    // each warp scans a run of experts, then adds what the warps before it counted
+    const int per = ((E + kWarps - 1) / kWarps + 31) & ~31;
+    int run = 0;
+    for (int e0 = warp * per; e0 < min(E, (warp + 1) * per); e0 += 32) {
+        const int e = e0 + lane;
+        int n = e < E ? (max(g.seg[e + 1] - g.seg[e], 0) + BN - 1) / BN : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (e < E) g.toff[e] = run + incl - n;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) scratch[warp] = run;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    for (int e = warp * per + lane; e < min(E, (warp + 1) * per); e += 32) g.toff[e] += before;
+    if (threadIdx.x == 0) {
+        int total = 0;
+        for (int w = 0; w < kWarps; ++w) total += scratch[w];
+        g.toff[E] = total;
+    }
+    __syncthreads();
+}
+
+// Walks the tiles blockIdx.x, blockIdx.x + gridDim.x, ...: m-tile fastest, then
+// the expert's row tiles.  An expert's rows are split into equal tiles
+// (multiples of 16), so that tiles sharing a weight tile run at one pace.
+template <int BN>
+struct Walker {
+    int ntg, m, g;
+    int row0, nrows;   // of the current tile
+    QB_DEV void seek(const Groups& gr, int E) {
+        while (g + 1 < E && gr.toff[g + 1] <= ntg) ++g;
+        const int t0 = gr.toff[g], nt = gr.toff[g + 1] - t0;
+        const int a = gr.seg[g], len = gr.seg[g + 1] - a;
+        const int per = ((nt == 1 ? len : (len + nt - 1) / nt) + 15) & ~15;
+        row0 = a + (ntg - t0) * per;
+        nrows = min(per, a + len - row0);
+    }
+    QB_DEV void start(const Groups& gr, int E, int m_total, int first) {
+        ntg = first / m_total;
+        m = first - ntg * m_total;
+        g = 0;
+        if (ntg < gr.toff[E]) seek(gr, E);
+    }
+    QB_DEV bool next(const Groups& gr, int E, int m_total, int step) {
+        const int was = ntg;
+        m += step;
+        while (m >= m_total) m -= m_total, ++ntg;
+        if (ntg >= gr.toff[E]) return false;
+        if (ntg != was) seek(gr, E);
+        return true;
+    }
+};
+
+}  // namespace qb

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 from typing import NamedTuple
 
-from . import (MAX_EXPERTS, QBMOE_BF16, QBMOE_EINVAL, QBMOE_F32, QbmoeError, _allocating_on, _check_device, _p,
+from . import (MAX_EXPERTS, QBMOE_BF16, QBMOE_EINVAL, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _allocating_on, _check_device, _p,
                _stream_ptr, load_library)
 
 BLOCK = 32
@@ -79,7 +79,7 @@ def mxfp4_quantize(x, values=False, stream=None):
     return (q, v) if values else q
 
 
-def _groups(what, w, offsets, R):
+def _groups(what, w, offsets):
     """Checked (E, N, K) of weights [N, K], or [E, N, K] with offsets."""
     import torch
     _check_mxfp4(what, "w", w, (2, 3))
@@ -107,17 +107,24 @@ def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
     rows that no expert owns are left unwritten."""
     import torch
     what = "mxfp4_matmul"
-    xq = x if isinstance(x, Mxfp4) else mxfp4_quantize(x, stream=stream)
-    _check_mxfp4(what, "x", xq, (2,))
-    R = xq.codes.shape[0]
-    E, N, K = _groups(what, w, offsets, R)
-    _need(what, xq.shape[1] == K, "x and w have the same K")
-    _check_device(what, xq.codes, xq.scales, w.codes, w.scales, offsets)
+    if isinstance(x, Mxfp4):
+        _check_mxfp4(what, "x", x, (2,))
+        rows, kind, scales = x.codes, QBMOE_MXFP4, x.scales
+        ld = x.shape[1]
+    else:
+        _need(what, x.dtype in (torch.float32, torch.bfloat16), "x is an Mxfp4 or fp32 or bf16 [R, K]")
+        rows, scales = x, None
+        kind, align = (QBMOE_F32, 4) if x.dtype == torch.float32 else (QBMOE_BF16, 8)
+        ld = _row_stride(what, "x", x, align)
+    R = rows.shape[0]
+    E, N, K = _groups(what, w, offsets)
+    _need(what, x.shape[1] == K, "x and w have the same K")
+    _check_device(what, rows, scales, w.codes, w.scales, offsets)
     lib = load_library()
     with _allocating_on(stream):
-        y = torch.empty((R, N), dtype=torch.bfloat16, device=xq.codes.device)
+        y = torch.empty((R, N), dtype=torch.bfloat16, device=rows.device)
         ws = _workspace(lib, R, E, N, K, y.device)
-        rc = lib.moe_mxfp4_matmul(R, E, N, K, _p(xq.codes), _p(xq.scales), _p(w.codes), _p(w.scales), _p(offsets),
+        rc = lib.moe_mxfp4_matmul(R, E, N, K, kind, _p(rows), ld, _p(scales), _p(w.codes), _p(w.scales), _p(offsets),
                                   _p(y), N, _p(ws), ws.numel(), _stream_ptr(stream))
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_matmul")
@@ -136,7 +143,7 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
     what = "mxfp4_matmul_backward"
     _check_mxfp4(what, "xq", xq, (2,))
     R = xq.codes.shape[0]
-    E, N, K = _groups(what, w, offsets, R)
+    E, N, K = _groups(what, w, offsets)
     _need(what, xq.shape[1] == K, "xq and w have the same K")
     _need(what, dy.dtype == torch.bfloat16 and tuple(dy.shape) == (R, N), "dy is bf16 [R, N]")
     ld = _row_stride(what, "dy", dy, 8)

@@ -311,8 +311,9 @@ def test_output_stride_and_rows_without_an_expert():
     lib = Q.load_library()
     y = torch.full((R, 64), 7.0, dtype=torch.bfloat16, device="cuda")
     ws = torch.empty(lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K), dtype=torch.uint8, device="cuda")
-    rc = lib.moe_mxfp4_matmul(R, E, N, K, *(t.data_ptr() for t in (x.codes, x.scales, w.codes, w.scales, off, y)), 64,
-                              ws.data_ptr(), ws.numel(), None)
+    rc = lib.moe_mxfp4_matmul(R, E, N, K, Q.QBMOE_MXFP4, x.codes.data_ptr(), K,
+                              *(t.data_ptr() for t in (x.scales, w.codes, w.scales, off, y)), 64, ws.data_ptr(),
+                              ws.numel(), None)
     torch.cuda.synchronize()
     assert rc == 0
     want, mags = M.matmul(xq[2], wq[2].reshape(E, N, K), offsets)
@@ -344,3 +345,24 @@ def test_offsets_past_32_bits():
     near(dx, wx, mx, N, True)
     near(dw[-1], ww[0], mw[0], R, False)
     assert not dw[:-1].any()
+
+
+def test_bounded_wait_reports_and_recovers():
+    """The issuer withholds its first accumulator: the waits run out, the status says so, the next call is right."""
+    import quantile_balanced_routing_gb300 as Q
+    lib = Q.load_library()
+    xq, wq, offsets, _ = product_case(611, 24, 264, 544, 2.0)
+    x, w, off = on_gpu(Q, xq, wq, offsets, 24, 264, 544)
+    want = Q.mxfp4_matmul(x, w, off)
+    assert Q.qbmoe_status(None, None) == 0
+    lib.qbmoe_set_wait_limit(None, 200)
+    lib.qbmoe_debug_stall(None, 1)
+    try:
+        Q.mxfp4_matmul(x, w, off)
+        assert Q.qbmoe_status(None, None) == Q.QBMOE_ETIMEOUT
+    finally:
+        lib.qbmoe_debug_stall(None, 0)
+        lib.qbmoe_set_wait_limit(None, 0)
+    assert Q.qbmoe_status(None, None) == 0
+    assert torch.equal(Q.mxfp4_matmul(x, w, off), want)
+    assert Q.qbmoe_status(None, None) == 0
