@@ -42,6 +42,7 @@ int qbh::device_init() {
     if (!rc) rc = qbh::route_init_attributes();
     if (!rc) rc = qbh::tc_init_attributes();
     if (!rc) rc = qbh::mx_product_init();
+    if (!rc) rc = qbh::mx_grad_init();
     if (rc) {
         cudaGetLastError();
         return rc;

@@ -47,6 +47,7 @@
 // act = SiTU-GLU(gate, up), stored as bf16 or as E4M3 pairs).
 #include "gemm_tc.cuh"
 #include "dispatch.cuh"
+#include "mxfp4_decode.cuh"
 #include "tc_ptx.cuh"
 
 #include <cudaTypedefs.h>
@@ -432,44 +433,6 @@ __device__ __forceinline__ void epilogue_tile(const TcParams& p, const TileInfo&
             }
         }
     }
-}
-
-// ---- MXFP4 (OCP MX: E2M1 elements, E8M0 scale per 32) -> bf16 ----------------
-// E2M1 magnitude index i = code & 7 has value {0, .5, 1, 1.5, 2, 3, 4, 6}[i].
-// Times 2^d its bf16 has exponent field f_i + d with f = {-, 126, 127, 127,
-// 128, 128, 129, 129} and mantissa {0, 0, 0, 0x40, 0, 0x40, 0, 0x40}; the
-// decode is exact while every field stays in [1, 254] (|d| <= 125).
-__device__ __forceinline__ float e2m1_to_f32(uint32_t code) {
-    const uint32_t ex = (code >> 1) & 3u, man = code & 1u;
-    const float v = ex == 0u ? 0.5f * (float)man : __int_as_float((int)(ex + 126u) << 23) * (1.0f + 0.5f * (float)man);
-    return (code & 8u) ? -v : v;
-}
-
-// High and low bytes of the eight magnitudes' bf16 at scale 2^d, packed four
-// per register for byte-permute lookups (h[0]/l[0]: indices 0-3, h[1]/l[1]: 4-7).
-__device__ __forceinline__ void mx_tables(int d, uint32_t (&h)[2], uint32_t (&l)[2]) {
-    const uint32_t a = 126 + d, b = a + 1, c = a + 2, e = a + 3;   // exponent fields
-    h[0] = ((a >> 1) << 8) | ((b >> 1) << 16) | ((b >> 1) << 24);
-    h[1] = (c >> 1) | ((c >> 1) << 8) | ((e >> 1) << 16) | ((e >> 1) << 24);
-    l[0] = ((a & 1u) << 15) | ((b & 1u) << 23) | (((b & 1u) << 31) | (0x40u << 24));
-    l[1] = ((c & 1u) << 7) | ((((c & 1u) << 7) | 0x40u) << 8) | ((e & 1u) << 23) | ((((e & 1u) << 7) | 0x40u) << 24);
-}
-
-// Eight E2M1 codes of one 32-bit word (code j in bits 4j..4j+3) -> four bf16
-// pairs (elements 2q and 2q+1 in o[q]).
-__device__ __forceinline__ void mx_decode_word(uint32_t w, const uint32_t (&h)[2], const uint32_t (&l)[2],
-                                               uint32_t (&o)[4]) {
-    const uint32_t sel0 = w & 0x7777u, sel1 = (w >> 16) & 0x7777u;     // magnitudes of codes 0-3, 4-7
-    const uint32_t h0 = __byte_perm(h[0], h[1], sel0), l0 = __byte_perm(l[0], l[1], sel0);
-    const uint32_t h1 = __byte_perm(h[0], h[1], sel1), l1 = __byte_perm(l[0], l[1], sel1);
-    o[0] = __byte_perm(l0, h0, 0x5140);
-    o[1] = __byte_perm(l0, h0, 0x7362);
-    o[2] = __byte_perm(l1, h1, 0x5140);
-    o[3] = __byte_perm(l1, h1, 0x7362);
-    // sign of code 2q is bit 3 of byte q (-> bit 15), of code 2q+1 bit 7 (-> bit 31)
-    const uint32_t w4 = w << 4;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] |= __byte_perm(w, w4, (q << 12) | ((4 + q) << 4)) & 0x80008000u;
 }
 
 // Every mode adds one warp after its others: the MMA waiter (see the MMA
@@ -881,7 +844,7 @@ __global__ void __launch_bounds__(threads_of<MODE>(), 1) k_tc_gemm(const __grid_
                             uint32_t pr = 0;
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const float v = e2m1_to_f32((words[j] >> (8 * b + 4 * h)) & 15u) * m;
+                                const float v = e2m1_value((words[j] >> (8 * b + 4 * h)) & 15u) * m;
                                 pr |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v)) << (16 * h);
                             }
                             o[b] = pr;

@@ -5,6 +5,7 @@
 // quantisation-aware post-training.  OCP MX: E2M1 elements, one E8M0 scale per
 // 32 along K.
 #include "mxfp4.cuh"
+#include "mxfp4_decode.cuh"
 
 #include <type_traits>
 
@@ -60,18 +61,6 @@ QB_DEV uint32_t e2m1_pair(float lo, float hi) {
     return r;
 }
 
-// E2M1 code -> value.
-QB_DEV float e2m1_value(uint32_t code) {
-    const uint32_t m = code & 7u;
-    const float v = m < 4u ? 0.5f * (float)m : (m < 6u ? (float)m - 2.0f : 2.0f * (float)m - 8.0f);
-    return (code & 8u) ? -v : v;
-}
-
-// E8M0 byte -> scale (0xFF: NaN).
-QB_DEV float e8m0_value(uint32_t b) {
-    return b == 0xffu ? __int_as_float(0x7fffffff) : __int_as_float(b ? (int)(b << 23) : 0x00400000);
-}
-
 template <typename T, bool kValues>
 __global__ void __launch_bounds__(kQThreads) k_mxfp4_quantize(long long rows, int K, const T* __restrict__ x,
                                                               long long ldx, uint8_t* __restrict__ codes,
@@ -109,103 +98,6 @@ __global__ void __launch_bounds__(kQThreads) k_mxfp4_quantize(long long rows, in
             Eight<T>::store(values + r * K + k, v);
         }
     }
-}
-
-// ---------------------------------------------------------------------------
-// Products on CUDA cores, 64 x 64 output tiles.  A grouped tile belongs to one
-// expert; its place is found by walking the offsets.
-// ---------------------------------------------------------------------------
-constexpr int kTile = 64, kStep = 32, kThreads = 256;
-
-struct Group {
-    int e, row0, row1;   // expert, tile rows [row0, row1)
-};
-QB_DEV bool find_tile(const int32_t* offsets, int E, int R, int tile, Group& g) {
-    int seen = 0;
-    for (int e = 0; e < E; ++e) {
-        const int a = offsets ? min(max(__ldg(offsets + e), 0), R) : 0;
-        const int b = offsets ? min(max(__ldg(offsets + e + 1), a), R) : R;
-        const int nt = (b - a + kTile - 1) / kTile;
-        if (tile < seen + nt) {
-            g.e = e;
-            g.row0 = a + (tile - seen) * kTile;
-            g.row1 = min(b, g.row0 + kTile);
-            return true;
-        }
-        seen += nt;
-    }
-    return false;
-}
-
-QB_DEV float mx_at(const uint8_t* codes, const uint8_t* scales, long long row, int K, int k) {
-    const uint32_t b = __ldg(codes + row * (K / 2) + k / 2);
-    return e2m1_value(k & 1 ? b >> 4 : b) * e8m0_value(__ldg(scales + row * (K / 32) + k / 32));
-}
-
-// acc[i][j] += sum_c a[c][ty + 16 i] b[c][tx + 16 j] over a staged step.
-QB_DEV void step_product(const float (&a)[kStep][kTile + 1], const float (&b)[kStep][kTile + 1], int n,
-                         float (&acc)[4][4]) {
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    for (int c = 0; c < n; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[c][ty + 16 * i], b[c][tx + 16 * j], acc[i][j]);
-}
-
-__global__ void __launch_bounds__(kThreads) k_dgrad(int R, int E, int N, int K, const __nv_bfloat16* dy,
-                                                    long long lddy, const uint8_t* wc, const uint8_t* ws,
-                                                    const int32_t* offsets, __nv_bfloat16* dx, long long lddx) {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-    Group g;
-    if (!find_tile(offsets, E, R, blockIdx.y, g)) return;
-    const int k0 = blockIdx.x * kTile;
-    float acc[4][4] = {};
-    for (int f0 = 0; f0 < N; f0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int r = i / kStep, c = i % kStep;
-            sa[c][r] = g.row0 + r < g.row1 && f0 + c < N ? __bfloat162float(dy[(long long)(g.row0 + r) * lddy + f0 + c])
-                                                         : 0.0f;
-            const int c2 = i / kTile, kk = i % kTile;
-            sb[c2][kk] = f0 + c2 < N && k0 + kk < K ? mx_at(wc, ws, (long long)g.e * N + f0 + c2, K, k0 + kk) : 0.0f;
-        }
-        __syncthreads();
-        step_product(sa, sb, kStep, acc);
-        __syncthreads();
-    }
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = g.row0 + ty + 16 * i, k = k0 + tx + 16 * j;
-            if (r < g.row1 && k < K) dx[(long long)r * lddx + k] = __float2bfloat16_rn(acc[i][j]);
-        }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_wgrad(int R, int N, int K, const __nv_bfloat16* dy, long long lddy,
-                                                    const uint8_t* xc, const uint8_t* xs, const int32_t* offsets,
-                                                    T* dw) {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-    const int e = blockIdx.z, f0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
-    const int a = offsets ? min(max(__ldg(offsets + e), 0), R) : 0;
-    const int b = offsets ? min(max(__ldg(offsets + e + 1), a), R) : R;
-    float acc[4][4] = {};
-    for (int r0 = a; r0 < b; r0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int c = i / kTile, j = i % kTile;
-            sa[c][j] = r0 + c < b && f0 + j < N ? __bfloat162float(dy[(long long)(r0 + c) * lddy + f0 + j]) : 0.0f;
-            sb[c][j] = r0 + c < b && k0 + j < K ? mx_at(xc, xs, r0 + c, K, k0 + j) : 0.0f;
-        }
-        __syncthreads();
-        step_product(sa, sb, kStep, acc);
-        __syncthreads();
-    }
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int f = f0 + ty + 16 * i, k = k0 + tx + 16 * j;
-            if (f < N && k < K) dw[((long long)e * N + f) * K + k] = from_f32<T>(acc[i][j]);
-        }
 }
 
 bool rows_ok(int K, int x_type, long long ldx) {
@@ -296,11 +188,13 @@ extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long 
         !qbh::aligned16(offsets))
         return QBMOE_EINVAL;
     if ((rc = qbh::device_init())) return rc;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    k_dgrad<<<dim3((K + kTile - 1) / kTile, (R + kTile - 1) / kTile + E), kThreads, 0, s>>>(
-        R, E, N, K, static_cast<const __nv_bfloat16*>(dy), lddy, w_codes, w_scales, offsets,
-        static_cast<__nv_bfloat16*>(dx), lddx);
-    return qbh::cuda_err(cudaGetLastError());
+    qbh::MxGrad g{};
+    g.weights = false;
+    g.R = R; g.E = E; g.N = N; g.K = K;
+    g.dy = dy; g.lddy = lddy;
+    g.codes = w_codes; g.scales = w_scales; g.offsets = offsets;
+    g.out = dx; g.ldo = lddx; g.out_type = QBMOE_BF16;
+    return qbh::mx_grad(g, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
@@ -313,13 +207,11 @@ extern "C" int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long 
     if (!dw || !qbh::aligned16(dw) || !qbh::aligned16(offsets)) return QBMOE_EINVAL;
     if (R > 0 && !all_aligned16(static_cast<const uint8_t*>(dy), x_codes, x_scales)) return QBMOE_EINVAL;
     if ((rc = qbh::device_init())) return rc;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid((K + kTile - 1) / kTile, (N + kTile - 1) / kTile, E);
-    const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(dy);
-    if (dw_dtype == QBMOE_F32)
-        k_wgrad<float><<<grid, kThreads, 0, s>>>(R, N, K, d, lddy, x_codes, x_scales, offsets, static_cast<float*>(dw));
-    else
-        k_wgrad<__nv_bfloat16><<<grid, kThreads, 0, s>>>(R, N, K, d, lddy, x_codes, x_scales, offsets,
-                                                         static_cast<__nv_bfloat16*>(dw));
-    return qbh::cuda_err(cudaGetLastError());
+    qbh::MxGrad g{};
+    g.weights = true;
+    g.R = R; g.E = E; g.N = N; g.K = K;
+    g.dy = dy; g.lddy = lddy;
+    g.codes = x_codes; g.scales = x_scales; g.offsets = offsets;
+    g.out = dw; g.ldo = K; g.out_type = dw_dtype;
+    return qbh::mx_grad(g, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -7,7 +7,9 @@
 
 namespace qbh {
 
-int mx_product_init();   // mxfp4_product.cu: kernel attributes, once per device (device_init)
+// Kernel attributes, once per device (device_init).
+int mx_product_init();   // mxfp4_product.cu
+int mx_grad_init();      // mxfp4_grad.cu
 
 // Status word of the calls that take no context (one per device): the first
 // code a kernel recorded since it was last taken, then cleared.
@@ -43,6 +45,20 @@ struct MxProduct {
     long long raw_ld;
 };
 int mx_product(const MxProduct& p, cudaStream_t s);
+
+// dx (codes and scales of the weights) or dw (of the rows) from dy [R, N] bf16.
+struct MxGrad {
+    bool weights;
+    int R, E, N, K;
+    const void* dy;
+    long long lddy;
+    const uint8_t *codes, *scales;
+    const int32_t* offsets;
+    void* out;
+    long long ldo;
+    int out_type;
+};
+int mx_grad(const MxGrad& g, cudaStream_t s);
 
 }  // namespace qbh
 
