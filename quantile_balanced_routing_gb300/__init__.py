@@ -13,7 +13,6 @@ torch conveniences that allocate outputs with torch and call them:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -167,19 +166,24 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream or None
 
 
-def _allocating_on(stream):
-    """Allocate on the stream a call runs on, so that the memory is not reused
-    before that stream is done with it."""
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _refuse(what: str, msg: str):
+    raise QbmoeError(QBMOE_EINVAL, f"{what}: {msg}")
 
 
-def _check_device(what, *tensors):
-    """Every given tensor lives on the current CUDA device."""
+def _here(what: str, *tensors) -> int:
+    """The current stream's handle, once every given tensor is known to live on
+    the current CUDA device."""
     import torch
+    dev = -1
     for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
-            raise QbmoeError(QBMOE_EINVAL, f"{what}: tensors are on the current CUDA device (got {t.device})")
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or (dev >= 0 and d != dev):
+                _refuse(what, f"tensors are on the current CUDA device (got {t.device})")
+            dev = d
+    if dev != torch._C._cuda_getDevice():
+        _refuse(what, f"tensors are on the current CUDA device (got cuda:{dev})")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 # ---------------------------------------------------------------------------

@@ -2,14 +2,14 @@
 
 Argument checks and allocation around ``moe_balance_loss`` and
 ``moe_router_backward`` (see include/qbmoe.h for the formulas); every step runs
-in libqbmoe's CUDA kernels.
+in libqbmoe's CUDA kernels.  A call's host side is what a small batch costs, so
+the checks are plain comparisons without intermediate objects.
 """
 from __future__ import annotations
 
 from typing import NamedTuple
 
-from . import (MAX_EXPERTS, MAX_TOPK, QBMOE_BF16, QBMOE_EINVAL, QBMOE_F32, QbmoeError, _allocating_on, _check_device,
-               _p, _stream_ptr, load_library)
+from . import MAX_EXPERTS, MAX_TOPK, QBMOE_BF16, QBMOE_F32, QbmoeError, _here, _p, _refuse, load_library
 
 
 class BalanceLoss(NamedTuple):
@@ -19,36 +19,41 @@ class BalanceLoss(NamedTuple):
     tokens: "torch.Tensor"   # [S] int32, valid tokens
 
 
+def _row_stride(what, name, t, n):
+    """Elements between the rows of t [T, n]; torch leaves the stride of a single row free."""
+    ld, one = t.stride()
+    if t.shape[0] == 1:
+        ld = n
+    if one != 1 or ld < n:
+        _refuse(what, f"{name}: a token's values are contiguous")
+    return ld
+
+
 def _router_args(what, logits, idx, seq_offsets, token_mask):
-    """Checked (T, n, k, S, dtype code) of a routed batch."""
+    """Checked (T, n, k, S, dtype code, row stride) of a routed batch."""
     import torch
-
-    def need(ok, msg):
-        if not ok:
-            raise QbmoeError(QBMOE_EINVAL, f"{what}: {msg}")
-
-    need(logits.dim() == 2 and logits.dtype in (torch.float32, torch.bfloat16), "logits are fp32 or bf16 [T, n]")
+    if logits.dim() != 2 or (logits.dtype is not torch.float32 and logits.dtype is not torch.bfloat16):
+        _refuse(what, "logits are fp32 or bf16 [T, n]")
     T, n = logits.shape
-    need(T >= 1 and 2 <= n <= MAX_EXPERTS, f"T >= 1 and 2 <= n <= {MAX_EXPERTS}")
-    need(logits.stride(1) == 1 and (logits.stride(0) >= n or T == 1), "a token's logits are contiguous")
-    need(idx.dtype == torch.int32 and idx.dim() == 2 and idx.shape[0] == T and idx.is_contiguous(),
-         "idx is contiguous int32 [T, k]")
+    if T < 1 or n < 2 or n > MAX_EXPERTS:
+        _refuse(what, f"T >= 1 and 2 <= n <= {MAX_EXPERTS}")
+    ld = _row_stride(what, "logits", logits, n)
+    if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != T or not idx.is_contiguous():
+        _refuse(what, "idx is contiguous int32 [T, k]")
     k = idx.shape[1]
-    need(1 <= k <= min(n, MAX_TOPK), f"1 <= k <= min(n, {MAX_TOPK})")
+    if k < 1 or k > n or k > MAX_TOPK:
+        _refuse(what, f"1 <= k <= min(n, {MAX_TOPK})")
     S = 1
     if seq_offsets is not None:
-        need(seq_offsets.dtype == torch.int32 and seq_offsets.dim() == 1 and seq_offsets.shape[0] >= 2 and
-             seq_offsets.is_contiguous(), "seq_offsets is contiguous int32 [S + 1]")
+        if seq_offsets.dtype is not torch.int32 or seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2 or \
+                not seq_offsets.is_contiguous():
+            _refuse(what, "seq_offsets is contiguous int32 [S + 1]")
         S = seq_offsets.shape[0] - 1
-    if token_mask is not None:
-        need(token_mask.dtype in (torch.bool, torch.uint8) and tuple(token_mask.shape) == (T,) and
-             token_mask.is_contiguous(), "token_mask is contiguous bool or uint8 [T]")
-    _check_device(what, logits, idx, seq_offsets, token_mask)
-    return T, n, k, S, QBMOE_F32 if logits.dtype == torch.float32 else QBMOE_BF16
-
-
-def _ld(t):
-    return max(t.stride(0), t.shape[1])   # torch leaves the stride of a single row free
+    if token_mask is not None and (
+            (token_mask.dtype is not torch.bool and token_mask.dtype is not torch.uint8) or token_mask.dim() != 1 or
+            token_mask.shape[0] != T or not token_mask.is_contiguous()):
+        _refuse(what, "token_mask is contiguous bool or uint8 [T]")
+    return T, n, k, S, QBMOE_F32 if logits.dtype is torch.float32 else QBMOE_BF16, ld
 
 
 def balance_loss(logits, idx, seq_offsets=None, token_mask=None, stream=None) -> BalanceLoss:
@@ -59,18 +64,19 @@ def balance_loss(logits, idx, seq_offsets=None, token_mask=None, stream=None) ->
     sequence), token_mask [T] bool, False for padding.  The caller weighs and
     sums ``loss``; its gradient goes into :func:`router_backward`."""
     import torch
-    T, n, k, S, dt = _router_args("balance_loss", logits, idx, seq_offsets, token_mask)
-    lib, dev = load_library(), logits.device
+    if stream is not None:   # outputs and scratch are allocated on the stream that uses them
+        with torch.cuda.stream(stream):
+            return balance_loss(logits, idx, seq_offsets, token_mask)
+    T, n, k, S, dt, ld = _router_args("balance_loss", logits, idx, seq_offsets, token_mask)
+    cur = _here("balance_loss", logits, idx, seq_offsets, token_mask)
+    lib, dev, empty = load_library(), logits.device, torch.empty
+    r = BalanceLoss(empty(S, dtype=torch.float32, device=dev), empty((S, n), dtype=torch.int32, device=dev),
+                    empty((S, n), dtype=torch.float32, device=dev), empty(S, dtype=torch.int32, device=dev))
     nbytes = lib.qbmoe_balance_workspace_bytes(T, n, S)
-    with _allocating_on(stream):
-        r = BalanceLoss(torch.empty((S,), dtype=torch.float32, device=dev),
-                        torch.empty((S, n), dtype=torch.int32, device=dev),
-                        torch.empty((S, n), dtype=torch.float32, device=dev),
-                        torch.empty((S,), dtype=torch.int32, device=dev))
-        ws = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=dev)
-        rc = lib.moe_balance_loss(T, n, k, S, dt, _p(logits), _ld(logits), _p(idx), _p(seq_offsets), _p(token_mask),
-                                  _p(r.loss), _p(r.counts), _p(r.probs), _p(r.tokens), _p(ws), ws.numel(),
-                                  _stream_ptr(stream))
+    ws = empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = lib.moe_balance_loss(T, n, k, S, dt, logits.data_ptr(), ld, idx.data_ptr(), _p(seq_offsets), _p(token_mask),
+                              r.loss.data_ptr(), r.counts.data_ptr(), r.probs.data_ptr(), r.tokens.data_ptr(),
+                              ws.data_ptr(), nbytes, cur)
     if rc:
         raise QbmoeError(rc, "moe_balance_loss")
     return r
@@ -85,36 +91,36 @@ def router_backward(logits, idx, dw=None, dloss=None, counts=None, tokens=None, 
     with the counts and tokens that :func:`balance_loss` returned.  Either may
     be None.  out may be the logits themselves."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return router_backward(logits, idx, dw, dloss, counts, tokens, seq_offsets, token_mask, out)
     what = "router_backward"
-    T, n, k, S, dt = _router_args(what, logits, idx, seq_offsets, token_mask)
-
-    def need(ok, msg):
-        if not ok:
-            raise QbmoeError(QBMOE_EINVAL, f"{what}: {msg}")
-
-    need(dw is not None or dloss is not None, "needs dw or dloss")
-    if dw is not None:
-        need(dw.dtype == torch.float32 and tuple(dw.shape) == (T, k) and dw.is_contiguous(),
-             "dw is contiguous fp32 [T, k]")
-    if dloss is not None:
-        need(counts is not None and tokens is not None, "dloss needs counts and tokens")
-        need(dloss.dtype == torch.float32 and tuple(dloss.shape) == (S,) and dloss.is_contiguous(), "dloss is fp32 [S]")
-        need(counts.dtype == torch.int32 and tuple(counts.shape) == (S, n) and counts.is_contiguous(),
-             "counts is contiguous int32 [S, n]")
-        need(tokens.dtype == torch.int32 and tuple(tokens.shape) == (S,) and tokens.is_contiguous(),
-             "tokens is int32 [S]")
-    else:
+    T, n, k, S, dt, ld = _router_args(what, logits, idx, seq_offsets, token_mask)
+    if dw is None and dloss is None:
+        _refuse(what, "needs dw or dloss")
+    if dw is not None and (dw.dtype is not torch.float32 or dw.shape != idx.shape or not dw.is_contiguous()):
+        _refuse(what, "dw is contiguous fp32 [T, k]")
+    if dloss is None:
         counts = tokens = None
-    if out is not None:
-        need(out.dtype == logits.dtype and tuple(out.shape) == (T, n) and out.stride(1) == 1 and
-             (out.stride(0) >= n or T == 1), "out is [T, n] of the logits' type, a token's gradient contiguous")
-    _check_device(what, logits, dw, dloss, counts, tokens, out)
-    with _allocating_on(stream):
-        if out is None:
-            out = torch.empty((T, n), dtype=logits.dtype, device=logits.device)
-        rc = load_library().moe_router_backward(T, n, k, S, dt, _p(logits), _ld(logits), _p(idx), _p(seq_offsets),
-                                                _p(token_mask), _p(dw), _p(dloss), _p(counts), _p(tokens), _p(out),
-                                                _ld(out), _stream_ptr(stream))
+    else:
+        if counts is None or tokens is None:
+            _refuse(what, "dloss needs counts and tokens")
+        if dloss.dtype is not torch.float32 or dloss.shape != (S,) or not dloss.is_contiguous():
+            _refuse(what, "dloss is contiguous fp32 [S]")
+        if counts.dtype is not torch.int32 or counts.shape != (S, n) or not counts.is_contiguous():
+            _refuse(what, "counts is contiguous int32 [S, n]")
+        if tokens.dtype is not torch.int32 or tokens.shape != (S,) or not tokens.is_contiguous():
+            _refuse(what, "tokens is contiguous int32 [S]")
+    if out is not None and (out.dtype is not logits.dtype or out.shape != logits.shape):
+        _refuse(what, "out is [T, n] of the logits' type")
+    cur = _here(what, logits, idx, seq_offsets, token_mask, dw, dloss, counts, tokens, out)
+    if out is None:
+        out, ldg = torch.empty((T, n), dtype=logits.dtype, device=logits.device), n
+    else:
+        ldg = _row_stride(what, "out", out, n)
+    rc = load_library().moe_router_backward(T, n, k, S, dt, logits.data_ptr(), ld, idx.data_ptr(), _p(seq_offsets),
+                                            _p(token_mask), _p(dw), _p(dloss), _p(counts), _p(tokens), out.data_ptr(),
+                                            ldg, cur)
     if rc:
         raise QbmoeError(rc, "moe_router_backward")
     return out

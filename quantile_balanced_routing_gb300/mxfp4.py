@@ -8,8 +8,7 @@ from __future__ import annotations
 
 from typing import NamedTuple
 
-from . import (MAX_EXPERTS, QBMOE_BF16, QBMOE_EINVAL, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _allocating_on, _check_device, _p,
-               _stream_ptr, load_library)
+from . import MAX_EXPERTS, QBMOE_BF16, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _here, _p, _refuse, load_library
 
 BLOCK = 32
 
@@ -25,27 +24,30 @@ class Mxfp4(NamedTuple):
         return tuple(self.codes.shape[:-1]) + (2 * self.codes.shape[-1],)
 
 
-def _need(what, ok, msg):
-    if not ok:
-        raise QbmoeError(QBMOE_EINVAL, f"{what}: {msg}")
-
-
-def _check_mxfp4(what, name, t, dims):
+def _mxfp4_shape(what, name, t):
+    """Shape (..., K) of a well-formed Mxfp4."""
     import torch
-    _need(what, isinstance(t, Mxfp4), f"{name} is an Mxfp4 (codes, scales)")
-    _need(what, t.codes.dtype == torch.uint8 and t.scales.dtype == torch.uint8 and t.codes.is_contiguous() and
-          t.scales.is_contiguous(), f"{name}'s codes and scales are contiguous uint8")
-    _need(what, t.codes.dim() in dims and tuple(t.scales.shape) ==
-          tuple(t.codes.shape[:-1]) + (t.codes.shape[-1] * 2 // BLOCK,) and t.codes.shape[-1] % (BLOCK // 2) == 0 and
-          t.codes.shape[-1] > 0, f"{name} is codes [..., K/2] and scales [..., K/32], K a multiple of {BLOCK}")
+    if not isinstance(t, Mxfp4):
+        _refuse(what, f"{name} is an Mxfp4 (codes, scales)")
+    c, s = t
+    if c.dtype is not torch.uint8 or s.dtype is not torch.uint8 or not c.is_contiguous() or not s.is_contiguous():
+        _refuse(what, f"{name}'s codes and scales are contiguous uint8")
+    lead, half = c.shape[:-1], c.shape[-1]
+    if half == 0 or half % (BLOCK // 2) or s.dim() != c.dim() or s.shape[-1] * (BLOCK // 2) != half or \
+            s.shape[:-1] != lead:
+        _refuse(what, f"{name} is codes [..., K/2] and scales [..., K/32], K a multiple of {BLOCK}")
+    return (*lead, 2 * half)
 
 
 def _row_stride(what, name, t, align):
-    """Row stride of a matrix whose rows are contiguous."""
-    _need(what, t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1) and
-          (t.shape[0] <= 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % align == 0)),
-          f"{name} is a matrix with contiguous rows, their stride a multiple of {align} elements")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    """Elements between the rows of a matrix whose rows are contiguous."""
+    ld, one = t.stride()
+    rows, cols = t.shape
+    if rows <= 1:
+        ld = cols
+    if (one != 1 and cols != 1) or ld < cols or ld % align:
+        _refuse(what, f"{name} is a matrix with contiguous rows, their stride a multiple of {align} elements")
+    return ld
 
 
 def mxfp4_quantize(x, values=False, stream=None):
@@ -56,47 +58,52 @@ def mxfp4_quantize(x, values=False, stream=None):
     2^(floor(log2 max|x|) - 2); elements round to nearest, ties to even.  A matrix
     may have strided rows."""
     import torch
+    if stream is not None:   # outputs are allocated on the stream that writes them
+        with torch.cuda.stream(stream):
+            return mxfp4_quantize(x, values)
     what = "mxfp4_quantize"
-    _need(what, x.dtype in (torch.float32, torch.bfloat16) and x.dim() >= 1, "x is fp32 or bf16 [..., K]")
+    f32 = x.dtype is torch.float32
+    if (not f32 and x.dtype is not torch.bfloat16) or x.dim() < 1:
+        _refuse(what, "x is fp32 or bf16 [..., K]")
     K = x.shape[-1]
-    _need(what, K > 0 and K % BLOCK == 0, f"K is a multiple of {BLOCK}")
-    align = 4 if x.dtype == torch.float32 else 8
+    if K == 0 or K % BLOCK:
+        _refuse(what, f"K is a multiple of {BLOCK}")
     if x.dim() == 2:
-        ld = _row_stride(what, "x", x, align)
+        ld, lead, rows = _row_stride(what, "x", x, 4 if f32 else 8), (x.shape[0],), x.shape[0]
     else:
-        _need(what, x.is_contiguous(), "x is contiguous, or a matrix with contiguous rows")
-        ld = K
-    _check_device(what, x)
-    rows = x.numel() // K
-    with _allocating_on(stream):
-        q = Mxfp4(torch.empty(x.shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device),
-                  torch.empty(x.shape[:-1] + (K // BLOCK,), dtype=torch.uint8, device=x.device))
-        v = torch.empty(x.shape, dtype=x.dtype, device=x.device) if values else None
-        rc = load_library().moe_mxfp4_quantize(rows, K, QBMOE_F32 if x.dtype == torch.float32 else QBMOE_BF16, _p(x),
-                                               ld, _p(q.codes), _p(q.scales), _p(v), _stream_ptr(stream))
+        if not x.is_contiguous():
+            _refuse(what, "x is contiguous, or a matrix with contiguous rows")
+        ld, lead, rows = K, tuple(x.shape[:-1]), x.numel() // K
+    cur = _here(what, x)
+    dev, empty = x.device, torch.empty
+    codes = empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    scales = empty((*lead, K // BLOCK), dtype=torch.uint8, device=dev)
+    v = empty(x.shape, dtype=x.dtype, device=dev) if values else None
+    rc = load_library().moe_mxfp4_quantize(rows, K, QBMOE_F32 if f32 else QBMOE_BF16, x.data_ptr(), ld,
+                                           codes.data_ptr(), scales.data_ptr(), _p(v), cur)
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_quantize")
-    return (q, v) if values else q
+    return (Mxfp4(codes, scales), v) if values else Mxfp4(codes, scales)
 
 
 def _groups(what, w, offsets):
     """Checked (E, N, K) of weights [N, K], or [E, N, K] with offsets."""
     import torch
-    _check_mxfp4(what, "w", w, (2, 3))
-    shape = w.shape
-    E = shape[0] if len(shape) == 3 else 1
-    _need(what, (len(shape) == 3) == (offsets is not None) or E == 1, "w is [E, N, K] with offsets, [N, K] without")
-    _need(what, 1 <= E <= MAX_EXPERTS, f"1 to {MAX_EXPERTS} experts")
-    _need(what, shape[-2] > 0 and shape[-2] % 8 == 0, "N is a multiple of 8")
-    if offsets is not None:
-        _need(what, offsets.dtype == torch.int32 and tuple(offsets.shape) == (E + 1,) and offsets.is_contiguous(),
-              "offsets is contiguous int32 [E + 1]")
-    return E, shape[-2], shape[-1]
-
-
-def _workspace(lib, R, E, N, K, dev):
-    import torch
-    return torch.empty((max(lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K), 256),), dtype=torch.uint8, device=dev)
+    shape = _mxfp4_shape(what, "w", w)
+    if len(shape) == 3 and offsets is not None:
+        E, N, K = shape
+    elif len(shape) == 2 and offsets is None:
+        E, (N, K) = 1, shape
+    else:
+        _refuse(what, "w is [E, N, K] with offsets, [N, K] without")
+    if E < 1 or E > MAX_EXPERTS:
+        _refuse(what, f"1 to {MAX_EXPERTS} experts")
+    if N == 0 or N % 8:
+        _refuse(what, "N is a multiple of 8")
+    if offsets is not None and (offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or
+                                not offsets.is_contiguous()):
+        _refuse(what, "offsets is contiguous int32 [E + 1]")
+    return E, N, K
 
 
 def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
@@ -106,26 +113,31 @@ def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
     Grouped: w [E, N, K] and offsets [E + 1] int32, the rows in expert order;
     rows that no expert owns are left unwritten."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mxfp4_matmul(x, w, offsets)
     what = "mxfp4_matmul"
-    if isinstance(x, Mxfp4):
-        _check_mxfp4(what, "x", x, (2,))
-        rows, kind, scales = x.codes, QBMOE_MXFP4, x.scales
-        ld = x.shape[1]
-    else:
-        _need(what, x.dtype in (torch.float32, torch.bfloat16), "x is an Mxfp4 or fp32 or bf16 [R, K]")
-        rows, scales = x, None
-        kind, align = (QBMOE_F32, 4) if x.dtype == torch.float32 else (QBMOE_BF16, 8)
-        ld = _row_stride(what, "x", x, align)
-    R = rows.shape[0]
     E, N, K = _groups(what, w, offsets)
-    _need(what, x.shape[1] == K, "x and w have the same K")
-    _check_device(what, rows, scales, w.codes, w.scales, offsets)
-    lib = load_library()
-    with _allocating_on(stream):
-        y = torch.empty((R, N), dtype=torch.bfloat16, device=rows.device)
-        ws = _workspace(lib, R, E, N, K, y.device)
-        rc = lib.moe_mxfp4_matmul(R, E, N, K, kind, _p(rows), ld, _p(scales), _p(w.codes), _p(w.scales), _p(offsets),
-                                  _p(y), N, _p(ws), ws.numel(), _stream_ptr(stream))
+    if isinstance(x, Mxfp4):
+        shape = _mxfp4_shape(what, "x", x)
+        rows, kind, scales, ld = x.codes, QBMOE_MXFP4, x.scales, K
+    else:
+        shape, rows, scales = x.shape, x, None
+        kind = QBMOE_F32 if x.dtype is torch.float32 else QBMOE_BF16
+        if kind == QBMOE_BF16 and x.dtype is not torch.bfloat16:
+            _refuse(what, "x is an Mxfp4, or fp32 or bf16")
+    if len(shape) != 2 or shape[1] != K:
+        _refuse(what, "x is [R, K] with the K of w")
+    if scales is None:
+        ld = _row_stride(what, "x", x, 4 if kind == QBMOE_F32 else 8)
+    R = shape[0]
+    cur = _here(what, rows, scales, w.codes, w.scales, offsets)
+    lib, dev = load_library(), rows.device
+    y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    nbytes = lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = lib.moe_mxfp4_matmul(R, E, N, K, kind, rows.data_ptr(), ld, _p(scales), w.codes.data_ptr(),
+                              w.scales.data_ptr(), _p(offsets), y.data_ptr(), N, ws.data_ptr(), nbytes, cur)
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_matmul")
     return y
@@ -140,30 +152,37 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
     values that xq and w stand for; a trainer passes them straight through its
     quantisation.  need_dx / need_dw False: None in that place."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mxfp4_matmul_backward(dy, xq, w, offsets, need_dx, need_dw, dw_dtype)
     what = "mxfp4_matmul_backward"
-    _check_mxfp4(what, "xq", xq, (2,))
-    R = xq.codes.shape[0]
     E, N, K = _groups(what, w, offsets)
-    _need(what, xq.shape[1] == K, "xq and w have the same K")
-    _need(what, dy.dtype == torch.bfloat16 and tuple(dy.shape) == (R, N), "dy is bf16 [R, N]")
+    shape = _mxfp4_shape(what, "xq", xq)
+    if len(shape) != 2 or shape[1] != K:
+        _refuse(what, "xq is [R, K] with the K of w")
+    R = shape[0]
+    if dy.dtype is not torch.bfloat16 or dy.shape != (R, N):
+        _refuse(what, "dy is bf16 [R, N]")
     ld = _row_stride(what, "dy", dy, 8)
-    dw_dtype = dw_dtype or torch.float32
-    _need(what, dw_dtype in (torch.float32, torch.bfloat16), "dw is fp32 or bf16")
-    _check_device(what, dy, xq.codes, xq.scales, w.codes, w.scales, offsets)
-    lib, dev, dx, dw, rc = load_library(), dy.device, None, None, 0
-    with _allocating_on(stream):
-        ws = _workspace(lib, R, E, N, K, dev)
-        if need_dx:
-            dx = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
-            rc = lib.moe_mxfp4_dgrad(R, E, N, K, _p(dy), ld, _p(w.codes), _p(w.scales), _p(offsets), _p(dx), K,
-                                     _p(ws), ws.numel(), _stream_ptr(stream))
-            if rc:
-                raise QbmoeError(rc, "moe_mxfp4_dgrad")
-        if need_dw:
-            dw = torch.empty(w.shape, dtype=dw_dtype, device=dev)
-            rc = lib.moe_mxfp4_wgrad(R, E, N, K, _p(dy), ld, _p(xq.codes), _p(xq.scales), _p(offsets),
-                                     QBMOE_F32 if dw_dtype == torch.float32 else QBMOE_BF16, _p(dw), _p(ws),
-                                     ws.numel(), _stream_ptr(stream))
-            if rc:
-                raise QbmoeError(rc, "moe_mxfp4_wgrad")
+    f32 = dw_dtype is None or dw_dtype is torch.float32
+    if not f32 and dw_dtype is not torch.bfloat16:
+        _refuse(what, "dw is fp32 or bf16")
+    cur = _here(what, dy, xq.codes, xq.scales, w.codes, w.scales, offsets)
+    lib, dev, dx, dw = load_library(), dy.device, None, None
+    nbytes = lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if need_dx:
+        dx = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
+        rc = lib.moe_mxfp4_dgrad(R, E, N, K, dy.data_ptr(), ld, w.codes.data_ptr(), w.scales.data_ptr(), _p(offsets),
+                                 dx.data_ptr(), K, ws.data_ptr(), nbytes, cur)
+        if rc:
+            raise QbmoeError(rc, "moe_mxfp4_dgrad")
+    if need_dw:
+        dw = torch.empty((N, K) if offsets is None else (E, N, K), dtype=torch.float32 if f32 else torch.bfloat16,
+                         device=dev)
+        rc = lib.moe_mxfp4_wgrad(R, E, N, K, dy.data_ptr(), ld, xq.codes.data_ptr(), xq.scales.data_ptr(),
+                                 _p(offsets), QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), ws.data_ptr(), nbytes,
+                                 cur)
+        if rc:
+            raise QbmoeError(rc, "moe_mxfp4_wgrad")
     return dx, dw
