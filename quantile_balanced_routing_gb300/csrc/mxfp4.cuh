@@ -23,9 +23,9 @@ void mx_set_stall(int on);
 
 int sm_count();
 // 2-D row-major tensor map: cols elements a row (row stride ld bytes), box
-// {box_cols, box_rows}, 128-byte swizzle, zeros outside.
+// {box_cols, box_rows}, 128-byte swizzle unless `plain`, zeros outside.
 bool encode_rows(CUtensorMap* m, CUtensorMapDataType type, const void* base, long long rows, long long cols,
-                 long long ld_bytes, int box_cols, int box_rows);
+                 long long ld_bytes, int box_cols, int box_rows, bool plain = false);
 
 // Rows of fp32 or bf16 (x_type) to codes and scales, and the values if wanted (mxfp4.cu).
 int mx_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes, uint8_t* scales,
@@ -109,34 +109,41 @@ QB_DEV void load_groups(const Groups& g, const int32_t* offsets, int E, int R, i
     __syncthreads();
 }
 
-// Walks the tiles blockIdx.x, blockIdx.x + gridDim.x, ...: m-tile fastest, then
-// the expert's row tiles.  An expert's rows are split into equal tiles
-// (multiples of 16), so that tiles sharing a weight tile run at one pace.
+// Walks the tiles blockIdx.x, blockIdx.x + gridDim.x, ... of a grid whose m
+// index is fastest, then the row tiles of all experts.  Every lane of the warp
+// calls: the expert is found 32 experts a step (one at a time, a stride of 304
+// tiles over experts with a few rows each cost 7 us a tile).  An expert's
+// rows are split into equal tiles (multiples of 16), so that tiles sharing a
+// weight tile run at one pace.
 template <int BN>
 struct Walker {
     int ntg, m, g;
     int row0, nrows;   // of the current tile
     QB_DEV void seek(const Groups& gr, int E) {
-        while (g + 1 < E && gr.toff[g + 1] <= ntg) ++g;
+        const int lane = threadIdx.x & 31;
+        for (;;) {
+            const int e = g + 1 + lane;
+            const unsigned le = __ballot_sync(0xffffffffu, e < E && gr.toff[e] <= ntg);
+            g += __popc(le);   // toff never falls: the lanes that pass come first
+            if (le != 0xffffffffu) break;
+        }
         const int t0 = gr.toff[g], nt = gr.toff[g + 1] - t0;
         const int a = gr.seg[g], len = gr.seg[g + 1] - a;
         const int per = ((nt == 1 ? len : (len + nt - 1) / nt) + 15) & ~15;
         row0 = a + (ntg - t0) * per;
         nrows = min(per, a + len - row0);
     }
-    QB_DEV void start(const Groups& gr, int E, int m_total, int first) {
-        ntg = first / m_total;
-        m = first - ntg * m_total;
+    QB_DEV void start(const Groups& gr, int E, int m_total) {
+        ntg = blockIdx.x / m_total;
+        m = blockIdx.x - ntg * m_total;
         g = 0;
         if (ntg < gr.toff[E]) seek(gr, E);
     }
-    QB_DEV bool next(const Groups& gr, int E, int m_total, int step) {
+    QB_DEV void next(const Groups& gr, int E, int m_total) {
         const int was = ntg;
-        m += step;
+        m += gridDim.x;
         while (m >= m_total) m -= m_total, ++ntg;
-        if (ntg >= gr.toff[E]) return false;
-        if (ntg != was) seek(gr, E);
-        return true;
+        if (ntg != was && ntg < gr.toff[E]) seek(gr, E);
     }
 };
 

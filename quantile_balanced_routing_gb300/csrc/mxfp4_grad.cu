@@ -76,11 +76,11 @@ struct Tiles {
     }
     QB_DEV void start(const Params& p, const Groups& gr) {
         t = blockIdx.x;
-        if (!kWeights) w.start(gr, p.E, p.n_tiles, t);
+        if (!kWeights) w.start(gr, p.E, p.n_tiles);
     }
     QB_DEV void next(const Params& p, const Groups& gr) {
         t += gridDim.x;
-        if (!kWeights) w.next(gr, p.E, p.n_tiles, gridDim.x);
+        if (!kWeights) w.next(gr, p.E, p.n_tiles);
     }
     QB_DEV Tile get(const Params& p, const Groups& gr) const {
         Tile x;
@@ -173,21 +173,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
     Tiles<kWeights> it;
     const int n_tiles = it.count(p, gr);
     it.start(p, gr);
+    auto expired = [&] {
+        set_status(p.status, QBMOE_ETIMEOUT);
+        *abort_flag = 1;
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------- TMA of A
         uint32_t issued = 0, last_par = 0;
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            for (; it.t < n_tiles && !*abort_flag; it.next(p, gr)) {
-                const Tile x = it.get(p, gr);
-                for (int c0 = 0; c0 < x.len; c0 += kC) {
-                    if (!tc::mbar_wait(&empty[s], ph ^ 1u, lim)) {
-                        set_status(p.status, QBMOE_ETIMEOUT);
-                        *abort_flag = 1;
-                        break;
-                    }
+        int s = 0;
+        uint32_t ph = 0;
+        for (; it.t < n_tiles; it.next(p, gr)) {
+            const Tile x = it.get(p, gr);
+            int stop = 0;
+            if (lane == 0) {
+                stop = *abort_flag;
+                for (int c0 = 0; c0 < x.len && !stop; c0 += kC) {
+                    if (!tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim)) { expired(); stop = 1; break; }
                     uint8_t* A = a_ring + s * kABytes;
                     if (kWeights && x.len - c0 < kC) {
                         tc::mbar_arrive(&full[s]);   // the converters write this stage's A
@@ -205,12 +207,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                     if (++s == kStages) { s = 0; ph ^= 1u; }
                 }
             }
+            if (__shfl_sync(0xffffffffu, stop, 0)) break;
         }
-        __syncwarp();
         __syncthreads();
         if (lane == 0 && *abort_flag)
-            for (int s = 0; s < kStages; ++s)
-                if ((issued >> s) & 1u) tc::mbar_wait(&full[s], (last_par >> s) & 1u, kDrainWait);
+            for (int i = 0; i < kStages; ++i)
+                if ((issued >> i) & 1u) tc::mbar_wait(&full[i], (last_par >> i) & 1u, kDrainWait);
     } else if (warp >= kConvWarp && warp < kEpiWarp) {
         // ---------------------------------------------------------- converters
         // Thread (r, b) of a stage: steps r and r + 32, column block b (32
@@ -271,11 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 }
                 int w = 1;
                 if (lane == 0) {
-                    w = !*abort_flag && tc::mbar_wait(&empty[s], ph ^ 1u, lim);
-                    if (!w) {
-                        set_status(p.status, *abort_flag ? 0 : QBMOE_ETIMEOUT);
-                        *abort_flag = 1;
-                    }
+                    w = !*abort_flag && tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim);
+                    if (!w && !*abort_flag) expired();
                 }
                 if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
                 if (own_a) {
@@ -379,11 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             const Tile x = it.get(p, gr);
             if (lane == 0) {
                 if (!dead && *abort_flag) dead = true;
-                if (!dead && !tc::mbar_wait(&acce[ab], aph ^ 1u, lim)) {
-                    set_status(p.status, QBMOE_ETIMEOUT);
-                    *abort_flag = 1;
-                    dead = true;
-                }
+                if (!dead && !tc::mbar_wait_spin(&acce[ab], aph ^ 1u, lim)) { expired(); dead = true; }
                 go_flag[h & 1] = dead ? 0 : 1;
             }
             if ((ab ^= 1) == 0) aph ^= 1u;
@@ -395,11 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             for (int c0 = 0; c0 < x.len; c0 += kC) {
                 if (lane == 0) {
                     if (!dead && *abort_flag) dead = true;
-                    if (!dead && !tc::mbar_wait(&full[s], ph, lim)) {
-                        set_status(p.status, QBMOE_ETIMEOUT);
-                        *abort_flag = 1;
-                        dead = true;
-                    }
+                    if (!dead && !tc::mbar_wait_spin(&full[s], ph, lim)) { expired(); dead = true; }
                 }
                 __syncwarp();
                 tc::named_bar_sync(kHandoffBar, 64);
@@ -425,10 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             int ok = 1;
             if (lane == 0) {
                 ok = tc::mbar_wait(&accf[ab], fph, lim);
-                if (!ok) {
-                    set_status(p.status, QBMOE_ETIMEOUT);
-                    *abort_flag = 1;
-                }
+                if (!ok) expired();
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc::tc_fence_after();

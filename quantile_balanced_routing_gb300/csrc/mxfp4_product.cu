@@ -11,16 +11,20 @@
 //
 // One persistent warp-specialised kernel.  A stage is 256 elements of K: the
 // packed codes of 128 weight rows and of the tile's rows (128 bytes each, TMA,
-// 128-byte swizzle) and their scales.
-//   warp 0     TMA producer (one lane)
-//   warp 1     TMEM owner, MMA issuer (one lane): copies a stage's scales to
-//              TMEM (tcgen05.cp, in order with the MMAs), 4 x K = 64 MMAs, one
-//              commit that frees the stage
-//   warp 2     the issuer's waiter (an mbarrier wait by the issuing thread
-//              slows its MMA stream): waits, then releases it through a named barrier
-//   warps 3, 4 scale loaders (even and odd stages): global -> registers one
-//              stage ahead -> shared memory in the order tcgen05.cp wants
-//   warps 5-8  epilogue: TMEM -> per-warp transpose in shared memory -> bf16
+// 128-byte swizzle); their scales come in groups of two stages (16 bytes a row).
+//   warp 0      TMA producer (one lane): codes, and the scale groups where the
+//               scale rows are multiples of 16 bytes (K % 512 == 0)
+//   warp 1      TMEM owner, MMA issuer (one lane): 4 x K = 64 MMAs a stage and
+//               one commit that frees it
+//   warp 2      the issuer's waiter (an mbarrier wait by the issuing thread
+//               slows its MMA stream): waits, then releases it through a named barrier
+//   warp 3      scale loader for any other K: global -> registers a group ahead
+//               -> shared memory
+//   warps 4-7   scale writers, one per TMEM lane quarter: a group's scales from
+//               shared memory to the stages' TMEM slots (tcgen05.st).  Copying them
+//               with tcgen05.cp from the issuer cost it 6 more instructions a
+//               stage: 813 cycles of issue, against 375 of MMAs at N = 192.
+//   warps 8-11  epilogue: TMEM -> per-warp transpose in shared memory -> bf16
 // Two accumulators alternate, so a tile's epilogue overlaps the next tile's
 // main loop.  Every mbarrier wait is bounded: on expiry the kernel records
 // QBMOE_ETIMEOUT, stops, lets its own copies and MMAs finish and frees TMEM.
@@ -37,9 +41,8 @@ using namespace qb;
 
 constexpr int kStageK = 256;                 // elements of K per stage (128 bytes of codes a row)
 constexpr int kABytes = 128 * 128;           // weight codes of a stage
-constexpr int kSfaBytes = 1024;              // weight scales of a stage: two 512-byte blocks (K = 128 each)
-constexpr int kThreads = 288;
-constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfWarp = 3, kEpiWarp = 5;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8;
 constexpr int kHandoffBar = 1;
 constexpr int kEpiRow = 36;                  // transpose row: 32 features, 4 words of padding
 constexpr long long kDefaultWait = 1LL << 17;   // polls (<= 20 us each) before a wait expires
@@ -47,13 +50,15 @@ constexpr long long kDrainWait = 1LL << 12;
 
 struct Params {
     CUtensorMap a, b;                        // codes of the weights [E N, K / 2] and of the rows [R, K / 2]
-    const uint8_t* a_sc;                     // [E N, K / 32]
-    const uint8_t* b_sc;                     // [R, K / 32]
+    CUtensorMap a_sf, b_sf;                  // their scales [., K / 32] (K % 512 == 0)
+    const uint8_t* a_sc;
+    const uint8_t* b_sc;
     const int32_t* offsets;
     __nv_bfloat16* y;
     long long ldy;
     int R, E, N, K, nkb, m_total;
-    int sf_bytes;                            // bytes of a scale load: 8 (K % 256 == 0), 4 (K % 128 == 0) or 1
+    int sf_tma;                              // scale groups by TMA
+    int sf_bytes;                            // else bytes of a scale load: 8 (K % 256 == 0), 4 (K % 128 == 0) or 1
     int weights_ready;                       // nothing enqueued just before this kernel wrote the weights or the offsets
     int* status;
     long long wait_limit;
@@ -64,16 +69,17 @@ template <int BN>
 struct Shape {
     static constexpr int kBox = BN >= 32 ? 32 : 16;              // rows per TMA copy of B
     static constexpr int kNB = (BN + 127) / 128;                 // 128-row blocks of B's scales
+    static constexpr int kBJ = (BN + 31) / 32;                   // 32-row blocks
     static constexpr int kBBytes = BN * 128;
-    static constexpr int kSfbBytes = 2 * kNB * 512;
-    static constexpr int kStage = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-    static constexpr int kSfCols = 2 * 4 + 2 * 4 * kNB;          // TMEM columns of a stage's scales
-    static constexpr int kColsUsed = 2 * BN + 2 * kSfCols;       // two accumulators, two scale slots
-    static constexpr uint32_t kCols = kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
+    static constexpr int kStage = kABytes + kBBytes;
+    static constexpr int kSfBytes = (128 + BN) * 16;             // scales of a group
+    static constexpr int kSfCols = 8 + 8 * kNB;                  // TMEM columns of a stage's scales
+    static constexpr int stages = BN == 64 ? 7 : BN == 128 ? 5 : 4;
+    static constexpr int kColsUsed = 2 * BN + stages * kSfCols;  // two accumulators, a scale slot per stage
+    static constexpr uint32_t kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
     static_assert(kColsUsed <= 512, "TMEM columns");
-    static constexpr int stages = BN == 16 ? 4 : BN == 64 ? 7 : BN == 128 ? 5 : 4;
     static constexpr int smem(int E) {
-        return 1024 + stages * kStage + 4 * 16 * kEpiRow * 4 + (2 * (E + 1) + 64) * 4 + 256;
+        return 1024 + stages * kStage + 2 * kSfBytes + 4 * 16 * kEpiRow * 4 + (2 * (E + 1) + 64) * 4 + 256;
     }
 };
 
@@ -92,31 +98,32 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-// 32 rows of 16 bytes (512 contiguous bytes) to 4 TMEM columns, the 32 lanes
-// repeated in the four lane quarters.
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t saddr) {
-    // no swizzle; 8-row groups 128 bytes apart; descriptor version 1
-    const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-// The 8 scale bytes of one row and stage; bytes past the row's end are 0 (their codes are, too).
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int pitch, int kb, int bytes) {
-    const uint8_t* p = row + kb * 8;
-    if (bytes == 8) return __ldg(reinterpret_cast<const uint2*>(p));
-    const int left = pitch - kb * 8;
-    uint2 v = make_uint2(0, 0);
-    if (bytes == 4) {
-        v.x = __ldg(reinterpret_cast<const uint32_t*>(p));
-        if (left > 4) v.y = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
+// 16 scale bytes of one row (a group of two stages); bytes past the row's end
+// are 0 (their codes are, too).
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int at, int bytes) {
+    const uint8_t* p = row + at;
+    const int left = pitch - at;
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (bytes == 8) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        v[0] = x.x, v[1] = x.y;
+        if (left > 8) {
+            const uint2 y = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+            v[2] = y.x, v[3] = y.y;
+        }
+    } else if (bytes == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (left > 4 * i) v[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = i < left ? __ldg(p + i) : 0u;
-            if (i < 4) v.x |= b << (8 * i); else v.y |= b << (8 * (i - 4));
-        }
+        for (int i = 0; i < 16; ++i)
+            if (left > i) v[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
     }
-    return v;
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 template <int BN>
@@ -127,12 +134,13 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* a_ring = smem;
     uint8_t* b_ring = a_ring + S * kABytes;
-    uint8_t* sfa_ring = b_ring + S * Sh::kBBytes;
-    uint8_t* sfb_ring = sfa_ring + S * kSfaBytes;
-    float* epi = reinterpret_cast<float*>(sfb_ring + S * Sh::kSfbBytes);    // [4][16][kEpiRow]
+    uint8_t* sf_ring = b_ring + S * Sh::kBBytes;                 // [2][128 + BN rows][16]
+    float* epi = reinterpret_cast<float*>(sf_ring + 2 * Sh::kSfBytes);    // [4][16][kEpiRow]
     uint64_t* full = reinterpret_cast<uint64_t*>(epi + 4 * 16 * kEpiRow);
     uint64_t* empty = full + S;
-    uint64_t* accf = empty + S;
+    uint64_t* sf_full = empty + S;
+    uint64_t* sf_empty = sf_full + 2;
+    uint64_t* accf = sf_empty + 2;
     uint64_t* acce = accf + 2;
     uint64_t* drain = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -147,10 +155,12 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     const long long lim = p.wait_limit > 0 ? p.wait_limit : kDefaultWait;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            tc::mbar_init(&full[s], 2);      // the TMA producer and the stage's scale loader
+            tc::mbar_init(&full[s], 5);      // the TMA producer and the four scale writers
             tc::mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(&sf_full[a], 1);
+            tc::mbar_init(&sf_empty[a], 4);
             tc::mbar_init(&accf[a], 1);
             tc::mbar_init(&acce[a], 4);
         }
@@ -172,29 +182,44 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     const uint32_t tbase = *tmem_slot;
     const int n_tiles = gr.toff[p.E] * p.m_total;
     Walker<BN> w;
-    w.start(gr, p.E, p.m_total, blockIdx.x);
+    w.start(gr, p.E, p.m_total);
     const int first = blockIdx.x, step = gridDim.x;
+    auto expired = [&] {
+        set_status(p.status, QBMOE_ETIMEOUT);
+        *abort_flag = 1;
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
-        uint32_t issued = 0, last_par = 0;
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            bool rows_ready = !p.weights_ready;
-            for (int t = first; t < n_tiles && !*abort_flag; t += step, w.next(gr, p.E, p.m_total, step)) {
-                const int n_eff = (w.nrows + 15) & ~15;
-                const int boxes = (n_eff + Sh::kBox - 1) / Sh::kBox;
+        uint32_t issued = 0, last_par = 0, sf_issued = 0, sf_par = 0;
+        int s = 0, gs = 0;
+        uint32_t ph = 0, gph = 0;
+        bool rows_ready = !p.weights_ready;
+        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total)) {
+            int stop = 0;
+            if (lane == 0) {
+                const int boxes = (w.nrows + Sh::kBox - 1) / Sh::kBox;
                 const int ya = w.g * p.N + w.m * 128;
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!tc::mbar_wait(&empty[s], ph ^ 1u, lim)) {
-                        set_status(p.status, QBMOE_ETIMEOUT);
-                        *abort_flag = 1;
-                        break;
+                stop = *abort_flag;
+                for (int kb = 0; kb < p.nkb && !stop; ++kb) {
+                    if (p.sf_tma && (kb & 1) == 0) {
+                        if (!tc::mbar_wait_spin(&sf_empty[gs], gph ^ 1u, lim)) { expired(); stop = 1; break; }
+                        uint8_t* SF = sf_ring + gs * Sh::kSfBytes;
+                        tc::mbar_expect_tx(&sf_full[gs], Sh::kSfBytes);
+                        tc::tma_load_2d(SF, &p.a_sf, &sf_full[gs], kb * 8, ya);
+                        if (!rows_ready) {   // the rows' codes come from the kernel before this one
+                            pdl_wait();
+                            rows_ready = true;
+                        }
+                        tc::tma_load_2d(SF + 128 * 16, &p.b_sf, &sf_full[gs], kb * 8, w.row0);
+                        sf_issued |= 1u << gs;
+                        sf_par = (sf_par & ~(1u << gs)) | (gph << gs);
+                        if ((gs ^= 1) == 0) gph ^= 1u;
                     }
+                    if (!tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim)) { expired(); stop = 1; break; }
                     tc::mbar_expect_tx(&full[s], kABytes + boxes * Sh::kBox * 128);
                     tc::tma_load_2d(a_ring + s * kABytes, &p.a, &full[s], kb * 128, ya);
-                    if (!rows_ready) {   // the rows' codes come from the kernel before this one
+                    if (!rows_ready) {
                         pdl_wait();
                         rows_ready = true;
                     }
@@ -206,91 +231,126 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
+            if (__shfl_sync(0xffffffffu, stop, 0)) break;
         }
-        __syncwarp();
         __syncthreads();
-        if (lane == 0 && *abort_flag)   // every copy has landed before shared memory is released
-            for (int s = 0; s < S; ++s)
-                if ((issued >> s) & 1u) tc::mbar_wait(&full[s], (last_par >> s) & 1u, kDrainWait);
-    } else if (warp == kSfWarp || warp == kSfWarp + 1) {
-        // ---------------------------------------------------------- scale loaders
-        // Loader v takes the stages it = v, v + 2, ... of the CTA's sequence of
-        // (tile, K block) pairs and has the next one's bytes in registers while
-        // it waits for a slot.
-        constexpr int kBJ = BN / 32 + (BN % 32 ? 1 : 0);
-        const int v = warp - kSfWarp, pitch = p.K / 32;
-        const long long last_a = (long long)p.E * p.N - 1;
-        uint2 ra[4], rb[kBJ];
-        auto fetch = [&](int kb) {
+        if (lane == 0 && *abort_flag) {   // every copy has landed before shared memory is released
+            for (int i = 0; i < S; ++i)
+                if ((issued >> i) & 1u) tc::mbar_wait(&full[i], (last_par >> i) & 1u, kDrainWait);
+            for (int i = 0; i < 2; ++i)
+                if ((sf_issued >> i) & 1u) tc::mbar_wait(&sf_full[i], (sf_par >> i) & 1u, kDrainWait);
+        }
+    } else if (warp == kSfLoadWarp) {
+        // ---------------------------------------------------------- scale loader
+        // Lane l takes rows l, l + 32, ... of the weight tile and of the row tile;
+        // the next group's bytes are in registers while it waits for a slot.
+        if (!p.sf_tma) {
+            const int pitch = p.K / 32;
+            const long long last_a = (long long)p.E * p.N - 1;
+            uint4 ra[4], rb[Sh::kBJ];
+            auto fetch = [&](int kb) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const long long row = min((long long)w.g * p.N + w.m * 128 + lane + 32 * j, last_a);
-                ra[j] = load_scales(p.a_sc + row * pitch, pitch, kb, p.sf_bytes);
-            }
+                for (int j = 0; j < 4; ++j) {
+                    const long long row = min((long long)w.g * p.N + w.m * 128 + lane + 32 * j, last_a);
+                    ra[j] = load_scales(p.a_sc + row * pitch, pitch, kb * 8, p.sf_bytes);
+                }
 #pragma unroll
-            for (int j = 0; j < kBJ; ++j) {
-                const int r = min(w.row0 + lane + 32 * j, p.R - 1);
-                rb[j] = 32 * j < w.nrows ? load_scales(p.b_sc + (long long)r * pitch, pitch, kb, p.sf_bytes)
-                                         : make_uint2(0, 0);
+                for (int j = 0; j < Sh::kBJ; ++j) {
+                    const int r = min(w.row0 + lane + 32 * j, p.R - 1);
+                    rb[j] = 32 * j < w.nrows ? load_scales(p.b_sc + (long long)r * pitch, pitch, kb * 8, p.sf_bytes)
+                                             : make_uint4(0, 0, 0, 0);
+                }
+            };
+            if (p.weights_ready) pdl_wait();
+            int gs = 0, kb = 0, t = first;
+            uint32_t gph = 0;
+            if (t < n_tiles) fetch(0);
+            while (t < n_tiles) {
+                int ok = 1;
+                if (lane == 0) {
+                    ok = !*abort_flag;
+                    if (ok && !tc::mbar_wait_spin(&sf_empty[gs], gph ^ 1u, lim)) { expired(); ok = 0; }
+                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                uint4* SF = reinterpret_cast<uint4*>(sf_ring + gs * Sh::kSfBytes);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) SF[lane + 32 * j] = ra[j];
+#pragma unroll
+                for (int j = 0; j < Sh::kBJ; ++j)
+                    if (lane + 32 * j < BN) SF[128 + lane + 32 * j] = rb[j];
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sf_full[gs]);
+                if ((gs ^= 1) == 0) gph ^= 1u;
+                kb += 2;
+                if (kb >= p.nkb) {
+                    kb = 0;
+                    t += step;
+                    if (t < n_tiles) w.next(gr, p.E, p.m_total);
+                }
+                if (t < n_tiles) fetch(kb);
             }
-        };
-        if (p.weights_ready) pdl_wait();
-        int t = first, kb = v;
-        bool have = t < n_tiles;
-        auto settle = [&] {   // kb may run past its tile: into the next ones
-            while (have && kb >= p.nkb) {
-                kb -= p.nkb;
-                t += step;
-                have = t < n_tiles && w.next(gr, p.E, p.m_total, step);
-            }
-        };
-        settle();
-        if (have) fetch(kb);
-        int s = v;
-        uint32_t ph = 0;
-        while (s >= S) { s -= S; ph ^= 1u; }
-        while (have) {
-            int ok = 1;
-            if (lane == 0) {
-                ok = !*abort_flag && tc::mbar_wait(&empty[s], ph ^ 1u, lim);
-                if (!ok) {
-                    set_status(p.status, *abort_flag ? 0 : QBMOE_ETIMEOUT);
-                    *abort_flag = 1;
+        }
+        __syncthreads();
+    } else if (warp >= kSfWarp && warp < kSfWarp + 4) {
+        // ---------------------------------------------------------- scale writers
+        // The MMA reads the scale words of row r (four bytes: K = 128) from lane
+        // r % 32, column r / 32 of a slot, in each lane quarter.
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        int s = 0, gs = 0;
+        uint32_t ph = 0, gph = 0;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += step) {
+            for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += 2) {
+                uint4 ra[4], rb[4 * Sh::kNB];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (kb0 + u >= p.nkb) break;
+                    int go = 1;
+                    if (lane == 0) {
+                        go = !*abort_flag && (u || tc::mbar_wait_spin(&sf_full[gs], gph, lim)) &&
+                             tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim);
+                        if (!go && !*abort_flag) expired();
+                    }
+                    if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
+                    if (u == 0) {
+                        const uint4* SF = reinterpret_cast<const uint4*>(sf_ring + gs * Sh::kSfBytes);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) ra[j] = SF[lane + 32 * j];
+#pragma unroll
+                        for (int j = 0; j < 4 * Sh::kNB; ++j)
+                            rb[j] = lane + 32 * j < BN ? SF[128 + lane + 32 * j] : make_uint4(0, 0, 0, 0);
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&sf_empty[gs]);   // the group is in registers
+                        if ((gs ^= 1) == 0) gph ^= 1u;
+                    }
+                    tc::tc_fence_after();
+                    const uint32_t slot = tbase + lanes + 2 * BN + s * Sh::kSfCols;
+                    uint32_t va[8], vb[8 * Sh::kNB];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) va[4 * c + j] = word(ra[j], 2 * u + c);
+#pragma unroll
+                        for (int j = 0; j < 4 * Sh::kNB; ++j) vb[4 * Sh::kNB * c + j] = word(rb[j], 2 * u + c);
+                    }
+                    tc::tmem_st8(slot, va);
+                    if constexpr (Sh::kNB == 2) tc::tmem_st16(slot + 8, vb); else tc::tmem_st8(slot + 8, vb);
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&full[s]);
+                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            uint4* A = reinterpret_cast<uint4*>(sfa_ring + s * kSfaBytes);
-            A[lane] = make_uint4(ra[0].x, ra[1].x, ra[2].x, ra[3].x);
-            A[32 + lane] = make_uint4(ra[0].y, ra[1].y, ra[2].y, ra[3].y);
-            uint4* B = reinterpret_cast<uint4*>(sfb_ring + s * Sh::kSfbBytes);
-#pragma unroll
-            for (int nb = 0; nb < Sh::kNB; ++nb) {
-                uint32_t x[4] = {}, y[4] = {};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * nb + j < kBJ) x[j] = rb[4 * nb + j].x, y[j] = rb[4 * nb + j].y;
-                B[nb * 32 + lane] = make_uint4(x[0], x[1], x[2], x[3]);
-                B[(Sh::kNB + nb) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-            kb += 2;
-            settle();
-            if (have) fetch(kb);
-            tc::fence_proxy_async_smem();   // generic-proxy writes -> tcgen05.cp reads
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&full[s]);
-            s += 2;
-            if (s >= S) { s -= S; ph ^= 1u; }
         }
         __syncthreads();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
-        int s = 0, ab = 0, h = 0, sb = 0;
+        int s = 0, ab = 0, h = 0;
         const uint64_t a0 = tc::desc_sw128(tc::smem_u32(a_ring)), b0 = tc::desc_sw128(tc::smem_u32(b_ring));
-        const uint32_t sfa0 = tc::smem_u32(sfa_ring), sfb0 = tc::smem_u32(sfb_ring);
-        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total, step)) {
+        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total)) {
             const uint32_t n_eff = (w.nrows + 15) & ~15;
-            const uint32_t id[2] = {idesc_mxf4(n_eff, 0), idesc_mxf4(n_eff, 2)};
-            const int nb = n_eff > 128 ? 2 : 1;
+            const uint32_t id0 = idesc_mxf4(n_eff, 0), id2 = idesc_mxf4(n_eff, 2);
             tc::named_bar_sync(kHandoffBar, 64);   // the accumulator is free (or stop)
             const bool go = go_flag[h & 1] != 0;
             ++h;
@@ -300,31 +360,23 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
                 tc::named_bar_sync(kHandoffBar, 64);   // stage s has landed
                 if (lane == 0) {
                     tc::tc_fence_after();
-                    const uint32_t ca = tbase + 2 * BN + sb * Sh::kSfCols, cb = ca + 8;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        cp_scales(ca + 4 * c, sfa0 + s * kSfaBytes + 512 * c);
-                        for (int i = 0; i < nb; ++i)
-                            cp_scales(cb + 4 * (Sh::kNB * c + i), sfb0 + s * Sh::kSfbBytes + 512 * (Sh::kNB * c + i));
-                    }
+                    const uint32_t ca = tbase + 2 * BN + s * Sh::kSfCols, cb = ca + 8;
                     const uint64_t ad = a0 + (uint64_t)(s * (kABytes >> 4)), bd = b0 + (uint64_t)(s * (Sh::kBBytes >> 4));
                     const int left = p.K - kb * kStageK;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk * 64 < left)
-                            mma_mxf4(d, ad + 2 * kk, bd + 2 * kk, id[kk & 1], ca + 4 * (kk >> 1),
-                                     cb + 4 * Sh::kNB * (kk >> 1), (kb | kk) != 0);
+                    mma_mxf4(d, ad, bd, id0, ca, cb, kb != 0);
+                    if (left > 64) mma_mxf4(d, ad + 2, bd + 2, id2, ca, cb, 1);
+                    if (left > 128) mma_mxf4(d, ad + 4, bd + 4, id0, ca + 4, cb + 4 * Sh::kNB, 1);
+                    if (left > 192) mma_mxf4(d, ad + 6, bd + 6, id2, ca + 4, cb + 4 * Sh::kNB, 1);
                     tc::tc_commit(&empty[s]);
                 }
                 __syncwarp();
-                sb ^= 1;
                 if (++s == S) s = 0;
             }
             if (lane == 0 && !(p.stall && t == first)) tc::tc_commit(&accf[ab]);
             __syncwarp();
             ab ^= 1;
         }
-        if (lane == 0) {   // every MMA and copy of this thread is done before TMEM is freed
+        if (lane == 0) {   // every MMA of this thread is done before TMEM is freed
             tc::tc_commit(drain);
             tc::mbar_wait(drain, 0, kDefaultWait);
         }
@@ -338,11 +390,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         for (int t = first; t < n_tiles; t += step) {
             if (lane == 0) {
                 if (!dead && *abort_flag) dead = true;
-                if (!dead && !tc::mbar_wait(&acce[ab], aph ^ 1u, lim)) {
-                    set_status(p.status, QBMOE_ETIMEOUT);
-                    *abort_flag = 1;
-                    dead = true;
-                }
+                if (!dead && !tc::mbar_wait_spin(&acce[ab], aph ^ 1u, lim)) { expired(); dead = true; }
                 go_flag[h & 1] = dead ? 0 : 1;
             }
             if ((ab ^= 1) == 0) aph ^= 1u;
@@ -354,11 +402,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if (lane == 0) {
                     if (!dead && *abort_flag) dead = true;
-                    if (!dead && !tc::mbar_wait(&full[s], ph, lim)) {
-                        set_status(p.status, QBMOE_ETIMEOUT);
-                        *abort_flag = 1;
-                        dead = true;
-                    }
+                    if (!dead && !tc::mbar_wait_spin(&full[s], ph, lim)) { expired(); dead = true; }
                 }
                 __syncwarp();
                 tc::named_bar_sync(kHandoffBar, 64);
@@ -376,14 +420,11 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         float* st = epi + q * 16 * kEpiRow;
         int ab = 0;
         uint32_t fph = 0;
-        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total, step)) {
+        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total)) {
             int ok = 1;
             if (lane == 0) {
                 ok = tc::mbar_wait(&accf[ab], fph, lim);
-                if (!ok) {
-                    set_status(p.status, QBMOE_ETIMEOUT);
-                    *abort_flag = 1;
-                }
+                if (!ok) expired();
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc::tc_fence_after();
@@ -462,6 +503,9 @@ template <int BN>
 int launch(const qbh::MxProduct& q, Params& p, cudaStream_t s) {
     if (!qbh::encode_rows(&p.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x_codes, q.R, q.K / 2, q.K / 2, 128, Shape<BN>::kBox))
         return QBMOE_ECUDA;
+    if (p.sf_tma && !qbh::encode_rows(&p.b_sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x_scales, q.R, q.K / 32, q.K / 32, 16, BN,
+                                      true))
+        return QBMOE_ECUDA;
     // row tiles of all experts: at most one ragged tile for each that has rows
     const long long tiles = ((long long)(q.R / BN) + min(q.E, q.R)) * p.m_total;
     const int grid = (int)min(tiles, (long long)qbh::sm_count() * (BN == 16 ? 2 : 1));
@@ -489,7 +533,7 @@ int mx_product_init() {
     if (!rc) rc = set_attributes<16>();
     if (!rc) rc = set_attributes<64>();
     if (!rc) rc = set_attributes<128>();
-    if (!rc) rc = set_attributes<224>();
+    if (!rc) rc = set_attributes<192>();
     if (!rc) g_status_ptr[dev] = static_cast<int*>(f);
     return rc;
 }
@@ -516,7 +560,7 @@ int sm_count() {
 }
 
 bool encode_rows(CUtensorMap* m, CUtensorMapDataType type, const void* base, long long rows, long long cols,
-                 long long ld_bytes, int box_cols, int box_rows) {
+                 long long ld_bytes, int box_cols, int box_rows, bool plain) {
     const auto encode = encoder();
     if (!encode) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -524,13 +568,17 @@ bool encode_rows(CUtensorMap* m, CUtensorMapDataType type, const void* base, lon
     cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     cuuint32_t es[2] = {1, 1};
     return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  plain ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int mx_product(const MxProduct& q, cudaStream_t s) {
     Params p{};
     if (!encode_rows(&p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w_codes, (long long)q.E * q.N, q.K / 2, q.K / 2, 128, 128))
+        return QBMOE_ECUDA;
+    p.sf_tma = q.K % 512 == 0;
+    if (p.sf_tma && !encode_rows(&p.a_sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w_scales, (long long)q.E * q.N, q.K / 32,
+                                 q.K / 32, 16, 128, true))
         return QBMOE_ECUDA;
     p.a_sc = q.w_scales;
     p.b_sc = q.x_scales;
@@ -550,7 +598,7 @@ int mx_product(const MxProduct& q, cudaStream_t s) {
     if (avg <= 16) return launch<16>(q, p, s);
     if (avg <= 64) return launch<64>(q, p, s);
     if (avg <= 128) return launch<128>(q, p, s);
-    return launch<224>(q, p, s);
+    return launch<192>(q, p, s);
 }
 
 }  // namespace qbh
