@@ -111,39 +111,49 @@ QB_DEV void load_groups(const Groups& g, const int32_t* offsets, int E, int R, i
 
 // Walks the tiles blockIdx.x, blockIdx.x + gridDim.x, ... of a grid whose m
 // index is fastest, then the row tiles of all experts.  Every lane of the warp
-// calls: the expert is found 32 experts a step (one at a time, a stride of 304
-// tiles over experts with a few rows each cost 7 us a tile).  An expert's
-// rows are split into equal tiles (multiples of 16), so that tiles sharing a
-// weight tile run at one pace.
+// calls.  Lane l holds what the tiles of expert base + l need, so a step is a
+// ballot and three shuffles; shared memory (whose latency is several hundred
+// cycles while the tensor cores stream their operands from it) is read once
+// per 32 experts.  An expert's rows are split into equal tiles (multiples of
+// 16), so that tiles sharing a weight tile run at one pace.
 template <int BN>
 struct Walker {
     int ntg, m, g;
-    int row0, nrows;   // of the current tile
-    QB_DEV void seek(const Groups& gr, int E) {
-        const int lane = threadIdx.x & 31;
-        for (;;) {
-            const int e = g + 1 + lane;
-            const unsigned le = __ballot_sync(0xffffffffu, e < E && gr.toff[e] <= ntg);
-            g += __popc(le);   // toff never falls: the lanes that pass come first
-            if (le != 0xffffffffu) break;
-        }
-        const int t0 = gr.toff[g], nt = gr.toff[g + 1] - t0;
-        const int a = gr.seg[g], len = gr.seg[g + 1] - a;
-        const int per = ((nt == 1 ? len : (len + nt - 1) / nt) + 15) & ~15;
-        row0 = a + (ntg - t0) * per;
-        nrows = min(per, a + len - row0);
+    int row0, nrows;              // of the current tile
+    int base, w_first, w_next, w_row, w_end, w_per;   // this lane's expert: tiles [first, next), rows, rows a tile
+    int total;
+    QB_DEV void window(const Groups& gr, int E, int from) {
+        base = from;
+        const int e = min(from + (int)(threadIdx.x & 31), E - 1);
+        const bool past = from + (int)(threadIdx.x & 31) >= E;
+        w_first = gr.toff[e];
+        w_next = past ? 0x7fffffff : gr.toff[e + 1];
+        w_row = gr.seg[e];
+        w_end = gr.seg[e + 1];
+        const int len = w_end - w_row, nt = max(w_next - w_first, 1);
+        w_per = ((nt == 1 || past ? len : (len + nt - 1) / nt) + 15) & ~15;
+    }
+    QB_DEV void seek(const Groups& gr, int E) {   // ntg < total
+        unsigned le;
+        while ((le = __ballot_sync(0xffffffffu, w_next <= ntg)) == 0xffffffffu) window(gr, E, base + 32);
+        const int i = __popc(le);   // toff never falls: the lanes that pass come first
+        g = base + i;
+        const int per = __shfl_sync(0xffffffffu, w_per, i), t0 = __shfl_sync(0xffffffffu, w_first, i);
+        row0 = __shfl_sync(0xffffffffu, w_row, i) + (ntg - t0) * per;
+        nrows = min(per, __shfl_sync(0xffffffffu, w_end, i) - row0);
     }
     QB_DEV void start(const Groups& gr, int E, int m_total) {
+        total = gr.toff[E];
         ntg = blockIdx.x / m_total;
         m = blockIdx.x - ntg * m_total;
-        g = 0;
-        if (ntg < gr.toff[E]) seek(gr, E);
+        window(gr, E, 0);
+        if (ntg < total) seek(gr, E);
     }
     QB_DEV void next(const Groups& gr, int E, int m_total) {
         const int was = ntg;
         m += gridDim.x;
         while (m >= m_total) m -= m_total, ++ntg;
-        if (ntg != was && ntg < gr.toff[E]) seek(gr, E);
+        if (ntg != was && ntg < total) seek(gr, E);
     }
 };
 

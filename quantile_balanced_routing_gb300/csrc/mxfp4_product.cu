@@ -12,19 +12,19 @@
 // One persistent warp-specialised kernel.  A stage is 256 elements of K: the
 // packed codes of 128 weight rows and of the tile's rows (128 bytes each, TMA,
 // 128-byte swizzle); their scales come in groups of two stages (16 bytes a row).
-//   warp 0      TMA producer (one lane): codes, and the scale groups where the
-//               scale rows are multiples of 16 bytes (K % 512 == 0)
+//   warps 0, 12 TMA producers (one lane each): the weights' codes, the rows' codes
 //   warp 1      TMEM owner, MMA issuer (one lane): 4 x K = 64 MMAs a stage and
 //               one commit that frees it
 //   warp 2      the issuer's waiter (an mbarrier wait by the issuing thread
 //               slows its MMA stream): waits, then releases it through a named barrier
-//   warp 3      scale loader for any other K: global -> registers a group ahead
-//               -> shared memory
+//   warp 3      scale groups to shared memory: by TMA (one lane) where the scale
+//               rows are multiples of 16 bytes (K % 512 == 0), else through
+//               registers, a group ahead
 //   warps 4-7   scale writers, one per TMEM lane quarter: a group's scales from
 //               shared memory to the stages' TMEM slots (tcgen05.st).  Copying them
 //               with tcgen05.cp from the issuer cost it 6 more instructions a
 //               stage: 813 cycles of issue, against 375 of MMAs at N = 192.
-//   warps 8-11  epilogue: TMEM -> per-warp transpose in shared memory -> bf16
+//   warps 8-11  epilogue: TMEM -> bf16 pairs of features -> 64 bytes a row and warp
 // Two accumulators alternate, so a tile's epilogue overlaps the next tile's
 // main loop.  Every mbarrier wait is bounded: on expiry the kernel records
 // QBMOE_ETIMEOUT, stops, lets its own copies and MMAs finish and frees TMEM.
@@ -41,15 +41,16 @@ using namespace qb;
 
 constexpr int kStageK = 256;                 // elements of K per stage (128 bytes of codes a row)
 constexpr int kABytes = 128 * 128;           // weight codes of a stage
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8;
+constexpr int kThreads = 416;
+constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8, kProdBWarp = 12;
 constexpr int kHandoffBar = 1;
-constexpr int kEpiRow = 36;                  // transpose row: 32 features, 4 words of padding
+constexpr int kMaxBoxes = 3;                 // row-tile maps: heights BN / n, 2 BN / n, ...
 constexpr long long kDefaultWait = 1LL << 17;   // polls (<= 20 us each) before a wait expires
 constexpr long long kDrainWait = 1LL << 12;
 
 struct Params {
-    CUtensorMap a, b;                        // codes of the weights [E N, K / 2] and of the rows [R, K / 2]
+    CUtensorMap a;                           // codes of the weights [E N, K / 2]
+    CUtensorMap b[kMaxBoxes];                // and of the rows [R, K / 2], one map per box height
     CUtensorMap a_sf, b_sf;                  // their scales [., K / 32] (K % 512 == 0)
     const uint8_t* a_sc;
     const uint8_t* b_sc;
@@ -67,7 +68,8 @@ struct Params {
 
 template <int BN>
 struct Shape {
-    static constexpr int kBox = BN >= 32 ? 32 : 16;              // rows per TMA copy of B
+    static constexpr int kBoxes = BN == 192 ? 3 : BN == 128 ? 2 : 1;
+    static constexpr int kBox = BN / kBoxes;                     // a row tile is one copy, of the least multiple that holds it
     static constexpr int kNB = (BN + 127) / 128;                 // 128-row blocks of B's scales
     static constexpr int kBJ = (BN + 31) / 32;                   // 32-row blocks
     static constexpr int kBBytes = BN * 128;
@@ -79,7 +81,7 @@ struct Shape {
     static constexpr uint32_t kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
     static_assert(kColsUsed <= 512, "TMEM columns");
     static constexpr int smem(int E) {
-        return 1024 + stages * kStage + 2 * kSfBytes + 4 * 16 * kEpiRow * 4 + (2 * (E + 1) + 64) * 4 + 256;
+        return 1024 + stages * kStage + 2 * kSfBytes + (2 * (E + 1) + 64) * 4 + 256;
     }
 };
 
@@ -135,8 +137,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     uint8_t* a_ring = smem;
     uint8_t* b_ring = a_ring + S * kABytes;
     uint8_t* sf_ring = b_ring + S * Sh::kBBytes;                 // [2][128 + BN rows][16]
-    float* epi = reinterpret_cast<float*>(sf_ring + 2 * Sh::kSfBytes);    // [4][16][kEpiRow]
-    uint64_t* full = reinterpret_cast<uint64_t*>(epi + 4 * 16 * kEpiRow);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sf_ring + 2 * Sh::kSfBytes);
     uint64_t* empty = full + S;
     uint64_t* sf_full = empty + S;
     uint64_t* sf_empty = sf_full + 2;
@@ -148,14 +149,14 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     volatile int* go_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     int* scratch = reinterpret_cast<int*>(tmem_slot + 4);                     // [kThreads / 32]
     Groups gr;
-    gr.seg = scratch + 12;
+    gr.seg = scratch + 16;
     gr.toff = gr.seg + p.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long lim = p.wait_limit > 0 ? p.wait_limit : kDefaultWait;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            tc::mbar_init(&full[s], 5);      // the TMA producer and the four scale writers
+            tc::mbar_init(&full[s], 6);      // the two TMA producers and the four scale writers
             tc::mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -169,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         tc::fence_mbar_init();
         tc::fence_proxy_async_smem();
         tc::prefetch_tmap(&p.a);
-        tc::prefetch_tmap(&p.b);
     }
     if (warp == kMmaWarp) {
         tc::tmem_alloc(tmem_slot, Sh::kCols);
@@ -189,43 +189,29 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         *abort_flag = 1;
     };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------- TMA producer
-        uint32_t issued = 0, last_par = 0, sf_issued = 0, sf_par = 0;
-        int s = 0, gs = 0;
-        uint32_t ph = 0, gph = 0;
-        bool rows_ready = !p.weights_ready;
-        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total)) {
+    if (warp == 0 || warp == kProdBWarp) {
+        // ---------------------------------------------------------- TMA producers
+        const bool is_a = warp == 0;
+        uint32_t issued = 0, last_par = 0;
+        int s = 0;
+        uint32_t ph = 0;
+        if (!is_a && p.weights_ready) pdl_wait();   // the rows' codes come from the kernel before this one
+        for (int t = first; t < n_tiles; t += step) {
+            const int box = (w.nrows - 1) / Sh::kBox;
+            const CUtensorMap* map = is_a ? &p.a : &p.b[box];
+            uint8_t* dst = is_a ? a_ring : b_ring;
+            const int row = is_a ? w.g * p.N + w.m * 128 : w.row0;
+            const uint32_t bytes = is_a ? kABytes : (box + 1) * Sh::kBox * 128;
+            constexpr int kAStride = kABytes, kBStride = Sh::kBBytes;
+            const int stride = is_a ? kAStride : kBStride;
+            w.next(gr, p.E, p.m_total);
             int stop = 0;
             if (lane == 0) {
-                const int boxes = (w.nrows + Sh::kBox - 1) / Sh::kBox;
-                const int ya = w.g * p.N + w.m * 128;
                 stop = *abort_flag;
                 for (int kb = 0; kb < p.nkb && !stop; ++kb) {
-                    if (p.sf_tma && (kb & 1) == 0) {
-                        if (!tc::mbar_wait_spin(&sf_empty[gs], gph ^ 1u, lim)) { expired(); stop = 1; break; }
-                        uint8_t* SF = sf_ring + gs * Sh::kSfBytes;
-                        tc::mbar_expect_tx(&sf_full[gs], Sh::kSfBytes);
-                        tc::tma_load_2d(SF, &p.a_sf, &sf_full[gs], kb * 8, ya);
-                        if (!rows_ready) {   // the rows' codes come from the kernel before this one
-                            pdl_wait();
-                            rows_ready = true;
-                        }
-                        tc::tma_load_2d(SF + 128 * 16, &p.b_sf, &sf_full[gs], kb * 8, w.row0);
-                        sf_issued |= 1u << gs;
-                        sf_par = (sf_par & ~(1u << gs)) | (gph << gs);
-                        if ((gs ^= 1) == 0) gph ^= 1u;
-                    }
                     if (!tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim)) { expired(); stop = 1; break; }
-                    tc::mbar_expect_tx(&full[s], kABytes + boxes * Sh::kBox * 128);
-                    tc::tma_load_2d(a_ring + s * kABytes, &p.a, &full[s], kb * 128, ya);
-                    if (!rows_ready) {
-                        pdl_wait();
-                        rows_ready = true;
-                    }
-                    for (int i = 0; i < boxes; ++i)
-                        tc::tma_load_2d(b_ring + s * Sh::kBBytes + i * Sh::kBox * 128, &p.b, &full[s], kb * 128,
-                                        w.row0 + i * Sh::kBox);
+                    tc::mbar_expect_tx(&full[s], bytes);
+                    tc::tma_load_2d(dst + s * stride, map, &full[s], kb * 128, row);
                     issued |= 1u << s;
                     last_par = (last_par & ~(1u << s)) | (ph << s);
                     if (++s == S) { s = 0; ph ^= 1u; }
@@ -234,17 +220,39 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
             if (__shfl_sync(0xffffffffu, stop, 0)) break;
         }
         __syncthreads();
-        if (lane == 0 && *abort_flag) {   // every copy has landed before shared memory is released
+        if (lane == 0 && *abort_flag)   // every copy has landed before shared memory is released
             for (int i = 0; i < S; ++i)
                 if ((issued >> i) & 1u) tc::mbar_wait(&full[i], (last_par >> i) & 1u, kDrainWait);
-            for (int i = 0; i < 2; ++i)
-                if ((sf_issued >> i) & 1u) tc::mbar_wait(&sf_full[i], (sf_par >> i) & 1u, kDrainWait);
-        }
     } else if (warp == kSfLoadWarp) {
-        // ---------------------------------------------------------- scale loader
-        // Lane l takes rows l, l + 32, ... of the weight tile and of the row tile;
-        // the next group's bytes are in registers while it waits for a slot.
-        if (!p.sf_tma) {
+        // ---------------------------------------------------------- scale groups
+        // Without TMA, lane l takes rows l, l + 32, ... of the weight tile and of
+        // the row tile; the next group's bytes are in registers while it waits
+        // for a slot.
+        uint32_t sf_issued = 0, sf_par = 0;
+        if (p.weights_ready) pdl_wait();
+        if (p.sf_tma) {
+            int gs = 0;
+            uint32_t gph = 0;
+            for (int t = first; t < n_tiles; t += step) {
+                const int ya = w.g * p.N + w.m * 128, yb = w.row0;
+                w.next(gr, p.E, p.m_total);
+                int stop = 0;
+                if (lane == 0) {
+                    stop = *abort_flag;
+                    for (int kb = 0; kb < p.nkb && !stop; kb += 2) {
+                        if (!tc::mbar_wait_spin(&sf_empty[gs], gph ^ 1u, lim)) { expired(); stop = 1; break; }
+                        uint8_t* SF = sf_ring + gs * Sh::kSfBytes;
+                        tc::mbar_expect_tx(&sf_full[gs], Sh::kSfBytes);
+                        tc::tma_load_2d(SF, &p.a_sf, &sf_full[gs], kb * 8, ya);
+                        tc::tma_load_2d(SF + 128 * 16, &p.b_sf, &sf_full[gs], kb * 8, yb);
+                        sf_issued |= 1u << gs;
+                        sf_par = (sf_par & ~(1u << gs)) | (gph << gs);
+                        if ((gs ^= 1) == 0) gph ^= 1u;
+                    }
+                }
+                if (__shfl_sync(0xffffffffu, stop, 0)) break;
+            }
+        } else {
             const int pitch = p.K / 32;
             const long long last_a = (long long)p.E * p.N - 1;
             uint4 ra[4], rb[Sh::kBJ];
@@ -261,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
                                              : make_uint4(0, 0, 0, 0);
                 }
             };
-            if (p.weights_ready) pdl_wait();
             int gs = 0, kb = 0, t = first;
             uint32_t gph = 0;
             if (t < n_tiles) fetch(0);
@@ -291,6 +298,9 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
             }
         }
         __syncthreads();
+        if (lane == 0 && *abort_flag)
+            for (int i = 0; i < 2; ++i)
+                if ((sf_issued >> i) & 1u) tc::mbar_wait(&sf_full[i], (sf_par >> i) & 1u, kDrainWait);
     } else if (warp >= kSfWarp && warp < kSfWarp + 4) {
         // ---------------------------------------------------------- scale writers
         // The MMA reads the scale words of row r (four bytes: K = 128) from lane
@@ -348,9 +358,10 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         // ---------------------------------------------------------- MMA issuer
         int s = 0, ab = 0, h = 0;
         const uint64_t a0 = tc::desc_sw128(tc::smem_u32(a_ring)), b0 = tc::desc_sw128(tc::smem_u32(b_ring));
-        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total)) {
+        for (int t = first; t < n_tiles; t += step) {
             const uint32_t n_eff = (w.nrows + 15) & ~15;
             const uint32_t id0 = idesc_mxf4(n_eff, 0), id2 = idesc_mxf4(n_eff, 2);
+            w.next(gr, p.E, p.m_total);
             tc::named_bar_sync(kHandoffBar, 64);   // the accumulator is free (or stop)
             const bool go = go_flag[h & 1] != 0;
             ++h;
@@ -413,14 +424,18 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         __syncthreads();
     } else {
         // ---------------------------------------------------------- epilogue
-        // Lane q * 32 + lane of an accumulator holds weight row m * 128 + 32 q +
-        // lane; a warp turns 16 rows' worth of its 32 features around in its own
-        // piece of shared memory and stores 64 bytes a row.
+        // Lane 32 q + i of an accumulator holds weight row m * 128 + 32 q + i.
+        // Neighbouring lanes exchange one of every two rows' values, so that a
+        // lane stores two features of one row and a warp 64 bytes of two rows:
+        // no shared memory, whose latency the MMAs raise.
         const int q = warp & 3;
-        float* st = epi + q * 16 * kEpiRow;
         int ab = 0;
         uint32_t fph = 0;
-        for (int t = first; t < n_tiles; t += step, w.next(gr, p.E, p.m_total)) {
+        for (int t = first; t < n_tiles; t += step) {
+            const int nrows = w.nrows, odd = lane & 1;
+            const int f = w.m * 128 + 32 * q + (lane & ~1);
+            __nv_bfloat16* out = p.y + (long long)(w.row0 + odd) * p.ldy + f;
+            w.next(gr, p.E, p.m_total);
             int ok = 1;
             if (lane == 0) {
                 ok = tc::mbar_wait(&accf[ab], fph, lim);
@@ -428,27 +443,15 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc::tc_fence_after();
-            const int j = lane >> 1, half = lane & 1;
-            const int f = w.m * 128 + 32 * q + 16 * half;
-            __nv_bfloat16* out = p.y + (long long)(w.row0 + j) * p.ldy + f;
-            for (int c0 = 0; c0 < w.nrows; c0 += 16) {
+            for (int c0 = 0; c0 < nrows; c0 += 16) {
                 float v[16];
                 tc::tmem_ld16(tbase + ab * BN + (static_cast<uint32_t>(32 * q) << 16) + c0, v);
-                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) st[i * kEpiRow + lane] = v[i];
-                __syncwarp();
-                if (c0 + j < w.nrows) {
-                    const float4* src = reinterpret_cast<const float4*>(st + j * kEpiRow + 16 * half);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float4 a = src[2 * g], b = src[2 * g + 1];
-                        const __nv_bfloat162 o[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
-                                                     __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
-                        if (f + 8 * g < p.N)
-                            *reinterpret_cast<uint4*>(out + (long long)c0 * p.ldy + 8 * g) =
-                                *reinterpret_cast<const uint4*>(o);
-                    }
+                for (int i = 0; i < 16; i += 2) {
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                    const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
+                    if (c0 + i + odd < nrows && f < p.N)
+                        *reinterpret_cast<__nv_bfloat162*>(out + (long long)(c0 + i) * p.ldy) = o;
                 }
             }
             tc::tc_fence_before();
@@ -501,8 +504,10 @@ int set_attributes() {
 
 template <int BN>
 int launch(const qbh::MxProduct& q, Params& p, cudaStream_t s) {
-    if (!qbh::encode_rows(&p.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x_codes, q.R, q.K / 2, q.K / 2, 128, Shape<BN>::kBox))
-        return QBMOE_ECUDA;
+    for (int i = 0; i < Shape<BN>::kBoxes; ++i)
+        if (!qbh::encode_rows(&p.b[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x_codes, q.R, q.K / 2, q.K / 2, 128,
+                              Shape<BN>::kBox * (i + 1)))
+            return QBMOE_ECUDA;
     if (p.sf_tma && !qbh::encode_rows(&p.b_sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x_scales, q.R, q.K / 32, q.K / 32, 16, BN,
                                       true))
         return QBMOE_ECUDA;
