@@ -4,11 +4,9 @@
 //
 // Notation: s = sigmoid(x), c = 1 - s, S_t = sum_j s_tj, p_tj = s_tj / S_t.
 // Both kernels make one pass over the [T, n] logits with one warp per token:
-// a lane keeps n / 32 of the row's scores in registers, so S_t (and, in the
-// backward pass, sum_j f_j p_tj) is a warp reduction and no row is read twice.
+// a lane keeps n / 32 of the row in registers, so S_t (and, in the backward
+// pass, sum_j f_j s_tj) is a warp reduction and no row is read twice.
 #include "common.cuh"
-
-#include <climits>
 
 namespace {
 
@@ -19,14 +17,24 @@ constexpr int kBalThreads = 32 * kBalWarps;
 constexpr int kMaxPerLane = QBMOE_MAX_EXPERTS / 32;   // 32 logits of a row per lane
 constexpr float kLogitLimit = 80.0f;
 
-// s = sigmoid(x) and c = 1 - s for x clamped to [-80, 80]; c = e^-x s keeps
-// its relative precision where s rounds to 1.  The hardware exponential and
-// reciprocal: relative error about 2^-22, far below the gradients' use.
-QB_DEV void score_pair(float x, float& s, float& c) {
-    x = x < -kLogitLimit ? -kLogitLimit : x > kLogitLimit ? kLogitLimit : x;   // a NaN stays one
-    const float e = __expf(-x);
-    s = __frcp_rn(1.0f + e);
-    c = e * s;
+// e = exp(-x) and s = 1 / (1 + e) = sigmoid(x), x clamped to [-80, 80] from below
+// (above 80 s is 1 either way) and a NaN kept.  The hardware exponential and
+// reciprocal: relative error about |x| 2^-24 + 2^-22.
+QB_DEV float score(float x, float& e) {
+    float lo;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(x), "f"(-kLogitLimit));
+    e = __expf(-lo);
+    float s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
+// s and its derivative s (1 - s) = e s^2, which keeps its relative precision
+// where s rounds to 1 and is 0 where the clamp holds.
+QB_DEV float score_slope(float x, float& slope) {
+    float e;
+    const float s = score(x, e);
+    slope = fabsf(x) > kLogitLimit ? 0.0f : e * s * s;
+    return s;
 }
 
 template <typename T> struct Vec;   // elements of T in 16 bytes
@@ -91,7 +99,8 @@ struct BalanceArgs {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kBalThreads) k_balance_partial(const BalanceArgs a) {
+__global__ void __launch_bounds__(kBalThreads, 3) k_balance_partial(const BalanceArgs a) {
+    pdl_trigger();
     extern __shared__ float sm[];
     float* red = sm;                                              // [kBalWarps][n]
     int* cnt = reinterpret_cast<int*>(sm + kBalWarps * a.n);      // [n]
@@ -120,16 +129,21 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_partial(const BalanceAr
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kMaxPerLane / V; ++i)
+                if (32 * i * V < a.n) {   // uniform: groups past the row cost nothing
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float s = 0.0f, c;
-                    if ((32 * i + lane) * V < a.n) score_pair(x[i * V + v], s, c);
-                    x[i * V + v] = s;
-                    sum += s;
+                    for (int v = 0; v < V; ++v) {
+                        float e;
+                        x[i * V + v] = (32 * i + lane) * V < a.n ? score(x[i * V + v], e) : 0.0f;
+                        sum += x[i * V + v];
+                    }
                 }
-            const float inv = 1.0f / warp_sum(sum);
+            const float inv = __fdividef(1.0f, warp_sum(sum));
 #pragma unroll
-            for (int i = 0; i < kMaxPerLane; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+            for (int i = 0; i < kMaxPerLane / V; ++i)
+                if (32 * i * V < a.n) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[i * V + v] = fmaf(x[i * V + v], inv, acc[i * V + v]);
+                }
         }
 #pragma unroll
         for (int i = 0; i < kMaxPerLane / V; ++i)
@@ -167,6 +181,7 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
     __shared__ bool last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int q = blockIdx.y, j = blockIdx.x * 32 + lane;
+    pdl_wait();
     const int o0 = a.seq ? min(max(__ldg(a.seq + q), 0), a.T) : 0;
     const int o1 = a.seq ? min(max(__ldg(a.seq + q + 1), o0), a.T) : a.T;
     const int f = o0 / a.chunk, g = o1 > o0 ? (o1 - 1) / a.chunk + 1 : f;   // chunks [f, g)
@@ -212,12 +227,16 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  With f_j = dloss n counts_j / (k T_q^2) and D = sum_j f_j p_j:
-//   dx_j = p_j c_j (f_j - D)                             balance loss
-//        + w_i c_j (dw_i - sum_l dw_l w_l)  for j = idx_i   mixture weights
+// Backward.  With f_j = dloss n counts_j / (k T_q^2), D = sum_j f_j p_j and the
+// slope d_j = s_j c_j:
+//   dx_j = d_j (f_j - D) / S_t                              balance loss
+//        + d_j (dw_i - sum_l dw_l w_l) / sum_l s_(idx_l)    j = idx_i, mixture weights
+// A CTA has a chunk of tokens and f of the chunk's sequence in shared memory
+// (a chunk that crosses a boundary goes through its sequences in turn).  The
+// dense row is stored first, then the k chosen entries over it.
 // ---------------------------------------------------------------------------
 struct RouterGradArgs {
-    int T, n, k, S, per_warp;
+    int T, n, k, S, chunk;
     long long ld, ldg;
     const void* logits;
     const int32_t* idx;
@@ -231,115 +250,107 @@ struct RouterGradArgs {
 };
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kBalThreads) k_router_backward(const RouterGradArgs a) {
-    extern __shared__ float sm[];   // [kBalWarps][n]: the row's mixture-weight terms, zero between tokens
+__global__ void __launch_bounds__(kBalThreads, 4) k_router_backward(const RouterGradArgs a) {
+    extern __shared__ __align__(16) float fs[];   // [n rounded up to 8]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* sp = sm + warp * a.n;
-    for (int j = lane; j < a.n; j += 32) sp[j] = 0.0f;
-    __syncwarp();
-    const long long first = ((long long)blockIdx.x * kBalWarps + warp) * a.per_warp;
-    const int t1 = (int)min((long long)a.T, first + a.per_warp);
-    float f[kMaxPerLane] = {};
-    int q = -1, q_end = INT_MIN;
-    for (int t = (int)min(first, (long long)a.T); t < t1; ++t) {
-        const T* row = static_cast<const T*>(a.logits) + (long long)t * a.ld;
-        T* out = static_cast<T*>(a.out) + (long long)t * a.ldg;
-        const bool live = !a.mask || __ldg(a.mask + t);
-        float x[kMaxPerLane];
-        if (live) {
-            if (a.dloss && t >= q_end) {   // the next sequence's frequencies
-                q = a.seq ? find_seq(a.seq, a.S, t) : 0;
-                q_end = a.seq && q + 1 < a.S ? __ldg(a.seq + q + 1) : INT_MAX;
+    const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
+    int q = a.dloss && a.seq ? find_seq(a.seq, a.S, c0) : 0;
+    for (int t0 = c0; t0 < c1; ++q) {
+        const int t1 = a.dloss && a.seq && q + 1 < a.S ? min(c1, max(t0, __ldg(a.seq + q + 1))) : c1;
+        if (t1 > t0) {
+            __syncthreads();   // the last sequence's readers are done
+            float scale = 0.0f;
+            if (a.dloss) {
                 const float tq = fmaxf((float)__ldg(a.tokens + q), 1.0f);
-                const float scale = __ldg(a.dloss + q) * ((float)a.n / ((float)a.k * tq)) / tq;
-#pragma unroll
-                for (int i = 0; i < kMaxPerLane / V; ++i)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int j = (32 * i + lane) * V + v;
-                        f[i * V + v] = j < a.n ? scale * (float)__ldg(a.counts + (long long)q * a.n + j) : 0.0f;
-                    }
+                scale = __ldg(a.dloss + q) * ((float)a.n / ((float)a.k * tq)) / tq;
             }
-            load_row<T, V>(row, a.n, lane, x);
-            if (a.dw) {
-                float s = 0.0f, c = 0.0f, d = 0.0f;
-                int id = -1;
-                if (lane < a.k) {
-                    id = __ldg(a.idx + (long long)t * a.k + lane);
-                    if ((unsigned)id < (unsigned)a.n) {
-                        score_pair(to_f32<T>(row[id]), s, c);
-                        d = __ldg(a.dw + (long long)t * a.k + lane);
-                    } else {
-                        id = -1;
-                    }
-                }
-                const float sum = warp_sum(s);
-                const float w = sum > 0.0f ? s / sum : 0.0f;
-                const float dot = warp_sum(d * w);
-                if (id >= 0) atomicAdd(sp + id, w * c * (d - dot));
-                __syncwarp();
-            }
+            for (int j = threadIdx.x; j < a.n; j += kBalThreads)
+                fs[j] = a.dloss ? scale * (float)__ldg(a.counts + (long long)q * a.n + j) : 0.0f;
+            __syncthreads();
         }
-        float sum = 0.0f, dot = 0.0f;
-        float g[kMaxPerLane];   // c, then the gradient
-#pragma unroll
-        for (int i = 0; i < kMaxPerLane / V; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = i * V + v;
-                float s = 0.0f, c = 0.0f;
-                if (live && (32 * i + lane) * V < a.n) {
-                    score_pair(x[e], s, c);
-                    if (fabsf(x[e]) > kLogitLimit) c = 0.0f;   // clamped: no slope
-                }
-                x[e] = s;
-                g[e] = c;
-                sum += s;
-                dot = fmaf(f[e], s, dot);
+        for (int t = t0 + warp; t < t1; t += kBalWarps) {
+            const T* row = static_cast<const T*>(a.logits) + (long long)t * a.ld;
+            T* out = static_cast<T*>(a.out) + (long long)t * a.ldg;
+            if (a.mask && !__ldg(a.mask + t)) {
+                for (int j = lane; j < a.n; j += 32) out[j] = from_f32<T>(0.0f);
+                continue;
             }
-        if (live) {
-            const float inv = 1.0f / warp_sum(sum);
-            const float D = warp_sum(dot) * inv;
+            float x[kMaxPerLane];   // the row, then its slopes
+            load_row<T, V>(row, a.n, lane, x);
+            // the chosen experts, one a lane
+            int id = -1;
+            float d = 0.0f, own = 0.0f, slope = 0.0f;
+            if (a.dw && lane < a.k) {
+                id = __ldg(a.idx + (long long)t * a.k + lane);
+                if ((unsigned)id < (unsigned)a.n) {
+                    d = __ldg(a.dw + (long long)t * a.k + lane);
+                    own = score_slope(to_f32<T>(row[id]), slope);
+                } else {
+                    id = -1;
+                }
+            }
+            float sum = 0.0f, dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kMaxPerLane / V; ++i)
+            for (int i = 0; i < kMaxPerLane / V; ++i) {
+                const int j = (32 * i + lane) * V;
+                if (j >= a.n) continue;
+                float f[V];
+                if constexpr (V == 1) f[0] = fs[j];
+                else
+#pragma unroll
+                    for (int u = 0; u < V / 4; ++u)
+                        *reinterpret_cast<float4*>(f + 4 * u) = *reinterpret_cast<const float4*>(fs + j + 4 * u);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const int e = i * V + v, j = (32 * i + lane) * V + v;
-                    // a clamped logit gets 0 from the mixture weights too
-                    const float m = a.dw && j < a.n ? (g[e] == 0.0f ? 0.0f : sp[j]) : 0.0f;
-                    g[e] = fmaf(x[e] * inv * g[e], f[e] - D, m);
+                    float sl;
+                    const float s = score_slope(x[i * V + v], sl);
+                    x[i * V + v] = sl;
+                    sum += s;
+                    dot = fmaf(f[v], s, dot);
                 }
+            }
+            const float inv = __fdividef(1.0f, warp_sum(sum));
+            const float D = warp_sum(dot) * inv;
+            float w_inv = 0.0f, mean = 0.0f;
             if (a.dw) {
-                __syncwarp();
-                if (lane < a.k) {
-                    const int id = __ldg(a.idx + (long long)t * a.k + lane);
-                    if ((unsigned)id < (unsigned)a.n) sp[id] = 0.0f;
+                const float chosen = warp_sum(own);
+                w_inv = chosen > 0.0f ? 1.0f / chosen : 0.0f;
+                mean = warp_sum(d * own) * w_inv;
+            }
+#pragma unroll
+            for (int i = 0; i < kMaxPerLane / V; ++i) {
+                const int j = (32 * i + lane) * V;
+                if (j >= a.n) continue;
+                if constexpr (V == 1) {
+                    out[j] = from_f32<T>(x[i] * ((fs[j] - D) * inv));
+                } else {
+                    float f[V];
+#pragma unroll
+                    for (int u = 0; u < V / 4; ++u)
+                        *reinterpret_cast<float4*>(f + 4 * u) = *reinterpret_cast<const float4*>(fs + j + 4 * u);
+                    uint4 o;
+                    T* e = reinterpret_cast<T*>(&o);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) e[v] = from_f32<T>(x[i * V + v] * ((f[v] - D) * inv));
+                    *reinterpret_cast<uint4*>(out + j) = o;
                 }
-                __syncwarp();
+            }
+            if (a.dw) {
+                __syncwarp();   // the row is stored before the chosen entries
+                if (id >= 0) out[id] = from_f32<T>(slope * fmaf(fs[id] - D, inv, (d - mean) * w_inv));
             }
         }
-#pragma unroll
-        for (int i = 0; i < kMaxPerLane / V; ++i) {
-            const int j = (32 * i + lane) * V;
-            if (j >= a.n) continue;
-            if (V == 1) {
-                out[j] = from_f32<T>(g[i]);
-            } else {
-                uint4 u;
-                T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[v] = from_f32<T>(g[i * V + v]);
-                *reinterpret_cast<uint4*>(out + j) = u;
-            }
-        }
+        t0 = t1;
     }
 }
 
-// Tokens per forward CTA: about two CTAs a SM at full size, one token a warp at least.
-int balance_chunk(int T) {
-    const int per = (T + 303) / 304;
+// Tokens per CTA: one wave of `ctas` a SM at full size (what the registers
+// allow), one token a warp at least.
+int chunk_of(int T, int ctas) {
+    const int per = (T + 152 * ctas - 1) / (152 * ctas);
     return ((per + kBalWarps - 1) / kBalWarps) * kBalWarps;
 }
+int balance_chunk(int T) { return chunk_of(T, 3); }
 
 struct BalanceLayout {
     size_t part_p, part_c, part_t, ticket, loss_part, total;
@@ -421,8 +432,7 @@ extern "C" int moe_balance_loss(int T, int n, int k, int S, int logit_dtype, con
         else k_balance_partial<__nv_bfloat16, 1><<<a.nchunk, kBalThreads, smem, s>>>(a);
     }
     if ((rc = qbh::cuda_err(cudaGetLastError()))) return rc;
-    k_balance_finish<<<dim3((n + 31) / 32, S), kBalThreads, 0, s>>>(a);
-    return qbh::cuda_err(cudaGetLastError());
+    return qbh::launch_pdl(k_balance_finish, dim3((n + 31) / 32, S), dim3(kBalThreads), 0, s, a);
 }
 
 extern "C" int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void* logits, long long ld,
@@ -445,12 +455,10 @@ extern "C" int moe_router_backward(int T, int n, int k, int S, int logit_dtype, 
     a.T = T; a.n = n; a.k = k; a.S = S; a.ld = ld; a.ldg = ldg;
     a.logits = logits; a.idx = idx; a.seq = seq_offsets; a.mask = token_mask;
     a.dw = dw; a.dloss = dloss; a.counts = counts; a.tokens = tokens; a.out = dlogits;
-    // consecutive tokens per warp, so that a sequence's frequencies stay in
-    // registers: about two CTAs a SM
-    a.per_warp = (T + 304 * kBalWarps - 1) / (304 * kBalWarps);
-    const int grid = (int)(((long long)T + (long long)a.per_warp * kBalWarps - 1) / ((long long)a.per_warp * kBalWarps));
+    a.chunk = chunk_of(T, 4);
+    const int grid = (T + a.chunk - 1) / a.chunk;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t smem = (size_t)kBalWarps * n * 4;
+    const size_t smem = (size_t)((n + 7) & ~7) * 4;
     if (logit_dtype == QBMOE_F32) {
         if (vector_rows<float>(n, logits, ld) && vector_rows<float>(n, dlogits, ldg))
             k_router_backward<float, 4><<<grid, kBalThreads, smem, s>>>(a);

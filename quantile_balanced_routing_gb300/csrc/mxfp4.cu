@@ -7,6 +7,8 @@
 #include "mxfp4.cuh"
 #include "mxfp4_decode.cuh"
 
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 namespace {
@@ -14,17 +16,32 @@ namespace {
 using namespace qb;
 
 // ---------------------------------------------------------------------------
-// Quantisation.  Four consecutive lanes hold one block of 32 (8 elements each);
-// the block's largest magnitude is two shuffles away.
+// Quantisation: one pass over the rows, bound by HBM.  Four consecutive lanes
+// hold one block of 32 (8 elements each); the block's largest magnitude is two
+// shuffles away.  A thread has kQUnroll pieces in flight, a CTA's width apart.
+// Contiguous rows are one long row, so that no index is divided.
 // ---------------------------------------------------------------------------
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 256, kQUnroll = 4;
 
-// 8 elements of a row from 16-byte loads.
+// 8 elements of a row: loads, the largest magnitude as fp32 bits (an infinity or
+// a NaN is above every finite number), the values as fp32, and stores.
 template <typename T> struct Eight;
 template <> struct Eight<float> {
-    static QB_DEV void load(const float* p, float (&x)[8]) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    float4 a, b;
+    QB_DEV void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    QB_DEV void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    QB_DEV uint32_t amax() const {
+        float x[8];
+        get(x);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+        return m;
     }
     static QB_DEV void store(float* p, const float (&x)[8]) {
         reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -32,14 +49,20 @@ template <> struct Eight<float> {
     }
 };
 template <> struct Eight<__nv_bfloat16> {
-    static QB_DEV void load(const __nv_bfloat16* p, float (&x)[8]) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    uint4 u;
+    QB_DEV void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    QB_DEV void get(float (&x)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(w[i] << 16);
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
+    }
+    QB_DEV uint32_t amax() const {   // both halves of a word at once
+        const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                    __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+        return max(m & 0xffff0000u, m << 16);
     }
     static QB_DEV void store(__nv_bfloat16* p, const float (&x)[8]) {
         uint32_t w[4];
@@ -52,50 +75,80 @@ template <> struct Eight<__nv_bfloat16> {
     }
 };
 
-// Two floats to a byte of E2M1 codes (lo in the low nibble): round to nearest,
-// ties to even, magnitudes above 6 to 6.
-QB_DEV uint32_t e2m1_pair(float lo, float hi) {
-    uint16_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}"
-        : "=h"(r) : "f"(hi), "f"(lo));
+// Eight floats to eight E2M1 codes (element 0 in the low nibble): round to
+// nearest, ties to even, magnitudes above 6 to 6.
+QB_DEV uint32_t e2m1_codes(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
+// Eight codes to their values.
+QB_DEV void e2m1_values(uint32_t q, float (&x)[8]) {
+    uint32_t h[4];   // pairs of fp16
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(q));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
 
+// Row blockIdx.y, blockIdx.y + gridDim.y, ... of `items` pieces of 8 elements (a
+// multiple of 4, so the lanes of a block share its fate).
 template <typename T, bool kValues>
-__global__ void __launch_bounds__(kQThreads) k_mxfp4_quantize(long long rows, int K, const T* __restrict__ x,
+__global__ void __launch_bounds__(kQThreads) k_mxfp4_quantize(long long rows, long long items, const T* __restrict__ x,
                                                               long long ldx, uint8_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales, T* __restrict__ values) {
     pdl_trigger();   // a product of these rows may set itself up meanwhile
-    const int per_row = K / 8;   // a multiple of 4: the lanes of a block share its fate
-    const long long items = rows * per_row;
-    for (long long it = (long long)blockIdx.x * kQThreads + threadIdx.x; it < items;
-         it += (long long)gridDim.x * kQThreads) {
-        const long long r = it / per_row;
-        const int k = (int)(it - r * per_row) * 8;
-        float v[8];
-        Eight<T>::load(x + r * ldx + k, v);
-        uint32_t m = 0;   // largest magnitude as bits: an infinity or a NaN is above every finite number
+    const long long first = (long long)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x;
+    const uint32_t group = 0xfu << (threadIdx.x & 28);
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
+        Eight<T> in[kQUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        const uint32_t group = 0xfu << (threadIdx.x & 28);
-        m = max(m, __shfl_xor_sync(group, m, 1));
-        m = max(m, __shfl_xor_sync(group, m, 2));
-        // a subnormal maximum has exponent field 0: below 2^-126, so e < -127 and the clamp holds
-        const int e = max((int)(m >> 23) - 127 - 2, -127);
-        const bool bad = m >= 0x7f800000u;
-        const float inv = __int_as_float((127 - e) << 23);   // 2^-e: -127 <= e <= 125 (not used when bad)
-        uint32_t q = 0;
+        for (int i = 0; i < kQUnroll; ++i)
+            if (first + i * kQThreads < items) in[i].load(x + r * ldx + (first + i * kQThreads) * 8);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q |= e2m1_pair(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
-        if (bad) q = 0;
-        reinterpret_cast<uint32_t*>(codes)[it] = q;
-        const uint32_t sb = bad ? 0xffu : (uint32_t)(e + 127);
-        if ((threadIdx.x & 3) == 0) scales[it >> 2] = (uint8_t)sb;
-        if (kValues) {
-            const float sc = e8m0_value(sb);
+        for (int i = 0; i < kQUnroll; ++i) {
+            const long long at = first + i * kQThreads;
+            if (at >= items) break;
+            uint32_t m = in[i].amax();
+            m = max(m, __shfl_xor_sync(group, m, 1));
+            m = max(m, __shfl_xor_sync(group, m, 2));
+            // a subnormal maximum has exponent field 0: below 2^-126, so e < -127 and the clamp holds
+            const int e = max((int)(m >> 23) - 127 - 2, -127);
+            const bool bad = m >= 0x7f800000u;
+            const float inv = __int_as_float((127 - e) << 23);   // 2^-e: -127 <= e <= 125 (not used when bad)
+            float v[8];
+            in[i].get(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = e2m1_value(q >> (4 * i)) * sc;
-            Eight<T>::store(values + r * K + k, v);
+            for (int j = 0; j < 8; ++j) v[j] *= inv;
+            const uint32_t q = bad ? 0u : e2m1_codes(v);
+            const long long out = r * items + at;
+            reinterpret_cast<uint32_t*>(codes)[out] = q;
+            const uint32_t sb = bad ? 0xffu : (uint32_t)(e + 127);
+            if ((threadIdx.x & 3) == 0) scales[out >> 2] = (uint8_t)sb;
+            if (kValues) {
+                const float sc = e8m0_value(sb);
+                e2m1_values(q, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= sc;
+                Eight<T>::store(values + out * 8, v);
+            }
         }
     }
 }
@@ -121,12 +174,14 @@ namespace qbh {
 
 int mx_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes, uint8_t* scales,
                 void* values, cudaStream_t s) {
-    const long long items = rows * (K / 8);
-    const int grid = (int)min((items + kQThreads - 1) / kQThreads, 8LL * sm_count());
+    long long n = rows, items = K / 8;
+    if (ldx == K) items *= n, n = 1;
+    const dim3 grid((unsigned)((items + kQThreads * kQUnroll - 1) / (kQThreads * kQUnroll)),
+                    (unsigned)min(n, 65535LL));
     auto go = [&](auto tag, auto with) {
         using T = decltype(tag);
         k_mxfp4_quantize<T, decltype(with)::value><<<grid, kQThreads, 0, s>>>(
-            rows, K, static_cast<const T*>(x), ldx, codes, scales, static_cast<T*>(values));
+            n, items, static_cast<const T*>(x), ldx, codes, scales, static_cast<T*>(values));
     };
     if (x_type == QBMOE_F32) values ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
     else values ? go(__nv_bfloat16{}, std::true_type{}) : go(__nv_bfloat16{}, std::false_type{});

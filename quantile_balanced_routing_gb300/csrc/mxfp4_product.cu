@@ -44,7 +44,7 @@ constexpr int kABytes = 128 * 128;           // weight codes of a stage
 constexpr int kThreads = 416;
 constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8, kProdBWarp = 12;
 constexpr int kHandoffBar = 1;
-constexpr int kMaxBoxes = 3;                 // row-tile maps: heights BN / n, 2 BN / n, ...
+constexpr int kMaxBoxes = 4;                 // row-tile maps: heights BN / n, 2 BN / n, ...
 constexpr long long kDefaultWait = 1LL << 17;   // polls (<= 20 us each) before a wait expires
 constexpr long long kDrainWait = 1LL << 12;
 
@@ -68,7 +68,7 @@ struct Params {
 
 template <int BN>
 struct Shape {
-    static constexpr int kBoxes = BN == 192 ? 3 : BN == 128 ? 2 : 1;
+    static constexpr int kBoxes = BN == 208 ? 4 : BN == 128 ? 2 : 1;
     static constexpr int kBox = BN / kBoxes;                     // a row tile is one copy, of the least multiple that holds it
     static constexpr int kNB = (BN + 127) / 128;                 // 128-row blocks of B's scales
     static constexpr int kBJ = (BN + 31) / 32;                   // 32-row blocks
@@ -538,7 +538,7 @@ int mx_product_init() {
     if (!rc) rc = set_attributes<16>();
     if (!rc) rc = set_attributes<64>();
     if (!rc) rc = set_attributes<128>();
-    if (!rc) rc = set_attributes<192>();
+    if (!rc) rc = set_attributes<208>();
     if (!rc) g_status_ptr[dev] = static_cast<int*>(f);
     return rc;
 }
@@ -603,7 +603,7 @@ int mx_product(const MxProduct& q, cudaStream_t s) {
     if (avg <= 16) return launch<16>(q, p, s);
     if (avg <= 64) return launch<64>(q, p, s);
     if (avg <= 128) return launch<128>(q, p, s);
-    return launch<192>(q, p, s);
+    return launch<208>(q, p, s);
 }
 
 }  // namespace qbh
