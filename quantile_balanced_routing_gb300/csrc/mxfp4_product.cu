@@ -12,7 +12,10 @@
 // One persistent warp-specialised kernel.  A stage is 256 elements of K: the
 // packed codes of 128 weight rows and of the tile's rows (128 bytes each, TMA,
 // 128-byte swizzle); their scales come in groups of two stages (16 bytes a row).
-//   warps 0, 12 TMA producers (one lane each): the weights' codes, the rows' codes
+//   warp 0      TMA producer of both operands' codes (one lane); it alone waits
+//               for a free stage and then meets the scale writers at a named
+//               barrier (a suspended mbarrier wait takes about a microsecond to come
+//               back, and every warp that polls instead slows the others)
 //   warp 1      TMEM owner, MMA issuer (one lane): 4 x K = 64 MMAs a stage and
 //               one commit that frees it
 //   warp 2      the issuer's waiter (an mbarrier wait by the issuing thread
@@ -41,9 +44,9 @@ using namespace qb;
 
 constexpr int kStageK = 256;                 // elements of K per stage (128 bytes of codes a row)
 constexpr int kABytes = 128 * 128;           // weight codes of a stage
-constexpr int kThreads = 416;
-constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8, kProdBWarp = 12;
-constexpr int kHandoffBar = 1;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4;
+constexpr int kHandoffBar = 1, kStageBar = 2;
 constexpr int kMaxBoxes = 4;                 // row-tile maps: heights BN / n, 2 BN / n, ...
 constexpr long long kDefaultWait = 1LL << 17;   // polls (<= 20 us each) before a wait expires
 constexpr long long kDrainWait = 1LL << 12;
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     const long long lim = p.wait_limit > 0 ? p.wait_limit : kDefaultWait;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            tc::mbar_init(&full[s], 6);      // the two TMA producers and the four scale writers
+            tc::mbar_init(&full[s], 5);      // the TMA producer and the four scale writers
             tc::mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -189,35 +192,35 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         *abort_flag = 1;
     };
 
-    if (warp == 0 || warp == kProdBWarp) {
-        // ---------------------------------------------------------- TMA producers
-        const bool is_a = warp == 0;
+    if (warp == 0) {
+        // ---------------------------------------------------------- TMA producer
         uint32_t issued = 0, last_par = 0;
         int s = 0;
         uint32_t ph = 0;
-        if (!is_a && p.weights_ready) pdl_wait();   // the rows' codes come from the kernel before this one
+        bool rows_ready = !p.weights_ready;
+        bool dead = false;   // lane 0: an expiry; only the meetings go on
         for (int t = first; t < n_tiles; t += step) {
             const int box = (w.nrows - 1) / Sh::kBox;
-            const CUtensorMap* map = is_a ? &p.a : &p.b[box];
-            uint8_t* dst = is_a ? a_ring : b_ring;
-            const int row = is_a ? w.g * p.N + w.m * 128 : w.row0;
-            const uint32_t bytes = is_a ? kABytes : (box + 1) * Sh::kBox * 128;
-            constexpr int kAStride = kABytes, kBStride = Sh::kBBytes;
-            const int stride = is_a ? kAStride : kBStride;
+            const int ya = w.g * p.N + w.m * 128, yb = w.row0;
             w.next(gr, p.E, p.m_total);
-            int stop = 0;
-            if (lane == 0) {
-                stop = *abort_flag;
-                for (int kb = 0; kb < p.nkb && !stop; ++kb) {
-                    if (!tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim)) { expired(); stop = 1; break; }
-                    tc::mbar_expect_tx(&full[s], bytes);
-                    tc::tma_load_2d(dst + s * stride, map, &full[s], kb * 128, row);
+            if (lane == 0 && *abort_flag) dead = true;
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (lane == 0 && !dead && !tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim)) { expired(); dead = true; }
+                if (lane == 0 && !dead) {
+                    tc::mbar_expect_tx(&full[s], kABytes + (box + 1) * Sh::kBox * 128);
+                    tc::tma_load_2d(a_ring + s * kABytes, &p.a, &full[s], kb * 128, ya);
+                    if (!rows_ready) {   // the rows' codes come from the kernel before this one
+                        pdl_wait();
+                        rows_ready = true;
+                    }
+                    tc::tma_load_2d(b_ring + s * Sh::kBBytes, &p.b[box], &full[s], kb * 128, yb);
                     issued |= 1u << s;
                     last_par = (last_par & ~(1u << s)) | (ph << s);
-                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
+                __syncwarp();
+                tc::named_bar_sync(kStageBar, 160);
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
-            if (__shfl_sync(0xffffffffu, stop, 0)) break;
         }
         __syncthreads();
         if (lane == 0 && *abort_flag)   // every copy has landed before shared memory is released
@@ -307,21 +310,20 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         // r % 32, column r / 32 of a slot, in each lane quarter.
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         int s = 0, gs = 0;
-        uint32_t ph = 0, gph = 0;
-        bool ok = true;
-        for (int t = first; t < n_tiles && ok; t += step) {
-            for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += 2) {
+        uint32_t gph = 0;
+        bool dead = false;
+        for (int t = first; t < n_tiles; t += step) {
+            if (lane == 0 && *abort_flag) dead = true;
+            for (int kb0 = 0; kb0 < p.nkb; kb0 += 2) {
                 uint4 ra[4], rb[4 * Sh::kNB];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (kb0 + u >= p.nkb) break;
-                    int go = 1;
-                    if (lane == 0) {
-                        go = !*abort_flag && (u || tc::mbar_wait_spin(&sf_full[gs], gph, lim)) &&
-                             tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim);
-                        if (!go && !*abort_flag) expired();
+                    tc::named_bar_sync(kStageBar, 160);   // the stage's slot is free
+                    if (u == 0) {
+                        if (lane == 0 && !dead && !tc::mbar_wait_spin(&sf_full[gs], gph, lim)) { expired(); dead = true; }
+                        __syncwarp();
                     }
-                    if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
                     if (u == 0) {
                         const uint4* SF = reinterpret_cast<const uint4*>(sf_ring + gs * Sh::kSfBytes);
 #pragma unroll
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&full[s]);
-                    if (++s == S) { s = 0; ph ^= 1u; }
+                    if (++s == S) s = 0;
                 }
             }
         }
