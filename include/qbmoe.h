@@ -313,6 +313,8 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  *   QBMOE_MXFP4: x the codes, x_scales the scales, ldx = K.  x_type QBMOE_F32
  *   or QBMOE_BF16: x [R, K] of that type, row stride ldx elements, quantised
  *   into the workspace first as moe_mxfp4_quantize does; x_scales is not used.
+ *   workspace: device, 256-byte aligned, >= qbmoe_mxfp4_workspace_bytes(R, K)
+ *   bytes; not used, and may be NULL, when x is MXFP4.
  * moe_mxfp4_dgrad:   dx[r][k] = sum_f dy[r][f] w[e(r)][f][k], dy [R, N] bf16
  *   (row stride lddy), dx [R, K] bf16 (row stride lddx).
  * moe_mxfp4_wgrad:   dw[e][f][k] = sum over e's rows of dy[r][f] x[r][k],
@@ -321,23 +323,22 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  * The gradients are those of the product for the values x and w stand for; a
  * trainer that quantises its own activations and weights passes them straight
  * through the rounding.  Products are exact, sums fp32, each output rounded
- * once.  All pointers 16-byte aligned, strides multiples of 8 elements.
- * workspace: device, 256-byte aligned, >= qbmoe_mxfp4_workspace_bytes(R, E, N,
- * K) bytes (one size serves the three calls).  A bounded wait that expires is
- * reported by qbmoe_status(NULL, stream).
+ * once.  All pointers 16-byte aligned, strides multiples of 8 elements and at
+ * most 2^27, N and K at most 2^24.
+ * A bounded wait that expires is reported by qbmoe_status(NULL, stream).
  */
 int moe_mxfp4_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes,
                        uint8_t* scales, void* values, qbmoe_stream_t stream);
-size_t qbmoe_mxfp4_workspace_bytes(int R, int E, int N, int K);
+size_t qbmoe_mxfp4_workspace_bytes(int R, int K);
 int moe_mxfp4_matmul(int R, int E, int N, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales,
                      const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets, void* y, long long ldy,
                      void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
 int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,
                     const uint8_t* w_scales, const int32_t* offsets, void* dx, long long lddx,
-                    void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+                    qbmoe_stream_t stream);
 int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
                     const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
-                    void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+                    qbmoe_stream_t stream);
 
 /*
  * ---------------------------------------------------------------------------

@@ -130,11 +130,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_balance_loss.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_router_backward.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, ll, vp]
     lib.moe_mxfp4_quantize.argtypes = [ll, i, i, vp, ll, vp, vp, vp, vp]
-    lib.qbmoe_mxfp4_workspace_bytes.argtypes = [i, i, i, i]
+    lib.qbmoe_mxfp4_workspace_bytes.argtypes = [i, i]
     lib.qbmoe_mxfp4_workspace_bytes.restype = sz
     lib.moe_mxfp4_matmul.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, ll, vp, sz, vp]
-    lib.moe_mxfp4_dgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, vp, ll, vp, sz, vp]
-    lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp, sz, vp]
+    lib.moe_mxfp4_dgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, vp, ll, vp]
+    lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp]
     for nm in ("moe_balance_loss", "moe_router_backward", "moe_mxfp4_quantize", "moe_mxfp4_matmul",
                "moe_mxfp4_dgrad", "moe_mxfp4_wgrad"):
         getattr(lib, nm).restype = i

@@ -157,14 +157,15 @@ bool rows_ok(int K, int x_type, long long ldx) {
     return (x_type == QBMOE_F32 || x_type == QBMOE_BF16) && ldx >= K && ldx % (x_type == QBMOE_BF16 ? 8 : 4) == 0;
 }
 
+// The kernels index up to 16 rows with 32 bits.
+constexpr int kMaxK = 1 << 24;
+constexpr long long kMaxStride = 1LL << 27;
+
 bool product_sizes_ok(int R, int E, int N, int K, const int32_t* offsets) {
-    return R >= 0 && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && K >= 32 && K % 32 == 0 &&
-           (offsets || E == 1);
+    return R >= 0 && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && N <= kMaxK && K >= 32 &&
+           K % 32 == 0 && K <= kMaxK && (offsets || E == 1);
 }
-int check_workspace(const void* ws, size_t bytes, int R, int E, int N, int K) {
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return QBMOE_EINVAL;
-    return bytes < qbmoe_mxfp4_workspace_bytes(R, E, N, K) ? QBMOE_EWORKSPACE : QBMOE_OK;
-}
+bool stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= kMaxStride; }
 template <typename... P>
 bool all_aligned16(const P*... p) { return ((p != nullptr && qbh::aligned16(p)) && ...); }
 
@@ -200,8 +201,8 @@ extern "C" int moe_mxfp4_quantize(long long rows, int K, int x_type, const void*
     return qbh::mx_quantize(rows, K, x_type, x, ldx, codes, scales, values, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t qbmoe_mxfp4_workspace_bytes(int R, int E, int N, int K) {
-    if (R < 0 || E < 1 || E > QBMOE_MAX_EXPERTS || N < 8 || N % 8 || K < 32 || K % 32) return 0;
+extern "C" size_t qbmoe_mxfp4_workspace_bytes(int R, int K) {
+    if (R < 0 || K < 32 || K % 32 || K > kMaxK) return 0;
     // codes and scales of rows that come in another type
     return 256 + qbh::align_up((size_t)R * (K / 2), 256) + qbh::align_up((size_t)R * (K / 32), 256);
 }
@@ -210,18 +211,19 @@ extern "C" int moe_mxfp4_matmul(int R, int E, int N, int K, int x_type, const vo
                                 const uint8_t* x_scales, const uint8_t* w_codes, const uint8_t* w_scales,
                                 const int32_t* offsets, void* y, long long ldy, void* workspace,
                                 size_t workspace_bytes, qbmoe_stream_t stream) {
-    if (!product_sizes_ok(R, E, N, K, offsets) || ldy < N || ldy % 8) return QBMOE_EINVAL;
+    if (!product_sizes_ok(R, E, N, K, offsets) || !stride_ok(ldy, N)) return QBMOE_EINVAL;
     if (x_type == QBMOE_MXFP4 ? ldx != K : !rows_ok(K, x_type, ldx)) return QBMOE_EINVAL;
-    int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
-    if (rc) return rc;
+    const bool raw = x_type != QBMOE_MXFP4;
+    if (raw && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)) return QBMOE_EINVAL;
+    if (raw && workspace_bytes < qbmoe_mxfp4_workspace_bytes(R, K)) return QBMOE_EWORKSPACE;
     if (R == 0) return QBMOE_OK;
     if (!all_aligned16(static_cast<const uint8_t*>(x), w_codes, w_scales, static_cast<const uint8_t*>(y)) ||
-        !qbh::aligned16(offsets) || (x_type == QBMOE_MXFP4 && !all_aligned16(x_scales)))
+        !qbh::aligned16(offsets) || (!raw && !all_aligned16(x_scales)))
         return QBMOE_EINVAL;
-    if ((rc = qbh::device_init())) return rc;
+    const int rc = qbh::device_init();
+    if (rc) return rc;
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* scales = codes + qbh::align_up((size_t)R * (K / 2), 256);
-    const bool raw = x_type != QBMOE_MXFP4;
     qbh::MxProduct p{};
     p.R = R; p.E = E; p.N = N; p.K = K;
     p.x_codes = raw ? codes : static_cast<uint8_t*>(const_cast<void*>(x));
@@ -234,15 +236,14 @@ extern "C" int moe_mxfp4_matmul(int R, int E, int N, int K, int x_type, const vo
 
 extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,
                                const uint8_t* w_scales, const int32_t* offsets, void* dx, long long lddx,
-                               void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
-    if (!product_sizes_ok(R, E, N, K, offsets) || lddy < N || lddy % 8 || lddx < K || lddx % 8) return QBMOE_EINVAL;
-    int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
-    if (rc) return rc;
+                               qbmoe_stream_t stream) {
+    if (!product_sizes_ok(R, E, N, K, offsets) || !stride_ok(lddy, N) || !stride_ok(lddx, K)) return QBMOE_EINVAL;
     if (R == 0) return QBMOE_OK;
     if (!all_aligned16(static_cast<const uint8_t*>(dy), w_codes, w_scales, static_cast<const uint8_t*>(dx)) ||
         !qbh::aligned16(offsets))
         return QBMOE_EINVAL;
-    if ((rc = qbh::device_init())) return rc;
+    const int rc = qbh::device_init();
+    if (rc) return rc;
     qbh::MxGrad g{};
     g.weights = false;
     g.R = R; g.E = E; g.N = N; g.K = K;
@@ -254,14 +255,13 @@ extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long 
 
 extern "C" int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
                                const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
-                               void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
-    if (!product_sizes_ok(R, E, N, K, offsets) || lddy < N || lddy % 8) return QBMOE_EINVAL;
+                               qbmoe_stream_t stream) {
+    if (!product_sizes_ok(R, E, N, K, offsets) || !stride_ok(lddy, N)) return QBMOE_EINVAL;
     if (dw_dtype != QBMOE_F32 && dw_dtype != QBMOE_BF16) return QBMOE_EINVAL;
-    int rc = check_workspace(workspace, workspace_bytes, R, E, N, K);
-    if (rc) return rc;
     if (!dw || !qbh::aligned16(dw) || !qbh::aligned16(offsets)) return QBMOE_EINVAL;
     if (R > 0 && !all_aligned16(static_cast<const uint8_t*>(dy), x_codes, x_scales)) return QBMOE_EINVAL;
-    if ((rc = qbh::device_init())) return rc;
+    const int rc = qbh::device_init();
+    if (rc) return rc;
     qbh::MxGrad g{};
     g.weights = true;
     g.R = R; g.E = E; g.N = N; g.K = K;

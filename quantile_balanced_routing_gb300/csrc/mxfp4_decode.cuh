@@ -48,4 +48,24 @@ __device__ __forceinline__ void mx_decode_word(uint32_t w, const uint32_t (&h)[2
     for (int q = 0; q < 4; ++q) o[q] |= __byte_perm(w, w4, (q << 12) | ((4 + q) << 4)) & 0x80008000u;
 }
 
+// The E8M0 scale as a pair of bf16 (byte 0 is the subnormal 2^-127, 0xFF NaN).
+QB_DEV __nv_bfloat162 e8m0_bf16x2(uint32_t sc) {
+    const uint32_t b = sc == 0u ? 0x0040u : sc == 255u ? 0x7fffu : sc << 7;
+    const uint32_t bb = b * 0x10001u;
+    return *reinterpret_cast<const __nv_bfloat162*>(&bb);
+}
+
+// Eight E2M1 codes of one word -> four bf16 pairs times the scale: the same
+// lookups as mx_decode_word at scale 1, then one exact multiplication a pair
+// (an overflow gives infinity, as rounding the value would).
+QB_DEV void mx_decode_scaled(uint32_t w, __nv_bfloat162 scale, uint32_t (&o)[4]) {
+    const uint32_t h[2] = {0x3f3f3f00u, 0x40404040u}, l[2] = {0xc0800000u, 0xc0804000u};
+    mx_decode_word(w, h, l, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[i]), scale);
+        o[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
 }  // namespace qb

@@ -49,7 +49,7 @@ constexpr int kConvPer = kConvWarps / kStages;       // warps of a slot
 constexpr int kItems = kC * 4 / (32 * kConvPer);     // 32-column blocks a thread decodes
 constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;   // 608
 constexpr int kMmaWarp = 1, kWaitWarp = 2;
-constexpr int kHandoffBar = 1, kSlotBar = 2;          // kSlotBar + slot
+constexpr int kHandoffBar = 1, kEpiBar = 2, kSlotBar = 3;   // kSlotBar + slot
 constexpr long long kDefaultWait = 1LL << 17;
 constexpr long long kDrainWait = 1LL << 12;
 
@@ -64,6 +64,7 @@ struct Params {
     long long ldo;
     int R, E, N, K;
     int k_tiles, f_tiles, f_per; // 128-column tiles of K; weights: tiles of N and features in each
+    int step_e, step_f, step_k;  // weights: the grid size in those units
     int* status;
     long long wait_limit;
     int stall;
@@ -82,30 +83,44 @@ struct Tile {
 };
 template <bool kWeights>
 struct Tiles {
-    Walker<kN> w;
+    Walker<kN> w;      // rows
+    int e, ft, kt;     // weights: expert, feature tile, column tile (fastest)
     int t;
     QB_DEV int count(const Params& p, const Groups& gr) const {
         return kWeights ? p.E * p.f_tiles * p.k_tiles : gr.toff[p.E] * p.k_tiles;
     }
     QB_DEV void start(const Params& p, const Groups& gr) {
         t = blockIdx.x;
-        if (!kWeights) w.start(gr, p.E, p.k_tiles);
+        if (kWeights) {
+            const int row = t / p.k_tiles;
+            kt = t - row * p.k_tiles;
+            e = row / p.f_tiles;
+            ft = row - e * p.f_tiles;
+        } else {
+            w.start(gr, p.E, p.k_tiles);
+        }
     }
     QB_DEV void next(const Params& p, const Groups& gr) {
         t += gridDim.x;
-        if (!kWeights) w.next(gr, p.E, p.k_tiles);
+        if (kWeights) {   // the grid's stride in (e, ft, kt), with carries
+            kt += p.step_k;
+            ft += p.step_f;
+            e += p.step_e;
+            if (kt >= p.k_tiles) kt -= p.k_tiles, ++ft;
+            if (ft >= p.f_tiles) ft -= p.f_tiles, ++e;
+        } else {
+            w.next(gr, p.E, p.k_tiles);
+        }
     }
     QB_DEV Tile get(const Params& p, const Groups& gr) const {
         Tile x;
         if (kWeights) {
-            const int per = p.f_tiles * p.k_tiles;
-            x.e = t / per;
-            const int rem = t - x.e * per, ft = rem / p.k_tiles;
-            x.kt = rem - ft * p.k_tiles;
+            x.e = e;
+            x.kt = kt;
             x.row0 = ft * p.f_per;
             x.cols = min(p.f_per, p.N - x.row0);
-            x.b0 = gr.seg[x.e];
-            x.len = max(gr.seg[x.e + 1] - x.b0, 0);
+            x.b0 = gr.seg[e];
+            x.len = max(gr.seg[e + 1] - x.b0, 0);
             x.q0 = x.b0;
         } else {
             x.e = w.g;
@@ -259,13 +274,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
     } else if (warp >= kConvWarp && warp < kEpiWarp) {
         // ---------------------------------------------------------- converters
         // Thread (c, b) of a pair: steps c, c + 16, .. of a stage, column block b (32
-        // columns, one scale).  Four consecutive lanes read 64 bytes of one row; the
-        // upper two blocks write their 16-byte chunks in another order, so that
-        // eight lanes' stores fall on eight different chunk places.
+        // columns, one scale).  A warp reads 64 bytes of each of 8 rows; eight
+        // consecutive lanes have eight rows, whose 16-byte chunks the swizzle puts
+        // in eight different places.
         const int slot = (warp - kConvWarp) / kConvPer;
         const int ct = threadIdx.x - (kConvWarp + slot * kConvPer) * 32;
         constexpr int kPair = 32 * kConvPer, kRowsPer = kPair / 4;
-        const int b = ct & 3, c = ct >> 2, sw = b & 2;
+        const int b = lane >> 3, c = (ct >> 5) * 8 + (lane & 7);
         const int half = p.K / 2, pitch = p.K / 32;
         Cursor<kWeights> cur;
         cur.start(p, gr, n_tiles, it, slot);
@@ -277,15 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
         auto fetch = [&] {
             if (!cur.live) return;
             const int k = cur.x.kt * kM + 32 * b;
+            const int left = k < p.K ? cur.x.len - cur.c - c : 0;   // steps from this thread's first to the end
+            const uint8_t* codes = p.codes + (cur.x.q0 + cur.c + c) * half + k / 2;
+            const uint8_t* scales = p.scales + (cur.x.q0 + cur.c + c) * pitch + k / 32;
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int step = cur.c + c + kRowsPer * i;
                 v[i].q = make_uint4(0, 0, 0, 0);
                 v[i].sc = 127;
-                if (step < cur.x.len && k < p.K) {
-                    const long long row = cur.x.q0 + step;
-                    v[i].q = __ldg(reinterpret_cast<const uint4*>(p.codes + row * half + k / 2));
-                    v[i].sc = __ldg(p.scales + row * pitch + k / 32);
+                if (kRowsPer * i < left) {
+                    v[i].q = __ldg(reinterpret_cast<const uint4*>(codes + i * (kRowsPer * half)));
+                    v[i].sc = __ldg(scales + i * (kRowsPer * pitch));
                 }
             }
             if constexpr (kWeights) {
@@ -304,8 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             }
         };
         fetch();
-        uint8_t* A = a_ring + slot * kABytes;
         uint8_t* B = b_ring + slot * kBBytes;
+        uint4* dst[4];   // of the thread's first step; the swizzle repeats every 8 steps
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            dst[j] = reinterpret_cast<uint4*>(a_ring + slot * kABytes + mn_offset(c, 4 * b + j));
         while (cur.live) {
             tc::named_bar_sync(kSlotBar + slot, 32 + 32 * kConvPer);   // the slot is free
             if constexpr (kWeights) {
@@ -318,35 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             }
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                uint32_t q[4] = {v[i].q.x, v[i].q.y, v[i].q.z, v[i].q.w};
-                if (sw) { uint32_t t = q[0]; q[0] = q[2]; q[2] = t; t = q[1]; q[1] = q[3]; q[3] = t; }
-                const uint32_t sc = v[i].sc;
-                const int step = c + kRowsPer * i;
-                if (sc >= 2 && sc <= 252) {
-                    uint32_t th[2], tl[2];
-                    mx_tables((int)sc - 127, th, tl);
+                const uint32_t q[4] = {v[i].q.x, v[i].q.y, v[i].q.z, v[i].q.w};
+                const __nv_bfloat162 scale = e8m0_bf16x2(v[i].sc);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t o[4];
-                        mx_decode_word(q[j], th, tl, o);
-                        *reinterpret_cast<uint4*>(A + mn_offset(step, 4 * b + (j ^ sw))) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                } else {
-                    const float m = e8m0_value(sc);
-#pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t word = j < 2 ? (j ? q[1] : q[0]) : (j == 2 ? q[2] : q[3]);
-                        uint32_t o[4];
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const __nv_bfloat162 u = __floats2bfloat162_rn(e2m1_value(word >> (8 * h)) * m,
-                                                                           e2m1_value(word >> (8 * h + 4)) * m);
-                            o[h] = *reinterpret_cast<const uint32_t*>(&u);
-                        }
-                        *reinterpret_cast<uint4*>(A + mn_offset(step, 4 * b + (j ^ sw))) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t o[4];
+                    mx_decode_scaled(q[j], scale, o);
+                    dst[j][i * (kRowsPer * 128 / 16)] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             tc::fence_proxy_async_smem();   // generic-proxy writes -> tcgen05.mma reads
@@ -436,16 +433,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
         // time; bf16: neighbouring lanes exchange one of every two rows' values
         // and a warp stores 64 bytes of two rows.
         const int q = warp & 3, odd = lane & 1, part = (warp - kEpiWarp) >> 2;
+        const uint32_t ldo = (uint32_t)p.ldo;
+        bool dead = false;
         int ab = 0;
         uint32_t fph = 0;
         for (; it.t < n_tiles; it.next(p, gr)) {
             const Tile x = it.get(p, gr);
-            int ok = 1;
-            if (lane == 0) {
-                ok = tc::mbar_wait(&accf[ab], fph, lim);
-                if (!ok) expired();
+            if (warp == kEpiWarp && lane == 0) {   // one poller; an expiry leaves undefined outputs and a status
+                if (!dead && *abort_flag) dead = true;
+                if (!dead && !tc::mbar_wait_spin(&accf[ab], fph, lim)) { expired(); dead = true; }
             }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            __syncwarp();
+            tc::named_bar_sync(kEpiBar, 32 * kEpiWarps);
             tc::tc_fence_after();
             const long long first_row = kWeights ? (long long)x.e * p.N + x.row0 : x.row0;
             const int k = x.kt * kM + 32 * q;   // K is a multiple of 32: a warp's columns are all there or none
@@ -457,18 +456,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 if (x.len == 0)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = 0.0f;   // no rows: nothing was accumulated
+                Out* o = out + (long long)c0 * p.ldo;
+                const int left = cols - c0;
                 if constexpr (sizeof(Out) == 4) {
+                    o += lane;
+                    if (left >= 16) {   // no test a row
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c0 + i < cols) out[(long long)(c0 + i) * p.ldo + lane] = v[i];
+                        for (int i = 0; i < 16; ++i) o[(uint32_t)i * ldo] = v[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < left) o[(uint32_t)i * ldo] = v[i];
+                    }
                 } else {
+                    o += lane & ~1;
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                        const __nv_bfloat162 o =
+                        const __nv_bfloat162 h =
                             odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
-                        if (c0 + i + odd < cols)
-                            *reinterpret_cast<__nv_bfloat162*>(out + (long long)(c0 + i + odd) * p.ldo + (lane & ~1)) = o;
+                        if (i + odd < left) *reinterpret_cast<__nv_bfloat162*>(o + (uint32_t)(i + odd) * ldo) = h;
                     }
                 }
             }
@@ -488,8 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
 }
 
 template <bool kWeights, typename Out>
-int launch(const Params& p, long long tiles, cudaStream_t s) {
+int launch(Params& p, long long tiles, cudaStream_t s) {
     const int grid = (int)min(tiles, (long long)qbh::sm_count());
+    p.step_k = grid % p.k_tiles;
+    p.step_f = grid / p.k_tiles % p.f_tiles;
+    p.step_e = grid / p.k_tiles / p.f_tiles;
     k_mx_grad<kWeights, Out><<<grid, kThreads, smem_bytes(p.E), s>>>(p);
     return qbh::cuda_err(cudaGetLastError());
 }

@@ -12,10 +12,12 @@
 // One persistent warp-specialised kernel.  A stage is 256 elements of K: the
 // packed codes of 128 weight rows and of the tile's rows (128 bytes each, TMA,
 // 128-byte swizzle); their scales come in groups of two stages (16 bytes a row).
-//   warp 0      TMA producer of both operands' codes (one lane); it alone waits
-//               for a free stage and then meets the scale writers at a named
-//               barrier (a suspended mbarrier wait takes about a microsecond to come
-//               back, and every warp that polls instead slows the others)
+//   warp 0      TMA producer of the weights' codes (one lane); once it has a free
+//               stage it meets the scale writers at a named barrier (a
+//               suspended mbarrier wait takes about a microsecond to come back, and
+//               every warp that polls instead slows the others)
+//   last warp   TMA producer of the rows' codes (one lane that issued both took 570
+//               cycles a stage)
 //   warp 1      TMEM owner, MMA issuer (one lane): 4 x K = 64 MMAs a stage and
 //               one commit that frees it
 //   warp 2      the issuer's waiter (an mbarrier wait by the issuing thread
@@ -27,7 +29,8 @@
 //               shared memory to the stages' TMEM slots (tcgen05.st).  Copying them
 //               with tcgen05.cp from the issuer cost it 6 more instructions a
 //               stage: 813 cycles of issue, against 375 of MMAs at N = 192.
-//   warps 8-11  epilogue: TMEM -> bf16 pairs of features -> 64 bytes a row and warp
+//   warps 8+    epilogue, two warps per lane quarter (one on 16-row tiles): TMEM
+//               -> bf16 pairs of features -> 64 bytes a row and warp
 // Two accumulators alternate, so a tile's epilogue overlaps the next tile's
 // main loop.  Every mbarrier wait is bounded: on expiry the kernel records
 // QBMOE_ETIMEOUT, stops, lets its own copies and MMAs finish and frees TMEM.
@@ -44,9 +47,9 @@ using namespace qb;
 
 constexpr int kStageK = 256;                 // elements of K per stage (128 bytes of codes a row)
 constexpr int kABytes = 128 * 128;           // weight codes of a stage
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4;
-constexpr int kHandoffBar = 1, kStageBar = 2;
+constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8;
+constexpr int kSfSlots = 4;                  // scale groups in flight
+constexpr int kHandoffBar = 1, kEpiBar = 2, kStageBar = 3;
 constexpr int kMaxBoxes = 4;                 // row-tile maps: heights BN / n, 2 BN / n, ...
 constexpr long long kDefaultWait = 1LL << 17;   // polls (<= 20 us each) before a wait expires
 constexpr long long kDrainWait = 1LL << 12;
@@ -71,6 +74,9 @@ struct Params {
 
 template <int BN>
 struct Shape {
+    static constexpr int kEpiWarps = BN == 16 ? 4 : 8;
+    static constexpr int kProdBWarp = kEpiWarp + kEpiWarps;
+    static constexpr int kThreads = (kProdBWarp + 1) * 32;
     static constexpr int kBoxes = BN == 208 ? 4 : BN == 128 ? 2 : 1;
     static constexpr int kBox = BN / kBoxes;                     // a row tile is one copy, of the least multiple that holds it
     static constexpr int kNB = (BN + 127) / 128;                 // 128-row blocks of B's scales
@@ -84,7 +90,7 @@ struct Shape {
     static constexpr uint32_t kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
     static_assert(kColsUsed <= 512, "TMEM columns");
     static constexpr int smem(int E) {
-        return 1024 + stages * kStage + 2 * kSfBytes + (2 * (E + 1) + 64) * 4 + 256;
+        return 1024 + stages * kStage + kSfSlots * kSfBytes + (2 * (E + 1) + 64) * 4 + 256;
     }
 };
 
@@ -132,19 +138,19 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 }
 
 template <int BN>
-__global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_product(const __grid_constant__ Params p) {
     using Sh = Shape<BN>;
     constexpr int S = Sh::stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* a_ring = smem;
     uint8_t* b_ring = a_ring + S * kABytes;
-    uint8_t* sf_ring = b_ring + S * Sh::kBBytes;                 // [2][128 + BN rows][16]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sf_ring + 2 * Sh::kSfBytes);
+    uint8_t* sf_ring = b_ring + S * Sh::kBBytes;                 // [kSfSlots][128 + BN rows][16]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sf_ring + kSfSlots * Sh::kSfBytes);
     uint64_t* empty = full + S;
     uint64_t* sf_full = empty + S;
-    uint64_t* sf_empty = sf_full + 2;
-    uint64_t* accf = sf_empty + 2;
+    uint64_t* sf_empty = sf_full + kSfSlots;
+    uint64_t* accf = sf_empty + kSfSlots;
     uint64_t* acce = accf + 2;
     uint64_t* drain = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -152,21 +158,23 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     volatile int* go_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     int* scratch = reinterpret_cast<int*>(tmem_slot + 4);                     // [kThreads / 32]
     Groups gr;
-    gr.seg = scratch + 16;
+    gr.seg = scratch + 24;
     gr.toff = gr.seg + p.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long lim = p.wait_limit > 0 ? p.wait_limit : kDefaultWait;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            tc::mbar_init(&full[s], 5);      // the TMA producer and the four scale writers
+            tc::mbar_init(&full[s], 6);      // the two TMA producers and four scale writers
             tc::mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < kSfSlots; ++a) {
             tc::mbar_init(&sf_full[a], 1);
             tc::mbar_init(&sf_empty[a], 4);
+        }
+        for (int a = 0; a < 2; ++a) {
             tc::mbar_init(&accf[a], 1);
-            tc::mbar_init(&acce[a], 4);
+            tc::mbar_init(&acce[a], Sh::kEpiWarps);
         }
         tc::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
     }
     if (!p.weights_ready) pdl_wait();
     tc::tc_fence_before();
-    load_groups<BN, kThreads>(gr, p.offsets, p.E, p.R, scratch);
+    load_groups<BN, Sh::kThreads>(gr, p.offsets, p.E, p.R, scratch);
     tc::tc_fence_after();
     const uint32_t tbase = *tmem_slot;
     const int n_tiles = gr.toff[p.E] * p.m_total;
@@ -192,33 +200,34 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         *abort_flag = 1;
     };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------- TMA producer
+    if (warp == 0 || warp == Sh::kProdBWarp) {
+        // ---------------------------------------------------------- TMA producers
+        const bool is_a = warp == 0;
         uint32_t issued = 0, last_par = 0;
         int s = 0;
         uint32_t ph = 0;
-        bool rows_ready = !p.weights_ready;
+        if (!is_a && p.weights_ready) pdl_wait();   // the rows' codes come from the kernel before this one
         bool dead = false;   // lane 0: an expiry; only the meetings go on
         for (int t = first; t < n_tiles; t += step) {
             const int box = (w.nrows - 1) / Sh::kBox;
-            const int ya = w.g * p.N + w.m * 128, yb = w.row0;
+            const CUtensorMap* map = is_a ? &p.a : &p.b[box];
+            const int row = is_a ? w.g * p.N + w.m * 128 : w.row0;
+            const uint32_t bytes = is_a ? kABytes : (box + 1) * Sh::kBox * 128;
+            constexpr int kAStride = kABytes, kBStride = Sh::kBBytes;
+            const int stride = is_a ? kAStride : kBStride;
+            uint8_t* ring = is_a ? a_ring : b_ring;
             w.next(gr, p.E, p.m_total);
             if (lane == 0 && *abort_flag) dead = true;
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if (lane == 0 && !dead && !tc::mbar_wait_spin(&empty[s], ph ^ 1u, lim)) { expired(); dead = true; }
                 if (lane == 0 && !dead) {
-                    tc::mbar_expect_tx(&full[s], kABytes + (box + 1) * Sh::kBox * 128);
-                    tc::tma_load_2d(a_ring + s * kABytes, &p.a, &full[s], kb * 128, ya);
-                    if (!rows_ready) {   // the rows' codes come from the kernel before this one
-                        pdl_wait();
-                        rows_ready = true;
-                    }
-                    tc::tma_load_2d(b_ring + s * Sh::kBBytes, &p.b[box], &full[s], kb * 128, yb);
+                    tc::mbar_expect_tx(&full[s], bytes);
+                    tc::tma_load_2d(ring + s * stride, map, &full[s], kb * 128, row);
                     issued |= 1u << s;
                     last_par = (last_par & ~(1u << s)) | (ph << s);
                 }
                 __syncwarp();
-                tc::named_bar_sync(kStageBar, 160);
+                if (is_a) tc::named_bar_sync(kStageBar, 160);
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
         }
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
                         tc::tma_load_2d(SF + 128 * 16, &p.b_sf, &sf_full[gs], kb * 8, yb);
                         sf_issued |= 1u << gs;
                         sf_par = (sf_par & ~(1u << gs)) | (gph << gs);
-                        if ((gs ^= 1) == 0) gph ^= 1u;
+                        if (++gs == kSfSlots) { gs = 0; gph ^= 1u; }
                     }
                 }
                 if (__shfl_sync(0xffffffffu, stop, 0)) break;
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
                     if (lane + 32 * j < BN) SF[128 + lane + 32 * j] = rb[j];
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sf_full[gs]);
-                if ((gs ^= 1) == 0) gph ^= 1u;
+                if (++gs == kSfSlots) { gs = 0; gph ^= 1u; }
                 kb += 2;
                 if (kb >= p.nkb) {
                     kb = 0;
@@ -302,9 +311,9 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         }
         __syncthreads();
         if (lane == 0 && *abort_flag)
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kSfSlots; ++i)
                 if ((sf_issued >> i) & 1u) tc::mbar_wait(&sf_full[i], (sf_par >> i) & 1u, kDrainWait);
-    } else if (warp >= kSfWarp && warp < kSfWarp + 4) {
+    } else if (warp >= kSfWarp && warp < kEpiWarp) {
         // ---------------------------------------------------------- scale writers
         // The MMA reads the scale words of row r (four bytes: K = 128) from lane
         // r % 32, column r / 32 of a slot, in each lane quarter.
@@ -315,28 +324,19 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         for (int t = first; t < n_tiles; t += step) {
             if (lane == 0 && *abort_flag) dead = true;
             for (int kb0 = 0; kb0 < p.nkb; kb0 += 2) {
+                const int stages = min(2, p.nkb - kb0);
+                if (lane == 0 && !dead && !tc::mbar_wait_spin(&sf_full[gs], gph, lim)) { expired(); dead = true; }
+                __syncwarp();
+                const uint4* SF = reinterpret_cast<const uint4*>(sf_ring + gs * Sh::kSfBytes);
                 uint4 ra[4], rb[4 * Sh::kNB];
 #pragma unroll
+                for (int j = 0; j < 4; ++j) ra[j] = SF[lane + 32 * j];
+#pragma unroll
+                for (int j = 0; j < 4 * Sh::kNB; ++j)
+                    rb[j] = lane + 32 * j < BN ? SF[128 + lane + 32 * j] : make_uint4(0, 0, 0, 0);
+#pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (kb0 + u >= p.nkb) break;
-                    tc::named_bar_sync(kStageBar, 160);   // the stage's slot is free
-                    if (u == 0) {
-                        if (lane == 0 && !dead && !tc::mbar_wait_spin(&sf_full[gs], gph, lim)) { expired(); dead = true; }
-                        __syncwarp();
-                    }
-                    if (u == 0) {
-                        const uint4* SF = reinterpret_cast<const uint4*>(sf_ring + gs * Sh::kSfBytes);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) ra[j] = SF[lane + 32 * j];
-#pragma unroll
-                        for (int j = 0; j < 4 * Sh::kNB; ++j)
-                            rb[j] = lane + 32 * j < BN ? SF[128 + lane + 32 * j] : make_uint4(0, 0, 0, 0);
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&sf_empty[gs]);   // the group is in registers
-                        if ((gs ^= 1) == 0) gph ^= 1u;
-                    }
-                    tc::tc_fence_after();
-                    const uint32_t slot = tbase + lanes + 2 * BN + s * Sh::kSfCols;
+                    if (u >= stages) break;
                     uint32_t va[8], vb[8 * Sh::kNB];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -345,14 +345,21 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
 #pragma unroll
                         for (int j = 0; j < 4 * Sh::kNB; ++j) vb[4 * Sh::kNB * c + j] = word(rb[j], 2 * u + c);
                     }
+                    tc::named_bar_sync(kStageBar, 160);   // the stage's slot is free
+                    tc::tc_fence_after();
+                    const int at = s + u < S ? s + u : s + u - S;
+                    const uint32_t slot = tbase + lanes + 2 * BN + at * Sh::kSfCols;
                     tc::tmem_st8(slot, va);
                     if constexpr (Sh::kNB == 2) tc::tmem_st16(slot + 8, vb); else tc::tmem_st8(slot + 8, vb);
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&full[s]);
-                    if (++s == S) s = 0;
+                    if (lane == 0) tc::mbar_arrive(&full[at]);
                 }
+                if (lane == 0) tc::mbar_arrive(&sf_empty[gs]);   // read before the stages' arrivals
+                s += stages;
+                if (s >= S) s -= S;
+                if (++gs == kSfSlots) { gs = 0; gph ^= 1u; }
             }
         }
         __syncthreads();
@@ -370,16 +377,22 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
             if (!go) break;
             const uint32_t d = tbase + ab * BN;
             for (int kb = 0; kb < p.nkb; ++kb) {
+                // the stage's addresses, before the wait for it
+                const uint32_t ca = tbase + 2 * BN + s * Sh::kSfCols, cb = ca + 8;
+                const uint64_t ad = a0 + (uint64_t)(s * (kABytes >> 4)), bd = b0 + (uint64_t)(s * (Sh::kBBytes >> 4));
+                const int left = p.K - kb * kStageK;
                 tc::named_bar_sync(kHandoffBar, 64);   // stage s has landed
                 if (lane == 0) {
                     tc::tc_fence_after();
-                    const uint32_t ca = tbase + 2 * BN + s * Sh::kSfCols, cb = ca + 8;
-                    const uint64_t ad = a0 + (uint64_t)(s * (kABytes >> 4)), bd = b0 + (uint64_t)(s * (Sh::kBBytes >> 4));
-                    const int left = p.K - kb * kStageK;
                     mma_mxf4(d, ad, bd, id0, ca, cb, kb != 0);
-                    if (left > 64) mma_mxf4(d, ad + 2, bd + 2, id2, ca, cb, 1);
-                    if (left > 128) mma_mxf4(d, ad + 4, bd + 4, id0, ca + 4, cb + 4 * Sh::kNB, 1);
-                    if (left > 192) mma_mxf4(d, ad + 6, bd + 6, id2, ca + 4, cb + 4 * Sh::kNB, 1);
+                    if (left > 192) {
+                        mma_mxf4(d, ad + 2, bd + 2, id2, ca, cb, 1);
+                        mma_mxf4(d, ad + 4, bd + 4, id0, ca + 4, cb + 4 * Sh::kNB, 1);
+                        mma_mxf4(d, ad + 6, bd + 6, id2, ca + 4, cb + 4 * Sh::kNB, 1);
+                    } else {
+                        if (left > 64) mma_mxf4(d, ad + 2, bd + 2, id2, ca, cb, 1);
+                        if (left > 128) mma_mxf4(d, ad + 4, bd + 4, id0, ca + 4, cb + 4 * Sh::kNB, 1);
+                    }
                     tc::tc_commit(&empty[s]);
                 }
                 __syncwarp();
@@ -430,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
         // Neighbouring lanes exchange one of every two rows' values, so that a
         // lane stores two features of one row and a warp 64 bytes of two rows:
         // no shared memory, whose latency the MMAs raise.
-        const int q = warp & 3;
+        const int q = warp & 3, part = (warp - kEpiWarp) >> 2;
+        bool dead = false;
         int ab = 0;
         uint32_t fph = 0;
         for (int t = first; t < n_tiles; t += step) {
@@ -438,22 +452,23 @@ __global__ void __launch_bounds__(kThreads, BN == 16 ? 2 : 1) k_mx_product(const
             const int f = w.m * 128 + 32 * q + (lane & ~1);
             __nv_bfloat16* out = p.y + (long long)(w.row0 + odd) * p.ldy + f;
             w.next(gr, p.E, p.m_total);
-            int ok = 1;
-            if (lane == 0) {
-                ok = tc::mbar_wait(&accf[ab], fph, lim);
-                if (!ok) expired();
+            if (warp == kEpiWarp && lane == 0) {   // one poller; an expiry leaves undefined outputs and a status
+                if (!dead && *abort_flag) dead = true;
+                if (!dead && !tc::mbar_wait_spin(&accf[ab], fph, lim)) { expired(); dead = true; }
             }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            __syncwarp();
+            tc::named_bar_sync(kEpiBar, 32 * Sh::kEpiWarps);
             tc::tc_fence_after();
-            for (int c0 = 0; c0 < nrows; c0 += 16) {
+            for (int c0 = 16 * part; c0 < nrows; c0 += 4 * Sh::kEpiWarps) {
                 float v[16];
                 tc::tmem_ld16(tbase + ab * BN + (static_cast<uint32_t>(32 * q) << 16) + c0, v);
+                __nv_bfloat16* o = out + (long long)c0 * p.ldy;
+                const int left = f < p.N ? nrows - c0 - odd : 0;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                    const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
-                    if (c0 + i + odd < nrows && f < p.N)
-                        *reinterpret_cast<__nv_bfloat162*>(out + (long long)(c0 + i) * p.ldy) = o;
+                    const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
+                    if (i < left) *reinterpret_cast<__nv_bfloat162*>(o + (uint32_t)i * (uint32_t)p.ldy) = h;
                 }
             }
             tc::tc_fence_before();
@@ -521,9 +536,9 @@ int launch(const qbh::MxProduct& q, Params& p, cudaStream_t s) {
         // the product may set itself up, and load weights, while its rows are quantised
         const int rc = qbh::mx_quantize(q.R, q.K, q.raw_type, q.raw, q.raw_ld, q.x_codes, q.x_scales, nullptr, s);
         if (rc) return rc;
-        return qbh::launch_pdl(k_mx_product<BN>, dim3(grid), dim3(kThreads), smem, s, p);
+        return qbh::launch_pdl(k_mx_product<BN>, dim3(grid), dim3(Shape<BN>::kThreads), smem, s, p);
     }
-    k_mx_product<BN><<<grid, kThreads, smem, s>>>(p);
+    k_mx_product<BN><<<grid, Shape<BN>::kThreads, smem, s>>>(p);
     return qbh::cuda_err(cudaGetLastError());
 }
 

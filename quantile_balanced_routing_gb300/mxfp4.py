@@ -32,11 +32,11 @@ def _mxfp4_shape(what, name, t):
     c, s = t
     if c.dtype is not torch.uint8 or s.dtype is not torch.uint8 or not c.is_contiguous() or not s.is_contiguous():
         _refuse(what, f"{name}'s codes and scales are contiguous uint8")
-    lead, half = c.shape[:-1], c.shape[-1]
-    if half == 0 or half % (BLOCK // 2) or s.dim() != c.dim() or s.shape[-1] * (BLOCK // 2) != half or \
-            s.shape[:-1] != lead:
+    (*lead, half), (*lead_s, blocks) = c.shape, s.shape
+    if half == 0 or blocks * (BLOCK // 2) != half or lead != lead_s:
         _refuse(what, f"{name} is codes [..., K/2] and scales [..., K/32], K a multiple of {BLOCK}")
-    return (*lead, 2 * half)
+    lead.append(2 * half)
+    return lead
 
 
 def _row_stride(what, name, t, align):
@@ -134,10 +134,12 @@ def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
     cur = _here(what, rows, scales, w.codes, w.scales, offsets)
     lib, dev = load_library(), rows.device
     y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
-    nbytes = lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws, nbytes = None, 0
+    if scales is None:
+        nbytes = lib.qbmoe_mxfp4_workspace_bytes(R, K)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     rc = lib.moe_mxfp4_matmul(R, E, N, K, kind, rows.data_ptr(), ld, _p(scales), w.codes.data_ptr(),
-                              w.scales.data_ptr(), _p(offsets), y.data_ptr(), N, ws.data_ptr(), nbytes, cur)
+                              w.scales.data_ptr(), _p(offsets), y.data_ptr(), N, _p(ws), nbytes, cur)
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_matmul")
     return y
@@ -169,20 +171,17 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
         _refuse(what, "dw is fp32 or bf16")
     cur = _here(what, dy, xq.codes, xq.scales, w.codes, w.scales, offsets)
     lib, dev, dx, dw = load_library(), dy.device, None, None
-    nbytes = lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if need_dx:
         dx = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
         rc = lib.moe_mxfp4_dgrad(R, E, N, K, dy.data_ptr(), ld, w.codes.data_ptr(), w.scales.data_ptr(), _p(offsets),
-                                 dx.data_ptr(), K, ws.data_ptr(), nbytes, cur)
+                                 dx.data_ptr(), K, cur)
         if rc:
             raise QbmoeError(rc, "moe_mxfp4_dgrad")
     if need_dw:
         dw = torch.empty((N, K) if offsets is None else (E, N, K), dtype=torch.float32 if f32 else torch.bfloat16,
                          device=dev)
         rc = lib.moe_mxfp4_wgrad(R, E, N, K, dy.data_ptr(), ld, xq.codes.data_ptr(), xq.scales.data_ptr(),
-                                 _p(offsets), QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), ws.data_ptr(), nbytes,
-                                 cur)
+                                 _p(offsets), QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), cur)
         if rc:
             raise QbmoeError(rc, "moe_mxfp4_wgrad")
     return dx, dw

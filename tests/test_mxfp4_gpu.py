@@ -310,10 +310,8 @@ def test_output_stride_and_rows_without_an_expert():
     x, w, off = on_gpu(Q, xq, wq, offsets, E, N, K)
     lib = Q.load_library()
     y = torch.full((R, 64), 7.0, dtype=torch.bfloat16, device="cuda")
-    ws = torch.empty(lib.qbmoe_mxfp4_workspace_bytes(R, E, N, K), dtype=torch.uint8, device="cuda")
     rc = lib.moe_mxfp4_matmul(R, E, N, K, Q.QBMOE_MXFP4, x.codes.data_ptr(), K,
-                              *(t.data_ptr() for t in (x.scales, w.codes, w.scales, off, y)), 64, ws.data_ptr(),
-                              ws.numel(), None)
+                              *(t.data_ptr() for t in (x.scales, w.codes, w.scales, off, y)), 64, None, 0, None)
     torch.cuda.synchronize()
     assert rc == 0
     want, mags = M.matmul(xq[2], wq[2].reshape(E, N, K), offsets)
@@ -351,18 +349,22 @@ def test_bounded_wait_reports_and_recovers():
     """The issuer withholds its first accumulator: the waits run out, the status says so, the next call is right."""
     import quantile_balanced_routing_gb300 as Q
     lib = Q.load_library()
-    xq, wq, offsets, _ = product_case(611, 24, 264, 544, 2.0)
+    xq, wq, offsets, dy = product_case(611, 24, 264, 544, 2.0)
     x, w, off = on_gpu(Q, xq, wq, offsets, 24, 264, 544)
-    want = Q.mxfp4_matmul(x, w, off)
+    dy = dy.cuda()
+    calls = [lambda: Q.mxfp4_matmul(x, w, off), lambda: Q.mxfp4_matmul_backward(dy, x, w, off, need_dw=False)[0],
+             lambda: Q.mxfp4_matmul_backward(dy, x, w, off, need_dx=False)[1]]
+    want = [f() for f in calls]
     assert Q.qbmoe_status(None, None) == 0
-    lib.qbmoe_set_wait_limit(None, 200)
-    lib.qbmoe_debug_stall(None, 1)
-    try:
-        Q.mxfp4_matmul(x, w, off)
-        assert Q.qbmoe_status(None, None) == Q.QBMOE_ETIMEOUT
-    finally:
-        lib.qbmoe_debug_stall(None, 0)
-        lib.qbmoe_set_wait_limit(None, 0)
-    assert Q.qbmoe_status(None, None) == 0
-    assert torch.equal(Q.mxfp4_matmul(x, w, off), want)
-    assert Q.qbmoe_status(None, None) == 0
+    for f, right in zip(calls, want):
+        lib.qbmoe_set_wait_limit(None, 200)
+        lib.qbmoe_debug_stall(None, 1)
+        try:
+            f()
+            assert Q.qbmoe_status(None, None) == Q.QBMOE_ETIMEOUT
+        finally:
+            lib.qbmoe_debug_stall(None, 0)
+            lib.qbmoe_set_wait_limit(None, 0)
+        assert Q.qbmoe_status(None, None) == 0
+        assert torch.equal(f(), right)
+        assert Q.qbmoe_status(None, None) == 0

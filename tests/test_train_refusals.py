@@ -68,16 +68,16 @@ def test_quantize_refuses(lib, at, value):
 
 # R, E, N, K, x_type, x, ldx, x_scales, w_codes, w_scales, offsets, y, ldy, workspace, bytes, stream
 MATMUL = [4, 2, 16, 64, 2, FAKE, 64, FAKE, FAKE, FAKE, FAKE, FAKE, 16, FAKE, BIG, None]
-# R, E, N, K, dy, lddy, w_codes, w_scales, offsets, dx, lddx, workspace, bytes, stream
-DGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, FAKE, 64, FAKE, BIG, None]
-# R, E, N, K, dy, lddy, x_codes, x_scales, offsets, dw_dtype, dw, workspace, bytes, stream
-WGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, 0, FAKE, FAKE, BIG, None]
-SIZES = [(0, -1), (1, 0), (1, 1025), (2, 0), (2, 12), (3, 0), (3, 48)]
+# R, E, N, K, dy, lddy, w_codes, w_scales, offsets, dx, lddx, stream
+DGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, FAKE, 64, None]
+# R, E, N, K, dy, lddy, x_codes, x_scales, offsets, dw_dtype, dw, stream
+WGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, 0, FAKE, None]
+SIZES = [(0, -1), (1, 0), (1, 1025), (2, 0), (2, 12), (3, 0), (3, 48), (3, 1 << 25)]
 
 
 @pytest.mark.parametrize("at,value", SIZES + [(4, 3), (5, None), (5, FAKE + 8), (6, 72), (7, FAKE + 8),
                                               (7, None), (8, None), (9, FAKE + 8), (10, None), (10, FAKE + 4),
-                                              (11, None), (12, 8), (12, 20), (13, None), (13, FAKE + 16), (4, 1 << 20)])
+                                              (11, None), (12, 8), (12, 20), (12, 1 << 28), (4, 1 << 20)])
 def test_matmul_refuses(lib, at, value):
     assert lib.moe_mxfp4_matmul(*changed(MATMUL, at, value)) == Q.QBMOE_EINVAL
 
@@ -87,24 +87,27 @@ def test_matmul_refuses_rows_it_cannot_quantise(lib, x_type, ldx):
     assert lib.moe_mxfp4_matmul(*changed(changed(MATMUL, 4, x_type), 6, ldx)) == Q.QBMOE_EINVAL
 
 
+@pytest.mark.parametrize("workspace", [None, FAKE + 16])
+def test_matmul_needs_an_aligned_workspace_to_quantise(lib, workspace):
+    assert lib.moe_mxfp4_matmul(*changed(changed(MATMUL, 4, 1), 13, workspace)) == Q.QBMOE_EINVAL
+
+
 @pytest.mark.parametrize("at,value", SIZES + [(4, None), (5, 8), (5, 20), (6, None), (7, FAKE + 8), (8, None),
-                                              (9, None), (10, 63), (10, 68), (11, None)])
+                                              (9, None), (10, 63), (10, 68), (10, 1 << 28)])
 def test_dgrad_refuses(lib, at, value):
     assert lib.moe_mxfp4_dgrad(*changed(DGRAD, at, value)) == Q.QBMOE_EINVAL
 
 
 @pytest.mark.parametrize("at,value", SIZES + [(4, None), (5, 8), (5, 20), (6, None), (7, FAKE + 8), (8, None),
-                                              (9, 2), (10, None), (10, FAKE + 8), (11, FAKE + 64)])
+                                              (9, 2), (10, None), (10, FAKE + 8), (5, 1 << 28)])
 def test_wgrad_refuses(lib, at, value):
     assert lib.moe_mxfp4_wgrad(*changed(WGRAD, at, value)) == Q.QBMOE_EINVAL
 
 
 def test_workspace_too_small(lib):
-    need = lib.qbmoe_mxfp4_workspace_bytes(4, 2, 16, 64)
-    assert need > 0 and lib.qbmoe_mxfp4_workspace_bytes(4, 2, 12, 64) == 0
-    for fn, args, at in ((lib.moe_mxfp4_matmul, MATMUL, 14), (lib.moe_mxfp4_dgrad, DGRAD, 12),
-                         (lib.moe_mxfp4_wgrad, WGRAD, 12)):
-        assert fn(*changed(args, at, need - 1)) == Q.QBMOE_EWORKSPACE
+    need = lib.qbmoe_mxfp4_workspace_bytes(4, 64)
+    assert need > 4 * 34 and lib.qbmoe_mxfp4_workspace_bytes(4, 48) == 0
+    assert lib.moe_mxfp4_matmul(*changed(changed(MATMUL, 4, 1), 14, need - 1)) == Q.QBMOE_EWORKSPACE
 
 
 def refuses(fn, *args, **kw):
