@@ -41,6 +41,7 @@ int qbh::device_init() {
     int rc = check_device_arch(dev);
     if (!rc) rc = qbh::route_init_attributes();
     if (!rc) rc = qbh::tc_init_attributes();
+    if (!rc) rc = qbh::balance_init();
     if (!rc) rc = qbh::mx_product_init();
     if (!rc) rc = qbh::mx_grad_init();
     if (rc) {

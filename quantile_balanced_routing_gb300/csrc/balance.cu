@@ -232,8 +232,10 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 //   dx_j = d_j (f_j - D) / S_t                              balance loss
 //        + d_j (dw_i - sum_l dw_l w_l) / sum_l s_(idx_l)    j = idx_i, mixture weights
 // A CTA has a chunk of tokens and f of the chunk's sequence in shared memory
-// (a chunk that crosses a boundary goes through its sequences in turn).  The
-// dense row is stored first, then the k chosen entries over it.
+// (a chunk that crosses a boundary goes through its sequences in turn).  A warp
+// has its next row on the way to shared memory (cp.async) while it works on this
+// one, where rows are 16-byte vectors.  The dense row is stored first, then the k
+// chosen entries over it.
 // ---------------------------------------------------------------------------
 struct RouterGradArgs {
     int T, n, k, S, chunk;
@@ -249,12 +251,46 @@ struct RouterGradArgs {
     void* out;
 };
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+
 template <typename T, int V>
-__global__ void __launch_bounds__(kBalThreads, 4) k_router_backward(const RouterGradArgs a) {
-    extern __shared__ __align__(16) float fs[];   // [n rounded up to 8]
+__global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const RouterGradArgs a) {
+    extern __shared__ __align__(16) float fs[];   // [n rounded up to 8], then two rows a warp (V > 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    T* rows = reinterpret_cast<T*>(fs + ((a.n + 7) & ~7)) + (size_t)2 * warp * a.n;
     const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
+    // this token's mask, and the expert and gradient of the lane's route
+    auto scalars = [&](int t, bool& live, int& id, float& d) {
+        live = t < c1 && (!a.mask || __ldg(a.mask + t));
+        id = -1;
+        d = 0.0f;
+        if (a.dw && lane < a.k && t < c1) {
+            id = __ldg(a.idx + (long long)t * a.k + lane);
+            d = __ldg(a.dw + (long long)t * a.k + lane);
+        }
+    };
+    auto fetch = [&](int t, int buf) {
+        if constexpr (V > 1) {
+            if (t < c1) {
+                const T* row = static_cast<const T*>(a.logits) + (long long)t * a.ld;
+                for (int j = lane * V; j < a.n; j += 32 * V) cp_async16(rows + buf * a.n + j, row + j);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
     int q = a.dloss && a.seq ? find_seq(a.seq, a.S, c0) : 0;
+    // The warp's tokens c0 + warp, c0 + warp + 8, ... in turn, whatever their sequence.
+    int t = c0 + warp, buf = 0;
+    bool live;
+    int id;
+    float d;
+    fetch(t, buf);
+    scalars(t, live, id, d);
     for (int t0 = c0; t0 < c1; ++q) {
         const int t1 = a.dloss && a.seq && q + 1 < a.S ? min(c1, max(t0, __ldg(a.seq + q + 1))) : c1;
         if (t1 > t0) {
@@ -268,77 +304,89 @@ __global__ void __launch_bounds__(kBalThreads, 4) k_router_backward(const Router
                 fs[j] = a.dloss ? scale * (float)__ldg(a.counts + (long long)q * a.n + j) : 0.0f;
             __syncthreads();
         }
-        for (int t = t0 + warp; t < t1; t += kBalWarps) {
+        for (; t < t1; t += kBalWarps, buf ^= 1) {
             const T* row = static_cast<const T*>(a.logits) + (long long)t * a.ld;
             T* out = static_cast<T*>(a.out) + (long long)t * a.ldg;
-            if (a.mask && !__ldg(a.mask + t)) {
+            fetch(t + kBalWarps, buf ^ 1);
+            bool next_live;
+            int next_id;
+            float next_d;
+            scalars(t + kBalWarps, next_live, next_id, next_d);
+            if constexpr (V > 1) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                __syncwarp();
+                row = rows + buf * a.n;
+            }
+            if (!live) {
                 for (int j = lane; j < a.n; j += 32) out[j] = from_f32<T>(0.0f);
-                continue;
-            }
-            float x[kMaxPerLane];   // the row, then its slopes
-            load_row<T, V>(row, a.n, lane, x);
-            // the chosen experts, one a lane
-            int id = -1;
-            float d = 0.0f, own = 0.0f, slope = 0.0f;
-            if (a.dw && lane < a.k) {
-                id = __ldg(a.idx + (long long)t * a.k + lane);
-                if ((unsigned)id < (unsigned)a.n) {
-                    d = __ldg(a.dw + (long long)t * a.k + lane);
-                    own = score_slope(to_f32<T>(row[id]), slope);
-                } else {
-                    id = -1;
-                }
-            }
-            float sum = 0.0f, dot = 0.0f;
+            } else {
+                // the chosen experts, one a lane
+                float own = 0.0f, slope = 0.0f;
+                const bool chosen = (unsigned)id < (unsigned)a.n;
+                if (chosen) own = score_slope(to_f32<T>(row[id]), slope);
+                else d = 0.0f;
+                float x[kMaxPerLane];   // the row, then its slopes
+                if (V == 1) load_row<T, V>(row, a.n, lane, x);
+                float sum = 0.0f, dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kMaxPerLane / V; ++i) {
-                const int j = (32 * i + lane) * V;
-                if (j >= a.n) continue;
-                float f[V];
-                if constexpr (V == 1) f[0] = fs[j];
-                else
-#pragma unroll
-                    for (int u = 0; u < V / 4; ++u)
-                        *reinterpret_cast<float4*>(f + 4 * u) = *reinterpret_cast<const float4*>(fs + j + 4 * u);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float sl;
-                    const float s = score_slope(x[i * V + v], sl);
-                    x[i * V + v] = sl;
-                    sum += s;
-                    dot = fmaf(f[v], s, dot);
-                }
-            }
-            const float inv = __fdividef(1.0f, warp_sum(sum));
-            const float D = warp_sum(dot) * inv;
-            float w_inv = 0.0f, mean = 0.0f;
-            if (a.dw) {
-                const float chosen = warp_sum(own);
-                w_inv = chosen > 0.0f ? 1.0f / chosen : 0.0f;
-                mean = warp_sum(d * own) * w_inv;
-            }
-#pragma unroll
-            for (int i = 0; i < kMaxPerLane / V; ++i) {
-                const int j = (32 * i + lane) * V;
-                if (j >= a.n) continue;
-                if constexpr (V == 1) {
-                    out[j] = from_f32<T>(x[i] * ((fs[j] - D) * inv));
-                } else {
+                for (int i = 0; i < kMaxPerLane / V; ++i) {
+                    const int j = (32 * i + lane) * V;
+                    if (j >= a.n) continue;
                     float f[V];
+                    if constexpr (V == 1) {
+                        f[0] = fs[j];
+                    } else {
 #pragma unroll
-                    for (int u = 0; u < V / 4; ++u)
-                        *reinterpret_cast<float4*>(f + 4 * u) = *reinterpret_cast<const float4*>(fs + j + 4 * u);
-                    uint4 o;
-                    T* e = reinterpret_cast<T*>(&o);
+                        for (int u = 0; u < V / 4; ++u)
+                            *reinterpret_cast<float4*>(f + 4 * u) = *reinterpret_cast<const float4*>(fs + j + 4 * u);
+                        const uint4 u = *reinterpret_cast<const uint4*>(row + j);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) e[v] = from_f32<T>(x[i * V + v] * ((f[v] - D) * inv));
-                    *reinterpret_cast<uint4*>(out + j) = o;
+                        for (int v = 0; v < V; ++v) x[i * V + v] = to_f32<T>(reinterpret_cast<const T*>(&u)[v]);
+                    }
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float sl;
+                        const float s = score_slope(x[i * V + v], sl);
+                        x[i * V + v] = sl;
+                        sum += s;
+                        dot = fmaf(f[v], s, dot);
+                    }
+                }
+                const float inv = __fdividef(1.0f, warp_sum(sum));
+                const float D = warp_sum(dot) * inv;
+                float w_inv = 0.0f, mean = 0.0f;
+                if (a.dw) {
+                    const float all = warp_sum(own);
+                    w_inv = all > 0.0f ? 1.0f / all : all != all ? all : 0.0f;
+                    mean = warp_sum(d * own) * w_inv;
+                }
+#pragma unroll
+                for (int i = 0; i < kMaxPerLane / V; ++i) {
+                    const int j = (32 * i + lane) * V;
+                    if (j >= a.n) continue;
+                    if constexpr (V == 1) {
+                        out[j] = from_f32<T>(x[i] * ((fs[j] - D) * inv));
+                    } else {
+                        float f[V];
+#pragma unroll
+                        for (int u = 0; u < V / 4; ++u)
+                            *reinterpret_cast<float4*>(f + 4 * u) = *reinterpret_cast<const float4*>(fs + j + 4 * u);
+                        uint4 o;
+                        T* e = reinterpret_cast<T*>(&o);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) e[v] = from_f32<T>(x[i * V + v] * ((f[v] - D) * inv));
+                        *reinterpret_cast<uint4*>(out + j) = o;
+                    }
+                }
+                if (a.dw) {
+                    __syncwarp();   // the row is stored before the chosen entries
+                    if (chosen) out[id] = from_f32<T>(slope * fmaf(fs[id] - D, inv, (d - mean) * w_inv));
                 }
             }
-            if (a.dw) {
-                __syncwarp();   // the row is stored before the chosen entries
-                if (id >= 0) out[id] = from_f32<T>(slope * fmaf(fs[id] - D, inv, (d - mean) * w_inv));
-            }
+            __syncwarp();   // the row's readers are done before its buffer is filled again
+            live = next_live;
+            id = next_id;
+            d = next_d;
         }
         t0 = t1;
     }
@@ -386,6 +434,15 @@ bool vector_rows(int n, const void* p, long long ld) {
 }
 
 }  // namespace
+
+int qbh::balance_init() {
+    const int most = QBMOE_MAX_EXPERTS * 4 * (1 + 2 * kBalWarps);
+    int rc = cuda_err(cudaFuncSetAttribute(k_router_backward<float, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    if (!rc)
+        rc = cuda_err(cudaFuncSetAttribute(k_router_backward<__nv_bfloat16, 8>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    return rc;
+}
 
 extern "C" size_t qbmoe_balance_workspace_bytes(int T, int n, int S) {
     if (T < 1 || n < 2 || n > QBMOE_MAX_EXPERTS || S < 1 || S > 65535) return 0;
@@ -455,18 +512,18 @@ extern "C" int moe_router_backward(int T, int n, int k, int S, int logit_dtype, 
     a.T = T; a.n = n; a.k = k; a.S = S; a.ld = ld; a.ldg = ldg;
     a.logits = logits; a.idx = idx; a.seq = seq_offsets; a.mask = token_mask;
     a.dw = dw; a.dloss = dloss; a.counts = counts; a.tokens = tokens; a.out = dlogits;
-    a.chunk = chunk_of(T, 4);
+    a.chunk = chunk_of(T, 3);
     const int grid = (T + a.chunk - 1) / a.chunk;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t smem = (size_t)((n + 7) & ~7) * 4;
+    const size_t fbytes = (size_t)((n + 7) & ~7) * 4, rbytes = (size_t)2 * kBalWarps * n * es;   // at most 68 KB
     if (logit_dtype == QBMOE_F32) {
         if (vector_rows<float>(n, logits, ld) && vector_rows<float>(n, dlogits, ldg))
-            k_router_backward<float, 4><<<grid, kBalThreads, smem, s>>>(a);
-        else k_router_backward<float, 1><<<grid, kBalThreads, smem, s>>>(a);
+            k_router_backward<float, 4><<<grid, kBalThreads, fbytes + rbytes, s>>>(a);
+        else k_router_backward<float, 1><<<grid, kBalThreads, fbytes, s>>>(a);
     } else {
         if (vector_rows<__nv_bfloat16>(n, logits, ld) && vector_rows<__nv_bfloat16>(n, dlogits, ldg))
-            k_router_backward<__nv_bfloat16, 8><<<grid, kBalThreads, smem, s>>>(a);
-        else k_router_backward<__nv_bfloat16, 1><<<grid, kBalThreads, smem, s>>>(a);
+            k_router_backward<__nv_bfloat16, 8><<<grid, kBalThreads, fbytes + rbytes, s>>>(a);
+        else k_router_backward<__nv_bfloat16, 1><<<grid, kBalThreads, fbytes, s>>>(a);
     }
     return qbh::cuda_err(cudaGetLastError());
 }

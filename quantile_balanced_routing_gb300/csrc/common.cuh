@@ -116,6 +116,7 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int device_init();
 int route_init_attributes();   // route.cu
 int tc_init_attributes();      // gemm_tc.cu
+int balance_init();            // balance.cu
 
 // Route kernels (route.cu)
 struct RouteBuffers {

@@ -20,12 +20,12 @@
 //                warp that polls instead slows the others: dx 692 us with each
 //                converter warp polling, 1190 us with each suspended.)
 //   warp 1       TMEM owner and MMA issuer (one lane), warp 2 its waiter
-//   warps 3-10   converters in four pairs, one for each slot of the ring: codes
-//                and scales from global memory (a slot's turn ahead, in registers)
-//                to bf16 in the swizzled A tile.  A stage costs a warp about 1300
-//                cycles of latency whether it decodes one block a thread or
-//                four, so the stages in the ring are decoded side by side.
-//   warps 11-18  epilogue, two per lane quarter: TMEM -> registers -> 64 or 128
+//   warps 3-18   converters, four warps for each slot of the ring: codes and scales
+//                from global memory (a slot's turn ahead, in registers) to bf16 in
+//                the swizzled A tile.  Decoding a stage is mostly latency, so the
+//                stages in the ring are decoded side by side (two warps a slot:
+//                dx 537 us where four take 509).
+//   warps 19-26  epilogue, two per lane quarter: TMEM -> registers -> 64 or 128
 //                bytes of a row per store
 // A weight gradient's last stage may reach past its expert's rows, where another
 // expert's gradient may be infinite, and 0 * inf is not 0: whole groups of 16 rows
@@ -44,10 +44,10 @@ constexpr int kABytes = kM * kC * 2, kBBytes = kN * kC * 2;
 constexpr int kBlockBytes = kC * 128;                // 64 columns x 64 steps of an MN-major tile
 constexpr int kBox = 64;                             // heights of the row-tile maps: 64, 128, 192, 256
 constexpr int kStages = 4;
-constexpr int kConvWarp = 3, kConvWarps = 8, kEpiWarp = kConvWarp + kConvWarps, kEpiWarps = 8;
+constexpr int kConvWarp = 3, kConvWarps = 16, kEpiWarp = kConvWarp + kConvWarps, kEpiWarps = 8;
 constexpr int kConvPer = kConvWarps / kStages;       // warps of a slot
 constexpr int kItems = kC * 4 / (32 * kConvPer);     // 32-column blocks a thread decodes
-constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;   // 608
+constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;   // 864
 constexpr int kMmaWarp = 1, kWaitWarp = 2;
 constexpr int kHandoffBar = 1, kEpiBar = 2, kSlotBar = 3;   // kSlotBar + slot
 constexpr long long kDefaultWait = 1LL << 17;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
     volatile int* go_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     int* scratch = reinterpret_cast<int*>(tmem_slot + 4);                     // [kThreads / 32]
     Groups gr;
-    gr.seg = scratch + 20;
+    gr.seg = scratch + 32;
     gr.toff = gr.seg + p.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -273,20 +273,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 if ((issued >> i) & 1u) tc::mbar_wait(&full[i], (last_par >> i) & 1u, kDrainWait);
     } else if (warp >= kConvWarp && warp < kEpiWarp) {
         // ---------------------------------------------------------- converters
-        // Thread (c, b) of a pair: steps c, c + 16, .. of a stage, column block b (32
+        // Thread (c, b) of a slot: steps c and c + 32 of a stage, column block b (32
         // columns, one scale).  A warp reads 64 bytes of each of 8 rows; eight
         // consecutive lanes have eight rows, whose 16-byte chunks the swizzle puts
         // in eight different places.
         const int slot = (warp - kConvWarp) / kConvPer;
         const int ct = threadIdx.x - (kConvWarp + slot * kConvPer) * 32;
-        constexpr int kPair = 32 * kConvPer, kRowsPer = kPair / 4;
+        constexpr int kTeam = 32 * kConvPer, kRowsPer = kTeam / 4;
         const int b = lane >> 3, c = (ct >> 5) * 8 + (lane & 7);
         const int half = p.K / 2, pitch = p.K / 32;
         Cursor<kWeights> cur;
         cur.start(p, gr, n_tiles, it, slot);
         Item v[kItems];
         // the last, partial group of 16 rows of dy: 16 steps x 32 chunks of 8 features
-        constexpr int kTail = 16 * 32 / kPair;
+        constexpr int kTail = 16 * 32 / kTeam;
         uint4 bv[kWeights ? kTail : 1];
         int rem = 0;   // its rows
         auto fetch = [&] {
