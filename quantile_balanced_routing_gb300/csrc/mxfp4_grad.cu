@@ -41,6 +41,7 @@ using namespace qb;
 
 constexpr int kM = 128, kN = 256, kC = 64;           // tile of D, contraction steps per stage
 constexpr int kABytes = kM * kC * 2, kBBytes = kN * kC * 2;
+static_assert(kN == 256, "the last, partial group of dy rows is written as 32 chunks of 8 features");
 constexpr int kBlockBytes = kC * 128;                // 64 columns x 64 steps of an MN-major tile
 constexpr int kBox = 64;                             // heights of the row-tile maps: 64, 128, 192, 256
 constexpr int kStages = 4;
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             const uint32_t idesc = tc::idesc_bf16_m128((x.cols + 15) & ~15) | major;
             for (int c0 = 0; c0 < x.len; c0 += kC) {
                 tc::named_bar_sync(kHandoffBar, 64);
-                if (lane == 0) {
+                if (tc::elect_one()) {
                     tc::tc_fence_after();
                     const uint64_t ad = a0 + (uint64_t)(s * (kABytes >> 4)), bd = b0 + (uint64_t)(s * (kBBytes >> 4));
                     const int left = x.len - c0;
@@ -386,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 __syncwarp();
                 if (++s == kStages) s = 0;
             }
-            if (lane == 0 && !(p.stall && it.t == first)) tc::tc_commit(&accf[ab]);
+            if (tc::elect_one() && !(p.stall && it.t == first)) tc::tc_commit(&accf[ab]);
             __syncwarp();
             ab ^= 1;
         }
-        if (lane == 0) {
+        if (tc::elect_one()) {
             tc::tc_commit(drain);
             tc::mbar_wait(drain, 0, kDefaultWait);
         }

@@ -18,8 +18,9 @@
 //               every warp that polls instead slows the others)
 //   last warp   TMA producer of the rows' codes (one lane that issued both took 570
 //               cycles a stage)
-//   warp 1      TMEM owner, MMA issuer (one lane): 4 x K = 64 MMAs a stage and
-//               one commit that frees it
+//   warp 1      TMEM owner, MMA issuer (one elected lane; a branch on the lane number
+//               makes the issue slower: 567 against 545 us at the prefill case): 4 x
+//               K = 64 MMAs a stage and one commit that frees it
 //   warp 2      the issuer's waiter (an mbarrier wait by the issuing thread
 //               slows its MMA stream): waits, then releases it through a named barrier
 //   warp 3      scale groups to shared memory: by TMA (one lane) where the scale
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
                 const uint64_t ad = a0 + (uint64_t)(s * (kABytes >> 4)), bd = b0 + (uint64_t)(s * (Sh::kBBytes >> 4));
                 const int left = p.K - kb * kStageK;
                 tc::named_bar_sync(kHandoffBar, 64);   // stage s has landed
-                if (lane == 0) {
+                if (tc::elect_one()) {
                     tc::tc_fence_after();
                     mma_mxf4(d, ad, bd, id0, ca, cb, kb != 0);
                     if (left > 192) {
@@ -398,11 +399,11 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
                 __syncwarp();
                 if (++s == S) s = 0;
             }
-            if (lane == 0 && !(p.stall && t == first)) tc::tc_commit(&accf[ab]);
+            if (tc::elect_one() && !(p.stall && t == first)) tc::tc_commit(&accf[ab]);
             __syncwarp();
             ab ^= 1;
         }
-        if (lane == 0) {   // every MMA of this thread is done before TMEM is freed
+        if (tc::elect_one()) {   // every MMA of this thread is done before TMEM is freed
             tc::tc_commit(drain);
             tc::mbar_wait(drain, 0, kDefaultWait);
         }
