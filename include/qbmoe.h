@@ -319,7 +319,9 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  *   (row stride lddy), dx [R, K] bf16 (row stride lddx).
  * moe_mxfp4_wgrad:   dw[e][f][k] = sum over e's rows of dy[r][f] x[r][k],
  *   dw [E, N, K] contiguous, QBMOE_F32 or QBMOE_BF16; zeros for an expert
- *   without rows.
+ *   without rows.  workspace: device, 256-byte aligned, >=
+ *   qbmoe_mxfp4_wgrad_workspace_bytes(R, E, N, K) bytes (0, and NULL allowed,
+ *   unless the matrices are few and small).
  * The gradients are those of the product for the values x and w stand for; a
  * trainer that quantises its own activations and weights passes them straight
  * through the rounding.  Products are exact, sums fp32, each output rounded
@@ -336,9 +338,10 @@ int moe_mxfp4_matmul(int R, int E, int N, int K, int x_type, const void* x, long
 int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* w_codes,
                     const uint8_t* w_scales, const int32_t* offsets, void* dx, long long lddx,
                     qbmoe_stream_t stream);
+size_t qbmoe_mxfp4_wgrad_workspace_bytes(int R, int E, int N, int K);
 int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
                     const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
-                    qbmoe_stream_t stream);
+                    void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
 
 /*
  * ---------------------------------------------------------------------------

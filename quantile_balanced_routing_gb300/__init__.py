@@ -134,7 +134,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qbmoe_mxfp4_workspace_bytes.restype = sz
     lib.moe_mxfp4_matmul.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, ll, vp, sz, vp]
     lib.moe_mxfp4_dgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, vp, ll, vp]
-    lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp]
+    lib.qbmoe_mxfp4_wgrad_workspace_bytes.argtypes = [i, i, i, i]
+    lib.qbmoe_mxfp4_wgrad_workspace_bytes.restype = sz
+    lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp, sz, vp]
     for nm in ("moe_balance_loss", "moe_router_backward", "moe_mxfp4_quantize", "moe_mxfp4_matmul",
                "moe_mxfp4_dgrad", "moe_mxfp4_wgrad"):
         getattr(lib, nm).restype = i

@@ -253,17 +253,28 @@ extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long 
     return qbh::mx_grad(g, reinterpret_cast<cudaStream_t>(stream));
 }
 
+extern "C" size_t qbmoe_mxfp4_wgrad_workspace_bytes(int R, int E, int N, int K) {
+    if (R < 0 || E < 1 || E > QBMOE_MAX_EXPERTS || N < 8 || N % 8 || N > kMaxK || K < 32 || K % 32 || K > kMaxK)
+        return 0;
+    const int splits = qbh::mx_wgrad_splits(R, E, N, K);
+    return splits > 1 ? (size_t)splits * E * N * K * 4 : 0;
+}
+
 extern "C" int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
                                const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
-                               qbmoe_stream_t stream) {
+                               void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
     if (!product_sizes_ok(R, E, N, K, offsets) || !stride_ok(lddy, N)) return QBMOE_EINVAL;
     if (dw_dtype != QBMOE_F32 && dw_dtype != QBMOE_BF16) return QBMOE_EINVAL;
     if (!dw || !qbh::aligned16(dw) || !qbh::aligned16(offsets)) return QBMOE_EINVAL;
     if (R > 0 && !all_aligned16(static_cast<const uint8_t*>(dy), x_codes, x_scales)) return QBMOE_EINVAL;
     const int rc = qbh::device_init();
     if (rc) return rc;
+    const size_t need = qbmoe_mxfp4_wgrad_workspace_bytes(R, E, N, K);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)) return QBMOE_EINVAL;
+    if (workspace_bytes < need) return QBMOE_EWORKSPACE;
     qbh::MxGrad g{};
     g.weights = true;
+    g.parts = need ? workspace : nullptr;
     g.R = R; g.E = E; g.N = N; g.K = K;
     g.dy = dy; g.lddy = lddy;
     g.codes = x_codes; g.scales = x_scales; g.offsets = offsets;

@@ -57,8 +57,10 @@ struct MxGrad {
     void* out;
     long long ldo;
     int out_type;
+    void* parts;   // dw in parts: fp32 [splits, E, N, K], NULL for one part
 };
 int mx_grad(const MxGrad& g, cudaStream_t s);
+int mx_wgrad_splits(int R, int E, int N, int K);
 
 }  // namespace qbh
 

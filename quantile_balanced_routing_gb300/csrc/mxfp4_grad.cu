@@ -20,17 +20,22 @@
 //                warp that polls instead slows the others: dx 692 us with each
 //                converter warp polling, 1190 us with each suspended.)
 //   warp 1       TMEM owner and MMA issuer (one lane), warp 2 its waiter
-//   warps 3-18   converters, four warps for each slot of the ring: codes and scales
-//                from global memory (a slot's turn ahead, in registers) to bf16 in
-//                the swizzled A tile.  Decoding a stage is mostly latency, so the
-//                stages in the ring are decoded side by side (two warps a slot:
-//                dx 537 us where four take 509).
-//   warps 19-26  epilogue, two per lane quarter: TMEM -> registers -> 64 or 128
-//                bytes of a row per store
+//   warps 3+     converters, two or four warps for each slot of the ring: codes and
+//                scales from global memory (a slot's turn ahead, in registers) to
+//                bf16 in the swizzled A tile.  Decoding a stage is mostly latency, so
+//                the stages in the ring are decoded side by side.
+//   the rest     epilogue, one or two per lane quarter: TMEM -> registers -> 64 or
+//                128 bytes of a row per store
 // A weight gradient's last stage may reach past its expert's rows, where another
 // expert's gradient may be infinite, and 0 * inf is not 0: whole groups of 16 rows
 // come by TMA, the converters write the last group with zeros past the end, and
 // groups beyond it are not multiplied.
+// The tensor cores' fp32 accumulation drops low bits: its error grows with the
+// number of steps (6.8e-6 of dw's norm over 40000 rows, where fp32 additions lose
+// 1e-7).  An fp32 weight gradient therefore takes its rows kSegRows at a time:
+// the epilogue adds each later segment to what it stored for the ones before.
+// Where there are fewer tiles than SMs, an expert's rows are also cut into
+// parts for different CTAs, summed in order by a second kernel.
 #include "mxfp4.cuh"
 #include "mxfp4_decode.cuh"
 #include "tc_ptx.cuh"
@@ -44,11 +49,21 @@ constexpr int kABytes = kM * kC * 2, kBBytes = kN * kC * 2;
 static_assert(kN == 256, "the last, partial group of dy rows is written as 32 chunks of 8 features");
 constexpr int kBlockBytes = kC * 128;                // 64 columns x 64 steps of an MN-major tile
 constexpr int kBox = 64;                             // heights of the row-tile maps: 64, 128, 192, 256
+constexpr long long kSms = 152;
+constexpr int kSegRows = 4096;                       // rows accumulated on the tensor cores alone (fp32 dw)
 constexpr int kStages = 4;
-constexpr int kConvWarp = 3, kConvWarps = 16, kEpiWarp = kConvWarp + kConvWarps, kEpiWarps = 8;
-constexpr int kConvPer = kConvWarps / kStages;       // warps of a slot
-constexpr int kItems = kC * 4 / (32 * kConvPer);     // 32-column blocks a thread decodes
-constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;   // 864
+constexpr int kConvWarp = 3;
+// Warps by direction.  dx: 16 converters decode a slot in half the latency of 8
+// (509 against 537 us).  dw needs more registers a converter (the tail of dy), and spills
+// at 72: 8 converters and 4 epilogue warps, 725 us, against 949 with 16 and 8.
+template <bool kWeights>
+struct Warps {
+    static constexpr int kConv = kWeights ? 8 : 16, kEpi = kWeights ? 4 : 8;
+    static constexpr int kEpiFirst = kConvWarp + kConv;
+    static constexpr int kConvPer = kConv / kStages;           // warps of a slot
+    static constexpr int kItems = kC * 4 / (32 * kConvPer);    // 32-column blocks a thread decodes
+    static constexpr int kThreads = (kEpiFirst + kEpi) * 32;
+};
 constexpr int kMmaWarp = 1, kWaitWarp = 2;
 constexpr int kHandoffBar = 1, kEpiBar = 2, kSlotBar = 3;   // kSlotBar + slot
 constexpr long long kDefaultWait = 1LL << 17;
@@ -65,7 +80,9 @@ struct Params {
     long long ldo;
     int R, E, N, K;
     int k_tiles, f_tiles, f_per; // 128-column tiles of K; weights: tiles of N and features in each
-    int step_e, step_f, step_k;  // weights: the grid size in those units
+    int splits;                  // weights: parts of each expert's rows, out [splits, E, N, K]
+    int seg_rows;                // weights: rows per accumulation
+    int step_e, step_s, step_f, step_k;   // weights: the grid size in experts, parts and tiles
     int* status;
     long long wait_limit;
     int stall;
@@ -79,50 +96,77 @@ constexpr int smem_bytes(int E) {
 // (rows of dx, features of dw), and its contraction: `len` steps from Q row `q0`.
 struct Tile {
     int e, row0, cols, kt, len;
-    long long q0;
-    int b0;          // weights: first row of dy
+    long long q0;    // (weights: b0)
+    int b0;          // weights: first row of dy and of Q
+    bool first;      // nothing is stored for this tile yet
 };
 template <bool kWeights>
 struct Tiles {
     Walker<kN> w;      // rows
-    int e, ft, kt;     // weights: expert, feature tile, column tile (fastest)
+    int e, part, ft, kt;   // weights: expert, part of its rows, feature tile, column tile (fastest)
+    int r0, r1;            // weights: rows of the part that are still to do
+    bool first;
     int t;
     QB_DEV int count(const Params& p, const Groups& gr) const {
-        return kWeights ? p.E * p.f_tiles * p.k_tiles : gr.toff[p.E] * p.k_tiles;
+        return kWeights ? p.E * p.splits * p.f_tiles * p.k_tiles : gr.toff[p.E] * p.k_tiles;
+    }
+    QB_DEV void range(const Params& p, const Groups& gr) {
+        if (e >= p.E) return;   // past the last tile
+        const int a = gr.seg[e], len = max(gr.seg[e + 1] - a, 0);
+        r0 = a;
+        r1 = a + len;
+        if (p.splits > 1) {
+            const long long per = (len / p.splits + kC) / kC * kC;
+            r0 = a + (int)min((long long)len, part * per);
+            r1 = a + (int)min((long long)len, (part + 1) * per);
+        }
+        first = true;
     }
     QB_DEV void start(const Params& p, const Groups& gr) {
         t = blockIdx.x;
         if (kWeights) {
-            const int row = t / p.k_tiles;
-            kt = t - row * p.k_tiles;
-            e = row / p.f_tiles;
-            ft = row - e * p.f_tiles;
+            int rest = t / p.k_tiles;
+            kt = t - rest * p.k_tiles;
+            ft = rest % p.f_tiles;
+            rest /= p.f_tiles;
+            part = rest % p.splits;
+            e = rest / p.splits;
+            range(p, gr);
         } else {
             w.start(gr, p.E, p.k_tiles);
         }
     }
     QB_DEV void next(const Params& p, const Groups& gr) {
-        t += gridDim.x;
-        if (kWeights) {   // the grid's stride in (e, ft, kt), with carries
+        if (kWeights) {
+            if (r1 - r0 > p.seg_rows) {   // the same tile's next rows
+                r0 += p.seg_rows;
+                first = false;
+                return;
+            }
+            t += gridDim.x;   // the grid's stride in (e, part, ft, kt), with carries
             kt += p.step_k;
             ft += p.step_f;
+            part += p.step_s;
             e += p.step_e;
             if (kt >= p.k_tiles) kt -= p.k_tiles, ++ft;
-            if (ft >= p.f_tiles) ft -= p.f_tiles, ++e;
+            if (ft >= p.f_tiles) ft -= p.f_tiles, ++part;
+            if (part >= p.splits) part -= p.splits, ++e;
+            range(p, gr);
         } else {
+            t += gridDim.x;
             w.next(gr, p.E, p.k_tiles);
         }
     }
     QB_DEV Tile get(const Params& p, const Groups& gr) const {
         Tile x;
         if (kWeights) {
-            x.e = e;
+            x.e = part * p.E + e;   // of the output
             x.kt = kt;
             x.row0 = ft * p.f_per;
             x.cols = min(p.f_per, p.N - x.row0);
-            x.b0 = gr.seg[e];
-            x.len = max(gr.seg[e + 1] - x.b0, 0);
-            x.q0 = x.b0;
+            x.b0 = r0;
+            x.len = min(r1 - r0, p.seg_rows);
+            x.first = first;
         } else {
             x.e = w.g;
             x.kt = w.m;
@@ -131,6 +175,7 @@ struct Tiles {
             x.len = p.N;
             x.q0 = (long long)w.g * p.N;
             x.b0 = 0;
+            x.first = true;
         }
         return x;
     }
@@ -173,6 +218,11 @@ __device__ __forceinline__ int mn_offset(int c, int chunk) {
     return (chunk >> 3) * kBlockBytes + c * 128 + (((chunk & 7) ^ (c & 7)) << 4);
 }
 
+// (32-bit shared addresses: the converters are short of registers.)
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 32 columns of one step: codes and their scale byte; zeros where there is nothing.
 struct Item {
     uint4 q;
@@ -180,7 +230,10 @@ struct Item {
 };
 
 template <bool kWeights, typename Out>
-__global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const __grid_constant__ Params p) {
+    constexpr int kConvPer = Warps<kWeights>::kConvPer, kItems = Warps<kWeights>::kItems;
+    constexpr int kEpiWarp = Warps<kWeights>::kEpiFirst, kEpiWarps = Warps<kWeights>::kEpi;
+    constexpr int kThreads = Warps<kWeights>::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* a_ring = smem;
@@ -274,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 if ((issued >> i) & 1u) tc::mbar_wait(&full[i], (last_par >> i) & 1u, kDrainWait);
     } else if (warp >= kConvWarp && warp < kEpiWarp) {
         // ---------------------------------------------------------- converters
-        // Thread (c, b) of a slot: steps c and c + 32 of a stage, column block b (32
+        // Thread (c, b) of a slot: steps c, c + 8 warps, .. of a stage, column block b (32
         // columns, one scale).  A warp reads 64 bytes of each of 8 rows; eight
         // consecutive lanes have eight rows, whose 16-byte chunks the swizzle puts
         // in eight different places.
@@ -294,8 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             if (!cur.live) return;
             const int k = cur.x.kt * kM + 32 * b;
             const int left = k < p.K ? cur.x.len - cur.c - c : 0;   // steps from this thread's first to the end
-            const uint8_t* codes = p.codes + (cur.x.q0 + cur.c + c) * half + k / 2;
-            const uint8_t* scales = p.scales + (cur.x.q0 + cur.c + c) * pitch + k / 32;
+            const long long from = (kWeights ? (long long)cur.x.b0 : cur.x.q0) + cur.c + c;
+            const uint8_t* codes = p.codes + from * half + k / 2;
+            const uint8_t* scales = p.scales + from * pitch + k / 32;
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
                 v[i].q = make_uint4(0, 0, 0, 0);
@@ -321,11 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
             }
         };
         fetch();
-        uint8_t* B = b_ring + slot * kBBytes;
-        uint4* dst[4];   // of the thread's first step; the swizzle repeats every 8 steps
+        const uint32_t B = tc::smem_u32(b_ring + slot * kBBytes);
+        uint32_t dst[4];   // of the thread's first step; the swizzle repeats every 8 steps
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            dst[j] = reinterpret_cast<uint4*>(a_ring + slot * kABytes + mn_offset(c, 4 * b + j));
+        for (int j = 0; j < 4; ++j) dst[j] = tc::smem_u32(a_ring + slot * kABytes + mn_offset(c, 4 * b + j));
         while (cur.live) {
             tc::named_bar_sync(kSlotBar + slot, 32 + 32 * kConvPer);   // the slot is free
             if constexpr (kWeights) {
@@ -333,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                     const int h0 = (cur.x.len - cur.c) & ~15;
 #pragma unroll
                     for (int i = 0; i < kTail; ++i)
-                        *reinterpret_cast<uint4*>(B + mn_offset(h0 + (ct >> 5) + kConvPer * i, ct & 31)) = bv[i];
+                        st_shared16(B + mn_offset(h0 + (ct >> 5) + kConvPer * i, ct & 31), bv[i]);
                 }
             }
 #pragma unroll
@@ -344,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 for (int j = 0; j < 4; ++j) {
                     uint32_t o[4];
                     mx_decode_scaled(q[j], scale, o);
-                    dst[j][i * (kRowsPer * 128 / 16)] = make_uint4(o[0], o[1], o[2], o[3]);
+                    st_shared16(dst[j] + i * (kRowsPer * 128), make_uint4(o[0], o[1], o[2], o[3]));
                 }
             }
             tc::fence_proxy_async_smem();   // generic-proxy writes -> tcgen05.mma reads
@@ -461,6 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
                 const int left = cols - c0;
                 if constexpr (sizeof(Out) == 4) {
                     o += lane;
+                    if (!x.first) {     // this thread stored the sum so far
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < left) v[i] += o[(uint32_t)i * ldo];
+                    }
                     if (left >= 16) {   // no test a row
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[(uint32_t)i * ldo] = v[i];
@@ -498,12 +556,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_grad(const __grid_constant__
 template <bool kWeights, typename Out>
 int launch(Params& p, long long tiles, cudaStream_t s) {
     const int grid = (int)min(tiles, (long long)qbh::sm_count());
+    int rest = grid / p.k_tiles;
     p.step_k = grid % p.k_tiles;
-    p.step_f = grid / p.k_tiles % p.f_tiles;
-    p.step_e = grid / p.k_tiles / p.f_tiles;
-    k_mx_grad<kWeights, Out><<<grid, kThreads, smem_bytes(p.E), s>>>(p);
+    p.step_f = rest % p.f_tiles;
+    rest /= p.f_tiles;
+    p.step_s = rest % p.splits;
+    p.step_e = rest / p.splits;
+    k_mx_grad<kWeights, Out><<<grid, Warps<kWeights>::kThreads, smem_bytes(p.E), s>>>(p);
     return qbh::cuda_err(cudaGetLastError());
 }
+// out = sum over the parts, in order; four values a thread.
+template <typename Out>
+__global__ void __launch_bounds__(256) k_sum_parts(const float4* __restrict__ parts, int splits, long long quads,
+                                                   Out* __restrict__ out) {
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < quads; i += (long long)gridDim.x * 256) {
+        float4 s = __ldg(parts + i);
+        for (int j = 1; j < splits; ++j) {
+            const float4 v = __ldg(parts + j * quads + i);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        if constexpr (sizeof(Out) == 4) {
+            reinterpret_cast<float4*>(out)[i] = s;
+        } else {
+            const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
+            reinterpret_cast<uint2*>(out)[i] = *reinterpret_cast<const uint2*>(h);
+        }
+    }
+}
+
 template <bool kWeights, typename Out>
 int set_attributes() {
     return qbh::cuda_err(cudaFuncSetAttribute(k_mx_grad<kWeights, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -519,6 +599,15 @@ int mx_grad_init() {
     if (!rc) rc = set_attributes<true, float>();
     if (!rc) rc = set_attributes<true, __nv_bfloat16>();
     return rc;
+}
+
+// Parts of each expert's rows: as many as there are SMs (152, whatever the device
+// says: the order of the sums is part of the result) for each tile, with at
+// least four stages of rows an expert on average in each.  (40000 rows, 264 x 544: 10
+// tiles, 273 us in one part, %PARTS% us in 15.)
+int mx_wgrad_splits(int R, int E, int N, int K) {
+    const long long tiles = (long long)E * ((N + kN - 1) / kN) * ((K + kM - 1) / kM);
+    return (int)max(1LL, min(kSms / tiles, (long long)R / E / (4 * kC)));
 }
 
 int mx_grad(const MxGrad& q, cudaStream_t s) {
@@ -538,6 +627,9 @@ int mx_grad(const MxGrad& q, cudaStream_t s) {
     p.k_tiles = (q.K + kM - 1) / kM;
     p.f_tiles = (q.N + kN - 1) / kN;
     p.f_per = ((q.N + p.f_tiles - 1) / p.f_tiles + 15) & ~15;
+    p.splits = q.weights ? mx_wgrad_splits(q.R, q.E, q.N, q.K) : 1;
+    // bf16 sums need no more than the tensor cores keep
+    p.seg_rows = q.out_type == QBMOE_F32 || p.splits > 1 ? kSegRows : 0x7fffffff;
     p.status = mx_status();
     p.wait_limit = mx_wait_limit();
     p.stall = mx_stall();
@@ -545,7 +637,20 @@ int mx_grad(const MxGrad& q, cudaStream_t s) {
         const long long tiles = ((long long)(q.R / kN) + min(q.E, q.R)) * p.k_tiles;
         return launch<false, __nv_bfloat16>(p, tiles, s);
     }
-    const long long tiles = (long long)q.E * p.f_tiles * p.k_tiles;
+    const long long tiles = (long long)q.E * p.splits * p.f_tiles * p.k_tiles;
+    if (p.splits > 1) {
+        p.out = q.parts;
+        const int rc = launch<true, float>(p, tiles, s);
+        if (rc) return rc;
+        const long long quads = (long long)q.E * q.N * q.K / 4;
+        const int grid = (int)min((quads + 255) / 256, 8LL * sm_count());
+        const float4* parts = static_cast<const float4*>(q.parts);
+        if (q.out_type == QBMOE_F32)
+            k_sum_parts<float><<<grid, 256, 0, s>>>(parts, p.splits, quads, static_cast<float*>(q.out));
+        else
+            k_sum_parts<__nv_bfloat16><<<grid, 256, 0, s>>>(parts, p.splits, quads, static_cast<__nv_bfloat16*>(q.out));
+        return cuda_err(cudaGetLastError());
+    }
     return q.out_type == QBMOE_F32 ? launch<true, float>(p, tiles, s) : launch<true, __nv_bfloat16>(p, tiles, s);
 }
 

@@ -180,8 +180,10 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
     if need_dw:
         dw = torch.empty((N, K) if offsets is None else (E, N, K), dtype=torch.float32 if f32 else torch.bfloat16,
                          device=dev)
+        nbytes = lib.qbmoe_mxfp4_wgrad_workspace_bytes(R, E, N, K)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         rc = lib.moe_mxfp4_wgrad(R, E, N, K, dy.data_ptr(), ld, xq.codes.data_ptr(), xq.scales.data_ptr(),
-                                 _p(offsets), QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), cur)
+                                 _p(offsets), QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), _p(ws), nbytes, cur)
         if rc:
             raise QbmoeError(rc, "moe_mxfp4_wgrad")
     return dx, dw

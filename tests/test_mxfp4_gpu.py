@@ -183,6 +183,33 @@ def test_product_gradients(R, E, N, K, skew, dw_dtype):
     assert Q.qbmoe_status(None, None) == 0
 
 
+@pytest.mark.parametrize("R,E,N,K", [(20000, 1, 136, 96), (30011, 3, 64, 160), (9000, 1, 2048, 2560), (13000, 2, 1032, 2304)])
+def test_weight_gradient_over_many_rows(R, E, N, K):
+    """Long sums, in parts (few tiles) and in segments (many): an fp32 gradient keeps the accuracy of fp32 additions.
+    A sum of R products with random signs is within about sqrt(R) 2^-24 of its size when each addition rounds;
+    the tensor cores' own accumulation over R rows would be off by R 2^-32 or so, ten times that at these sizes."""
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(R)
+    xq = M.quantize(rows(r, R, K).numpy())
+    offsets = np.concatenate([[0], np.sort(r.randint(0, R, E - 1)), [R]]).astype(np.int32)
+    dy = torch.from_numpy(r.standard_normal((R, N)).astype(np.float32)).bfloat16()
+    w = Q.Mxfp4(torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda"),
+                torch.zeros(E, N, K // 32, dtype=torch.uint8, device="cuda"))
+    x = Q.Mxfp4(torch.from_numpy(xq[0]).cuda(), torch.from_numpy(xq[1]).cuda())
+    off = torch.from_numpy(offsets).cuda()
+    _, dw = Q.mxfp4_matmul_backward(dy.cuda(), x, w, off, need_dx=False)
+    assert Q.qbmoe_status(None, None) == 0
+    some = np.unique(np.concatenate([np.arange(0, N, 37), [N - 1]]))
+    for e, (a, b) in enumerate(M.groups(offsets, R)):
+        want = dy[a:b].double().numpy()[:, some].T @ xq[2][a:b]
+        got = dw[e, some].double().cpu().numpy()
+        assert np.linalg.norm(got - want) < 1e-6 * np.linalg.norm(want)
+    _, again = Q.mxfp4_matmul_backward(dy.cuda(), x, w, off, need_dx=False)
+    assert torch.equal(dw, again)
+    _, half = Q.mxfp4_matmul_backward(dy.cuda(), x, w, off, need_dx=False, dw_dtype=torch.bfloat16)
+    assert float((half.float() - dw).norm() / dw.norm()) < 2.0 ** -8
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_product_quantises_its_rows(dtype):
     import quantile_balanced_routing_gb300 as Q

@@ -70,8 +70,8 @@ def test_quantize_refuses(lib, at, value):
 MATMUL = [4, 2, 16, 64, 2, FAKE, 64, FAKE, FAKE, FAKE, FAKE, FAKE, 16, FAKE, BIG, None]
 # R, E, N, K, dy, lddy, w_codes, w_scales, offsets, dx, lddx, stream
 DGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, FAKE, 64, None]
-# R, E, N, K, dy, lddy, x_codes, x_scales, offsets, dw_dtype, dw, stream
-WGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, 0, FAKE, None]
+# R, E, N, K, dy, lddy, x_codes, x_scales, offsets, dw_dtype, dw, workspace, bytes, stream
+WGRAD = [4, 2, 16, 64, FAKE, 16, FAKE, FAKE, FAKE, 0, FAKE, None, 0, None]
 SIZES = [(0, -1), (1, 0), (1, 1025), (2, 0), (2, 12), (3, 0), (3, 48), (3, 1 << 25)]
 
 
@@ -108,6 +108,18 @@ def test_workspace_too_small(lib):
     need = lib.qbmoe_mxfp4_workspace_bytes(4, 64)
     assert need > 4 * 34 and lib.qbmoe_mxfp4_workspace_bytes(4, 48) == 0
     assert lib.moe_mxfp4_matmul(*changed(changed(MATMUL, 4, 1), 14, need - 1)) == Q.QBMOE_EWORKSPACE
+
+
+def test_weight_gradient_workspace(lib):
+    # many tiles, or few rows: none; one small matrix over many rows: its parts
+    assert lib.qbmoe_mxfp4_wgrad_workspace_bytes(65536, 224, 1024, 3584) == 0
+    assert lib.qbmoe_mxfp4_wgrad_workspace_bytes(300, 1, 264, 544) == 0
+    need = lib.qbmoe_mxfp4_wgrad_workspace_bytes(40000, 1, 264, 544)
+    assert need > 264 * 544 * 4 and need % (264 * 544 * 4) == 0
+    big = [40000, 1, 264, 544, FAKE, 264, FAKE, FAKE, FAKE, 0, FAKE, FAKE, need, None]
+    for at, value, code in ((11, None, Q.QBMOE_EINVAL), (11, FAKE + 8, Q.QBMOE_EINVAL), (12, need - 1, Q.QBMOE_EWORKSPACE)):
+        rc = lib.moe_mxfp4_wgrad(*changed(big, at, value))
+        assert rc in (code, Q.QBMOE_ECUDA, Q.QBMOE_EARCH)    # without a GPU the device is asked first
 
 
 def refuses(fn, *args, **kw):
