@@ -326,7 +326,7 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  * trainer that quantises its own activations and weights passes them straight
  * through the rounding.  Products are exact, sums fp32, each output rounded
  * once.  All pointers 16-byte aligned, strides multiples of 8 elements and at
- * most 2^27, N and K at most 2^24.
+ * most 2^27, N and K at most 2^24, E N below 2^31.
  * A bounded wait that expires is reported by qbmoe_status(NULL, stream).
  */
 int moe_mxfp4_quantize(long long rows, int K, int x_type, const void* x, long long ldx, uint8_t* codes,

@@ -163,7 +163,7 @@ constexpr long long kMaxStride = 1LL << 27;
 
 bool product_sizes_ok(int R, int E, int N, int K, const int32_t* offsets) {
     return R >= 0 && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && N <= kMaxK && K >= 32 &&
-           K % 32 == 0 && K <= kMaxK && (offsets || E == 1);
+           K % 32 == 0 && K <= kMaxK && (long long)E * N <= 0x7fffffffLL && (offsets || E == 1);
 }
 bool stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= kMaxStride; }
 template <typename... P>

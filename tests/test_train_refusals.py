@@ -82,6 +82,11 @@ def test_matmul_refuses(lib, at, value):
     assert lib.moe_mxfp4_matmul(*changed(MATMUL, at, value)) == Q.QBMOE_EINVAL
 
 
+def test_products_refuse_too_many_weight_rows(lib):
+    E, N = 1024, 1 << 22
+    assert lib.moe_mxfp4_matmul(*(MATMUL[:1] + [E, N] + MATMUL[3:12] + [N] + MATMUL[13:])) == Q.QBMOE_EINVAL
+
+
 @pytest.mark.parametrize("x_type,ldx", [(0, 63), (0, 66), (1, 63), (1, 68), (0, 32)])
 def test_matmul_refuses_rows_it_cannot_quantise(lib, x_type, ldx):
     assert lib.moe_mxfp4_matmul(*changed(changed(MATMUL, 4, x_type), 6, ldx)) == Q.QBMOE_EINVAL
