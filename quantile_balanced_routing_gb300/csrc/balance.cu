@@ -23,7 +23,7 @@ constexpr float kLogitLimit = 80.0f;
 QB_DEV float score(float x, float& e) {
     float lo;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(x), "f"(-kLogitLimit));
-    e = __expf(-lo);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(lo * -1.4426950408889634f));   // no subnormal between the limits
     float s;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
     return s;

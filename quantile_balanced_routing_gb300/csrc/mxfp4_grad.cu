@@ -604,7 +604,7 @@ int mx_grad_init() {
 // Parts of each expert's rows: as many as there are SMs (152, whatever the device
 // says: the order of the sums is part of the result) for each tile, with at
 // least four stages of rows an expert on average in each.  (40000 rows, 264 x 544: 10
-// tiles, 273 us in one part, %PARTS% us in 15.)
+// tiles, 270 us in one part, 31 us in 15.)
 int mx_wgrad_splits(int R, int E, int N, int K) {
     const long long tiles = (long long)E * ((N + kN - 1) / kN) * ((K + kM - 1) / kM);
     return (int)max(1LL, min(kSms / tiles, (long long)R / E / (4 * kC)));
