@@ -6,37 +6,39 @@ and scales are the layout :class:`LatentMoE` takes for MXFP4 experts.
 """
 from __future__ import annotations
 
-from typing import NamedTuple
-
 from . import MAX_EXPERTS, QBMOE_BF16, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _here, _p, _refuse, load_library
 
 BLOCK = 32
 
 
-class Mxfp4(NamedTuple):
-    """An MXFP4 tensor [..., K]: two E2M1 codes a byte (element 2i in the low
-    nibble) and one E8M0 scale byte per 32 elements."""
-    codes: "torch.Tensor"    # uint8 [..., K / 2]
-    scales: "torch.Tensor"   # uint8 [..., K / 32]
+class Mxfp4:
+    """An MXFP4 tensor [..., K]: ``codes`` uint8 [..., K / 2], two E2M1 codes a
+    byte (element 2i in the low nibble), and ``scales`` uint8 [..., K / 32], one
+    E8M0 byte per 32 elements.  Checked when it is made, so that the calls that
+    take it need not."""
+    __slots__ = ("codes", "scales", "shape")
 
-    @property
-    def shape(self):
-        return tuple(self.codes.shape[:-1]) + (2 * self.codes.shape[-1],)
+    def __init__(self, codes, scales):
+        import torch
+        if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or not codes.is_contiguous() or \
+                not scales.is_contiguous():
+            _refuse("Mxfp4", "codes and scales are contiguous uint8")
+        if codes.dim() < 1 or scales.dim() < 1:
+            _refuse("Mxfp4", "codes [..., K/2] and scales [..., K/32]")
+        (*lead, half), (*lead_s, blocks) = codes.shape, scales.shape
+        if half == 0 or blocks * (BLOCK // 2) != half or lead != lead_s:
+            _refuse("Mxfp4", f"codes [..., K/2] and scales [..., K/32], K a multiple of {BLOCK}")
+        self.codes, self.scales, self.shape = codes, scales, (*lead, 2 * half)
+
+    def __iter__(self):
+        return iter((self.codes, self.scales))
 
 
-def _mxfp4_shape(what, name, t):
-    """Shape (..., K) of a well-formed Mxfp4."""
-    import torch
-    if not isinstance(t, Mxfp4):
-        _refuse(what, f"{name} is an Mxfp4 (codes, scales)")
-    c, s = t
-    if c.dtype is not torch.uint8 or s.dtype is not torch.uint8 or not c.is_contiguous() or not s.is_contiguous():
-        _refuse(what, f"{name}'s codes and scales are contiguous uint8")
-    (*lead, half), (*lead_s, blocks) = c.shape, s.shape
-    if half == 0 or blocks * (BLOCK // 2) != half or lead != lead_s:
-        _refuse(what, f"{name} is codes [..., K/2] and scales [..., K/32], K a multiple of {BLOCK}")
-    lead.append(2 * half)
-    return lead
+def _made(codes, scales, shape):
+    """An Mxfp4 of tensors known to be right."""
+    q = object.__new__(Mxfp4)
+    q.codes, q.scales, q.shape = codes, scales, shape
+    return q
 
 
 def _row_stride(what, name, t, align):
@@ -83,13 +85,16 @@ def mxfp4_quantize(x, values=False, stream=None):
                                            codes.data_ptr(), scales.data_ptr(), _p(v), cur)
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_quantize")
-    return (Mxfp4(codes, scales), v) if values else Mxfp4(codes, scales)
+    q = _made(codes, scales, (*lead, K))
+    return (q, v) if values else q
 
 
 def _groups(what, w, offsets):
     """Checked (E, N, K) of weights [N, K], or [E, N, K] with offsets."""
     import torch
-    shape = _mxfp4_shape(what, "w", w)
+    if not isinstance(w, Mxfp4):
+        _refuse(what, "w is an Mxfp4")
+    shape = w.shape
     if len(shape) == 3 and offsets is not None:
         E, N, K = shape
     elif len(shape) == 2 and offsets is None:
@@ -119,7 +124,7 @@ def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
     what = "mxfp4_matmul"
     E, N, K = _groups(what, w, offsets)
     if isinstance(x, Mxfp4):
-        shape = _mxfp4_shape(what, "x", x)
+        shape = x.shape
         rows, kind, scales, ld = x.codes, QBMOE_MXFP4, x.scales, K
     else:
         shape, rows, scales = x.shape, x, None
@@ -159,7 +164,7 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
             return mxfp4_matmul_backward(dy, xq, w, offsets, need_dx, need_dw, dw_dtype)
     what = "mxfp4_matmul_backward"
     E, N, K = _groups(what, w, offsets)
-    shape = _mxfp4_shape(what, "xq", xq)
+    shape = xq.shape if isinstance(xq, Mxfp4) else ()
     if len(shape) != 2 or shape[1] != K:
         _refuse(what, "xq is [R, K] with the K of w")
     R = shape[0]

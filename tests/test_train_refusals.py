@@ -156,14 +156,20 @@ def test_python_refuses_wrong_tensors():
     off = torch.zeros(4, dtype=torch.int32)
     assert "current CUDA device" in refuses(Q.mxfp4_matmul, xq, w)
     refuses(Q.mxfp4_matmul, xq, (u8(16, 32), u8(16, 2)))
-    refuses(Q.mxfp4_matmul, xq, Q.Mxfp4(u8(16, 48), u8(16, 3)))
+    refuses(Q.mxfp4_matmul, xq, Q.Mxfp4(u8(16, 48), u8(16, 3)))      # another K
     refuses(Q.mxfp4_matmul, xq, Q.Mxfp4(u8(12, 32), u8(12, 2)))
+    refuses(Q.mxfp4_matmul, torch.zeros(4, 64).half(), w)
     refuses(Q.mxfp4_matmul, xq, wg)
     refuses(Q.mxfp4_matmul, xq, wg, off[:3])
     refuses(Q.mxfp4_matmul, xq, wg, off.long())
-    refuses(Q.mxfp4_matmul, Q.Mxfp4(u8(4, 32), u8(4, 3)), w)
+    refuses(Q.Mxfp4, u8(4, 32), u8(4, 3))
+    refuses(Q.Mxfp4, u8(4, 32), u8(5, 2))
+    refuses(Q.Mxfp4, u8(4, 24), u8(4, 1))
+    refuses(Q.Mxfp4, u8(4, 32).int(), u8(4, 2))
+    refuses(Q.Mxfp4, u8(32, 4).t(), u8(4, 2))
     dy = torch.zeros(4, 16, dtype=torch.bfloat16)
     refuses(Q.mxfp4_matmul_backward, dy.float(), xq, w)
     refuses(Q.mxfp4_matmul_backward, dy[:3], xq, w)
     refuses(Q.mxfp4_matmul_backward, dy, xq, w, dw_dtype=torch.float16)
+    refuses(Q.mxfp4_matmul_backward, dy, (xq.codes, xq.scales), w)
     refuses(Q.mxfp4_matmul_backward, dy, xq, wg)
