@@ -36,6 +36,10 @@
 // the epilogue adds each later segment to what it stored for the ones before.
 // Where there are fewer tiles than SMs, an expert's rows are also cut into
 // parts for different CTAs, summed in order by a second kernel.
+//
+// Measured (65536 rows over 224 experts, 1024 x 3584): dx 515 us, 780 cycles a stage
+// of which the MMAs are 330: decoding (1600 instructions a stage) and hand-offs bound
+// it; dw in fp32 720 us, 3.3 GB of stores, which alone take 500.
 #include "mxfp4.cuh"
 #include "mxfp4_decode.cuh"
 #include "tc_ptx.cuh"
