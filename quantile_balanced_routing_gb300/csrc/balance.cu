@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 // has its next row on the way to shared memory (cp.async) while it works on this
 // one, where rows are 16-byte vectors.  The dense row is stored first, then the k
 // chosen entries over it.  16384 x 896 fp32: 22 us (118 MB: 17 us at the copy rate),
-// bound by issue (62%) as much as by memory; keeping f and the slopes' factors
-// in registers instead took 83 us (one CTA a SM).
+// bound by issue (62%) as much as by memory; keeping more than the slopes in
+// registers (fewer CTAs a SM, the chosen entries selected in the dense pass) took 83.
 // ---------------------------------------------------------------------------
 struct RouterGradArgs {
     int T, n, k, S, chunk;

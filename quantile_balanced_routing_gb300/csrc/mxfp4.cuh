@@ -23,7 +23,8 @@ void mx_set_stall(int on);
 
 int sm_count();
 // 2-D row-major tensor map: cols elements a row (row stride ld bytes), box
-// {box_cols, box_rows}, 128-byte swizzle unless `plain`, zeros outside.
+// {box_cols, box_rows}, zeros outside; swizzled over the box's 128 bytes, or 64 of
+// codes, unless `plain`.
 bool encode_rows(CUtensorMap* m, CUtensorMapDataType type, const void* base, long long rows, long long cols,
                  long long ld_bytes, int box_cols, int box_rows, bool plain = false);
 

@@ -48,24 +48,40 @@ __device__ __forceinline__ void mx_decode_word(uint32_t w, const uint32_t (&h)[2
     for (int q = 0; q < 4; ++q) o[q] |= __byte_perm(w, w4, (q << 12) | ((4 + q) << 4)) & 0x80008000u;
 }
 
-// The E8M0 scale as a pair of bf16 (byte 0 is the subnormal 2^-127, 0xFF NaN).
-QB_DEV __nv_bfloat162 e8m0_bf16x2(uint32_t sc) {
-    const uint32_t b = sc == 0u ? 0x0040u : sc == 255u ? 0x7fffu : sc << 7;
+// An E2M1 code's magnitude in bits 6..8 of a bf16 (two exponent bits and one of the
+// mantissa) and its sign in bit 15 are the code's value times 2^-126, subnormals
+// included: one exact product with 2^126 times the scale decodes it.  The factor as
+// a pair of bf16; scales from 2^2 on, whose factor has no bf16, take 2^126 first
+// (mx_rescale).
+constexpr uint32_t kMxLargeScale = 129;   // 2^2
+QB_DEV __nv_bfloat162 mx_factor(uint32_t sc) {
+    const uint32_t b = (sc < kMxLargeScale ? sc + 126u : 253u) << 7;
     const uint32_t bb = b * 0x10001u;
     return *reinterpret_cast<const __nv_bfloat162*>(&bb);
 }
+QB_DEV uint32_t mx_mul2(uint32_t v, __nv_bfloat162 f) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), f);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-// Eight E2M1 codes of one word -> four bf16 pairs times the scale: the same
-// lookups as mx_decode_word at scale 1, then one exact multiplication a pair
-// (an overflow gives infinity, as rounding the value would).
-QB_DEV void mx_decode_scaled(uint32_t w, __nv_bfloat162 scale, uint32_t (&o)[4]) {
-    const uint32_t h[2] = {0x3f3f3f00u, 0x40404040u}, l[2] = {0xc0800000u, 0xc0804000u};
-    mx_decode_word(w, h, l, o);
+// Eight E2M1 codes of one word -> four bf16 pairs times the factor: elements q and
+// q + 4 in o[q], the two that lie 16 bits apart in the word (memory order would
+// take another four permutations).
+QB_DEV void mx_decode_pairs(uint32_t w, __nv_bfloat162 factor, uint32_t (&o)[4]) {
+    constexpr uint32_t S = 0x80008000u, M = 0x01c001c0u;
+    o[0] = mx_mul2(((w << 12) & S) | ((w << 6) & M), factor);
+    o[1] = mx_mul2(((w << 8) & S) | ((w << 2) & M), factor);
+    o[2] = mx_mul2(((w << 4) & S) | ((w >> 2) & M), factor);
+    o[3] = mx_mul2((w & S) | ((w >> 6) & M), factor);
+}
+
+// The rest of a scale from 2^2 on (an overflow gives infinity, as rounding the
+// value would; 0xFF gives NaN).
+QB_DEV void mx_rescale(uint32_t sc, uint32_t (&o)[4]) {
+    const uint32_t b = (sc == 255u ? 0x7fffu : sc << 7) * 0x10001u;
+    const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[i]), scale);
-        o[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+    for (int q = 0; q < 4; ++q) o[q] = mx_mul2(o[q], scale);
 }
 
 }  // namespace qb

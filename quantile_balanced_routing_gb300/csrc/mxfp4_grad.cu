@@ -21,10 +21,12 @@
 //                converter warp polling, 1190 us with each suspended.)
 //   warp 1       TMEM owner and MMA issuer (one lane), warp 2 its waiter
 //   warps 3+     converters, two or four warps for each slot of the ring: codes and
-//                scales from global memory (a slot's turn ahead, in registers) to
-//                bf16 in the swizzled A tile.  Decoding a stage is mostly latency, so
-//                the stages in the ring are decoded side by side.
-//   the rest     epilogue, one or two per lane quarter: TMEM -> registers -> 64 or
+//                scales, which each warp copies by TMA to a buffer of its own a slot's
+//                turn ahead, to bf16 in the swizzled A tile.  Decoding a stage is mostly
+//                latency, so the stages in the ring are decoded side by side.  (Loads
+//                of the same lead from global memory to registers: dx 496 instead of 424
+//                us, dw 728 instead of 680.)
+//   the rest     epilogue, one per lane quarter: TMEM -> registers -> 64 or
 //                128 bytes of a row per store
 // A weight gradient's last stage may reach past its expert's rows, where another
 // expert's gradient may be infinite, and 0 * inf is not 0: whole groups of 16 rows
@@ -37,9 +39,9 @@
 // Where there are fewer tiles than SMs, an expert's rows are also cut into
 // parts for different CTAs, summed in order by a second kernel.
 //
-// Measured (65536 rows over 224 experts, 1024 x 3584): dx 515 us, 780 cycles a stage
-// of which the MMAs are 330: decoding (1600 instructions a stage) and hand-offs bound
-// it; dw in fp32 720 us, 3.3 GB of stores, which alone take 500.
+// Measured (65536 rows over 224 experts, 1024 x 3584): dx 424 us, 640 cycles a stage
+// of which the MMAs are 330: the hand-offs between the warps bound it; dw in fp32
+// 680 us, 3.3 GB of stores, which alone take 500.
 #include "mxfp4.cuh"
 #include "mxfp4_decode.cuh"
 #include "tc_ptx.cuh"
@@ -58,16 +60,17 @@ constexpr int kSegRows = 4096;                       // rows accumulated on the 
 constexpr int kStages = 4;
 constexpr int kConvWarp = 3;
 // Warps by direction.  dx: 16 converters decode a slot in half the latency of 8
-// (509 against 537 us).  dw needs more registers a converter (the tail of dy), and spills
-// at 72: 8 converters and 4 epilogue warps, 725 us, against 949 with 16 and 8.
+// (424 against 441 us).  dw needs more registers a converter (the tail of dy), and spills
+// with 16 (760 against 680 us).  8 epilogue warps gain neither (dx 430, dw 750).
 template <bool kWeights>
 struct Warps {
-    static constexpr int kConv = kWeights ? 8 : 16, kEpi = kWeights ? 4 : 8;
+    static constexpr int kConv = kWeights ? 8 : 16, kEpi = 4;
     static constexpr int kEpiFirst = kConvWarp + kConv;
     static constexpr int kConvPer = kConv / kStages;           // warps of a slot
     static constexpr int kItems = kC * 4 / (32 * kConvPer);    // 32-column blocks a thread decodes
     static constexpr int kThreads = (kEpiFirst + kEpi) * 32;
 };
+constexpr int kRawBytes = kC * kM / 2, kRawScales = kC * 16;   // codes and scales (16 bytes a row) of a stage
 constexpr int kMmaWarp = 1, kWaitWarp = 2;
 constexpr int kHandoffBar = 1, kEpiBar = 2, kSlotBar = 3;   // kSlotBar + slot
 constexpr long long kDefaultWait = 1LL << 17;
@@ -75,9 +78,10 @@ constexpr long long kDrainWait = 1LL << 12;
 
 struct Params {
     CUtensorMap b[4];            // dy [R, N] bf16: boxes of 64 features x 64 i rows; weights: x 64 and x 16 rows
+    CUtensorMap q, q_sf;         // Q's codes [., K / 2] and, if sf_tma, scales [., K / 32]: a converter warp's rows
+    int sf_tma;
     const __nv_bfloat16* dy;
     long long lddy;
-    const uint8_t* codes;        // Q's codes [., K / 2] and scales [., K / 32]
     const uint8_t* scales;
     const int32_t* offsets;
     void* out;
@@ -93,7 +97,7 @@ struct Params {
 };
 
 constexpr int smem_bytes(int E) {
-    return 1024 + kStages * (kABytes + kBBytes) + (2 * (E + 1) + 64) * 4 + 256;
+    return 1024 + kStages * (kABytes + kBBytes + kRawBytes + kRawScales) + (2 * (E + 1) + 64) * 4 + 512;
 }
 
 // One tile of D: columns kt * 128 .. of K for the output rows [row0, row0 + cols)
@@ -227,11 +231,22 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// 32 columns of one step: codes and their scale byte; zeros where there is nothing.
-struct Item {
-    uint4 q;
-    uint32_t sc;
-};
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_byte(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// (Straight into a 32-bit register: a conversion would wait for the load.)
+__device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 
 template <bool kWeights, typename Out>
 __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const __grid_constant__ Params p) {
@@ -242,12 +257,15 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* a_ring = smem;
     uint8_t* b_ring = a_ring + kStages * kABytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(b_ring + kStages * kBBytes);
+    uint8_t* raw_codes = b_ring + kStages * kBBytes;           // a part for each converter warp
+    uint8_t* raw_scales = raw_codes + kStages * kRawBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(raw_scales + kStages * kRawScales);
     uint64_t* empty = full + kStages;
     uint64_t* accf = empty + kStages;
     uint64_t* acce = accf + 2;
     uint64_t* drain = acce + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* raw = drain + 1;                                 // [converter warps]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw + Warps<kWeights>::kConv + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* go_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     int* scratch = reinterpret_cast<int*>(tmem_slot + 4);                     // [kThreads / 32]
@@ -267,6 +285,7 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
             tc::mbar_init(&acce[a], kEpiWarps);
         }
         tc::mbar_init(drain, 1);
+        for (int i = 0; i < Warps<kWeights>::kConv; ++i) tc::mbar_init(&raw[i], 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
         tc::fence_proxy_async_smem();
@@ -331,36 +350,54 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
                 if ((issued >> i) & 1u) tc::mbar_wait(&full[i], (last_par >> i) & 1u, kDrainWait);
     } else if (warp >= kConvWarp && warp < kEpiWarp) {
         // ---------------------------------------------------------- converters
-        // Thread (c, b) of a slot: steps c, c + 8 warps, .. of a stage, column block b (32
-        // columns, one scale).  A warp reads 64 bytes of each of 8 rows; eight
-        // consecutive lanes have eight rows, whose 16-byte chunks the swizzle puts
-        // in eight different places.
-        const int slot = (warp - kConvWarp) / kConvPer;
+        // A warp has 8 kItems consecutive steps of its slot's stages, a thread (c, b) of
+        // them steps c, c + 8, .. and column block b (32 columns, one scale); eight
+        // consecutive lanes have eight rows, whose 16-byte chunks the swizzles put in
+        // eight different places.  Once a stage's codes are in registers the copy of
+        // the next turn's may overwrite them.  Scales come with them where their rows
+        // are 16-byte multiples, by plain loads otherwise.
+        const int slot = (warp - kConvWarp) / kConvPer, team = (warp - kConvWarp) % kConvPer;
         const int ct = threadIdx.x - (kConvWarp + slot * kConvPer) * 32;
-        constexpr int kTeam = 32 * kConvPer, kRowsPer = kTeam / 4;
-        const int b = lane >> 3, c = (ct >> 5) * 8 + (lane & 7);
-        const int half = p.K / 2, pitch = p.K / 32;
+        constexpr int kRows = 8 * kItems;
+        static_assert(kRows * kConvPer == kC);
+        const int b = lane >> 3, c = team * kRows + (lane & 7);
+        uint64_t* arrived = &raw[warp - kConvWarp];
+        uint8_t* my_codes = raw_codes + (warp - kConvWarp) * (kRows * 64);
+        uint8_t* my_scales = raw_scales + (warp - kConvWarp) * (kRows * 16);
+        // row i of 64 bytes: chunk b is at b ^ (i / 2 % 4)
+        const uint32_t code_at = tc::smem_u32(my_codes) + (lane & 7) * 64 + ((b ^ ((lane & 7) >> 1)) << 4);
+        const uint32_t scale_at = tc::smem_u32(my_scales) + (lane & 7) * 16 + b;
+        const int pitch = p.K / 32;
         Cursor<kWeights> cur;
         cur.start(p, gr, n_tiles, it, slot);
-        Item v[kItems];
+        uint32_t sc[kItems];
         // the last, partial group of 16 rows of dy: 16 steps x 32 chunks of 8 features
-        constexpr int kTail = 16 * 32 / kTeam;
+        constexpr int kTail = 16 * 32 / (32 * kConvPer);
         uint4 bv[kWeights ? kTail : 1];
-        int rem = 0;   // its rows
-        auto fetch = [&] {
+        int rem = 0;     // its rows
+        int left = 0;    // steps from this thread's first to the end of the tile
+        bool dead = false, asked = false;   // lane 0: an expiry; a copy is on its way
+        uint32_t ph = 0;
+        auto first_row = [&] { return (int)((kWeights ? (long long)cur.x.b0 : cur.x.q0) + cur.c + team * kRows); };
+        auto ask = [&] {
+            if (cur.live && lane == 0 && !dead) {
+                const int k = cur.x.kt * kM, row = first_row();
+                tc::mbar_expect_tx(arrived, kRows * (p.sf_tma ? 80 : 64));
+                tc::tma_load_2d(my_codes, &p.q, arrived, k / 2, row);
+                if (p.sf_tma) tc::tma_load_2d(my_scales, &p.q_sf, arrived, k / 32 & ~15, row);
+                asked = true;
+            }
+        };
+        auto fetch = [&] {   // the rest of a stage
             if (!cur.live) return;
-            const int k = cur.x.kt * kM + 32 * b;
-            const int left = k < p.K ? cur.x.len - cur.c - c : 0;   // steps from this thread's first to the end
-            const long long from = (kWeights ? (long long)cur.x.b0 : cur.x.q0) + cur.c + c;
-            const uint8_t* codes = p.codes + from * half + k / 2;
-            const uint8_t* scales = p.scales + from * pitch + k / 32;
+            left = cur.x.len - cur.c - c;
+            if (!p.sf_tma) {
+                const int k = cur.x.kt * kM;
+                const uint8_t* scales = p.scales + ((long long)first_row() + (lane & 7)) * pitch + k / 32 + b;
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                v[i].q = make_uint4(0, 0, 0, 0);
-                v[i].sc = 127;
-                if (kRowsPer * i < left) {
-                    v[i].q = __ldg(reinterpret_cast<const uint4*>(codes + i * (kRowsPer * half)));
-                    v[i].sc = __ldg(scales + i * (kRowsPer * pitch));
+                for (int i = 0; i < kItems; ++i) {
+                    sc[i] = 127;
+                    if (8 * i < left && k + 32 * b < p.K) sc[i] = ld_byte(scales + i * (8 * pitch));
                 }
             }
             if constexpr (kWeights) {
@@ -378,13 +415,32 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
                 }
             }
         };
+        ask();
         fetch();
         const uint32_t B = tc::smem_u32(b_ring + slot * kBBytes);
         uint32_t dst[4];   // of the thread's first step; the swizzle repeats every 8 steps
 #pragma unroll
         for (int j = 0; j < 4; ++j) dst[j] = tc::smem_u32(a_ring + slot * kABytes + mn_offset(c, 4 * b + j));
         while (cur.live) {
-            tc::named_bar_sync(kSlotBar + slot, 32 + 32 * kConvPer);   // the slot is free
+            if (lane == 0 && !dead) {
+                if (tc::mbar_wait_spin(arrived, ph, lim)) {
+                    asked = false;
+                } else {
+                    expired();
+                    dead = true;
+                }
+                ph ^= 1u;
+            }
+            __syncwarp();
+            uint4 v[kItems];
+            const uint32_t first_scale = scale_at + ((cur.x.kt & 3) << 2);
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                v[i] = ld_shared16(code_at + i * 512);
+                if (p.sf_tma) sc[i] = ld_shared_byte(first_scale + i * 128);
+                if (8 * i >= left) v[i] = make_uint4(0, 0, 0, 0), sc[i] = 127;   // another expert's rows
+            }
+            tc::named_bar_sync(kSlotBar + slot, 32 + 32 * kConvPer);   // the slot is free, the codes are read
             if constexpr (kWeights) {
                 if (rem) {
                     const int h0 = (cur.x.len - cur.c) & ~15;
@@ -393,23 +449,26 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
                         st_shared16(B + mn_offset(h0 + (ct >> 5) + kConvPer * i, ct & 31), bv[i]);
                 }
             }
+            cur.advance(p, gr, n_tiles, kStages);
+            ask();
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const uint32_t q[4] = {v[i].q.x, v[i].q.y, v[i].q.z, v[i].q.w};
-                const __nv_bfloat162 scale = e8m0_bf16x2(v[i].sc);
+                const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const __nv_bfloat162 factor = mx_factor(sc[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t o[4];
-                    mx_decode_scaled(q[j], scale, o);
-                    st_shared16(dst[j] + i * (kRowsPer * 128), make_uint4(o[0], o[1], o[2], o[3]));
+                    mx_decode_pairs(q[j], factor, o);
+                    if (sc[i] >= kMxLargeScale) mx_rescale(sc[i], o);
+                    st_shared16(dst[j] + i * 1024, make_uint4(o[0], o[1], o[2], o[3]));
                 }
             }
             tc::fence_proxy_async_smem();   // generic-proxy writes -> tcgen05.mma reads
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&full[slot]);
-            cur.advance(p, gr, n_tiles, kStages);
             fetch();
         }
+        if (lane == 0 && asked) tc::mbar_wait(arrived, ph ^ 1u, kDrainWait);
         __syncthreads();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
@@ -486,11 +545,13 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
         __syncthreads();
     } else {
         // ---------------------------------------------------------- epilogue
-        // Lane 32 q + i of an accumulator is column kt * 128 + 32 q + i of K, its
-        // TMEM columns are output rows.  fp32: a warp stores 128 bytes of a row at a
-        // time; bf16: neighbouring lanes exchange one of every two rows' values
-        // and a warp stores 64 bytes of two rows.
-        const int q = warp & 3, odd = lane & 1, part = (warp - kEpiWarp) >> 2;
+        // Lane 32 q + i of an accumulator is a column of kt * 128 + 32 q .. + 31 of K, in
+        // the order in which the converters decode a word: lanes 2 j and 2 j + 1 of
+        // eight are columns j and j + 4.  Its TMEM columns are output rows.  fp32: a
+        // warp stores 128 bytes of a row at a time; bf16: lanes of neighbouring columns
+        // exchange one of every two rows' values and a warp stores 64 bytes of two rows.
+        const int column = (lane & ~7) | ((lane & 7) >> 1) | ((lane & 1) << 2);
+        const int q = warp & 3, odd = (lane >> 1) & 1;
         const uint32_t ldo = (uint32_t)p.ldo;
         bool dead = false;
         int ab = 0;
@@ -508,7 +569,7 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
             const int k = x.kt * kM + 32 * q;   // K is a multiple of 32: a warp's columns are all there or none
             const int cols = k < p.K ? x.cols : 0;
             Out* out = static_cast<Out*>(p.out) + first_row * p.ldo + k;
-            for (int c0 = 16 * part; c0 < cols; c0 += 4 * kEpiWarps) {
+            for (int c0 = 0; c0 < cols; c0 += 16) {
                 float v[16];
                 tc::tmem_ld16(tbase + ab * kN + (static_cast<uint32_t>(32 * q) << 16) + c0, v);
                 if (x.len == 0)
@@ -517,7 +578,7 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
                 Out* o = out + (long long)c0 * p.ldo;
                 const int left = cols - c0;
                 if constexpr (sizeof(Out) == 4) {
-                    o += lane;
+                    o += column;
                     if (!x.first) {     // this thread stored the sum so far
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -532,10 +593,10 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
                             if (i < left) o[(uint32_t)i * ldo] = v[i];
                     }
                 } else {
-                    o += lane & ~1;
+                    o += column & ~1;
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 2);
                         const __nv_bfloat162 h =
                             odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
                         if (i + odd < left) *reinterpret_cast<__nv_bfloat162*>(o + (uint32_t)(i + odd) * ldo) = h;
@@ -623,9 +684,17 @@ int mx_grad(const MxGrad& q, cudaStream_t s) {
         if (!encode_rows(&p.b[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, q.R ? q.R : 1, q.N, q.lddy * 2, 64,
                          q.weights ? (i ? 16 : kC) : kBox * (i + 1)))
             return QBMOE_ECUDA;
+    const long long q_rows = q.weights ? q.R : (long long)q.E * q.N;
+    const int box = q.weights ? 8 * Warps<true>::kItems : 8 * Warps<false>::kItems;
+    // a TMA row is a multiple of 16 bytes
+    p.sf_tma = q.K % 512 == 0 && aligned16(q.scales);
+    if (q_rows &&
+        (!encode_rows(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, q_rows, q.K / 2, q.K / 2, 64, box) ||
+         (p.sf_tma && !encode_rows(&p.q_sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.scales, q_rows, q.K / 32, q.K / 32, 16, box, true))))
+        return QBMOE_ECUDA;
     p.dy = static_cast<const __nv_bfloat16*>(q.dy);
     p.lddy = q.lddy;
-    p.codes = q.codes; p.scales = q.scales; p.offsets = q.offsets;
+    p.scales = q.scales; p.offsets = q.offsets;
     p.out = q.out; p.ldo = q.ldo;
     p.R = q.R; p.E = q.E; p.N = q.N; p.K = q.K;
     p.k_tiles = (q.K + kM - 1) / kM;

@@ -395,3 +395,20 @@ def test_bounded_wait_reports_and_recovers():
         assert Q.qbmoe_status(None, None) == 0
         assert torch.equal(f(), right)
         assert Q.qbmoe_status(None, None) == 0
+
+
+@pytest.mark.parametrize("K", [512, 544, 96])
+def test_gradients_decode_every_code_and_scale(K):
+    """With the identity as dy the gradients are the operands' values, exactly, at every scale whose
+    values are normal and finite (blocks of a row take scales 37 apart)."""
+    import quantile_balanced_routing_gb300 as Q
+    n = 256
+    row, block = np.arange(n)[:, None], np.arange(K // 32)[None]
+    scales = (2 + (row + 37 * block) % 251).astype(np.uint8)          # 2 .. 252
+    byte = (np.arange(K // 2)[None] * 17 + 5 * row) % 256               # both codes of a byte, all pairs
+    codes = byte.astype(np.uint8)
+    q, _, _ = on_gpu(Q, (codes, scales), (codes, scales), None, 0, n, K)
+    want = M.decode(codes, scales)
+    dx, dw = Q.mxfp4_matmul_backward(torch.eye(n).bfloat16().cuda(), q, q)
+    assert np.array_equal(dx.double().cpu().numpy(), want)
+    assert np.array_equal(dw.double().cpu().numpy(), want)
