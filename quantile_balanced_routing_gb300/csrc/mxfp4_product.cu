@@ -36,11 +36,12 @@
 // main loop.
 //
 // Measured (weights 1024 x 3584 an expert): 4096 rows over 896 experts 252 us, the
-// packed weights at 6.9 TB/s; 262144 rows over 896 experts 545 us (3.5 PFLOP/s, 5.1 TB/s);
-// 1999 rows by 3584 x 7168 24 us (4.3 PFLOP/s).  The row tile is 208 so that two
-// accumulators and four stages' scale slots fill TMEM's 512 columns; larger tiles wait
-// on the hand-offs between the warps (570 to 800 cycles a stage, MMAs 300 to 400),
-// 16-row tiles on HBM.
+// packed weights at 6.9 TB/s; 262144 rows over 896 experts 508 us (3.8 PFLOP/s, 5.5 TB/s);
+// 1999 rows by 3584 x 7168 24 us (4.3 PFLOP/s).  16-row tiles are bound by HBM, larger
+// ones by the time a stage's slot is held (copies and hand-offs, about 3000 cycles, of
+// which the MMAs are 300 to 400): what fits in flight counts.  Tiles of 192 rows
+// with five slots take 508 us where 208 with four take 545, 160 with five 538, 144 with
+// six 532 and 128 with six 558 (with five 599).
 // Every mbarrier wait is bounded: on expiry the kernel records
 // QBMOE_ETIMEOUT, stops, lets its own copies and MMAs finish and frees TMEM.
 #include "mxfp4.cuh"
@@ -57,7 +58,6 @@ using namespace qb;
 constexpr int kStageK = 256;                 // elements of K per stage (128 bytes of codes a row)
 constexpr int kABytes = 128 * 128;           // weight codes of a stage
 constexpr int kMmaWarp = 1, kWaitWarp = 2, kSfLoadWarp = 3, kSfWarp = 4, kEpiWarp = 8;
-constexpr int kSfSlots = 4;                  // scale groups in flight
 constexpr int kHandoffBar = 1, kEpiBar = 2, kStageBar = 3;
 constexpr int kMaxBoxes = 4;                 // row-tile maps: heights BN / n, 2 BN / n, ...
 constexpr long long kDefaultWait = 1LL << 17;   // polls (<= 20 us each) before a wait expires
@@ -86,7 +86,7 @@ struct Shape {
     static constexpr int kEpiWarps = BN == 16 ? 4 : 8;
     static constexpr int kProdBWarp = kEpiWarp + kEpiWarps;
     static constexpr int kThreads = (kProdBWarp + 1) * 32;
-    static constexpr int kBoxes = BN == 208 ? 4 : BN == 128 ? 2 : 1;
+    static constexpr int kBoxes = BN > 128 ? 4 : BN == 128 ? 2 : 1;
     static constexpr int kBox = BN / kBoxes;                     // a row tile is one copy, of the least multiple that holds it
     static constexpr int kNB = (BN + 127) / 128;                 // 128-row blocks of B's scales
     static constexpr int kBJ = (BN + 31) / 32;                   // 32-row blocks
@@ -94,10 +94,12 @@ struct Shape {
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kSfBytes = (128 + BN) * 16;             // scales of a group
     static constexpr int kSfCols = 8 + 8 * kNB;                  // TMEM columns of a stage's scales
-    static constexpr int stages = BN == 64 ? 7 : BN == 128 ? 5 : 4;
+    static constexpr int kSfSlots = BN <= 64 ? 4 : 3;            // scale groups in flight, of two stages each
+    static constexpr int stages = BN == 64 ? 7 : BN == 128 ? 6 : BN == 192 ? 5 : 4;
     static constexpr int kColsUsed = 2 * BN + stages * kSfCols;  // two accumulators, a scale slot per stage
     static constexpr uint32_t kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
     static_assert(kColsUsed <= 512, "TMEM columns");
+    static_assert(stages <= 2 * kSfSlots, "scales in flight for every stage");
     static constexpr int smem(int E) {
         return 1024 + stages * kStage + kSfSlots * kSfBytes + (2 * (E + 1) + 64) * 4 + 256;
     }
@@ -149,7 +151,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 template <int BN>
 __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_product(const __grid_constant__ Params p) {
     using Sh = Shape<BN>;
-    constexpr int S = Sh::stages;
+    constexpr int S = Sh::stages, kSfSlots = Sh::kSfSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* a_ring = smem;
@@ -564,6 +566,7 @@ int mx_product_init() {
     if (!rc) rc = set_attributes<16>();
     if (!rc) rc = set_attributes<64>();
     if (!rc) rc = set_attributes<128>();
+    if (!rc) rc = set_attributes<192>();
     if (!rc) rc = set_attributes<208>();
     if (!rc) g_status_ptr[dev] = static_cast<int*>(f);
     return rc;
@@ -627,11 +630,19 @@ int mx_product(const MxProduct& q, cudaStream_t s) {
     p.status = mx_status();
     p.wait_limit = g_wait_limit;
     p.stall = g_stall;
-    // Row tile: the smallest that holds an average expert's rows.
+    // Row tile: the smallest that holds an average expert's rows, 192 beyond. One
+    // matrix whose tiles of 208 rows save over a quarter of the grid's rounds takes those (by
+    // 3584 x 7168, 1040 rows, one round or two: 23.2 against 27.3 us; 1999 rows, two
+    // or three: 31.4 against 33.5).
+    const auto rounds = [&](int rows) {
+        const long long tiles = (long long)((q.R + rows - 1) / rows) * p.m_total;
+        return (tiles + sm_count() - 1) / sm_count();
+    };
     const int avg = (q.R + q.E - 1) / q.E;
     if (avg <= 16) return launch<16>(q, p, s);
     if (avg <= 64) return launch<64>(q, p, s);
     if (avg <= 128) return launch<128>(q, p, s);
+    if (q.E > 1 || 4 * rounds(208) >= 3 * rounds(192)) return launch<192>(q, p, s);
     return launch<208>(q, p, s);
 }
 

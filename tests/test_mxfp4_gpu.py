@@ -412,3 +412,14 @@ def test_gradients_decode_every_code_and_scale(K):
     dx, dw = Q.mxfp4_matmul_backward(torch.eye(n).bfloat16().cuda(), q, q)
     assert np.array_equal(dx.double().cpu().numpy(), want)
     assert np.array_equal(dw.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("R,N,K", [(208, 152 * 128, 96), (203, 152 * 128 - 56, 512), (386, 76 * 128, 544)])
+def test_product_of_one_matrix_in_fewer_rounds(R, N, K):
+    """Rows that tiles of 208 hold in one round of the grid less than tiles of 192."""
+    import quantile_balanced_routing_gb300 as Q
+    xq, wq, _, _ = product_case(R, 0, N, K, 0.0)
+    x, w, _ = on_gpu(Q, xq, wq, None, 0, N, K)
+    want, mags = M.matmul(xq[2], wq[2][None], None)
+    near(Q.mxfp4_matmul(x, w), want, mags, K, True)
+    assert Q.qbmoe_status(None, None) == 0
