@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 // slope d_j = s_j c_j:
 //   dx_j = d_j (f_j - D) / S_t                              balance loss
 //        + d_j (dw_i - sum_l dw_l w_l) / sum_l s_(idx_l)    j = idx_i, mixture weights
+// The slope is divided by the sum first: that quotient is at most 1, where the
+// reciprocal of a sum alone reaches e^80.
 // A CTA has a chunk of tokens and f of the chunk's sequence in shared memory
 // (a chunk that crosses a boundary goes through its sequences in turn).  A warp
 // has its next row on the way to shared memory (cp.async) while it works on this
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const Router
                     const int j = (32 * i + lane) * V;
                     if (j >= a.n) continue;
                     if constexpr (V == 1) {
-                        out[j] = from_f32<T>(x[i] * ((fs[j] - D) * inv));
+                        out[j] = from_f32<T>((x[i] * inv) * (fs[j] - D));
                     } else {
                         float f[V];
 #pragma unroll
@@ -378,13 +380,14 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const Router
                         uint4 o;
                         T* e = reinterpret_cast<T*>(&o);
 #pragma unroll
-                        for (int v = 0; v < V; ++v) e[v] = from_f32<T>(x[i * V + v] * ((f[v] - D) * inv));
+                        for (int v = 0; v < V; ++v) e[v] = from_f32<T>((x[i * V + v] * inv) * (f[v] - D));
                         *reinterpret_cast<uint4*>(out + j) = o;
                     }
                 }
                 if (a.dw) {
                     __syncwarp();   // the row is stored before the chosen entries
-                    if (chosen) out[id] = from_f32<T>(slope * fmaf(fs[id] - D, inv, (d - mean) * w_inv));
+                    if (chosen)
+                        out[id] = from_f32<T>(fmaf(slope * inv, fs[id] - D, (slope * w_inv) * (d - mean)));
                 }
             }
             __syncwarp();   // the row's readers are done before its buffer is filled again

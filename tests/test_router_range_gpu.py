@@ -1,0 +1,39 @@
+"""The router's gradient where scores are tiny: tokens whose logits lie around the clamp at -80.
+
+A score there is about 2^-115, its reciprocal 2^115: a product of the reciprocal with
+a large upstream gradient leaves fp32's range although the gradient itself does not.
+
+Tolerance.  Weights and shares are quotients of scores within |x| 2^-24 + 2^-21 of their
+values, |x| <= 80: 2^-16 covers a quotient and the rounding of the sums, and the two
+differences that make a gradient (d - mean, f - D) are bounded by twice the largest
+term: 2^-14 of the largest term.
+"""
+import numpy as np
+import pytest
+
+import mx_reference as M
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def saturated(T, n, k, lo, hi, seed):
+    r = np.random.RandomState(seed)
+    x = r.uniform(lo, hi, (T, n)).astype(np.float32)
+    idx = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    idx[1::2] = np.argsort(x, axis=1, kind="stable")[1::2, :k]       # the lowest: where the clamp holds
+    return r, torch.from_numpy(x), torch.from_numpy(np.ascontiguousarray(idx).astype(np.int32))
+
+
+@pytest.mark.parametrize("n,k", [(16, 2), (101, 7), (896, 16)])      # 16-byte rows, odd rows, the layer's
+@pytest.mark.parametrize("size", [2e4, 1e30])
+@pytest.mark.parametrize("lo,hi", [(-85.0, -79.0), (-80.0, -70.0)])
+def test_mixture_weights_of_tiny_scores(n, k, size, lo, hi):
+    import quantile_balanced_routing_gb300 as Q
+    r, x, idx = saturated(40, n, k, lo, hi, n)
+    dw = (size * r.choice([-1.0, 0.5, 1.0], (40, k))).astype(np.float32)
+    g = Q.router_backward(x.cuda(), idx.cuda(), dw=torch.from_numpy(dw).cuda()).double().cpu().numpy()
+    want = M.router_grad(x.numpy(), idx.numpy(), dw, None, None, None)
+    assert np.isfinite(g).all()
+    assert (g[x.numpy() < -80] == 0).all()
+    assert np.abs(g - want).max() < 2.0 ** -14 * np.abs(dw).max()
