@@ -234,8 +234,10 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 //   dx_j = d_j (f_j - D) / S_t                              balance loss
 //        + d_j (dw_i - sum_l dw_l w_l) / sum_l s_(idx_l)    j = idx_i, mixture weights
 // The slope is divided by the sum first: that quotient is at most 1, where the
-// reciprocal of a sum alone reaches e^80.
-// A CTA has a chunk of tokens and f of the chunk's sequence in shared memory
+// reciprocal of a sum alone reaches e^80.  Likewise D is summed over the counts (the
+// factor of f after it) and the mean over weights, not scores: a score of e^-80 times
+// a small gradient would be subnormal.
+// A CTA has a chunk of tokens and the counts of the chunk's sequence in shared memory
 // (a chunk that crosses a boundary goes through its sequences in turn).  A warp
 // has its next row on the way to shared memory (cp.async) while it works on this
 // one, where rows are 16-byte vectors.  The dense row is stored first, then the k
@@ -297,17 +299,18 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const Router
     float d;
     fetch(t, buf);
     scalars(t, live, id, d);
+    float scale = 0.0f;   // f_j = scale counts_j
     for (int t0 = c0; t0 < c1; ++q) {
         const int t1 = a.dloss && a.seq && q + 1 < a.S ? min(c1, max(t0, __ldg(a.seq + q + 1))) : c1;
         if (t1 > t0) {
             __syncthreads();   // the last sequence's readers are done
-            float scale = 0.0f;
+            scale = 0.0f;
             if (a.dloss) {
                 const float tq = fmaxf((float)__ldg(a.tokens + q), 1.0f);
                 scale = __ldg(a.dloss + q) * ((float)a.n / ((float)a.k * tq)) / tq;
             }
             for (int j = threadIdx.x; j < a.n; j += kBalThreads)
-                fs[j] = a.dloss ? scale * (float)__ldg(a.counts + (long long)q * a.n + j) : 0.0f;
+                fs[j] = a.dloss ? (float)__ldg(a.counts + (long long)q * a.n + j) : 0.0f;
             __syncthreads();
         }
         for (; t < t1; t += kBalWarps, buf ^= 1) {
@@ -359,19 +362,19 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const Router
                     }
                 }
                 const float inv = __fdividef(1.0f, warp_sum(sum));
-                const float D = warp_sum(dot) * inv;
+                const float D = scale * (warp_sum(dot) * inv);
                 float w_inv = 0.0f, mean = 0.0f;
                 if (a.dw) {
                     const float all = warp_sum(own);
                     w_inv = all > 0.0f ? 1.0f / all : all != all ? all : 0.0f;
-                    mean = warp_sum(d * own) * w_inv;
+                    mean = warp_sum(d * (own * w_inv));
                 }
 #pragma unroll
                 for (int i = 0; i < kMaxPerLane / V; ++i) {
                     const int j = (32 * i + lane) * V;
                     if (j >= a.n) continue;
                     if constexpr (V == 1) {
-                        out[j] = from_f32<T>((x[i] * inv) * (fs[j] - D));
+                        out[j] = from_f32<T>((x[i] * inv) * fmaf(fs[j], scale, -D));
                     } else {
                         float f[V];
 #pragma unroll
@@ -380,14 +383,14 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const Router
                         uint4 o;
                         T* e = reinterpret_cast<T*>(&o);
 #pragma unroll
-                        for (int v = 0; v < V; ++v) e[v] = from_f32<T>((x[i * V + v] * inv) * (f[v] - D));
+                        for (int v = 0; v < V; ++v) e[v] = from_f32<T>((x[i * V + v] * inv) * fmaf(f[v], scale, -D));
                         *reinterpret_cast<uint4*>(out + j) = o;
                     }
                 }
                 if (a.dw) {
                     __syncwarp();   // the row is stored before the chosen entries
                     if (chosen)
-                        out[id] = from_f32<T>(fmaf(slope * inv, fs[id] - D, (slope * w_inv) * (d - mean)));
+                        out[id] = from_f32<T>(fmaf(slope * inv, fmaf(fs[id], scale, -D), (slope * w_inv) * (d - mean)));
                 }
             }
             __syncwarp();   // the row's readers are done before its buffer is filled again

@@ -1,7 +1,8 @@
 """The router's gradient where scores are tiny: tokens whose logits lie around the clamp at -80.
 
 A score there is about 2^-115, its reciprocal 2^115: a product of the reciprocal with
-a large upstream gradient leaves fp32's range although the gradient itself does not.
+a large upstream gradient, or of the score with a small one, leaves fp32's normal
+range although the gradient itself does not.
 
 Tolerance.  Weights and shares are quotients of scores within |x| 2^-24 + 2^-21 of their
 values, |x| <= 80: 2^-16 covers a quotient and the rounding of the sums, and the two
@@ -26,7 +27,7 @@ def saturated(T, n, k, lo, hi, seed):
 
 
 @pytest.mark.parametrize("n,k", [(16, 2), (101, 7), (896, 16)])      # 16-byte rows, odd rows, the layer's
-@pytest.mark.parametrize("size", [2e4, 1e30])
+@pytest.mark.parametrize("size", [2e4, 1e30, 1e-10, 1e-20])
 @pytest.mark.parametrize("lo,hi", [(-85.0, -79.0), (-80.0, -70.0)])
 def test_mixture_weights_of_tiny_scores(n, k, size, lo, hi):
     import quantile_balanced_routing_gb300 as Q
@@ -37,3 +38,20 @@ def test_mixture_weights_of_tiny_scores(n, k, size, lo, hi):
     assert np.isfinite(g).all()
     assert (g[x.numpy() < -80] == 0).all()
     assert np.abs(g - want).max() < 2.0 ** -14 * np.abs(dw).max()
+
+
+@pytest.mark.parametrize("n,k", [(16, 2), (101, 7), (896, 16)])
+@pytest.mark.parametrize("size", [1e6, 1e-6, 1e-12])
+def test_balance_loss_of_tiny_scores(n, k, size):
+    import quantile_balanced_routing_gb300 as Q
+    _, x, idx = saturated(40, n, k, -80.5, -76.0, n)
+    r = Q.balance_loss(x.cuda(), idx.cuda())
+    dl = np.array([size], np.float32)
+    g = Q.router_backward(x.cuda(), idx.cuda(), dloss=torch.from_numpy(dl).cuda(), counts=r.counts, tokens=r.tokens)
+    g, counts = g.double().cpu().numpy(), r.counts.cpu().numpy()
+    want = M.router_grad(x.numpy(), idx.numpy(), None, dl, counts, r.tokens.cpu().numpy())
+    f = size * n / (k * 40.0 ** 2) * counts.max()
+    assert np.isfinite(g).all()
+    assert (g[x.numpy() < -80] == 0).all()
+    # a token's share of every expert is about 1 / n: so is the size of its gradients
+    assert np.abs(g - want).max() < 2.0 ** -14 * f * (M.scores(x.numpy()) / M.scores(x.numpy()).sum(1, keepdims=True)).max()
