@@ -361,8 +361,9 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_router_backward(const Router
                         dot = fmaf(f[v], s, dot);
                     }
                 }
-                const float inv = __fdividef(1.0f, warp_sum(sum));
-                const float D = scale * (warp_sum(dot) * inv);
+                // without a balance loss the scores of the others are not part of the gradient (nor a NaN there)
+                const float inv = a.dloss ? __fdividef(1.0f, warp_sum(sum)) : 0.0f;
+                const float D = a.dloss ? scale * (warp_sum(dot) * inv) : 0.0f;
                 float w_inv = 0.0f, mean = 0.0f;
                 if (a.dw) {
                     const float all = warp_sum(own);

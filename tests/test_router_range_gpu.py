@@ -55,3 +55,18 @@ def test_balance_loss_of_tiny_scores(n, k, size):
     assert (g[x.numpy() < -80] == 0).all()
     # a token's share of every expert is about 1 / n: so is the size of its gradients
     assert np.abs(g - want).max() < 2.0 ** -14 * f * (M.scores(x.numpy()) / M.scores(x.numpy()).sum(1, keepdims=True)).max()
+
+
+@pytest.mark.parametrize("n", [32, 33])
+def test_nan_of_an_expert_that_was_not_chosen(n):
+    """Without a balance loss only the chosen scores enter a token's gradient: a NaN elsewhere stays in its place."""
+    import quantile_balanced_routing_gb300 as Q
+    r, x, idx = saturated(20, n, 3, -3.0, 3.0, n)
+    dw = torch.from_numpy(r.standard_normal((20, 3)).astype(np.float32)).cuda()
+    clean = Q.router_backward(x.cuda(), idx.cuda(), dw=dw)
+    other = next(j for j in range(n) if j not in idx[7].tolist())
+    x[7, other] = float("nan")
+    g = Q.router_backward(x.cuda(), idx.cuda(), dw=dw)
+    keep = torch.ones(20, n, dtype=torch.bool)
+    keep[7, other] = False
+    assert torch.equal(g.cpu()[keep], clean.cpu()[keep])
