@@ -70,3 +70,48 @@ def test_nan_of_an_expert_that_was_not_chosen(n):
     keep = torch.ones(20, n, dtype=torch.bool)
     keep[7, other] = False
     assert torch.equal(g.cpu()[keep], clean.cpu()[keep])
+
+
+def one_token_sequences(T, n, k):
+    x = torch.empty(T, n).uniform_(-80, 80, generator=torch.Generator().manual_seed(n))
+    idx = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :k].to(torch.int32).contiguous()
+    return x, idx, torch.arange(T + 1, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("n", [64, 63])
+def test_scores_keep_fp32_over_the_whole_range(n):
+    """Shares of single tokens, element by element.  A score is within 2^-21 of its value: 2^-22 for the exponential,
+    2^-23 for the reciprocal, 2^-24 for each of two roundings.  Its sum adds 8 roundings, the quotient 3: 2^-19 covers
+    a share.  (An exponent rounded once before the exponential is off by up to 115 2^-25, 2^-18 of the score.)"""
+    import quantile_balanced_routing_gb300 as Q
+    x, idx, off = one_token_sequences(512, n, 4)
+    r = Q.balance_loss(x.cuda(), idx.cuda(), off.cuda())
+    loss, _, want, _ = M.balance(x.double().numpy(), idx.numpy(), off.numpy())
+    got = r.probs.double().cpu().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -19 * want).all()
+    assert (np.abs(r.loss.double().cpu().numpy() - loss) <= 2.0 ** -18 * loss).all()
+
+
+@pytest.mark.parametrize("n", [64, 63])
+def test_gradients_keep_fp32_over_the_whole_range(n):
+    """Element by element, against the size of the terms that an element is the difference of: its slope over the sum
+    of scores times the largest gradient.  Slope and quotient are within 2^-18.5, the mean within 2^-19.5: 2^-17."""
+    import quantile_balanced_routing_gb300 as Q
+    x, idx, off = one_token_sequences(512, n, 4)
+    r = np.random.RandomState(n)
+    dw, dl = r.standard_normal((512, 4)).astype(np.float32), r.standard_normal(512).astype(np.float32)
+    xs, up = x.double().numpy(), lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    _, counts, _, tokens = M.balance(xs, idx.numpy(), off.numpy())
+    s = M.scores(xs)
+    slope = s * M.scores(-xs)
+    chosen = np.zeros(s.shape)
+    np.put_along_axis(chosen, idx.numpy(), 1.0, 1)
+    g = Q.router_backward(x.cuda(), idx.cuda(), dw=up(dw)).double().cpu().numpy()
+    want = M.router_grad(xs, idx.numpy(), dw, None, counts, tokens, off.numpy())
+    size = slope / (s * chosen).sum(1, keepdims=True) * np.abs(dw).max(1, keepdims=True)
+    assert (np.abs(g - want) <= 2.0 ** -17 * size * chosen).all()
+    g = Q.router_backward(x.cuda(), idx.cuda(), dloss=up(dl), counts=up(counts.astype(np.int32)),
+                          tokens=up(tokens.astype(np.int32)), seq_offsets=off.cuda()).double().cpu().numpy()
+    want = M.router_grad(xs, idx.numpy(), None, dl, counts, tokens, off.numpy())
+    size = slope / s.sum(1, keepdims=True) * (np.abs(dl) * n / 4)[:, None]
+    assert (np.abs(g - want) <= 2.0 ** -17 * size).all()
