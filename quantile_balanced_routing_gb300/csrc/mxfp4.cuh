@@ -14,7 +14,7 @@ int mx_grad_init();      // mxfp4_grad.cu
 // Status word of the calls that take no context (one per device): the first
 // code a kernel recorded since it was last taken, then cleared.
 int* mx_status();
-int mx_status_take();
+int mx_status_take(cudaStream_t s);
 // Test hooks of those calls (qbmoe_set_wait_limit / qbmoe_debug_stall without a context).
 long long mx_wait_limit();
 void mx_set_wait_limit(long long polls);

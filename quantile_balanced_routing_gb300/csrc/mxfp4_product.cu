@@ -576,12 +576,13 @@ int* mx_status() {
     const int dev = current_device();
     return dev < 0 ? nullptr : g_status_ptr[dev];
 }
-int mx_status_take() {
+int mx_status_take(cudaStream_t s) {
     int* p = mx_status();
     if (!p) return QBMOE_OK;   // no call has run on this device
     int v = 0;
-    if (cudaMemcpy(&v, p, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return QBMOE_ECUDA;
-    if (v != 0 && cudaMemset(p, 0, 4) != cudaSuccess) return QBMOE_ECUDA;
+    if (cudaMemcpyAsync(&v, p, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess) return QBMOE_ECUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return QBMOE_ECUDA;
+    if (v != 0 && cudaMemsetAsync(p, 0, 4, s) != cudaSuccess) return QBMOE_ECUDA;
     return v;
 }
 long long mx_wait_limit() { return g_wait_limit; }
