@@ -457,8 +457,10 @@ int moe_latent_forward(qbmoe_ctx* ctx, int T, const void* x, const float* logits
  * Synchronise `stream`, then return and clear the context's device status
  * word: QBMOE_OK, QBMOE_ETIMEOUT (a bounded wait expired; the kernel
  * returned early and its outputs are undefined) or QBMOE_EDEVICE.
- * ctx may be NULL: the status word of the calls that take no context
- * (moe_mxfp4_*, one word per device) instead.
+ * ctx may be NULL: QBMOE_ETIMEOUT if a bounded wait of any call that takes no
+ * context (moe_mxfp4_*) has expired on the current device since the calling
+ * host thread last asked, in whichever thread or stream (a thread that never
+ * asked: since the library was loaded).
  */
 int qbmoe_status(qbmoe_ctx* ctx, qbmoe_stream_t stream);
 

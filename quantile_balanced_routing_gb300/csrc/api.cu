@@ -430,7 +430,7 @@ extern "C" int qbmoe_status(qbmoe_ctx* c, qbmoe_stream_t stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess) return QBMOE_ECUDA;
     if (cudaGetLastError() != cudaSuccess) return QBMOE_ECUDA;
-    if (!c) return qbh::mx_status_take(s);
+    if (!c) return qbh::mx_new_expiries(s);
     int v = 0;
     if (cudaMemcpy(&v, c->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return QBMOE_ECUDA;
     if (v != 0 && cudaMemset(c->status, 0, 4) != cudaSuccess) return QBMOE_ECUDA;

@@ -11,10 +11,11 @@ namespace qbh {
 int mx_product_init();   // mxfp4_product.cu
 int mx_grad_init();      // mxfp4_grad.cu
 
-// Status word of the calls that take no context (one per device): the first
-// code a kernel recorded since it was last taken, then cleared.
-int* mx_status();
-int mx_status_take(cudaStream_t s);
+// Expired waits of the calls that take no context, counted on each device; and, after
+// synchronising s, whether there were any since the calling thread last asked
+// (QBMOE_OK or QBMOE_ETIMEOUT).
+int* mx_expiries();
+int mx_new_expiries(cudaStream_t s);
 // Test hooks of those calls (qbmoe_set_wait_limit / qbmoe_debug_stall without a context).
 long long mx_wait_limit();
 void mx_set_wait_limit(long long polls);

@@ -91,7 +91,7 @@ struct Params {
     int splits;                  // weights: parts of each expert's rows, out [splits, E, N, K]
     int seg_rows;                // weights: rows per accumulation
     int step_e, step_s, step_f, step_k;   // weights: the grid size in experts, parts and tiles
-    int* status;
+    int* expiries;
     long long wait_limit;
     int stall;
 };
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(Warps<kWeights>::kThreads, 1) k_mx_grad(const 
     const int n_tiles = it.count(p, gr);
     it.start(p, gr);
     auto expired = [&] {
-        set_status(p.status, QBMOE_ETIMEOUT);
+        if (p.expiries) atomicAdd(p.expiries, 1);
         *abort_flag = 1;
     };
 
@@ -703,7 +703,7 @@ int mx_grad(const MxGrad& q, cudaStream_t s) {
     p.splits = q.weights ? mx_wgrad_splits(q.R, q.E, q.N, q.K) : 1;
     // bf16 sums need no more than the tensor cores keep
     p.seg_rows = q.out_type == QBMOE_F32 || p.splits > 1 ? kSegRows : 0x7fffffff;
-    p.status = mx_status();
+    p.expiries = mx_expiries();
     p.wait_limit = mx_wait_limit();
     p.stall = mx_stall();
     if (!q.weights) {

@@ -42,8 +42,8 @@
 // which the MMAs are 300 to 400): what fits in flight counts.  Tiles of 192 rows
 // with five slots take 508 us where 208 with four take 545, 160 with five 538, 144 with
 // six 532 and 128 with six 558 (with five 599).
-// Every mbarrier wait is bounded: on expiry the kernel records
-// QBMOE_ETIMEOUT, stops, lets its own copies and MMAs finish and frees TMEM.
+// Every mbarrier wait is bounded: on expiry the kernel counts it
+// (mx_expiries), stops, lets its own copies and MMAs finish and frees TMEM.
 #include "mxfp4.cuh"
 #include "tc_ptx.cuh"
 
@@ -76,7 +76,7 @@ struct Params {
     int sf_tma;                              // scale groups by TMA
     int sf_bytes;                            // else bytes of a scale load: 8 (K % 256 == 0), 4 (K % 128 == 0) or 1
     int weights_ready;                       // nothing enqueued just before this kernel wrote the weights or the offsets
-    int* status;
+    int* expiries;
     long long wait_limit;
     int stall;                               // test hook: withhold the first accumulator hand-off
 };
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
     w.start(gr, p.E, p.m_total);
     const int first = blockIdx.x, step = gridDim.x;
     auto expired = [&] {
-        set_status(p.status, QBMOE_ETIMEOUT);
+        if (p.expiries) atomicAdd(p.expiries, 1);
         *abort_flag = 1;
     };
 
@@ -499,8 +499,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
 }
 
 constexpr int kMaxDevices = 64;
-__device__ int g_status;
-int* g_status_ptr[kMaxDevices] = {};
+__device__ int g_expiries;
+int* g_expiries_ptr[kMaxDevices] = {};
 int g_sms[kMaxDevices] = {};
 long long g_wait_limit = 0;
 int g_stall = 0;
@@ -561,29 +561,34 @@ int mx_product_init() {
     const int dev = current_device();
     if (dev < 0) return QBMOE_ECUDA;
     void* f = nullptr;
-    int rc = cuda_err(cudaGetSymbolAddress(&f, g_status));
+    int rc = cuda_err(cudaGetSymbolAddress(&f, g_expiries));
     if (!rc) rc = cuda_err(cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev));
     if (!rc) rc = set_attributes<16>();
     if (!rc) rc = set_attributes<64>();
     if (!rc) rc = set_attributes<128>();
     if (!rc) rc = set_attributes<192>();
     if (!rc) rc = set_attributes<208>();
-    if (!rc) g_status_ptr[dev] = static_cast<int*>(f);
+    if (!rc) g_expiries_ptr[dev] = static_cast<int*>(f);
     return rc;
 }
 
-int* mx_status() {
+int* mx_expiries() {
     const int dev = current_device();
-    return dev < 0 ? nullptr : g_status_ptr[dev];
+    return dev < 0 ? nullptr : g_expiries_ptr[dev];
 }
-int mx_status_take(cudaStream_t s) {
-    int* p = mx_status();
+int mx_new_expiries(cudaStream_t s) {
+    int* p = mx_expiries();
     if (!p) return QBMOE_OK;   // no call has run on this device
+    // how often a wait had expired when this thread last asked; the count is never
+    // reset, so that no thread takes another's answer
+    thread_local int t_seen[kMaxDevices] = {};
     int v = 0;
     if (cudaMemcpyAsync(&v, p, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess) return QBMOE_ECUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return QBMOE_ECUDA;
-    if (v != 0 && cudaMemsetAsync(p, 0, 4, s) != cudaSuccess) return QBMOE_ECUDA;
-    return v;
+    int& seen = t_seen[current_device()];
+    const int rc = v == seen ? QBMOE_OK : QBMOE_ETIMEOUT;
+    seen = v;
+    return rc;
 }
 long long mx_wait_limit() { return g_wait_limit; }
 void mx_set_wait_limit(long long polls) { g_wait_limit = polls > 0 ? polls : 0; }
@@ -628,7 +633,7 @@ int mx_product(const MxProduct& q, cudaStream_t s) {
     p.m_total = (q.N + 127) / 128;
     p.sf_bytes = q.K % 256 == 0 ? 8 : q.K % 128 == 0 ? 4 : 1;
     p.weights_ready = q.raw != nullptr;
-    p.status = mx_status();
+    p.expiries = mx_expiries();
     p.wait_limit = g_wait_limit;
     p.stall = g_stall;
     // Row tile: the smallest that holds an average expert's rows, 192 beyond. One

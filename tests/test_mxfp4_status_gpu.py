@@ -1,8 +1,17 @@
-"""Status of the calls that take no context."""
+"""Status of the calls that take no context, from two host threads and streams."""
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def other():
+    """Runs a function in a second thread, always the same one."""
+    with ThreadPoolExecutor(max_workers=1) as pool:
+        yield lambda f: pool.submit(f).result()
 
 
 @pytest.fixture
@@ -12,6 +21,32 @@ def product():
     x, w = (Q.mxfp4_quantize(torch.randn(r, 256, generator=g, device="cuda")) for r in (40, 128))
     torch.cuda.synchronize()
     return lambda: Q.mxfp4_matmul(x, w)
+
+
+@pytest.fixture
+def hooks():
+    """Sets (wait limit, stall); both are put back afterwards."""
+    import quantile_balanced_routing_gb300 as Q
+    lib = Q.load_library()
+
+    def arm(limit, stall):
+        assert lib.qbmoe_set_wait_limit(None, limit) == 0 and lib.qbmoe_debug_stall(None, stall) == 0
+    yield arm
+    arm(0, 0)
+
+
+def test_one_thread_does_not_take_the_timeout_of_another(other, product, hooks):
+    import quantile_balanced_routing_gb300 as Q
+    ask = lambda: Q.qbmoe_status(None, None)  # noqa: E731
+    product()
+    ask(), other(ask)                    # what earlier tests left
+    hooks(200, 1)
+    product()
+    hooks(0, 0)
+    torch.cuda.synchronize()
+    assert other(ask) == Q.QBMOE_ETIMEOUT
+    assert ask() == Q.QBMOE_ETIMEOUT
+    assert ask() == 0 and other(ask) == 0
 
 
 def test_status_of_a_stream_does_not_wait_for_others(product):
