@@ -481,7 +481,7 @@ int qbmoe_route_last_launch_count(void);
 
 /* Test hook: cap on bounded device waits, in polls of at most 20 us each
  * (<= 0 restores the default of 2^17).  Applies to launches made after the
- * call.  ctx NULL: the moe_mxfp4_* calls. */
+ * call.  ctx NULL: the moe_mxfp4_* calls of the calling host thread. */
 int qbmoe_set_wait_limit(qbmoe_ctx* ctx, long long iterations);
 
 /* Test hook: while enabled, the tensor-core GEMM kernels withhold their first
@@ -489,7 +489,7 @@ int qbmoe_set_wait_limit(qbmoe_ctx* ctx, long long iterations);
  * qbmoe_status reports QBMOE_ETIMEOUT (outputs undefined).  The kernels then
  * drain their own copies and MMAs, free TMEM and return; the context stays
  * usable.  No effect when the layer runs on CUDA cores.  ctx NULL: the
- * moe_mxfp4_* products. */
+ * moe_mxfp4_* products that the calling host thread makes. */
 int qbmoe_debug_stall(qbmoe_ctx* ctx, int enable);
 
 /* 1 when the context's bf16 GEMMs run on the tcgen05 tensor-core kernels, 0

@@ -16,7 +16,8 @@ int mx_grad_init();      // mxfp4_grad.cu
 // (QBMOE_OK or QBMOE_ETIMEOUT).
 int* mx_expiries();
 int mx_new_expiries(cudaStream_t s);
-// Test hooks of those calls (qbmoe_set_wait_limit / qbmoe_debug_stall without a context).
+// Test hooks of those calls (qbmoe_set_wait_limit / qbmoe_debug_stall without a
+// context), for the calls that the same host thread makes.
 long long mx_wait_limit();
 void mx_set_wait_limit(long long polls);
 int mx_stall();

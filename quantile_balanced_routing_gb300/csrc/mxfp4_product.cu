@@ -502,8 +502,9 @@ constexpr int kMaxDevices = 64;
 __device__ int g_expiries;
 int* g_expiries_ptr[kMaxDevices] = {};
 int g_sms[kMaxDevices] = {};
-long long g_wait_limit = 0;
-int g_stall = 0;
+// Test hooks: of the thread that sets them, for the calls it makes.
+thread_local long long t_wait_limit = 0;
+thread_local int t_stall = 0;
 
 int current_device() {
     int dev = 0;
@@ -590,10 +591,10 @@ int mx_new_expiries(cudaStream_t s) {
     seen = v;
     return rc;
 }
-long long mx_wait_limit() { return g_wait_limit; }
-void mx_set_wait_limit(long long polls) { g_wait_limit = polls > 0 ? polls : 0; }
-int mx_stall() { return g_stall; }
-void mx_set_stall(int on) { g_stall = on; }
+long long mx_wait_limit() { return t_wait_limit; }
+void mx_set_wait_limit(long long polls) { t_wait_limit = polls > 0 ? polls : 0; }
+int mx_stall() { return t_stall; }
+void mx_set_stall(int on) { t_stall = on; }
 int sm_count() {
     const int dev = current_device();
     return dev < 0 || g_sms[dev] < 1 ? 1 : g_sms[dev];
@@ -634,8 +635,8 @@ int mx_product(const MxProduct& q, cudaStream_t s) {
     p.sf_bytes = q.K % 256 == 0 ? 8 : q.K % 128 == 0 ? 4 : 1;
     p.weights_ready = q.raw != nullptr;
     p.expiries = mx_expiries();
-    p.wait_limit = g_wait_limit;
-    p.stall = g_stall;
+    p.wait_limit = t_wait_limit;
+    p.stall = t_stall;
     // Row tile: the smallest that holds an average expert's rows, 192 beyond. One
     // matrix whose tiles of 208 rows save over a quarter of the grid's rounds takes those (by
     // 3584 x 7168, 1040 rows, one round or two: 23.2 against 27.3 us; 1999 rows, two

@@ -1,4 +1,4 @@
-"""Status of the calls that take no context, from two host threads and streams."""
+"""Status and test hooks of the calls that take no context, from two host threads and streams."""
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -25,7 +25,7 @@ def product():
 
 @pytest.fixture
 def hooks():
-    """Sets (wait limit, stall); both are put back afterwards."""
+    """Sets (wait limit, stall) of the calling thread; this thread's are put back afterwards."""
     import quantile_balanced_routing_gb300 as Q
     lib = Q.load_library()
 
@@ -47,6 +47,17 @@ def test_one_thread_does_not_take_the_timeout_of_another(other, product, hooks):
     assert other(ask) == Q.QBMOE_ETIMEOUT
     assert ask() == Q.QBMOE_ETIMEOUT
     assert ask() == 0 and other(ask) == 0
+
+
+def test_hooks_are_those_of_the_thread_that_sets_them(other, product, hooks):
+    import quantile_balanced_routing_gb300 as Q
+    ask = lambda: Q.qbmoe_status(None, None)  # noqa: E731
+    want = product()
+    ask(), other(ask)
+    hooks(200, 1)
+    got = other(product)
+    assert ask() == 0 and other(ask) == 0
+    assert torch.equal(got, want)
 
 
 def test_status_of_a_stream_does_not_wait_for_others(product):
