@@ -387,6 +387,10 @@ class LatentMoE:
         return out
 
     def status(self, stream=None) -> int:
+        if not self.ctx:                 # closed: nothing of its own is left to report
+            import torch
+            (stream or torch.cuda.current_stream()).synchronize()
+            return QBMOE_OK
         return self.lib.qbmoe_status(self.ctx, _stream_ptr(stream))
 
     def set_timing(self, slots: int):
@@ -405,10 +409,10 @@ class LatentMoE:
         return self.lib.qbmoe_last_launch_count(self.ctx)
 
     def set_wait_limit(self, iterations: int):
-        return self.lib.qbmoe_set_wait_limit(self.ctx, iterations)
+        return self.lib.qbmoe_set_wait_limit(self.ctx, iterations) if self.ctx else QBMOE_EINVAL
 
     def debug_stall(self, on: bool):
-        return self.lib.qbmoe_debug_stall(self.ctx, int(on))
+        return self.lib.qbmoe_debug_stall(self.ctx, int(on)) if self.ctx else QBMOE_EINVAL
 
     @property
     def uses_tensor_cores(self) -> bool:

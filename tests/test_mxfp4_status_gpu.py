@@ -74,3 +74,16 @@ def test_status_of_a_stream_does_not_wait_for_others(product):
     assert Q.qbmoe_status(None, s.cuda_stream) == 0
     assert not done.query()
     torch.cuda.synchronize()
+
+
+def test_a_closed_layer_has_no_part_in_it(product, hooks):
+    import quantile_balanced_routing_gb300 as Q
+    lay = Q.LatentMoE(512, 512, 16, 2, 512, 0, max_tokens=32)
+    lay.close()
+    product()
+    Q.qbmoe_status(None, None)
+    hooks(200, 1)
+    product()
+    hooks(0, 0)
+    assert lay.status() == 0
+    assert Q.qbmoe_status(None, None) == Q.QBMOE_ETIMEOUT
