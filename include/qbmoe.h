@@ -59,6 +59,9 @@ enum { QBMOE_QB_JACOBI = 0, QBMOE_QB_GAUSS_SEIDEL = 1 };
 /* Limits of this build. */
 #define QBMOE_MAX_EXPERTS 1024
 #define QBMOE_MAX_TOPK 32
+/* Tokens, sequences or rows of a router-training or MXFP4 product call: 2^31 - 2^24, so
+ * that sizes rounded up to tiles, and row and tile counts added, stay in 32 bits. */
+#define QBMOE_MAX_ROWS 2130706432
 
 /*
  * Scores.  s = sigmoid(logit) is an exactly specified fp32 result: clamp the
@@ -270,8 +273,8 @@ int moe_route_qb_noalloc(int T, int n, int k, int qb_sweeps,
  * or all three NULL.  Padding tokens, and logits outside [-80, 80], get 0.
  * dlogits may equal logits (same stride).
  *
- * 1 <= T, 2 <= n <= QBMOE_MAX_EXPERTS, 1 <= k <= min(n, QBMOE_MAX_TOPK),
- * 1 <= S.  Device pointers are aligned to their element type only: rows of a
+ * 1 <= T <= QBMOE_MAX_ROWS, 2 <= n <= QBMOE_MAX_EXPERTS, 1 <= k <= min(n, QBMOE_MAX_TOPK),
+ * 1 <= S <= QBMOE_MAX_ROWS.  Device pointers are aligned to their element type only: rows of a
  * 16-byte-aligned base and stride are read as vectors.
  */
 size_t qbmoe_balance_workspace_bytes(int T, int n, int S);
@@ -300,12 +303,13 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  * holds an infinity or a NaN gets the scale byte 0xFF (NaN) and zero codes.
  * values (NULL if not wanted): [rows, K] contiguous, of x's type, what the codes
  * stand for, exact in either type (NaN throughout a 0xFF block).
- * x, codes and values 16-byte aligned, ldx * element size a multiple of 16.
+ * x, codes and values 16-byte aligned, ldx * element size a multiple of 16, rows * K at
+ * most 2^40.
  *
  * Grouped rows: R rows in expert order, offsets [E + 1] int32 device,
  * non-decreasing from 0 to R: rows offsets[e] .. offsets[e+1] - 1 belong to
  * expert e (an expert may have none).  offsets NULL: E = 1, all rows.
- * Rows that no expert owns are not written.  0 <= R, 1 <= E <=
+ * Rows that no expert owns are not written.  0 <= R <= QBMOE_MAX_ROWS, 1 <= E <=
  * QBMOE_MAX_EXPERTS, N a multiple of 8.
  *
  * moe_mxfp4_matmul:  y[r][f] = sum_k x[r][k] w[e(r)][f][k], x and w MXFP4

@@ -28,6 +28,7 @@ QBMOE_F32, QBMOE_BF16, QBMOE_MXFP4 = 0, 1, 2
 QBMOE_W_F32, QBMOE_W_BF16, QBMOE_W_MXFP4 = 0, 1, 2
 QBMOE_QB_JACOBI, QBMOE_QB_GAUSS_SEIDEL = 0, 1
 MAX_EXPERTS, MAX_TOPK = 1024, 32
+MAX_ROWS = (1 << 31) - (1 << 24)
 
 
 class QbmoeConfig(ctypes.Structure):

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 from typing import NamedTuple
 
-from . import MAX_EXPERTS, MAX_TOPK, QBMOE_BF16, QBMOE_F32, QbmoeError, _here, _p, _refuse, load_library
+from . import MAX_EXPERTS, MAX_ROWS, MAX_TOPK, QBMOE_BF16, QBMOE_F32, QbmoeError, _here, _p, _refuse, load_library
 
 
 class BalanceLoss(NamedTuple):
@@ -35,8 +35,8 @@ def _router_args(what, logits, idx, seq_offsets, token_mask):
     if logits.dim() != 2 or (logits.dtype is not torch.float32 and logits.dtype is not torch.bfloat16):
         _refuse(what, "logits are fp32 or bf16 [T, n]")
     T, n = logits.shape
-    if T < 1 or n < 2 or n > MAX_EXPERTS:
-        _refuse(what, f"T >= 1 and 2 <= n <= {MAX_EXPERTS}")
+    if T < 1 or T > MAX_ROWS or n < 2 or n > MAX_EXPERTS:
+        _refuse(what, f"1 to at most {MAX_ROWS} tokens and 2 <= n <= {MAX_EXPERTS}")
     ld = _row_stride(what, "logits", logits, n)
     if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != T or not idx.is_contiguous():
         _refuse(what, "idx is contiguous int32 [T, k]")
@@ -49,6 +49,8 @@ def _router_args(what, logits, idx, seq_offsets, token_mask):
                 not seq_offsets.is_contiguous():
             _refuse(what, "seq_offsets is contiguous int32 [S + 1]")
         S = seq_offsets.shape[0] - 1
+        if S > MAX_ROWS:
+            _refuse(what, f"at most {MAX_ROWS} sequences")
     if token_mask is not None and (
             (token_mask.dtype is not torch.bool and token_mask.dtype is not torch.uint8) or token_mask.dim() != 1 or
             token_mask.shape[0] != T or not token_mask.is_contiguous()):

@@ -444,7 +444,7 @@ BalanceLayout balance_layout(int T, int n, int S) {
 }
 
 bool router_sizes_ok(int T, int n, int k, int S, int dtype, long long ld) {
-    return T >= 1 && n >= 2 && n <= QBMOE_MAX_EXPERTS && k >= 1 && k <= n && k <= QBMOE_MAX_TOPK && S >= 1 &&
+    return T >= 1 && T <= QBMOE_MAX_ROWS && n >= 2 && n <= QBMOE_MAX_EXPERTS && k >= 1 && k <= n && k <= QBMOE_MAX_TOPK && S >= 1 &&
            S <= 65535 && (dtype == QBMOE_F32 || dtype == QBMOE_BF16) && ld >= n;
 }
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -467,7 +467,7 @@ int qbh::balance_init() {
 }
 
 extern "C" size_t qbmoe_balance_workspace_bytes(int T, int n, int S) {
-    if (T < 1 || n < 2 || n > QBMOE_MAX_EXPERTS || S < 1 || S > 65535) return 0;
+    if (T < 1 || T > QBMOE_MAX_ROWS || n < 2 || n > QBMOE_MAX_EXPERTS || S < 1 || S > 65535) return 0;
     return balance_layout(T, n, S).total;
 }
 

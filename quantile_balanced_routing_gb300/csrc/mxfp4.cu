@@ -164,7 +164,7 @@ constexpr int kMaxK = 1 << 24;
 constexpr long long kMaxStride = 1LL << 27;
 
 bool product_sizes_ok(int R, int E, int N, int K, const int32_t* offsets) {
-    return R >= 0 && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && N <= kMaxK && K >= 32 &&
+    return R >= 0 && R <= QBMOE_MAX_ROWS && E >= 1 && E <= QBMOE_MAX_EXPERTS && N >= 8 && N % 8 == 0 && N <= kMaxK && K >= 32 &&
            K % 32 == 0 && K <= kMaxK && (long long)E * N <= 0x7fffffffLL && (offsets || E == 1);
 }
 bool stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= kMaxStride; }
@@ -204,7 +204,7 @@ extern "C" int moe_mxfp4_quantize(long long rows, int K, int x_type, const void*
 }
 
 extern "C" size_t qbmoe_mxfp4_workspace_bytes(int R, int K) {
-    if (R < 0 || K < 32 || K % 32 || K > kMaxK) return 0;
+    if (R < 0 || R > QBMOE_MAX_ROWS || K < 32 || K % 32 || K > kMaxK) return 0;
     // codes and scales of rows that come in another type
     return 256 + qbh::align_up((size_t)R * (K / 2), 256) + qbh::align_up((size_t)R * (K / 32), 256);
 }
@@ -256,7 +256,7 @@ extern "C" int moe_mxfp4_dgrad(int R, int E, int N, int K, const void* dy, long 
 }
 
 extern "C" size_t qbmoe_mxfp4_wgrad_workspace_bytes(int R, int E, int N, int K) {
-    if (R < 0 || E < 1 || E > QBMOE_MAX_EXPERTS || N < 8 || N % 8 || N > kMaxK || K < 32 || K % 32 || K > kMaxK)
+    if (R < 0 || R > QBMOE_MAX_ROWS || E < 1 || E > QBMOE_MAX_EXPERTS || N < 8 || N % 8 || N > kMaxK || K < 32 || K % 32 || K > kMaxK)
         return 0;
     const int splits = qbh::mx_wgrad_splits(R, E, N, K);
     return splits > 1 ? (size_t)splits * E * N * K * 4 : 0;

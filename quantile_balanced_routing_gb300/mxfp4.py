@@ -6,9 +6,10 @@ and scales are the layout :class:`LatentMoE` takes for MXFP4 experts.
 """
 from __future__ import annotations
 
-from . import MAX_EXPERTS, QBMOE_BF16, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _here, _p, _refuse, load_library
+from . import MAX_EXPERTS, MAX_ROWS, QBMOE_BF16, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _here, _p, _refuse, load_library
 
 BLOCK = 32
+_MAX_COLS, _MAX_ELEMENTS = 1 << 24, 1 << 40
 
 
 class Mxfp4:
@@ -68,8 +69,10 @@ def mxfp4_quantize(x, values=False, stream=None):
     if (not f32 and x.dtype is not torch.bfloat16) or x.dim() < 1:
         _refuse(what, "x is fp32 or bf16 [..., K]")
     K = x.shape[-1]
-    if K == 0 or K % BLOCK:
-        _refuse(what, f"K is a multiple of {BLOCK}")
+    if K == 0 or K % BLOCK or K > 0x7fffffff:
+        _refuse(what, f"K is a multiple of {BLOCK}, at most 2^31 - 1")
+    if x.numel() > _MAX_ELEMENTS:
+        _refuse(what, "x has at most 2^40 elements")
     if x.dim() == 2:
         ld, lead, rows = _row_stride(what, "x", x, 4 if f32 else 8), (x.shape[0],), x.shape[0]
     else:
@@ -105,6 +108,8 @@ def _groups(what, w, offsets):
         _refuse(what, f"1 to {MAX_EXPERTS} experts")
     if N == 0 or N % 8:
         _refuse(what, "N is a multiple of 8")
+    if N > _MAX_COLS or K > _MAX_COLS or E * N > 0x7fffffff:
+        _refuse(what, "N and K are at most 2^24, E N at most 2^31 - 1")
     if offsets is not None and (offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or
                                 not offsets.is_contiguous()):
         _refuse(what, "offsets is contiguous int32 [E + 1]")
@@ -133,9 +138,11 @@ def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
             _refuse(what, "x is an Mxfp4, or fp32 or bf16")
     if len(shape) != 2 or shape[1] != K:
         _refuse(what, "x is [R, K] with the K of w")
+    R = shape[0]
+    if R > MAX_ROWS:
+        _refuse(what, f"at most {MAX_ROWS} rows")
     if scales is None:
         ld = _row_stride(what, "x", x, 4 if kind == QBMOE_F32 else 8)
-    R = shape[0]
     cur = _here(what, rows, scales, w.codes, w.scales, offsets)
     lib, dev = load_library(), rows.device
     y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
@@ -168,6 +175,8 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
     if len(shape) != 2 or shape[1] != K:
         _refuse(what, "xq is [R, K] with the K of w")
     R = shape[0]
+    if R > MAX_ROWS:
+        _refuse(what, f"at most {MAX_ROWS} rows")
     if dy.dtype is not torch.bfloat16 or dy.shape != (R, N):
         _refuse(what, "dy is bf16 [R, N]")
     ld = _row_stride(what, "dy", dy, 8)
