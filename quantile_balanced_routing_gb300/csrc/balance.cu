@@ -79,7 +79,7 @@ QB_DEV float warp_sum(float v) {
 QB_DEV int find_seq(const int32_t* off, int S, int t) {
     int lo = 0, hi = S;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);
         if (__ldg(off + mid) <= t) lo = mid; else hi = mid;
     }
     return lo;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kBalThreads, 3) k_balance_partial(const Balanc
     }
 }
 
-// CTA (b, q): experts 32 b .. 32 b + 31 of sequence q over its slots; the
+// CTA (q, b): experts 32 b .. 32 b + 31 of sequence q over its slots; the
 // sequence's last CTA adds up its loss.
 __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArgs a) {
     __shared__ float sp[kBalWarps][33];
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
     __shared__ int st[kBalWarps];
     __shared__ bool last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int q = blockIdx.y, j = blockIdx.x * 32 + lane;
+    const int q = blockIdx.x, j = blockIdx.y * 32 + lane;
     pdl_wait();
     const int o0 = a.seq ? min(max(__ldg(a.seq + q), 0), a.T) : 0;
     const int o1 = a.seq ? min(max(__ldg(a.seq + q + 1), o0), a.T) : a.T;
@@ -223,16 +223,16 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
         }
         const float l = warp_sum(j < a.n ? (float)c * p : 0.0f) * ((float)a.n * inv_t / (float)a.k);
         if (lane == 0) {
-            if (blockIdx.x == 0) a.tokens[q] = t;
-            a.loss_part[(long long)q * gridDim.x + blockIdx.x] = l;
+            if (blockIdx.y == 0) a.tokens[q] = t;
+            a.loss_part[(long long)q * gridDim.y + blockIdx.y] = l;
             __threadfence();
-            last = atomicAdd(a.ticket + q, 1u) == gridDim.x - 1;
+            last = atomicAdd(a.ticket + q, 1u) == gridDim.y - 1;
         }
         __syncwarp();
         if (last) {
             __threadfence();
-            const float v = lane < (int)gridDim.x
-                                ? *(volatile float*)(a.loss_part + (long long)q * gridDim.x + lane) : 0.0f;
+            const float v = lane < (int)gridDim.y
+                                ? *(volatile float*)(a.loss_part + (long long)q * gridDim.y + lane) : 0.0f;
             const float total = warp_sum(v);   // at most 32 CTAs a sequence
             if (lane == 0) a.loss[q] = total;
         }
@@ -445,7 +445,7 @@ BalanceLayout balance_layout(int T, int n, int S) {
 
 bool router_sizes_ok(int T, int n, int k, int S, int dtype, long long ld) {
     return T >= 1 && T <= QBMOE_MAX_ROWS && n >= 2 && n <= QBMOE_MAX_EXPERTS && k >= 1 && k <= n && k <= QBMOE_MAX_TOPK && S >= 1 &&
-           S <= 65535 && (dtype == QBMOE_F32 || dtype == QBMOE_BF16) && ld >= n;
+           S <= QBMOE_MAX_ROWS && (dtype == QBMOE_F32 || dtype == QBMOE_BF16) && ld >= n;
 }
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -467,7 +467,7 @@ int qbh::balance_init() {
 }
 
 extern "C" size_t qbmoe_balance_workspace_bytes(int T, int n, int S) {
-    if (T < 1 || T > QBMOE_MAX_ROWS || n < 2 || n > QBMOE_MAX_EXPERTS || S < 1 || S > 65535) return 0;
+    if (T < 1 || T > QBMOE_MAX_ROWS || n < 2 || n > QBMOE_MAX_EXPERTS || S < 1 || S > QBMOE_MAX_ROWS) return 0;
     return balance_layout(T, n, S).total;
 }
 
@@ -511,7 +511,7 @@ extern "C" int moe_balance_loss(int T, int n, int k, int S, int logit_dtype, con
         else k_balance_partial<__nv_bfloat16, 1><<<a.nchunk, kBalThreads, smem, s>>>(a);
     }
     if ((rc = qbh::cuda_err(cudaGetLastError()))) return rc;
-    return qbh::launch_pdl(k_balance_finish, dim3((n + 31) / 32, S), dim3(kBalThreads), 0, s, a);
+    return qbh::launch_pdl(k_balance_finish, dim3(S, (n + 31) / 32), dim3(kBalThreads), 0, s, a);
 }
 
 extern "C" int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void* logits, long long ld,

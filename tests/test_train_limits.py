@@ -73,3 +73,9 @@ def test_python_refuses_sizes_that_c_cannot_hold():
         with pytest.raises(Q.QbmoeError, match="at most") as e:
             call()
         assert e.value.code == Q.QBMOE_EINVAL
+
+
+def test_any_number_of_sequences_up_to_the_limit_has_a_workspace():
+    lib = Q.load_library()
+    for S in (65535, 65536, 1 << 20, MOST):
+        assert lib.qbmoe_balance_workspace_bytes(8, 2, S) > 16 * S
