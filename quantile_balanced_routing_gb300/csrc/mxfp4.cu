@@ -269,11 +269,11 @@ extern "C" int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long 
     if (dw_dtype != QBMOE_F32 && dw_dtype != QBMOE_BF16) return QBMOE_EINVAL;
     if (!dw || !qbh::aligned16(dw) || !qbh::aligned16(offsets)) return QBMOE_EINVAL;
     if (R > 0 && !all_aligned16(static_cast<const uint8_t*>(dy), x_codes, x_scales)) return QBMOE_EINVAL;
-    const int rc = qbh::device_init();
-    if (rc) return rc;
     const size_t need = qbmoe_mxfp4_wgrad_workspace_bytes(R, E, N, K);
     if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)) return QBMOE_EINVAL;
     if (workspace_bytes < need) return QBMOE_EWORKSPACE;
+    const int rc = qbh::device_init();
+    if (rc) return rc;
     qbh::MxGrad g{};
     g.weights = true;
     g.parts = need ? workspace : nullptr;

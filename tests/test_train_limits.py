@@ -79,3 +79,15 @@ def test_any_number_of_sequences_up_to_the_limit_has_a_workspace():
     lib = Q.load_library()
     for S in (65535, 65536, 1 << 20, MOST):
         assert lib.qbmoe_balance_workspace_bytes(8, 2, S) > 16 * S
+
+
+def test_weight_gradient_refuses_its_workspace_on_the_host():
+    """One small matrix over many rows needs a workspace; a wrong one is refused before any device is touched."""
+    lib = Q.load_library()
+    need = lib.qbmoe_mxfp4_wgrad_workspace_bytes(40000, 1, 264, 544)
+    call = lambda ws, size: lib.moe_mxfp4_wgrad(40000, 1, 264, 544, FAKE, 264, FAKE, FAKE, None, 0, FAKE, ws, size,  # noqa: E731
+                                                None)
+    assert need > 0
+    assert call(None, need) == Q.QBMOE_EINVAL
+    assert call(FAKE + 8, need) == Q.QBMOE_EINVAL
+    assert call(FAKE, need - 1) == Q.QBMOE_EWORKSPACE
