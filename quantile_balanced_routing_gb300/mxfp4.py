@@ -9,14 +9,15 @@ from __future__ import annotations
 from . import MAX_EXPERTS, MAX_ROWS, QBMOE_BF16, QBMOE_F32, QBMOE_MXFP4, QbmoeError, _here, _p, _refuse, load_library
 
 BLOCK = 32
-_MAX_COLS, _MAX_ELEMENTS = 1 << 24, 1 << 40
+_MAX_COLS, _MAX_STRIDE, _MAX_ELEMENTS = 1 << 24, 1 << 27, 1 << 40
 
 
 class Mxfp4:
     """An MXFP4 tensor [..., K]: ``codes`` uint8 [..., K / 2], two E2M1 codes a
     byte (element 2i in the low nibble), and ``scales`` uint8 [..., K / 32], one
     E8M0 byte per 32 elements.  Checked when it is made, so that the calls that
-    take it need not."""
+    take it need not.  The tensors may be slices of larger ones; codes start on a
+    16-byte boundary, as any row does, and scales that do not are copied by the calls."""
     __slots__ = ("codes", "scales", "shape")
 
     def __init__(self, codes, scales):
@@ -53,6 +54,19 @@ def _row_stride(what, name, t, align):
     return ld
 
 
+def _start(what, name, t):
+    """The address of a tensor that is read in 16-byte pieces."""
+    p = t.data_ptr()
+    if p & 15:
+        _refuse(what, f"{name} starts on a 16-byte boundary")
+    return p
+
+
+def _small(t):
+    """Scales or offsets that start on a 16-byte boundary: a copy of a slice that does not."""
+    return t if t is None or not t.data_ptr() & 15 else t.clone()
+
+
 def mxfp4_quantize(x, values=False, stream=None):
     """MXFP4 form of x [..., K] (fp32 or bf16), K a multiple of 32.
 
@@ -79,12 +93,13 @@ def mxfp4_quantize(x, values=False, stream=None):
         if not x.is_contiguous():
             _refuse(what, "x is contiguous, or a matrix with contiguous rows")
         ld, lead, rows = K, tuple(x.shape[:-1]), x.numel() // K
+    at = _start(what, "x", x)
     cur = _here(what, x)
     dev, empty = x.device, torch.empty
     codes = empty((*lead, K // 2), dtype=torch.uint8, device=dev)
     scales = empty((*lead, K // BLOCK), dtype=torch.uint8, device=dev)
     v = empty(x.shape, dtype=x.dtype, device=dev) if values else None
-    rc = load_library().moe_mxfp4_quantize(rows, K, QBMOE_F32 if f32 else QBMOE_BF16, x.data_ptr(), ld,
+    rc = load_library().moe_mxfp4_quantize(rows, K, QBMOE_F32 if f32 else QBMOE_BF16, at, ld,
                                            codes.data_ptr(), scales.data_ptr(), _p(v), cur)
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_quantize")
@@ -143,15 +158,17 @@ def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
         _refuse(what, f"at most {MAX_ROWS} rows")
     if scales is None:
         ld = _row_stride(what, "x", x, 4 if kind == QBMOE_F32 else 8)
+    x_at, w_at = _start(what, "x", rows), _start(what, "w", w.codes)
     cur = _here(what, rows, scales, w.codes, w.scales, offsets)
     lib, dev = load_library(), rows.device
+    scales, w_scales, offsets = _small(scales), _small(w.scales), _small(offsets)
     y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
     ws, nbytes = None, 0
     if scales is None:
         nbytes = lib.qbmoe_mxfp4_workspace_bytes(R, K)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    rc = lib.moe_mxfp4_matmul(R, E, N, K, kind, rows.data_ptr(), ld, _p(scales), w.codes.data_ptr(),
-                              w.scales.data_ptr(), _p(offsets), y.data_ptr(), N, _p(ws), nbytes, cur)
+    rc = lib.moe_mxfp4_matmul(R, E, N, K, kind, x_at, ld, _p(scales), w_at, w_scales.data_ptr(), _p(offsets),
+                              y.data_ptr(), N, _p(ws), nbytes, cur)
     if rc:
         raise QbmoeError(rc, "moe_mxfp4_matmul")
     return y
@@ -180,24 +197,28 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
     if dy.dtype is not torch.bfloat16 or dy.shape != (R, N):
         _refuse(what, "dy is bf16 [R, N]")
     ld = _row_stride(what, "dy", dy, 8)
+    if ld > _MAX_STRIDE:
+        _refuse(what, "dy's rows are at most 2^27 elements apart")
     f32 = dw_dtype is None or dw_dtype is torch.float32
     if not f32 and dw_dtype is not torch.bfloat16:
         _refuse(what, "dw is fp32 or bf16")
+    dy_at, x_at, w_at = _start(what, "dy", dy), _start(what, "xq", xq.codes), _start(what, "w", w.codes)
     cur = _here(what, dy, xq.codes, xq.scales, w.codes, w.scales, offsets)
-    lib, dev, dx, dw = load_library(), dy.device, None, None
+    lib, dev, dx, dw, offsets = load_library(), dy.device, None, None, _small(offsets)
     if need_dx:
+        w_scales = _small(w.scales)
         dx = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
-        rc = lib.moe_mxfp4_dgrad(R, E, N, K, dy.data_ptr(), ld, w.codes.data_ptr(), w.scales.data_ptr(), _p(offsets),
-                                 dx.data_ptr(), K, cur)
+        rc = lib.moe_mxfp4_dgrad(R, E, N, K, dy_at, ld, w_at, w_scales.data_ptr(), _p(offsets), dx.data_ptr(), K, cur)
         if rc:
             raise QbmoeError(rc, "moe_mxfp4_dgrad")
     if need_dw:
+        x_scales = _small(xq.scales)
         dw = torch.empty((N, K) if offsets is None else (E, N, K), dtype=torch.float32 if f32 else torch.bfloat16,
                          device=dev)
         nbytes = lib.qbmoe_mxfp4_wgrad_workspace_bytes(R, E, N, K)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        rc = lib.moe_mxfp4_wgrad(R, E, N, K, dy.data_ptr(), ld, xq.codes.data_ptr(), xq.scales.data_ptr(),
-                                 _p(offsets), QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), _p(ws), nbytes, cur)
+        rc = lib.moe_mxfp4_wgrad(R, E, N, K, dy_at, ld, x_at, x_scales.data_ptr(), _p(offsets),
+                                 QBMOE_F32 if f32 else QBMOE_BF16, dw.data_ptr(), _p(ws), nbytes, cur)
         if rc:
             raise QbmoeError(rc, "moe_mxfp4_wgrad")
     return dx, dw

@@ -68,6 +68,8 @@ def test_python_refuses_sizes_that_c_cannot_hold():
         lambda: Q.mxfp4_matmul(new(4, wrap), Q.Mxfp4(u8(8, wrap // 2), u8(8, wrap // 32))),
         lambda: Q.mxfp4_matmul(new(4, 32), Q.Mxfp4(u8(1024, 1 << 22, 16), u8(1024, 1 << 22, 1)), i32(1025)),
         lambda: Q.mxfp4_matmul_backward(new(wrap, 8), Q.Mxfp4(u8(wrap, 16), u8(wrap, 1)), one),
+        lambda: Q.mxfp4_matmul_backward(torch.empty_strided((4, 8), (1 << 28, 1), dtype=torch.bfloat16, device="meta"),
+                                        Q.Mxfp4(u8(4, 16), u8(4, 1)), one),
     ]
     for call in calls:
         with pytest.raises(Q.QbmoeError, match="at most") as e:
@@ -91,3 +93,30 @@ def test_weight_gradient_refuses_its_workspace_on_the_host():
     assert call(None, need) == Q.QBMOE_EINVAL
     assert call(FAKE + 8, need) == Q.QBMOE_EINVAL
     assert call(FAKE, need - 1) == Q.QBMOE_EWORKSPACE
+
+
+def test_python_names_what_is_off_a_16_byte_boundary():
+    def off(dtype, *shape):
+        size = 1
+        for s in shape:
+            size *= s
+        return torch.zeros(size + 1, dtype=dtype)[1:].view(shape)
+
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    w, x = (Q.Mxfp4(torch.zeros(r, 32, dtype=u8), torch.zeros(r, 2, dtype=u8)) for r in (16, 4))
+    bad = Q.Mxfp4(off(u8, 16, 32), w.scales)
+    dy = torch.zeros(4, 16, dtype=bf16)
+    calls = [
+        lambda: Q.mxfp4_quantize(off(bf16, 4, 64)),
+        lambda: Q.mxfp4_quantize(off(f32, 4, 64)),
+        lambda: Q.mxfp4_matmul(off(bf16, 4, 64), w),
+        lambda: Q.mxfp4_matmul(x, bad),
+        lambda: Q.mxfp4_matmul(bad, w),
+        lambda: Q.mxfp4_matmul_backward(off(bf16, 4, 16), x, w),
+        lambda: Q.mxfp4_matmul_backward(dy, x, bad),
+        lambda: Q.mxfp4_matmul_backward(torch.zeros(16, 16, dtype=bf16), bad, w),
+    ]
+    for call in calls:
+        with pytest.raises(Q.QbmoeError, match="16-byte boundary") as e:
+            call()
+        assert e.value.code == Q.QBMOE_EINVAL
