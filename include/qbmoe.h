@@ -328,8 +328,13 @@ int moe_router_backward(int T, int n, int k, int S, int logit_dtype, const void*
  *   unless the matrices are few and small).
  * The gradients are those of the product for the values x and w stand for; a
  * trainer that quantises its own activations and weights passes them straight
- * through the rounding.  Products are exact, sums fp32, each output rounded
- * once.  All pointers 16-byte aligned, strides multiples of 8 elements and at
+ * through the rounding.  A value above bf16's largest (scale bytes 253 and 254 with
+ * codes from 4 or 2 on; the quantiser makes none) counts as infinite in them.
+ * Products are exact.  Sums are the tensor cores' fp32 accumulation, which drops low
+ * bits (7e-6 of the norm over 40000 terms).  An fp32 weight gradient is therefore
+ * accumulated 4096 rows at a time, and the segments, like the parts that a workspace
+ * is for, added in fp32 (2e-7); a bf16 one only where it is cut into parts.
+ * Each output is rounded to its type once.  All pointers 16-byte aligned, strides multiples of 8 elements and at
  * most 2^27, N and K at most 2^24, E N below 2^31.
  * A bounded wait that expires is reported by qbmoe_status(NULL, stream).
  */

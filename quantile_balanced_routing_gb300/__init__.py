@@ -10,6 +10,8 @@ torch conveniences that allocate outputs with torch and call them:
 :func:`route_qb` and :class:`LatentMoE`, the router's training side
 (:func:`balance_loss`, :func:`router_backward`) and MXFP4 tensors
 (:func:`mxfp4_quantize`, :func:`mxfp4_matmul`, :func:`mxfp4_matmul_backward`).
+None of them is recorded by autograd: outputs carry no graph, also of inputs that
+require gradients, and a trainer calls the gradients itself.
 """
 from __future__ import annotations
 

@@ -64,7 +64,8 @@ def balance_loss(logits, idx, seq_offsets=None, token_mask=None, stream=None) ->
     logits [T, n] (fp32 or bf16, pre-sigmoid; rows may be strided), idx [T, k]
     int32 as returned by the router, seq_offsets [S + 1] int32 (None: one
     sequence), token_mask [T] bool, False for padding.  The caller weighs and
-    sums ``loss``; its gradient goes into :func:`router_backward`."""
+    sums ``loss``, which carries no graph; its gradient goes into
+    :func:`router_backward`."""
     import torch
     if stream is not None:   # outputs and scratch are allocated on the stream that uses them
         with torch.cuda.stream(stream):

@@ -90,8 +90,8 @@ QB_DEV int find_seq(const int32_t* off, int S, int t) {
 // in sequence q is summed into slot c + q (along the chunks and sequences that
 // overlap, c + q takes each value once), so no sum needs an atomic and the
 // order is fixed.  Three CTAs a SM is what the 32 running sums and 32 scores a lane
-// leave room for.  16384 x 896 fp32 in 9 sequences: 18 us with the finish kernel
-// (59 MB: 9 us at the copy rate); latency and issue (48%) bound it.
+// leave room for.  16384 x 896 fp32 in 9 sequences: 23 us with the finish kernel
+// (59 MB: 9 us at the copy rate), bf16 32; latency and issue (52%) bound it.
 // ---------------------------------------------------------------------------
 struct BalanceArgs {
     int T, n, k, S, chunk, nchunk;
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 // (a chunk that crosses a boundary goes through its sequences in turn).  A warp
 // has its next row on the way to shared memory (cp.async) while it works on this
 // one, where rows are 16-byte vectors.  The dense row is stored first, then the k
-// chosen entries over it.  16384 x 896 fp32: 22 us (118 MB: 17 us at the copy rate),
-// bound by issue (62%) as much as by memory; keeping more than the slopes in
+// chosen entries over it.  16384 x 896 fp32: 26 us (118 MB: 17 us at the copy rate),
+// bf16 24, bound by issue (61%) as much as by memory; keeping more than the slopes in
 // registers (fewer CTAs a SM, the chosen entries selected in the dense pass) took 83.
 // ---------------------------------------------------------------------------
 struct RouterGradArgs {

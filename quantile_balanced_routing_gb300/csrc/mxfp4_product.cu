@@ -42,6 +42,10 @@
 // which the MMAs are 300 to 400): what fits in flight counts.  Tiles of 192 rows
 // with five slots take 508 us where 208 with four take 545, 160 with five 538, 144 with
 // six 532 and 128 with six 558 (with five 599).
+// Scale rows that TMA cannot copy (K % 512 != 0) cost the loading warp one to sixteen
+// loads a row and group.  16384 rows over 56 experts of 1024 x K: K = 3584 (TMA) 53 us,
+// 3328 (8-byte loads) 65, 3456 (4-byte) 71, 3360 (1-byte) 378; one row by 6144 x K: 15.5,
+// 15.5, 15.5 and 35 us.  The last is bound by those loads alone.
 // Every mbarrier wait is bounded: on expiry the kernel counts it
 // (mx_expiries), stops, lets its own copies and MMAs finish and frees TMEM.
 #include "mxfp4.cuh"

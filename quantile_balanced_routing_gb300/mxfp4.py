@@ -134,7 +134,9 @@ def _groups(what, w, offsets):
 def mxfp4_matmul(x, w: Mxfp4, offsets=None, stream=None):
     """y [R, N] bf16 = x w^T for MXFP4 weights w [N, K].
 
-    x: an :class:`Mxfp4` [R, K], or fp32/bf16 rows, which are quantised first.
+    x: an :class:`Mxfp4` [R, K], or fp32/bf16 rows, which are quantised first: both
+    operands have 4 bits, where :class:`LatentMoE` keeps its activations at bf16
+    precision.  y carries no graph; :func:`mxfp4_matmul_backward` is its gradient.
     Grouped: w [E, N, K] and offsets [E + 1] int32, the rows in expert order;
     rows that no expert owns are left unwritten."""
     import torch
@@ -179,7 +181,8 @@ def mxfp4_matmul_backward(dy, xq: Mxfp4, w: Mxfp4, offsets=None, need_dx=True, n
     """Gradients (dx [R, K] bf16, dw [N, K] or [E, N, K]) of ``mxfp4_matmul(xq, w, offsets)``.
 
     dy [R, N] bf16 (rows may be strided); dw is fp32 unless dw_dtype says
-    bf16, and zero for an expert without rows.  They are the gradients for the
+    bf16, and zero for an expert without rows; dx of rows that no expert owns is left
+    unwritten.  They are the gradients for the
     values that xq and w stand for; a trainer passes them straight through its
     quantisation.  need_dx / need_dw False: None in that place."""
     import torch
