@@ -39,12 +39,14 @@ QB_DEV float score(float x, float& e) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
     return s;
 }
-// s and its derivative s (1 - s) = e s^2, which keeps its relative precision
-// where s rounds to 1 and is 0 where the clamp holds.
+// s and its derivative s (1 - s) = m - m^2 for the smaller m of s and 1 - s = e s: the
+// relative error is that of m (e s^2 would have that of s twice), also where s rounds
+// to 1.  0 where the clamp holds.
 QB_DEV float score_slope(float x, float& slope) {
     float e;
     const float s = score(x, e);
-    slope = fabsf(x) > kLogitLimit ? 0.0f : e * s * s;
+    const float m = fminf(s, e * s);
+    slope = fabsf(x) > kLogitLimit ? 0.0f : fmaf(-m, m, m);
     return s;
 }
 

@@ -115,3 +115,29 @@ def test_gradients_keep_fp32_over_the_whole_range(n):
     want = M.router_grad(xs, idx.numpy(), None, dl, counts, tokens, off.numpy())
     size = slope / s.sum(1, keepdims=True) * (np.abs(dl) * n / 4)[:, None]
     assert (np.abs(g - want) <= 2.0 ** -17 * size).all()
+
+
+@pytest.mark.parametrize("T,n,k", [(2048, 896, 16), (4000, 64, 6)])
+def test_gradients_are_as_near_as_plain_fp32(T, n, k):
+    """The error's norm against the formula is at most a quarter above that of its plain evaluation in 32-bit arithmetic
+    (each share times its complement, p c (f - D) and w c (dw - mean)), which rounds as often."""
+    import quantile_balanced_routing_gb300 as Q
+    g = torch.Generator().manual_seed(n)
+    new = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = new(T, n) + 1.4 * new(n)
+    idx = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :k].to(torch.int32).contiguous()
+    dw, dl = 0.1 * new(T, k), torch.tensor([0.01])
+    r = Q.balance_loss(x.cuda(), idx.cuda())
+    got = Q.router_backward(x.cuda(), idx.cuda(), dw=dw.cuda(), dloss=dl.cuda(), counts=r.counts, tokens=r.tokens)
+
+    def formula(x, dw, f):
+        s, c = 1 / (1 + torch.exp(-x)), 1 / (1 + torch.exp(x))
+        p, i = s / s.sum(1, keepdim=True), idx.long()
+        w = s.gather(1, i)
+        w = w / w.sum(1, keepdim=True)
+        return (p * c * (f - (f * p).sum(1, keepdim=True))).scatter_add(
+            1, i, w * c.gather(1, i) * (dw - (dw * w).sum(1, keepdim=True)))
+    counts = r.counts.cpu()
+    want = formula(x.double(), dw.double(), counts.double() * (dl.double() * n / (k * T * T)))
+    plain = formula(x, dw, counts.float() * (dl * n / (k * T * T)))
+    assert float((got.cpu() - want).norm()) <= 1.25 * float((plain - want).norm())
