@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_finish(const BalanceArg
 // has its next row on the way to shared memory (cp.async) while it works on this
 // one, where rows are 16-byte vectors.  The dense row is stored first, then the k
 // chosen entries over it.  16384 x 896 fp32: 26 us (118 MB: 17 us at the copy rate),
-// bf16 24, bound by issue (61%) as much as by memory; keeping more than the slopes in
+// bf16 24, bound by issue (60%) as much as by memory; keeping more than the slopes in
 // registers (fewer CTAs a SM, the chosen entries selected in the dense pass) took 83.
 // ---------------------------------------------------------------------------
 struct RouterGradArgs {
