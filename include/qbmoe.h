@@ -48,7 +48,8 @@ typedef enum {
 } qbmoe_status_t;
 
 /* Storage types. */
-enum { QBMOE_F32 = 0, QBMOE_BF16 = 1, QBMOE_MXFP4 = 2 /* moe_mxfp4_matmul's rows only */ };
+enum { QBMOE_F32 = 0, QBMOE_BF16 = 1, QBMOE_MXFP4 = 2 /* moe_mxfp4_matmul's rows only */,
+       QBMOE_MXFP8 = 3 /* rows of moe_mxfp4_matvec and moe_mxfp4_experts only */ };
 /* Routed-expert weight formats. */
 enum { QBMOE_W_F32 = 0, QBMOE_W_BF16 = 1, QBMOE_W_MXFP4 = 2 };
 /* QB sweep forms: every expert from the same biases (the default, one
@@ -351,6 +352,100 @@ size_t qbmoe_mxfp4_wgrad_workspace_bytes(int R, int E, int N, int K);
 int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, const uint8_t* x_codes,
                     const uint8_t* x_scales, const int32_t* offsets, int dw_dtype, void* dw,
                     void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The norm in front of a layer: the residual's addition, RMS norm of the sum,
+ * rows in 8 bits, and the gradient.
+ *
+ * An MXFP8 tensor [rows, K] is codes [rows, K] u8 (E4M3) and scales [rows, K/32]
+ * u8 (E8M0: 2^(byte - 127)), both contiguous; K is a multiple of 32.
+ *
+ * moe_add_rmsnorm, per row of H elements:
+ *   total = x + residual, one fp32 sum rounded to the residual's type
+ *   r = 1 / sqrt(sum_j total_j^2 / H + eps),  n_j = (total_j r) gamma_j
+ * x [T, H] of x_type, residual and total [T, H] of res_type (each QBMOE_F32 or
+ * QBMOE_BF16; total may be the residual, or x where types and strides agree).
+ * residual and total NULL: the norm of x itself.  gamma [H] fp32.
+ * codes NULL: y [T, H] of x_type takes n rounded once.  Else codes and scales
+ * take n in MXFP8 (H a multiple of 32): per 32 elements e = floor(log2 max|n|) - 7
+ * (at least -127; -127 for a block of zeros), code = n 2^-e in E4M3, rounded to
+ * nearest, ties to even.  Scaled magnitudes are below 256, so that none saturates.
+ * A block that holds an infinity or a NaN gets the scale byte 0xFF (NaN) and zero
+ * codes.  y, which may then be NULL, takes the values that the codes stand for, in
+ * QBMOE_BF16 (exact down to 2^-133; NaN throughout a 0xFF block).
+ *
+ * moe_add_rmsnorm_backward: for dn, the gradient of n (straight through the
+ * rounding), with total as moe_add_rmsnorm wrote it (x where there is no
+ * residual) and r of it formed anew:
+ *   dx = dtotal + r (g - total r^2 mean_j(g total)),  g = dn gamma
+ *   dgamma_j = sum_t dn total r
+ * dx, of total_type, is the gradient of x and of the residual alike; dtotal, of
+ * total_type, is the total's own gradient (NULL: none).  dn of dn_type.  dx may be dtotal (same
+ * stride), or dn where the types and strides agree.  dgamma [H] fp32, or NULL
+ * (then no workspace is used).
+ * workspace: device, 256-byte aligned, >= qbmoe_add_rmsnorm_workspace_bytes(T, H)
+ * bytes.  Sums are fp32 in a fixed order: bit-reproducible.
+ *
+ * 0 <= T <= QBMOE_MAX_ROWS, 1 <= H <= QBMOE_MAX_NORM, eps >= 0 and finite, row strides (ld*,
+ * in elements) >= H.  Pointers are aligned to their element type only: rows whose bases and strides are
+ * multiples of 16 bytes (and H of 8) are read as vectors.  codes are 8-byte aligned.
+ */
+int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long long ldx, int res_type, const void* residual,
+                    long long ldr, const float* gamma, float eps, void* total, long long ldt, void* y, long long ldy,
+                    uint8_t* codes, uint8_t* scales, qbmoe_stream_t stream);
+size_t qbmoe_add_rmsnorm_workspace_bytes(int T, int H);
+int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long long lddn, int total_type,
+                             const void* total, long long ldt, const float* gamma, float eps, const void* dtotal,
+                             long long lddt, void* dx, long long lddx, float* dgamma, void* workspace,
+                             size_t workspace_bytes, qbmoe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * MXFP4 weights with few rows, and the routed experts of a few tokens.
+ *
+ * moe_mxfp4_matvec: y[r][f] = sum_k x[r][k] w[e(r)][f][k] with rows grouped as
+ *   for moe_mxfp4_matmul (offsets [E + 1] or NULL; rows that no expert owns are not
+ *   written), but x at its own precision: QBMOE_BF16 [R, K], row stride ldx, or
+ *   QBMOE_MXFP8 (x the codes, x_scales the scales, ldx = K).  y [R, N] of y_type
+ *   (QBMOE_BF16 or QBMOE_F32), row stride ldy.  Each expert's weights are read
+ *   once per 8 or 16 of its rows: meant for few rows an expert.
+ *   workspace: device, 256-byte aligned, >= qbmoe_mxfp4_matvec_workspace_bytes(R, N, K)
+ *   bytes (0, and NULL allowed, up to K = 8192).
+ *
+ * moe_mxfp4_experts: for T tokens with the experts idx [T, k] (an entry outside
+ *   [0, E) stands for no route) and weights w [T, k] of moe_route_qb,
+ *     a[t][i] = SiTU-GLU(x[t] w_gate[e]^T, x[t] w_up[e]^T),  e = idx[t][i]
+ *     z[t]    = sum_i w[t][i] a[t][i] w_out[e]^T
+ *     y[t]    = round(z) (gamma NULL), or round((z r) gamma), r = 1 / sqrt(mean z^2 + rms_eps)
+ *   with SiTU-GLU of moe_latent_forward.  x [T, L] as above, w_gate and w_up MXFP4
+ *   [E, M, L], w_out [E, L, M], y [T, L] QBMOE_BF16 (row stride ldy), gamma [L] fp32.
+ *   T k at most QBMOE_MAX_ROUTES.  workspace: device, 256-byte aligned, >=
+ *   qbmoe_mxfp4_experts_workspace_bytes(T, k, L, M) bytes.
+ *
+ * Both multiply exact values: weights as they are; each block of 32 of a bf16 row as
+ * fp16 times a power of two, exact for elements down to 2^-29 of the block's largest and
+ * within 2^-40 of it below.  The SiTU-GLU's fp32 result is rounded to fp16 that way
+ * (2^-12).  Sums are fp32, in an order that does not depend on the other rows: bit-reproducible.
+ * 0 <= R <= QBMOE_MAX_ROWS, 1 <= E <= QBMOE_MAX_EXPERTS, 1 <= k <= QBMOE_MAX_TOPK, N a
+ * multiple of 8, K, L and M multiples of 32 and at most QBMOE_MATVEC_MAX_K, E N below 2^31.  Pointers
+ * 16-byte aligned (idx, w and gamma: 4), ldx a multiple of 8 elements; y aligned to its type.
+ * A bounded wait that expires is reported by qbmoe_status(NULL, stream).
+ */
+#define QBMOE_MAX_NORM 16384
+#define QBMOE_MAX_ROUTES 4096
+#define QBMOE_MATVEC_MAX_K 65536
+size_t qbmoe_mxfp4_matvec_workspace_bytes(int R, int N, int K);
+int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales,
+                     const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets, int y_type, void* y,
+                     long long ldy, void* workspace, size_t workspace_bytes, qbmoe_stream_t stream);
+size_t qbmoe_mxfp4_experts_workspace_bytes(int T, int k, int L, int M);
+int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, const void* x, long long ldx,
+                      const uint8_t* x_scales, const int32_t* idx, const float* w, const uint8_t* gate_codes,
+                      const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales,
+                      const uint8_t* out_codes, const uint8_t* out_scales, float beta1, float beta2,
+                      const float* gamma, float rms_eps, void* y, long long ldy, void* workspace,
+                      size_t workspace_bytes, qbmoe_stream_t stream);
 
 /*
  * ---------------------------------------------------------------------------

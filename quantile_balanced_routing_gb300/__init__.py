@@ -8,8 +8,11 @@ The C entry points are exposed under their C names (``moe_route_qb``,
 ``moe_latent_forward``, ``qbmoe_*``) taking plain integers/pointers, plus
 torch conveniences that allocate outputs with torch and call them:
 :func:`route_qb` and :class:`LatentMoE`, the router's training side
-(:func:`balance_loss`, :func:`router_backward`) and MXFP4 tensors
-(:func:`mxfp4_quantize`, :func:`mxfp4_matmul`, :func:`mxfp4_matmul_backward`).
+(:func:`balance_loss`, :func:`router_backward`), MXFP4 tensors
+(:func:`mxfp4_quantize`, :func:`mxfp4_matmul`, :func:`mxfp4_matmul_backward`), and
+what serves a few tokens: the norm in front of a layer (:func:`add_rmsnorm`,
+:func:`add_rmsnorm_backward`), products of few rows (:func:`mxfp4_matvec`) and
+the routed experts (:func:`mxfp4_experts`).
 None of them is recorded by autograd: outputs carry no graph, also of inputs that
 require gradients, and a trainer calls the gradients itself.
 """
@@ -26,11 +29,12 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "qbmoe.h")
 
 QBMOE_OK, QBMOE_EINVAL, QBMOE_ENOMEM, QBMOE_ECUDA = 0, -1, -2, -3
 QBMOE_EARCH, QBMOE_EWORKSPACE, QBMOE_ETIMEOUT, QBMOE_EDEVICE = -4, -5, -6, -7
-QBMOE_F32, QBMOE_BF16, QBMOE_MXFP4 = 0, 1, 2
+QBMOE_F32, QBMOE_BF16, QBMOE_MXFP4, QBMOE_MXFP8 = 0, 1, 2, 3
 QBMOE_W_F32, QBMOE_W_BF16, QBMOE_W_MXFP4 = 0, 1, 2
 QBMOE_QB_JACOBI, QBMOE_QB_GAUSS_SEIDEL = 0, 1
 MAX_EXPERTS, MAX_TOPK = 1024, 32
 MAX_ROWS = (1 << 31) - (1 << 24)
+MAX_NORM, MAX_ROUTES, MATVEC_MAX_K = 16384, 4096, 65536
 
 
 class QbmoeConfig(ctypes.Structure):
@@ -142,6 +146,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_mxfp4_wgrad.argtypes = [i, i, i, i, vp, ll, vp, vp, vp, i, vp, vp, sz, vp]
     for nm in ("moe_balance_loss", "moe_router_backward", "moe_mxfp4_quantize", "moe_mxfp4_matmul",
                "moe_mxfp4_dgrad", "moe_mxfp4_wgrad"):
+        getattr(lib, nm).restype = i
+    f = ctypes.c_float
+    lib.moe_add_rmsnorm.argtypes = [i, i, i, vp, ll, i, vp, ll, vp, f, vp, ll, vp, ll, vp, vp, vp]
+    lib.qbmoe_add_rmsnorm_workspace_bytes.argtypes = [i, i]
+    lib.qbmoe_add_rmsnorm_workspace_bytes.restype = sz
+    lib.moe_add_rmsnorm_backward.argtypes = [i, i, i, vp, ll, i, vp, ll, vp, f, vp, ll, vp, ll, vp, vp, sz, vp]
+    lib.qbmoe_mxfp4_matvec_workspace_bytes.argtypes = [i, i, i]
+    lib.qbmoe_mxfp4_matvec_workspace_bytes.restype = sz
+    lib.moe_mxfp4_matvec.argtypes = [i, i, i, i, i, vp, ll, vp, vp, vp, vp, i, vp, ll, vp, sz, vp]
+    lib.qbmoe_mxfp4_experts_workspace_bytes.argtypes = [i, i, i, i]
+    lib.qbmoe_mxfp4_experts_workspace_bytes.restype = sz
+    lib.moe_mxfp4_experts.argtypes = [i, i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp, f, f, vp, f, vp, ll,
+                                      vp, sz, vp]
+    for nm in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_mxfp4_matvec", "moe_mxfp4_experts"):
         getattr(lib, nm).restype = i
     lib.qbmoe_strerror.argtypes = [i]
     lib.qbmoe_strerror.restype = ctypes.c_char_p
@@ -424,3 +442,5 @@ class LatentMoE:
 
 from .balance import BalanceLoss, balance_loss, router_backward  # noqa: E402
 from .mxfp4 import Mxfp4, mxfp4_matmul, mxfp4_matmul_backward, mxfp4_quantize  # noqa: E402
+from .rmsnorm import AddRmsNorm, Mxfp8, add_rmsnorm, add_rmsnorm_backward  # noqa: E402
+from .matvec import mxfp4_experts, mxfp4_matvec  # noqa: E402

@@ -1,0 +1,392 @@
+// The norm in front of a layer (C ABI: moe_add_rmsnorm, moe_add_rmsnorm_backward):
+// the residual's addition, the RMS norm of the sum as rows of the input's type or
+// in MXFP8, and the gradients.
+//
+// A row is held in registers between its sum of squares and its outputs, so that each
+// input is read once and each output written once.  A thread's pieces are 8 consecutive
+// elements, kNormItems of them a block's width apart; four neighbouring threads hold a
+// block of 32, whose largest magnitude is two shuffles away.
+#include "common.cuh"
+
+#include <cuda_fp16.h>
+
+#include <math.h>
+#include <type_traits>
+
+namespace {
+
+using namespace qb;
+
+constexpr int kNormItems = 4;            // pieces of 8 elements a thread holds
+constexpr int kNormThreads = 512;        // most threads of a row
+constexpr int kRowWarps = 8;             // rows of a CTA when a warp holds a row
+constexpr int kGainParts = 608;          // most partial sums of the gain's gradient
+
+// 8 elements of a row from element 8 i on, zeros past its end.
+template <typename T, bool kVec>
+QB_DEV void load8(const T* __restrict__ row, int i, int H, float (&v)[8]) {
+    if (kVec && sizeof(T) == 4) {
+        const float4 a = reinterpret_cast<const float4*>(row)[2 * i], b = reinterpret_cast<const float4*>(row)[2 * i + 1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else if (kVec) {
+        const uint4 u = reinterpret_cast<const uint4*>(row)[i];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 8 * i + j < H ? to_f32<T>(row[8 * i + j]) : 0.0f;
+    }
+}
+template <typename T, bool kVec>
+QB_DEV void store8(T* __restrict__ row, int i, int H, const float (&v)[8]) {
+    if (kVec && sizeof(T) == 4) {
+        reinterpret_cast<float4*>(row)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(row)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (kVec) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        reinterpret_cast<uint4*>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (8 * i + j < H) row[8 * i + j] = from_f32<T>(v[j]);
+    }
+}
+
+// Sums of kSums values over the threads of a row, the same bits in each: a warp's by
+// shuffles, then the warps' in order.
+template <int kSums>
+QB_DEV void row_sum(float (&s)[kSums], float* scratch /* [kSums][kNormThreads / 32] */) {
+#pragma unroll
+    for (int q = 0; q < kSums; ++q)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
+    if (blockDim.x == 32) return;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+    __syncthreads();   // the scratch may still be read for the row before
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int q = 0; q < kSums; ++q) scratch[q * (kNormThreads / 32) + warp] = s[q];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSums; ++q) {
+        s[q] = 0.0f;
+        for (int w = 0; w < warps; ++w) s[q] += scratch[q * (kNormThreads / 32) + w];
+    }
+}
+
+// 1 / sqrt of the mean square, correctly rounded operations: once a row.
+QB_DEV float inverse_rms(float squares, int H, float eps) {
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, (float)H), eps)));
+}
+
+struct NormArgs {
+    int T, H;
+    const void* x;
+    long long ldx;
+    const void* residual;
+    long long ldr;
+    const float* gamma;
+    float eps;
+    void* total;
+    long long ldt;
+    void* y;
+    long long ldy;
+    uint8_t *codes, *scales;
+};
+
+// MXFP8 of a block whose 8 elements this thread holds; four neighbouring threads hold it.
+QB_DEV void mxfp8_store(float (&n)[8], uint8_t* codes, uint8_t* scale, float (&values)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(n[j]) & 0x7fffffffu);
+    const uint32_t group = 0xfu << (threadIdx.x & 28);
+    m = max(m, __shfl_xor_sync(group, m, 1));
+    m = max(m, __shfl_xor_sync(group, m, 2));
+    const int e = max((int)(m >> 23) - 127 - 7, -127);   // an exponent field of 0 is below -127
+    const bool bad = m >= 0x7f800000u;
+    const float inv = __int_as_float((127 - e) << 23);   // 2^-e: -127 <= e <= 120 (not used when bad)
+    uint32_t q[2];
+    asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 a, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 b, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 c, %7, %6;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 d, %9, %8;\n\t"
+        "mov.b32 %0, {a, b};\n\tmov.b32 %1, {c, d};\n\t}"
+        : "=r"(q[0]), "=r"(q[1])
+        : "f"(n[0] * inv), "f"(n[1] * inv), "f"(n[2] * inv), "f"(n[3] * inv), "f"(n[4] * inv), "f"(n[5] * inv),
+          "f"(n[6] * inv), "f"(n[7] * inv));
+    if (bad) q[0] = q[1] = 0;
+    *reinterpret_cast<uint2*>(codes) = make_uint2(q[0], q[1]);
+    if ((threadIdx.x & 3) == 0) *scale = (uint8_t)(bad ? 255 : e + 127);
+    const float sc = bad ? __int_as_float(0x7fffffff) : __int_as_float(e > -127 ? (e + 127) << 23 : 0x00400000);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        asm("{\n\t.reg .b16 lo, hi, p;\n\tmov.b32 {lo, hi}, %1;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+            : "=r"(h)
+            : "r"(q[i >> 1] >> (16 * (i & 1))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        values[2 * i] = f.x * sc;
+        values[2 * i + 1] = f.y * sc;
+    }
+}
+
+// One row a CTA of blockDim.x threads, or, with blockDim.x = 32, one a warp.
+template <typename TX, typename TR, bool kVec, bool kQuant>
+__global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) {
+    __shared__ float scratch[kNormThreads / 32];
+    const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;   // whole warps, and only where a warp holds a row
+    const int items = (a.H + 7) >> 3;
+    const TX* x = static_cast<const TX*>(a.x) + t * a.ldx;
+    float v[kNormItems][8];
+#pragma unroll
+    for (int i = 0; i < kNormItems; ++i) {
+        const int at = threadIdx.x + i * blockDim.x;
+        if (at < items) load8<TX, kVec>(x, at, a.H, v[i]);
+    }
+    if (a.residual) {
+        const TR* residual = static_cast<const TR*>(a.residual) + t * a.ldr;
+        TR* total = static_cast<TR*>(a.total) + t * a.ldt;
+        float r[kNormItems][8];
+#pragma unroll
+        for (int i = 0; i < kNormItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at < items) load8<TR, kVec>(residual, at, a.H, r[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kNormItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = to_f32<TR>(from_f32<TR>(v[i][j] + r[i][j]));
+            store8<TR, kVec>(total, at, a.H, v[i]);
+        }
+    }
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < kNormItems; ++i) {
+        if (threadIdx.x + i * blockDim.x >= items) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+    }
+    row_sum<1>(ss, scratch);
+    const float r = inverse_rms(ss[0], a.H, a.eps);
+#pragma unroll
+    for (int i = 0; i < kNormItems; ++i) {
+        const int at = threadIdx.x + i * blockDim.x;
+        if (at >= items) break;
+        float g[8], out[8];
+        load8<float, kVec>(a.gamma, at, a.H, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
+        if (kQuant) {
+            const long long block = t * (items >> 2) + (at >> 2);
+            mxfp8_store(v[i], a.codes + t * a.H + 8 * at, a.scales + block, out);
+            if (a.y) store8<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(a.y) + t * a.ldy, at, a.H, out);
+        } else {
+            store8<TX, kVec>(static_cast<TX*>(a.y) + t * a.ldy, at, a.H, v[i]);
+        }
+    }
+}
+
+struct NormGradArgs {
+    int T, H;
+    const void* dn;
+    long long lddn;
+    const void* total;
+    long long ldt;
+    const float* gamma;
+    float eps;
+    const void* dtotal;
+    long long lddt;
+    void* dx;
+    long long lddx;
+    float* parts;   // [gridDim.x, H] sums of dn total r, or NULL
+};
+
+// Rows blockIdx.x * blockDim.y + threadIdx.y, + gridDim.x * blockDim.y, ...: the sums of
+// squares and of g total are taken together; the gain's gradient adds up in registers.
+template <typename TD, typename TT, bool kVec>
+__global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const NormGradArgs a) {
+    __shared__ float scratch[2 * (kNormThreads / 32)];
+    extern __shared__ float lines[];   // [blockDim.y][H] where a warp holds a row
+    const int items = (a.H + 7) >> 3;
+    float acc[kNormItems][8] = {};
+    for (long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += (long long)gridDim.x * blockDim.y) {
+        float d[kNormItems][8], v[kNormItems][8], s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kNormItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            load8<TD, kVec>(static_cast<const TD*>(a.dn) + t * a.lddn, at, a.H, d[i]);
+            load8<TT, kVec>(static_cast<const TT*>(a.total) + t * a.ldt, at, a.H, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kNormItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            float g[8];
+            load8<float, kVec>(a.gamma, at, a.H, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[0] = fmaf(v[i][j], v[i][j], s[0]), s[1] = fmaf(d[i][j] * g[j], v[i][j], s[1]);
+        }
+        row_sum<2>(s, scratch);
+        const float r = inverse_rms(s[0], a.H, a.eps), c = s[1] / (float)a.H * r * r;
+#pragma unroll
+        for (int i = 0; i < kNormItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            float g[8], o[8] = {};
+            load8<float, kVec>(a.gamma, at, a.H, g);
+            if (a.dtotal) load8<TT, kVec>(static_cast<const TT*>(a.dtotal) + t * a.lddt, at, a.H, o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                acc[i][j] = fmaf(d[i][j], v[i][j] * r, acc[i][j]);
+                o[j] += (d[i][j] * g[j] - v[i][j] * c) * r;
+            }
+            store8<TT, kVec>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+        }
+    }
+    if (!a.parts) return;
+    float* part = a.parts + (long long)blockIdx.x * a.H;
+    if (blockDim.y == 1) {
+#pragma unroll
+        for (int i = 0; i < kNormItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at < items) store8<float, false>(part, at, a.H, acc[i]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kNormItems; ++i) {
+        const int at = threadIdx.x + i * blockDim.x;
+        if (at < items) store8<float, false>(lines + threadIdx.y * a.H, at, a.H, acc[i]);
+    }
+    __syncthreads();
+    for (int j = threadIdx.y * 32 + threadIdx.x; j < a.H; j += 32 * kRowWarps) {
+        float s = 0.0f;
+        for (int w = 0; w < kRowWarps; ++w) s += lines[w * a.H + j];
+        part[j] = s;
+    }
+}
+
+// dgamma: the parts of 32 columns a CTA, eight runs of them added in order.
+__global__ void __launch_bounds__(256) k_gain_finish(int parts, int H, const float* __restrict__ part,
+                                                     float* __restrict__ dgamma) {
+    __shared__ float line[8][33];
+    const int j = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.0f;
+    if (j < H)
+        for (int p = threadIdx.y; p < parts; p += 8) s += part[(long long)p * H + j];
+    line[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && j < H) {
+        for (int w = 1; w < 8; ++w) s += line[w][threadIdx.x];
+        dgamma[j] = s;
+    }
+}
+
+bool float_type(int t) { return t == QBMOE_F32 || t == QBMOE_BF16; }
+int size_of(int t) { return t == QBMOE_F32 ? 4 : 2; }
+bool at_elements(const void* p, int type) { return (reinterpret_cast<uintptr_t>(p) & (size_of(type) - 1)) == 0; }
+// Rows that are read in 16-byte pieces.
+bool vectors(const void* p, long long ld, int type) { return qbh::aligned16(p) && ld * size_of(type) % 16 == 0; }
+bool sizes_ok(int T, int H, float eps) {
+    return T >= 0 && T <= QBMOE_MAX_ROWS && H >= 1 && H <= QBMOE_MAX_NORM && eps >= 0.0f && isfinite(eps);
+}
+// A warp a row up to 1024 elements, else the threads that hold a row in kNormItems pieces each.
+dim3 row_block(int H) {
+    const int threads = ((H + 8 * kNormItems - 1) / (8 * kNormItems) + 31) & ~31;
+    return threads <= 32 ? dim3(32, kRowWarps) : dim3(threads);
+}
+int gain_parts(int T, int H) {
+    const long long ctas = (T + (long long)row_block(H).y - 1) / row_block(H).y;
+    return (int)(ctas < kGainParts ? ctas : kGainParts);
+}
+
+// Calls f with a value of each of two types.
+template <typename F>
+void with_types(int first, int second, F f) {
+    if (first == QBMOE_F32) second == QBMOE_F32 ? f(float{}, float{}) : f(float{}, __nv_bfloat16{});
+    else second == QBMOE_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+}
+
+}  // namespace
+
+extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long long ldx, int res_type,
+                               const void* residual, long long ldr, const float* gamma, float eps, void* total,
+                               long long ldt, void* y, long long ldy, uint8_t* codes, uint8_t* scales,
+                               qbmoe_stream_t stream) {
+    if (!sizes_ok(T, H, eps) || !float_type(x_type) || (codes && H % 32) || !codes != !scales) return QBMOE_EINVAL;
+    if (ldx < H || (y && ldy < H) || !residual != !total) return QBMOE_EINVAL;
+    if (residual && (!float_type(res_type) || ldr < H || ldt < H)) return QBMOE_EINVAL;
+    if (T == 0) return QBMOE_OK;
+    const int y_type = codes ? QBMOE_BF16 : x_type;
+    if (!x || !gamma || (!y && !codes) || !at_elements(x, x_type) || !at_elements(gamma, QBMOE_F32) || !at_elements(y, y_type) ||
+        (reinterpret_cast<uintptr_t>(codes) & 7u))
+        return QBMOE_EINVAL;
+    if (residual && (!at_elements(residual, res_type) || !at_elements(total, res_type))) return QBMOE_EINVAL;
+    const int rc = qbh::device_init();
+    if (rc) return rc;
+    const bool vec = H % 8 == 0 && vectors(x, ldx, x_type) && vectors(gamma, 0, QBMOE_F32) && vectors(y, y ? ldy : 0, y_type) &&
+                     (!residual || (vectors(residual, ldr, res_type) && vectors(total, ldt, res_type)));
+    const NormArgs a{T, H, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, codes, scales};
+    const dim3 block = row_block(H);
+    const unsigned grid = (unsigned)(((long long)T + block.y - 1) / block.y);
+    with_types(x_type, residual ? res_type : x_type, [&](auto tx, auto tr) {
+        using TX = decltype(tx);
+        using TR = decltype(tr);
+        auto go = [&](auto kern) { kern<<<grid, block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a); };
+        if (vec) codes ? go(k_add_rmsnorm<TX, TR, true, true>) : go(k_add_rmsnorm<TX, TR, true, false>);
+        else codes ? go(k_add_rmsnorm<TX, TR, false, true>) : go(k_add_rmsnorm<TX, TR, false, false>);
+    });
+    return qbh::cuda_err(cudaGetLastError());
+}
+
+extern "C" size_t qbmoe_add_rmsnorm_workspace_bytes(int T, int H) {
+    return sizes_ok(T, H, 0.0f) ? (size_t)gain_parts(T, H) * H * 4 : 0;
+}
+
+extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long long lddn, int total_type,
+                                        const void* total, long long ldt, const float* gamma, float eps,
+                                        const void* dtotal, long long lddt, void* dx, long long lddx, float* dgamma,
+                                        void* workspace, size_t workspace_bytes, qbmoe_stream_t stream) {
+    if (!sizes_ok(T, H, eps) || !float_type(dn_type) || !float_type(total_type)) return QBMOE_EINVAL;
+    if (lddn < H || ldt < H || lddx < H || (dtotal && lddt < H) || !at_elements(dgamma, QBMOE_F32)) return QBMOE_EINVAL;
+    if (T > 0 && (!dn || !total || !gamma || !dx || !at_elements(dn, dn_type) || !at_elements(total, total_type) ||
+                  !at_elements(gamma, QBMOE_F32) || !at_elements(dtotal, total_type) || !at_elements(dx, total_type)))
+        return QBMOE_EINVAL;
+    if (T > 0 && dgamma) {
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return QBMOE_EINVAL;
+        if (workspace_bytes < qbmoe_add_rmsnorm_workspace_bytes(T, H)) return QBMOE_EWORKSPACE;
+    }
+    if (T == 0 && !dgamma) return QBMOE_OK;
+    const int rc = qbh::device_init();
+    if (rc) return rc;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) return qbh::cuda_err(cudaMemsetAsync(dgamma, 0, (size_t)H * 4, s));
+    const bool vec = H % 8 == 0 && vectors(dn, lddn, dn_type) && vectors(total, ldt, total_type) &&
+                     vectors(gamma, 0, QBMOE_F32) && vectors(dtotal, dtotal ? lddt : 0, total_type) &&
+                     vectors(dx, lddx, total_type);
+    float* parts = dgamma ? static_cast<float*>(workspace) : nullptr;
+    const NormGradArgs a{T, H, dn, lddn, total, ldt, gamma, eps, dtotal, lddt, dx, lddx, parts};
+    const dim3 block = row_block(H);
+    const int grid = gain_parts(T, H);
+    const size_t smem = block.y > 1 ? (size_t)kRowWarps * H * 4 : 0;
+    with_types(dn_type, total_type, [&](auto td, auto tt) {
+        using TD = decltype(td);
+        using TT = decltype(tt);
+        if (vec) k_add_rmsnorm_backward<TD, TT, true><<<grid, block, smem, s>>>(a);
+        else k_add_rmsnorm_backward<TD, TT, false><<<grid, block, smem, s>>>(a);
+    });
+    if (dgamma) k_gain_finish<<<(H + 31) / 32, dim3(32, 8), 0, s>>>(grid, H, parts, dgamma);
+    return qbh::cuda_err(cudaGetLastError());
+}

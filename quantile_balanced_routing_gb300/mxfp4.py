@@ -49,6 +49,8 @@ def _row_stride(what, name, t, align):
     rows, cols = t.shape
     if rows <= 1:
         ld = cols
+    if rows == 0:            # no row to read: the strides may be anything
+        return ld
     if (one != 1 and cols != 1) or ld < cols or ld % align:
         _refuse(what, f"{name} is a matrix with contiguous rows, their stride a multiple of {align} elements")
     return ld
