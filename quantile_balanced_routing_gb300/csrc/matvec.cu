@@ -7,11 +7,12 @@
 // One kernel streams weights through shared memory and multiplies them with a few rows
 // that stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is
 // kWarps / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Its
-// rows come by untiled bulk copies, a row each, several units ahead; the warps take turns to
-// issue them (a 17th warp would leave 96 registers a thread instead of 128).  The 16 warps
-// divide the tiles and the depth: a warp owns a run of at most kNB blocks of 32 of K, for
-// which it holds the rows' elements as mma B operands, so that the rows cost no
-// bandwidth while weights go by.  Per block of 32 and tile:
+// rows come by untiled bulk copies, a row each, several units ahead, every warp issuing its
+// share (a lane's copies go one after the other; a 17th warp for them would leave 96
+// registers a thread instead of 128).  The 16 warps divide the tiles and the depth: a warp
+// owns a run of at most kNB blocks of 32 of K, for which it holds the rows' elements as
+// mma B operands, so that the rows cost no bandwidth while weights go by.  Per block of
+// 32 and tile:
 //   - ldmatrix hands each quad of lanes the 16 bytes of a weight row's block;
 //   - codes become fp16 (exact) two at a time, with one conversion;
 //   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
@@ -37,6 +38,7 @@ constexpr int kMaxStages = 16;
 constexpr int kLine = 20;                      // floats a column of 16 results takes: stores without bank conflicts
 constexpr long long kDefaultWait = 1LL << 17;  // polls (<= 20 us each) before a wait expires
 constexpr int kMaxDynamic = 226 * 1024;       // of 227 KB, a little being static
+constexpr int kSlack = 512;                    // loads ahead of a warp's last blocks stay in shared memory
 
 // What a launch computes.
 enum { kStore, kGlu, kDown };
@@ -57,7 +59,7 @@ struct StreamArgs {
     long long ldy;
     float beta1, beta2;
     // geometry
-    int splits;                  // warps along the depth; kWarps / splits tiles a unit
+    int splits, split_log;       // warps along the depth (a power of two); kWarps / splits tiles a unit
     int slabs, slab_blocks;      // the depth in slabs of this many blocks of 32
     int stages, stage_bytes, pitch, scale_pitch;
     int* expiries;
@@ -71,7 +73,7 @@ struct Shape {
     static constexpr int kPart = kCols * kLine + 8;            // floats of a warp's partial results
     static constexpr int kRed = 2 * kWarps * kPart * 4;        // double buffered
     static constexpr int kSx = kWarps * kNB * kCols * 4;       // scales of x
-    static constexpr int kBars = kMaxStages * 16;              // barriers, units issued
+    static constexpr int kBars = kMaxStages * 8;
     static size_t fixed(int E, int routes) {
         return kBars + kRed + kSx + qbh::align_up((size_t)(E + 1) * 8, 16) + qbh::align_up((size_t)routes * 2, 16);
     }
@@ -85,20 +87,27 @@ QB_DEV void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
         : "r"(w));
 }
 QB_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 QB_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
-QB_DEV uint32_t lds_u8(uint32_t addr) {
+QB_DEV uint32_t lds32(uint32_t addr) {
     uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
+}
+// Two E8M0 bytes, byte i of each word, as fp32 (0xFF: NaN).
+QB_DEV void scale_pair(uint32_t lo, uint32_t hi, int i, float& a, float& b) {
+    const uint32_t both = __byte_perm(lo, hi, (uint32_t)i | (uint32_t)(4 + i) << 4);
+    uint32_t h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, l;\n\t}" : "=r"(h) : "r"(both));
+    a = __uint_as_float(h << 16);
+    b = __uint_as_float(h & 0xffff0000u);
 }
 QB_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -316,7 +325,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
     extern __shared__ __align__(128) char sm[];
     __shared__ int scratch[kWarps];
     uint64_t* full = reinterpret_cast<uint64_t*>(sm);
-    int* issued = reinterpret_cast<int*>(full + kMaxStages);   // units brought to each stage
     float* red = reinterpret_cast<float*>(sm + S::kBars);
     float* sx_all = red + S::kRed / 4;
     int* seg = reinterpret_cast<int*>(sx_all + S::kSx / 4);
@@ -327,10 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
     const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
     if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) {
-            tc::mbar_init(full + s, 1);
-            issued[s] = 0;
-        }
+        for (int s = 0; s < a.stages; ++s) tc::mbar_init(full + s, kWarps);
         tc::fence_mbar_init();
     }
     group_rows<kMode, kCols>(a, seg, first, list, reinterpret_cast<int*>(ring), scratch);   // with barriers for the whole CTA
@@ -341,62 +346,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
     Units it;
     it.start(first, a.E, (a.N + tile_rows - 1) / tile_rows, a.slabs);
 
-    // One warp: bring a unit's rows to stage s.  A row's codes are blocks of 16 bytes; its scales
-    // start anywhere, so the 16-byte pieces that hold them are copied, except behind the tensor's
-    // last whole piece, where bytes go one by one.
-    auto bring = [&](const Units& to, int s) {
-        const int blk0 = to.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
-        char* stage = ring + (size_t)s * a.stage_bytes;
-        char* sstage = stage + rows_unit * a.pitch;
-        auto row = [&](int i, const uint8_t*& cp, const uint8_t*& sp, long long& at, uint32_t& len) {
-            const int f = kMode == kGlu ? (to.tile * tiles_unit + (i >> 4)) * 8 + (i & 7) : to.tile * rows_unit + i;
-            if (i >= rows_unit || f >= a.N) return false;
-            const bool up = kMode == kGlu && (i & 8);
-            const long long w = (long long)to.g * a.N + f;
-            cp = (up ? a.codes2 : a.codes) + (w * depth + blk0) * 16;
+    // Each warp brings one row of every tile of a unit, a lane each: codes are blocks of 16 bytes; a
+    // row's scales start anywhere, so the 16-byte pieces that hold them are copied, except
+    // behind the tensor's last whole piece, where bytes go one by one.
+    Units ahead = it;
+    const uint8_t *cp = nullptr, *sp = nullptr;   // this lane's row of the unit ahead, and its scales' tensor
+    long long at = 0;                             // its first scale byte there
+    const int my_row = lane * 16 + warp;          // of the unit; lanes past its tiles have none
+    int brought = 0;                              // units so far
+    auto bring = [&](int s) {
+        const int blk0 = ahead.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
+        const int f = kMode == kGlu ? (ahead.tile * tiles_unit + lane) * 8 + (warp & 7) : ahead.tile * rows_unit + my_row;
+        if (ahead.fresh) {
+            const bool up = kMode == kGlu && (warp & 8);
+            at = ((long long)ahead.g * a.N + f) * depth + blk0;
+            cp = (up ? a.codes2 : a.codes) + at * 16;
             sp = up ? a.scales2 : a.scales;
-            at = w * depth + blk0;
-            len = (uint32_t)(min((at + nblk + 15) & ~15LL, all & ~15LL) - (at & ~15LL));
-            return true;
-        };
-        const uint8_t *cp, *sp;
-        long long at;
-        uint32_t len, bytes = 0;
-        for (int i = lane; i < rows_unit; i += 32) {
-            if (!row(i, cp, sp, at, len)) continue;
-            bytes += nblk * 16 + len;
+        }
+        const bool mine = lane < tiles_unit && f < a.N;
+        char* stage = ring + (size_t)s * a.stage_bytes + my_row * a.pitch;
+        char* sstage = ring + (size_t)s * a.stage_bytes + rows_unit * a.pitch + my_row * a.scale_pitch;
+        const long long sat = at & ~15LL;
+        uint32_t len = 0;
+        if (mine) {
+            len = (uint32_t)(min((at + nblk + 15) & ~15LL, all & ~15LL) - sat);
             if (at + nblk > (all & ~15LL)) {
-                for (long long j = max(at, all & ~15LL); j < at + nblk; ++j)
-                    sstage[i * a.scale_pitch + (int)(j - (at & ~15LL))] = (char)sp[j];
+                for (long long j = max(at, all & ~15LL); j < at + nblk; ++j) sstage[j - sat] = (char)sp[j];
                 tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
             }
         }
-        bytes = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0) {
-            ++issued[s];
-            tc::mbar_expect_tx(full + s, bytes);
-        }
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine ? nblk * 16 + len : 0);
+        if (a.stall && warp == 0 && brought == 0) return;   // test hook: the first unit never arrives
+        if (lane == 0) tc::mbar_expect_tx(full + s, bytes);
         __syncwarp();
-        for (int i = lane; i < rows_unit; i += 32) {
-            if (!row(i, cp, sp, at, len)) continue;
-            bulk_load(tc::smem_u32(stage + i * a.pitch), cp, nblk * 16, full + s);
-            if (len) bulk_load(tc::smem_u32(sstage + i * a.scale_pitch), sp + (at & ~15LL), len, full + s);
+        if (mine) {
+            bulk_load(tc::smem_u32(stage), cp, nblk * 16, full + s);
+            if (len) bulk_load(tc::smem_u32(sstage), sp + sat, len, full + s);
         }
     };
-    Units ahead = it;
-    for (int i = 0; i < a.stages && ahead.u < ahead.end; ++i, ahead.next(first))
-        if (warp == i && !(a.stall && i == 0)) bring(ahead, i);
+    auto bring_next = [&](int s) {
+        bring(s);
+        cp += (long long)tile_rows * depth * 16;   // the same row of the next tile
+        at += (long long)tile_rows * depth;
+        ++brought;
+        ahead.next(first);
+    };
+    for (int i = 0; i < a.stages && ahead.u < ahead.end; ++i) bring_next(i);
 
-    const int wm = warp / a.splits, wk = warp - wm * a.splits;
+    const int wm = warp >> a.split_log, wk = warp & (a.splits - 1);
     const int g8 = lane >> 2, t4 = lane & 3;
     float* sx = sx_all + warp * (kNB * kCols);
-    // outputs: `parts` threads each, so that all threads add
-    const int per_unit = tiles_unit * 16 * kCols;
-    const int parts = max(1, kThreads / per_unit);
+    // Outputs of a unit: 16 kCols a tile, each summed by `parts` neighbouring threads so that all
+    // threads add.  Output o is column o / 16 % kCols of tile o / (16 kCols), its row o % 16 or, for
+    // kGlu, such that neighbours hold a feature's gate and up (rows 0 to 7 and 8 to 15).
+    const int outputs = tiles_unit * 16 * kCols;
+    const int parts_log = outputs >= kThreads ? 0 : outputs == kThreads / 2 ? 1 : 2, parts = 1 << parts_log;
+    const int o0 = threadIdx.x >> parts_log, part = threadIdx.x & (parts - 1);
+    const int oi = kMode == kGlu ? (o0 & 1) << 3 | (o0 >> 1 & 7) : o0 & 15;
     if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
     uint32_t B[kNB][kNG][4];
-    int s = 0, ph = 0, buf = 0, turn = 0, nb = 0, b0 = 0, row0 = 0, nrows = 0;
-    bool dead = false;                // a wait expired: only the barriers go on
+    int s = 0, ph = 0, buf = 0, nb = 0, b0 = 0, row0 = 0, nrows = 0;
+    bool dead = false;                // a wait expired
     for (; it.u < it.end; it.next(first)) {
         const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
         if (it.fresh) {
@@ -430,34 +440,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
             }
             __syncwarp();
         }
-        if (!dead && !tc::mbar_wait_spin(full + s, ph, lim)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
+        if (!tc::mbar_wait_spin(full + s, ph, lim)) dead = true;
         float acc[kNG][4] = {};
-        if (!dead) {
-            char* stage = ring + (size_t)s * a.stage_bytes;
+        {
+            const uint32_t stage = tc::smem_u32(ring + (size_t)s * a.stage_bytes);
             const int q = lane >> 3;
-            const uint32_t at = tc::smem_u32(stage) + (wm * 16 + (lane & 7) + (q & 1) * 8) * a.pitch + (b0 + (q >> 1)) * 16;
-            // a row's scales start at a byte of their first 16
-            uint32_t sat[2];
+            const uint32_t wat = stage + (wm * 16 + (lane & 7) + (q & 1) * 8) * a.pitch + (b0 + (q >> 1)) * 16;
+            // a row's scales start at a byte of their first 16: words of four, shifted into place
+            uint32_t sat[2], shift[2], sc[2], sw[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int i = wm * 16 + 8 * h + g8;
                 const int f = kMode == kGlu ? (it.tile * tiles_unit + wm) * 8 + g8 : it.tile * rows_unit + i;
                 const uint32_t start = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)f) * (uint32_t)depth + (uint32_t)blk0;
-                sat[h] = tc::smem_u32(stage + rows_unit * a.pitch) + i * a.scale_pitch + (start & 15u) + b0;
+                const uint32_t byte = stage + rows_unit * a.pitch + i * a.scale_pitch + (start & 15u) + b0;
+                sat[h] = byte & ~3u;
+                shift[h] = (byte & 3u) * 8;
+                sw[h] = lds32(sat[h]);
             }
+            uint32_t next[4];
+            ldmatrix4(next, wat);
 #pragma unroll
             for (int i = 0; i < kNB; i += 2) {
                 if (i >= nb) break;
-                uint32_t w[4];
-                ldmatrix4(w, at + i * 16);
+                uint32_t w[4] = {next[0], next[1], next[2], next[3]};
+                if (i + 2 < kNB) ldmatrix4(next, wat + (i + 2) * 16);   // what lies behind the row is not used
+                if (i % 4 == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t up = lds32(sat[h] + i + 4);
+                        sc[h] = __funnelshift_r(sw[h], up, shift[h]);
+                        sw[h] = up;
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (i + h >= nb) break;
                     uint32_t lo[4], hi[4];
                     codes_to_f16(w[2 * h], lo);
                     codes_to_f16(w[2 * h + 1], hi);
-                    const float s0 = e8m0_value(lds_u8(sat[0] + i + h)), s1 = e8m0_value(lds_u8(sat[1] + i + h));
+                    float s0, s1;
+                    scale_pair(sc[0], sc[1], (i + h) & 3, s0, s1);
 #pragma unroll
                     for (int j = 0; j < kNG; ++j) {
                         float d[4] = {};
@@ -481,26 +504,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
             mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[j][2];
             mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[j][3];
         }
-        __syncthreads();
+        if (__syncthreads_or(dead)) break;
         // every warp is done with the stage: the next unit for it comes
-        if (ahead.u < ahead.end) {
-            if (warp == turn && !dead) bring(ahead, s);
-            ahead.next(first);
-        }
-        turn = (turn + 1) % kWarps;
+        if (ahead.u < ahead.end) bring_next(s);
         if (++s == a.stages) s = 0, ph ^= 1;
-        for (int o = threadIdx.x / parts; o < per_unit; o += kThreads / parts) {
-            // neighbours hold a feature's gate and up (rows 0 to 7 and 8 to 15 of a tile)
-            const int i = kMode == kGlu ? (o & 1) << 3 | (o >> 1 & 7) : o & 15;
-            const int c = (o >> 4) % kCols, m = o / (16 * kCols);
+        for (int o = o0; o < outputs; o += kThreads >> parts_log) {
+            const int i = oi, c = (o >> 4) & (kCols - 1), m = o / (16 * kCols);
+            const float* from = red + (buf * kWarps + (m << a.split_log) + part) * S::kPart + c * kLine + i;
             float v = 0.0f;
-            for (int w = threadIdx.x % parts; w < a.splits; w += parts)
-                v += red[(buf * kWarps + m * a.splits + w) * S::kPart + c * kLine + i];
-            for (int d = 1; d < parts; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+#pragma unroll 4
+            for (int w = part; w < a.splits; w += parts, from += parts * S::kPart) v += *from;
+            if (parts_log > 0) v += __shfl_xor_sync(0xffffffffu, v, 1);
+            if (parts_log > 1) v += __shfl_xor_sync(0xffffffffu, v, 2);
             if (kMode == kGlu) {
                 const float u = __shfl_xor_sync(0xffffffffu, v, parts);
                 const int f = (it.tile * tiles_unit + m) * 8 + (i & 7);
-                if (threadIdx.x % parts || c >= nrows || f >= a.N) continue;
+                if (part || c >= nrows || f >= a.N) continue;
                 const long long r = list[row0 + c];
                 float* y = static_cast<float*>(a.y);
                 if (a.slabs > 1) y[((it.slab * 2LL + (i >> 3)) * a.R + r) * a.ldy + f] = v;
@@ -508,19 +527,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
                 continue;
             }
             const int f = it.tile * rows_unit + m * 16 + i;
-            if (threadIdx.x % parts || c >= nrows || f >= a.N) continue;
+            if (part || c >= nrows || f >= a.N) continue;
             const long long r = (kMode == kDown ? (int)list[row0 + c] : row0 + c) + (long long)it.slab * a.R;
             if (a.y_type == QBMOE_F32) static_cast<float*>(a.y)[r * a.ldy + f] = v;
             else static_cast<__nv_bfloat16*>(a.y)[r * a.ldy + f] = __float2bfloat16_rn(v);
         }
         buf ^= 1;
     }
-    if (dead) {   // no copy may be in flight when the CTA ends
-        if (lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
-        for (int i = 0; i < a.stages; ++i) {
-            const int n = *reinterpret_cast<volatile int*>(issued + i);
-            if (n) tc::mbar_wait(full + i, (n - 1) & 1, lim);
-        }
+    if (it.u < it.end) {   // a wait expired somewhere; no copy may be in flight when the CTA ends
+        if (dead && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
+        for (int i = 0; i < min(brought, a.stages); ++i)
+            tc::mbar_wait(full + i, ((brought - i + a.stages - 1) / a.stages - 1) & 1, lim);
     }
 }
 
@@ -631,6 +648,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs a
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
+constexpr int kRingThird = 62 * 1024;   // of the shared memory that a call with few experts leaves
 constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that 16 warps hold in 16 blocks each
 
 int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
@@ -650,12 +668,16 @@ int stream(StreamArgs a, cudaStream_t s) {
     const int ng = depth <= 128 && (long long)a.R > 8LL * a.E ? 2 : 1;
     a.slabs = slabs_of(a.K);
     a.slab_blocks = (depth + a.slabs - 1) / a.slabs;
-    a.splits = 1;
-    while (a.splits < kWarps && (a.slab_blocks + a.splits - 1) / a.splits > 8) a.splits *= 2;
-    const int per = (a.slab_blocks + a.splits - 1) / a.splits;
-    const int rows = 16 * (kWarps / a.splits);
     a.pitch = (a.slab_blocks | 1) * 16;                         // odd in 16 bytes: ldmatrix without bank conflicts
     a.scale_pitch = (((a.slab_blocks + 30) / 16) | 1) * 16;     // from any start within 16 bytes
+    // the fewest splits whose share a warp holds, and three units in flight
+    for (a.split_log = 0; a.split_log < 4; ++a.split_log) {
+        a.stage_bytes = 16 * (kWarps >> a.split_log) * (a.pitch + a.scale_pitch);
+        if (((a.slab_blocks - 1) >> a.split_log) + 1 <= 16 / ng && a.stage_bytes <= kRingThird) break;
+    }
+    a.splits = 1 << a.split_log;
+    const int per = ((a.slab_blocks - 1) >> a.split_log) + 1;
+    const int rows = 16 * (kWarps / a.splits);
     a.stage_bytes = rows * (a.pitch + a.scale_pitch);
     a.expiries = qbh::mx_expiries();
     a.wait_limit = qbh::mx_wait_limit();
@@ -663,9 +685,9 @@ int stream(StreamArgs a, cudaStream_t s) {
     return for_shape(ng, per, [&](auto shape, auto nb, auto n) {
         using S = decltype(shape);
         const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
-        a.stages = (int)((kMaxDynamic - fixed) / a.stage_bytes);
+        a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
         if (a.stages > kMaxStages) a.stages = kMaxStages;
-        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes;   // two stages or more, and over the 64 KB that hist takes
+        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 64 KB that hist takes
         const int unit = kMode == kGlu ? rows / 2 : rows;
         long long units = 0x7fffffff;
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + S::kCols - 1) / S::kCols) * ((a.N + unit - 1) / unit) * a.slabs;
