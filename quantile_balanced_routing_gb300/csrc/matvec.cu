@@ -6,17 +6,16 @@
 //
 // One kernel streams weights through shared memory and multiplies them with a few rows
 // that stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is
-// kWarps / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Its
-// rows come by untiled bulk copies, a row each, several units ahead, every warp issuing its
-// share (a lane's copies go one after the other; a 17th warp for them would leave 96
-// registers a thread instead of 128).  The 16 warps divide the tiles and the depth: a warp
-// owns a run of at most kNB blocks of 32 of K, for which it holds the rows' elements as
-// mma B operands, so that the rows cost no bandwidth while weights go by.  Per block of
-// 32 and tile:
+// 8 / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Two producer
+// warps bring a unit's codes and scales by untiled bulk copies, a row each, several units
+// ahead.  Eight consumer warps divide the tiles and the depth: a warp owns a run of kNB
+// blocks of 32 of K, for which it holds the rows' elements as mma B operands, so that the
+// rows cost no bandwidth while weights go by.  Per block of 32 and tile:
 //   - ldmatrix hands each quad of lanes the 16 bytes of a weight row's block;
 //   - codes become fp16 (exact) two at a time, with one conversion;
 //   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
 //   - the block's dot products, times the two scales, are added in fp32.
+// Two more warps add the shares of the depth, in order, and store.
 // Weight rows are the M operand of the small mma because a column costs nothing that way: up
 // to 8 rows of x take as long as one.  tcgen05 would need its operands decoded in shared
 // memory, or x as E4M3 pairs (the layer's way: bound by issue at few columns).
@@ -33,7 +32,9 @@ namespace {
 
 using namespace qb;
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                      // consumers: all columns fit 168 registers a thread
+constexpr int kFinishWarps = 2, kCodesWarp = 10;   // the last, 11, brings scales
+constexpr int kThreads = 384;
 constexpr int kMaxStages = 16;
 constexpr int kLine = 20;                      // floats a column of 16 results takes: stores without bank conflicts
 constexpr long long kDefaultWait = 1LL << 17;  // polls (<= 20 us each) before a wait expires
@@ -59,7 +60,7 @@ struct StreamArgs {
     long long ldy;
     float beta1, beta2;
     // geometry
-    int splits, split_log;       // warps along the depth (a power of two); kWarps / splits tiles a unit
+    int splits, split_log;       // consumers along the depth (a power of two); kWarps / splits tiles a unit
     int slabs, slab_blocks;      // the depth in slabs of this many blocks of 32
     int stages, stage_bytes, pitch, scale_pitch;
     int* expiries;
@@ -69,11 +70,12 @@ struct StreamArgs {
 
 template <int kNB, int kNG>
 struct Shape {
+    static constexpr int kBlocks = kNB, kGroups = kNG;
     static constexpr int kCols = 8 * kNG;                      // rows of x a unit takes
     static constexpr int kPart = kCols * kLine + 8;            // floats of a warp's partial results
     static constexpr int kRed = 2 * kWarps * kPart * 4;        // double buffered
     static constexpr int kSx = kWarps * kNB * kCols * 4;       // scales of x
-    static constexpr int kBars = kMaxStages * 8;
+    static constexpr int kBars = (2 * kMaxStages + 4) * 8;
     static size_t fixed(int E, int routes) {
         return kBars + kRed + kSx + qbh::align_up((size_t)(E + 1) * 8, 16) + qbh::align_up((size_t)routes * 2, 16);
     }
@@ -86,6 +88,13 @@ QB_DEV void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
 }
+// d = A B
+QB_DEV void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// d += A B
 QB_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -108,6 +117,15 @@ QB_DEV void scale_pair(uint32_t lo, uint32_t hi, int i, float& a, float& b) {
     asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, l;\n\t}" : "=r"(h) : "r"(both));
     a = __uint_as_float(h << 16);
     b = __uint_as_float(h & 0xffff0000u);
+}
+// (a x, b y), in one instruction.
+QB_DEV float2 mul2(float a, float b, float2 v) {
+    float2 r;
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a), "f"(b), "f"(v.x), "f"(v.y));
+    return r;
 }
 QB_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -194,8 +212,8 @@ struct Raw {
 // ---------------------------------------------------------------------------
 
 // Whole CTA: a[0 .. n - 1] to its exclusive sums, the total in a[n].
-QB_DEV void exclusive_scan(int* a, int n, int* scratch /* [kWarps] */) {
-    constexpr int W = kWarps;
+QB_DEV void exclusive_scan(int* a, int n, int* scratch /* [kThreads / 32] */) {
+    constexpr int W = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per = ((n + W - 1) / W + 31) & ~31;
     __syncthreads();
@@ -232,7 +250,7 @@ template <int kMode, int kCols>
 QB_DEV void group_rows(const StreamArgs& a, int* seg, int* first, uint16_t* list, int* hist, int* scratch) {
     if (kMode == kGlu || kMode == kDown) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int warps = min(kWarps, (a.R + 31) >> 5), per = ((a.R + warps - 1) / warps + 31) & ~31;
+        const int warps = min(kThreads / 32, (a.R + 31) >> 5), per = ((a.R + warps - 1) / warps + 31) & ~31;
         for (int i = threadIdx.x; i < warps * a.E; i += kThreads) hist[i] = 0;
         __syncthreads();
         for (int r = warp * per + lane; r < min(a.R, (warp + 1) * per); r += 32) {
@@ -317,14 +335,65 @@ struct Units {
     }
 };
 
+// A warp's share of a tile: 16 weight rows times kNB blocks of K.  wat: this lane's row of the four
+// 8 x 16-byte matrices that one ldmatrix loads (two blocks of 16 rows); lo, hi: the scales of
+// weight rows lane / 4 and 8 more.  kSome: only nb blocks are the warp's; for the rest B and the
+// scales of x are zeros, and the weights' scales, whatever lies there, are cleared lest one be NaN.
+template <int kNB, int kNG, bool kSome>
+QB_DEV void share(const uint32_t (&B)[kNB][kNG][4], const float* sx, uint32_t wat, uint32_t lo, uint32_t hi, int nb,
+                  float (&acc)[kNG][4]) {
+    uint32_t sat[2] = {lo & ~3u, hi & ~3u}, shift[2] = {(lo & 3u) * 8, (hi & 3u) * 8}, sw[2], sc[2], next[4];
+    sw[0] = lds32(sat[0]);
+    sw[1] = lds32(sat[1]);
+    ldmatrix4(next, wat);
+#pragma unroll
+    for (int i = 0; i < kNB; i += 2) {
+        if (kSome && i >= nb) break;
+        const uint32_t w[4] = {next[0], next[1], next[2], next[3]};
+        if (i + 2 < kNB) ldmatrix4(next, wat + (i + 2) * 16);
+        if (i % 4 == 0) {   // the scales of four blocks, shifted into place
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t up = lds32(sat[h] + i + 4);
+                sc[h] = __funnelshift_r(sw[h], up, shift[h]);
+                if (kSome && nb - i < 4) sc[h] &= (1u << 8 * (nb - i)) - 1;
+                sw[h] = up;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t p[4], q[4];
+            codes_to_f16(w[2 * h], p);
+            codes_to_f16(w[2 * h + 1], q);
+            float s0, s1;
+            scale_pair(sc[0], sc[1], (i + h) & 3, s0, s1);
+#pragma unroll
+            for (int j = 0; j < kNG; ++j) {
+                float d[4];
+                mma_f16_first(d, p[0], q[0], p[1], q[1], B[i + h][j][0], B[i + h][j][1]);
+                mma_f16(d, p[2], q[2], p[3], q[3], B[i + h][j][2], B[i + h][j][3]);
+                const float2 x = *reinterpret_cast<const float2*>(sx + (i + h) * (8 * kNG) + 8 * j);
+                const float2 u = mul2(d[0], d[1], x), v = mul2(d[2], d[3], x);
+                acc[j][0] = fmaf(u.x, s0, acc[j][0]);
+                acc[j][1] = fmaf(u.y, s0, acc[j][1]);
+                acc[j][2] = fmaf(v.x, s1, acc[j][2]);
+                acc[j][3] = fmaf(v.y, s1, acc[j][3]);
+            }
+        }
+    }
+}
+
 template <int kNB, int kNG, int kX, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
     using S = Shape<kNB, kNG>;
     constexpr int kCols = S::kCols;
     constexpr bool kRoutes = kMode == kGlu || kMode == kDown;
     extern __shared__ __align__(128) char sm[];
-    __shared__ int scratch[kWarps];
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm);
+    __shared__ int scratch[kThreads / 32];
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm);   // a unit's copies have landed
+    uint64_t* empty = full + kMaxStages;                // its consumers have read it
+    uint64_t* done = empty + kMaxStages;                // [2]: they have written their shares of the sums
+    uint64_t* freed = done + 2;                         // [2]: the sums are formed
     float* red = reinterpret_cast<float*>(sm + S::kBars);
     float* sx_all = red + S::kRed / 4;
     int* seg = reinterpret_cast<int*>(sx_all + S::kSx / 4);
@@ -335,210 +404,204 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const StreamArgs a) {
     const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
     if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) tc::mbar_init(full + s, kWarps);
+        for (int s = 0; s < a.stages; ++s) {
+            tc::mbar_init(full + s, 2);
+            tc::mbar_init(empty + s, kWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(done + i, kWarps);
+            tc::mbar_init(freed + i, kFinishWarps);
+        }
         tc::fence_mbar_init();
     }
     group_rows<kMode, kCols>(a, seg, first, list, reinterpret_cast<int*>(ring), scratch);   // with barriers for the whole CTA
     const int depth = a.K >> 5;                               // blocks of a weight row
-    const int tiles_unit = kWarps / a.splits, rows_unit = 16 * tiles_unit;
+    const int tiles_unit = kWarps >> a.split_log, rows_unit = 16 * tiles_unit;
     const int tile_rows = kMode == kGlu ? 8 * tiles_unit : rows_unit;   // features a unit
-    const long long all = (long long)a.E * a.N * depth;                 // scale bytes
+    bool ok = true;               // no wait of this warp has expired
+    int s = 0, ph = 0, buf = 0;
     Units it;
     it.start(first, a.E, (a.N + tile_rows - 1) / tile_rows, a.slabs);
 
-    // Each warp brings one row of every tile of a unit, a lane each: codes are blocks of 16 bytes; a
-    // row's scales start anywhere, so the 16-byte pieces that hold them are copied, except
-    // behind the tensor's last whole piece, where bytes go one by one.
-    Units ahead = it;
-    const uint8_t *cp = nullptr, *sp = nullptr;   // this lane's row of the unit ahead, and its scales' tensor
-    long long at = 0;                             // its first scale byte there
-    const int my_row = lane * 16 + warp;          // of the unit; lanes past its tiles have none
-    int brought = 0;                              // units so far
-    auto bring = [&](int s) {
-        const int blk0 = ahead.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
-        const int f = kMode == kGlu ? (ahead.tile * tiles_unit + lane) * 8 + (warp & 7) : ahead.tile * rows_unit + my_row;
-        if (ahead.fresh) {
-            const bool up = kMode == kGlu && (warp & 8);
-            at = ((long long)ahead.g * a.N + f) * depth + blk0;
-            cp = (up ? a.codes2 : a.codes) + at * 16;
-            sp = up ? a.scales2 : a.scales;
-        }
-        const bool mine = lane < tiles_unit && f < a.N;
-        char* stage = ring + (size_t)s * a.stage_bytes + my_row * a.pitch;
-        char* sstage = ring + (size_t)s * a.stage_bytes + rows_unit * a.pitch + my_row * a.scale_pitch;
-        const long long sat = at & ~15LL;
-        uint32_t len = 0;
-        if (mine) {
-            len = (uint32_t)(min((at + nblk + 15) & ~15LL, all & ~15LL) - sat);
-            if (at + nblk > (all & ~15LL)) {
-                for (long long j = max(at, all & ~15LL); j < at + nblk; ++j) sstage[j - sat] = (char)sp[j];
-                tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
+    if (warp >= kCodesWarp) {
+        // ---- producers: a lane a row.  Codes are blocks of 16 bytes.  A row's scales start anywhere, so
+        // the 16-byte pieces that hold them are copied, except behind the tensor's last whole
+        // piece, where bytes go one by one.
+        const bool codes = warp == kCodesWarp;
+        const long long all = (long long)a.E * a.N * depth, last = all & ~15LL;
+        int units = 0;
+        for (; it.u < it.end; it.next(first), ++units) {
+            if (units >= a.stages && !tc::mbar_wait(empty + s, ph ^ 1, lim)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
             }
-        }
-        const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine ? nblk * 16 + len : 0);
-        if (a.stall && warp == 0 && brought == 0) return;   // test hook: the first unit never arrives
-        if (lane == 0) tc::mbar_expect_tx(full + s, bytes);
-        __syncwarp();
-        if (mine) {
-            bulk_load(tc::smem_u32(stage), cp, nblk * 16, full + s);
-            if (len) bulk_load(tc::smem_u32(sstage), sp + sat, len, full + s);
-        }
-    };
-    auto bring_next = [&](int s) {
-        bring(s);
-        cp += (long long)tile_rows * depth * 16;   // the same row of the next tile
-        at += (long long)tile_rows * depth;
-        ++brought;
-        ahead.next(first);
-    };
-    for (int i = 0; i < a.stages && ahead.u < ahead.end; ++i) bring_next(i);
-
-    const int wm = warp >> a.split_log, wk = warp & (a.splits - 1);
-    const int g8 = lane >> 2, t4 = lane & 3;
-    float* sx = sx_all + warp * (kNB * kCols);
-    // Outputs of a unit: 16 kCols a tile, each summed by `parts` neighbouring threads so that all
-    // threads add.  Output o is column o / 16 % kCols of tile o / (16 kCols), its row o % 16 or, for
-    // kGlu, such that neighbours hold a feature's gate and up (rows 0 to 7 and 8 to 15).
-    const int outputs = tiles_unit * 16 * kCols;
-    const int parts_log = outputs >= kThreads ? 0 : outputs == kThreads / 2 ? 1 : 2, parts = 1 << parts_log;
-    const int o0 = threadIdx.x >> parts_log, part = threadIdx.x & (parts - 1);
-    const int oi = kMode == kGlu ? (o0 & 1) << 3 | (o0 >> 1 & 7) : o0 & 15;
-    if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
-    uint32_t B[kNB][kNG][4];
-    int s = 0, ph = 0, buf = 0, nb = 0, b0 = 0, row0 = 0, nrows = 0;
-    bool dead = false;                // a wait expired
-    for (; it.u < it.end; it.next(first)) {
-        const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
-        if (it.fresh) {
-            row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols;
-            nrows = min(kCols, seg[it.g + 1] - row0);
-            const int per = (nblk + a.splits - 1) / a.splits;
-            b0 = wk * per;
-            nb = max(0, min(per, nblk - b0));
+            const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
+            const uint32_t stage = tc::smem_u32(ring) + s * a.stage_bytes + (codes ? 0 : rows_unit * a.pitch);
+            uint32_t bytes = 0, len[4];
+            const uint8_t* from[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // at most 128 rows a unit
+                const int i = lane + 32 * j;
+                const int f = kMode == kGlu ? (it.tile * tiles_unit + (i >> 4)) * 8 + (i & 7) : it.tile * rows_unit + i;
+                const bool up = kMode == kGlu && (i & 8);
+                len[j] = 0;
+                if (i >= rows_unit || f >= a.N) continue;
+                const long long at = ((long long)it.g * a.N + f) * depth + blk0;
+                if (codes) {
+                    from[j] = (up ? a.codes2 : a.codes) + at * 16;
+                    len[j] = nblk * 16;
+                } else {
+                    const long long piece = at & ~15LL;
+                    const uint8_t* src = up ? a.scales2 : a.scales;
+                    from[j] = src + piece;
+                    len[j] = (uint32_t)(min((at + nblk + 15) & ~15LL, last) - piece);
+                    if (at + nblk > last) {
+                        for (long long k = max(at, last); k < at + nblk; ++k)
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(stage + i * a.scale_pitch + (uint32_t)(k - piece)), "r"((uint32_t)src[k]) : "memory");
+                        tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
+                    }
+                }
+                bytes += len[j];
+            }
+            bytes = __reduce_add_sync(0xffffffffu, bytes);
+            if (a.stall && codes && units == 0) bytes = 0;   // test hook: the first unit never arrives
+            else if (lane == 0) tc::mbar_expect_tx(full + s, bytes);
             __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (bytes && len[j]) bulk_load(stage + (lane + 32 * j) * (codes ? a.pitch : a.scale_pitch), from[j], len[j], full + s);
+            if (++s == a.stages) s = 0, ph ^= 1;
+        }
+        // no copy may be in flight when the CTA ends, also after a wait has expired
+        for (int i = 0; i < min(units, a.stages); ++i) {
+            if (--s < 0) s = a.stages - 1, ph ^= 1;
+            tc::mbar_wait(full + s, ph, ok ? lim : min(lim, 1LL << 10));
+        }
+    } else if (warp >= kWarps) {
+        // ---- sums of the consumers' shares, in order.  Output o of a unit is column o / 16 % kCols of
+        // tile o / (16 kCols), its row o % 16 or, for kGlu, such that neighbours hold a feature's gate
+        // and up (rows 0 to 7 and 8 to 15 of a tile).
+        constexpr int kLanes = 32 * kFinishWarps;
+        const int o0 = threadIdx.x - 32 * kWarps;
+        const int i = kMode == kGlu ? (o0 & 1) << 3 | (o0 >> 1 & 7) : o0 & 15;
+        const int outputs = tiles_unit * 16 * kCols;
+        int row0 = 0, nrows = 0;
+        for (; it.u < it.end; it.next(first)) {
+            if (it.fresh) {
+                row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols;
+                nrows = min(kCols, seg[it.g + 1] - row0);
+            }
+            if (!tc::mbar_wait_spin(done + buf, ph, lim)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const float* from = red + buf * (kWarps * S::kPart) + i;
+            for (int o = o0; o < outputs; o += kLanes) {
+                const int c = (o >> 4) & (kCols - 1), tile = o / (16 * kCols);
+                const float* p = from + (tile << a.split_log) * S::kPart + c * kLine;
+                float v[kWarps];
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v[0] += v[w];
+                if (kMode == kGlu) {
+                    const float u = __shfl_xor_sync(0xffffffffu, v[0], 1);
+                    const int f = (it.tile * tiles_unit + tile) * 8 + (i & 7);
+                    if (c >= nrows || f >= a.N) continue;
+                    const long long r = list[row0 + c];
+                    float* y = static_cast<float*>(a.y);
+                    if (a.slabs > 1) y[((it.slab * 2LL + (i >> 3)) * a.R + r) * a.ldy + f] = v[0];
+                    else if (i < 8) y[r * a.ldy + f] = situ_glu(v[0], u, a.beta1, a.beta2);
+                } else {
+                    const int f = it.tile * rows_unit + tile * 16 + i;
+                    if (c >= nrows || f >= a.N) continue;
+                    const long long r = (kMode == kDown ? (int)list[row0 + c] : row0 + c) + (long long)it.slab * a.R;
+                    if (kMode == kDown || a.y_type == QBMOE_F32) static_cast<float*>(a.y)[r * a.ldy + f] = v[0];
+                    else static_cast<__nv_bfloat16*>(a.y)[r * a.ldy + f] = __float2bfloat16_rn(v[0]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(freed + buf);
+            if (buf ^= 1, !buf) ph ^= 1;
+        }
+    } else {
+        // ---- consumers ----
+        const int wm = warp >> a.split_log, wk = warp & (a.splits - 1);
+        const int g8 = lane >> 2, t4 = lane & 3;
+        float* sx = sx_all + warp * (kNB * kCols);
+        if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
+        uint32_t B[kNB][kNG][4];
+        int b0 = 0, nb = 0, fph = 0;
+        uint32_t wat0 = 0, sat0 = 0, scale_at = 0;   // in stage 0: this lane's codes and scales; a row's first scale
+        const uint32_t scale_8 = kMode == kGlu ? 0 : 8 * depth;
+        for (; it.u < it.end; it.next(first)) {
+            if (it.fresh) {
+                const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
+                const int row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols, nrows = min(kCols, seg[it.g + 1] - row0);
+                const int per = ((nblk - 1) >> a.split_log) + 1;
+                b0 = wk * per;
+                nb = max(0, min(per, nblk - b0));
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kNG; ++j) {
+                    const int c = 8 * j + g8;
+                    const bool have = c < nrows;
+                    long long row = row0 + c;
+                    if (kRoutes) row = have ? list[row0 + c] : 0;
+                    if (kMode == kGlu) row = (int)row / a.k;
+                    // all loads of a batch before the first is used; blocks past the warp's share are zeros
+                    constexpr int kMost = kX == QBMOE_F32 ? 4 : 8, kBatch = kNB < kMost ? kNB : kMost;
+#pragma unroll
+                    for (int i0 = 0; i0 < kNB; i0 += kBatch) {
+                        Raw<kX> raw[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch && i0 + i < kNB; ++i) raw[i].load(a, row, blk0 + b0 + i0 + i, have && i0 + i < nb);
+#pragma unroll
+                        for (int i = 0; i < kBatch && i0 + i < kNB; ++i) {
+                            const float sc = raw[i].convert(B[i0 + i][j]);
+                            if (t4 == 0) sx[(i0 + i) * kCols + c] = sc;
+                        }
+                    }
+                }
+                __syncwarp();
+                const int q = lane >> 3, i = wm * 16 + g8;
+                wat0 = tc::smem_u32(ring) + (wm * 16 + (lane & 7) + (q & 1) * 8) * a.pitch + (b0 + (q >> 1)) * 16;
+                sat0 = tc::smem_u32(ring) + rows_unit * a.pitch + i * a.scale_pitch + b0;
+                const int f = kMode == kGlu ? (it.tile * tiles_unit + wm) * 8 + g8 : it.tile * rows_unit + i;
+                scale_at = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)f) * (uint32_t)depth + (uint32_t)blk0;
+            }
+            if (!tc::mbar_wait_spin(full + s, ph, lim)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            float acc[kNG][4] = {};
+            const uint32_t wat = wat0 + s * a.stage_bytes, sat = sat0 + s * a.stage_bytes;
+            // a row's scales start at a byte of their first 16
+            const uint32_t lo = sat + (scale_at & 15u), hi = sat + 8 * a.scale_pitch + ((scale_at + scale_8) & 15u);
+            scale_at += tile_rows * depth;
+            if (nb == kNB) share<kNB, kNG, false>(B, sx + 2 * t4, wat, lo, hi, nb, acc);
+            else share<kNB, kNG, true>(B, sx + 2 * t4, wat, lo, hi, nb, acc);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty + s);
+            if (++s == a.stages) s = 0, ph ^= 1;
+            if (!tc::mbar_wait_spin(freed + buf, fph ^ 1, lim)) ok = false;
+            float* mine = red + (buf * kWarps + warp) * S::kPart;
 #pragma unroll
             for (int j = 0; j < kNG; ++j) {
-                const int c = 8 * j + g8;
-                const bool have = c < nrows;
-                long long row = row0 + c;
-                if (kRoutes) row = have ? list[row0 + c] : 0;
-                if (kMode == kGlu) row = (int)row / a.k;
-                // all loads of a batch before the first is used
-                constexpr int kBatch = kX == QBMOE_F32 ? 4 : 8;
-#pragma unroll
-                for (int i0 = 0; i0 < kNB; i0 += kBatch) {
-                    if (i0 >= nb) break;   // the same for the whole warp
-                    Raw<kX> raw[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) raw[i].load(a, row, blk0 + b0 + i0 + i, have && i0 + i < nb);
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const float sc = raw[i].convert(B[i0 + i][j]);
-                        if (t4 == 0) sx[(i0 + i) * kCols + c] = sc;
-                    }
-                }
+                mine[(8 * j + 2 * t4) * kLine + g8] = acc[j][0];
+                mine[(8 * j + 2 * t4 + 1) * kLine + g8] = acc[j][1];
+                mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[j][2];
+                mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[j][3];
             }
             __syncwarp();
+            if (lane == 0) tc::mbar_arrive(done + buf);
+            if (buf ^= 1, !buf) fph ^= 1;
         }
-        if (!tc::mbar_wait_spin(full + s, ph, lim)) dead = true;
-        float acc[kNG][4] = {};
-        {
-            const uint32_t stage = tc::smem_u32(ring + (size_t)s * a.stage_bytes);
-            const int q = lane >> 3;
-            const uint32_t wat = stage + (wm * 16 + (lane & 7) + (q & 1) * 8) * a.pitch + (b0 + (q >> 1)) * 16;
-            // a row's scales start at a byte of their first 16: words of four, shifted into place
-            uint32_t sat[2], shift[2], sc[2], sw[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = wm * 16 + 8 * h + g8;
-                const int f = kMode == kGlu ? (it.tile * tiles_unit + wm) * 8 + g8 : it.tile * rows_unit + i;
-                const uint32_t start = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)f) * (uint32_t)depth + (uint32_t)blk0;
-                const uint32_t byte = stage + rows_unit * a.pitch + i * a.scale_pitch + (start & 15u) + b0;
-                sat[h] = byte & ~3u;
-                shift[h] = (byte & 3u) * 8;
-                sw[h] = lds32(sat[h]);
-            }
-            uint32_t next[4];
-            ldmatrix4(next, wat);
-#pragma unroll
-            for (int i = 0; i < kNB; i += 2) {
-                if (i >= nb) break;
-                uint32_t w[4] = {next[0], next[1], next[2], next[3]};
-                if (i + 2 < kNB) ldmatrix4(next, wat + (i + 2) * 16);   // what lies behind the row is not used
-                if (i % 4 == 0) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t up = lds32(sat[h] + i + 4);
-                        sc[h] = __funnelshift_r(sw[h], up, shift[h]);
-                        sw[h] = up;
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (i + h >= nb) break;
-                    uint32_t lo[4], hi[4];
-                    codes_to_f16(w[2 * h], lo);
-                    codes_to_f16(w[2 * h + 1], hi);
-                    float s0, s1;
-                    scale_pair(sc[0], sc[1], (i + h) & 3, s0, s1);
-#pragma unroll
-                    for (int j = 0; j < kNG; ++j) {
-                        float d[4] = {};
-                        mma_f16(d, lo[0], hi[0], lo[1], hi[1], B[i + h][j][0], B[i + h][j][1]);
-                        mma_f16(d, lo[2], hi[2], lo[3], hi[3], B[i + h][j][2], B[i + h][j][3]);
-                        const float2 x = *reinterpret_cast<const float2*>(sx + (i + h) * kCols + 8 * j + 2 * t4);
-                        acc[j][0] = fmaf(d[0] * x.x, s0, acc[j][0]);
-                        acc[j][1] = fmaf(d[1] * x.y, s0, acc[j][1]);
-                        acc[j][2] = fmaf(d[2] * x.x, s1, acc[j][2]);
-                        acc[j][3] = fmaf(d[3] * x.y, s1, acc[j][3]);
-                    }
-                }
-            }
-        }
-        // the warps' shares of the depth, added in order
-        float* mine = red + (buf * kWarps + warp) * S::kPart;
-#pragma unroll
-        for (int j = 0; j < kNG; ++j) {
-            mine[(8 * j + 2 * t4) * kLine + g8] = acc[j][0];
-            mine[(8 * j + 2 * t4 + 1) * kLine + g8] = acc[j][1];
-            mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[j][2];
-            mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[j][3];
-        }
-        if (__syncthreads_or(dead)) break;
-        // every warp is done with the stage: the next unit for it comes
-        if (ahead.u < ahead.end) bring_next(s);
-        if (++s == a.stages) s = 0, ph ^= 1;
-        for (int o = o0; o < outputs; o += kThreads >> parts_log) {
-            const int i = oi, c = (o >> 4) & (kCols - 1), m = o / (16 * kCols);
-            const float* from = red + (buf * kWarps + (m << a.split_log) + part) * S::kPart + c * kLine + i;
-            float v = 0.0f;
-#pragma unroll 4
-            for (int w = part; w < a.splits; w += parts, from += parts * S::kPart) v += *from;
-            if (parts_log > 0) v += __shfl_xor_sync(0xffffffffu, v, 1);
-            if (parts_log > 1) v += __shfl_xor_sync(0xffffffffu, v, 2);
-            if (kMode == kGlu) {
-                const float u = __shfl_xor_sync(0xffffffffu, v, parts);
-                const int f = (it.tile * tiles_unit + m) * 8 + (i & 7);
-                if (part || c >= nrows || f >= a.N) continue;
-                const long long r = list[row0 + c];
-                float* y = static_cast<float*>(a.y);
-                if (a.slabs > 1) y[((it.slab * 2LL + (i >> 3)) * a.R + r) * a.ldy + f] = v;
-                else if (i < 8) y[r * a.ldy + f] = situ_glu(v, u, a.beta1, a.beta2);
-                continue;
-            }
-            const int f = it.tile * rows_unit + m * 16 + i;
-            if (part || c >= nrows || f >= a.N) continue;
-            const long long r = (kMode == kDown ? (int)list[row0 + c] : row0 + c) + (long long)it.slab * a.R;
-            if (a.y_type == QBMOE_F32) static_cast<float*>(a.y)[r * a.ldy + f] = v;
-            else static_cast<__nv_bfloat16*>(a.y)[r * a.ldy + f] = __float2bfloat16_rn(v);
-        }
-        buf ^= 1;
     }
-    if (it.u < it.end) {   // a wait expired somewhere; no copy may be in flight when the CTA ends
-        if (dead && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
-        for (int i = 0; i < min(brought, a.stages); ++i)
-            tc::mbar_wait(full + i, ((brought - i + a.stages - 1) / a.stages - 1) & 1, lim);
-    }
+    if (!ok && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -648,16 +711,26 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs a
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kRingThird = 62 * 1024;   // of the shared memory that a call with few experts leaves
-constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that 16 warps hold in 16 blocks each
+constexpr int kSlabBlocks = 32 * kWarps;   // of 32: the deepest slab that the warps hold
 
 int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
 
+// Calls f with the shape whose warps hold `per` blocks of ng groups of 8 rows: the smallest of a
+// few sizes (what is beyond a warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n.
 template <typename F>
 int for_shape(int ng, int per, F f) {
-    if (ng == 2) return f(Shape<8, 2>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
-    if (per > 8) return f(Shape<16, 1>{}, std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    return f(Shape<8, 1>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+    if (ng == 2) {
+        if (per <= 4) return f(Shape<4, 2>{});
+        if (per <= 8) return f(Shape<8, 2>{});
+        if (per <= 14) return f(Shape<14, 2>{});
+        return f(Shape<16, 2>{});
+    }
+    if (per <= 4) return f(Shape<4, 1>{});
+    if (per <= 8) return f(Shape<8, 1>{});
+    if (per <= 14) return f(Shape<14, 1>{});
+    if (per <= 16) return f(Shape<16, 1>{});
+    if (per <= 28) return f(Shape<28, 1>{});
+    return f(Shape<32, 1>{});
 }
 
 // Geometry and launch.  Two groups of columns where experts have more than 8 rows on average
@@ -665,16 +738,13 @@ int for_shape(int ng, int per, F f) {
 template <int kX, int kMode>
 int stream(StreamArgs a, cudaStream_t s) {
     const int depth = a.K / 32;
-    const int ng = depth <= 128 && (long long)a.R > 8LL * a.E ? 2 : 1;
+    const int ng = depth <= 16 * kWarps && (long long)a.R > 8LL * a.E ? 2 : 1;
     a.slabs = slabs_of(a.K);
     a.slab_blocks = (depth + a.slabs - 1) / a.slabs;
     a.pitch = (a.slab_blocks | 1) * 16;                         // odd in 16 bytes: ldmatrix without bank conflicts
     a.scale_pitch = (((a.slab_blocks + 30) / 16) | 1) * 16;     // from any start within 16 bytes
-    // the fewest splits whose share a warp holds, and three units in flight
-    for (a.split_log = 0; a.split_log < 4; ++a.split_log) {
-        a.stage_bytes = 16 * (kWarps >> a.split_log) * (a.pitch + a.scale_pitch);
-        if (((a.slab_blocks - 1) >> a.split_log) + 1 <= 16 / ng && a.stage_bytes <= kRingThird) break;
-    }
+    // the fewest splits for which a warp's share is at most 16 blocks (a unit's fixed work then counts little) ..
+    while ((kWarps >> a.split_log) > 1 && (a.slab_blocks - 1) >> a.split_log >= 16) ++a.split_log;
     a.splits = 1 << a.split_log;
     const int per = ((a.slab_blocks - 1) >> a.split_log) + 1;
     const int rows = 16 * (kWarps / a.splits);
@@ -682,17 +752,17 @@ int stream(StreamArgs a, cudaStream_t s) {
     a.expiries = qbh::mx_expiries();
     a.wait_limit = qbh::mx_wait_limit();
     a.stall = qbh::mx_stall();
-    return for_shape(ng, per, [&](auto shape, auto nb, auto n) {
+    return for_shape(ng, per, [&](auto shape) {
         using S = decltype(shape);
         const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
         a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
         if (a.stages > kMaxStages) a.stages = kMaxStages;
-        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 64 KB that hist takes
+        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 48 KB that hist takes
         const int unit = kMode == kGlu ? rows / 2 : rows;
         long long units = 0x7fffffff;
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + S::kCols - 1) / S::kCols) * ((a.N + unit - 1) / unit) * a.slabs;
         const int grid = (int)min(units, (long long)qbh::sm_count());
-        const auto kern = k_stream<decltype(nb)::value, decltype(n)::value, kX, kMode>;
+        const auto kern = k_stream<S::kBlocks, S::kGroups, kX, kMode>;
         if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
         kern<<<grid, kThreads, smem, s>>>(a);
         return qbh::cuda_err(cudaGetLastError());
@@ -705,9 +775,11 @@ int set_smem() {
 }
 template <int kX, int kMode>
 int set_smem_all() {
-    int rc = set_smem<8, 1, kX, kMode>();
-    if (!rc) rc = set_smem<16, 1, kX, kMode>();
-    if (!rc) rc = set_smem<8, 2, kX, kMode>();
+    int rc = 0;
+    for (int ng = 1; ng <= 2; ++ng)
+        for (int per : {4, 8, 14, 16, 28, 32})
+            if (!rc && per <= 32 / ng)
+                rc = for_shape(ng, per, [](auto shape) { return set_smem<decltype(shape)::kBlocks, decltype(shape)::kGroups, kX, kMode>(); });
     return rc;
 }
 
