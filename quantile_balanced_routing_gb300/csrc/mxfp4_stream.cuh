@@ -1,0 +1,728 @@
+// MXFP4 weights streamed past a few rows: what moe_mxfp4_matvec and moe_mxfp4_experts share.
+//
+// One kernel brings weights through shared memory and multiplies them with a few rows that
+// stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is
+// 8 / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Eight
+// consumer warps divide the tiles and the depth: a warp owns a run of kNB blocks of 32 of K,
+// for which it holds the rows' elements as mma B operands, so that the rows cost no
+// bandwidth while weights go by.  Per block of 32 and tile:
+//   - ldmatrix hands each quad of lanes the 16 bytes of a weight row's block;
+//   - codes become fp16 (exact) two at a time, with one conversion;
+//   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
+//   - the block's dot products, times the two scales, are added in fp32.
+// Four service warps bring a unit's codes (TMA boxes of 128 bytes of every row; copies of
+// single rows cost 20 to 80 cycles each to issue) and scales several units ahead, add the
+// consumers' shares of the depth, in order, and store.
+// Weight rows are the M operand of the small mma because a column costs nothing that way: up
+// to 8 rows of x take as long as one.  tcgen05 would need its operands decoded in shared
+// memory, or x as E4M3 pairs (the layer's way: bound by issue at few columns).
+#pragma once
+
+#include "mxfp4.cuh"
+#include "mxfp4_decode.cuh"
+#include "tc_ptx.cuh"
+
+#include <cuda_fp16.h>
+
+#include <initializer_list>
+
+namespace {
+
+using namespace qb;
+
+constexpr int kWarps = 8, kService = 4;         // consumers and service warps: 168 registers a thread
+constexpr int kThreads = 32 * (kWarps + kService);
+constexpr int kMaxStages = 16;
+constexpr int kLine = 20;                      // floats a column of 16 results takes: stores without bank conflicts
+constexpr long long kDefaultWait = 1LL << 17;  // polls (<= 20 us each) before a wait expires
+constexpr int kMaxDynamic = 226 * 1024;       // of 227 KB, a little being static
+constexpr int kSlack = 128;                    // scales are read by the word, up to 8 bytes ahead
+
+// What a launch computes.
+enum { kStore, kGlu, kDown };
+constexpr int kBox = 8;                        // blocks of 32 in a row of a TMA box: 128 bytes of codes
+
+struct StreamArgs {
+    int R, E, N, K;              // rows of x, experts, weight rows (features of kGlu), depth
+    int x_type;
+    const void* x;               // kDown: fp32 [R, K]
+    long long ldx;
+    const uint8_t* x_scales;
+    CUtensorMap codes, codes2;           // [E N, K / 2] bytes; kGlu: gate and up
+    const uint8_t *scales, *scales2;     // [E, N, K / 32]
+    const int32_t* offsets;      // kStore: [E + 1] or NULL
+    const int32_t* idx;          // kGlu, kDown: routes [R]
+    int k;                       // kGlu: routes a token
+    int y_type;
+    void* y;                     // [slabs, R, N]; kGlu: fp32 [R, N], in slabs fp32 [slabs, 2, R, N]; kDown: fp32
+    long long ldy;
+    float beta1, beta2;
+    // geometry
+    int splits, split_log;       // consumers along the depth (a power of two); kWarps / splits tiles a unit
+    int slabs, slab_blocks;      // the depth in slabs of this many blocks of 32
+    int stages, stage_bytes;
+    int rows;                    // scales of a unit come row by row (slabs), else all together
+    int scale_pitch;             // bytes between the scales of its rows
+    int* expiries;
+    long long wait_limit;
+    int stall;
+};
+
+template <int kNB, int kNG>
+struct Shape {
+    static constexpr int kBlocks = kNB, kGroups = kNG;
+    static constexpr int kCols = 8 * kNG;                      // rows of x a unit takes
+    static constexpr int kPart = kCols * kLine + 8;            // floats of a warp's partial results
+    static constexpr int kRed = 2 * kWarps * kPart * 4;        // double buffered
+    static constexpr int kSx = kWarps * kNB * kCols * 4;       // scales of x
+    static constexpr int kBars = (kMaxStages + 4) * 8;
+    // before the ring, which starts at a multiple of 1024
+    static size_t fixed(int E, int routes) {
+        return kBars + kRed + kSx + qbh::align_up((size_t)(E + 1) * 8, 16) + (size_t)routes * 2 + 1024;
+    }
+};
+
+QB_DEV void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+// d = A B
+QB_DEV void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// d += A B
+QB_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+QB_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+QB_DEV uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+// Two E8M0 bytes, byte i of each word, as fp32 (0xFF: NaN).
+QB_DEV void scale_pair(uint32_t lo, uint32_t hi, int i, float& a, float& b) {
+    const uint32_t both = __byte_perm(lo, hi, (uint32_t)i | (uint32_t)(4 + i) << 4);
+    uint32_t h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, l;\n\t}" : "=r"(h) : "r"(both));
+    a = __uint_as_float(h << 16);
+    b = __uint_as_float(h & 0xffff0000u);
+}
+// (a x, b y), in one instruction.
+QB_DEV float2 mul2(float a, float b, float2 v) {
+    float2 r;
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a), "f"(b), "f"(v.x), "f"(v.y));
+    return r;
+}
+QB_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Rows of x as B operands.  Lane 4 c + t holds elements 8 t .. 8 t + 7 of column c's block:
+// the same share of K that ldmatrix gives lane 4 r + t of weight row r, so that the
+// products pair the right elements.
+// ---------------------------------------------------------------------------
+QB_DEV uint32_t f16_pair(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// A block whose largest magnitude m has these fp32 bits, as fp16: its largest element is put
+// into [2^15, 65504], so that a bf16 element is exact down to 2^-32 of it, and any element within
+// 2^-40 of it.  A block with an infinity or a NaN keeps those alone, which decide the result.
+QB_DEV float block_to_f16(const float (&v)[8], uint32_t m, uint32_t (&b)[4]) {
+    const int ef = max((int)((m + 0x1000u) >> 23), 16);   // of m rounded to fp16's 11 bits
+    const bool bad = m >= 0x7f800000u;
+    const float inv = __int_as_float((269 - ef) << 23);   // 2^(15 - exponent); not used when bad
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float p = v[2 * j] * inv, q = v[2 * j + 1] * inv;
+        if (bad) {
+            p = (__float_as_uint(v[2 * j]) & 0x7f800000u) == 0x7f800000u ? v[2 * j] : 0.0f;
+            q = (__float_as_uint(v[2 * j + 1]) & 0x7f800000u) == 0x7f800000u ? v[2 * j + 1] : 0.0f;
+        }
+        b[j] = f16_pair(p, q);
+    }
+    return bad ? 1.0f : __int_as_float((ef - 15) << 23);
+}
+// This lane's 8 elements of a block as they are stored: 16 bytes of bf16, 8 of E4M3 and a
+// scale byte, or 32 of fp32.
+template <int kX>
+struct Raw {
+    uint4 u, v;
+    QB_DEV void load(const StreamArgs& a, long long row, int blk, bool have) {
+        const int at = blk * 32 + 8 * (threadIdx.x & 3);
+        u = v = make_uint4(0, 0, 0, 0);
+        if (!have) return;
+        if (kX == QBMOE_MXFP8) {
+            const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + row * a.ldx + at);
+            u.x = q.x;
+            u.y = q.y;
+            u.z = a.x_scales[row * (a.K >> 5) + blk];
+        } else if (kX == QBMOE_F32) {   // from the kernel before
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + row * a.ldx + at);
+            u = __ldcg(p);
+            v = __ldcg(p + 1);
+        } else {
+            u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + row * a.ldx + at);
+        }
+    }
+    // The four pairs of fp16 and (in every lane of the quad) the block's scale.
+    QB_DEV float convert(uint32_t (&b)[4]) const {
+        if (kX == QBMOE_MXFP8) {
+            asm("{\n\t.reg .b16 p, q, r, s;\n\tmov.b32 {p, q}, %4;\n\tmov.b32 {r, s}, %5;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %0, p;\n\tcvt.rn.f16x2.e4m3x2 %1, q;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %2, r;\n\tcvt.rn.f16x2.e4m3x2 %3, s;\n\t}"
+                : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                : "r"(u.x), "r"(u.y));
+            return e8m0_value(u.z);
+        }
+        float f[8];
+        const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = __uint_as_float(kX == QBMOE_F32 ? w[j] : j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        return block_to_f16(f, m, b);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Which rows belong together.
+// ---------------------------------------------------------------------------
+
+// Whole CTA: a[0 .. n - 1] to its exclusive sums, the total in a[n].
+QB_DEV void exclusive_scan(int* a, int n, int* scratch /* [kThreads / 32] */) {
+    constexpr int W = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = ((n + W - 1) / W + 31) & ~31;
+    __syncthreads();
+    int run = 0;
+    for (int i0 = warp * per; i0 < min(n, (warp + 1) * per); i0 += 32) {
+        const int v = i0 + lane < n ? a[i0 + lane] : 0;
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (i0 + lane < n) a[i0 + lane] = run + incl - v;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) scratch[warp] = run;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    for (int i = warp * per + lane; i < min(n, (warp + 1) * per); i += 32) a[i] += before;
+    if (threadIdx.x == 0) a[n] = total;
+    __syncthreads();
+}
+
+// seg [E + 1]: first row of each expert (kGlu, kDown: place in list, the routes in expert
+// order); first [E + 1]: its first chunk of kCols rows.  Offsets out of order or out of
+// range are clamped, so that every chunk lies inside [0, R).  Every CTA makes the same list, in the
+// order of the routes: hist [warps][E] (in the ring, which nothing uses yet) counts each
+// warp's share of them.
+template <int kMode, int kCols>
+QB_DEV void group_rows(const StreamArgs& a, int* seg, int* first, uint16_t* list, int* hist, int* scratch) {
+    if (kMode == kGlu || kMode == kDown) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int warps = min(kThreads / 32, (a.R + 31) >> 5), per = ((a.R + warps - 1) / warps + 31) & ~31;
+        for (int i = threadIdx.x; i < warps * a.E; i += kThreads) hist[i] = 0;
+        __syncthreads();
+        for (int r = warp * per + lane; r < min(a.R, (warp + 1) * per); r += 32) {
+            const int e = __ldg(a.idx + r);
+            if (e >= 0 && e < a.E) atomicAdd(hist + warp * a.E + e, 1);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += kThreads) {
+            int n = 0;
+            for (int w = 0; w < warps; ++w) {
+                const int c = hist[w * a.E + e];
+                hist[w * a.E + e] = n;
+                n += c;
+            }
+            seg[e] = n | ((n + kCols - 1) / kCols) << 16;   // both sums at once: at most 4096 routes, and no more chunks
+        }
+        exclusive_scan(seg, a.E, scratch);
+        for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+            const int both = seg[e];
+            first[e] = both >> 16;
+            seg[e] = both & 0xffff;
+        }
+        __syncthreads();
+        for (int r0 = warp * per; r0 < min(a.R, (warp + 1) * per); r0 += 32) {
+            const int r = r0 + lane, e = r < a.R ? __ldg(a.idx + r) : -1;
+            const bool route = e >= 0 && e < a.E;
+            const uint32_t same = __match_any_sync(0xffffffffu, route ? e : -1), before = same & ((1u << lane) - 1);
+            int at = 0;
+            if (route) {
+                at = hist[warp * a.E + e];
+                list[seg[e] + at + __popc(before)] = (uint16_t)r;
+            }
+            __syncwarp();
+            if (route && !before) hist[warp * a.E + e] = at + __popc(same);
+            __syncwarp();
+        }
+        tc::fence_proxy_async_smem();   // bulk copies write the ring next
+        __syncthreads();
+    } else if (!a.offsets) {
+        if (threadIdx.x == 0) seg[0] = 0, seg[1] = a.R, first[0] = 0, first[1] = (a.R + kCols - 1) / kCols;
+        __syncthreads();
+    } else {
+        for (int e = threadIdx.x; e <= a.E; e += kThreads) seg[e] = min(max(__ldg(a.offsets + e), 0), a.R);
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += kThreads) first[e] = (max(seg[e + 1] - seg[e], 0) + kCols - 1) / kCols;
+        exclusive_scan(first, a.E, scratch);
+    }
+}
+
+// Walks this CTA's run of units: tiles fastest, then chunks of rows, then slabs of the depth.
+struct Units {
+    long long u, end;
+    int tile, tiles, chunk, chunks, slab;
+    int g;                 // expert of the chunk
+    bool fresh;            // the rows changed
+    QB_DEV void start(const int* first, int E, int tiles_, int slabs) {
+        tiles = tiles_;
+        chunks = first[E];
+        const long long total = (long long)chunks * tiles * slabs;
+        u = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
+        if (u >= end) return;
+        tile = (int)(u % tiles);
+        const long long c = u / tiles;
+        chunk = (int)(c % chunks);
+        slab = (int)(c / chunks);
+        g = 0;             // the last expert whose first chunk is not behind this one
+        for (int hi = E; hi - g > 1;) {
+            const int mid = (g + hi) >> 1;
+            if (first[mid] <= chunk) g = mid; else hi = mid;
+        }
+        fresh = true;
+    }
+    QB_DEV void next(const int* first) {
+        ++u;
+        fresh = false;
+        if (++tile < tiles || u >= end) return;
+        tile = 0;
+        fresh = true;
+        if (++chunk == chunks) chunk = 0, ++slab, g = 0;
+        while (first[g + 1] <= chunk) ++g;
+    }
+};
+
+// A warp's share of a tile: 16 weight rows times kNB blocks of K.  wat[p]: where this lane's row of
+// the four 8 x 16-byte matrices that the p-th ldmatrix loads (two blocks of 16 rows) lies, boxes
+// of four such loads apart by `box` bytes; lo, hi: the scales of weight rows lane / 4 and 8 more.
+// kSome: only nb blocks are the warp's; for the rest B and the scales of x are zeros, and the
+// weights' scales, whatever lies there, are cleared lest one be NaN.
+template <int kNB, int kNG, bool kSome>
+QB_DEV void share(const uint32_t (&B)[kNB][kNG][4], const float* sx, const uint32_t (&wat)[4], uint32_t box, uint32_t lo,
+                  uint32_t hi, int nb, float (&acc)[kNG][4]) {
+    uint32_t sat[2] = {lo & ~3u, hi & ~3u}, shift[2] = {(lo & 3u) * 8, (hi & 3u) * 8}, sw[2], sc[2], next[4];
+    sw[0] = lds32(sat[0]);
+    sw[1] = lds32(sat[1]);
+    if (!kSome || nb > 0) ldmatrix4(next, wat[0]);
+    uint32_t boxes = 0;
+#pragma unroll
+    for (int i = 0; i < kNB; i += 2) {
+        if (kSome && i >= nb) break;
+        const uint32_t w[4] = {next[0], next[1], next[2], next[3]};
+        if (i % 8 == 6) boxes += box;
+        if (i + 2 < kNB && (!kSome || i + 2 < nb)) ldmatrix4(next, wat[(i / 2 + 1) % 4] + boxes);
+        if (i % 4 == 0) {   // the scales of four blocks, shifted into place
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t up = lds32(sat[h] + i + 4);
+                sc[h] = __funnelshift_r(sw[h], up, shift[h]);
+                if (kSome && nb - i < 4) sc[h] &= (1u << 8 * (nb - i)) - 1;
+                sw[h] = up;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t p[4], q[4];
+            codes_to_f16(w[2 * h], p);
+            codes_to_f16(w[2 * h + 1], q);
+            float s0, s1;
+            scale_pair(sc[0], sc[1], (i + h) & 3, s0, s1);
+#pragma unroll
+            for (int j = 0; j < kNG; ++j) {
+                float d[4];
+                mma_f16_first(d, p[0], q[0], p[1], q[1], B[i + h][j][0], B[i + h][j][1]);
+                mma_f16(d, p[2], q[2], p[3], q[3], B[i + h][j][2], B[i + h][j][3]);
+                const float2 x = *reinterpret_cast<const float2*>(sx + (i + h) * (8 * kNG) + 8 * j);
+                const float2 u = mul2(d[0], d[1], x), v = mul2(d[2], d[3], x);
+                acc[j][0] = fmaf(u.x, s0, acc[j][0]);
+                acc[j][1] = fmaf(u.y, s0, acc[j][1]);
+                acc[j][2] = fmaf(v.x, s1, acc[j][2]);
+                acc[j][3] = fmaf(v.y, s1, acc[j][3]);
+            }
+        }
+    }
+}
+
+template <int kNB, int kNG, int kX, int kMode>
+__global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ StreamArgs a) {
+    using S = Shape<kNB, kNG>;
+    constexpr int kCols = S::kCols;
+    constexpr bool kRoutes = kMode == kGlu || kMode == kDown;
+    extern __shared__ __align__(128) char sm[];
+    __shared__ int scratch[kThreads / 32];
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm);   // a unit's copies have landed
+    uint64_t* done = full + kMaxStages;                 // [2]: the consumers have read it, and written their shares of the sums
+    uint64_t* freed = done + 2;                         // [2]: the sums are formed
+    float* red = reinterpret_cast<float*>(sm + S::kBars);
+    float* sx_all = red + S::kRed / 4;
+    int* seg = reinterpret_cast<int*>(sx_all + S::kSx / 4);
+    int* first = seg + a.E + 1;
+    uint16_t* list = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(seg) + (((a.E + 1) * 8 + 15) & ~15));
+    char* ring = reinterpret_cast<char*>(list) + (kRoutes ? a.R * 2 : 0);
+    ring += -tc::smem_u32(ring) & 1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
+    if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) tc::mbar_init(full + s, kService);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(done + i, kWarps);
+            tc::mbar_init(freed + i, kService);
+        }
+        tc::fence_mbar_init();
+    }
+    group_rows<kMode, kCols>(a, seg, first, list, reinterpret_cast<int*>(ring), scratch);   // with barriers for the whole CTA
+    // A stage: boxes of [rows_unit][128] swizzled bytes of codes, then scales.  kGlu: rows_unit / 2 rows
+    // of gate, then as many of up, in codes and scales alike; a tile is 8 of each.
+    const int depth = a.K >> 5;                               // blocks of a weight row
+    const int tiles_unit = kWarps >> a.split_log, rows_unit = 16 * tiles_unit;
+    const int features = kMode == kGlu ? 8 * tiles_unit : rows_unit;   // of a unit
+    const int box_bytes = rows_unit * 128, code_bytes = (a.slab_blocks + kBox - 1) / kBox * box_bytes;
+    // scales of the second half of a tile are this far behind the first's
+    const int half_bytes = kMode == kGlu ? (8 * tiles_unit * a.scale_pitch + 31) & ~15 : 8 * a.scale_pitch;
+    bool ok = true;               // no wait of this warp has expired
+    int s = 0, ph = 0, buf = 0;
+    Units it;
+    it.start(first, a.E, (a.N + features - 1) / features, a.slabs);
+
+    if (warp >= kWarps) {
+        // ---- service ----
+        const int me = warp - kWarps;
+        const long long last = ((long long)a.E * a.N * depth) & ~15LL;   // the end of the scales' last whole piece of 16 bytes
+        Units ahead = it;
+        int brought = 0, to = 0;
+        // This warp's part of the next unit's copies: every fourth box; the last warp also the scales.
+        // Scales start anywhere, so the 16-byte pieces that hold them are copied, except behind the
+        // tensor's last whole piece, where bytes go one by one.
+        auto bring = [&] {
+            const int blk0 = ahead.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0), boxes = (nblk + kBox - 1) / kBox;
+            const int f0 = ahead.tile * features, row0 = ahead.g * a.N + f0, rows = min(features, a.N - f0);
+            const uint32_t stage = tc::smem_u32(ring) + to * a.stage_bytes, sdst = stage + code_bytes;
+            uint64_t* bar = full + to;
+            uint32_t bytes = me < boxes ? ((boxes - 1 - me) / kService + 1) * box_bytes : 0;
+            const bool scales = me == kService - 1;
+            const int jobs = a.rows ? rows_unit : kMode == kGlu ? 2 : 1;   // runs of scales
+            // job j: `n` scales from `at` of their tensor on, to the piece at `dst`
+            auto job = [&](int j, long long& at, int& n, uint32_t& dst, const uint8_t*& from) {
+                const int half = kMode == kGlu ? (a.rows ? j / (8 * tiles_unit) : j) : 0, i = a.rows ? j - half * 8 * tiles_unit : 0;
+                at = (long long)(row0 + i) * depth + blk0;
+                n = i >= rows ? 0 : a.rows ? nblk : rows * depth;
+                dst = sdst + half * half_bytes + i * a.scale_pitch;
+                from = half ? a.scales2 : a.scales;
+            };
+            long long at;
+            int n;
+            uint32_t dst;
+            const uint8_t* from;
+            if (scales) {
+                uint32_t mine = 0;
+                for (int j = lane; j < jobs; j += 32) {
+                    job(j, at, n, dst, from);
+                    if (!n) continue;
+                    const long long piece = at & ~15LL;
+                    mine += (uint32_t)(min((at + n + 15) & ~15LL, last) - piece);
+                    if (at + n > last) {
+                        for (long long k = max(at, last); k < at + n; ++k)
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + (uint32_t)(k - piece)), "r"((uint32_t)from[k]) : "memory");
+                        tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
+                    }
+                }
+                bytes += __reduce_add_sync(0xffffffffu, mine);
+                __syncwarp();
+            }
+            if (!(a.stall && me == 0 && brought == 0)) {   // test hook: the first unit never arrives
+                if (lane == 0) {
+                    tc::mbar_expect_tx(bar, bytes);
+                    for (int b = me; b < boxes; b += kService) {
+                        const int x = (blk0 + b * kBox) * 16;
+                        tc::tma_load_2d(ring + to * a.stage_bytes + b * box_bytes, &a.codes, bar, x, row0);
+                        if (kMode == kGlu) tc::tma_load_2d(ring + to * a.stage_bytes + b * box_bytes + box_bytes / 2, &a.codes2, bar, x, row0);
+                    }
+                }
+                __syncwarp();
+                if (scales)
+                    for (int j = lane; j < jobs; j += 32) {
+                        job(j, at, n, dst, from);
+                        const long long piece = at & ~15LL;
+                        const uint32_t len = n ? (uint32_t)(min((at + n + 15) & ~15LL, last) - piece) : 0;
+                        if (len) bulk_load(dst, from + piece, len, bar);
+                    }
+            }
+            ++brought;
+            if (++to == a.stages) to = 0;
+            ahead.next(first);
+        };
+        for (int i = 0; i < a.stages && ahead.u < ahead.end; ++i) bring();
+
+        // Output o of a unit is column o / 16 % kCols of tile o / (16 kCols), its row o % 16 or, for kGlu,
+        // such that neighbours hold a feature's gate and up (rows 0 to 7 and 8 to 15 of a tile).
+        constexpr int kLanes = 32 * kService;
+        const int o0 = threadIdx.x - 32 * kWarps;
+        const int i = kMode == kGlu ? (o0 & 1) << 3 | (o0 >> 1 & 7) : o0 & 15;
+        const int outputs = tiles_unit * 16 * kCols;
+        int row0 = 0, nrows = 0;
+        for (; it.u < it.end; it.next(first)) {
+            if (it.fresh) {
+                row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols;
+                nrows = min(kCols, seg[it.g + 1] - row0);
+            }
+            if (!tc::mbar_wait(done + buf, ph, lim)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            if (ahead.u < ahead.end) bring();
+            const float* from = red + buf * (kWarps * S::kPart) + i;
+            for (int o = o0; o < outputs; o += kLanes) {
+                const int c = (o >> 4) & (kCols - 1), tile = o / (16 * kCols);
+                const float* p = from + (tile << a.split_log) * S::kPart + c * kLine;
+                float v[kWarps];
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) v[0] += v[w];
+                if (kMode == kGlu) {
+                    const float u = __shfl_xor_sync(0xffffffffu, v[0], 1);
+                    const int f = it.tile * features + tile * 8 + (i & 7);
+                    if (c >= nrows || f >= a.N) continue;
+                    const long long r = list[row0 + c];
+                    float* y = static_cast<float*>(a.y);
+                    if (a.slabs > 1) y[((it.slab * 2LL + (i >> 3)) * a.R + r) * a.ldy + f] = v[0];
+                    else if (i < 8) y[r * a.ldy + f] = situ_glu(v[0], u, a.beta1, a.beta2);
+                } else {
+                    const int f = it.tile * features + tile * 16 + i;
+                    if (c >= nrows || f >= a.N) continue;
+                    const long long r = (kMode == kDown ? (int)list[row0 + c] : row0 + c) + (long long)it.slab * a.R;
+                    if (kMode == kDown || a.y_type == QBMOE_F32) static_cast<float*>(a.y)[r * a.ldy + f] = v[0];
+                    else static_cast<__nv_bfloat16*>(a.y)[r * a.ldy + f] = __float2bfloat16_rn(v[0]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(freed + buf);
+            if (buf ^= 1, !buf) ph ^= 1;
+        }
+        if (!ok)   // no copy may be in flight when the CTA ends
+            for (int j = 0; j < min(brought, a.stages); ++j)
+                tc::mbar_wait(full + j, ((brought - j + a.stages - 1) / a.stages - 1) & 1, min(lim, 1LL << 10));
+    } else {
+        // ---- consumers ----
+        const int wm = warp >> a.split_log, wk = warp & (a.splits - 1);
+        const int g8 = lane >> 2, t4 = lane & 3;
+        float* sx = sx_all + warp * (kNB * kCols);
+        if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
+        uint32_t B[kNB][kNG][4];
+        int nb = 0, fph = 0;
+        uint32_t wat0[4], sat0 = 0, scale_at = 0;   // in stage 0: this lane's codes and scales; the unit's first scale
+        for (; it.u < it.end; it.next(first)) {
+            if (it.fresh) {
+                const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
+                const int row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols, nrows = min(kCols, seg[it.g + 1] - row0);
+                const int per = (((nblk - 1) >> a.split_log) + 2) & ~1;   // even: an ldmatrix does not leave its box
+                const int b0 = wk * per;
+                nb = max(0, min(per, nblk - b0));
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kNG; ++j) {
+                    const int c = 8 * j + g8;
+                    const bool have = c < nrows;
+                    long long row = row0 + c;
+                    if (kRoutes) row = have ? list[row0 + c] : 0;
+                    if (kMode == kGlu) row = (int)row / a.k;
+                    // all loads of a batch before the first is used; blocks past the warp's share are zeros
+                    constexpr int kMost = kX == QBMOE_F32 ? 4 : 8, kBatch = kNB < kMost ? kNB : kMost;
+#pragma unroll
+                    for (int i0 = 0; i0 < kNB; i0 += kBatch) {
+                        Raw<kX> raw[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch && i0 + i < kNB; ++i) raw[i].load(a, row, blk0 + b0 + i0 + i, have && i0 + i < nb);
+#pragma unroll
+                        for (int i = 0; i < kBatch && i0 + i < kNB; ++i) {
+                            const float sc = raw[i].convert(B[i0 + i][j]);
+                            if (t4 == 0) sx[(i0 + i) * kCols + c] = sc;
+                        }
+                    }
+                }
+                __syncwarp();
+                // ldmatrix: lanes 8 q .. 8 q + 7 give the rows of matrix q: rows 0 to 7 or 8 to 15 of block 0 or 1
+                const int q = lane >> 3, half = q & 1, r = (kMode == kGlu ? 8 * (wm + half * tiles_unit) : 16 * wm + 8 * half) + (lane & 7);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {   // box rows of 128 bytes, their 16-byte pieces swizzled
+                    const int b = b0 + 2 * p + (q >> 1);
+                    wat0[p] = tc::smem_u32(ring) + (b / kBox) * box_bytes + r * 128 + (((b & (kBox - 1)) ^ (r & 7)) << 4);
+                }
+                sat0 = tc::smem_u32(ring) + code_bytes + ((kMode == kGlu ? 8 : 16) * wm + g8) * a.scale_pitch + b0;
+                // row by row, each row's scales have a start of their own
+                const int f = it.tile * features + (a.rows ? (kMode == kGlu ? 8 : 16) * wm + g8 : 0);
+                scale_at = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)f) * (uint32_t)depth + (uint32_t)blk0;
+            }
+            if (!tc::mbar_wait_spin(full + s, ph, lim)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            float acc[kNG][4] = {};
+            const uint32_t off = s * a.stage_bytes, sat = sat0 + off;
+            const uint32_t wat[4] = {wat0[0] + off, wat0[1] + off, wat0[2] + off, wat0[3] + off};
+            // scales start at a byte of their first 16
+            const uint32_t lo = sat + (scale_at & 15u);
+            const uint32_t hi = sat + half_bytes + ((scale_at + (a.rows && kMode != kGlu ? 8 * depth : 0)) & 15u);
+            scale_at += features * depth;
+            if (nb == kNB) share<kNB, kNG, false>(B, sx + 2 * t4, wat, box_bytes, lo, hi, nb, acc);
+            else share<kNB, kNG, true>(B, sx + 2 * t4, wat, box_bytes, lo, hi, nb, acc);
+            if (++s == a.stages) s = 0, ph ^= 1;
+            if (!tc::mbar_wait_spin(freed + buf, fph ^ 1, lim)) ok = false;
+            float* mine = red + (buf * kWarps + warp) * S::kPart;
+#pragma unroll
+            for (int j = 0; j < kNG; ++j) {
+                mine[(8 * j + 2 * t4) * kLine + g8] = acc[j][0];
+                mine[(8 * j + 2 * t4 + 1) * kLine + g8] = acc[j][1];
+                mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[j][2];
+                mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[j][3];
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(done + buf);
+            if (buf ^= 1, !buf) fph ^= 1;
+        }
+    }
+    if (!ok && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr int kSlabBlocks = 32 * kWarps;   // of 32: the deepest slab that the warps hold
+
+int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
+
+// Calls f with the shape whose warps hold `per` blocks of ng groups of 8 rows: the smallest of a
+// few sizes (what is beyond a warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n.
+// Calls f with the shape whose warps hold `per` blocks of ng groups of 8 rows: the smallest of a
+// few sizes (what is beyond a warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n.
+template <typename F>
+int for_shape(int ng, int per, F f) {
+    if (ng == 2) {
+        if (per <= 8) return f(Shape<8, 2>{});
+        if (per <= 14) return f(Shape<14, 2>{});
+        return f(Shape<16, 2>{});
+    }
+    if (per <= 4) return f(Shape<4, 1>{});
+    if (per <= 8) return f(Shape<8, 1>{});
+    if (per <= 14) return f(Shape<14, 1>{});
+    if (per <= 16) return f(Shape<16, 1>{});
+    if (per <= 28) return f(Shape<28, 1>{});
+    return f(Shape<32, 1>{});
+}
+
+// Geometry and launch; codes (kGlu: gate) and codes2 (up) are the weights' [E, N, K / 2].  Two
+// groups of columns where experts have more than 8 rows on average and the depth allows it.
+template <int kX, int kMode>
+int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream_t s) {
+    const int depth = a.K / 32;
+    const int ng = depth <= 16 * kWarps && (long long)a.R > 8LL * a.E ? 2 : 1;
+    a.slabs = slabs_of(a.K);
+    a.slab_blocks = ((depth + a.slabs - 1) / a.slabs + kBox - 1) / kBox * kBox;   // whole boxes
+    a.slab_blocks = min(a.slab_blocks, depth);
+    // the fewest splits for which a warp's share is at most 16 blocks
+    while ((kWarps >> a.split_log) > 1 && (a.slab_blocks - 1) >> a.split_log >= 16) ++a.split_log;
+    a.splits = 1 << a.split_log;
+    const int per = (((a.slab_blocks - 1) >> a.split_log) + 2) & ~1;
+    const int rows = 16 * (kWarps / a.splits), box_rows = kMode == kGlu ? rows / 2 : rows;
+    a.rows = a.slabs > 1;
+    // row by row: pieces that hold a slab's scales from any start within 16 bytes, an odd number of
+    // 16 bytes apart, so that eight rows lie in different banks
+    a.scale_pitch = a.rows ? (((a.slab_blocks + 30) / 16) | 1) * 16 : depth;
+    a.stage_bytes = (int)qbh::align_up((size_t)(a.slab_blocks + kBox - 1) / kBox * rows * 128 + rows * a.scale_pitch + 64, 1024);
+    a.expiries = qbh::mx_expiries();
+    a.wait_limit = qbh::mx_wait_limit();
+    a.stall = qbh::mx_stall();
+    const long long w_rows = (long long)a.E * a.N;
+    if (!qbh::encode_rows(&a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows)) return QBMOE_ECUDA;
+    if (codes2 && !qbh::encode_rows(&a.codes2, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes2, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows))
+        return QBMOE_ECUDA;
+    return for_shape(ng, per, [&](auto shape) {
+        using S = decltype(shape);
+        const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
+        a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
+        if (a.stages > kMaxStages) a.stages = kMaxStages;
+        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 48 KB that hist takes
+        long long units = 0x7fffffff;
+        if (kMode == kStore && !a.offsets) units = (((long long)a.R + S::kCols - 1) / S::kCols) * ((a.N + rows - 1) / rows) * a.slabs;
+        const int grid = (int)min(units, (long long)qbh::sm_count());
+        const auto kern = k_stream<S::kBlocks, S::kGroups, kX, kMode>;
+        if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
+        kern<<<grid, kThreads, smem, s>>>(a);
+        return qbh::cuda_err(cudaGetLastError());
+    });
+}
+
+template <int kNB, int kNG, int kX, int kMode>
+int set_smem() {
+    return qbh::cuda_err(cudaFuncSetAttribute(k_stream<kNB, kNG, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
+}
+template <int kX, int kMode>
+int set_smem_all() {
+    int rc = 0;
+    for (int ng = 1; ng <= 2; ++ng)
+        for (int per : {4, 8, 14, 16, 28, 32})
+            if (!rc && per <= 32 / ng)
+                rc = for_shape(ng, per, [](auto shape) { return set_smem<decltype(shape)::kBlocks, decltype(shape)::kGroups, kX, kMode>(); });
+    return rc;
+}
+
+constexpr int kMaxCols = 1 << 24;
+bool rows_ok(int K, int x_type, long long ldx) {
+    return x_type == QBMOE_MXFP8 ? ldx == K : x_type == QBMOE_BF16 && ldx >= K && ldx % 8 == 0;
+}
+bool depth_ok(int K) { return K >= 32 && K % 32 == 0 && K <= QBMOE_MATVEC_MAX_K; }
+bool all_aligned16(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!p || !qbh::aligned16(p)) return false;
+    return true;
+}
+bool at_bytes(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
