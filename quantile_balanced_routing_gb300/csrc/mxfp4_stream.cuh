@@ -2,7 +2,7 @@
 //
 // One kernel brings weights through shared memory and multiplies them with a few rows that
 // stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is
-// 8 / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Eight
+// kMT 8 / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Eight
 // consumer warps divide the tiles and the depth: a warp owns a run of kNB blocks of 32 of K,
 // for which it holds the rows' elements as mma B operands, so that the rows cost no
 // bandwidth while weights go by.  Per block of 32 and tile:
@@ -10,9 +10,9 @@
 //   - codes become fp16 (exact) two at a time, with one conversion;
 //   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
 //   - the block's dot products, times the two scales, are added in fp32.
-// Four service warps bring a unit's codes (TMA boxes of 128 bytes of every row; copies of
-// single rows cost 20 to 80 cycles each to issue) and scales several units ahead, add the
-// consumers' shares of the depth, in order, and store.
+// Two producer warps, a unit each in turn, bring its codes (TMA boxes of 128 bytes of every
+// row; a copy costs 20 to 80 cycles to issue, so not one for every row) and scales several units
+// ahead; two more add the consumers' shares of the depth, in order, and store.
 // Weight rows are the M operand of the small mma because a column costs nothing that way: up
 // to 8 rows of x take as long as one.  tcgen05 would need its operands decoded in shared
 // memory, or x as E4M3 pairs (the layer's way: bound by issue at few columns).
@@ -30,8 +30,8 @@ namespace {
 
 using namespace qb;
 
-constexpr int kWarps = 8, kService = 4;         // consumers and service warps: 168 registers a thread
-constexpr int kThreads = 32 * (kWarps + kService);
+constexpr int kWarps = 8;                      // consumers; then two producers and two that sum
+constexpr int kThreads = 32 * (kWarps + 4);    // 168 registers a thread
 constexpr int kMaxStages = 16;
 constexpr int kLine = 20;                      // floats a column of 16 results takes: stores without bank conflicts
 constexpr long long kDefaultWait = 1LL << 17;  // polls (<= 20 us each) before a wait expires
@@ -58,7 +58,7 @@ struct StreamArgs {
     long long ldy;
     float beta1, beta2;
     // geometry
-    int splits, split_log;       // consumers along the depth (a power of two); kWarps / splits tiles a unit
+    int splits, split_log;       // consumers along the depth (a power of two)
     int slabs, slab_blocks;      // the depth in slabs of this many blocks of 32
     int stages, stage_bytes;
     int rows;                    // scales of a unit come row by row (slabs), else all together
@@ -68,14 +68,14 @@ struct StreamArgs {
     int stall;
 };
 
-template <int kNB, int kNG>
+template <int kNB, int kNG, int kMT>
 struct Shape {
-    static constexpr int kBlocks = kNB, kGroups = kNG;
+    static constexpr int kBlocks = kNB, kGroups = kNG, kTiles = kMT;
     static constexpr int kCols = 8 * kNG;                      // rows of x a unit takes
     static constexpr int kPart = kCols * kLine + 8;            // floats of a warp's partial results
-    static constexpr int kRed = 2 * kWarps * kPart * 4;        // double buffered
+    static constexpr int kRed = 2 * kWarps * kMT * kPart * 4;  // double buffered
     static constexpr int kSx = kWarps * kNB * kCols * 4;       // scales of x
-    static constexpr int kBars = (kMaxStages + 4) * 8;
+    static constexpr int kBars = (2 * kMaxStages + 4) * 8;
     // before the ring, which starts at a multiple of 1024
     static size_t fixed(int E, int routes) {
         return kBars + kRed + kSx + qbh::align_up((size_t)(E + 1) * 8, 16) + (size_t)routes * 2 + 1024;
@@ -387,15 +387,16 @@ QB_DEV void share(const uint32_t (&B)[kNB][kNG][4], const float* sx, const uint3
     }
 }
 
-template <int kNB, int kNG, int kX, int kMode>
+template <int kNB, int kNG, int kMT, int kX, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ StreamArgs a) {
-    using S = Shape<kNB, kNG>;
+    using S = Shape<kNB, kNG, kMT>;
     constexpr int kCols = S::kCols;
     constexpr bool kRoutes = kMode == kGlu || kMode == kDown;
     extern __shared__ __align__(128) char sm[];
     __shared__ int scratch[kThreads / 32];
     uint64_t* full = reinterpret_cast<uint64_t*>(sm);   // a unit's copies have landed
-    uint64_t* done = full + kMaxStages;                 // [2]: the consumers have read it, and written their shares of the sums
+    uint64_t* empty = full + kMaxStages;                // its consumers have read it
+    uint64_t* done = empty + kMaxStages;                // [2]: they have written their shares of the sums
     uint64_t* freed = done + 2;                         // [2]: the sums are formed
     float* red = reinterpret_cast<float*>(sm + S::kBars);
     float* sx_all = red + S::kRed / 4;
@@ -408,10 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
     if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
     if (threadIdx.x == 0) {
-        for (int s = 0; s < a.stages; ++s) tc::mbar_init(full + s, kService);
+        for (int s = 0; s < a.stages; ++s) {
+            tc::mbar_init(full + s, 1);
+            tc::mbar_init(empty + s, kWarps);
+        }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(done + i, kWarps);
-            tc::mbar_init(freed + i, kService);
+            tc::mbar_init(freed + i, 1);
         }
         tc::fence_mbar_init();
     }
@@ -419,107 +423,107 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     // A stage: boxes of [rows_unit][128] swizzled bytes of codes, then scales.  kGlu: rows_unit / 2 rows
     // of gate, then as many of up, in codes and scales alike; a tile is 8 of each.
     const int depth = a.K >> 5;                               // blocks of a weight row
-    const int tiles_unit = kWarps >> a.split_log, rows_unit = 16 * tiles_unit;
+    const int tiles_unit = kMT * kWarps >> a.split_log, rows_unit = 16 * tiles_unit;
     const int features = kMode == kGlu ? 8 * tiles_unit : rows_unit;   // of a unit
     const int box_bytes = rows_unit * 128, code_bytes = (a.slab_blocks + kBox - 1) / kBox * box_bytes;
     // scales of the second half of a tile are this far behind the first's
     const int half_bytes = kMode == kGlu ? (8 * tiles_unit * a.scale_pitch + 31) & ~15 : 8 * a.scale_pitch;
     bool ok = true;               // no wait of this warp has expired
-    int s = 0, ph = 0, buf = 0;
+    int s = 0, ph = 0;
     Units it;
     it.start(first, a.E, (a.N + features - 1) / features, a.slabs);
 
-    if (warp >= kWarps) {
-        // ---- service ----
+    if (warp >= kWarps && warp < kWarps + 2) {
+        // ---- producers: units in turn ----
         const int me = warp - kWarps;
         const long long last = ((long long)a.E * a.N * depth) & ~15LL;   // the end of the scales' last whole piece of 16 bytes
-        Units ahead = it;
-        int brought = 0, to = 0;
-        // This warp's part of the next unit's copies: every fourth box; the last warp also the scales.
-        // Scales start anywhere, so the 16-byte pieces that hold them are copied, except behind the
-        // tensor's last whole piece, where bytes go one by one.
-        auto bring = [&] {
-            const int blk0 = ahead.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0), boxes = (nblk + kBox - 1) / kBox;
-            const int f0 = ahead.tile * features, row0 = ahead.g * a.N + f0, rows = min(features, a.N - f0);
-            const uint32_t stage = tc::smem_u32(ring) + to * a.stage_bytes, sdst = stage + code_bytes;
-            uint64_t* bar = full + to;
-            uint32_t bytes = me < boxes ? ((boxes - 1 - me) / kService + 1) * box_bytes : 0;
-            const bool scales = me == kService - 1;
-            const int jobs = a.rows ? rows_unit : kMode == kGlu ? 2 : 1;   // runs of scales
-            // job j: `n` scales from `at` of their tensor on, to the piece at `dst`
-            auto job = [&](int j, long long& at, int& n, uint32_t& dst, const uint8_t*& from) {
-                const int half = kMode == kGlu ? (a.rows ? j / (8 * tiles_unit) : j) : 0, i = a.rows ? j - half * 8 * tiles_unit : 0;
-                at = (long long)(row0 + i) * depth + blk0;
-                n = i >= rows ? 0 : a.rows ? nblk : rows * depth;
-                dst = sdst + half * half_bytes + i * a.scale_pitch;
-                from = half ? a.scales2 : a.scales;
-            };
-            long long at;
-            int n;
-            uint32_t dst;
-            const uint8_t* from;
-            if (scales) {
-                uint32_t mine = 0;
-                for (int j = lane; j < jobs; j += 32) {
-                    job(j, at, n, dst, from);
-                    if (!n) continue;
-                    const long long piece = at & ~15LL;
-                    mine += (uint32_t)(min((at + n + 15) & ~15LL, last) - piece);
-                    if (at + n > last) {
-                        for (long long k = max(at, last); k < at + n; ++k)
-                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + (uint32_t)(k - piece)), "r"((uint32_t)from[k]) : "memory");
-                        tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
-                    }
-                }
-                bytes += __reduce_add_sync(0xffffffffu, mine);
-                __syncwarp();
-            }
-            if (!(a.stall && me == 0 && brought == 0)) {   // test hook: the first unit never arrives
-                if (lane == 0) {
-                    tc::mbar_expect_tx(bar, bytes);
-                    for (int b = me; b < boxes; b += kService) {
-                        const int x = (blk0 + b * kBox) * 16;
-                        tc::tma_load_2d(ring + to * a.stage_bytes + b * box_bytes, &a.codes, bar, x, row0);
-                        if (kMode == kGlu) tc::tma_load_2d(ring + to * a.stage_bytes + b * box_bytes + box_bytes / 2, &a.codes2, bar, x, row0);
-                    }
-                }
-                __syncwarp();
-                if (scales)
-                    for (int j = lane; j < jobs; j += 32) {
-                        job(j, at, n, dst, from);
-                        const long long piece = at & ~15LL;
-                        const uint32_t len = n ? (uint32_t)(min((at + n + 15) & ~15LL, last) - piece) : 0;
-                        if (len) bulk_load(dst, from + piece, len, bar);
-                    }
-            }
-            ++brought;
-            if (++to == a.stages) to = 0;
-            ahead.next(first);
-        };
-        for (int i = 0; i < a.stages && ahead.u < ahead.end; ++i) bring();
-
-        // Output o of a unit is column o / 16 % kCols of tile o / (16 kCols), its row o % 16 or, for kGlu,
-        // such that neighbours hold a feature's gate and up (rows 0 to 7 and 8 to 15 of a tile).
-        constexpr int kLanes = 32 * kService;
-        const int o0 = threadIdx.x - 32 * kWarps;
-        const int i = kMode == kGlu ? (o0 & 1) << 3 | (o0 >> 1 & 7) : o0 & 15;
-        const int outputs = tiles_unit * 16 * kCols;
-        int row0 = 0, nrows = 0;
-        for (; it.u < it.end; it.next(first)) {
-            if (it.fresh) {
-                row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols;
-                nrows = min(kCols, seg[it.g + 1] - row0);
-            }
-            if (!tc::mbar_wait(done + buf, ph, lim)) ok = false;
+        const int jobs = a.rows ? rows_unit : kMode == kGlu ? 2 : 1;     // runs of scales
+        int n = 0;
+        for (; it.u < it.end; it.next(first), ++n) {
+            const bool mine = (n & 1) == me;
+            const uint32_t to = s * a.stage_bytes;
+            uint64_t* bar = full + s;
+            if (mine && n >= a.stages && !tc::mbar_wait(empty + s, ph ^ 1, lim)) ok = false;
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
-            if (ahead.u < ahead.end) bring();
-            const float* from = red + buf * (kWarps * S::kPart) + i;
-            for (int o = o0; o < outputs; o += kLanes) {
+            if (++s == a.stages) s = 0, ph ^= 1;
+            if (!mine || (a.stall && n == 0)) continue;   // test hook: the first unit never arrives
+            const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0), boxes = (nblk + kBox - 1) / kBox;
+            const int f0 = it.tile * features, row0 = it.g * a.N + f0, rows = min(features, a.N - f0);
+            // Scales start anywhere, so the 16-byte pieces that hold them are copied, except behind the
+            // tensor's last whole piece, where bytes go one by one.  Run j: `n` scales from `at` of their
+            // tensor on, to the piece at `dst`.
+            auto run = [&](int j, long long& at, int& count, uint32_t& dst, const uint8_t*& from) {
+                const int half = kMode == kGlu ? (a.rows ? j / (8 * tiles_unit) : j) : 0, i = a.rows ? j - half * 8 * tiles_unit : 0;
+                at = (long long)(row0 + i) * depth + blk0;
+                count = i >= rows ? 0 : a.rows ? nblk : rows * depth;
+                dst = tc::smem_u32(ring) + to + code_bytes + half * half_bytes + i * a.scale_pitch;
+                from = half ? a.scales2 : a.scales;
+            };
+            long long at;
+            int count;
+            uint32_t dst, bytes = 0;
+            const uint8_t* from;
+            for (int j = lane; j < jobs; j += 32) {
+                run(j, at, count, dst, from);
+                if (!count) continue;
+                const long long piece = at & ~15LL;
+                bytes += (uint32_t)(min((at + count + 15) & ~15LL, last) - piece);
+                if (at + count > last) {
+                    for (long long k = max(at, last); k < at + count; ++k)
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + (uint32_t)(k - piece)), "r"((uint32_t)from[k]) : "memory");
+                    tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
+                }
+            }
+            bytes = __reduce_add_sync(0xffffffffu, bytes) + boxes * box_bytes;
+            if (lane == 0) {
+                tc::mbar_expect_tx(bar, bytes);
+                for (int b = 0; b < boxes; ++b) {
+                    const int x = (blk0 + b * kBox) * 16;
+                    tc::tma_load_2d(ring + to + b * box_bytes, &a.codes, bar, x, row0);
+                    if (kMode == kGlu) tc::tma_load_2d(ring + to + b * box_bytes + box_bytes / 2, &a.codes2, bar, x, row0);
+                }
+            }
+            __syncwarp();
+            for (int j = lane; j < jobs; j += 32) {
+                run(j, at, count, dst, from);
+                const long long piece = at & ~15LL;
+                const uint32_t len = count ? (uint32_t)(min((at + count + 15) & ~15LL, last) - piece) : 0;
+                if (len) bulk_load(dst, from + piece, len, bar);
+            }
+        }
+        if (!ok)   // no copy may be in flight when the CTA ends
+            for (int j = 0; j < min(n, a.stages); ++j)
+                tc::mbar_wait(full + j, ((n - j + a.stages - 1) / a.stages - 1) & 1, min(lim, 1LL << 10));
+    } else if (warp >= kWarps) {
+        // ---- sums of the consumers' shares, in order, a unit in turn.  Output o of a unit is column
+        // o / 16 % kCols of tile o / (16 kCols), its row o % 16 or, for kGlu, such that neighbours hold
+        // a feature's gate and up (rows 0 to 7 and 8 to 15 of a tile).
+        const int me = warp - kWarps - 2;
+        const int i = kMode == kGlu ? (lane & 1) << 3 | (lane >> 1 & 7) : lane & 15;
+        const int outputs = tiles_unit * 16 * kCols;
+        const float* base = red + me * (kWarps * kMT * S::kPart) + i;
+        int row0 = 0, nrows = 0, n = 0;
+        bool fresh = false;
+        for (; it.u < it.end; it.next(first), ++n) {
+            fresh |= it.fresh;
+            if ((n & 1) != me) continue;
+            if (fresh) {
+                row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols;
+                nrows = min(kCols, seg[it.g + 1] - row0);
+                fresh = false;
+            }
+            if (!tc::mbar_wait(done + me, ph, lim)) ok = false;
+            ph ^= 1;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            for (int o = lane; o < outputs; o += 32) {
                 const int c = (o >> 4) & (kCols - 1), tile = o / (16 * kCols);
-                const float* p = from + (tile << a.split_log) * S::kPart + c * kLine;
+                const float* p = base + (tile << a.split_log) * S::kPart + c * kLine;
                 float v[kWarps];
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
@@ -542,12 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 }
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(freed + buf);
-            if (buf ^= 1, !buf) ph ^= 1;
+            if (lane == 0) tc::mbar_arrive(freed + me);
         }
-        if (!ok)   // no copy may be in flight when the CTA ends
-            for (int j = 0; j < min(brought, a.stages); ++j)
-                tc::mbar_wait(full + j, ((brought - j + a.stages - 1) / a.stages - 1) & 1, min(lim, 1LL << 10));
     } else {
         // ---- consumers ----
         const int wm = warp >> a.split_log, wk = warp & (a.splits - 1);
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
         float* sx = sx_all + warp * (kNB * kCols);
         if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
         uint32_t B[kNB][kNG][4];
-        int nb = 0, fph = 0;
+        int nb = 0, buf = 0, fph = 0;
         uint32_t wat0[4], sat0 = 0, scale_at = 0;   // in stage 0: this lane's codes and scales; the unit's first scale
         for (; it.u < it.end; it.next(first)) {
             if (it.fresh) {
@@ -604,24 +604,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 ok = false;
                 break;
             }
-            float acc[kNG][4] = {};
-            const uint32_t off = s * a.stage_bytes, sat = sat0 + off;
-            const uint32_t wat[4] = {wat0[0] + off, wat0[1] + off, wat0[2] + off, wat0[3] + off};
+            const int apart = (kWarps >> a.split_log) * (kMode == kGlu ? 8 : 16);   // rows between this warp's tiles
+            const uint32_t off = s * a.stage_bytes;
             // scales start at a byte of their first 16
-            const uint32_t lo = sat + (scale_at & 15u);
-            const uint32_t hi = sat + half_bytes + ((scale_at + (a.rows && kMode != kGlu ? 8 * depth : 0)) & 15u);
+            const uint32_t in = scale_at & 15u, in_hi = (scale_at + (a.rows && kMode != kGlu ? 8 * depth : 0)) & 15u;
+            float acc[kMT][kNG][4] = {};
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                const uint32_t at = off + m * apart * 128, sat = sat0 + off + m * apart * a.scale_pitch;
+                const uint32_t wat[4] = {wat0[0] + at, wat0[1] + at, wat0[2] + at, wat0[3] + at};
+                // (row by row, apart depth is a multiple of 16: all tiles of the warp start alike)
+                if (nb == kNB) share<kNB, kNG, false>(B, sx + 2 * t4, wat, box_bytes, sat + in, sat + half_bytes + in_hi, nb, acc[m]);
+                else share<kNB, kNG, true>(B, sx + 2 * t4, wat, box_bytes, sat + in, sat + half_bytes + in_hi, nb, acc[m]);
+            }
             scale_at += features * depth;
-            if (nb == kNB) share<kNB, kNG, false>(B, sx + 2 * t4, wat, box_bytes, lo, hi, nb, acc);
-            else share<kNB, kNG, true>(B, sx + 2 * t4, wat, box_bytes, lo, hi, nb, acc);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty + s);
             if (++s == a.stages) s = 0, ph ^= 1;
             if (!tc::mbar_wait_spin(freed + buf, fph ^ 1, lim)) ok = false;
-            float* mine = red + (buf * kWarps + warp) * S::kPart;
 #pragma unroll
-            for (int j = 0; j < kNG; ++j) {
-                mine[(8 * j + 2 * t4) * kLine + g8] = acc[j][0];
-                mine[(8 * j + 2 * t4 + 1) * kLine + g8] = acc[j][1];
-                mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[j][2];
-                mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[j][3];
+            for (int m = 0; m < kMT; ++m) {
+                float* mine = red + ((buf * kMT + m) * kWarps + warp) * S::kPart;
+#pragma unroll
+                for (int j = 0; j < kNG; ++j) {
+                    mine[(8 * j + 2 * t4) * kLine + g8] = acc[m][j][0];
+                    mine[(8 * j + 2 * t4 + 1) * kLine + g8] = acc[m][j][1];
+                    mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[m][j][2];
+                    mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[m][j][3];
+                }
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(done + buf);
@@ -640,21 +650,20 @@ int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
 
 // Calls f with the shape whose warps hold `per` blocks of ng groups of 8 rows: the smallest of a
 // few sizes (what is beyond a warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n.
-// Calls f with the shape whose warps hold `per` blocks of ng groups of 8 rows: the smallest of a
-// few sizes (what is beyond a warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n.
+// Two tiles a warp, where three units of that size fit, halve what a unit costs besides.
 template <typename F>
 int for_shape(int ng, int per, F f) {
     if (ng == 2) {
-        if (per <= 8) return f(Shape<8, 2>{});
-        if (per <= 14) return f(Shape<14, 2>{});
-        return f(Shape<16, 2>{});
+        if (per <= 8) return f(Shape<8, 2, 2>{});
+        if (per <= 14) return f(Shape<14, 2, 1>{});
+        return f(Shape<16, 2, 1>{});
     }
-    if (per <= 4) return f(Shape<4, 1>{});
-    if (per <= 8) return f(Shape<8, 1>{});
-    if (per <= 14) return f(Shape<14, 1>{});
-    if (per <= 16) return f(Shape<16, 1>{});
-    if (per <= 28) return f(Shape<28, 1>{});
-    return f(Shape<32, 1>{});
+    if (per <= 4) return f(Shape<4, 1, 2>{});
+    if (per <= 8) return f(Shape<8, 1, 2>{});
+    if (per <= 14) return f(Shape<14, 1, 2>{});
+    if (per <= 16) return f(Shape<16, 1, 1>{});
+    if (per <= 28) return f(Shape<28, 1, 1>{});
+    return f(Shape<32, 1, 1>{});
 }
 
 // Geometry and launch; codes (kGlu: gate) and codes2 (up) are the weights' [E, N, K / 2].  Two
@@ -666,25 +675,25 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
     a.slabs = slabs_of(a.K);
     a.slab_blocks = ((depth + a.slabs - 1) / a.slabs + kBox - 1) / kBox * kBox;   // whole boxes
     a.slab_blocks = min(a.slab_blocks, depth);
-    // the fewest splits for which a warp's share is at most 16 blocks
-    while ((kWarps >> a.split_log) > 1 && (a.slab_blocks - 1) >> a.split_log >= 16) ++a.split_log;
+    // the fewest splits for which a warp's share is at most 16 blocks, and a unit at most 128 rows
+    for (a.split_log = 1; (kWarps >> a.split_log) > 1 && (a.slab_blocks - 1) >> a.split_log >= 16;) ++a.split_log;
     a.splits = 1 << a.split_log;
     const int per = (((a.slab_blocks - 1) >> a.split_log) + 2) & ~1;
-    const int rows = 16 * (kWarps / a.splits), box_rows = kMode == kGlu ? rows / 2 : rows;
     a.rows = a.slabs > 1;
     // row by row: pieces that hold a slab's scales from any start within 16 bytes, an odd number of
     // 16 bytes apart, so that eight rows lie in different banks
     a.scale_pitch = a.rows ? (((a.slab_blocks + 30) / 16) | 1) * 16 : depth;
-    a.stage_bytes = (int)qbh::align_up((size_t)(a.slab_blocks + kBox - 1) / kBox * rows * 128 + rows * a.scale_pitch + 64, 1024);
     a.expiries = qbh::mx_expiries();
     a.wait_limit = qbh::mx_wait_limit();
     a.stall = qbh::mx_stall();
-    const long long w_rows = (long long)a.E * a.N;
-    if (!qbh::encode_rows(&a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows)) return QBMOE_ECUDA;
-    if (codes2 && !qbh::encode_rows(&a.codes2, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes2, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows))
-        return QBMOE_ECUDA;
-    return for_shape(ng, per, [&](auto shape) {
+    return for_shape(ng, per, [&](auto shape) -> int {
         using S = decltype(shape);
+        const int rows = 16 * S::kTiles * (kWarps / a.splits), box_rows = kMode == kGlu ? rows / 2 : rows;
+        const long long w_rows = (long long)a.E * a.N;
+        if (!qbh::encode_rows(&a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows)) return QBMOE_ECUDA;
+        if (codes2 && !qbh::encode_rows(&a.codes2, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes2, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows))
+            return QBMOE_ECUDA;
+        a.stage_bytes = (int)qbh::align_up((size_t)(a.slab_blocks + kBox - 1) / kBox * rows * 128 + rows * a.scale_pitch + 64, 1024);
         const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
         a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
         if (a.stages > kMaxStages) a.stages = kMaxStages;
@@ -692,16 +701,16 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
         long long units = 0x7fffffff;
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + S::kCols - 1) / S::kCols) * ((a.N + rows - 1) / rows) * a.slabs;
         const int grid = (int)min(units, (long long)qbh::sm_count());
-        const auto kern = k_stream<S::kBlocks, S::kGroups, kX, kMode>;
+        const auto kern = k_stream<S::kBlocks, S::kGroups, S::kTiles, kX, kMode>;
         if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
         kern<<<grid, kThreads, smem, s>>>(a);
         return qbh::cuda_err(cudaGetLastError());
     });
 }
 
-template <int kNB, int kNG, int kX, int kMode>
+template <int kNB, int kNG, int kMT, int kX, int kMode>
 int set_smem() {
-    return qbh::cuda_err(cudaFuncSetAttribute(k_stream<kNB, kNG, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
+    return qbh::cuda_err(cudaFuncSetAttribute(k_stream<kNB, kNG, kMT, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
 }
 template <int kX, int kMode>
 int set_smem_all() {
@@ -709,7 +718,7 @@ int set_smem_all() {
     for (int ng = 1; ng <= 2; ++ng)
         for (int per : {4, 8, 14, 16, 28, 32})
             if (!rc && per <= 32 / ng)
-                rc = for_shape(ng, per, [](auto shape) { return set_smem<decltype(shape)::kBlocks, decltype(shape)::kGroups, kX, kMode>(); });
+                rc = for_shape(ng, per, [](auto shape) { return set_smem<decltype(shape)::kBlocks, decltype(shape)::kGroups, decltype(shape)::kTiles, kX, kMode>(); });
     return rc;
 }
 
