@@ -1,18 +1,20 @@
 // MXFP4 weights streamed past a few rows: what moe_mxfp4_matvec and moe_mxfp4_experts share.
 //
 // One kernel brings weights through shared memory and multiplies them with a few rows that
-// stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is
-// kMT 8 / splits tiles of 16 weight rows over the whole depth (or one slab of it).  Eight
-// consumer warps divide the tiles and the depth: a warp owns a run of kNB blocks of 32 of K,
-// for which it holds the rows' elements as mma B operands, so that the rows cost no
-// bandwidth while weights go by.  Per block of 32 and tile:
+// stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is kMT
+// tiles of 16 weight rows over the whole depth (or one slab of it).  Sixteen consumer warps
+// (four a scheduler hide the chain of load, conversion, product and sum; eight with 168
+// registers took half as long again) form groups that take units in turn, so that one group's
+// fixed work per unit falls into another's products.  The warps of a group divide the depth: a
+// warp owns a run of kNB blocks of 32 of K, for which it holds the rows' elements as mma B
+// operands, so that the rows cost no bandwidth while weights go by.  Per block of 32 and tile:
 //   - ldmatrix hands each quad of lanes the 16 bytes of a weight row's block;
 //   - codes become fp16 (exact) two at a time, with one conversion;
 //   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
 //   - the block's dot products, times the two scales, are added in fp32.
-// Two producer warps, a unit each in turn, bring its codes (TMA boxes of 128 bytes of every
-// row; a copy costs 20 to 80 cycles to issue, so not one for every row) and scales several units
-// ahead; two more add the consumers' shares of the depth, in order, and store.
+// Two producer warps, a unit each in turn, bring its codes (long rows one by one, short ones
+// in TMA boxes: a copy costs 20 to 80 cycles to issue) and scales several units ahead; two more
+// add the consumers' shares of the depth, in order, and store.
 // Weight rows are the M operand of the small mma because a column costs nothing that way: up
 // to 8 rows of x take as long as one.  tcgen05 would need its operands decoded in shared
 // memory, or x as E4M3 pairs (the layer's way: bound by issue at few columns).
@@ -30,8 +32,9 @@ namespace {
 
 using namespace qb;
 
-constexpr int kWarps = 8;                      // consumers; then two producers and two that sum
-constexpr int kThreads = 32 * (kWarps + 4);    // 168 registers a thread
+constexpr int kWarps = 16, kWarpsLog = 4;      // consumers; then two producers and two that sum
+constexpr int kThreads = 32 * (kWarps + 4);    // 96 registers a thread
+constexpr int kCols = 8;                       // rows of x a unit takes
 constexpr int kMaxStages = 16;
 constexpr int kLine = 20;                      // floats a column of 16 results takes: stores without bank conflicts
 constexpr long long kDefaultWait = 1LL << 17;  // polls (<= 20 us each) before a wait expires
@@ -49,6 +52,7 @@ struct StreamArgs {
     long long ldx;
     const uint8_t* x_scales;
     CUtensorMap codes, codes2;           // [E N, K / 2] bytes; kGlu: gate and up
+    const uint8_t *w, *w2;               // the same, for copies of single rows
     const uint8_t *scales, *scales2;     // [E, N, K / 32]
     const int32_t* offsets;      // kStore: [E + 1] or NULL
     const int32_t* idx;          // kGlu, kDown: routes [R]
@@ -58,9 +62,10 @@ struct StreamArgs {
     long long ldy;
     float beta1, beta2;
     // geometry
-    int splits, split_log;       // consumers along the depth (a power of two)
+    int splits, split_log;       // consumers along the depth (a power of two): a group
     int slabs, slab_blocks;      // the depth in slabs of this many blocks of 32
     int stages, stage_bytes;
+    int pitch;                   // bytes between the rows of a unit that come one by one; 0: they come in boxes
     int rows;                    // scales of a unit come row by row (slabs), else all together
     int scale_pitch;             // bytes between the scales of its rows
     int* expiries;
@@ -68,14 +73,15 @@ struct StreamArgs {
     int stall;
 };
 
-template <int kNB, int kNG, int kMT>
+// kNB blocks of 32 a warp, kMT tiles a unit.  Up to a box of blocks, weights come in boxes.
+template <int kNB, int kMT>
 struct Shape {
-    static constexpr int kBlocks = kNB, kGroups = kNG, kTiles = kMT;
-    static constexpr int kCols = 8 * kNG;                      // rows of x a unit takes
+    static constexpr int kBlocks = kNB, kTiles = kMT;
+    static constexpr bool kBoxes = kNB <= kBox;
     static constexpr int kPart = kCols * kLine + 8;            // floats of a warp's partial results
-    static constexpr int kRed = 2 * kWarps * kMT * kPart * 4;  // double buffered
+    static constexpr int kRed = 2 * kWarps * kMT * kPart * 4;  // two slots a group
     static constexpr int kSx = kWarps * kNB * kCols * 4;       // scales of x
-    static constexpr int kBars = (2 * kMaxStages + 4) * 8;
+    static constexpr int kBars = (2 * kMaxStages + 4 * kWarps) * 8;
     // before the ring, which starts at a multiple of 1024
     static size_t fixed(int E, int routes) {
         return kBars + kRed + kSx + qbh::align_up((size_t)(E + 1) * 8, 16) + (size_t)routes * 2 + 1024;
@@ -111,11 +117,11 @@ QB_DEV uint32_t lds32(uint32_t addr) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
-// Two E8M0 bytes, byte i of each word, as fp32 (0xFF: NaN).
-QB_DEV void scale_pair(uint32_t lo, uint32_t hi, int i, float& a, float& b) {
-    const uint32_t both = __byte_perm(lo, hi, (uint32_t)i | (uint32_t)(4 + i) << 4);
+// Two E8M0 bytes of a word, the low two or the high two, as fp32 (0xFF: NaN).
+QB_DEV void scale_pair(uint32_t word, bool high, float& a, float& b) {
     uint32_t h;
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, l;\n\t}" : "=r"(h) : "r"(both));
+    if (high) asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, u;\n\t}" : "=r"(h) : "r"(word));
+    else asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, l;\n\t}" : "=r"(h) : "r"(word));
     a = __uint_as_float(h << 16);
     b = __uint_as_float(h & 0xffff0000u);
 }
@@ -247,14 +253,14 @@ QB_DEV void exclusive_scan(int* a, int n, int* scratch /* [kThreads / 32] */) {
 // range are clamped, so that every chunk lies inside [0, R).  Every CTA makes the same list, in the
 // order of the routes: hist [warps][E] (in the ring, which nothing uses yet) counts each
 // warp's share of them.
-template <int kMode, int kCols>
+template <int kMode>
 QB_DEV void group_rows(const StreamArgs& a, int* seg, int* first, uint16_t* list, int* hist, int* scratch) {
     if (kMode == kGlu || kMode == kDown) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int warps = min(kThreads / 32, (a.R + 31) >> 5), per = ((a.R + warps - 1) / warps + 31) & ~31;
+        const int warps = min(8, (a.R + 31) >> 5), per = ((a.R + warps - 1) / warps + 31) & ~31;
         for (int i = threadIdx.x; i < warps * a.E; i += kThreads) hist[i] = 0;
         __syncthreads();
-        for (int r = warp * per + lane; r < min(a.R, (warp + 1) * per); r += 32) {
+        for (int r = warp * per + lane; r < min(a.R, (warp + 1) * per) && warp < warps; r += 32) {
             const int e = __ldg(a.idx + r);
             if (e >= 0 && e < a.E) atomicAdd(hist + warp * a.E + e, 1);
         }
@@ -275,7 +281,7 @@ QB_DEV void group_rows(const StreamArgs& a, int* seg, int* first, uint16_t* list
             seg[e] = both & 0xffff;
         }
         __syncthreads();
-        for (int r0 = warp * per; r0 < min(a.R, (warp + 1) * per); r0 += 32) {
+        for (int r0 = warp * per; r0 < min(a.R, (warp + 1) * per) && warp < warps; r0 += 32) {
             const int r = r0 + lane, e = r < a.R ? __ldg(a.idx + r) : -1;
             const bool route = e >= 0 && e < a.E;
             const uint32_t same = __match_any_sync(0xffffffffu, route ? e : -1), before = same & ((1u << lane) - 1);
@@ -336,68 +342,82 @@ struct Units {
     }
 };
 
-// A warp's share of a tile: 16 weight rows times kNB blocks of K.  wat[p]: where this lane's row of
-// the four 8 x 16-byte matrices that the p-th ldmatrix loads (two blocks of 16 rows) lies, boxes
-// of four such loads apart by `box` bytes; lo, hi: the scales of weight rows lane / 4 and 8 more.
-// kSome: only nb blocks are the warp's; for the rest B and the scales of x are zeros, and the
-// weights' scales, whatever lies there, are cleared lest one be NaN.
-template <int kNB, int kNG, bool kSome>
-QB_DEV void share(const uint32_t (&B)[kNB][kNG][4], const float* sx, const uint32_t (&wat)[4], uint32_t box, uint32_t lo,
-                  uint32_t hi, int nb, float (&acc)[kNG][4]) {
-    uint32_t sat[2] = {lo & ~3u, hi & ~3u}, shift[2] = {(lo & 3u) * 8, (hi & 3u) * 8}, sw[2], sc[2], next[4];
-    sw[0] = lds32(sat[0]);
-    sw[1] = lds32(sat[1]);
-    if (!kSome || nb > 0) ldmatrix4(next, wat[0]);
-    uint32_t boxes = 0;
+// A warp's share of kMT tiles: each 16 weight rows times kNB blocks of K.  wat: this lane's row of the
+// four 8 x 16-byte matrices that an ldmatrix loads (two blocks of 16 rows), of every of the first four
+// loads in a box, whose 16-byte pieces are swizzled, else of the first alone; lo, hi: the scales of
+// weight rows lane / 4 and 8 more; tiles apart by `tile` bytes of codes and `tile_sc` of scales.  kSome:
+// only nb blocks are the warp's; for the rest B and the scales of x are zeros, and the weights'
+// scales, whatever lies there, are cleared lest one be NaN.
+template <int kNB, int kMT, bool kSome>
+QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (&wat)[4], uint32_t tile, uint32_t lo, uint32_t hi,
+                  uint32_t tile_sc, int nb, float (&acc)[kMT][4]) {
+    constexpr bool kBoxes = kNB <= kBox;
+    auto load = [&](uint32_t (&w)[4], int i, int m) { ldmatrix4(w, (kBoxes ? wat[i / 2 % 4] : wat[0] + i * 16) + m * tile); };
+    uint32_t sat[kMT][2], shift[kMT][2], sw[kMT][2], sc[kMT][2], next[kMT][4];
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t byte = (h ? hi : lo) + m * tile_sc;
+            sat[m][h] = byte & ~3u;
+            shift[m][h] = (byte & 3u) * 8;
+            sw[m][h] = lds32(sat[m][h]);
+        }
+        if (!kSome || nb > 0) load(next[m], 0, m);
+    }
 #pragma unroll
     for (int i = 0; i < kNB; i += 2) {
         if (kSome && i >= nb) break;
-        const uint32_t w[4] = {next[0], next[1], next[2], next[3]};
-        if (i % 8 == 6) boxes += box;
-        if (i + 2 < kNB && (!kSome || i + 2 < nb)) ldmatrix4(next, wat[(i / 2 + 1) % 4] + boxes);
-        if (i % 4 == 0) {   // the scales of four blocks, shifted into place
+        uint32_t w[kMT][4];
+        float wsc[kMT][2][2];   // scales of rows lane / 4 and 8 more, two blocks each
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[m][j] = next[m][j];
+            if (i + 2 < kNB && (!kSome || i + 2 < nb)) load(next[m], i + 2, m);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t up = lds32(sat[h] + i + 4);
-                sc[h] = __funnelshift_r(sw[h], up, shift[h]);
-                if (kSome && nb - i < 4) sc[h] &= (1u << 8 * (nb - i)) - 1;
-                sw[h] = up;
+                if (i % 4 == 0) {   // the scales of four blocks, shifted into place
+                    const uint32_t up = lds32(sat[m][h] + i + 4);
+                    sc[m][h] = __funnelshift_r(sw[m][h], up, shift[m][h]);
+                    if (kSome && nb - i < 4) sc[m][h] &= (1u << 8 * (nb - i)) - 1;
+                    sw[m][h] = up;
+                }
+                scale_pair(sc[m][h], i % 4 != 0, wsc[m][h][0], wsc[m][h][1]);
             }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t p[4], q[4];
-            codes_to_f16(w[2 * h], p);
-            codes_to_f16(w[2 * h + 1], q);
-            float s0, s1;
-            scale_pair(sc[0], sc[1], (i + h) & 3, s0, s1);
+            const float2 x = *reinterpret_cast<const float2*>(sx + (i + h) * kCols);
 #pragma unroll
-            for (int j = 0; j < kNG; ++j) {
+            for (int m = 0; m < kMT; ++m) {
+                uint32_t p[4], q[4];
+                codes_to_f16(w[m][2 * h], p);
+                codes_to_f16(w[m][2 * h + 1], q);
                 float d[4];
-                mma_f16_first(d, p[0], q[0], p[1], q[1], B[i + h][j][0], B[i + h][j][1]);
-                mma_f16(d, p[2], q[2], p[3], q[3], B[i + h][j][2], B[i + h][j][3]);
-                const float2 x = *reinterpret_cast<const float2*>(sx + (i + h) * (8 * kNG) + 8 * j);
+                mma_f16_first(d, p[0], q[0], p[1], q[1], B[i + h][0], B[i + h][1]);
+                mma_f16(d, p[2], q[2], p[3], q[3], B[i + h][2], B[i + h][3]);
                 const float2 u = mul2(d[0], d[1], x), v = mul2(d[2], d[3], x);
-                acc[j][0] = fmaf(u.x, s0, acc[j][0]);
-                acc[j][1] = fmaf(u.y, s0, acc[j][1]);
-                acc[j][2] = fmaf(v.x, s1, acc[j][2]);
-                acc[j][3] = fmaf(v.y, s1, acc[j][3]);
+                acc[m][0] = fmaf(u.x, wsc[m][0][h], acc[m][0]);
+                acc[m][1] = fmaf(u.y, wsc[m][0][h], acc[m][1]);
+                acc[m][2] = fmaf(v.x, wsc[m][1][h], acc[m][2]);
+                acc[m][3] = fmaf(v.y, wsc[m][1][h], acc[m][3]);
             }
         }
     }
 }
 
-template <int kNB, int kNG, int kMT, int kX, int kMode>
+template <int kNB, int kMT, int kX, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ StreamArgs a) {
-    using S = Shape<kNB, kNG, kMT>;
-    constexpr int kCols = S::kCols;
+    using S = Shape<kNB, kMT>;
+    constexpr bool kBoxes = S::kBoxes;
     constexpr bool kRoutes = kMode == kGlu || kMode == kDown;
     extern __shared__ __align__(128) char sm[];
     __shared__ int scratch[kThreads / 32];
     uint64_t* full = reinterpret_cast<uint64_t*>(sm);   // a unit's copies have landed
     uint64_t* empty = full + kMaxStages;                // its consumers have read it
-    uint64_t* done = empty + kMaxStages;                // [2]: they have written their shares of the sums
-    uint64_t* freed = done + 2;                         // [2]: the sums are formed
+    uint64_t* done = empty + kMaxStages;                // [2 groups]: they have written their shares of the sums
+    uint64_t* freed = done + 2 * kWarps;                // [2 groups]: the sums are formed
     float* red = reinterpret_cast<float*>(sm + S::kBars);
     float* sx_all = red + S::kRed / 4;
     int* seg = reinterpret_cast<int*>(sx_all + S::kSx / 4);
@@ -411,23 +431,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             tc::mbar_init(full + s, 1);
-            tc::mbar_init(empty + s, kWarps);
+            tc::mbar_init(empty + s, a.splits);
         }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(done + i, kWarps);
+        for (int i = 0; i < 2 * kWarps; ++i) {
+            tc::mbar_init(done + i, a.splits);
             tc::mbar_init(freed + i, 1);
         }
         tc::fence_mbar_init();
     }
-    group_rows<kMode, kCols>(a, seg, first, list, reinterpret_cast<int*>(ring), scratch);   // with barriers for the whole CTA
-    // A stage: boxes of [rows_unit][128] swizzled bytes of codes, then scales.  kGlu: rows_unit / 2 rows
+    group_rows<kMode>(a, seg, first, list, reinterpret_cast<int*>(ring), scratch);   // with barriers for the whole CTA
+    // A stage: boxes of [rows_unit][128] swizzled bytes of codes, or rows, then scales.  kGlu: rows_unit / 2 rows
     // of gate, then as many of up, in codes and scales alike; a tile is 8 of each.
     const int depth = a.K >> 5;                               // blocks of a weight row
-    const int tiles_unit = kMT * kWarps >> a.split_log, rows_unit = 16 * tiles_unit;
-    const int features = kMode == kGlu ? 8 * tiles_unit : rows_unit;   // of a unit
-    const int box_bytes = rows_unit * 128, code_bytes = (a.slab_blocks + kBox - 1) / kBox * box_bytes;
+    constexpr int rows_unit = 16 * kMT;
+    constexpr int features = kMode == kGlu ? 8 * kMT : rows_unit;       // of a unit
+    const int group_log = kWarpsLog - a.split_log, groups = 1 << group_log;
+    constexpr int box_bytes = rows_unit * 128;
+    const int code_bytes = kBoxes ? (a.slab_blocks + kBox - 1) / kBox * box_bytes : rows_unit * a.pitch;
     // scales of the second half of a tile are this far behind the first's
-    const int half_bytes = kMode == kGlu ? (8 * tiles_unit * a.scale_pitch + 31) & ~15 : 8 * a.scale_pitch;
+    const int half_bytes = kMode == kGlu ? (8 * kMT * a.scale_pitch + 31) & ~15 : 8 * a.scale_pitch;
     bool ok = true;               // no wait of this warp has expired
     int s = 0, ph = 0;
     Units it;
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
             // tensor's last whole piece, where bytes go one by one.  Run j: `n` scales from `at` of their
             // tensor on, to the piece at `dst`.
             auto run = [&](int j, long long& at, int& count, uint32_t& dst, const uint8_t*& from) {
-                const int half = kMode == kGlu ? (a.rows ? j / (8 * tiles_unit) : j) : 0, i = a.rows ? j - half * 8 * tiles_unit : 0;
+                const int half = kMode == kGlu ? (a.rows ? j / (8 * kMT) : j) : 0, i = a.rows ? j - half * 8 * kMT : 0;
                 at = (long long)(row0 + i) * depth + blk0;
                 count = i >= rows ? 0 : a.rows ? nblk : rows * depth;
                 dst = tc::smem_u32(ring) + to + code_bytes + half * half_bytes + i * a.scale_pitch;
@@ -477,16 +499,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                     tc::fence_proxy_async_smem();   // before a later unit's copy to the same place
                 }
             }
-            bytes = __reduce_add_sync(0xffffffffu, bytes) + boxes * box_bytes;
+            bytes = __reduce_add_sync(0xffffffffu, bytes) + (kBoxes ? boxes * box_bytes : rows * nblk * (kMode == kGlu ? 32 : 16));
             if (lane == 0) {
                 tc::mbar_expect_tx(bar, bytes);
-                for (int b = 0; b < boxes; ++b) {
+                for (int b = 0; kBoxes && b < boxes; ++b) {
                     const int x = (blk0 + b * kBox) * 16;
                     tc::tma_load_2d(ring + to + b * box_bytes, &a.codes, bar, x, row0);
                     if (kMode == kGlu) tc::tma_load_2d(ring + to + b * box_bytes + box_bytes / 2, &a.codes2, bar, x, row0);
                 }
             }
             __syncwarp();
+            if (!kBoxes) {
+                for (int j = lane; j < rows_unit; j += 32) {
+                    const int half = kMode == kGlu && j >= rows_unit / 2, i = j - half * (rows_unit / 2);
+                    if (i < rows)
+                        bulk_load(tc::smem_u32(ring) + to + j * a.pitch, (half ? a.w2 : a.w) + ((long long)(row0 + i) * depth + blk0) * 16, nblk * 16, bar);
+                }
+            }
             for (int j = lane; j < jobs; j += 32) {
                 run(j, at, count, dst, from);
                 const long long piece = at & ~15LL;
@@ -503,8 +532,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
         // a feature's gate and up (rows 0 to 7 and 8 to 15 of a tile).
         const int me = warp - kWarps - 2;
         const int i = kMode == kGlu ? (lane & 1) << 3 | (lane >> 1 & 7) : lane & 15;
-        const int outputs = tiles_unit * 16 * kCols;
-        const float* base = red + me * (kWarps * kMT * S::kPart) + i;
         int row0 = 0, nrows = 0, n = 0;
         bool fresh = false;
         for (; it.u < it.end; it.next(first), ++n) {
@@ -515,20 +542,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 nrows = min(kCols, seg[it.g + 1] - row0);
                 fresh = false;
             }
-            if (!tc::mbar_wait(done + me, ph, lim)) ok = false;
-            ph ^= 1;
+            const int turn = n >> group_log, slot = 2 * (n & (groups - 1)) + (turn & 1);
+            if (!tc::mbar_wait(done + slot, (turn >> 1) & 1, lim)) ok = false;
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
-            for (int o = lane; o < outputs; o += 32) {
+            const float* base = red + (slot << a.split_log) * (kMT * S::kPart) + i;
+#pragma unroll
+            for (int o = lane; o < rows_unit * kCols; o += 32) {
                 const int c = (o >> 4) & (kCols - 1), tile = o / (16 * kCols);
                 const float* p = base + (tile << a.split_log) * S::kPart + c * kLine;
-                float v[kWarps];
+                float v[8];
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
+                for (int w = 0; w < 8; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) v[0] += v[w];
+                for (int w = 0; w < 8; ++w) {
+                    if (a.splits == 16) v[w] += p[(w + 8) * S::kPart];
+                    if (w > 0) v[0] += v[w];
+                }
                 if (kMode == kGlu) {
                     const float u = __shfl_xor_sync(0xffffffffu, v[0], 1);
                     const int f = it.tile * features + tile * 8 + (i & 7);
@@ -546,96 +578,95 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 }
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(freed + me);
+            if (lane == 0) tc::mbar_arrive(freed + slot);
         }
     } else {
         // ---- consumers ----
-        const int wm = warp >> a.split_log, wk = warp & (a.splits - 1);
+        const int group = warp >> a.split_log, wk = warp & (a.splits - 1);
         const int g8 = lane >> 2, t4 = lane & 3;
         float* sx = sx_all + warp * (kNB * kCols);
         if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
-        uint32_t B[kNB][kNG][4];
-        int nb = 0, buf = 0, fph = 0;
-        uint32_t wat0[4], sat0 = 0, scale_at = 0;   // in stage 0: this lane's codes and scales; the unit's first scale
-        for (; it.u < it.end; it.next(first)) {
-            if (it.fresh) {
+        uint32_t B[kNB][4];
+        int nb = 0, turn = 0;
+        bool fresh = false;
+        uint32_t wat0[4], sat0 = 0;   // in stage 0: this lane's codes and scales
+        auto skip = [&](int units) {   // to this group's next unit, with its stage
+            for (int j = 0; j < units && it.u < it.end; ++j) {
+                it.next(first);
+                fresh |= it.fresh;
+                if (++s == a.stages) s = 0, ph ^= 1;
+            }
+        };
+        fresh = it.fresh;
+        for (skip(group); it.u < it.end; skip(groups), ++turn) {
+            if (fresh) {
+                fresh = false;
                 const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
                 const int row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols, nrows = min(kCols, seg[it.g + 1] - row0);
-                const int per = (((nblk - 1) >> a.split_log) + 2) & ~1;   // even: an ldmatrix does not leave its box
+                const int per = kBoxes ? kBox : ((nblk - 1) >> a.split_log) + 1;
                 const int b0 = wk * per;
                 nb = max(0, min(per, nblk - b0));
                 __syncwarp();
+                const bool have = g8 < nrows;
+                long long row = row0 + g8;
+                if (kRoutes) row = have ? list[row0 + g8] : 0;
+                if (kMode == kGlu) row = (int)row / a.k;
+                // all loads of a batch before the first is used; blocks past the warp's share are zeros
+                constexpr int kMost = kX == QBMOE_F32 ? 4 : 8, kBatch = kNB < kMost ? kNB : kMost;
 #pragma unroll
-                for (int j = 0; j < kNG; ++j) {
-                    const int c = 8 * j + g8;
-                    const bool have = c < nrows;
-                    long long row = row0 + c;
-                    if (kRoutes) row = have ? list[row0 + c] : 0;
-                    if (kMode == kGlu) row = (int)row / a.k;
-                    // all loads of a batch before the first is used; blocks past the warp's share are zeros
-                    constexpr int kMost = kX == QBMOE_F32 ? 4 : 8, kBatch = kNB < kMost ? kNB : kMost;
+                for (int i0 = 0; i0 < kNB; i0 += kBatch) {
+                    Raw<kX> raw[kBatch];
 #pragma unroll
-                    for (int i0 = 0; i0 < kNB; i0 += kBatch) {
-                        Raw<kX> raw[kBatch];
+                    for (int i = 0; i < kBatch && i0 + i < kNB; ++i) raw[i].load(a, row, blk0 + b0 + i0 + i, have && i0 + i < nb);
 #pragma unroll
-                        for (int i = 0; i < kBatch && i0 + i < kNB; ++i) raw[i].load(a, row, blk0 + b0 + i0 + i, have && i0 + i < nb);
-#pragma unroll
-                        for (int i = 0; i < kBatch && i0 + i < kNB; ++i) {
-                            const float sc = raw[i].convert(B[i0 + i][j]);
-                            if (t4 == 0) sx[(i0 + i) * kCols + c] = sc;
-                        }
+                    for (int i = 0; i < kBatch && i0 + i < kNB; ++i) {
+                        const float sc = raw[i].convert(B[i0 + i]);
+                        if (t4 == 0) sx[(i0 + i) * kCols + g8] = sc;
                     }
                 }
                 __syncwarp();
                 // ldmatrix: lanes 8 q .. 8 q + 7 give the rows of matrix q: rows 0 to 7 or 8 to 15 of block 0 or 1
-                const int q = lane >> 3, half = q & 1, r = (kMode == kGlu ? 8 * (wm + half * tiles_unit) : 16 * wm + 8 * half) + (lane & 7);
+                const int q = lane >> 3, half = q & 1, r = (kMode == kGlu ? 8 * kMT : 8) * half + (lane & 7);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {   // box rows of 128 bytes, their 16-byte pieces swizzled
+                for (int p = 0; p < (kBoxes ? 4 : 1); ++p) {
                     const int b = b0 + 2 * p + (q >> 1);
-                    wat0[p] = tc::smem_u32(ring) + (b / kBox) * box_bytes + r * 128 + (((b & (kBox - 1)) ^ (r & 7)) << 4);
+                    wat0[p] = tc::smem_u32(ring) + (kBoxes ? wk * box_bytes + r * 128 + (((b & (kBox - 1)) ^ (r & 7)) << 4) : r * a.pitch + b * 16);
                 }
-                sat0 = tc::smem_u32(ring) + code_bytes + ((kMode == kGlu ? 8 : 16) * wm + g8) * a.scale_pitch + b0;
-                // row by row, each row's scales have a start of their own
-                const int f = it.tile * features + (a.rows ? (kMode == kGlu ? 8 : 16) * wm + g8 : 0);
-                scale_at = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)f) * (uint32_t)depth + (uint32_t)blk0;
+                sat0 = tc::smem_u32(ring) + code_bytes + g8 * a.scale_pitch + b0;
             }
             if (!tc::mbar_wait_spin(full + s, ph, lim)) ok = false;
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
-            const int apart = (kWarps >> a.split_log) * (kMode == kGlu ? 8 : 16);   // rows between this warp's tiles
+            constexpr int apart = kMode == kGlu ? 8 : 16;   // rows between tiles
             const uint32_t off = s * a.stage_bytes;
-            // scales start at a byte of their first 16
-            const uint32_t in = scale_at & 15u, in_hi = (scale_at + (a.rows && kMode != kGlu ? 8 * depth : 0)) & 15u;
-            float acc[kMT][kNG][4] = {};
+            // scales start at a byte of their first 16: the unit's, or row by row each row's (then a unit is one tile)
+            const uint32_t start = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)(it.tile * features + (a.rows ? g8 : 0))) * (uint32_t)depth +
+                                   (uint32_t)it.slab * (uint32_t)a.slab_blocks;
+            const uint32_t in = start & 15u, in_hi = (start + (a.rows && kMode != kGlu ? 8 * depth : 0)) & 15u;
+            float acc[kMT][4] = {};
+            uint32_t wat[4];
 #pragma unroll
-            for (int m = 0; m < kMT; ++m) {
-                const uint32_t at = off + m * apart * 128, sat = sat0 + off + m * apart * a.scale_pitch;
-                const uint32_t wat[4] = {wat0[0] + at, wat0[1] + at, wat0[2] + at, wat0[3] + at};
-                // (row by row, apart depth is a multiple of 16: all tiles of the warp start alike)
-                if (nb == kNB) share<kNB, kNG, false>(B, sx + 2 * t4, wat, box_bytes, sat + in, sat + half_bytes + in_hi, nb, acc[m]);
-                else share<kNB, kNG, true>(B, sx + 2 * t4, wat, box_bytes, sat + in, sat + half_bytes + in_hi, nb, acc[m]);
-            }
-            scale_at += features * depth;
+            for (int p = 0; p < (kBoxes ? 4 : 1); ++p) wat[p] = wat0[p] + off;
+            const uint32_t lo = sat0 + off + in, hi = sat0 + off + half_bytes + in_hi;
+            const uint32_t tile = apart * (kBoxes ? 128 : a.pitch), tile_sc = apart * a.scale_pitch;
+            if (nb == kNB) share<kNB, kMT, false>(B, sx + 2 * t4, wat, tile, lo, hi, tile_sc, nb, acc);
+            else share<kNB, kMT, true>(B, sx + 2 * t4, wat, tile, lo, hi, tile_sc, nb, acc);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(empty + s);
-            if (++s == a.stages) s = 0, ph ^= 1;
-            if (!tc::mbar_wait_spin(freed + buf, fph ^ 1, lim)) ok = false;
+            const int slot = 2 * group + (turn & 1);
+            if (!tc::mbar_wait_spin(freed + slot, ((turn >> 1) & 1) ^ 1, lim)) ok = false;
 #pragma unroll
             for (int m = 0; m < kMT; ++m) {
-                float* mine = red + ((buf * kMT + m) * kWarps + warp) * S::kPart;
-#pragma unroll
-                for (int j = 0; j < kNG; ++j) {
-                    mine[(8 * j + 2 * t4) * kLine + g8] = acc[m][j][0];
-                    mine[(8 * j + 2 * t4 + 1) * kLine + g8] = acc[m][j][1];
-                    mine[(8 * j + 2 * t4) * kLine + g8 + 8] = acc[m][j][2];
-                    mine[(8 * j + 2 * t4 + 1) * kLine + g8 + 8] = acc[m][j][3];
-                }
+                float* mine = red + (((slot * kMT + m) << a.split_log) + wk) * S::kPart;
+                mine[2 * t4 * kLine + g8] = acc[m][0];
+                mine[(2 * t4 + 1) * kLine + g8] = acc[m][1];
+                mine[2 * t4 * kLine + g8 + 8] = acc[m][2];
+                mine[(2 * t4 + 1) * kLine + g8 + 8] = acc[m][3];
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(done + buf);
-            if (buf ^= 1, !buf) fph ^= 1;
+            if (lane == 0) tc::mbar_arrive(done + slot);
         }
     }
     if (!ok && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
@@ -644,41 +675,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kSlabBlocks = 32 * kWarps;   // of 32: the deepest slab that the warps hold
+constexpr int kSlabBlocks = 16 * kWarps;   // of 32: the deepest slab that the warps hold
 
 int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
 
-// Calls f with the shape whose warps hold `per` blocks of ng groups of 8 rows: the smallest of a
-// few sizes (what is beyond a warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n.
-// Two tiles a warp, where three units of that size fit, halve what a unit costs besides.
+// Calls f with the shape whose warps hold `per` blocks: the smallest of three sizes (what is beyond
+// a warp's share is multiplied with zeros).  14 is K = 7 2^n.
 template <typename F>
-int for_shape(int ng, int per, F f) {
-    if (ng == 2) {
-        if (per <= 8) return f(Shape<8, 2, 2>{});
-        if (per <= 14) return f(Shape<14, 2, 1>{});
-        return f(Shape<16, 2, 1>{});
-    }
-    if (per <= 4) return f(Shape<4, 1, 2>{});
-    if (per <= 8) return f(Shape<8, 1, 2>{});
-    if (per <= 14) return f(Shape<14, 1, 2>{});
-    if (per <= 16) return f(Shape<16, 1, 1>{});
-    if (per <= 28) return f(Shape<28, 1, 1>{});
-    return f(Shape<32, 1, 1>{});
+int for_shape(int per, F f) {
+    if (per <= 8) return f(Shape<8, 2>{});
+    if (per <= 14) return f(Shape<14, 1>{});
+    return f(Shape<16, 1>{});
 }
 
-// Geometry and launch; codes (kGlu: gate) and codes2 (up) are the weights' [E, N, K / 2].  Two
-// groups of columns where experts have more than 8 rows on average and the depth allows it.
+// Geometry and launch; codes (kGlu: gate) and codes2 (up) are the weights' [E, N, K / 2].
 template <int kX, int kMode>
 int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream_t s) {
     const int depth = a.K / 32;
-    const int ng = depth <= 16 * kWarps && (long long)a.R > 8LL * a.E ? 2 : 1;
     a.slabs = slabs_of(a.K);
     a.slab_blocks = ((depth + a.slabs - 1) / a.slabs + kBox - 1) / kBox * kBox;   // whole boxes
     a.slab_blocks = min(a.slab_blocks, depth);
-    // the fewest splits for which a warp's share is at most 16 blocks, and a unit at most 128 rows
-    for (a.split_log = 1; (kWarps >> a.split_log) > 1 && (a.slab_blocks - 1) >> a.split_log >= 16;) ++a.split_log;
+    // the smallest groups whose warps hold the depth, a box each where eight hold it so
+    const int most = a.slab_blocks <= 8 * kBox ? kBox : 16;
+    while ((a.slab_blocks - 1) >> a.split_log >= most) ++a.split_log;
     a.splits = 1 << a.split_log;
-    const int per = (((a.slab_blocks - 1) >> a.split_log) + 2) & ~1;
+    const int per = ((a.slab_blocks - 1) >> a.split_log) + 1;
     a.rows = a.slabs > 1;
     // row by row: pieces that hold a slab's scales from any start within 16 bytes, an odd number of
     // 16 bytes apart, so that eight rows lie in different banks
@@ -686,39 +707,46 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
     a.expiries = qbh::mx_expiries();
     a.wait_limit = qbh::mx_wait_limit();
     a.stall = qbh::mx_stall();
-    return for_shape(ng, per, [&](auto shape) -> int {
+    return for_shape(per, [&](auto shape) -> int {
         using S = decltype(shape);
-        const int rows = 16 * S::kTiles * (kWarps / a.splits), box_rows = kMode == kGlu ? rows / 2 : rows;
-        const long long w_rows = (long long)a.E * a.N;
-        if (!qbh::encode_rows(&a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows)) return QBMOE_ECUDA;
-        if (codes2 && !qbh::encode_rows(&a.codes2, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes2, w_rows, a.K / 2, a.K / 2, 16 * kBox, box_rows))
-            return QBMOE_ECUDA;
-        a.stage_bytes = (int)qbh::align_up((size_t)(a.slab_blocks + kBox - 1) / kBox * rows * 128 + rows * a.scale_pitch + 64, 1024);
+        const int rows = 16 * S::kTiles, box_rows = kMode == kGlu ? rows / 2 : rows;
+        a.w = codes;
+        a.w2 = codes2;
+        // long rows come one by one, an odd number of 16 bytes apart (ldmatrix without bank conflicts); short ones in boxes
+        a.pitch = S::kBoxes ? 0 : (a.slab_blocks | 1) * 16;
+        for (int i = 0; S::kBoxes && i < (codes2 ? 2 : 1); ++i)
+            if (!qbh::encode_rows(i ? &a.codes2 : &a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? codes2 : codes, (long long)a.E * a.N, a.K / 2, a.K / 2,
+                                  16 * kBox, box_rows))
+                return QBMOE_ECUDA;
+        const size_t codes_at = a.pitch ? (size_t)rows * a.pitch : (size_t)(a.slab_blocks + kBox - 1) / kBox * rows * 128;
+        a.stage_bytes = (int)qbh::align_up(codes_at + rows * a.scale_pitch + 64, 1024);
         const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
         a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
         if (a.stages > kMaxStages) a.stages = kMaxStages;
-        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 48 KB that hist takes
+        // A stage belongs to one group, and (their number being even, or the group alone) to one order of
+        // filling and reading: a warp that waits for a barrier's next phase has seen the one before, which a
+        // parity cannot tell from the one after.
+        a.stages -= a.stages % (kWarps / a.splits);
+        const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 32 KB that hist takes
         long long units = 0x7fffffff;
-        if (kMode == kStore && !a.offsets) units = (((long long)a.R + S::kCols - 1) / S::kCols) * ((a.N + rows - 1) / rows) * a.slabs;
+        if (kMode == kStore && !a.offsets) units = (((long long)a.R + kCols - 1) / kCols) * ((a.N + rows - 1) / rows) * a.slabs;
         const int grid = (int)min(units, (long long)qbh::sm_count());
-        const auto kern = k_stream<S::kBlocks, S::kGroups, S::kTiles, kX, kMode>;
+        const auto kern = k_stream<S::kBlocks, S::kTiles, kX, kMode>;
         if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
         kern<<<grid, kThreads, smem, s>>>(a);
         return qbh::cuda_err(cudaGetLastError());
     });
 }
 
-template <int kNB, int kNG, int kMT, int kX, int kMode>
-int set_smem() {
-    return qbh::cuda_err(cudaFuncSetAttribute(k_stream<kNB, kNG, kMT, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
-}
 template <int kX, int kMode>
 int set_smem_all() {
     int rc = 0;
-    for (int ng = 1; ng <= 2; ++ng)
-        for (int per : {4, 8, 14, 16, 28, 32})
-            if (!rc && per <= 32 / ng)
-                rc = for_shape(ng, per, [](auto shape) { return set_smem<decltype(shape)::kBlocks, decltype(shape)::kGroups, decltype(shape)::kTiles, kX, kMode>(); });
+    for (int per : {8, 14, 16})
+        if (!rc)
+            rc = for_shape(per, [](auto shape) {
+                using S = decltype(shape);
+                return qbh::cuda_err(cudaFuncSetAttribute(k_stream<S::kBlocks, S::kTiles, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
+            });
     return rc;
 }
 

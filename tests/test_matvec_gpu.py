@@ -317,3 +317,22 @@ def test_a_decode_step_of_a_block():
     want, bound = F.experts(f64(h), idx.cpu().numpy(), f64(w), gv, uv, ov, lat, 1e-6)
     near(z, want, bound + 2.0 ** -8 * np.abs(want))
     assert Q.qbmoe_status(None, None) == 0
+
+
+@pytest.mark.parametrize("N,K", [(65536, 64), (32768, 256), (32768, 512), (24576, 1024), (16384, 2048), (8192, 3584), (8192, 4096), (4096, 7168)])
+def test_many_tiles(N, K):
+    """Each stage of the weights' ring is filled many times, also with groups of warps at different paces."""
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(N)
+    off = np.array([0, 3, 3, 5, 14], np.int32)
+    x, xv = rows(r, 14, K, "mxfp8")
+    codes = torch.randint(0, 256, (4, N, K // 2), dtype=torch.uint8, device="cuda", generator=torch.Generator("cuda").manual_seed(N))
+    scales = torch.randint(110, 124, (4, N, K // 32), dtype=torch.uint8, device="cuda", generator=torch.Generator("cuda").manual_seed(K))
+    w = Q.Mxfp4(codes, scales)
+    first = Q.mxfp4_matvec(x, w, offsets=cuda(off)[0], out_dtype=torch.float32)
+    for _ in range(20):
+        assert torch.equal(Q.mxfp4_matvec(x, w, offsets=cuda(off)[0], out_dtype=torch.float32), first)
+    some = r.choice(N, 300, replace=False)
+    wv = M.decode(codes.cpu().numpy()[:, some], scales.cpu().numpy()[:, some])
+    want, bound = grouped(xv, wv, off)
+    near(first[:, torch.from_numpy(some).cuda()], want, bound + HALF[torch.float32] * np.abs(want))
