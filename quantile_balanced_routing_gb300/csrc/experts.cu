@@ -30,17 +30,25 @@ struct CombineArgs {
     __nv_bfloat16* y;
     long long ldy;
 };
-constexpr int kCombineThreads = 256, kCombineKeep = 4;
+constexpr int kCombineThreads = 512, kCombineKeep = 2;
 
-// Four elements of a token's weighted sum, its routes in order.
-QB_DEV float4 weighted(const CombineArgs& a, const int* e, const float* w, int t, int f) {
+// Four elements of a token's weighted sum, its routes in order; the loads of eight routes before the first
+// is used.  n routes have an expert: `row` is theirs.
+QB_DEV float4 weighted(const CombineArgs& a, const int* row, const float* w, int n, int f) {
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < a.k; ++i) {
-        if (e[i] < 0 || e[i] >= a.E) continue;
-        for (int b = 0; b < a.slabs; ++b) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.rows + (((long long)b * a.T + t) * a.k + i) * a.L + f));
-            s.x = fmaf(w[i], v.x, s.x); s.y = fmaf(w[i], v.y, s.y); s.z = fmaf(w[i], v.z, s.z); s.w = fmaf(w[i], v.w, s.w);
+    for (int b = 0; b < a.slabs; ++b) {
+        const float* rows = a.rows + (long long)b * a.T * a.k * a.L + f;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(rows + (long long)row[i0 + i] * a.L));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i0 + i >= n) break;
+                s.x = fmaf(w[i0 + i], v[i].x, s.x); s.y = fmaf(w[i0 + i], v[i].y, s.y);
+                s.z = fmaf(w[i0 + i], v[i].z, s.z); s.w = fmaf(w[i0 + i], v[i].w, s.w);
+            }
         }
     }
     return s;
@@ -50,28 +58,31 @@ QB_DEV float4 weighted(const CombineArgs& a, const int* e, const float* w, int t
 // kCombineKeep 4 kCombineThreads features stay in registers; wider ones are formed again.
 __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs a) {
     __shared__ float part[kCombineThreads / 32];
-    __shared__ int e[QBMOE_MAX_TOPK];
+    __shared__ int row[QBMOE_MAX_TOPK], routes;
     __shared__ float w[QBMOE_MAX_TOPK];
     const int t = blockIdx.x;
-    if ((int)threadIdx.x < a.k) {
-        e[threadIdx.x] = a.idx[(long long)t * a.k + threadIdx.x];
-        w[threadIdx.x] = a.w[(long long)t * a.k + threadIdx.x];
+    if (threadIdx.x < 32) {   // the routes that have an expert, in order
+        const int r = t * a.k + threadIdx.x, e = (int)threadIdx.x < a.k ? a.idx[r] : -1;
+        const unsigned have = __ballot_sync(0xffffffffu, e >= 0 && e < a.E);
+        const int at = __popc(have & ((1u << threadIdx.x) - 1));
+        if (have >> threadIdx.x & 1) row[at] = r, w[at] = a.w[r];
+        if (threadIdx.x == 0) routes = __popc(have);
     }
     __syncthreads();
     pdl_wait();
-    const int n = a.L >> 2;
+    const int n = a.L >> 2, m = routes;
     float4 keep[kCombineKeep];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < kCombineKeep; ++i) {
         const int at = threadIdx.x + i * kCombineThreads;
-        if (at < n) keep[i] = weighted(a, e, w, t, 4 * at);
+        if (at < n) keep[i] = weighted(a, row, w, m, 4 * at);
     }
     auto square = [&](const float4& v) { ss = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, ss)))); };
 #pragma unroll
     for (int i = 0; i < kCombineKeep; ++i)
         if ((int)threadIdx.x + i * kCombineThreads < n) square(keep[i]);
-    for (int at = threadIdx.x + kCombineKeep * kCombineThreads; at < n; at += kCombineThreads) square(weighted(a, e, w, t, 4 * at));
+    for (int at = threadIdx.x + kCombineKeep * kCombineThreads; at < n; at += kCombineThreads) square(weighted(a, row, w, m, 4 * at));
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
@@ -88,7 +99,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs a
 #pragma unroll
     for (int i = 0; i < kCombineKeep; ++i)
         if ((int)threadIdx.x + i * kCombineThreads < n) store(threadIdx.x + i * kCombineThreads, keep[i]);
-    for (int at = threadIdx.x + kCombineKeep * kCombineThreads; at < n; at += kCombineThreads) store(at, weighted(a, e, w, t, 4 * at));
+    for (int at = threadIdx.x + kCombineKeep * kCombineThreads; at < n; at += kCombineThreads) store(at, weighted(a, row, w, m, 4 * at));
 }
 
 // Scratch of an experts call: act; gate and up in slabs; the routes' rows.

@@ -32,10 +32,10 @@ namespace {
 
 using namespace qb;
 
-constexpr int kWarps = 16, kWarpsLog = 4;      // consumers; then two producers and two that sum
-constexpr int kThreads = 32 * (kWarps + 4);    // 96 registers a thread
+constexpr int kWarps = 8;                      // consumers; then two producers and two that sum
+constexpr int kThreads = 32 * (kWarps + 4);    // 168 registers a thread
 constexpr int kCols = 8;                       // rows of x a unit takes
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 32;
 constexpr int kLine = 20;                      // floats a column of 16 results takes: stores without bank conflicts
 constexpr long long kDefaultWait = 1LL << 17;  // polls (<= 20 us each) before a wait expires
 constexpr int kMaxDynamic = 226 * 1024;       // of 227 KB, a little being static
@@ -62,7 +62,7 @@ struct StreamArgs {
     long long ldy;
     float beta1, beta2;
     // geometry
-    int splits, split_log;       // consumers along the depth (a power of two): a group
+    int splits, groups;          // consumers along the depth: a group; kWarps / splits of them
     int slabs, slab_blocks;      // the depth in slabs of this many blocks of 32
     int stages, stage_bytes;
     int pitch;                   // bytes between the rows of a unit that come one by one; 0: they come in boxes
@@ -73,17 +73,18 @@ struct StreamArgs {
     int stall;
 };
 
-// kNB blocks of 32 a warp, kMT tiles a unit.  Up to a box of blocks, weights come in boxes.
-template <int kNB, int kMT>
+// kNB blocks of 32 a warp, kMT tiles a unit; weights come in boxes, a whole number a warp, or row by row.
+template <int kNB, int kMT, bool kBoxed>
 struct Shape {
     static constexpr int kBlocks = kNB, kTiles = kMT;
-    static constexpr bool kBoxes = kNB <= kBox;
+    static constexpr bool kBoxes = kBoxed;
+    static constexpr int kStaged = kBoxes ? kMT : 1;           // tiles a stage
     static constexpr int kPart = kCols * kLine + 8;            // floats of a warp's partial results
     static constexpr int kRed = 2 * kWarps * kMT * kPart * 4;  // two slots a group
     static constexpr int kSx = kWarps * kNB * kCols * 4;       // scales of x
     static constexpr int kBars = (2 * kMaxStages + 4 * kWarps) * 8;
     // before the ring, which starts at a multiple of 1024
-    static size_t fixed(int E, int routes) {
+    static size_t fixed(int E, int routes) {   // bytes
         return kBars + kRed + kSx + qbh::align_up((size_t)(E + 1) * 8, 16) + (size_t)routes * 2 + 1024;
     }
 };
@@ -331,34 +332,37 @@ struct Units {
         }
         fresh = true;
     }
-    QB_DEV void next(const int* first) {
-        ++u;
+    // Goes on by n units.
+    QB_DEV void next(const int* first, int n = 1) {
+        u += n;
         fresh = false;
-        if (++tile < tiles || u >= end) return;
-        tile = 0;
+        if ((tile += n) < tiles || u >= end) return;
         fresh = true;
-        if (++chunk == chunks) chunk = 0, ++slab, g = 0;
-        while (first[g + 1] <= chunk) ++g;
+        while (tile >= tiles) {
+            tile -= tiles;
+            if (++chunk == chunks) chunk = 0, ++slab, g = 0;
+            while (first[g + 1] <= chunk) ++g;
+        }
     }
 };
 
 // A warp's share of kMT tiles: each 16 weight rows times kNB blocks of K.  wat: this lane's row of the
 // four 8 x 16-byte matrices that an ldmatrix loads (two blocks of 16 rows), of every of the first four
-// loads in a box, whose 16-byte pieces are swizzled, else of the first alone; lo, hi: the scales of
-// weight rows lane / 4 and 8 more; tiles apart by `tile` bytes of codes and `tile_sc` of scales.  kSome:
-// only nb blocks are the warp's; for the rest B and the scales of x are zeros, and the weights'
-// scales, whatever lies there, are cleared lest one be NaN.
-template <int kNB, int kMT, bool kSome>
-QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (&wat)[4], uint32_t tile, uint32_t lo, uint32_t hi,
-                  uint32_t tile_sc, int nb, float (&acc)[kMT][4]) {
-    constexpr bool kBoxes = kNB <= kBox;
-    auto load = [&](uint32_t (&w)[4], int i, int m) { ldmatrix4(w, (kBoxes ? wat[i / 2 % 4] : wat[0] + i * 16) + m * tile); };
+// loads in a box, whose 16-byte pieces are swizzled, else of the first alone; `at`: where each tile's
+// stage lies; lo, hi: the scales of its weight rows lane / 4 and 8 more.  kSome: only nb blocks are the
+// warp's; for the rest B and the scales of x are zeros, and the weights' scales, whatever lies there, are
+// cleared lest one be NaN.
+template <int kNB, int kMT, bool kBoxes, bool kSome>
+QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (&wat)[4], const uint32_t (&at)[kMT],
+                  const uint32_t (&lo)[kMT], const uint32_t (&hi)[kMT], int nb, float (&acc)[kMT][4]) {
+    constexpr int box_bytes = 16 * kMT * 128;   // (boxes hold all tiles of a unit)
+    auto load = [&](uint32_t (&w)[4], int i, int m) { ldmatrix4(w, (kBoxes ? wat[i / 2 % 4] + i / kBox * box_bytes : wat[0] + i * 16) + at[m]); };
     uint32_t sat[kMT][2], shift[kMT][2], sw[kMT][2], sc[kMT][2], next[kMT][4];
 #pragma unroll
     for (int m = 0; m < kMT; ++m) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t byte = (h ? hi : lo) + m * tile_sc;
+            const uint32_t byte = h ? hi[m] : lo[m];
             sat[m][h] = byte & ~3u;
             shift[m][h] = (byte & 3u) * 8;
             sw[m][h] = lds32(sat[m][h]);
@@ -387,7 +391,7 @@ QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2 && i + h < kNB; ++h) {
             const float2 x = *reinterpret_cast<const float2*>(sx + (i + h) * kCols);
 #pragma unroll
             for (int m = 0; m < kMT; ++m) {
@@ -407,9 +411,9 @@ QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (
     }
 }
 
-template <int kNB, int kMT, int kX, int kMode>
+template <int kNB, int kMT, bool kBoxed, int kX, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ StreamArgs a) {
-    using S = Shape<kNB, kMT>;
+    using S = Shape<kNB, kMT, kBoxed>;
     constexpr bool kBoxes = S::kBoxes;
     constexpr bool kRoutes = kMode == kGlu || kMode == kDown;
     extern __shared__ __align__(128) char sm[];
@@ -440,45 +444,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
         tc::fence_mbar_init();
     }
     group_rows<kMode>(a, seg, first, list, reinterpret_cast<int*>(ring), scratch);   // with barriers for the whole CTA
-    // A stage: boxes of [rows_unit][128] swizzled bytes of codes, or rows, then scales.  kGlu: rows_unit / 2 rows
-    // of gate, then as many of up, in codes and scales alike; a tile is 8 of each.
+    // A stage holds kST tiles: boxes of [16 kST][128] swizzled bytes of codes, or rows, then scales; kGlu: 8 kST rows
+    // of gate, then as many of up, in codes and scales alike.  A unit lies in kMT / kST stages one after the other.
+    constexpr int kST = S::kStaged, kStages = kMT / kST;
     const int depth = a.K >> 5;                               // blocks of a weight row
-    constexpr int rows_unit = 16 * kMT;
-    constexpr int features = kMode == kGlu ? 8 * kMT : rows_unit;       // of a unit
-    const int group_log = kWarpsLog - a.split_log, groups = 1 << group_log;
-    constexpr int box_bytes = rows_unit * 128;
-    const int code_bytes = kBoxes ? (a.slab_blocks + kBox - 1) / kBox * box_bytes : rows_unit * a.pitch;
+    constexpr int rows_tile = kMode == kGlu ? 8 : 16;                                // features of a tile
+    constexpr int features = rows_tile * kMT, staged = rows_tile * kST;              // of a unit, of a stage
+    const int groups = a.groups;
+    constexpr int box_bytes = 16 * kST * 128;
+    const int code_bytes = kBoxes ? (a.slab_blocks + kBox - 1) / kBox * box_bytes : 16 * a.pitch;
     // scales of the second half of a tile are this far behind the first's
-    const int half_bytes = kMode == kGlu ? (8 * kMT * a.scale_pitch + 31) & ~15 : 8 * a.scale_pitch;
+    const int half_bytes = kMode == kGlu ? (staged * a.scale_pitch + 31) & ~15 : 8 * a.scale_pitch;
     bool ok = true;               // no wait of this warp has expired
     int s = 0, ph = 0;
     Units it;
     it.start(first, a.E, (a.N + features - 1) / features, a.slabs);
 
     if (warp >= kWarps && warp < kWarps + 2) {
-        // ---- producers: units in turn ----
+        // ---- producers: stages in turn ----
         const int me = warp - kWarps;
         const long long last = ((long long)a.E * a.N * depth) & ~15LL;   // the end of the scales' last whole piece of 16 bytes
-        const int jobs = a.rows ? rows_unit : kMode == kGlu ? 2 : 1;     // runs of scales
-        int n = 0;
-        for (; it.u < it.end; it.next(first), ++n) {
-            const bool mine = (n & 1) == me;
+        const int jobs = a.rows ? 16 : kMode == kGlu ? 2 : 1;            // runs of scales
+        const long long total = (it.end - it.u) * kStages;
+        constexpr int step = 2 / kStages;                                // units
+        const int m = me % kStages;
+        int n = me;                                                      // fill
+        if (step == 2 && me) it.next(first);
+        s = me % a.stages;
+        for (; it.u < it.end; it.next(first, step), n += 2) {
+            if (n >= a.stages && ok && !tc::mbar_wait(empty + s, ph ^ 1, lim)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) break;
             const uint32_t to = s * a.stage_bytes;
             uint64_t* bar = full + s;
-            if (mine && n >= a.stages && !tc::mbar_wait(empty + s, ph ^ 1, lim)) ok = false;
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            if (++s == a.stages) s = 0, ph ^= 1;
-            if (!mine || (a.stall && n == 0)) continue;   // test hook: the first unit never arrives
+            if ((s += 2) >= a.stages) s -= a.stages, ph ^= 1;
+            if (a.stall && n == 0) continue;   // test hook: the first stage never fills
             const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0), boxes = (nblk + kBox - 1) / kBox;
-            const int f0 = it.tile * features, row0 = it.g * a.N + f0, rows = min(features, a.N - f0);
+            const int f0 = it.tile * features + m * staged, row0 = it.g * a.N + f0, rows = min(staged, a.N - f0);
+            if (rows <= 0) {                   // a unit's second tile, past the last feature
+                if (lane == 0) tc::mbar_arrive(bar);
+                continue;
+            }
             // Scales start anywhere, so the 16-byte pieces that hold them are copied, except behind the
             // tensor's last whole piece, where bytes go one by one.  Run j: `n` scales from `at` of their
             // tensor on, to the piece at `dst`.
             auto run = [&](int j, long long& at, int& count, uint32_t& dst, const uint8_t*& from) {
-                const int half = kMode == kGlu ? (a.rows ? j / (8 * kMT) : j) : 0, i = a.rows ? j - half * 8 * kMT : 0;
+                const int half = kMode == kGlu ? (a.rows ? j / 8 : j) : 0, i = a.rows ? j - half * 8 : 0;
                 at = (long long)(row0 + i) * depth + blk0;
                 count = i >= rows ? 0 : a.rows ? nblk : rows * depth;
                 dst = tc::smem_u32(ring) + to + code_bytes + half * half_bytes + i * a.scale_pitch;
@@ -510,10 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
             }
             __syncwarp();
             if (!kBoxes) {
-                for (int j = lane; j < rows_unit; j += 32) {
-                    const int half = kMode == kGlu && j >= rows_unit / 2, i = j - half * (rows_unit / 2);
-                    if (i < rows)
-                        bulk_load(tc::smem_u32(ring) + to + j * a.pitch, (half ? a.w2 : a.w) + ((long long)(row0 + i) * depth + blk0) * 16, nblk * 16, bar);
+                const int half = kMode == kGlu && lane >= 8, i = lane - half * 8;
+                if (lane < 16 && i < rows) {
+                        bulk_load(tc::smem_u32(ring) + to + lane * a.pitch, (half ? a.w2 : a.w) + ((long long)(row0 + i) * depth + blk0) * 16, nblk * 16, bar);
                 }
             }
             for (int j = lane; j < jobs; j += 32) {
@@ -523,54 +532,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 if (len) bulk_load(dst, from + piece, len, bar);
             }
         }
-        if (!ok)   // no copy may be in flight when the CTA ends
-            for (int j = 0; j < min(n, a.stages); ++j)
-                tc::mbar_wait(full + j, ((n - j + a.stages - 1) / a.stages - 1) & 1, min(lim, 1LL << 10));
+        ok = __all_sync(0xffffffffu, ok);
+        // No copy may be in flight when the CTA ends, also when the consumers gave up: the last fills of
+        // each stage have landed.  (Fill n is the n / stages-th of stage n % stages.)
+        for (int j = n - 2; j >= 0 && j > n - 2 - a.stages; j -= 2)
+            if (!ok || j + a.stages >= total)
+                if (!tc::mbar_wait(full + j % a.stages, (j / a.stages) & 1, ok ? lim : min(lim, 1LL << 10))) ok = false;
     } else if (warp >= kWarps) {
         // ---- sums of the consumers' shares, in order, a unit in turn.  Output o of a unit is column
         // o / 16 % kCols of tile o / (16 kCols), its row o % 16 or, for kGlu, such that neighbours hold
         // a feature's gate and up (rows 0 to 7 and 8 to 15 of a tile).
         const int me = warp - kWarps - 2;
         const int i = kMode == kGlu ? (lane & 1) << 3 | (lane >> 1 & 7) : lane & 15;
-        int row0 = 0, nrows = 0, n = 0;
-        bool fresh = false;
-        for (; it.u < it.end; it.next(first), ++n) {
-            fresh |= it.fresh;
-            if ((n & 1) != me) continue;
-            if (fresh) {
+        int row0 = 0, nrows = 0, group = me % groups, turn = me / groups;
+        if (me) it.next(first), it.fresh = true;
+        for (; it.u < it.end; it.next(first, 2)) {
+            if (it.fresh) {
                 row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols;
                 nrows = min(kCols, seg[it.g + 1] - row0);
-                fresh = false;
             }
-            const int turn = n >> group_log, slot = 2 * (n & (groups - 1)) + (turn & 1);
+            const int slot = 2 * group + (turn & 1);
             if (!tc::mbar_wait(done + slot, (turn >> 1) & 1, lim)) ok = false;
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            const float* base = red + (slot << a.split_log) * (kMT * S::kPart) + i;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            for (group += 2; group >= groups; group -= groups) ++turn;
+            const float* base = red + slot * a.splits * (kMT * S::kPart) + i;
+            for (int o = lane; o >> 5 < kMT * ((nrows + 1) >> 1); o += 32) {   // two columns at once, of those that exist
+                const int pair = o >> 5, tile = kMT == 1 ? 0 : pair >= (nrows + 1) >> 1, c = 2 * (pair - tile * ((nrows + 1) >> 1)) + (lane >> 4);
+                const float* p = base + tile * a.splits * S::kPart + c * kLine;
+                float v[kWarps];
 #pragma unroll
-            for (int o = lane; o < rows_unit * kCols; o += 32) {
-                const int c = (o >> 4) & (kCols - 1), tile = o / (16 * kCols);
-                const float* p = base + (tile << a.split_log) * S::kPart + c * kLine;
-                float v[8];
+                for (int w = 0; w < kWarps; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) v[w] = w < a.splits ? p[w * S::kPart] : 0.0f;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    if (a.splits == 16) v[w] += p[(w + 8) * S::kPart];
-                    if (w > 0) v[0] += v[w];
-                }
+                for (int w = 1; w < kWarps; ++w) v[0] += v[w];
                 if (kMode == kGlu) {
                     const float u = __shfl_xor_sync(0xffffffffu, v[0], 1);
-                    const int f = it.tile * features + tile * 8 + (i & 7);
+                    const int f = it.tile * features + tile * rows_tile + (i & 7);
                     if (c >= nrows || f >= a.N) continue;
                     const long long r = list[row0 + c];
                     float* y = static_cast<float*>(a.y);
                     if (a.slabs > 1) y[((it.slab * 2LL + (i >> 3)) * a.R + r) * a.ldy + f] = v[0];
                     else if (i < 8) y[r * a.ldy + f] = situ_glu(v[0], u, a.beta1, a.beta2);
                 } else {
-                    const int f = it.tile * features + tile * 16 + i;
+                    const int f = it.tile * features + tile * rows_tile + i;
                     if (c >= nrows || f >= a.N) continue;
                     const long long r = (kMode == kDown ? (int)list[row0 + c] : row0 + c) + (long long)it.slab * a.R;
                     if (kMode == kDown || a.y_type == QBMOE_F32) static_cast<float*>(a.y)[r * a.ldy + f] = v[0];
@@ -582,28 +585,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
         }
     } else {
         // ---- consumers ----
-        const int group = warp >> a.split_log, wk = warp & (a.splits - 1);
+        const int group = warp / a.splits, wk = warp - group * a.splits;
         const int g8 = lane >> 2, t4 = lane & 3;
         float* sx = sx_all + warp * (kNB * kCols);
         if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
         uint32_t B[kNB][4];
         int nb = 0, turn = 0;
-        bool fresh = false;
-        uint32_t wat0[4], sat0 = 0;   // in stage 0: this lane's codes and scales
-        auto skip = [&](int units) {   // to this group's next unit, with its stage
-            for (int j = 0; j < units && it.u < it.end; ++j) {
-                it.next(first);
-                fresh |= it.fresh;
-                if (++s == a.stages) s = 0, ph ^= 1;
-            }
-        };
-        fresh = it.fresh;
-        for (skip(group); it.u < it.end; skip(groups), ++turn) {
-            if (fresh) {
-                fresh = false;
+        uint32_t wat0[4], sat0 = 0, start = 0;   // in stage 0: this lane's codes and scales; the first scale's place in its tensor
+        const uint32_t in_second = a.rows && kMode != kGlu ? 8 * depth : 0;   // (row by row the second half's are elsewhere)
+        float* mine0 = red + (2 * group * kMT * a.splits + wk) * S::kPart + 2 * t4 * kLine + g8;
+        if (group) it.next(first, group), it.fresh = true;
+        s = group * kStages;
+        for (; it.u < it.end; it.next(first, groups), ++turn) {
+            if (it.fresh) {
                 const int blk0 = it.slab * a.slab_blocks, nblk = min(a.slab_blocks, depth - blk0);
                 const int row0 = seg[it.g] + (it.chunk - first[it.g]) * kCols, nrows = min(kCols, seg[it.g + 1] - row0);
-                const int per = kBoxes ? kBox : ((nblk - 1) >> a.split_log) + 1;
+                const int per = kBoxes ? kNB : (nblk + a.splits - 1) / a.splits;
                 const int b0 = wk * per;
                 nb = max(0, min(per, nblk - b0));
                 __syncwarp();
@@ -626,66 +623,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 }
                 __syncwarp();
                 // ldmatrix: lanes 8 q .. 8 q + 7 give the rows of matrix q: rows 0 to 7 or 8 to 15 of block 0 or 1
-                const int q = lane >> 3, half = q & 1, r = (kMode == kGlu ? 8 * kMT : 8) * half + (lane & 7);
+                const int q = lane >> 3, half = q & 1, r = (kMode == kGlu ? staged : 8) * half + (lane & 7);
 #pragma unroll
                 for (int p = 0; p < (kBoxes ? 4 : 1); ++p) {
                     const int b = b0 + 2 * p + (q >> 1);
-                    wat0[p] = tc::smem_u32(ring) + (kBoxes ? wk * box_bytes + r * 128 + (((b & (kBox - 1)) ^ (r & 7)) << 4) : r * a.pitch + b * 16);
+                    wat0[p] = tc::smem_u32(ring) + (kBoxes ? b0 / kBox * box_bytes + r * 128 + (((b & (kBox - 1)) ^ (r & 7)) << 4) : r * a.pitch + b * 16);
                 }
                 sat0 = tc::smem_u32(ring) + code_bytes + g8 * a.scale_pitch + b0;
+                // scales start at a byte of their first 16: the unit's, or row by row each row's (then a unit is one tile)
+                start = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)(it.tile * features + (a.rows ? g8 : 0))) * (uint32_t)depth + (uint32_t)blk0;
             }
-            if (!tc::mbar_wait_spin(full + s, ph, lim)) ok = false;
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            constexpr int apart = kMode == kGlu ? 8 : 16;   // rows between tiles
-            const uint32_t off = s * a.stage_bytes;
-            // scales start at a byte of their first 16: the unit's, or row by row each row's (then a unit is one tile)
-            const uint32_t start = ((uint32_t)it.g * (uint32_t)a.N + (uint32_t)(it.tile * features + (a.rows ? g8 : 0))) * (uint32_t)depth +
-                                   (uint32_t)it.slab * (uint32_t)a.slab_blocks;
-            const uint32_t in = start & 15u, in_hi = (start + (a.rows && kMode != kGlu ? 8 * depth : 0)) & 15u;
-            float acc[kMT][4] = {};
-            uint32_t wat[4];
-#pragma unroll
-            for (int p = 0; p < (kBoxes ? 4 : 1); ++p) wat[p] = wat0[p] + off;
-            const uint32_t lo = sat0 + off + in, hi = sat0 + off + half_bytes + in_hi;
-            const uint32_t tile = apart * (kBoxes ? 128 : a.pitch), tile_sc = apart * a.scale_pitch;
-            if (nb == kNB) share<kNB, kMT, false>(B, sx + 2 * t4, wat, tile, lo, hi, tile_sc, nb, acc);
-            else share<kNB, kMT, true>(B, sx + 2 * t4, wat, tile, lo, hi, tile_sc, nb, acc);
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(empty + s);
-            const int slot = 2 * group + (turn & 1);
-            if (!tc::mbar_wait_spin(freed + slot, ((turn >> 1) & 1) ^ 1, lim)) ok = false;
+            uint32_t at[kMT], lo[kMT], hi[kMT];
 #pragma unroll
             for (int m = 0; m < kMT; ++m) {
-                float* mine = red + (((slot * kMT + m) << a.split_log) + wk) * S::kPart;
-                mine[2 * t4 * kLine + g8] = acc[m][0];
-                mine[(2 * t4 + 1) * kLine + g8] = acc[m][1];
-                mine[2 * t4 * kLine + g8 + 8] = acc[m][2];
-                mine[(2 * t4 + 1) * kLine + g8 + 8] = acc[m][3];
+                const bool wrap = s + m / kST >= a.stages;   // (one group: else its stages do not cross the ring's end)
+                const int of = s + m / kST - (wrap ? a.stages : 0);
+                // after a wait has expired nothing is waited for any more: what follows is undefined, and ends
+                if (m % kST == 0 && ok && !tc::mbar_wait_spin(full + of, ph ^ (wrap ? 1 : 0), lim)) ok = false;
+                const uint32_t stage = of * a.stage_bytes, in = m / kST * staged * depth, row = m % kST * rows_tile;
+                at[m] = stage + row * 128;   // (rows one by one: a tile a stage)
+                lo[m] = sat0 + stage + row * a.scale_pitch + ((start + in) & 15u);
+                hi[m] = sat0 + stage + row * a.scale_pitch + half_bytes + ((start + in + in_second) & 15u);
+            }
+            start += groups * features * depth;
+            float acc[kMT][4] = {};
+            if (nb == kNB) share<kNB, kMT, kBoxes, false>(B, sx + 2 * t4, wat0, at, lo, hi, nb, acc);
+            else share<kNB, kMT, kBoxes, true>(B, sx + 2 * t4, wat0, at, lo, hi, nb, acc);
+            __syncwarp();
+#pragma unroll
+            for (int m = 0; m < kStages; ++m)
+                if (lane == 0) tc::mbar_arrive(empty + (s + m >= a.stages ? s + m - a.stages : s + m));
+            if ((s += groups * kStages) >= a.stages) s -= a.stages, ph ^= 1;
+            const int slot = 2 * group + (turn & 1);
+            if (ok && !tc::mbar_wait_spin(freed + slot, ((turn >> 1) & 1) ^ 1, lim)) ok = false;
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+                float* mine = mine0 + ((turn & 1) * kMT + m) * a.splits * S::kPart;
+                mine[0] = acc[m][0];
+                mine[kLine] = acc[m][1];
+                mine[8] = acc[m][2];
+                mine[kLine + 8] = acc[m][3];
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(done + slot);
         }
     }
-    if (!ok && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
+    if (!__all_sync(0xffffffffu, ok) && lane == 0 && a.expiries) atomicAdd(a.expiries, 1);
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kSlabBlocks = 16 * kWarps;   // of 32: the deepest slab that the warps hold
+constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that twelve warps hold in 22 blocks each
 
 int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
 
-// Calls f with the shape whose warps hold `per` blocks: the smallest of three sizes (what is beyond
-// a warp's share is multiplied with zeros).  14 is K = 7 2^n.
+// Calls f with the shape whose warps hold `per` blocks: the smallest of a few sizes (what is beyond a
+// warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n; two tiles a unit halve what a
+// unit costs besides, where the registers allow them.
 template <typename F>
-int for_shape(int per, F f) {
-    if (per <= 8) return f(Shape<8, 2>{});
-    if (per <= 14) return f(Shape<14, 1>{});
-    return f(Shape<16, 1>{});
+int for_shape(bool boxes, int per, F f) {
+    if (boxes) return per <= kBox ? f(Shape<kBox, 2, true>{}) : f(Shape<2 * kBox, 2, true>{});
+    if (per <= 14) return f(Shape<14, 2, false>{});
+    if (per <= 16) return f(Shape<16, 2, false>{});
+    if (per <= 28) return f(Shape<28, 1, false>{});
+    return f(Shape<32, 1, false>{});
 }
 
 // Geometry and launch; codes (kGlu: gate) and codes2 (up) are the weights' [E, N, K / 2].
@@ -695,11 +697,12 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
     a.slabs = slabs_of(a.K);
     a.slab_blocks = ((depth + a.slabs - 1) / a.slabs + kBox - 1) / kBox * kBox;   // whole boxes
     a.slab_blocks = min(a.slab_blocks, depth);
-    // the smallest groups whose warps hold the depth, a box each where eight hold it so
-    const int most = a.slab_blocks <= 8 * kBox ? kBox : 16;
-    while ((a.slab_blocks - 1) >> a.split_log >= most) ++a.split_log;
-    a.splits = 1 << a.split_log;
-    const int per = ((a.slab_blocks - 1) >> a.split_log) + 1;
+    // short rows (up to eight boxes): the smallest groups whose warps have two each; else all warps are one group
+    const int n_boxes = (a.slab_blocks + kBox - 1) / kBox;
+    const bool boxes = n_boxes <= 8;
+    a.splits = !boxes || n_boxes > 8 ? kWarps : n_boxes > 4 ? 4 : (n_boxes + 1) / 2;
+    a.groups = kWarps / a.splits;
+    const int per = boxes ? (n_boxes == 1 ? 1 : 2) * kBox : (a.slab_blocks + a.splits - 1) / a.splits;
     a.rows = a.slabs > 1;
     // row by row: pieces that hold a slab's scales from any start within 16 bytes, an odd number of
     // 16 bytes apart, so that eight rows lie in different banks
@@ -707,9 +710,9 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
     a.expiries = qbh::mx_expiries();
     a.wait_limit = qbh::mx_wait_limit();
     a.stall = qbh::mx_stall();
-    return for_shape(per, [&](auto shape) -> int {
+    return for_shape(boxes, per, [&](auto shape) -> int {
         using S = decltype(shape);
-        const int rows = 16 * S::kTiles, box_rows = kMode == kGlu ? rows / 2 : rows;
+        const int rows = 16 * S::kTiles, staged = 16 * S::kStaged, box_rows = kMode == kGlu ? staged / 2 : staged;
         a.w = codes;
         a.w2 = codes2;
         // long rows come one by one, an odd number of 16 bytes apart (ldmatrix without bank conflicts); short ones in boxes
@@ -718,20 +721,20 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
             if (!qbh::encode_rows(i ? &a.codes2 : &a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? codes2 : codes, (long long)a.E * a.N, a.K / 2, a.K / 2,
                                   16 * kBox, box_rows))
                 return QBMOE_ECUDA;
-        const size_t codes_at = a.pitch ? (size_t)rows * a.pitch : (size_t)(a.slab_blocks + kBox - 1) / kBox * rows * 128;
-        a.stage_bytes = (int)qbh::align_up(codes_at + rows * a.scale_pitch + 64, 1024);
+        const size_t code_bytes = a.pitch ? (size_t)16 * a.pitch : (size_t)(a.slab_blocks + kBox - 1) / kBox * staged * 128;
+        a.stage_bytes = (int)qbh::align_up(code_bytes + staged * a.scale_pitch + 64, 1024);
         const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
         a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
         if (a.stages > kMaxStages) a.stages = kMaxStages;
-        // A stage belongs to one group, and (their number being even, or the group alone) to one order of
-        // filling and reading: a warp that waits for a barrier's next phase has seen the one before, which a
-        // parity cannot tell from the one after.
-        a.stages -= a.stages % (kWarps / a.splits);
+        // Where groups take turns a stage belongs to one of them, and to one producer (their number being even):
+        // a warp that waits for a barrier's next phase has then seen the one before, which a parity
+        // cannot tell from the one after.
+        if (a.groups > 1) a.stages -= a.stages % (a.groups * (1 + a.groups % 2) * S::kTiles / S::kStaged);
         const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 32 KB that hist takes
         long long units = 0x7fffffff;
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + kCols - 1) / kCols) * ((a.N + rows - 1) / rows) * a.slabs;
         const int grid = (int)min(units, (long long)qbh::sm_count());
-        const auto kern = k_stream<S::kBlocks, S::kTiles, kX, kMode>;
+        const auto kern = k_stream<S::kBlocks, S::kTiles, S::kBoxes, kX, kMode>;
         if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
         kern<<<grid, kThreads, smem, s>>>(a);
         return qbh::cuda_err(cudaGetLastError());
@@ -741,11 +744,11 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
 template <int kX, int kMode>
 int set_smem_all() {
     int rc = 0;
-    for (int per : {8, 14, 16})
+    for (int per : {kBox, 2 * kBox, 14, -16, 28, 32})
         if (!rc)
-            rc = for_shape(per, [](auto shape) {
+            rc = for_shape(per == kBox || per == 2 * kBox, abs(per), [](auto shape) {
                 using S = decltype(shape);
-                return qbh::cuda_err(cudaFuncSetAttribute(k_stream<S::kBlocks, S::kTiles, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
+                return qbh::cuda_err(cudaFuncSetAttribute(k_stream<S::kBlocks, S::kTiles, S::kBoxes, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
             });
     return rc;
 }
