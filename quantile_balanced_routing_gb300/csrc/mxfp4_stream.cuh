@@ -743,13 +743,15 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
 
 template <int kX, int kMode>
 int set_smem_all() {
+    auto set = [](auto shape) {
+        using S = decltype(shape);
+        return qbh::cuda_err(cudaFuncSetAttribute(k_stream<S::kBlocks, S::kTiles, S::kBoxes, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
+    };
     int rc = 0;
-    for (int per : {kBox, 2 * kBox, 14, -16, 28, 32})
-        if (!rc)
-            rc = for_shape(per == kBox || per == 2 * kBox, abs(per), [](auto shape) {
-                using S = decltype(shape);
-                return qbh::cuda_err(cudaFuncSetAttribute(k_stream<S::kBlocks, S::kTiles, S::kBoxes, kX, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic));
-            });
+    for (int per : {kBox, 2 * kBox})
+        if (!rc) rc = for_shape(true, per, set);
+    for (int per : {14, 16, 28, 32})
+        if (!rc) rc = for_shape(false, per, set);
     return rc;
 }
 
