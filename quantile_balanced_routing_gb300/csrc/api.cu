@@ -46,6 +46,7 @@ int qbh::device_init() {
     if (!rc) rc = qbh::mx_grad_init();
     if (!rc) rc = qbh::matvec_init();
     if (!rc) rc = qbh::experts_init();
+    if (!rc) rc = qbh::rmsnorm_init();
     if (rc) {
         cudaGetLastError();
         return rc;

@@ -6,7 +6,11 @@
 // input is read once and each output written once.  A thread's pieces are 8 consecutive
 // elements, kNormItems of them a block's width apart; four neighbouring threads hold a
 // block of 32, whose largest magnitude is two shuffles away.
-#include "common.cuh"
+//
+// Many rows go through k_add_rmsnorm_rows and k_add_rmsnorm_backward_rows: persistent CTAs whose
+// next rows come to shared memory by asynchronous copies meanwhile, so that HBM does not wait for a row's
+// reduction.  Few rows, short rows and rows off 16-byte boundaries go through the kernels without a ring.
+#include "mxfp4.cuh"
 
 #include <cuda_fp16.h>
 
@@ -197,6 +201,96 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) 
     }
 }
 
+// Rows blockIdx.x, + gridDim.x, .. in a ring of `stages` rows of `bytes`.  A thread copies the pieces
+// that it reads itself, so the ring needs no barrier: a thread waits for its own copies alone.
+struct Ring {
+    int stages, bytes;
+};
+constexpr int kRingStages = 4;
+
+QB_DEV void copy16(char* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+QB_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `rows` rows of this thread's copies have landed.
+QB_DEV void copies_wait(int rows) {
+    if (rows == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (rows == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (rows == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+// This thread's pieces of 8 elements of a row.
+template <typename T, int kItems>
+QB_DEV void copy_row(char* dst, const T* row, int items) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int at = threadIdx.x + i * blockDim.x;
+        if (at >= items) break;
+#pragma unroll
+        for (int b = 0; b < 8 * (int)sizeof(T); b += 16)
+            copy16(dst + 8 * at * (int)sizeof(T) + b, reinterpret_cast<const char*>(row + 8 * at) + b);
+    }
+}
+
+template <typename TX, typename TR, bool kQuant, int kItems>
+__global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsnorm_rows(const NormArgs a, const Ring ring) {
+    extern __shared__ __align__(128) char sm[];
+    __shared__ float scratch[kNormThreads / 32];
+    const int items = a.H >> 3, x_bytes = a.H * (int)sizeof(TX);
+    long long next = blockIdx.x;
+    auto bring = [&](int s) {
+        if (next < a.T) {
+            char* dst = sm + s * ring.bytes;
+            copy_row<TX, kItems>(dst, static_cast<const TX*>(a.x) + next * a.ldx, items);
+            if (a.residual) copy_row<TR, kItems>(dst + x_bytes, static_cast<const TR*>(a.residual) + next * a.ldr, items);
+        }
+        next += gridDim.x;
+        copies_commit();
+    };
+    for (int i = 0; i < ring.stages; ++i) bring(i);
+    int s = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+        copies_wait(ring.stages - 1);
+        const TX* x = reinterpret_cast<const TX*>(sm + s * ring.bytes);
+        const TR* residual = reinterpret_cast<const TR*>(sm + s * ring.bytes + x_bytes);
+        float v[kItems][8], ss[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            load8<TX, true>(x, at, a.H, v[i]);
+            if (a.residual) {
+                float r[8];
+                load8<TR, true>(residual, at, a.H, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = to_f32<TR>(from_f32<TR>(v[i][j] + r[j]));
+                store8<TR, true>(static_cast<TR*>(a.total) + t * a.ldt, at, a.H, v[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+        }
+        bring(s);   // this thread has read its pieces
+        if (++s == ring.stages) s = 0;
+        row_sum<1>(ss, scratch);
+        const float r = inverse_rms(ss[0], a.H, a.eps);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            float g[8], out[8];
+            load8<float, true>(a.gamma, at, a.H, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
+            if (kQuant) {
+                mxfp8_store(v[i], a.codes + t * a.H + 8 * at, a.scales + t * (items >> 2) + (at >> 2), out);
+                if (a.y) store8<__nv_bfloat16, true>(static_cast<__nv_bfloat16*>(a.y) + t * a.ldy, at, a.H, out);
+            } else {
+                store8<TX, true>(static_cast<TX*>(a.y) + t * a.ldy, at, a.H, v[i]);
+            }
+        }
+    }
+}
+
 struct NormGradArgs {
     int T, H;
     const void* dn;
@@ -278,14 +372,83 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const Nor
     }
 }
 
+// The same over a ring of rows: dn, total and dtotal are read twice from shared memory, which leaves
+// registers for the gain's sums.
+template <typename TD, typename TT, int kItems>
+__global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsnorm_backward_rows(const NormGradArgs a, const Ring ring) {
+    extern __shared__ __align__(128) char sm[];
+    __shared__ float scratch[2 * (kNormThreads / 32)];
+    const int items = a.H >> 3, d_bytes = a.H * (int)sizeof(TD), t_bytes = a.H * (int)sizeof(TT);
+    long long next = blockIdx.x;
+    auto bring = [&](int s) {
+        if (next < a.T) {
+            char* dst = sm + s * ring.bytes;
+            copy_row<TD, kItems>(dst, static_cast<const TD*>(a.dn) + next * a.lddn, items);
+            copy_row<TT, kItems>(dst + d_bytes, static_cast<const TT*>(a.total) + next * a.ldt, items);
+            if (a.dtotal) copy_row<TT, kItems>(dst + d_bytes + t_bytes, static_cast<const TT*>(a.dtotal) + next * a.lddt, items);
+        }
+        next += gridDim.x;
+        copies_commit();
+    };
+    for (int i = 0; i < ring.stages; ++i) bring(i);
+    float acc[kItems][8] = {};
+    int s = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+        copies_wait(ring.stages - 1);
+        const TD* dn = reinterpret_cast<const TD*>(sm + s * ring.bytes);
+        const TT* total = reinterpret_cast<const TT*>(sm + s * ring.bytes + d_bytes);
+        const TT* dtotal = reinterpret_cast<const TT*>(sm + s * ring.bytes + d_bytes + t_bytes);
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            float d[8], v[8], g[8];
+            load8<TD, true>(dn, at, a.H, d);
+            load8<TT, true>(total, at, a.H, v);
+            load8<float, true>(a.gamma, at, a.H, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], v[j], sum[0]), sum[1] = fmaf(d[j] * g[j], v[j], sum[1]);
+        }
+        row_sum<2>(sum, scratch);
+        const float r = inverse_rms(sum[0], a.H, a.eps), c = sum[1] / (float)a.H * r * r;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int at = threadIdx.x + i * blockDim.x;
+            if (at >= items) break;
+            float d[8], v[8], g[8], o[8] = {};
+            load8<TD, true>(dn, at, a.H, d);
+            load8<TT, true>(total, at, a.H, v);
+            load8<float, true>(a.gamma, at, a.H, g);
+            if (a.dtotal) load8<TT, true>(dtotal, at, a.H, o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                acc[i][j] = fmaf(d[j], v[j] * r, acc[i][j]);
+                o[j] += (d[j] * g[j] - v[j] * c) * r;
+            }
+            store8<TT, true>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+        }
+        bring(s);   // this thread has read its pieces
+        if (++s == ring.stages) s = 0;
+    }
+    if (!a.parts) return;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int at = threadIdx.x + i * blockDim.x;
+        if (at < items) store8<float, true>(a.parts + (long long)blockIdx.x * a.H, at, a.H, acc[i]);
+    }
+}
+
 // dgamma: the parts of 32 columns a CTA, eight runs of them added in order.
 __global__ void __launch_bounds__(256) k_gain_finish(int parts, int H, const float* __restrict__ part,
                                                      float* __restrict__ dgamma) {
     __shared__ float line[8][33];
     const int j = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
-    if (j < H)
+    if (j < H) {
+#pragma unroll 8
         for (int p = threadIdx.y; p < parts; p += 8) s += part[(long long)p * H + j];
+    }
     line[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && j < H) {
@@ -312,6 +475,20 @@ int gain_parts(int T, int H) {
     return (int)(ctas < kGainParts ? ctas : kGainParts);
 }
 
+// Whether the rows go through a ring, and its shape: enough rows for two CTAs a SM to take several
+// each, and two rows at least in half of the shared memory.
+constexpr int kRingBytes = 112 * 1024;
+bool use_ring(int T, int H, bool vec) { return vec && H > 1024 && T >= 8 * qbh::sm_count(); }
+Ring ring_of(int bytes) {
+    Ring r{};
+    r.bytes = (bytes + 127) & ~127;
+    r.stages = kRingBytes / r.bytes;
+    if (r.stages > kRingStages) r.stages = kRingStages;
+    return r;
+}
+// Threads of a ring's CTA: two pieces of 8 elements each up to 8192, four beyond.
+int ring_threads(int H) { return ((H + 8 * (H > 8192 ? 4 : 2) - 1) / (8 * (H > 8192 ? 4 : 2)) + 31) & ~31; }
+
 // Calls f with a value of each of two types.
 template <typename F>
 void with_types(int first, int second, F f) {
@@ -319,7 +496,30 @@ void with_types(int first, int second, F f) {
     else second == QBMOE_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
+template <typename K>
+int allow_ring(K kern) { return qbh::cuda_err(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)); }
+
 }  // namespace
+
+namespace qbh {
+
+int rmsnorm_init() {
+    int rc = 0;
+    for (int i = 0; i < 4 && !rc; ++i)
+        with_types(i & 1 ? QBMOE_BF16 : QBMOE_F32, i & 2 ? QBMOE_BF16 : QBMOE_F32, [&](auto first, auto second) {
+            using A = decltype(first);
+            using B = decltype(second);
+            rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 2>);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 2>);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 4>);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 4>);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 2>);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 4>);
+        });
+    return rc;
+}
+
+}  // namespace qbh
 
 extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long long ldx, int res_type,
                                const void* residual, long long ldr, const float* gamma, float eps, void* total,
@@ -341,9 +541,19 @@ extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long lon
     const NormArgs a{T, H, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, codes, scales};
     const dim3 block = row_block(H);
     const unsigned grid = (unsigned)(((long long)T + block.y - 1) / block.y);
+    const Ring ring = ring_of(H * (size_of(x_type) + (residual ? size_of(res_type) : 0)));
+    const bool rows = use_ring(T, H, vec) && ring.stages >= 2;
     with_types(x_type, residual ? res_type : x_type, [&](auto tx, auto tr) {
         using TX = decltype(tx);
         using TR = decltype(tr);
+        if (rows) {
+            auto stream_rows = [&](auto kern) {
+                kern<<<2 * qbh::sm_count(), ring_threads(H), ring.stages * ring.bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a, ring);
+            };
+            if (H <= 8192) codes ? stream_rows(k_add_rmsnorm_rows<TX, TR, true, 2>) : stream_rows(k_add_rmsnorm_rows<TX, TR, false, 2>);
+            else codes ? stream_rows(k_add_rmsnorm_rows<TX, TR, true, 4>) : stream_rows(k_add_rmsnorm_rows<TX, TR, false, 4>);
+            return;
+        }
         auto go = [&](auto kern) { kern<<<grid, block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a); };
         if (vec) codes ? go(k_add_rmsnorm<TX, TR, true, true>) : go(k_add_rmsnorm<TX, TR, true, false>);
         else codes ? go(k_add_rmsnorm<TX, TR, false, true>) : go(k_add_rmsnorm<TX, TR, false, false>);
@@ -379,11 +589,18 @@ extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* d
     float* parts = dgamma ? static_cast<float*>(workspace) : nullptr;
     const NormGradArgs a{T, H, dn, lddn, total, ldt, gamma, eps, dtotal, lddt, dx, lddx, parts};
     const dim3 block = row_block(H);
-    const int grid = gain_parts(T, H);
+    const Ring ring = ring_of(H * (size_of(dn_type) + size_of(total_type) * (dtotal ? 2 : 1)));
+    const bool rows = use_ring(T, H, vec) && ring.stages >= 2;
+    const int grid = rows ? min(2 * qbh::sm_count(), kGainParts) : gain_parts(T, H);
     const size_t smem = block.y > 1 ? (size_t)kRowWarps * H * 4 : 0;
     with_types(dn_type, total_type, [&](auto td, auto tt) {
         using TD = decltype(td);
         using TT = decltype(tt);
+        if (rows) {
+            if (H <= 8192) k_add_rmsnorm_backward_rows<TD, TT, 2><<<grid, ring_threads(H), ring.stages * ring.bytes, s>>>(a, ring);
+            else k_add_rmsnorm_backward_rows<TD, TT, 4><<<grid, ring_threads(H), ring.stages * ring.bytes, s>>>(a, ring);
+            return;
+        }
         if (vec) k_add_rmsnorm_backward<TD, TT, true><<<grid, block, smem, s>>>(a);
         else k_add_rmsnorm_backward<TD, TT, false><<<grid, block, smem, s>>>(a);
     });
