@@ -63,7 +63,7 @@ QB_DEV void store8(T* __restrict__ row, int i, int H, const float (&v)[8]) {
 }
 
 // Sums of kSums values over the threads of a row, the same bits in each: a warp's by
-// shuffles, then the warps' in order.
+// shuffles, then the warps' sums by shuffles.
 template <int kSums>
 QB_DEV void row_sum(float (&s)[kSums], float* scratch /* [kSums][kNormThreads / 32] */) {
 #pragma unroll
@@ -79,8 +79,10 @@ QB_DEV void row_sum(float (&s)[kSums], float* scratch /* [kSums][kNormThreads / 
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < kSums; ++q) {
-        s[q] = 0.0f;
-        for (int w = 0; w < warps; ++w) s[q] += scratch[q * (kNormThreads / 32) + w];
+        const int lane = threadIdx.x & 31;
+        s[q] = lane < warps ? scratch[q * (kNormThreads / 32) + lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
     }
 }
 
@@ -218,6 +220,14 @@ QB_DEV void copies_wait(int rows) {
     else if (rows == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else if (rows == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+// The gain in shared memory, the two halves of each piece apart: 16 bytes a thread without conflicts.
+QB_DEV void gain_to_smem(float4* g, const float* gamma, int items) {
+    for (int i = threadIdx.x; i < 2 * items; i += blockDim.x) g[(i & 1) * items + (i >> 1)] = reinterpret_cast<const float4*>(gamma)[i];
+}
+QB_DEV void gain8(const float4* gain, int at, int items, float (&g)[8]) {
+    const float4 a = gain[at], b = gain[items + at];
+    g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
 }
 // This thread's pieces of 8 elements of a row.
 template <typename T, int kItems>
@@ -376,9 +386,11 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const Nor
 // registers for the gain's sums.
 template <typename TD, typename TT, int kItems>
 __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsnorm_backward_rows(const NormGradArgs a, const Ring ring) {
-    extern __shared__ __align__(128) char sm[];
+    extern __shared__ __align__(128) char smem[];
     __shared__ float scratch[2 * (kNormThreads / 32)];
     const int items = a.H >> 3, d_bytes = a.H * (int)sizeof(TD), t_bytes = a.H * (int)sizeof(TT);
+    float4* gain = reinterpret_cast<float4*>(smem);
+    char* sm = smem + a.H * 4;
     long long next = blockIdx.x;
     auto bring = [&](int s) {
         if (next < a.T) {
@@ -391,6 +403,8 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
         copies_commit();
     };
     for (int i = 0; i < ring.stages; ++i) bring(i);
+    gain_to_smem(gain, a.gamma, items);
+    __syncthreads();
     float acc[kItems][8] = {};
     int s = 0;
     for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
             float d[8], v[8], g[8];
             load8<TD, true>(dn, at, a.H, d);
             load8<TT, true>(total, at, a.H, v);
-            load8<float, true>(a.gamma, at, a.H, g);
+            gain8(gain, at, items, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], v[j], sum[0]), sum[1] = fmaf(d[j] * g[j], v[j], sum[1]);
         }
@@ -419,7 +433,7 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
             float d[8], v[8], g[8], o[8] = {};
             load8<TD, true>(dn, at, a.H, d);
             load8<TT, true>(total, at, a.H, v);
-            load8<float, true>(a.gamma, at, a.H, g);
+            gain8(gain, at, items, g);
             if (a.dtotal) load8<TT, true>(dtotal, at, a.H, o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -439,20 +453,21 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
     }
 }
 
-// dgamma: the parts of 32 columns a CTA, eight runs of them added in order.
-__global__ void __launch_bounds__(256) k_gain_finish(int parts, int H, const float* __restrict__ part,
+// dgamma: the parts of 32 columns a CTA, kFinishRows runs of them added in order.
+constexpr int kFinishRows = 32;
+__global__ void __launch_bounds__(32 * kFinishRows) k_gain_finish(int parts, int H, const float* __restrict__ part,
                                                      float* __restrict__ dgamma) {
-    __shared__ float line[8][33];
+    __shared__ float line[kFinishRows][33];
     const int j = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
     if (j < H) {
 #pragma unroll 8
-        for (int p = threadIdx.y; p < parts; p += 8) s += part[(long long)p * H + j];
+        for (int p = threadIdx.y; p < parts; p += kFinishRows) s += part[(long long)p * H + j];
     }
     line[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && j < H) {
-        for (int w = 1; w < 8; ++w) s += line[w][threadIdx.x];
+        for (int w = 1; w < kFinishRows; ++w) s += line[w][threadIdx.x];
         dgamma[j] = s;
     }
 }
@@ -475,19 +490,30 @@ int gain_parts(int T, int H) {
     return (int)(ctas < kGainParts ? ctas : kGainParts);
 }
 
-// Whether the rows go through a ring, and its shape: enough rows for two CTAs a SM to take several
-// each, and two rows at least in half of the shared memory.
+// Whether the rows go through a ring, and its shape: two CTAs a SM up to rows of 8192, one beyond,
+// with two rows at least (and the gain, where it is read twice a row) in their shared memory, and
+// rows enough for several a CTA.
 constexpr int kRingBytes = 112 * 1024;
-bool use_ring(int T, int H, bool vec) { return vec && H > 1024 && T >= 8 * qbh::sm_count(); }
-Ring ring_of(int bytes) {
-    Ring r{};
-    r.bytes = (bytes + 127) & ~127;
-    r.stages = kRingBytes / r.bytes;
-    if (r.stages > kRingStages) r.stages = kRingStages;
+constexpr int kWide = 8192;
+struct RingShape {
+    Ring ring;
+    bool use;
+    int grid, threads;
+    size_t smem;
+};
+RingShape ring_of(int T, int H, int bytes, int gain_bytes, bool vec) {
+    const int per_sm = H > kWide ? 1 : 2, items = H > kWide ? 4 : 2;
+    RingShape r{};
+    r.ring.bytes = bytes;
+    r.ring.stages = (kRingBytes * (2 / per_sm) - gain_bytes) / bytes;
+    if (r.ring.stages > kRingStages) r.ring.stages = kRingStages;
+    r.grid = per_sm * qbh::sm_count();
+    if (r.grid > kGainParts) r.grid = kGainParts;
+    r.threads = ((H + 8 * items - 1) / (8 * items) + 31) & ~31;
+    r.smem = gain_bytes + (size_t)r.ring.stages * bytes;
+    r.use = vec && H > 1024 && T >= 4 * r.grid && r.ring.stages >= 2;
     return r;
 }
-// Threads of a ring's CTA: two pieces of 8 elements each up to 8192, four beyond.
-int ring_threads(int H) { return ((H + 8 * (H > 8192 ? 4 : 2) - 1) / (8 * (H > 8192 ? 4 : 2)) + 31) & ~31; }
 
 // Calls f with a value of each of two types.
 template <typename F>
@@ -497,7 +523,9 @@ void with_types(int first, int second, F f) {
 }
 
 template <typename K>
-int allow_ring(K kern) { return qbh::cuda_err(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)); }
+int allow_ring(K kern, int bytes) {
+    return qbh::cuda_err(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+}
 
 }  // namespace
 
@@ -509,12 +537,12 @@ int rmsnorm_init() {
         with_types(i & 1 ? QBMOE_BF16 : QBMOE_F32, i & 2 ? QBMOE_BF16 : QBMOE_F32, [&](auto first, auto second) {
             using A = decltype(first);
             using B = decltype(second);
-            rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 2>);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 2>);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 4>);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 4>);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 2>);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 4>);
+            rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 2>, kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 2>, kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 4>, 2 * kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 4>, 2 * kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 2>, kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 4>, 2 * kRingBytes);
         });
     return rc;
 }
@@ -541,16 +569,15 @@ extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long lon
     const NormArgs a{T, H, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, codes, scales};
     const dim3 block = row_block(H);
     const unsigned grid = (unsigned)(((long long)T + block.y - 1) / block.y);
-    const Ring ring = ring_of(H * (size_of(x_type) + (residual ? size_of(res_type) : 0)));
-    const bool rows = use_ring(T, H, vec) && ring.stages >= 2;
+    const RingShape rows = ring_of(T, H, H * (size_of(x_type) + (residual ? size_of(res_type) : 0)), 0, vec);
     with_types(x_type, residual ? res_type : x_type, [&](auto tx, auto tr) {
         using TX = decltype(tx);
         using TR = decltype(tr);
-        if (rows) {
+        if (rows.use) {
             auto stream_rows = [&](auto kern) {
-                kern<<<2 * qbh::sm_count(), ring_threads(H), ring.stages * ring.bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a, ring);
+                kern<<<rows.grid, rows.threads, rows.smem, reinterpret_cast<cudaStream_t>(stream)>>>(a, rows.ring);
             };
-            if (H <= 8192) codes ? stream_rows(k_add_rmsnorm_rows<TX, TR, true, 2>) : stream_rows(k_add_rmsnorm_rows<TX, TR, false, 2>);
+            if (H <= kWide) codes ? stream_rows(k_add_rmsnorm_rows<TX, TR, true, 2>) : stream_rows(k_add_rmsnorm_rows<TX, TR, false, 2>);
             else codes ? stream_rows(k_add_rmsnorm_rows<TX, TR, true, 4>) : stream_rows(k_add_rmsnorm_rows<TX, TR, false, 4>);
             return;
         }
@@ -589,21 +616,20 @@ extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* d
     float* parts = dgamma ? static_cast<float*>(workspace) : nullptr;
     const NormGradArgs a{T, H, dn, lddn, total, ldt, gamma, eps, dtotal, lddt, dx, lddx, parts};
     const dim3 block = row_block(H);
-    const Ring ring = ring_of(H * (size_of(dn_type) + size_of(total_type) * (dtotal ? 2 : 1)));
-    const bool rows = use_ring(T, H, vec) && ring.stages >= 2;
-    const int grid = rows ? min(2 * qbh::sm_count(), kGainParts) : gain_parts(T, H);
+    const RingShape rows = ring_of(T, H, H * (size_of(dn_type) + size_of(total_type) * (dtotal ? 2 : 1)), H * 4, vec);
+    const int grid = rows.use ? rows.grid : gain_parts(T, H);
     const size_t smem = block.y > 1 ? (size_t)kRowWarps * H * 4 : 0;
     with_types(dn_type, total_type, [&](auto td, auto tt) {
         using TD = decltype(td);
         using TT = decltype(tt);
-        if (rows) {
-            if (H <= 8192) k_add_rmsnorm_backward_rows<TD, TT, 2><<<grid, ring_threads(H), ring.stages * ring.bytes, s>>>(a, ring);
-            else k_add_rmsnorm_backward_rows<TD, TT, 4><<<grid, ring_threads(H), ring.stages * ring.bytes, s>>>(a, ring);
+        if (rows.use) {
+            if (H <= kWide) k_add_rmsnorm_backward_rows<TD, TT, 2><<<grid, rows.threads, rows.smem, s>>>(a, rows.ring);
+            else k_add_rmsnorm_backward_rows<TD, TT, 4><<<grid, rows.threads, rows.smem, s>>>(a, rows.ring);
             return;
         }
         if (vec) k_add_rmsnorm_backward<TD, TT, true><<<grid, block, smem, s>>>(a);
         else k_add_rmsnorm_backward<TD, TT, false><<<grid, block, smem, s>>>(a);
     });
-    if (dgamma) k_gain_finish<<<(H + 31) / 32, dim3(32, 8), 0, s>>>(grid, H, parts, dgamma);
+    if (dgamma) k_gain_finish<<<(H + 31) / 32, dim3(32, kFinishRows), 0, s>>>(grid, H, parts, dgamma);
     return qbh::cuda_err(cudaGetLastError());
 }

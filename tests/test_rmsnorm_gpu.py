@@ -209,3 +209,26 @@ def test_many_short_rows():
     dx, dg = Q.add_rmsnorm_backward(wide.cuda(), wide.cuda(), torch.ones(2240).cuda(), eps=EPS)
     near(dx, wx, 2.0 ** -18 * mx + 2.0 ** -8 * np.abs(wx))
     near(dg, wg, (2.0 ** -19 + 1100 * 2.0 ** -24) * mg)
+
+
+@pytest.mark.parametrize("x,res", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("T,H", [(1216, 1032), (1217, 3584), (2500, 1056), (609, 8200), (1531, 8192), (610, 16384)])
+def test_many_rows(T, H, x, res):
+    """Rows enough that each CTA takes several in turn."""
+    import quantile_balanced_routing_gb300 as Q
+    a, b, o, g = data(T, T, H, x), data(T + 1, T, H + 8, res, 2.0)[:, :H], data(T + 2, T, H, res), gain(H, H)
+    total = (a.float() + b.float()).to(res)
+    n = F.norm(f64(total), f64(g), EPS)
+    got = Q.add_rmsnorm(a.cuda(), g.cuda(), residual=b.cuda(), eps=EPS)
+    assert torch.equal(got.total.cpu(), total)
+    near(got.y, n, (2.0 ** -19 + HALF[x]) * np.abs(n))
+    if H % 32 == 0:
+        r = Q.add_rmsnorm(a.cuda(), g.cuda(), residual=b.cuda(), eps=EPS, mxfp8=True)
+        assert torch.equal(r.total.cpu(), total)
+        near8(r.q, r.y, n)
+    for dtotal in (None, o):
+        kw = {} if dtotal is None else dict(dtotal=o.cuda())
+        (wx, mx), (wg, mg) = F.norm_backward(f64(a), f64(total), f64(g), None if dtotal is None else f64(o), EPS)
+        dx, dg = Q.add_rmsnorm_backward(a.cuda(), total.cuda(), g.cuda(), eps=EPS, **kw)
+        near(dx, wx, 2.0 ** -18 * mx + HALF[res] * np.abs(wx))
+        near(dg, wg, (2.0 ** -19 + (T + 100) * 2.0 ** -24) * mg)
