@@ -409,9 +409,9 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *   written), but x at its own precision: QBMOE_BF16 [R, K], row stride ldx, or
  *   QBMOE_MXFP8 (x the codes, x_scales the scales, ldx = K).  y [R, N] of y_type
  *   (QBMOE_BF16 or QBMOE_F32), row stride ldy.  Each expert's weights are read
- *   once per 8 or 16 of its rows: meant for few rows an expert.
+ *   once per 8 of its rows, or 24 (below): meant for few rows an expert.
  *   workspace: device, 256-byte aligned, >= qbmoe_mxfp4_matvec_workspace_bytes(R, N, K)
- *   bytes (0, and NULL allowed, up to K = 8192).
+ *   bytes (0, and NULL allowed, for few rows and small weights up to K = 8192).
  *
  * moe_mxfp4_experts: for T tokens with the experts idx [T, k] (an entry outside
  *   [0, E) stands for no route) and weights w [T, k] of moe_route_qb,
@@ -423,10 +423,14 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *   T k at most QBMOE_MAX_ROUTES.  workspace: device, 256-byte aligned, >=
  *   qbmoe_mxfp4_experts_workspace_bytes(T, k, L, M) bytes.
  *
- * Both multiply exact values: weights as they are; each block of 32 of a bf16 row as
- * fp16 times a power of two, exact for elements down to 2^-29 of the block's largest and
- * within 2^-40 of it below.  The SiTU-GLU's fp32 result is rounded to fp16 that way
- * (2^-12).  Sums are fp32, in an order that does not depend on the other rows: bit-reproducible.
+ * Both take weights and MXFP8 rows as they are.  Small calls, depths that are not multiples of 256 or
+ * over 8192, and calls with an infinity or a block of magnitudes below 2^-100 in x take each block of 32 of a
+ * bf16 row as fp16 times a power of two: exact for elements down to 2^-29 of the block's largest
+ * and within 2^-40 of it below; the SiTU-GLU's fp32 result is rounded to fp16 that way
+ * (2^-12).  All others take bf16 rows, and the SiTU-GLU's result, as sums of eight MXFP4 rows: within
+ * 2^-22 of a block's largest (bf16 elements down to 2^-14 of it are exact), and of 2^-121.  Sums are fp32 in a
+ * fixed order: bit-reproducible.  So are a block's products before the weights' scale: where they pass
+ * fp32's range the result is infinite.
  * 0 <= R <= QBMOE_MAX_ROWS, 1 <= E <= QBMOE_MAX_EXPERTS, 1 <= k <= QBMOE_MAX_TOPK, N a
  * multiple of 8, K, L and M multiples of 32 and at most QBMOE_MATVEC_MAX_K, E N below 2^31.  Pointers
  * 16-byte aligned (idx, w and gamma: 4), ldx a multiple of 8 elements; y aligned to its type.

@@ -47,6 +47,7 @@ int qbh::device_init() {
     if (!rc) rc = qbh::matvec_init();
     if (!rc) rc = qbh::experts_init();
     if (!rc) rc = qbh::rmsnorm_init();
+    if (!rc) rc = qbh::pieces_init();
     if (rc) {
         cudaGetLastError();
         return rc;

@@ -3,6 +3,7 @@
 // [K3-width] 延伸解读 on deployment: routed-expert weights in MXFP4; Q&A SiTU-GLU and
 // RMSNorm: the experts' activation and the norm of their weighted sum.
 #include "mxfp4_stream.cuh"
+#include "pieces.cuh"
 
 namespace {
 
@@ -102,10 +103,24 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs a
     for (int at = threadIdx.x + kCombineKeep * kCombineThreads; at < n; at += kCombineThreads) store(at, weighted(a, row, w, m, 4 * at));
 }
 
-// Scratch of an experts call: act; gate and up in slabs; the routes' rows.
+// Scratch of an experts call: act; gate and up in slabs; the routes' rows.  In pieces: x's pieces where the rows
+// come later, gate and up where act would be, act's pieces, and what a split leaves.
 struct ExpertsScratch {
-    size_t act, parts, rows, bytes;
+    size_t act, parts, rows, act_pieces, offsets, row_map, flags, bytes;
+    bool pieces;
     ExpertsScratch(int T, int k, int L, int M) {
+        pieces = qbh::pieces_ok(L) && qbh::pieces_ok(M) && slabs_of(L) == 1 && slabs_of(M) == 1;
+        if (pieces) {
+            const size_t R = (size_t)T * k;
+            act = parts = 0;
+            rows = qbh::align_up(2 * R * M * 4, 256);
+            act_pieces = rows + max(qbh::align_up(R * L * 4, 256), qbh::piece_bytes(R, L));
+            offsets = act_pieces + qbh::piece_bytes(R, M);
+            row_map = offsets + qbh::align_up((QBMOE_MAX_EXPERTS + 1) * 4, 256);
+            flags = row_map + qbh::align_up(R * 4, 256);
+            bytes = flags + qbh::kPieceFlags * 4;
+            return;
+        }
         const size_t R = (size_t)T * k, up = slabs_of(L), down = slabs_of(M);
         act = 0;
         parts = qbh::align_up(R * M * 4, 256);
@@ -161,7 +176,23 @@ extern "C" int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, 
     a.idx = idx; a.k = k;
     a.y_type = QBMOE_F32; a.y = slabs_of(L) > 1 ? parts : act; a.ldy = M;
     a.beta1 = beta1; a.beta2 = beta2;
-    int rc2 = x_type == QBMOE_BF16 ? ::stream<QBMOE_BF16, kGlu>(a, gate_codes, up_codes, s) : ::stream<QBMOE_MXFP8, kGlu>(a, gate_codes, up_codes, s);
+    int rc2 = 0;
+    if (at.pieces && qbh::pieces_pay(min(E, a.R), a.R, 3LL * L * M)) {
+        uint8_t *xp = reinterpret_cast<uint8_t*>(rows), *ap = reinterpret_cast<uint8_t*>(base + at.act_pieces);
+        int32_t *offsets = reinterpret_cast<int32_t*>(base + at.offsets), *row_map = reinterpret_cast<int32_t*>(base + at.row_map);
+        int* flags = reinterpret_cast<int*>(base + at.flags);
+        rc2 = qbh::split_routes(T, k, E, L, x_type, x, ldx, x_scales, idx, xp, offsets, row_map, flags, &a.n_flags, s);
+        if (rc2) return rc2;
+        const qbh::PieceProduct up{a.R, E, M, L, xp, xp + qbh::piece_code_bytes(a.R, L), gate_codes, gate_scales, up_codes, up_scales,
+                                   offsets, nullptr, act, QBMOE_F32, 2LL * M};
+        if ((rc2 = qbh::piece_product(up, s))) return rc2;
+        if ((rc2 = qbh::split_glu(a.R, E, M, act, beta1, beta2, offsets, ap, s))) return rc2;
+        const qbh::PieceProduct down{a.R, E, L, M, ap, ap + qbh::piece_code_bytes(a.R, M), out_codes, out_scales, nullptr, nullptr,
+                                     offsets, row_map, rows, QBMOE_F32, L};
+        if ((rc2 = qbh::piece_product(down, s))) return rc2;
+        a.flags = flags;
+    }
+    rc2 = x_type == QBMOE_BF16 ? ::stream<QBMOE_BF16, kGlu>(a, gate_codes, up_codes, s) : ::stream<QBMOE_MXFP8, kGlu>(a, gate_codes, up_codes, s);
     if (rc2) return rc2;
     if (slabs_of(L) > 1) {
         const long long blocks = ((long long)a.R * M + 255) / 256;

@@ -2,6 +2,7 @@
 //
 // [K3-width] 延伸解读 on deployment: MXFP4 weights.
 #include "mxfp4_stream.cuh"
+#include "pieces.cuh"
 
 namespace {
 
@@ -20,6 +21,24 @@ __global__ void __launch_bounds__(256) k_slab_sum(int slabs, int R, int N, int E
     }
 }
 
+// Scratch of a call: parts of the slabs; or the rows' pieces, their offsets and flags.
+constexpr long long kMostPieces = 1LL << 25;   // elements of x that are split: 143 MB of pieces
+struct MatvecScratch {
+    size_t parts = 0, offsets = 0, flags = 0, bytes = 0;
+    bool pieces;
+    MatvecScratch(int R, int N, int K) {
+        pieces = qbh::pieces_ok(K) && slabs_of(K) == 1 && (long long)R * K <= kMostPieces &&
+                 qbh::pieces_pay(min(R, QBMOE_MAX_EXPERTS), R, (long long)N * K);   // for some E
+        if (pieces) {
+            offsets = qbh::piece_bytes(R, K);
+            flags = offsets + qbh::align_up((QBMOE_MAX_EXPERTS + 1) * 4, 256);
+            bytes = flags + qbh::kPieceFlags * 4;
+        } else if (slabs_of(K) > 1) {
+            bytes = (size_t)slabs_of(K) * R * N * 4;
+        }
+    }
+};
+
 }  // namespace
 
 namespace qbh {
@@ -32,8 +51,8 @@ int matvec_init() {
 }  // namespace qbh
 
 extern "C" size_t qbmoe_mxfp4_matvec_workspace_bytes(int R, int N, int K) {
-    if (R < 0 || R > QBMOE_MAX_ROWS || N < 8 || N % 8 || N > kMaxCols || !depth_ok(K) || slabs_of(K) == 1) return 0;
-    return (size_t)slabs_of(K) * R * N * 4;
+    if (R < 0 || R > QBMOE_MAX_ROWS || N < 8 || N % 8 || N > kMaxCols || !depth_ok(K)) return 0;
+    return MatvecScratch(R, N, K).bytes;
 }
 
 extern "C" int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const void* x, long long ldx,
@@ -43,7 +62,8 @@ extern "C" int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const vo
     if (R < 0 || R > QBMOE_MAX_ROWS || E < 1 || E > QBMOE_MAX_EXPERTS || (!offsets && E != 1) || !depth_ok(K) || N < 8 || N % 8 ||
         N > kMaxCols || (long long)E * N > 0x7fffffffLL || !rows_ok(K, x_type, ldx) || ldy < N || (y_type != QBMOE_F32 && y_type != QBMOE_BF16))
         return QBMOE_EINVAL;
-    const size_t need = qbmoe_mxfp4_matvec_workspace_bytes(R, N, K);
+    const MatvecScratch at(R, N, K);
+    const size_t need = at.bytes;
     if (need && (!workspace || !at_bytes(workspace, 256))) return QBMOE_EINVAL;
     if (workspace_bytes < need) return QBMOE_EWORKSPACE;
     if (R == 0) return QBMOE_OK;
@@ -57,11 +77,23 @@ extern "C" int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const vo
     a.R = R; a.E = E; a.N = N; a.K = K;
     a.x_type = x_type; a.x = x; a.ldx = ldx; a.x_scales = x_scales;
     a.scales = w_scales; a.offsets = offsets;
-    a.y_type = need ? QBMOE_F32 : y_type;
-    a.y = need ? workspace : y;
-    a.ldy = need ? N : ldy;
+    const bool slabs = slabs_of(K) > 1;
+    a.y_type = slabs ? QBMOE_F32 : y_type;
+    a.y = slabs ? workspace : y;
+    a.ldy = slabs ? N : ldy;
+    if (at.pieces && qbh::pieces_pay(min(E, R), R, (long long)N * K)) {
+        uint8_t* pieces = static_cast<uint8_t*>(workspace);
+        int32_t* piece_offsets = reinterpret_cast<int32_t*>(pieces + at.offsets);
+        int* flags = reinterpret_cast<int*>(pieces + at.flags);
+        int rc2 = qbh::split_rows(R, E, K, x_type, x, ldx, x_scales, offsets, pieces, piece_offsets, flags, &a.n_flags, s);
+        if (rc2) return rc2;
+        const qbh::PieceProduct p{R, E, N, K, pieces, pieces + qbh::piece_code_bytes(R, K), w_codes, w_scales, nullptr, nullptr,
+                                  offsets ? piece_offsets : nullptr, nullptr, y, y_type, ldy};
+        if ((rc2 = qbh::piece_product(p, s))) return rc2;
+        a.flags = flags;
+    }
     const int rc2 = x_type == QBMOE_BF16 ? ::stream<QBMOE_BF16, kStore>(a, w_codes, nullptr, s) : ::stream<QBMOE_MXFP8, kStore>(a, w_codes, nullptr, s);
-    if (rc2 || !need) return rc2;
+    if (rc2 || !slabs) return rc2;
     const long long blocks = ((long long)R * N + 255) / 256;
     k_slab_sum<<<(unsigned)min(blocks, 8LL * qbh::sm_count()), 256, 0, s>>>(slabs_of(K), R, N, E, offsets, static_cast<float*>(workspace), y_type, y, ldy);
     return qbh::cuda_err(cudaGetLastError());

@@ -13,6 +13,7 @@ int mx_grad_init();      // mxfp4_grad.cu
 int matvec_init();       // matvec.cu
 int experts_init();      // experts.cu
 int rmsnorm_init();      // rmsnorm.cu
+int pieces_init();       // pieces.cu
 
 // Expired waits of the calls that take no context, counted on each device; and, after
 // synchronising s, whether there were any since the calling thread last asked

@@ -49,6 +49,7 @@
 // Every mbarrier wait is bounded: on expiry the kernel counts it
 // (mx_expiries), stops, lets its own copies and MMAs finish and frees TMEM.
 #include "mxfp4.cuh"
+#include "pieces.cuh"
 #include "tc_ptx.cuh"
 
 #include <cudaTypedefs.h>
@@ -83,7 +84,23 @@ struct Params {
     int* expiries;
     long long wait_limit;
     int stall;                               // test hook: withhold the first accumulator hand-off
+    // rows in pieces alone
+    CUtensorMap a2, a2_sf;                   // a second tensor of weights
+    const uint8_t* a2_sc;
+    int m_half;                              // its tiles come from this m on
+    const int32_t* row_map;                  // or NULL: where rows of y lie
+    void* sums;                              // y, of sums_type
+    int sums_type;
 };
+// The weights that a tile takes, and its first row in them.
+struct TileRows {
+    bool second;
+    int m;
+};
+__device__ __forceinline__ TileRows tile_rows(const Params& p, int m) {
+    const bool second = m >= p.m_half;
+    return {second, second ? m - p.m_half : m};
+}
 
 template <int BN>
 struct Shape {
@@ -152,7 +169,8 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-template <int BN>
+// kPieced: every eight columns are the pieces of one row of x, and are added, the smallest first.
+template <int BN, bool kPieced>
 __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_product(const __grid_constant__ Params p) {
     using Sh = Shape<BN>;
     constexpr int S = Sh::stages, kSfSlots = Sh::kSfSlots;
@@ -225,8 +243,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
         bool dead = false;   // lane 0: an expiry; only the meetings go on
         for (int t = first; t < n_tiles; t += step) {
             const int box = (w.nrows - 1) / Sh::kBox;
-            const CUtensorMap* map = is_a ? &p.a : &p.b[box];
-            const int row = is_a ? w.g * p.N + w.m * 128 : w.row0;
+            const TileRows of = kPieced ? tile_rows(p, w.m) : TileRows{false, w.m};
+            const CUtensorMap* map = !is_a ? &p.b[box] : of.second ? &p.a2 : &p.a;
+            const int row = is_a ? w.g * p.N + of.m * 128 : w.row0;
             const uint32_t bytes = is_a ? kABytes : (box + 1) * Sh::kBox * 128;
             constexpr int kAStride = kABytes, kBStride = Sh::kBBytes;
             const int stride = is_a ? kAStride : kBStride;
@@ -261,7 +280,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
             int gs = 0;
             uint32_t gph = 0;
             for (int t = first; t < n_tiles; t += step) {
-                const int ya = w.g * p.N + w.m * 128, yb = w.row0;
+                const TileRows of = kPieced ? tile_rows(p, w.m) : TileRows{false, w.m};
+                const int ya = w.g * p.N + of.m * 128, yb = w.row0;
+                const CUtensorMap* map = of.second ? &p.a2_sf : &p.a_sf;
                 w.next(gr, p.E, p.m_total);
                 int stop = 0;
                 if (lane == 0) {
@@ -270,7 +291,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
                         if (!tc::mbar_wait_spin(&sf_empty[gs], gph ^ 1u, lim)) { expired(); stop = 1; break; }
                         uint8_t* SF = sf_ring + gs * Sh::kSfBytes;
                         tc::mbar_expect_tx(&sf_full[gs], Sh::kSfBytes);
-                        tc::tma_load_2d(SF, &p.a_sf, &sf_full[gs], kb * 8, ya);
+                        tc::tma_load_2d(SF, map, &sf_full[gs], kb * 8, ya);
                         tc::tma_load_2d(SF + 128 * 16, &p.b_sf, &sf_full[gs], kb * 8, yb);
                         sf_issued |= 1u << gs;
                         sf_par = (sf_par & ~(1u << gs)) | (gph << gs);
@@ -284,10 +305,12 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
             const long long last_a = (long long)p.E * p.N - 1;
             uint4 ra[4], rb[Sh::kBJ];
             auto fetch = [&](int kb) {
+                const TileRows of = kPieced ? tile_rows(p, w.m) : TileRows{false, w.m};
+                const uint8_t* sc = of.second ? p.a2_sc : p.a_sc;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const long long row = min((long long)w.g * p.N + w.m * 128 + lane + 32 * j, last_a);
-                    ra[j] = load_scales(p.a_sc + row * pitch, pitch, kb * 8, p.sf_bytes);
+                    const long long row = min((long long)w.g * p.N + of.m * 128 + lane + 32 * j, last_a);
+                    ra[j] = load_scales(sc + row * pitch, pitch, kb * 8, p.sf_bytes);
                 }
 #pragma unroll
                 for (int j = 0; j < Sh::kBJ; ++j) {
@@ -464,7 +487,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
         uint32_t fph = 0;
         for (int t = first; t < n_tiles; t += step) {
             const int nrows = w.nrows, odd = lane & 1;
-            const int f = w.m * 128 + 32 * q + (lane & ~1);
+            const TileRows of = kPieced ? tile_rows(p, w.m) : TileRows{false, w.m};
+            const int f = of.m * 128 + 32 * q + (kPieced ? lane : lane & ~1), row0 = w.row0 / qbh::kPieces;
             __nv_bfloat16* out = p.y + (long long)(w.row0 + odd) * p.ldy + f;
             w.next(gr, p.E, p.m_total);
             if (warp == kEpiWarp && lane == 0) {   // one poller; an expiry leaves undefined outputs and a status
@@ -477,6 +501,20 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
             for (int c0 = 16 * part; c0 < nrows; c0 += 4 * Sh::kEpiWarps) {
                 float v[16];
                 tc::tmem_ld16(tbase + ab * BN + (static_cast<uint32_t>(32 * q) << 16) + c0, v);
+                if constexpr (kPieced) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += qbh::kPieces) {
+                        if (f >= p.N || c0 + i >= nrows) break;
+                        float sum = v[i];
+#pragma unroll
+                        for (int j = 1; j < qbh::kPieces; ++j) sum += v[i + j];
+                        const int r = row0 + (c0 + i) / qbh::kPieces;
+                        const long long at = (p.row_map ? __ldg(p.row_map + r) : r) * p.ldy + f + (of.second ? p.N : 0);
+                        if (p.sums_type == QBMOE_F32) static_cast<float*>(p.sums)[at] = sum;
+                        else static_cast<__nv_bfloat16*>(p.sums)[at] = __float2bfloat16_rn(sum);
+                    }
+                    continue;
+                }
                 __nv_bfloat16* o = out + (long long)c0 * p.ldy;
                 const int left = f < p.N ? nrows - c0 - odd : 0;
 #pragma unroll
@@ -529,13 +567,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-template <int BN>
+template <int BN, bool kPieced>
 int set_attributes() {
-    return qbh::cuda_err(cudaFuncSetAttribute(k_mx_product<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return qbh::cuda_err(cudaFuncSetAttribute(k_mx_product<BN, kPieced>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               Shape<BN>::smem(QBMOE_MAX_EXPERTS)));
 }
 
-template <int BN>
+template <int BN, bool kPieced = false>
 int launch(const qbh::MxProduct& q, Params& p, cudaStream_t s) {
     for (int i = 0; i < Shape<BN>::kBoxes; ++i)
         if (!qbh::encode_rows(&p.b[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x_codes, q.R, q.K / 2, q.K / 2, 128,
@@ -552,9 +590,10 @@ int launch(const qbh::MxProduct& q, Params& p, cudaStream_t s) {
         // the product may set itself up, and load weights, while its rows are quantised
         const int rc = qbh::mx_quantize(q.R, q.K, q.raw_type, q.raw, q.raw_ld, q.x_codes, q.x_scales, nullptr, s);
         if (rc) return rc;
-        return qbh::launch_pdl(k_mx_product<BN>, dim3(grid), dim3(Shape<BN>::kThreads), smem, s, p);
+        return qbh::launch_pdl(k_mx_product<BN, kPieced>, dim3(grid), dim3(Shape<BN>::kThreads), smem, s, p);
     }
-    k_mx_product<BN><<<grid, Shape<BN>::kThreads, smem, s>>>(p);
+    if (kPieced) return qbh::launch_pdl(k_mx_product<BN, kPieced>, dim3(grid), dim3(Shape<BN>::kThreads), smem, s, p);
+    k_mx_product<BN, kPieced><<<grid, Shape<BN>::kThreads, smem, s>>>(p);
     return qbh::cuda_err(cudaGetLastError());
 }
 
@@ -568,11 +607,15 @@ int mx_product_init() {
     void* f = nullptr;
     int rc = cuda_err(cudaGetSymbolAddress(&f, g_expiries));
     if (!rc) rc = cuda_err(cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev));
-    if (!rc) rc = set_attributes<16>();
-    if (!rc) rc = set_attributes<64>();
-    if (!rc) rc = set_attributes<128>();
-    if (!rc) rc = set_attributes<192>();
-    if (!rc) rc = set_attributes<208>();
+    if (!rc) rc = set_attributes<16, false>();
+    if (!rc) rc = set_attributes<64, false>();
+    if (!rc) rc = set_attributes<128, false>();
+    if (!rc) rc = set_attributes<192, false>();
+    if (!rc) rc = set_attributes<208, false>();
+    if (!rc) rc = set_attributes<16, true>();
+    if (!rc) rc = set_attributes<64, true>();
+    if (!rc) rc = set_attributes<128, true>();
+    if (!rc) rc = set_attributes<192, true>();
     if (!rc) g_expiries_ptr[dev] = static_cast<int*>(f);
     return rc;
 }
@@ -620,27 +663,63 @@ bool encode_rows(CUtensorMap* m, CUtensorMapDataType type, const void* base, lon
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int mx_product(const MxProduct& q, cudaStream_t s) {
-    Params p{};
-    if (!encode_rows(&p.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w_codes, (long long)q.E * q.N, q.K / 2, q.K / 2, 128, 128))
-        return QBMOE_ECUDA;
+}  // namespace qbh
+
+namespace {
+
+bool encode_weights(CUtensorMap* codes, CUtensorMap* scales, const uint8_t* w_codes, const uint8_t* w_scales, long long rows, int K) {
+    return qbh::encode_rows(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, rows, K / 2, K / 2, 128, 128) &&
+           (K % 512 || qbh::encode_rows(scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_scales, rows, K / 32, K / 32, 16, 128, true));
+}
+
+// What all products share.
+bool params_of(const qbh::MxProduct& q, Params& p) {
+    if (!encode_weights(&p.a, &p.a_sf, q.w_codes, q.w_scales, (long long)q.E * q.N, q.K)) return false;
     p.sf_tma = q.K % 512 == 0;
-    if (p.sf_tma && !encode_rows(&p.a_sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w_scales, (long long)q.E * q.N, q.K / 32,
-                                 q.K / 32, 16, 128, true))
-        return QBMOE_ECUDA;
     p.a_sc = q.w_scales;
     p.b_sc = q.x_scales;
     p.offsets = q.offsets;
-    p.y = static_cast<__nv_bfloat16*>(q.y);
     p.ldy = q.ldy;
     p.R = q.R; p.E = q.E; p.N = q.N; p.K = q.K;
     p.nkb = (q.K + kStageK - 1) / kStageK;
     p.m_total = (q.N + 127) / 128;
     p.sf_bytes = q.K % 256 == 0 ? 8 : q.K % 128 == 0 ? 4 : 1;
     p.weights_ready = q.raw != nullptr;
-    p.expiries = mx_expiries();
+    p.expiries = qbh::mx_expiries();
     p.wait_limit = t_wait_limit;
     p.stall = t_stall;
+    return true;
+}
+
+}  // namespace
+
+namespace qbh {
+
+int piece_product(const PieceProduct& q, cudaStream_t s) {
+    const MxProduct m{q.R * kPieces, q.E, q.N, q.K, const_cast<uint8_t*>(q.x_codes), const_cast<uint8_t*>(q.x_scales),
+                      q.w_codes, q.w_scales, q.offsets, nullptr, q.ldy, nullptr, 0, 0};
+    Params p{};
+    if (!params_of(m, p)) return QBMOE_ECUDA;
+    p.m_half = p.m_total;
+    if (q.w2_codes) {
+        if (!encode_weights(&p.a2, &p.a2_sf, q.w2_codes, q.w2_scales, (long long)q.E * q.N, q.K)) return QBMOE_ECUDA;
+        p.a2_sc = q.w2_scales;
+        p.m_total *= 2;
+    }
+    p.row_map = q.row_map;
+    p.sums = q.y;
+    p.sums_type = q.y_type;
+    const int avg = (m.R + q.E - 1) / q.E;
+    if (avg <= 16) return launch<16, true>(m, p, s);
+    if (avg <= 64) return launch<64, true>(m, p, s);
+    if (avg <= 128) return launch<128, true>(m, p, s);
+    return launch<192, true>(m, p, s);
+}
+
+int mx_product(const MxProduct& q, cudaStream_t s) {
+    Params p{};
+    if (!params_of(q, p)) return QBMOE_ECUDA;
+    p.y = static_cast<__nv_bfloat16*>(q.y);
     // Row tile: the smallest that holds an average expert's rows, 192 beyond. One
     // matrix whose tiles of 208 rows save over a quarter of the grid's rounds takes those (by
     // 3584 x 7168, 1040 rows, one round or two: 23.2 against 27.3 us; 1999 rows, two

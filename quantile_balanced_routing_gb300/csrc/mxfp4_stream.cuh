@@ -71,6 +71,8 @@ struct StreamArgs {
     int* expiries;
     long long wait_limit;
     int stall;
+    const int* flags;            // NULL, or: nothing to do unless one of n_flags is set
+    int n_flags;
 };
 
 // kNB blocks of 32 a warp, kMT tiles a unit; weights come in boxes, a whole number a warp, or row by row.
@@ -432,6 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
     if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
+    if (a.flags) {
+        int any = 0;
+        for (int i = threadIdx.x; i < a.n_flags; i += kThreads) any |= __ldcg(a.flags + i);
+        if (!__syncthreads_or(any)) return;
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             tc::mbar_init(full + s, 1);

@@ -1,0 +1,55 @@
+// Rows as sums of MXFP4 rows, for the block-scaled tensor cores.
+//
+// An element of a block of 32 becomes a whole number of 22 bits and a sign, in units of 2^-21 of the
+// power of two below the block's largest; its eight octal digits, from -4 to 4, are E2M1 values,
+// and digit i's MXFP4 row has the block's scale times 8^i.  So a row is the sum of eight MXFP4 rows,
+// within 2^-22 of each block's largest: E4M3 elements and bf16 elements down to 2^-14 of it are exact.
+// The product of eight columns for one costs the tensor cores what they have to spare while weights stream.
+#pragma once
+
+#include "mxfp4.cuh"
+
+namespace qbh {
+
+constexpr int kPieces = 8;
+constexpr int kPieceFlags = 1024;   // most CTAs of a split
+
+// Whether pieces pay: by the elements of weights that products of eight rows at a time would read, n matrices
+// of `elements` each and once more per eight rows.  One row by 6144 x K = 7168 (50 M) takes 23 us as it is and
+// 26 in pieces, by 12288 (99 M) 29 and 27; 64 rows by 896 x 7168 (58 M) 25 and 23; 128 rows over 24 matrices of
+// 512 x 1024 (21 M) 17 and 20; the experts (3584 x 1024, three matrices) of a token's 4 routes (50 M) 43 and 46,
+// of 8 (99 M) 57 and 49, of 256 tokens' 16 (15 G) 1325 and 895 with a cold cache.
+inline bool pieces_pay(long long n, long long rows, long long elements) { return (n + rows / 8) * elements >= 1LL << 26; }
+inline bool pieces_ok(int K) { return K % 256 == 0; }   // whole words of scales for a warp
+inline size_t piece_code_bytes(long long rows, int K) { return align_up((size_t)rows * kPieces * (K / 2), 256); }
+inline size_t piece_bytes(long long rows, int K) {
+    return piece_code_bytes(rows, K) + align_up((size_t)rows * kPieces * (K / 32), 256);
+}
+
+// y [R, N] (with a second tensor [R, 2 N]: its products behind the first's), rows moved by row_map, from the
+// pieces of R rows; offsets [E + 1] count pieces.
+struct PieceProduct {
+    int R, E, N, K;
+    const uint8_t *x_codes, *x_scales;
+    const uint8_t *w_codes, *w_scales, *w2_codes, *w2_scales;
+    const int32_t* offsets;
+    const int32_t* row_map;
+    void* y;
+    int y_type;
+    long long ldy;
+};
+int piece_product(const PieceProduct& p, cudaStream_t s);
+
+// The pieces of x [R, K] (bf16 or MXFP8), the rows that an expert owns; offsets become those of pieces.  A CTA
+// with a block that has none (an infinity, magnitudes below 2^-100) sets its flag.
+int split_rows(int R, int E, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales, const int32_t* offsets,
+               uint8_t* pieces, int32_t* piece_offsets, int* flags, int* n_flags, cudaStream_t s);
+// The same for the tokens' routes idx [T k] in expert order; row_map: the route at each place.
+int split_routes(int T, int k, int E, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales, const int32_t* idx,
+                 uint8_t* pieces, int32_t* piece_offsets, int32_t* row_map, int* flags, int* n_flags, cudaStream_t s);
+// The pieces of SiTU-GLU(h[:, :M], h[:, M:]), h [R, 2 M] fp32, for the rows that piece_offsets count.
+int split_glu(int R, int E, int M, const float* h, float beta1, float beta2, const int32_t* piece_offsets, uint8_t* pieces,
+              cudaStream_t s);
+int pieces_init();
+
+}  // namespace qbh

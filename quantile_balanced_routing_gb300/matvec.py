@@ -33,9 +33,9 @@ def _input(what, x, K):
 def mxfp4_matvec(x, w: Mxfp4, offsets=None, out_dtype=None, stream=None):
     """y [R, N] = x w^T for few rows x and MXFP4 weights w [N, K].
 
-    x is not rounded, where :func:`mxfp4_matmul` takes 4-bit rows: an :class:`Mxfp8`
+    x keeps its precision, where :func:`mxfp4_matmul` takes 4-bit rows: an :class:`Mxfp8`
     [R, K], or bf16 (rows may be strided).  y is bf16, or fp32 with out_dtype.  Meant for
-    few rows a matrix: its weights are read again for every 8 or 16 rows.
+    few rows a matrix: its weights are read again for every 8 to 24 rows.
     Grouped: w [E, N, K] and offsets [E + 1] int32, the rows in expert order;
     rows that no expert owns are left unwritten."""
     import torch

@@ -97,7 +97,8 @@ def test_matvec_refuses_strides_off_16_bytes(lib, ldx):
 
 
 def test_matvec_workspace(lib):
-    assert lib.qbmoe_mxfp4_matvec_workspace_bytes(100, 4096, 8192) == 0
+    assert lib.qbmoe_mxfp4_matvec_workspace_bytes(100, 64, 8192) == 0
+    assert lib.qbmoe_mxfp4_matvec_workspace_bytes(100, 4096, 8192) >= 100 * 8 * (4096 + 256)   # in pieces
     need = lib.qbmoe_mxfp4_matvec_workspace_bytes(4, 16, 16384)
     if need:
         big = changed(changed(changed(MATVEC, 3, 16384), 6, 16384), 15, BIG)

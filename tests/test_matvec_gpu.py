@@ -336,3 +336,184 @@ def test_many_tiles(N, K):
     wv = M.decode(codes.cpu().numpy()[:, some], scales.cpu().numpy()[:, some])
     want, bound = grouped(xv, wv, off)
     near(first[:, torch.from_numpy(some).cuda()], want, bound + HALF[torch.float32] * np.abs(want))
+
+
+# Calls whose rows become sums of MXFP4 rows: from 2^26 elements of weights on, read once and per eight rows again.
+# A bf16 element is then within 2^-22 of its block's largest: 2^-22 sum_b max_b sum_(k in b) |w| more.
+def in_pieces(n, R, N, K):
+    return (n + R // 8) * N * K >= 1 << 26
+
+
+# (In the experts' bound that is far inside the additions' term, K 2^-24 of the sum of magnitudes, as K >= 512; the
+# SiTU-GLU's result keeps 2^-22 where the bound allows 2^-12.)
+def dropped(xv, wv):
+    """2^-22 of each block's largest, times the block's weights."""
+    R, K = xv.shape
+    return 2.0 ** -22 * np.abs(xv).reshape(R, K // 32, 32).max(2) @ np.abs(wv).reshape(-1, K // 32, 32).sum(2).T
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("R,N,K", [(1000, 648, 1024), (2101, 648, 768), (4100, 640, 256), (67, 1048, 7168), (700, 264, 8192)])
+def test_dense_in_pieces(R, N, K, kind):
+    import quantile_balanced_routing_gb300 as Q
+    assert in_pieces(1, R, N, K)
+    r = np.random.RandomState(R + N + K)
+    x, xv = rows(r, R, K, kind)
+    w, wv = weights(r, N, K)
+    want, bound = F.product(xv, wv)
+    bound = bound + dropped(xv, wv)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = Q.mxfp4_matvec(x, w, out_dtype=dtype)
+        near(y, want, bound + HALF[dtype] * np.abs(want))
+    assert torch.equal(Q.mxfp4_matvec(x, w), y)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("loads,N,K", [([1, 0, 2, 3] * 100, 144, 1024), ([0, 5, 9, 0, 1, 30, 7, 8] * 20, 328, 768),
+                                       ([40, 0, 1, 100, 3] * 12, 264, 1280), ([300, 0, 25, 513], 648, 1024)])
+def test_grouped_in_pieces(loads, N, K, kind):
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(len(loads) + N + K)
+    off = np.concatenate([[0], np.cumsum(loads)]).astype(np.int32)
+    assert in_pieces(min(len(loads), off[-1]), off[-1], N, K)
+    x, xv = rows(r, int(off[-1]), K, kind)
+    w, wv = weights(r, len(loads), N, K)
+    want, bound = grouped(xv, wv, off)
+    for e, (lo, hi) in enumerate(M.groups(off, off[-1])):
+        if hi > lo:
+            bound[lo:hi] += dropped(xv[lo:hi], wv[e])
+    for dtype in (torch.float32, torch.bfloat16):
+        near(Q.mxfp4_matvec(x, w, offsets=cuda(off)[0], out_dtype=dtype), want, bound + HALF[dtype] * np.abs(want))
+
+
+def test_rows_without_an_expert_and_the_space_between_rows_stay_in_pieces():
+    r = np.random.RandomState(1)
+    R, N, K = 1100, 648, 768
+    assert in_pieces(3, R, N, K)
+    w, wv = weights(r, 3, N, K)
+    t = torch.from_numpy(r.standard_normal((R, K + 24))).to(torch.bfloat16).cuda()
+    x = t[:, 8:8 + K]
+    for off in ([4, 4, 9, 1015], [0, 903, 903, 903], [R, R, R, R]):
+        x[:off[0]], x[off[3]:] = float("nan"), float("inf")   # nobody's
+        y = torch.full((R, N + 9), 7.0, device="cuda")
+        assert call(x, K, w, cuda(np.array(off, np.int32))[0], y) == 0
+        lo, hi = off[0], off[-1]
+        want, bound = grouped(f64(x)[lo:hi], wv, np.array(off) - lo)
+        if hi > lo:
+            bound += np.maximum.reduce([dropped(f64(x)[lo:hi], wv[e]) for e in range(3)])
+        near(y[lo:hi, :N], want, bound + 2.0 ** -24 * np.abs(want))
+        assert (y[:lo] == 7).all() and (y[hi:] == 7).all() and (y[:, N:] == 7).all()
+        t.copy_(torch.from_numpy(r.standard_normal((R, K + 24))).to(torch.bfloat16))
+    y = torch.zeros(R, N, device="cuda")   # offsets out of order and out of range stay in their tensors
+    assert call(x, K, w, cuda(np.array([-5, 1 << 30, 7, R + 9], np.int32))[0], y) == 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("infinite", [False, True])
+def test_bad_rows_in_pieces(infinite):
+    """NaN stays in its row; infinities and tiny blocks take the other kernel, with the same meaning."""
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(2)
+    R, N, K = 1000, 648, 1024
+    w, wv = weights(r, N, K)
+    x = r.standard_normal((R, K))
+    x[0] *= 1e30
+    x[1] *= 1e-20
+    x[2, :32] *= 1e20
+    x[4], x[6, 41] = 0.0, np.nan
+    if infinite:
+        x[1] *= 1e-12
+        x[5, 40], x[7, 50], x[7, 51] = np.inf, np.inf, -np.inf
+    t = torch.from_numpy(x).to(torch.bfloat16)
+    y = f64(Q.mxfp4_matvec(t.cuda(), w, out_dtype=torch.float32))
+    fine = [i for i in range(R) if i not in ((5, 6, 7) if infinite else (6,))]
+    want, bound = F.product(f64(t)[fine], wv)
+    near(torch.from_numpy(y[fine]), want, bound + dropped(f64(t)[fine], wv) + 2.0 ** -24 * np.abs(want))
+    assert np.isnan(y[6]).all()
+    if infinite:
+        nz = wv[:, 40] != 0
+        assert np.array_equal(y[5][nz], np.sign(wv[nz, 40]) * np.inf) and np.isnan(y[5][~nz]).all()
+        assert not np.isfinite(y[7]).any()
+
+
+def test_mxfp8_extremes_in_pieces():
+    """Every E4M3 code but the NaNs, alone in its block, and scales in range and out of it."""
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(3)
+    R, N, K = 2048, 640, 512
+    codes = np.zeros((R, K), np.uint8)
+    codes[np.arange(R), r.randint(0, K, R)] = np.arange(R) % 256
+    codes[codes & 127 == 127] = 1
+    w, wv = weights(r, N, K)
+    for lo, hi in ((118, 136), (20, 230), (0, 254)):
+        scales = r.randint(lo, hi + 1, (R, K // 32)).astype(np.uint8)
+        xv = F.decode8(codes, scales)
+        y = f64(Q.mxfp4_matvec(Q.Mxfp8(*cuda(codes, scales)), w, out_dtype=torch.float32))
+        want = xv @ wv.T
+        # an element times a code of up to 6, before the weight's scale (2^-7 to 2^-5), is an fp32 number:
+        # beyond 2^128 it is infinite, though the product would be finite
+        fine = (np.abs(want) < 1e38) & ((np.abs(want) > 1e-36) | (want == 0)) & (6 * np.abs(xv).max(1) < 2.0 ** 128)[:, None]
+        assert np.array_equal(y[fine], want[fine].astype(np.float32))
+    scales[9, 3] = 255
+    y = Q.mxfp4_matvec(Q.Mxfp8(*cuda(codes, scales)), w)
+    assert torch.isnan(y[9]).all() and not torch.isnan(y[10:]).any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("T,k,E,L,Mi,gamma", [(100, 8, 16, 768, 512, True), (1, 16, 40, 2048, 768, False), (260, 4, 7, 512, 512, True),
+                                              (33, 32, 40, 1024, 256, True)])
+def test_experts_in_pieces(T, k, E, L, Mi, gamma, kind):
+    import quantile_balanced_routing_gb300 as Q
+    assert in_pieces(min(E, T * k), T * k, 3 * L, Mi)
+    r = np.random.RandomState(T + k + E + L)
+    x, xv = rows(r, T, L, kind)
+    (g, gv), (u, uv), (o, ov) = weights(r, E, Mi, L), weights(r, E, Mi, L), weights(r, E, L, Mi)
+    idx, w = routed(r, T, k, E, distinct=k <= E)
+    if T > 9:
+        idx[0] = 3                                                  # one expert k times
+        idx[1, 2], idx[2], idx[3, 0] = -1, E, 1 << 30               # no route: one, all, one
+    gain = (1 + 0.3 * r.standard_normal(L)).astype(np.float32) if gamma else None
+    run = lambda: Q.mxfp4_experts(x, *cuda(idx, w), g, u, o, gamma=cuda(gain)[0] if gamma else None)  # noqa: E731
+    y = run()
+    want, bound = F.experts(xv, idx, w.astype(np.float64), gv, uv, ov, gain, 1e-6)
+    near(y, want, bound + 2.0 ** -8 * np.abs(want))
+    assert torch.equal(run(), y) and (T <= 9 or not y[2].any())
+    if kind == "bf16" and T > 9:   # a token with an infinity, and one with a NaN
+        x = x.clone()
+        x[4, 3], x[5, 60] = float("inf"), float("nan")
+        y = run()
+        keep = [t for t in range(T) if t not in (4, 5)]
+        near(y[keep], want[keep], bound[keep] + 2.0 ** -8 * np.abs(want[keep]))
+        assert torch.isnan(y[5]).all()
+
+
+def test_in_pieces_captured_replayed_and_on_two_streams():
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(4)
+    E, L, Mi, T, k = 16, 768, 512, 100, 8
+    (g, _), (u, _), (o, _) = weights(r, E, Mi, L), weights(r, E, Mi, L), weights(r, E, L, Mi)
+    x, _ = rows(r, T, L, "bf16")
+    many, _ = rows(r, 1400, L, "bf16")
+    idx, w = cuda(*routed(r, T, k, E))
+    off = torch.linspace(0, 1400, E + 1, device="cuda").to(torch.int32)
+    assert in_pieces(E, 1400, Mi, L) and in_pieces(E, T * k, 3 * L, Mi)
+    run = lambda s=None: (Q.mxfp4_matvec(many, g, offsets=off, stream=s), Q.mxfp4_experts(x, idx, w, g, u, o, stream=s))  # noqa: E731
+    want = run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [run(s) for _ in range(5) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for pair in got for a, b in zip(pair, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    x.copy_(rows(r, T, L, "bf16")[0])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, run()))
+    x[3, 3] = float("inf")           # the replayed graph decides anew
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) for a, b in zip(captured, run()))
+    assert Q.qbmoe_status(None, None) == 0
