@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
     if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
     if (a.flags) {
+        pdl_wait();   // whoever waits for this kernel waits for those before it, too
         int any = 0;
         for (int i = threadIdx.x; i < a.n_flags; i += kThreads) any |= __ldcg(a.flags + i);
         if (!__syncthreads_or(any)) return;
@@ -742,7 +743,7 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + kCols - 1) / kCols) * ((a.N + rows - 1) / rows) * a.slabs;
         const int grid = (int)min(units, (long long)qbh::sm_count());
         const auto kern = k_stream<S::kBlocks, S::kTiles, S::kBoxes, kX, kMode>;
-        if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
+        if (kMode == kDown || a.flags) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
         kern<<<grid, kThreads, smem, s>>>(a);
         return qbh::cuda_err(cudaGetLastError());
     });

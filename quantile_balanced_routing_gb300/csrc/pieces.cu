@@ -9,9 +9,16 @@ constexpr int kSplitThreads = 256;
 // This lane's 8 elements of a block, as the four lanes of the block's quad have them, times 2^up.
 struct Block {
     float f[8];
+    uint32_t most;  // bits of the largest magnitude of this lane's
     int up;         // exponent of the block's own scale
     bool nan;       // whose scale is NaN
 };
+QB_DEV uint32_t largest(const float (&f)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+    return m;
+}
 template <int kX>
 QB_DEV Block block_of(const void* x, long long ldx, const uint8_t* x_scales, int K, long long row, int at) {
     Block b;
@@ -31,14 +38,20 @@ QB_DEV Block block_of(const void* x, long long ldx, const uint8_t* x_scales, int
             b.f[2 * j] = v.x;
             b.f[2 * j + 1] = v.y;
         }
+        b.most = largest(b.f);
         const int s = x_scales[row * (K >> 5) + (at >> 2)];
         b.nan = s == 255;
         b.up = s - 127;
     } else {
         const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + row * ldx + 8 * at);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b.f[2 * j] = __uint_as_float(w[j] << 16), b.f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int j = 0; j < 4; ++j) {
+            b.f[2 * j] = __uint_as_float(w[j] << 16), b.f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+        }
+        b.most = max(m << 16, m & 0xffff0000u);
     }
     return b;
 }
@@ -52,9 +65,7 @@ struct Pieces {
 // Whole warp.  special: the block has no such pieces (a NaN has: a scale of NaN).
 QB_DEV Pieces pieces_of(const Block& b, bool& special) {
     Pieces p;
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(b.f[j]) & 0x7fffffffu);
+    uint32_t m = b.most;
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     int e = max((int)(m >> 23) - 127, -100);                 // the largest is in [2^e, 2^(e + 1)), or tiny
@@ -64,21 +75,30 @@ QB_DEV Pieces pieces_of(const Block& b, bool& special) {
     special |= m == 0x7f800000u || (m != 0 && m < (27u << 23)) || (!bad && (base < 0 || base + 3 * (qbh::kPieces - 1) > 254));
     if (base < 0 || base + 3 * (qbh::kPieces - 1) > 254) bad = true;
     const float unit = __int_as_float((127 + 21 - e) << 23); // 2^(21 - e)
-    // digits from 0 to 7, 4 too many each: 4 (8^8 - 1) / 7 added to the whole number
-    uint32_t u[8];
+    // Digits from 0 to 7, 4 too many each: 4 (8^8 - 1) / 7 added to the whole number, which the sum with 1.5 2^23 has
+    // in its low bits.  An element's octal digits move to nibbles of their own, the byte selection turns four at
+    // once into codes (0xE, 0xD, 0xC, 0xA for -4 .. -1, then 0, 2, 4, 5), two elements' codes share bytes, and those of
+    // four pairs change places with the pieces.
+    uint32_t pair[4][2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = (uint32_t)((bad ? 0 : __float2int_rn(b.f[j] * unit)) + 9586980);
-    // a digit's code by the byte selection of four at once: 0xE, 0xD, 0xC, 0xA (-4 .. -1), 0, 2, 4, 5 (0 .. 3)
+    for (int j = 0; j < 8; ++j) {
+        uint32_t u = __float_as_uint(fmaf(bad ? 0.0f : b.f[j], unit, 12582912.0f)) - 0x4b400000u + 9586980u;
+        u += (u & 0xfff000u) * 15u;
+        u += (u & 0x0fc00fc0u) * 3u;
+        u += u & 0x38383838u;
+        const uint32_t lo = j & 1 ? 0xa0c0d0e0u : 0x0a0c0d0eu, hi = j & 1 ? 0x50402000u : 0x05040200u;
+        const uint32_t a = __byte_perm(lo, hi, u), c = __byte_perm(lo, hi, u >> 16);
+        pair[j >> 1][0] = j & 1 ? pair[j >> 1][0] | a : a;
+        pair[j >> 1][1] = j & 1 ? pair[j >> 1][1] | c : c;
+    }
 #pragma unroll
-    for (int i = 0; i < qbh::kPieces; ++i) {
-        uint32_t even = 0, odd = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int by = 4 * j - 3 * i;
-            even |= (by > 0 ? u[2 * j] << by : u[2 * j] >> -by) & (7u << 4 * j);
-            odd |= (by > 0 ? u[2 * j + 1] << by : u[2 * j + 1] >> -by) & (7u << 4 * j);
-        }
-        p.codes[i] = __byte_perm(0x0a0c0d0eu, 0x05040200u, even) | __byte_perm(0xa0c0d0e0u, 0x50402000u, odd);
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t a = __byte_perm(pair[0][h], pair[1][h], 0x5140), c = __byte_perm(pair[2][h], pair[3][h], 0x5140);
+        const uint32_t d = __byte_perm(pair[0][h], pair[1][h], 0x7362), f = __byte_perm(pair[2][h], pair[3][h], 0x7362);
+        p.codes[4 * h] = __byte_perm(a, c, 0x5410);
+        p.codes[4 * h + 1] = __byte_perm(a, c, 0x7632);
+        p.codes[4 * h + 2] = __byte_perm(d, f, 0x5410);
+        p.codes[4 * h + 3] = __byte_perm(d, f, 0x7632);
     }
     const int lane = threadIdx.x & 31;
     const uint32_t byte = (lane & 3) ? 0u : (uint32_t)(bad ? 255 : base) << (8 * (lane >> 2 & 3));
@@ -115,10 +135,9 @@ __global__ void __launch_bounds__(kSplitThreads) k_split_rows(const SplitArgs a)
     if (a.offsets)
         for (int e = blockIdx.x * kSplitThreads + threadIdx.x; e <= a.E; e += gridDim.x * kSplitThreads)
             a.piece_offsets[e] = min(max(a.offsets[e], 0), a.R) * qbh::kPieces;
-    const int lane = threadIdx.x & 31, warps = a.K >> 8;
-    const long long n = (long long)max(hi - lo, 0) * warps;
+    const uint32_t lane = threadIdx.x & 31, warps = a.K >> 8, n = max(hi - lo, 0) * warps;   // (at most 2^17)
     bool special = false;
-    for (long long i = (long long)blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); i < n; i += (long long)gridDim.x * (kSplitThreads / 32)) {
+    for (uint32_t i = blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); i < n; i += gridDim.x * (kSplitThreads / 32)) {
         const long long row = lo + i / warps;
         const int at = (int)(i % warps) * 32 + lane;
         store_pieces(pieces_of(block_of<kX>(a.x, a.ldx, a.x_scales, a.K, row, at), special), a.codes, a.scales, row, a.K, at);
@@ -178,9 +197,8 @@ struct GluArgs {
 };
 __global__ void __launch_bounds__(kSplitThreads) k_split_glu(const GluArgs a) {
     pdl_trigger();
-    const int rows = min(a.piece_offsets[a.E] / qbh::kPieces, a.R), lane = threadIdx.x & 31, warps = a.M >> 8;
-    for (long long i = (long long)blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); i < (long long)rows * warps;
-         i += (long long)gridDim.x * (kSplitThreads / 32)) {
+    const uint32_t rows = min(a.piece_offsets[a.E] / qbh::kPieces, a.R), lane = threadIdx.x & 31, warps = a.M >> 8;
+    for (uint32_t i = blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); i < rows * warps; i += gridDim.x * (kSplitThreads / 32)) {
         const long long row = i / warps;
         const int at = (int)(i % warps) * 32 + lane;
         const float4* g = reinterpret_cast<const float4*>(a.h + row * 2 * a.M) + 2 * at;
@@ -193,6 +211,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_split_glu(const GluArgs a) {
         b.f[2] = situ_glu(g0.z, u0.z, a.beta1, a.beta2); b.f[3] = situ_glu(g0.w, u0.w, a.beta1, a.beta2);
         b.f[4] = situ_glu(g1.x, u1.x, a.beta1, a.beta2); b.f[5] = situ_glu(g1.y, u1.y, a.beta1, a.beta2);
         b.f[6] = situ_glu(g1.z, u1.z, a.beta1, a.beta2); b.f[7] = situ_glu(g1.w, u1.w, a.beta1, a.beta2);
+        b.most = largest(b.f);
         bool special = false;   // finite, and what is below 2^-121 is as good as zero
         store_pieces(pieces_of(b, special), a.codes, a.scales, row, a.M, at);
     }
