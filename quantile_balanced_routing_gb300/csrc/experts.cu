@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs a
 // Scratch of an experts call: act; gate and up in slabs; the routes' rows.  In pieces: x's pieces where the rows
 // come later, gate and up where act would be, act's pieces, and what a split leaves.
 struct ExpertsScratch {
-    size_t act, parts, rows, act_pieces, offsets, row_map, flags, bytes;
+    size_t act, parts, rows, act_pieces, offsets, row_map, odd, bytes;
     bool pieces;
     ExpertsScratch(int T, int k, int L, int M) {
         pieces = qbh::pieces_ok(L) && qbh::pieces_ok(M) && slabs_of(L) == 1 && slabs_of(M) == 1;
@@ -117,8 +117,8 @@ struct ExpertsScratch {
             act_pieces = rows + max(qbh::align_up(R * L * 4, 256), qbh::piece_bytes(R, L));
             offsets = act_pieces + qbh::piece_bytes(R, M);
             row_map = offsets + qbh::align_up((QBMOE_MAX_EXPERTS + 1) * 4, 256);
-            flags = row_map + qbh::align_up(R * 4, 256);
-            bytes = flags + qbh::kPieceFlags * 4;
+            odd = row_map + qbh::align_up(R * 4, 256);
+            bytes = odd + R * qbh::kOddBytes;
             return;
         }
         const size_t R = (size_t)T * k, up = slabs_of(L), down = slabs_of(M);
@@ -169,42 +169,42 @@ extern "C" int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, 
     char* base = static_cast<char*>(workspace);
     float *act = reinterpret_cast<float*>(base + at.act), *parts = reinterpret_cast<float*>(base + at.parts), *rows = reinterpret_cast<float*>(base + at.rows);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    StreamArgs a{};
-    a.R = T * k; a.E = E; a.N = M; a.K = L;
-    a.x_type = x_type; a.x = x; a.ldx = ldx; a.x_scales = x_scales;
-    a.scales = gate_scales; a.scales2 = up_scales;
-    a.idx = idx; a.k = k;
-    a.y_type = QBMOE_F32; a.y = slabs_of(L) > 1 ? parts : act; a.ldy = M;
-    a.beta1 = beta1; a.beta2 = beta2;
+    const int R = T * k;
     int rc2 = 0;
-    if (at.pieces && qbh::pieces_pay(min(E, a.R), a.R, 3LL * L * M)) {
+    if (at.pieces && qbh::pieces_pay(min(E, R), R, 3LL * L * M)) {
         uint8_t *xp = reinterpret_cast<uint8_t*>(rows), *ap = reinterpret_cast<uint8_t*>(base + at.act_pieces);
         int32_t *offsets = reinterpret_cast<int32_t*>(base + at.offsets), *row_map = reinterpret_cast<int32_t*>(base + at.row_map);
-        int* flags = reinterpret_cast<int*>(base + at.flags);
-        rc2 = qbh::split_routes(T, k, E, L, x_type, x, ldx, x_scales, idx, xp, offsets, row_map, flags, &a.n_flags, s);
+        uint8_t* odd = reinterpret_cast<uint8_t*>(base + at.odd);
+        const qbh::PieceSource from{x_type, x, ldx, x_scales, row_map, k, odd};
+        if ((rc2 = qbh::split_routes(T, k, E, L, from, idx, xp, offsets, row_map, odd, s))) return rc2;
+        if ((rc2 = qbh::piece_product({R, E, M, L, xp, xp + qbh::piece_code_bytes(R, L), gate_codes, gate_scales, up_codes, up_scales,
+                                       offsets, nullptr, act, QBMOE_F32, 2LL * M, from}, s)))
+            return rc2;
+        if ((rc2 = qbh::split_glu(R, E, M, act, beta1, beta2, offsets, ap, s))) return rc2;
+        if ((rc2 = qbh::piece_product({R, E, L, M, ap, ap + qbh::piece_code_bytes(R, M), out_codes, out_scales, nullptr, nullptr,
+                                       offsets, row_map, rows, QBMOE_F32, L, {}}, s)))
+            return rc2;
+    } else {
+        StreamArgs a{};
+        a.R = R; a.E = E; a.N = M; a.K = L;
+        a.x_type = x_type; a.x = x; a.ldx = ldx; a.x_scales = x_scales;
+        a.scales = gate_scales; a.scales2 = up_scales;
+        a.idx = idx; a.k = k;
+        a.y_type = QBMOE_F32; a.y = slabs_of(L) > 1 ? parts : act; a.ldy = M;
+        a.beta1 = beta1; a.beta2 = beta2;
+        rc2 = x_type == QBMOE_BF16 ? ::stream<QBMOE_BF16, kGlu>(a, gate_codes, up_codes, s) : ::stream<QBMOE_MXFP8, kGlu>(a, gate_codes, up_codes, s);
         if (rc2) return rc2;
-        const qbh::PieceProduct up{a.R, E, M, L, xp, xp + qbh::piece_code_bytes(a.R, L), gate_codes, gate_scales, up_codes, up_scales,
-                                   offsets, nullptr, act, QBMOE_F32, 2LL * M};
-        if ((rc2 = qbh::piece_product(up, s))) return rc2;
-        if ((rc2 = qbh::split_glu(a.R, E, M, act, beta1, beta2, offsets, ap, s))) return rc2;
-        const qbh::PieceProduct down{a.R, E, L, M, ap, ap + qbh::piece_code_bytes(a.R, M), out_codes, out_scales, nullptr, nullptr,
-                                     offsets, row_map, rows, QBMOE_F32, L};
-        if ((rc2 = qbh::piece_product(down, s))) return rc2;
-        a.flags = flags;
+        if (slabs_of(L) > 1) {
+            const long long blocks = ((long long)R * M + 255) / 256;
+            k_glu_sum<<<(unsigned)min(blocks, 8LL * qbh::sm_count()), 256, 0, s>>>(slabs_of(L), R, M, E, idx, parts, beta1, beta2, act);
+            if ((rc2 = qbh::cuda_err(cudaGetLastError()))) return rc2;
+        }
+        a.N = L; a.K = M;
+        a.x_type = QBMOE_F32; a.x = act; a.ldx = M; a.x_scales = nullptr;
+        a.scales = out_scales; a.scales2 = nullptr;
+        a.y = rows; a.ldy = L;
+        if ((rc2 = ::stream<QBMOE_F32, kDown>(a, out_codes, nullptr, s))) return rc2;
     }
-    rc2 = x_type == QBMOE_BF16 ? ::stream<QBMOE_BF16, kGlu>(a, gate_codes, up_codes, s) : ::stream<QBMOE_MXFP8, kGlu>(a, gate_codes, up_codes, s);
-    if (rc2) return rc2;
-    if (slabs_of(L) > 1) {
-        const long long blocks = ((long long)a.R * M + 255) / 256;
-        k_glu_sum<<<(unsigned)min(blocks, 8LL * qbh::sm_count()), 256, 0, s>>>(slabs_of(L), a.R, M, E, idx, parts, beta1, beta2, act);
-        if ((rc2 = qbh::cuda_err(cudaGetLastError()))) return rc2;
-    }
-    StreamArgs d = a;
-    d.N = L; d.K = M;
-    d.x_type = QBMOE_F32; d.x = act; d.ldx = M; d.x_scales = nullptr;
-    d.scales = out_scales; d.scales2 = nullptr;
-    d.y = rows; d.ldy = L;
-    if ((rc2 = ::stream<QBMOE_F32, kDown>(d, out_codes, nullptr, s))) return rc2;
     const CombineArgs c{T, k, E, L, slabs_of(M), idx, w, rows, gamma, rms_eps, static_cast<__nv_bfloat16*>(y), ldy};
     return qbh::launch_pdl(k_combine, dim3(T), dim3(kCombineThreads), 0, s, c);
 }

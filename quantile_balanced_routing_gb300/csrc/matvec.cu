@@ -21,18 +21,18 @@ __global__ void __launch_bounds__(256) k_slab_sum(int slabs, int R, int N, int E
     }
 }
 
-// Scratch of a call: parts of the slabs; or the rows' pieces, their offsets and flags.
+// Scratch of a call: parts of the slabs; or the rows' pieces, their offsets and odd bytes.
 constexpr long long kMostPieces = 1LL << 25;   // elements of x that are split: 143 MB of pieces
 struct MatvecScratch {
-    size_t parts = 0, offsets = 0, flags = 0, bytes = 0;
+    size_t parts = 0, offsets = 0, odd = 0, bytes = 0;
     bool pieces;
     MatvecScratch(int R, int N, int K) {
         pieces = qbh::pieces_ok(K) && slabs_of(K) == 1 && (long long)R * K <= kMostPieces &&
                  qbh::pieces_pay(min(R, QBMOE_MAX_EXPERTS), R, (long long)N * K);   // for some E
         if (pieces) {
             offsets = qbh::piece_bytes(R, K);
-            flags = offsets + qbh::align_up((QBMOE_MAX_EXPERTS + 1) * 4, 256);
-            bytes = flags + qbh::kPieceFlags * 4;
+            odd = offsets + qbh::align_up((QBMOE_MAX_EXPERTS + 1) * 4, 256);
+            bytes = odd + (size_t)R * qbh::kOddBytes;
         } else if (slabs_of(K) > 1) {
             bytes = (size_t)slabs_of(K) * R * N * 4;
         }
@@ -73,6 +73,15 @@ extern "C" int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const vo
     const int rc = qbh::device_init();
     if (rc) return rc;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (at.pieces && qbh::pieces_pay(min(E, R), R, (long long)N * K)) {
+        uint8_t* pieces = static_cast<uint8_t*>(workspace);
+        int32_t* piece_offsets = reinterpret_cast<int32_t*>(pieces + at.offsets);
+        const qbh::PieceSource from{x_type, x, ldx, x_scales, nullptr, 1, pieces + at.odd};
+        const int rc2 = qbh::split_rows(R, E, K, from, offsets, pieces, piece_offsets, pieces + at.odd, s);
+        if (rc2) return rc2;
+        return qbh::piece_product({R, E, N, K, pieces, pieces + qbh::piece_code_bytes(R, K), w_codes, w_scales, nullptr, nullptr,
+                                   offsets ? piece_offsets : nullptr, nullptr, y, y_type, ldy, from}, s);
+    }
     StreamArgs a{};
     a.R = R; a.E = E; a.N = N; a.K = K;
     a.x_type = x_type; a.x = x; a.ldx = ldx; a.x_scales = x_scales;
@@ -81,17 +90,6 @@ extern "C" int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const vo
     a.y_type = slabs ? QBMOE_F32 : y_type;
     a.y = slabs ? workspace : y;
     a.ldy = slabs ? N : ldy;
-    if (at.pieces && qbh::pieces_pay(min(E, R), R, (long long)N * K)) {
-        uint8_t* pieces = static_cast<uint8_t*>(workspace);
-        int32_t* piece_offsets = reinterpret_cast<int32_t*>(pieces + at.offsets);
-        int* flags = reinterpret_cast<int*>(pieces + at.flags);
-        int rc2 = qbh::split_rows(R, E, K, x_type, x, ldx, x_scales, offsets, pieces, piece_offsets, flags, &a.n_flags, s);
-        if (rc2) return rc2;
-        const qbh::PieceProduct p{R, E, N, K, pieces, pieces + qbh::piece_code_bytes(R, K), w_codes, w_scales, nullptr, nullptr,
-                                  offsets ? piece_offsets : nullptr, nullptr, y, y_type, ldy};
-        if ((rc2 = qbh::piece_product(p, s))) return rc2;
-        a.flags = flags;
-    }
     const int rc2 = x_type == QBMOE_BF16 ? ::stream<QBMOE_BF16, kStore>(a, w_codes, nullptr, s) : ::stream<QBMOE_MXFP8, kStore>(a, w_codes, nullptr, s);
     if (rc2 || !slabs) return rc2;
     const long long blocks = ((long long)R * N + 255) / 256;

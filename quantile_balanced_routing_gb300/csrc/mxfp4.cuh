@@ -88,7 +88,7 @@ QB_DEV void load_groups(const Groups& g, const int32_t* offsets, int E, int R, i
     constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e <= E; e += kThreads)
-        g.seg[e] = offsets ? min(max(__ldg(offsets + e), 0), R) : (e ? R : 0);
+        g.seg[e] = offsets ? min(max(__ldcg(offsets + e), 0), R) : (e ? R : 0);
     __syncthreads();
     // each warp scans a run of experts, then adds what the warps before it counted
     const int per = ((E + kWarps - 1) / kWarps + 31) & ~31;

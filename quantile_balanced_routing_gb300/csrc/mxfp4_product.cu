@@ -46,13 +46,16 @@
 // loads a row and group.  16384 rows over 56 experts of 1024 x K: K = 3584 (TMA) 53 us,
 // 3328 (8-byte loads) 65, 3456 (4-byte) 71, 3360 (1-byte) 378; one row by 6144 x K: 15.5,
 // 15.5, 15.5 and 35 us.  The last is bound by those loads alone.
+// Rows in pieces (pieces.cuh) take the same kernel with another epilogue and, for gate and up, a second tensor of weights.
 // Every mbarrier wait is bounded: on expiry the kernel counts it
 // (mx_expiries), stops, lets its own copies and MMAs finish and frees TMEM.
 #include "mxfp4.cuh"
+#include "mxfp4_decode.cuh"
 #include "pieces.cuh"
 #include "tc_ptx.cuh"
 
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 
 #include <mutex>
 
@@ -91,6 +94,8 @@ struct Params {
     const int32_t* row_map;                  // or NULL: where rows of y lie
     void* sums;                              // y, of sums_type
     int sums_type;
+    qbh::PieceSource x;
+    const uint8_t *a_codes, *a2_codes;
 };
 // The weights that a tile takes, and its first row in them.
 struct TileRows {
@@ -167,6 +172,34 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+    return __low2float(*reinterpret_cast<const __half2*>(&h));
+}
+// The product of row r of a piece product with weight row `row`, from x itself: for the rows that have no pieces.
+__device__ __noinline__ float plain_product(const Params& p, int r, long long row, bool second) {
+    const int K = p.K, blocks = K >> 5;
+    const long long from = p.x.map ? __ldcg(p.x.map + r) / p.x.div : r;
+    const uint8_t* codes = (second ? p.a2_codes : p.a_codes) + row * (K >> 1);
+    const uint8_t* scales = (second ? p.a2_sc : p.a_sc) + row * blocks;
+    float sum = 0.0f;
+    for (int b = 0; b < blocks; ++b) {
+        const uint4 c4 = __ldg(reinterpret_cast<const uint4*>(codes) + b);
+        const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+        float s = 0.0f;
+        for (int j = 0; j < 32; ++j) {
+            const long long at = from * p.x.ldx + 32 * b + j;
+            const float x = p.x.x_type == QBMOE_MXFP8 ? e4m3_value(static_cast<const uint8_t*>(p.x.x)[at])
+                                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p.x.x)[at]);
+            s = fmaf(x, e2m1_value(c[j >> 3] >> (4 * (j & 7)) & 15), s);
+        }
+        if (p.x.x_type == QBMOE_MXFP8) s *= e8m0_value(p.x.x_scales[from * blocks + b]);
+        sum = fmaf(s, e8m0_value(scales[b]), sum);
+    }
+    return sum;
 }
 
 // kPieced: every eight columns are the pieces of one row of x, and are added, the smallest first.
@@ -486,10 +519,25 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
         int ab = 0;
         uint32_t fph = 0;
         for (int t = first; t < n_tiles; t += step) {
-            const int nrows = w.nrows, odd = lane & 1;
+            const int nrows = w.nrows, right = lane & 1;
             const TileRows of = kPieced ? tile_rows(p, w.m) : TileRows{false, w.m};
             const int f = of.m * 128 + 32 * q + (kPieced ? lane : lane & ~1), row0 = w.row0 / qbh::kPieces;
-            __nv_bfloat16* out = p.y + (long long)(w.row0 + odd) * p.ldy + f;
+            __nv_bfloat16* out = p.y + (long long)(w.row0 + right) * p.ldy + f;
+            uint32_t odd = 0;        // the tile's rows without pieces
+            int place = row0 + lane; // where this lane's row goes: read before the wait
+            if constexpr (kPieced) {
+                static_assert(BN <= 32 * qbh::kPieces, "a lane a row");
+                if (lane * qbh::kPieces < nrows) {
+                    if (p.x.odd) {
+                        const uint4* o = reinterpret_cast<const uint4*>(p.x.odd + (long long)(row0 + lane) * qbh::kOddBytes);
+                        const uint4 u = __ldcg(o), v = __ldcg(o + 1);
+                        odd = u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w;
+                    }
+                    if (p.row_map) place = __ldcg(p.row_map + row0 + lane);
+                }
+                odd = __ballot_sync(0xffffffffu, odd != 0);
+            }
+            const long long wrow = (long long)w.g * p.N + f;
             w.next(gr, p.E, p.m_total);
             if (warp == kEpiWarp && lane == 0) {   // one poller; an expiry leaves undefined outputs and a status
                 if (!dead && *abort_flag) dead = true;
@@ -504,23 +552,24 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
                 if constexpr (kPieced) {
 #pragma unroll
                     for (int i = 0; i < 16; i += qbh::kPieces) {
-                        if (f >= p.N || c0 + i >= nrows) break;
+                        const int j0 = (c0 + i) / qbh::kPieces, to = __shfl_sync(0xffffffffu, place, j0);
+                        if (f >= p.N || c0 + i >= nrows) continue;
                         float sum = v[i];
 #pragma unroll
                         for (int j = 1; j < qbh::kPieces; ++j) sum += v[i + j];
-                        const int r = row0 + (c0 + i) / qbh::kPieces;
-                        const long long at = (p.row_map ? __ldg(p.row_map + r) : r) * p.ldy + f + (of.second ? p.N : 0);
+                        if (odd >> j0 & 1) sum = plain_product(p, row0 + j0, wrow, of.second);
+                        const long long at = to * p.ldy + f + (of.second ? p.N : 0);
                         if (p.sums_type == QBMOE_F32) static_cast<float*>(p.sums)[at] = sum;
                         else static_cast<__nv_bfloat16*>(p.sums)[at] = __float2bfloat16_rn(sum);
                     }
                     continue;
                 }
                 __nv_bfloat16* o = out + (long long)c0 * p.ldy;
-                const int left = f < p.N ? nrows - c0 - odd : 0;
+                const int left = f < p.N ? nrows - c0 - right : 0;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                    const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
+                    const float got = __shfl_xor_sync(0xffffffffu, right ? v[i] : v[i + 1], 1);
+                    const __nv_bfloat162 h = right ? __floats2bfloat162_rn(got, v[i + 1]) : __floats2bfloat162_rn(v[i], got);
                     if (i < left) *reinterpret_cast<__nv_bfloat162*>(o + (uint32_t)i * (uint32_t)p.ldy) = h;
                 }
             }
@@ -707,6 +756,9 @@ int piece_product(const PieceProduct& q, cudaStream_t s) {
         p.m_total *= 2;
     }
     p.row_map = q.row_map;
+    p.x = q.x;
+    p.a_codes = q.w_codes;
+    p.a2_codes = q.w2_codes;
     p.sums = q.y;
     p.sums_type = q.y_type;
     const int avg = (m.R + q.E - 1) / q.E;

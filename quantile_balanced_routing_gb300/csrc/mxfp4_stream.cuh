@@ -1,23 +1,27 @@
-// MXFP4 weights streamed past a few rows: what moe_mxfp4_matvec and moe_mxfp4_experts share.
+// MXFP4 weights streamed past a few rows: what moe_mxfp4_matvec and moe_mxfp4_experts share for small calls
+// and for depths that pieces.cuh does not take.
 //
 // One kernel brings weights through shared memory and multiplies them with a few rows that
 // stay in registers.  A persistent CTA a SM takes a contiguous run of units; a unit is kMT
-// tiles of 16 weight rows over the whole depth (or one slab of it).  Sixteen consumer warps
-// (four a scheduler hide the chain of load, conversion, product and sum; eight with 168
-// registers took half as long again) form groups that take units in turn, so that one group's
-// fixed work per unit falls into another's products.  The warps of a group divide the depth: a
+// tiles of 16 weight rows over the whole depth (or one slab of it).  Eight consumer warps of 168 registers
+// form groups that take units in turn, so that one group's fixed work per unit falls into another's products
+// (sixteen warps of 96 registers, one tile a unit: 413 against 408 us by 896 experts of 1024 x 3584, and 4096 rows'
+// whole experts 1524 against 1370; twelve warps 430 and 1862).  The warps of a group divide the depth: a
 // warp owns a run of kNB blocks of 32 of K, for which it holds the rows' elements as mma B
 // operands, so that the rows cost no bandwidth while weights go by.  Per block of 32 and tile:
 //   - ldmatrix hands each quad of lanes the 16 bytes of a weight row's block;
 //   - codes become fp16 (exact) two at a time, with one conversion;
 //   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
 //   - the block's dot products, times the two scales, are added in fp32.
-// Two producer warps, a unit each in turn, bring its codes (long rows one by one, short ones
+// Two producer warps, a stage each in turn, bring codes (long rows one by one, short ones
 // in TMA boxes: a copy costs 20 to 80 cycles to issue) and scales several units ahead; two more
 // add the consumers' shares of the depth, in order, and store.
 // Weight rows are the M operand of the small mma because a column costs nothing that way: up
-// to 8 rows of x take as long as one.  tcgen05 would need its operands decoded in shared
-// memory, or x as E4M3 pairs (the layer's way: bound by issue at few columns).
+// to 8 rows of x take as long as one.
+//
+// Measured (cold caches): one row by 6144 x 7168 23 us with the launch (the weights alone take 3.5), by
+// 12288 x 7168 29.  A large call spends 74 cycles a scheduler on a block and tile (the products' own
+// instructions take 35, HBM 46): waits, sums and scales of each unit; pieces.cuh has those.
 #pragma once
 
 #include "mxfp4.cuh"
@@ -71,8 +75,6 @@ struct StreamArgs {
     int* expiries;
     long long wait_limit;
     int stall;
-    const int* flags;            // NULL, or: nothing to do unless one of n_flags is set
-    int n_flags;
 };
 
 // kNB blocks of 32 a warp, kMT tiles a unit; weights come in boxes, a whole number a warp, or row by row.
@@ -434,12 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long lim = a.wait_limit > 0 ? a.wait_limit : kDefaultWait;
     if (kRoutes) pdl_trigger();   // the next kernel may set itself up meanwhile
-    if (a.flags) {
-        pdl_wait();   // whoever waits for this kernel waits for those before it, too
-        int any = 0;
-        for (int i = threadIdx.x; i < a.n_flags; i += kThreads) any |= __ldcg(a.flags + i);
-        if (!__syncthreads_or(any)) return;
-    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             tc::mbar_init(full + s, 1);
@@ -743,7 +739,7 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + kCols - 1) / kCols) * ((a.N + rows - 1) / rows) * a.slabs;
         const int grid = (int)min(units, (long long)qbh::sm_count());
         const auto kern = k_stream<S::kBlocks, S::kTiles, S::kBoxes, kX, kMode>;
-        if (kMode == kDown || a.flags) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
+        if (kMode == kDown) return qbh::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
         kern<<<grid, kThreads, smem, s>>>(a);
         return qbh::cuda_err(cudaGetLastError());
     });

@@ -124,8 +124,13 @@ struct SplitArgs {
     const int32_t* idx;         // split_routes
     uint8_t *codes, *scales;
     int32_t *piece_offsets, *row_map;
-    int* flags;
+    uint8_t* odd;
 };
+// Whole warp: the odd byte of its 256 elements; the first's warp clears what is behind the row's last.
+QB_DEV void store_odd(uint8_t* odd, long long row, int chunk, int chunks, bool any) {
+    const int lane = threadIdx.x & 31;
+    if (lane == chunk || (chunk == 0 && lane >= chunks)) odd[row * qbh::kOddBytes + lane] = lane == chunk && any;
+}
 
 // A warp 256 elements of a row.
 template <int kX>
@@ -136,14 +141,13 @@ __global__ void __launch_bounds__(kSplitThreads) k_split_rows(const SplitArgs a)
         for (int e = blockIdx.x * kSplitThreads + threadIdx.x; e <= a.E; e += gridDim.x * kSplitThreads)
             a.piece_offsets[e] = min(max(a.offsets[e], 0), a.R) * qbh::kPieces;
     const uint32_t lane = threadIdx.x & 31, warps = a.K >> 8, n = max(hi - lo, 0) * warps;   // (at most 2^17)
-    bool special = false;
     for (uint32_t i = blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); i < n; i += gridDim.x * (kSplitThreads / 32)) {
         const long long row = lo + i / warps;
-        const int at = (int)(i % warps) * 32 + lane;
+        const int chunk = i % warps, at = chunk * 32 + lane;
+        bool special = false;
         store_pieces(pieces_of(block_of<kX>(a.x, a.ldx, a.x_scales, a.K, row, at), special), a.codes, a.scales, row, a.K, at);
+        store_odd(a.odd, row, chunk, warps, __any_sync(0xffffffffu, special));
     }
-    special = __syncthreads_or(special);
-    if (threadIdx.x == 0) a.flags[blockIdx.x] = special;
 }
 
 // The same for tokens: a token's pieces go to each of its routes' places in expert order.
@@ -171,21 +175,18 @@ __global__ void __launch_bounds__(kThreads) k_split_routes(const SplitArgs a) {
     }
     __syncthreads();
     const int lane = threadIdx.x & 31, warps = a.K >> 8, T = a.R / a.k;
-    bool special = false;
     for (int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < T * warps; i += gridDim.x * (kThreads / 32)) {
-        const int t = i / warps, at = (i % warps) * 32 + lane;
-        bool odd = false, any = false;
-        const Pieces p = pieces_of(block_of<kX>(a.x, a.ldx, a.x_scales, a.K, t, at), odd);
+        const int t = i / warps, chunk = i % warps, at = chunk * 32 + lane;
+        bool special = false;
+        const Pieces p = pieces_of(block_of<kX>(a.x, a.ldx, a.x_scales, a.K, t, at), special);
+        special = __any_sync(0xffffffffu, special);
         for (int j = 0; j < a.k; ++j) {
             const int to = place[t * a.k + j];
             if (to == 0xffff) continue;
             store_pieces(p, a.codes, a.scales, to, a.K, at);
-            any = true;
+            store_odd(a.odd, to, chunk, warps, special);
         }
-        special |= odd && any;
     }
-    special = __syncthreads_or(special);
-    if (threadIdx.x == 0) a.flags[blockIdx.x] = special;
 }
 
 struct GluArgs {
@@ -221,28 +222,28 @@ constexpr int kRoutesSmem = (2 * (QBMOE_MAX_EXPERTS + 1) + 8 * QBMOE_MAX_EXPERTS
 
 int grid_of(long long warps_total, int warps_cta, int per_sm) {
     const long long ctas = (warps_total + warps_cta - 1) / warps_cta, most = (long long)per_sm * qbh::sm_count();
-    return (int)max(1LL, min(min(ctas, most), (long long)qbh::kPieceFlags));
+    return (int)max(1LL, min(ctas, most));
 }
 
 }  // namespace
 
 namespace qbh {
 
-int split_rows(int R, int E, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales, const int32_t* offsets,
-               uint8_t* pieces, int32_t* piece_offsets, int* flags, int* n_flags, cudaStream_t s) {
-    const SplitArgs a{R, E, K, 1, x, ldx, x_scales, offsets, nullptr, pieces, pieces + piece_code_bytes(R, K), piece_offsets, nullptr, flags};
-    *n_flags = grid_of((long long)R * (K / 256), kSplitThreads / 32, 6);
-    if (x_type == QBMOE_MXFP8) k_split_rows<QBMOE_MXFP8><<<*n_flags, kSplitThreads, 0, s>>>(a);
-    else k_split_rows<QBMOE_BF16><<<*n_flags, kSplitThreads, 0, s>>>(a);
+int split_rows(int R, int E, int K, const PieceSource& x, const int32_t* offsets, uint8_t* pieces, int32_t* piece_offsets,
+               uint8_t* odd, cudaStream_t s) {
+    const SplitArgs a{R, E, K, 1, x.x, x.ldx, x.x_scales, offsets, nullptr, pieces, pieces + piece_code_bytes(R, K), piece_offsets, nullptr, odd};
+    const int grid = grid_of((long long)R * (K / 256), kSplitThreads / 32, 6);
+    if (x.x_type == QBMOE_MXFP8) k_split_rows<QBMOE_MXFP8><<<grid, kSplitThreads, 0, s>>>(a);
+    else k_split_rows<QBMOE_BF16><<<grid, kSplitThreads, 0, s>>>(a);
     return cuda_err(cudaGetLastError());
 }
 
-int split_routes(int T, int k, int E, int K, int x_type, const void* x, long long ldx, const uint8_t* x_scales, const int32_t* idx,
-                 uint8_t* pieces, int32_t* piece_offsets, int32_t* row_map, int* flags, int* n_flags, cudaStream_t s) {
-    const SplitArgs a{T * k, E, K, k, x, ldx, x_scales, nullptr, idx, pieces, pieces + piece_code_bytes((long long)T * k, K), piece_offsets, row_map, flags};
-    *n_flags = grid_of((long long)T * (K / 256), kThreads / 32, 2);
-    if (x_type == QBMOE_MXFP8) k_split_routes<QBMOE_MXFP8><<<*n_flags, kThreads, kRoutesSmem, s>>>(a);
-    else k_split_routes<QBMOE_BF16><<<*n_flags, kThreads, kRoutesSmem, s>>>(a);
+int split_routes(int T, int k, int E, int K, const PieceSource& x, const int32_t* idx, uint8_t* pieces, int32_t* piece_offsets,
+                 int32_t* row_map, uint8_t* odd, cudaStream_t s) {
+    const SplitArgs a{T * k, E, K, k, x.x, x.ldx, x.x_scales, nullptr, idx, pieces, pieces + piece_code_bytes((long long)T * k, K), piece_offsets, row_map, odd};
+    const int grid = grid_of((long long)T * (K / 256), kThreads / 32, 2);
+    if (x.x_type == QBMOE_MXFP8) k_split_routes<QBMOE_MXFP8><<<grid, kThreads, kRoutesSmem, s>>>(a);
+    else k_split_routes<QBMOE_BF16><<<grid, kThreads, kRoutesSmem, s>>>(a);
     return cuda_err(cudaGetLastError());
 }
 
