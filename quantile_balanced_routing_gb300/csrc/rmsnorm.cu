@@ -10,6 +10,10 @@
 // Many rows go through k_add_rmsnorm_rows and k_add_rmsnorm_backward_rows: persistent CTAs whose
 // next rows come to shared memory by asynchronous copies meanwhile, so that HBM does not wait for a row's
 // reduction.  Few rows, short rows and rows off 16-byte boundaries go through the kernels without a ring.
+//
+// Measured, 16384 x 7168 bf16 with residual: forward to MXFP8 and its values 173 us (6.1 TB/s, 90% of the copy rate; 238
+// without the ring), backward with dtotal 158 us (5.9 TB/s; 331, and 189 with the gain read from global memory).
+// HBM bounds both.  Rows of odd widths are read an element at a time: 16384 x 2021, 176 and 260 us for a floor of 39.
 #include "mxfp4.cuh"
 
 #include <cuda_fp16.h>
@@ -25,6 +29,8 @@ constexpr int kNormItems = 4;            // pieces of 8 elements a thread holds
 constexpr int kNormThreads = 512;        // most threads of a row
 constexpr int kRowWarps = 8;             // rows of a CTA when a warp holds a row
 constexpr int kGainParts = 608;          // most partial sums of the gain's gradient
+constexpr int kRingParts = 1520;         // with rows in a ring
+constexpr int kRingRow = 512;            // shortest row of a ring
 
 // 8 elements of a row from element 8 i on, zeros past its end.
 template <typename T, bool kVec>
@@ -490,10 +496,17 @@ int gain_parts(int T, int H) {
     return (int)(ctas < kGainParts ? ctas : kGainParts);
 }
 
-// Whether the rows go through a ring, and its shape: two CTAs a SM up to rows of 8192, one beyond,
-// with two rows at least (and the gain, where it is read twice a row) in their shared memory, and
-// rows enough for several a CTA.
-constexpr int kRingBytes = 112 * 1024;
+// Whether the rows go through a ring, and its shape: up to rows of 8192 as many CTAs a SM as 64 registers a thread
+// and `least` rows (and the gain, where it is read twice a row) each in shared memory allow, one beyond.  Measured in us with
+// a ring and without, forward and backward, bf16 (floor: bytes at the copy rate):
+//   310 x 7168 (3)      10, 12    18, 27        65536 x 2048 (158)  170, 203   182, 379
+//   1000 x 7168 (8)     16, 23    25, 39        65536 x 1056 (81)   100, 139   137, 309
+//   8192 x 7168 (69)    80, 111   88, 135       65536 x 1024 (79)    94, 111   100, 129
+//   8192 x 3584 (35)    43, 57    55, 74        131072 x 512 (79)   115, 125   119, 139
+// and not better for 200000 x 256 (94, 125; 129, 121), nor for fp32 alone (8192 x 4096: 88, 86; 96, 88), whose 16-byte reads
+// meet in shared memory's banks, nor with two rows forward (fp32, 8192 x 7168: 154, 143).
+constexpr int kRingBytes = 224 * 1024;     // a SM's
+constexpr int kRingCta = 112 * 1024;
 constexpr int kWide = 8192;
 struct RingShape {
     Ring ring;
@@ -501,17 +514,21 @@ struct RingShape {
     int grid, threads;
     size_t smem;
 };
-RingShape ring_of(int T, int H, int bytes, int gain_bytes, bool vec) {
-    const int per_sm = H > kWide ? 1 : 2, items = H > kWide ? 4 : 2;
+RingShape ring_of(int T, int H, int bytes, int gain_bytes, int least, bool able) {
+    const int items = H > kWide ? 4 : 2;
     RingShape r{};
+    r.threads = ((H + 8 * items - 1) / (8 * items) + 31) & ~31;
+    int per_sm = H > kWide ? 1 : max(2, 1024 / r.threads);
     r.ring.bytes = bytes;
-    r.ring.stages = (kRingBytes * (2 / per_sm) - gain_bytes) / bytes;
+    for (;; --per_sm) {
+        r.ring.stages = (kRingBytes / per_sm - (per_sm > 2 ? 1280 : 0) - gain_bytes) / bytes;   // (a CTA's own KB, and its sums)
+        if (r.ring.stages >= least || per_sm <= 2) break;
+    }
     if (r.ring.stages > kRingStages) r.ring.stages = kRingStages;
     r.grid = per_sm * qbh::sm_count();
-    if (r.grid > kGainParts) r.grid = kGainParts;
-    r.threads = ((H + 8 * items - 1) / (8 * items) + 31) & ~31;
+    if (r.grid > kRingParts) r.grid = kRingParts;
     r.smem = gain_bytes + (size_t)r.ring.stages * bytes;
-    r.use = vec && H > 1024 && T >= 4 * r.grid && r.ring.stages >= 2;
+    r.use = able && H >= kRingRow && T >= r.grid && r.ring.stages >= least;
     return r;
 }
 
@@ -537,12 +554,12 @@ int rmsnorm_init() {
         with_types(i & 1 ? QBMOE_BF16 : QBMOE_F32, i & 2 ? QBMOE_BF16 : QBMOE_F32, [&](auto first, auto second) {
             using A = decltype(first);
             using B = decltype(second);
-            rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 2>, kRingBytes);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 2>, kRingBytes);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 4>, 2 * kRingBytes);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 4>, 2 * kRingBytes);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 2>, kRingBytes);
-            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 4>, 2 * kRingBytes);
+            rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 2>, kRingCta);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 2>, kRingCta);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, false, 4>, kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_rows<A, B, true, 4>, kRingBytes);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 2>, kRingCta);
+            if (!rc) rc = allow_ring(k_add_rmsnorm_backward_rows<A, B, 4>, kRingBytes);
         });
     return rc;
 }
@@ -569,7 +586,7 @@ extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long lon
     const NormArgs a{T, H, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, codes, scales};
     const dim3 block = row_block(H);
     const unsigned grid = (unsigned)(((long long)T + block.y - 1) / block.y);
-    const RingShape rows = ring_of(T, H, H * (size_of(x_type) + (residual ? size_of(res_type) : 0)), 0, vec);
+    const RingShape rows = ring_of(T, H, H * (size_of(x_type) + (residual ? size_of(res_type) : 0)), 0, 3, vec && (x_type == QBMOE_BF16 || (residual && res_type == QBMOE_BF16)));
     with_types(x_type, residual ? res_type : x_type, [&](auto tx, auto tr) {
         using TX = decltype(tx);
         using TR = decltype(tr);
@@ -589,7 +606,7 @@ extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long lon
 }
 
 extern "C" size_t qbmoe_add_rmsnorm_workspace_bytes(int T, int H) {
-    return sizes_ok(T, H, 0.0f) ? (size_t)gain_parts(T, H) * H * 4 : 0;
+    return sizes_ok(T, H, 0.0f) ? (size_t)min(T, kRingParts) * H * 4 : 0;   // (gain_parts, or a ring's grid, at most)
 }
 
 extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long long lddn, int total_type,
@@ -616,7 +633,7 @@ extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* d
     float* parts = dgamma ? static_cast<float*>(workspace) : nullptr;
     const NormGradArgs a{T, H, dn, lddn, total, ldt, gamma, eps, dtotal, lddt, dx, lddx, parts};
     const dim3 block = row_block(H);
-    const RingShape rows = ring_of(T, H, H * (size_of(dn_type) + size_of(total_type) * (dtotal ? 2 : 1)), H * 4, vec);
+    const RingShape rows = ring_of(T, H, H * (size_of(dn_type) + size_of(total_type) * (dtotal ? 2 : 1)), H * 4, 2, vec && (dn_type == QBMOE_BF16 || total_type == QBMOE_BF16));
     const int grid = rows.use ? rows.grid : gain_parts(T, H);
     const size_t smem = block.y > 1 ? (size_t)kRowWarps * H * 4 : 0;
     with_types(dn_type, total_type, [&](auto td, auto tt) {

@@ -212,7 +212,8 @@ def test_many_short_rows():
 
 
 @pytest.mark.parametrize("x,res", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.float32)])
-@pytest.mark.parametrize("T,H", [(1216, 1032), (1217, 3584), (2500, 1056), (609, 8200), (1531, 8192), (610, 16384)])
+@pytest.mark.parametrize("T,H", [(1216, 1032), (1217, 3584), (2500, 1056), (609, 8200), (1531, 8192), (610, 16384),
+                                 (1531, 512), (1700, 1032), (3001, 640), (1521, 2048)])
 def test_many_rows(T, H, x, res):
     """Rows enough that each CTA takes several in turn."""
     import quantile_balanced_routing_gb300 as Q
