@@ -3,9 +3,9 @@
 // in MXFP8, and the gradients.
 //
 // A row is held in registers between its sum of squares and its outputs, so that each
-// input is read once and each output written once.  A thread's pieces are 8 consecutive
-// elements, kNormItems of them a block's width apart; four neighbouring threads hold a
-// block of 32, whose largest magnitude is two shuffles away.
+// input is read once and each output written once.  A thread's pieces are 8
+// elements (consecutive where rows are vectors), kNormItems of them a block's width apart; four neighbouring threads
+// hold a block of 32, whose largest magnitude is two shuffles away.
 //
 // Many rows go through k_add_rmsnorm_rows and k_add_rmsnorm_backward_rows: persistent CTAs whose
 // next rows come to shared memory by asynchronous copies meanwhile, so that HBM does not wait for a row's
@@ -13,7 +13,8 @@
 //
 // Measured, 16384 x 7168 bf16 with residual: forward to MXFP8 and its values 173 us (6.1 TB/s, 90% of the copy rate; 238
 // without the ring), backward with dtotal 158 us (5.9 TB/s; 331, and 189 with the gain read from global memory).
-// HBM bounds both.  Rows of odd widths are read an element at a time: 16384 x 2021, 176 and 260 us for a floor of 39.
+// HBM bounds both.  Rows of odd widths are read an element at a time and bound by issue: 16384 x 2021 bf16, 141 and
+// 176 us for a floor of 39.
 #include "mxfp4.cuh"
 
 #include <cuda_fp16.h>
@@ -28,32 +29,41 @@ using namespace qb;
 constexpr int kNormItems = 4;            // pieces of 8 elements a thread holds
 constexpr int kNormThreads = 512;        // most threads of a row
 constexpr int kRowWarps = 8;             // rows of a CTA when a warp holds a row
-constexpr int kGainParts = 608;          // most partial sums of the gain's gradient
+constexpr int kGainParts = 608;          // most partial sums of the gain's gradient (twice as many CTAs of 64 threads:
+                                         // 16384 x 2021 bf16, 176 us, 289 with 608)
 constexpr int kRingParts = 1520;         // with rows in a ring
 constexpr int kRingRow = 512;            // shortest row of a ring
 
-// 8 elements of a row from element 8 i on, zeros past its end.
-template <typename T, bool kVec>
+// How a piece of 8 elements lies in its row: together, read at once or one by one; or 32 elements apart, a warp's
+// pieces sharing 256 elements, so that the reads of a row off 16-byte boundaries are contiguous over the lanes
+// (16384 x 2021 bf16: 143 us, 176 one by one; 4096 x 7001 fp32 90).
+enum { kOnes, kVector, kSpread };
+template <int kForm>
+QB_DEV int element(int i, int j) { return kForm == kSpread ? ((i & ~31) << 3) + 32 * j + (i & 31) : 8 * i + j; }
+template <int kForm>
+QB_DEV int pieces(int H) { return kForm == kSpread ? (H + 255) >> 8 << 5 : (H + 7) >> 3; }
+// Piece i of a row, zeros past its end.
+template <typename T, int kForm>
 QB_DEV void load8(const T* __restrict__ row, int i, int H, float (&v)[8]) {
-    if (kVec && sizeof(T) == 4) {
+    if (kForm == kVector && sizeof(T) == 4) {
         const float4 a = reinterpret_cast<const float4*>(row)[2 * i], b = reinterpret_cast<const float4*>(row)[2 * i + 1];
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else if (kVec) {
+    } else if (kForm == kVector) {
         const uint4 u = reinterpret_cast<const uint4*>(row)[i];
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 8 * i + j < H ? to_f32<T>(row[8 * i + j]) : 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = element<kForm>(i, j) < H ? to_f32<T>(row[element<kForm>(i, j)]) : 0.0f;
     }
 }
-template <typename T, bool kVec>
+template <typename T, int kForm>
 QB_DEV void store8(T* __restrict__ row, int i, int H, const float (&v)[8]) {
-    if (kVec && sizeof(T) == 4) {
+    if (kForm == kVector && sizeof(T) == 4) {
         reinterpret_cast<float4*>(row)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4*>(row)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if (kVec) {
+    } else if (kForm == kVector) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -64,7 +74,7 @@ QB_DEV void store8(T* __restrict__ row, int i, int H, const float (&v)[8]) {
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (8 * i + j < H) row[8 * i + j] = from_f32<T>(v[j]);
+            if (element<kForm>(i, j) < H) row[element<kForm>(i, j)] = from_f32<T>(v[j]);
     }
 }
 
@@ -151,18 +161,18 @@ QB_DEV void mxfp8_store(float (&n)[8], uint8_t* codes, uint8_t* scale, float (&v
 }
 
 // One row a CTA of blockDim.x threads, or, with blockDim.x = 32, one a warp.
-template <typename TX, typename TR, bool kVec, bool kQuant>
+template <typename TX, typename TR, int kForm, bool kQuant>
 __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) {
     __shared__ float scratch[kNormThreads / 32];
     const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     if (t >= a.T) return;   // whole warps, and only where a warp holds a row
-    const int items = (a.H + 7) >> 3;
+    const int items = pieces<kForm>(a.H);
     const TX* x = static_cast<const TX*>(a.x) + t * a.ldx;
     float v[kNormItems][8];
 #pragma unroll
     for (int i = 0; i < kNormItems; ++i) {
         const int at = threadIdx.x + i * blockDim.x;
-        if (at < items) load8<TX, kVec>(x, at, a.H, v[i]);
+        if (at < items) load8<TX, kForm>(x, at, a.H, v[i]);
     }
     if (a.residual) {
         const TR* residual = static_cast<const TR*>(a.residual) + t * a.ldr;
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) 
 #pragma unroll
         for (int i = 0; i < kNormItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
-            if (at < items) load8<TR, kVec>(residual, at, a.H, r[i]);
+            if (at < items) load8<TR, kForm>(residual, at, a.H, r[i]);
         }
 #pragma unroll
         for (int i = 0; i < kNormItems; ++i) {
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) 
             if (at >= items) break;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = to_f32<TR>(from_f32<TR>(v[i][j] + r[i][j]));
-            store8<TR, kVec>(total, at, a.H, v[i]);
+            store8<TR, kForm>(total, at, a.H, v[i]);
         }
     }
     float ss[1] = {0.0f};
@@ -196,15 +206,15 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) 
         const int at = threadIdx.x + i * blockDim.x;
         if (at >= items) break;
         float g[8], out[8];
-        load8<float, kVec>(a.gamma, at, a.H, g);
+        load8<float, kForm>(a.gamma, at, a.H, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
         if (kQuant) {
             const long long block = t * (items >> 2) + (at >> 2);
             mxfp8_store(v[i], a.codes + t * a.H + 8 * at, a.scales + block, out);
-            if (a.y) store8<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(a.y) + t * a.ldy, at, a.H, out);
+            if (a.y) store8<__nv_bfloat16, kForm>(static_cast<__nv_bfloat16*>(a.y) + t * a.ldy, at, a.H, out);
         } else {
-            store8<TX, kVec>(static_cast<TX*>(a.y) + t * a.ldy, at, a.H, v[i]);
+            store8<TX, kForm>(static_cast<TX*>(a.y) + t * a.ldy, at, a.H, v[i]);
         }
     }
 }
@@ -274,13 +284,13 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
         for (int i = 0; i < kItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
-            load8<TX, true>(x, at, a.H, v[i]);
+            load8<TX, kVector>(x, at, a.H, v[i]);
             if (a.residual) {
                 float r[8];
-                load8<TR, true>(residual, at, a.H, r);
+                load8<TR, kVector>(residual, at, a.H, r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = to_f32<TR>(from_f32<TR>(v[i][j] + r[j]));
-                store8<TR, true>(static_cast<TR*>(a.total) + t * a.ldt, at, a.H, v[i]);
+                store8<TR, kVector>(static_cast<TR*>(a.total) + t * a.ldt, at, a.H, v[i]);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
@@ -294,14 +304,14 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
             float g[8], out[8];
-            load8<float, true>(a.gamma, at, a.H, g);
+            load8<float, kVector>(a.gamma, at, a.H, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
             if (kQuant) {
                 mxfp8_store(v[i], a.codes + t * a.H + 8 * at, a.scales + t * (items >> 2) + (at >> 2), out);
-                if (a.y) store8<__nv_bfloat16, true>(static_cast<__nv_bfloat16*>(a.y) + t * a.ldy, at, a.H, out);
+                if (a.y) store8<__nv_bfloat16, kVector>(static_cast<__nv_bfloat16*>(a.y) + t * a.ldy, at, a.H, out);
             } else {
-                store8<TX, true>(static_cast<TX*>(a.y) + t * a.ldy, at, a.H, v[i]);
+                store8<TX, kVector>(static_cast<TX*>(a.y) + t * a.ldy, at, a.H, v[i]);
             }
         }
     }
@@ -324,11 +334,11 @@ struct NormGradArgs {
 
 // Rows blockIdx.x * blockDim.y + threadIdx.y, + gridDim.x * blockDim.y, ...: the sums of
 // squares and of g total are taken together; the gain's gradient adds up in registers.
-template <typename TD, typename TT, bool kVec>
+template <typename TD, typename TT, int kForm>
 __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const NormGradArgs a) {
     __shared__ float scratch[2 * (kNormThreads / 32)];
     extern __shared__ float lines[];   // [blockDim.y][H] where a warp holds a row
-    const int items = (a.H + 7) >> 3;
+    const int items = pieces<kForm>(a.H);
     float acc[kNormItems][8] = {};
     for (long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += (long long)gridDim.x * blockDim.y) {
         float d[kNormItems][8], v[kNormItems][8], s[2] = {0.0f, 0.0f};
@@ -336,15 +346,15 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const Nor
         for (int i = 0; i < kNormItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
-            load8<TD, kVec>(static_cast<const TD*>(a.dn) + t * a.lddn, at, a.H, d[i]);
-            load8<TT, kVec>(static_cast<const TT*>(a.total) + t * a.ldt, at, a.H, v[i]);
+            load8<TD, kForm>(static_cast<const TD*>(a.dn) + t * a.lddn, at, a.H, d[i]);
+            load8<TT, kForm>(static_cast<const TT*>(a.total) + t * a.ldt, at, a.H, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < kNormItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
             float g[8];
-            load8<float, kVec>(a.gamma, at, a.H, g);
+            load8<float, kForm>(a.gamma, at, a.H, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] = fmaf(v[i][j], v[i][j], s[0]), s[1] = fmaf(d[i][j] * g[j], v[i][j], s[1]);
         }
@@ -355,14 +365,14 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const Nor
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
             float g[8], o[8] = {};
-            load8<float, kVec>(a.gamma, at, a.H, g);
-            if (a.dtotal) load8<TT, kVec>(static_cast<const TT*>(a.dtotal) + t * a.lddt, at, a.H, o);
+            load8<float, kForm>(a.gamma, at, a.H, g);
+            if (a.dtotal) load8<TT, kForm>(static_cast<const TT*>(a.dtotal) + t * a.lddt, at, a.H, o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 acc[i][j] = fmaf(d[i][j], v[i][j] * r, acc[i][j]);
                 o[j] += (d[i][j] * g[j] - v[i][j] * c) * r;
             }
-            store8<TT, kVec>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+            store8<TT, kForm>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
         }
     }
     if (!a.parts) return;
@@ -371,14 +381,14 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const Nor
 #pragma unroll
         for (int i = 0; i < kNormItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
-            if (at < items) store8<float, false>(part, at, a.H, acc[i]);
+            if (at < items) store8<float, kForm == kSpread ? kSpread : kOnes>(part, at, a.H, acc[i]);
         }
         return;
     }
 #pragma unroll
     for (int i = 0; i < kNormItems; ++i) {
         const int at = threadIdx.x + i * blockDim.x;
-        if (at < items) store8<float, false>(lines + threadIdx.y * a.H, at, a.H, acc[i]);
+        if (at < items) store8<float, kForm == kSpread ? kSpread : kOnes>(lines + threadIdx.y * a.H, at, a.H, acc[i]);
     }
     __syncthreads();
     for (int j = threadIdx.y * 32 + threadIdx.x; j < a.H; j += 32 * kRowWarps) {
@@ -424,8 +434,8 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
             float d[8], v[8], g[8];
-            load8<TD, true>(dn, at, a.H, d);
-            load8<TT, true>(total, at, a.H, v);
+            load8<TD, kVector>(dn, at, a.H, d);
+            load8<TT, kVector>(total, at, a.H, v);
             gain8(gain, at, items, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], v[j], sum[0]), sum[1] = fmaf(d[j] * g[j], v[j], sum[1]);
@@ -437,16 +447,16 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
             const int at = threadIdx.x + i * blockDim.x;
             if (at >= items) break;
             float d[8], v[8], g[8], o[8] = {};
-            load8<TD, true>(dn, at, a.H, d);
-            load8<TT, true>(total, at, a.H, v);
+            load8<TD, kVector>(dn, at, a.H, d);
+            load8<TT, kVector>(total, at, a.H, v);
             gain8(gain, at, items, g);
-            if (a.dtotal) load8<TT, true>(dtotal, at, a.H, o);
+            if (a.dtotal) load8<TT, kVector>(dtotal, at, a.H, o);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 acc[i][j] = fmaf(d[j], v[j] * r, acc[i][j]);
                 o[j] += (d[j] * g[j] - v[j] * c) * r;
             }
-            store8<TT, true>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+            store8<TT, kVector>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
         }
         bring(s);   // this thread has read its pieces
         if (++s == ring.stages) s = 0;
@@ -455,7 +465,7 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int at = threadIdx.x + i * blockDim.x;
-        if (at < items) store8<float, true>(a.parts + (long long)blockIdx.x * a.H, at, a.H, acc[i]);
+        if (at < items) store8<float, kVector>(a.parts + (long long)blockIdx.x * a.H, at, a.H, acc[i]);
     }
 }
 
@@ -493,7 +503,8 @@ dim3 row_block(int H) {
 }
 int gain_parts(int T, int H) {
     const long long ctas = (T + (long long)row_block(H).y - 1) / row_block(H).y;
-    return (int)(ctas < kGainParts ? ctas : kGainParts);
+    const long long most = row_block(H).y == 1 && row_block(H).x <= 64 ? 2 * kGainParts : kGainParts;   // eight small CTAs a SM
+    return (int)(ctas < most ? ctas : most);
 }
 
 // Whether the rows go through a ring, and its shape: up to rows of 8192 as many CTAs a SM as 64 registers a thread
@@ -599,8 +610,8 @@ extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long lon
             return;
         }
         auto go = [&](auto kern) { kern<<<grid, block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a); };
-        if (vec) codes ? go(k_add_rmsnorm<TX, TR, true, true>) : go(k_add_rmsnorm<TX, TR, true, false>);
-        else codes ? go(k_add_rmsnorm<TX, TR, false, true>) : go(k_add_rmsnorm<TX, TR, false, false>);
+        if (vec) codes ? go(k_add_rmsnorm<TX, TR, kVector, true>) : go(k_add_rmsnorm<TX, TR, kVector, false>);
+        else codes ? go(k_add_rmsnorm<TX, TR, kOnes, true>) : go(k_add_rmsnorm<TX, TR, kSpread, false>);   // (a block of codes is four threads')
     });
     return qbh::cuda_err(cudaGetLastError());
 }
@@ -644,8 +655,8 @@ extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* d
             else k_add_rmsnorm_backward_rows<TD, TT, 4><<<grid, rows.threads, rows.smem, s>>>(a, rows.ring);
             return;
         }
-        if (vec) k_add_rmsnorm_backward<TD, TT, true><<<grid, block, smem, s>>>(a);
-        else k_add_rmsnorm_backward<TD, TT, false><<<grid, block, smem, s>>>(a);
+        if (vec) k_add_rmsnorm_backward<TD, TT, kVector><<<grid, block, smem, s>>>(a);
+        else k_add_rmsnorm_backward<TD, TT, kSpread><<<grid, block, smem, s>>>(a);
     });
     if (dgamma) k_gain_finish<<<(H + 31) / 32, dim3(32, kFinishRows), 0, s>>>(grid, H, parts, dgamma);
     return qbh::cuda_err(cudaGetLastError());
