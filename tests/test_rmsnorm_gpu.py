@@ -233,3 +233,22 @@ def test_many_rows(T, H, x, res):
         dx, dg = Q.add_rmsnorm_backward(a.cuda(), total.cuda(), g.cuda(), eps=EPS, **kw)
         near(dx, wx, 2.0 ** -18 * mx + HALF[res] * np.abs(wx))
         near(dg, wg, (2.0 ** -19 + (T + 100) * 2.0 ** -24) * mg)
+
+
+@pytest.mark.parametrize("T,H", [(3, 40), (5, 33), (1600, 640)])
+def test_gradient_against_differences(T, H):
+    """The loss sum(dy n(total)) along random directions of total and gamma, by central differences in 64 bits."""
+    import quantile_balanced_routing_gb300 as Q
+    v, d, g = data(T, T, H, torch.float32, 0.3), data(T + 1, T, H, torch.float32, 0.3), gain(H, H)
+    dx, dg = (f64(t) for t in Q.add_rmsnorm_backward(d.cuda(), v.cuda(), g.cuda(), eps=EPS))
+    (_, mx), (_, mg) = F.norm_backward(f64(d), f64(v), f64(g), None, EPS)
+    r = np.random.RandomState(H)
+    loss = lambda t, c: (f64(d) * F.norm(t, c, EPS)).sum()  # noqa: E731
+    h = 1e-5   # the differences' own error: h^2 times the third derivative (at most 100 times the first's sum), and 2^-52 of the loss over h
+    for _ in range(4):
+        u, c = r.standard_normal((T, H)), r.standard_normal(H)
+        got, want = (dx * u).sum(), (loss(f64(v) + h * u, f64(g)) - loss(f64(v) - h * u, f64(g))) / (2 * h)
+        noise = 2.0 ** -50 * np.abs(f64(d) * F.norm(f64(v), f64(g), EPS)).sum() / h
+        assert abs(got - want) <= ((2.0 ** -18 + 1e-8) * mx * np.abs(u)).sum() + noise
+        got, want = (dg * c).sum(), (loss(f64(v), f64(g) + h * c) - loss(f64(v), f64(g) - h * c)) / (2 * h)
+        assert abs(got - want) <= ((2.0 ** -19 + (T + 100) * 2.0 ** -24) * mg * np.abs(c)).sum() + noise
