@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
         tc::tmem_alloc(tmem_slot, Sh::kCols);
         tc::tmem_relinquish();
     }
+    if (kPieced) pdl_trigger();   // the next kernel may set itself up meanwhile
     if (!p.weights_ready) pdl_wait();
     tc::tc_fence_before();
     load_groups<BN, Sh::kThreads>(gr, p.offsets, p.E, p.R, scratch);

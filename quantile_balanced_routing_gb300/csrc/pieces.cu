@@ -198,13 +198,14 @@ struct GluArgs {
 };
 __global__ void __launch_bounds__(kSplitThreads) k_split_glu(const GluArgs a) {
     pdl_trigger();
-    const uint32_t rows = min(a.piece_offsets[a.E] / qbh::kPieces, a.R), lane = threadIdx.x & 31, warps = a.M >> 8;
+    pdl_wait();   // h comes from the kernel before
+    const uint32_t rows = min(__ldcg(a.piece_offsets + a.E) / qbh::kPieces, a.R), lane = threadIdx.x & 31, warps = a.M >> 8;
     for (uint32_t i = blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); i < rows * warps; i += gridDim.x * (kSplitThreads / 32)) {
         const long long row = i / warps;
         const int at = (int)(i % warps) * 32 + lane;
         const float4* g = reinterpret_cast<const float4*>(a.h + row * 2 * a.M) + 2 * at;
         const float4* u = g + (a.M >> 2);
-        const float4 g0 = g[0], g1 = g[1], u0 = u[0], u1 = u[1];
+        const float4 g0 = __ldcg(g), g1 = __ldcg(g + 1), u0 = __ldcg(u), u1 = __ldcg(u + 1);
         Block b;
         b.up = 0;
         b.nan = false;
@@ -249,8 +250,7 @@ int split_routes(int T, int k, int E, int K, const PieceSource& x, const int32_t
 
 int split_glu(int R, int E, int M, const float* h, float beta1, float beta2, const int32_t* piece_offsets, uint8_t* pieces, cudaStream_t s) {
     const GluArgs a{R, E, M, h, beta1, beta2, piece_offsets, pieces, pieces + piece_code_bytes(R, M)};
-    k_split_glu<<<grid_of((long long)R * (M / 256), kSplitThreads / 32, 6), kSplitThreads, 0, s>>>(a);
-    return cuda_err(cudaGetLastError());
+    return launch_pdl(k_split_glu, dim3(grid_of((long long)R * (M / 256), kSplitThreads / 32, 6)), dim3(kSplitThreads), 0, s, a);
 }
 
 int pieces_init() {

@@ -9,7 +9,7 @@
 // (743 cycles a SM for a stage's bytes, 375 for its MMAs at 192).
 //
 // Measured (896 experts of 1024 x 3584, 4096 rows): split 26 us (67 MB of pieces to L2), product 255 us, the weights
-// at 6.8 TB/s; together 297, where the rows in registers (mxfp4_stream.cuh) take 408.  Experts of 256 tokens:
+// at 6.8 TB/s; together 290, where the rows in registers (mxfp4_stream.cuh) take 408.  Experts of 256 tokens:
 // split 31, gate and up 450 (6.7 TB/s), SiTU-GLU 21, down 256 (5.8 TB/s, with 59 MB of fp32 rows written), combine 11 to 20.
 #pragma once
 
