@@ -178,11 +178,11 @@ extern "C" int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, 
         const qbh::PieceSource from{x_type, x, ldx, x_scales, row_map, k, odd};
         if ((rc2 = qbh::split_routes(T, k, E, L, from, idx, xp, offsets, row_map, odd, s))) return rc2;
         if ((rc2 = qbh::piece_product({R, E, M, L, xp, xp + qbh::piece_code_bytes(R, L), gate_codes, gate_scales, up_codes, up_scales,
-                                       offsets, nullptr, act, QBMOE_F32, 2LL * M, from}, s)))
+                                       offsets, nullptr, act, QBMOE_F32, 2LL * M, from, true}, s)))
             return rc2;
         if ((rc2 = qbh::split_glu(R, E, M, act, beta1, beta2, offsets, ap, s))) return rc2;
         if ((rc2 = qbh::piece_product({R, E, L, M, ap, ap + qbh::piece_code_bytes(R, M), out_codes, out_scales, nullptr, nullptr,
-                                       offsets, row_map, rows, QBMOE_F32, L, {}}, s)))
+                                       offsets, row_map, rows, QBMOE_F32, L, {}, true}, s)))
             return rc2;
     } else {
         StreamArgs a{};

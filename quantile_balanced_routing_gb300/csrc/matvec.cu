@@ -80,7 +80,7 @@ extern "C" int moe_mxfp4_matvec(int R, int E, int N, int K, int x_type, const vo
         const int rc2 = qbh::split_rows(R, E, K, from, offsets, pieces, piece_offsets, pieces + at.odd, s);
         if (rc2) return rc2;
         return qbh::piece_product({R, E, N, K, pieces, pieces + qbh::piece_code_bytes(R, K), w_codes, w_scales, nullptr, nullptr,
-                                   offsets ? piece_offsets : nullptr, nullptr, y, y_type, ldy, from}, s);
+                                   offsets ? piece_offsets : nullptr, nullptr, y, y_type, ldy, from, false}, s);
     }
     StreamArgs a{};
     a.R = R; a.E = E; a.N = N; a.K = K;

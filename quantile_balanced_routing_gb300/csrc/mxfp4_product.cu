@@ -96,6 +96,7 @@ struct Params {
     int sums_type;
     qbh::PieceSource x;
     const uint8_t *a_codes, *a2_codes;
+    bool followed;
 };
 // The weights that a tile takes, and its first row in them.
 struct TileRows {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, BN == 16 ? 2 : 1) k_mx_pr
         tc::tmem_alloc(tmem_slot, Sh::kCols);
         tc::tmem_relinquish();
     }
-    if (kPieced) pdl_trigger();   // the next kernel may set itself up meanwhile
+    if (kPieced && p.followed) pdl_trigger();   // the next kernel may set itself up meanwhile
     if (!p.weights_ready) pdl_wait();
     tc::tc_fence_before();
     load_groups<BN, Sh::kThreads>(gr, p.offsets, p.E, p.R, scratch);
@@ -758,6 +759,7 @@ int piece_product(const PieceProduct& q, cudaStream_t s) {
     }
     p.row_map = q.row_map;
     p.x = q.x;
+    p.followed = q.followed;
     p.a_codes = q.w_codes;
     p.a2_codes = q.w2_codes;
     p.sums = q.y;

@@ -1,7 +1,7 @@
 // Rows as sums of MXFP4 rows, for the block-scaled tensor cores.
 //
 // An element of a block of 32 becomes a whole number of 22 bits and a sign, in units of 2^-21 of the
-// power of two below the block's largest; its eight octal digits, from -4 to 4, are E2M1 values,
+// power of two below the block's largest; its eight octal digits, from -4 to 3, are E2M1 values,
 // and digit i's MXFP4 row has the block's scale times 8^i.  So a row is the sum of eight MXFP4 rows,
 // within 2^-22 of each block's largest: E4M3 elements and bf16 elements down to 2^-14 of it are exact.
 // The product kernel (mxfp4_product.cu) takes them as columns, eight for one row of x, and adds each eight in its
@@ -9,7 +9,7 @@
 // (743 cycles a SM for a stage's bytes, 375 for its MMAs at 192).
 //
 // Measured (896 experts of 1024 x 3584, 4096 rows): split 26 us (67 MB of pieces to L2), product 255 us, the weights
-// at 6.8 TB/s; together 290, where the rows in registers (mxfp4_stream.cuh) take 408.  Experts of 256 tokens:
+// at 6.8 TB/s; together 290 to 296, where the rows in registers (mxfp4_stream.cuh) take 408.  Experts of 256 tokens:
 // split 31, gate and up 450 (6.7 TB/s), SiTU-GLU 21, down 256 (5.8 TB/s, with 59 MB of fp32 rows written), combine 11 to 20.
 #pragma once
 
@@ -54,6 +54,7 @@ struct PieceProduct {
     int y_type;
     long long ldy;
     PieceSource x;
+    bool followed;   // the next kernel is one that waits for this one before it reads anything: it may be launched early
 };
 int piece_product(const PieceProduct& p, cudaStream_t s);
 

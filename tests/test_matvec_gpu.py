@@ -519,3 +519,23 @@ def test_in_pieces_captured_replayed_and_on_two_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) for a, b in zip(captured, run()))
     assert Q.qbmoe_status(None, None) == 0
+
+
+def test_routing_of_logits_in_pieces():
+    """Kernels that are launched while the one before them drains see all of the products."""
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(11)
+    T, n, K = 1500, 896, 1024
+    assert in_pieces(1, T, n, K)
+    w, _ = weights(r, n, K)
+    batches = [torch.from_numpy(r.standard_normal((T, K))).to(torch.bfloat16).cuda() for _ in range(4)]
+    want = []
+    for x in batches:
+        logits = Q.mxfp4_matvec(x, w, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in Q.route_qb(logits, 16)])
+        torch.cuda.synchronize()
+    for _ in range(10):
+        for x, expect in zip(batches, want):
+            got = Q.route_qb(Q.mxfp4_matvec(x, w, out_dtype=torch.float32), 16)
+            assert all(torch.equal(a, b) for a, b in zip(got, expect))
