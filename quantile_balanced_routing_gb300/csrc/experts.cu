@@ -1,4 +1,6 @@
-// The routed experts of a few tokens (C ABI: moe_mxfp4_experts).
+// The routed experts of a few tokens (C ABI: moe_mxfp4_experts).  In pieces (pieces.cuh) five kernels: x split by
+// route, gate and up, SiTU-GLU split, down, and the tokens' sums; else (mxfp4_stream.cuh) three: gate, up and SiTU-GLU,
+// down, sums.  256 tokens' 16 routes over 896 experts, 3584 / 1024: 780 us, 1370 with three kernels.
 //
 // [K3-width] 延伸解读 on deployment: routed-expert weights in MXFP4; Q&A SiTU-GLU and
 // RMSNorm: the experts' activation and the norm of their weighted sum.

@@ -1,4 +1,5 @@
-// MXFP4 weights with few rows (C ABI: moe_mxfp4_matvec).
+// MXFP4 weights with few rows (C ABI: moe_mxfp4_matvec): in pieces where weights are many (pieces.cuh), else with the
+// rows in registers (mxfp4_stream.cuh).
 //
 // [K3-width] 延伸解读 on deployment: MXFP4 weights.
 #include "mxfp4_stream.cuh"

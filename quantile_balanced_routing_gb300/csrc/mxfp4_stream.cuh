@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that twelve warps hold in 22 blocks each
+constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that eight warps hold in 32 blocks each
 
 int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
 
