@@ -539,3 +539,35 @@ def test_routing_of_logits_in_pieces():
         for x, expect in zip(batches, want):
             got = Q.route_qb(Q.mxfp4_matvec(x, w, out_dtype=torch.float32), 16)
             assert all(torch.equal(a, b) for a, b in zip(got, expect))
+
+
+@pytest.mark.parametrize("R", [131072, 131080])
+def test_most_rows_in_pieces_and_beyond(R):
+    """2^25 elements of x are split; more are multiplied as they are."""
+    import quantile_balanced_routing_gb300 as Q
+    N, K = 32, 256
+    assert in_pieces(1, R, N, K)
+    r = np.random.RandomState(12)
+    w, wv = weights(r, N, K)
+    x = torch.randn(R, K, device="cuda", generator=torch.Generator("cuda").manual_seed(R)).to(torch.bfloat16)
+    y = Q.mxfp4_matvec(x, w, out_dtype=torch.float32).double()
+    wt = torch.from_numpy(wv).cuda()
+    want = x.double() @ wt.T
+    top = x.double().abs().view(R, K // 32, 32).amax(2)
+    bound = (K + 1) * 2.0 ** -24 * (x.double().abs() @ wt.abs().T) + 2.0 ** -22 * (top @ wt.abs().view(N, K // 32, 32).sum(2).T)
+    assert ((y - want).abs() <= bound).all()
+
+
+def test_no_row_has_pieces():
+    """The slow way for every row of the deepest product ends in time for the kernel's waits."""
+    import quantile_balanced_routing_gb300 as Q
+    r = np.random.RandomState(13)
+    R, N, K = 700, 264, 8192
+    assert in_pieces(1, R, N, K)
+    w, wv = weights(r, N, K)
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    x[:, ::32] = 2.0 ** -110                     # below what the scales follow
+    y = Q.mxfp4_matvec(x, w, out_dtype=torch.float32)
+    want = 2.0 ** -110 * wv[:, ::32].sum(1)
+    near(y, np.repeat(want[None], R, 0), K * 2.0 ** -24 * 2.0 ** -110 * np.abs(wv[:, ::32]).sum(1)[None].repeat(R, 0))
+    assert Q.qbmoe_status(None, None) == 0
