@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                 }
             }
             bytes = __reduce_add_sync(0xffffffffu, bytes) + (kBoxes ? boxes * box_bytes : rows * nblk * (kMode == kGlu ? 32 : 16));
+            __syncwarp();   // the other lanes' bytes come before lane 0's arrival (a reduction orders no memory)
             if (lane == 0) {
                 tc::mbar_expect_tx(bar, bytes);
                 for (int b = 0; kBoxes && b < boxes; ++b) {
