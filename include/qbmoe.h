@@ -425,8 +425,8 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *
  * Both take weights and MXFP8 rows as they are.  Small calls, and depths that are not multiples of 256 or
  * over 8192, take each block of 32 of a bf16 row as fp16 times a power of two: exact for elements
- * down to 2^-29 of the block's largest and within 2^-40 of it below; the SiTU-GLU's fp32 result is rounded
- * to fp16 that way (2^-12).  All others take bf16 rows, and the SiTU-GLU's result, as sums of eight MXFP4 rows:
+ * down to 2^-29 of the block's largest and within 2^-40 of it below; the SiTU-GLU's fp32 result as two such terms
+ * (within 2^-22 of the value, or 2^-40 of the block's largest).  All others take bf16 rows, and the SiTU-GLU's result, as sums of eight MXFP4 rows:
  * within 2^-22 of a block's largest (bf16 elements down to 2^-14 of it are exact); rows with
  * infinities or blocks of magnitudes below 2^-100 are multiplied as they are, slowly, and
  * what is below 2^-121 in the SiTU-GLU's result is dropped.  Sums are fp32 in a

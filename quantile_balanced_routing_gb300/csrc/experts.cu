@@ -111,19 +111,18 @@ struct ExpertsScratch {
     size_t act, parts, rows, act_pieces, offsets, row_map, odd, bytes;
     bool pieces;
     ExpertsScratch(int T, int k, int L, int M) {
+        const size_t R = (size_t)T * k, up = slabs_of(L), down = slabs_of(M, kDown);
         pieces = qbh::pieces_ok(L) && qbh::pieces_ok(M) && slabs_of(L) == 1 && slabs_of(M) == 1;
         if (pieces) {
-            const size_t R = (size_t)T * k;
             act = parts = 0;
             rows = qbh::align_up(2 * R * M * 4, 256);
-            act_pieces = rows + max(qbh::align_up(R * L * 4, 256), qbh::piece_bytes(R, L));
+            act_pieces = rows + max(qbh::align_up(down * R * L * 4, 256), qbh::piece_bytes(R, L));
             offsets = act_pieces + qbh::piece_bytes(R, M);
             row_map = offsets + qbh::align_up((QBMOE_MAX_EXPERTS + 1) * 4, 256);
             odd = row_map + qbh::align_up(R * 4, 256);
             bytes = odd + R * qbh::kOddBytes;
             return;
         }
-        const size_t R = (size_t)T * k, up = slabs_of(L), down = slabs_of(M);
         act = 0;
         parts = qbh::align_up(R * M * 4, 256);
         rows = parts + (up > 1 ? qbh::align_up(up * 2 * R * M * 4, 256) : 0);
@@ -172,8 +171,9 @@ extern "C" int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, 
     float *act = reinterpret_cast<float*>(base + at.act), *parts = reinterpret_cast<float*>(base + at.parts), *rows = reinterpret_cast<float*>(base + at.rows);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int R = T * k;
+    const bool in_pieces = at.pieces && qbh::pieces_pay(min(E, R), R, 3LL * L * M);
     int rc2 = 0;
-    if (at.pieces && qbh::pieces_pay(min(E, R), R, 3LL * L * M)) {
+    if (in_pieces) {
         uint8_t *xp = reinterpret_cast<uint8_t*>(rows), *ap = reinterpret_cast<uint8_t*>(base + at.act_pieces);
         int32_t *offsets = reinterpret_cast<int32_t*>(base + at.offsets), *row_map = reinterpret_cast<int32_t*>(base + at.row_map);
         uint8_t* odd = reinterpret_cast<uint8_t*>(base + at.odd);
@@ -207,6 +207,6 @@ extern "C" int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, 
         a.y = rows; a.ldy = L;
         if ((rc2 = ::stream<QBMOE_F32, kDown>(a, out_codes, nullptr, s))) return rc2;
     }
-    const CombineArgs c{T, k, E, L, slabs_of(M), idx, w, rows, gamma, rms_eps, static_cast<__nv_bfloat16*>(y), ldy};
+    const CombineArgs c{T, k, E, L, in_pieces ? 1 : slabs_of(M, kDown), idx, w, rows, gamma, rms_eps, static_cast<__nv_bfloat16*>(y), ldy};
     return qbh::launch_pdl(k_combine, dim3(T), dim3(kCombineThreads), 0, s, c);
 }

@@ -11,7 +11,9 @@
 // operands, so that the rows cost no bandwidth while weights go by.  Per block of 32 and tile:
 //   - ldmatrix hands each quad of lanes the 16 bytes of a weight row's block;
 //   - codes become fp16 (exact) two at a time, with one conversion;
-//   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B;
+//   - two m16n8k16 products, weights as A (16 rows), 8 columns of x as B (for the SiTU-GLU's fp32 results two more, of
+//     what fp16 leaves of them: with half as many blocks a warp, 256 tokens' 16 routes over 896 experts of 3552 / 992
+//     take 1484 us, with one term and all blocks 1587, with the second term in columns of its own 2071);
 //   - the block's dot products, times the two scales, are added in fp32.
 // Two producer warps, a stage each in turn, bring codes (long rows one by one, short ones
 // in TMA boxes: a copy costs 20 to 80 cycles to issue) and scales several units ahead; two more
@@ -47,6 +49,9 @@ constexpr int kSlack = 128;                    // scales are read by the word, u
 
 // What a launch computes.
 enum { kStore, kGlu, kDown };
+// fp16 terms of an element of x: the SiTU-GLU's fp32 results take two, the second of what the first leaves (together
+// within 2^-22 of the value), in half as many blocks a warp.
+constexpr int terms_of(int mode) { return mode == kDown ? 2 : 1; }
 constexpr int kBox = 8;                        // blocks of 32 in a row of a TMA box: 128 bytes of codes
 
 struct StreamArgs {
@@ -158,7 +163,10 @@ QB_DEV uint32_t f16_pair(float a, float b) {
 // A block whose largest magnitude m has these fp32 bits, as fp16: its largest element is put
 // into [2^15, 65504], so that a bf16 element is exact down to 2^-32 of it, and any element within
 // 2^-40 of it.  A block with an infinity or a NaN keeps those alone, which decide the result.
-QB_DEV float block_to_f16(const float (&v)[8], uint32_t m, uint32_t (&b)[4]) {
+// kTerms 2: pairs 4 to 7 hold what the first four leave of the elements, in the same unit: both within 2^-22 of an
+// element, or 2^-40 of the largest.
+template <int kTerms>
+QB_DEV float block_to_f16(const float (&v)[8], uint32_t m, uint32_t (&b)[4 * kTerms]) {
     const int ef = max((int)((m + 0x1000u) >> 23), 16);   // of m rounded to fp16's 11 bits
     const bool bad = m >= 0x7f800000u;
     const float inv = __int_as_float((269 - ef) << 23);   // 2^(15 - exponent); not used when bad
@@ -170,6 +178,10 @@ QB_DEV float block_to_f16(const float (&v)[8], uint32_t m, uint32_t (&b)[4]) {
             q = (__float_as_uint(v[2 * j + 1]) & 0x7f800000u) == 0x7f800000u ? v[2 * j + 1] : 0.0f;
         }
         b[j] = f16_pair(p, q);
+        if (kTerms == 2) {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&b[j]));
+            b[4 + j] = bad ? 0u : f16_pair(p - h.x, q - h.y);   // (exact differences)
+        }
     }
     return bad ? 1.0f : __int_as_float((ef - 15) << 23);
 }
@@ -195,8 +207,9 @@ struct Raw {
             u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + row * a.ldx + at);
         }
     }
-    // The four pairs of fp16 and (in every lane of the quad) the block's scale.
-    QB_DEV float convert(uint32_t (&b)[4]) const {
+    // The four pairs of fp16 a term and (in every lane of the quad) the block's scale.
+    template <int kTerms>
+    QB_DEV float convert(uint32_t (&b)[4 * kTerms]) const {
         if (kX == QBMOE_MXFP8) {
             asm("{\n\t.reg .b16 p, q, r, s;\n\tmov.b32 {p, q}, %4;\n\tmov.b32 {r, s}, %5;\n\t"
                 "cvt.rn.f16x2.e4m3x2 %0, p;\n\tcvt.rn.f16x2.e4m3x2 %1, q;\n\t"
@@ -215,7 +228,7 @@ struct Raw {
         for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        return block_to_f16(f, m, b);
+        return block_to_f16<kTerms>(f, m, b);
     }
 };
 
@@ -356,8 +369,8 @@ struct Units {
 // stage lies; lo, hi: the scales of its weight rows lane / 4 and 8 more.  kSome: only nb blocks are the
 // warp's; for the rest B and the scales of x are zeros, and the weights' scales, whatever lies there, are
 // cleared lest one be NaN.
-template <int kNB, int kMT, bool kBoxes, bool kSome>
-QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (&wat)[4], const uint32_t (&at)[kMT],
+template <int kNB, int kMT, bool kBoxes, bool kSome, int kTerms>
+QB_DEV void share(const uint32_t (&B)[kNB][4 * kTerms], const float* sx, const uint32_t (&wat)[4], const uint32_t (&at)[kMT],
                   const uint32_t (&lo)[kMT], const uint32_t (&hi)[kMT], int nb, float (&acc)[kMT][4]) {
     constexpr int box_bytes = 16 * kMT * 128;   // (boxes hold all tiles of a unit)
     auto load = [&](uint32_t (&w)[4], int i, int m) { ldmatrix4(w, (kBoxes ? wat[i / 2 % 4] + i / kBox * box_bytes : wat[0] + i * 16) + at[m]); };
@@ -405,6 +418,8 @@ QB_DEV void share(const uint32_t (&B)[kNB][4], const float* sx, const uint32_t (
                 float d[4];
                 mma_f16_first(d, p[0], q[0], p[1], q[1], B[i + h][0], B[i + h][1]);
                 mma_f16(d, p[2], q[2], p[3], q[3], B[i + h][2], B[i + h][3]);
+#pragma unroll
+                for (int t = 4; t < 4 * kTerms; t += 2) mma_f16(d, p[t - 4], q[t - 4], p[t - 3], q[t - 3], B[i + h][t], B[i + h][t + 1]);
                 const float2 u = mul2(d[0], d[1], x), v = mul2(d[2], d[3], x);
                 acc[m][0] = fmaf(u.x, wsc[m][0][h], acc[m][0]);
                 acc[m][1] = fmaf(u.y, wsc[m][0][h], acc[m][1]);
@@ -420,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
     using S = Shape<kNB, kMT, kBoxed>;
     constexpr bool kBoxes = S::kBoxes;
     constexpr bool kRoutes = kMode == kGlu || kMode == kDown;
+    constexpr int kTerms = terms_of(kMode);
     extern __shared__ __align__(128) char sm[];
     __shared__ int scratch[kThreads / 32];
     uint64_t* full = reinterpret_cast<uint64_t*>(sm);   // a unit's copies have landed
@@ -594,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
         const int g8 = lane >> 2, t4 = lane & 3;
         float* sx = sx_all + warp * (kNB * kCols);
         if (kMode == kDown) pdl_wait();   // the rows come from the kernel before
-        uint32_t B[kNB][4];
+        uint32_t B[kNB][4 * kTerms];
         int nb = 0, turn = 0;
         uint32_t wat0[4], sat0 = 0, start = 0;   // in stage 0: this lane's codes and scales; the first scale's place in its tensor
         const uint32_t in_second = a.rows && kMode != kGlu ? 8 * depth : 0;   // (row by row the second half's are elsewhere)
@@ -622,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
                     for (int i = 0; i < kBatch && i0 + i < kNB; ++i) raw[i].load(a, row, blk0 + b0 + i0 + i, have && i0 + i < nb);
 #pragma unroll
                     for (int i = 0; i < kBatch && i0 + i < kNB; ++i) {
-                        const float sc = raw[i].convert(B[i0 + i]);
+                        const float sc = raw[i].template convert<kTerms>(B[i0 + i]);
                         if (t4 == 0) sx[(i0 + i) * kCols + g8] = sc;
                     }
                 }
@@ -652,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
             }
             start += groups * features * depth;
             float acc[kMT][4] = {};
-            if (nb == kNB) share<kNB, kMT, kBoxes, false>(B, sx + 2 * t4, wat0, at, lo, hi, nb, acc);
-            else share<kNB, kMT, kBoxes, true>(B, sx + 2 * t4, wat0, at, lo, hi, nb, acc);
+            if (nb == kNB) share<kNB, kMT, kBoxes, false, kTerms>(B, sx + 2 * t4, wat0, at, lo, hi, nb, acc);
+            else share<kNB, kMT, kBoxes, true, kTerms>(B, sx + 2 * t4, wat0, at, lo, hi, nb, acc);
             __syncwarp();
 #pragma unroll
             for (int m = 0; m < kStages; ++m)
@@ -679,35 +695,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_stream(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that eight warps hold in 32 blocks each
+constexpr int kSlabBlocks = 256;   // of 32: the deepest slab that eight warps hold in 32 blocks each, or 16 of two terms
 
-int slabs_of(int K) { return (K / 32 + kSlabBlocks - 1) / kSlabBlocks; }
+int slabs_of(int K, int mode = kStore) {
+    const int most = kSlabBlocks / terms_of(mode);
+    return (K / 32 + most - 1) / most;
+}
 
 // Calls f with the shape whose warps hold `per` blocks: the smallest of a few sizes (what is beyond a
 // warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n; two tiles a unit halve what a
 // unit costs besides, where the registers allow them.
-template <typename F>
+template <int kMode, typename F>
 int for_shape(bool boxes, int per, F f) {
-    if (boxes) return per <= kBox ? f(Shape<kBox, 2, true>{}) : f(Shape<2 * kBox, 2, true>{});
-    if (per <= 14) return f(Shape<14, 2, false>{});
-    if (per <= 16) return f(Shape<16, 2, false>{});
-    if (per <= 28) return f(Shape<28, 1, false>{});
-    return f(Shape<32, 1, false>{});
+    if constexpr (terms_of(kMode) == 2) {
+        return boxes ? f(Shape<kBox, 2, true>{}) : f(Shape<16, 1, false>{});
+    } else {
+        if (boxes) return per <= kBox ? f(Shape<kBox, 2, true>{}) : f(Shape<2 * kBox, 2, true>{});
+        if (per <= 14) return f(Shape<14, 2, false>{});
+        if (per <= 16) return f(Shape<16, 2, false>{});
+        if (per <= 28) return f(Shape<28, 1, false>{});
+        return f(Shape<32, 1, false>{});
+    }
 }
 
 // Geometry and launch; codes (kGlu: gate) and codes2 (up) are the weights' [E, N, K / 2].
 template <int kX, int kMode>
 int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream_t s) {
     const int depth = a.K / 32;
-    a.slabs = slabs_of(a.K);
+    a.slabs = slabs_of(a.K, kMode);
     a.slab_blocks = ((depth + a.slabs - 1) / a.slabs + kBox - 1) / kBox * kBox;   // whole boxes
     a.slab_blocks = min(a.slab_blocks, depth);
-    // short rows (up to eight boxes): the smallest groups whose warps have two each; else all warps are one group
+    // short rows (up to eight boxes): the smallest groups whose warps have two each (of two terms, one); else all warps are one group
     const int n_boxes = (a.slab_blocks + kBox - 1) / kBox;
     const bool boxes = n_boxes <= 8;
-    a.splits = !boxes || n_boxes > 8 ? kWarps : n_boxes > 4 ? 4 : (n_boxes + 1) / 2;
+    const int warp_boxes = n_boxes == 1 || terms_of(kMode) == 2 ? 1 : 2, holders = (n_boxes + warp_boxes - 1) / warp_boxes;
+    a.splits = !boxes || holders > 4 ? kWarps : holders > 2 ? 4 : holders;
     a.groups = kWarps / a.splits;
-    const int per = boxes ? (n_boxes == 1 ? 1 : 2) * kBox : (a.slab_blocks + a.splits - 1) / a.splits;
+    const int per = boxes ? warp_boxes * kBox : (a.slab_blocks + a.splits - 1) / a.splits;
     a.rows = a.slabs > 1;
     // row by row: pieces that hold a slab's scales from any start within 16 bytes, an odd number of
     // 16 bytes apart, so that eight rows lie in different banks
@@ -715,7 +739,7 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
     a.expiries = qbh::mx_expiries();
     a.wait_limit = qbh::mx_wait_limit();
     a.stall = qbh::mx_stall();
-    return for_shape(boxes, per, [&](auto shape) -> int {
+    return for_shape<kMode>(boxes, per, [&](auto shape) -> int {
         using S = decltype(shape);
         const int rows = 16 * S::kTiles, staged = 16 * S::kStaged, box_rows = kMode == kGlu ? staged / 2 : staged;
         a.w = codes;
@@ -754,9 +778,9 @@ int set_smem_all() {
     };
     int rc = 0;
     for (int per : {kBox, 2 * kBox})
-        if (!rc) rc = for_shape(true, per, set);
+        if (!rc) rc = for_shape<kMode>(true, per, set);
     for (int per : {14, 16, 28, 32})
-        if (!rc) rc = for_shape(false, per, set);
+        if (!rc) rc = for_shape<kMode>(false, per, set);
     return rc;
 }
 
