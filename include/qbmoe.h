@@ -418,7 +418,8 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *     a[t][i] = SiTU-GLU(x[t] w_gate[e]^T, x[t] w_up[e]^T),  e = idx[t][i]
  *     z[t]    = sum_i w[t][i] a[t][i] w_out[e]^T
  *     y[t]    = round(z) (gamma NULL), or round((z r) gamma), r = 1 / sqrt(mean z^2 + rms_eps)
- *   with SiTU-GLU of moe_latent_forward.  x [T, L] as above, w_gate and w_up MXFP4
+ *   with SiTU-GLU of moe_latent_forward; beta1 and beta2 positive, beta1 beta2 at most 2^127,
+ *   rms_eps finite and not negative.  x [T, L] as above, w_gate and w_up MXFP4
  *   [E, M, L], w_out [E, L, M], y [T, L] QBMOE_BF16 (row stride ldy), gamma [L] fp32.
  *   T k at most QBMOE_MAX_ROUTES.  workspace: device, 256-byte aligned, >=
  *   qbmoe_mxfp4_experts_workspace_bytes(T, k, L, M) bytes.

@@ -7,6 +7,8 @@
 #include "mxfp4_stream.cuh"
 #include "pieces.cuh"
 
+#include <math.h>
+
 namespace {
 
 // act [R, M] from the slabs' parts [slabs, 2, R, M] of gate and up, for the routes that have an expert.
@@ -157,7 +159,8 @@ extern "C" int moe_mxfp4_experts(int T, int k, int E, int L, int M, int x_type, 
     if (T < 0 || k < 1 || k > QBMOE_MAX_TOPK || (long long)T * k > QBMOE_MAX_ROUTES || E < 1 || E > QBMOE_MAX_EXPERTS ||
         !depth_ok(L) || !depth_ok(M) || !rows_ok(L, x_type, ldx) || ldy < L)
         return QBMOE_EINVAL;
-    if (!(beta1 > 0.0f) || !(beta2 > 0.0f) || !(rms_eps >= 0.0f)) return QBMOE_EINVAL;
+    // (an activation is at most beta1 beta2, so that it is finite or NaN)
+    if (!(beta1 > 0.0f) || !(beta2 > 0.0f) || !(beta1 * beta2 <= 0x1p127f) || !(rms_eps >= 0.0f) || !isfinite(rms_eps)) return QBMOE_EINVAL;
     if (T == 0) return QBMOE_OK;
     if (!all_aligned16({x, gate_codes, gate_scales, up_codes, up_scales, out_codes, out_scales}) || !y || !at_bytes(y, 2) ||
         !idx || !at_bytes(idx, 4) || !w || !at_bytes(w, 4) || !at_bytes(gamma, 4) || (x_type == QBMOE_MXFP8 && !all_aligned16({x_scales})))

@@ -6,8 +6,6 @@ runs in libqbmoe's CUDA kernels.
 """
 from __future__ import annotations
 
-import math
-
 from . import (MATVEC_MAX_K, MAX_EXPERTS, MAX_ROUTES, MAX_ROWS, MAX_TOPK, QBMOE_BF16, QBMOE_F32, QBMOE_MXFP8,
                QbmoeError, _here, _p, _refuse, load_library)
 from .mxfp4 import Mxfp4, _groups, _row_stride, _small, _start
@@ -96,8 +94,8 @@ def mxfp4_experts(x, idx, w, gate: Mxfp4, up: Mxfp4, out: Mxfp4, gamma=None, eps
         _refuse(what, "w is contiguous fp32 [T, k]")
     if gamma is not None and (gamma.dtype is not torch.float32 or gamma.shape != (L,) or not gamma.is_contiguous()):
         _refuse(what, "gamma is contiguous fp32 [L]")
-    if not 0.0 <= eps < math.inf or not 0.0 < beta1 < math.inf or not 0.0 < beta2 < math.inf:
-        _refuse(what, "eps is not negative, beta1 and beta2 are positive")
+    if not 0.0 <= eps < 2.0 ** 128 or not 1e-45 < beta1 or not 1e-45 < beta2 or not beta1 * beta2 <= 2.0 ** 127:
+        _refuse(what, "eps is finite and not negative, beta1 and beta2 are positive, and beta1 beta2 is at most 2^127 (all of them as fp32)")
     g_at, u_at, o_at = _start(what, "gate", gate.codes), _start(what, "up", up.codes), _start(what, "out", out.codes)
     cur = _here(what, t, scales, idx, w, gate.codes, gate.scales, up.codes, up.scales, out.codes, out.scales, gamma)
     lib, dev = load_library(), t.device
