@@ -385,7 +385,8 @@ int moe_mxfp4_wgrad(int R, int E, int N, int K, const void* dy, long long lddy, 
  * stride), or dn where the types and strides agree.  dgamma [H] fp32, or NULL
  * (then no workspace is used).
  * workspace: device, 256-byte aligned, >= qbmoe_add_rmsnorm_workspace_bytes(T, H)
- * bytes.  Sums are fp32 in a fixed order: bit-reproducible.
+ * bytes.  Sums are fp32 in a fixed order: bit-reproducible.  Rows whose squares, or products with g, pass fp32's
+ * range or come near its least numbers are scaled by a power of two first; dn gamma itself is an fp32 number.
  *
  * 0 <= T <= QBMOE_MAX_ROWS, 1 <= H <= QBMOE_MAX_NORM, eps >= 0 and finite, row strides (ld*,
  * in elements) >= H.  Pointers are aligned to their element type only: rows whose bases and strides are
@@ -419,7 +420,7 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *     z[t]    = sum_i w[t][i] a[t][i] w_out[e]^T
  *     y[t]    = round(z) (gamma NULL), or round((z r) gamma), r = 1 / sqrt(mean z^2 + rms_eps)
  *   with SiTU-GLU of moe_latent_forward; beta1 and beta2 positive, beta1 beta2 at most 2^127,
- *   rms_eps finite and not negative.  x [T, L] as above, w_gate and w_up MXFP4
+ *   rms_eps finite and not negative; mean z^2 is an fp32 number.  x [T, L] as above, w_gate and w_up MXFP4
  *   [E, M, L], w_out [E, L, M], y [T, L] QBMOE_BF16 (row stride ldy), gamma [L] fp32.
  *   T k at most QBMOE_MAX_ROUTES.  workspace: device, 256-byte aligned, >=
  *   qbmoe_mxfp4_experts_workspace_bytes(T, k, L, M) bytes.

@@ -102,9 +102,52 @@ QB_DEV void row_sum(float (&s)[kSums], float* scratch /* [kSums][kNormThreads / 
     }
 }
 
-// 1 / sqrt of the mean square, correctly rounded operations: once a row.
-QB_DEV float inverse_rms(float squares, int H, float eps) {
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, (float)H), eps)));
+// The mean square, and 1 / sqrt of it, correctly rounded operations: once a row.
+QB_DEV float mean_square(float squares, int H, float eps) { return __fadd_rn(__fdiv_rn(squares, (float)H), eps); }
+QB_DEV float inverse_sqrt(float mean) { return __fdiv_rn(1.0f, __fsqrt_rn(mean)); }
+
+// Rows whose sum of squares left fp32's range or came near its least numbers take it again of elements times a
+// power of two, so that it lies between 2^-118 and 2^126.  The whole row decides alike, by the sum itself.  (The question
+// costs ordinary rows up to 2%: 16384 x 7168 bf16 173.2 us for 172.4 without it, the gradient 160.3 for 157.5.)
+struct Range {
+    float least, most;
+    QB_DEV bool holds(float squares) const { return squares >= least && squares <= most; }
+};
+constexpr float kLargest = 0x1.fffffep127f, kSmallMean = 0x1p-80f, kLargeMean = 0x1p60f;
+// most: of the mean square with eps.
+Range range_of(int H, float eps, float most) {
+    return {eps < kSmallMean ? kSmallMean * H : 0.0f, !(eps <= 0.5f * most) ? -1.0f : most < kLargest / 2 / H ? 0.5f * most * H : 0.5f * kLargest};
+}
+// 1 / rms as a product of two factors, in the order in which neither product leaves the range before its end.
+struct Factors {
+    float first, second;
+};
+template <typename F>
+QB_DEV Factors rescaled(float mean, int H, float eps, float* scratch, F squares) {
+    const float s = mean < kSmallMean ? 0x1p90f : mean <= kLargeMean ? 1.0f : 0x1p-72f;
+    float q[1] = {squares(s)};
+    row_sum<1>(q, scratch);
+    const float r = inverse_sqrt(mean_square(q[0], H, eps * s * s));
+    return s > 1.0f ? Factors{s, r} : Factors{r, s};
+}
+// v times its 1 / rms.
+template <int kItems>
+QB_DEV void normalise(float (&v)[kItems][8], int items, float mean, int H, float eps, float* scratch) {
+    const Factors f = rescaled(mean, H, eps, scratch, [&](float s) {
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (threadIdx.x + i * blockDim.x >= items) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q = fmaf(v[i][j] * s, v[i][j] * s, q);
+        }
+        return q;
+    });
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (threadIdx.x + i * blockDim.x < items) v[i][j] = v[i][j] * f.first * f.second;
 }
 
 struct NormArgs {
@@ -120,6 +163,7 @@ struct NormArgs {
     void* y;
     long long ldy;
     uint8_t *codes, *scales;
+    Range range;
 };
 
 // MXFP8 of a block whose 8 elements this thread holds; four neighbouring threads hold it.
@@ -200,7 +244,11 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm(const NormArgs a) 
         for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
     }
     row_sum<1>(ss, scratch);
-    const float r = inverse_rms(ss[0], a.H, a.eps);
+    float r = inverse_sqrt(mean_square(ss[0], a.H, a.eps));
+    if (!a.range.holds(ss[0])) {
+        normalise<kNormItems>(v, items, mean_square(ss[0], a.H, a.eps), a.H, a.eps, scratch);
+        r = 1.0f;
+    }
 #pragma unroll
     for (int i = 0; i < kNormItems; ++i) {
         const int at = threadIdx.x + i * blockDim.x;
@@ -298,7 +346,11 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
         bring(s);   // this thread has read its pieces
         if (++s == ring.stages) s = 0;
         row_sum<1>(ss, scratch);
-        const float r = inverse_rms(ss[0], a.H, a.eps);
+        float r = inverse_sqrt(mean_square(ss[0], a.H, a.eps));
+        if (!a.range.holds(ss[0])) {
+            normalise<kItems>(v, items, mean_square(ss[0], a.H, a.eps), a.H, a.eps, scratch);
+            r = 1.0f;
+        }
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
@@ -317,6 +369,25 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
     }
 }
 
+// Of a row's gradient out of range: 1 / rms as two factors, and the mean of g times the normed row.  `squares` and
+// `products` are the row's sums over this thread's pieces.
+struct GradFactors {
+    Factors f;
+    float whole, rest;   // 1 / rms itself, and 1, unless it passes the range
+    float mean;
+};
+template <typename F, typename P>
+QB_DEV GradFactors grad_rescaled(float mean, int H, float eps, float* scratch, F squares, P products) {
+    GradFactors g;
+    g.f = rescaled(mean, H, eps, scratch, squares);
+    float q[1] = {products(g.f)};
+    row_sum<1>(q, scratch);
+    g.mean = q[0] / (float)H;
+    const float whole = g.f.first * g.f.second;
+    g.whole = whole <= kLargest ? whole : g.f.first;
+    g.rest = whole <= kLargest ? 1.0f : g.f.second;
+    return g;
+}
 struct NormGradArgs {
     int T, H;
     const void* dn;
@@ -330,6 +401,9 @@ struct NormGradArgs {
     void* dx;
     long long lddx;
     float* parts;   // [gridDim.x, H] sums of dn total r, or NULL
+    Range range;
+    // Whether a row's gradient is formed of the sums at hand: the products' must be finite, too.
+    QB_DEV bool ordinary(const float (&s)[2]) const { return range.holds(s[0]) && fabsf(s[1]) <= kLargest; }
 };
 
 // Rows blockIdx.x * blockDim.y + threadIdx.y, + gridDim.x * blockDim.y, ...: the sums of
@@ -359,7 +433,51 @@ __global__ void __launch_bounds__(kNormThreads) k_add_rmsnorm_backward(const Nor
             for (int j = 0; j < 8; ++j) s[0] = fmaf(v[i][j], v[i][j], s[0]), s[1] = fmaf(d[i][j] * g[j], v[i][j], s[1]);
         }
         row_sum<2>(s, scratch);
-        const float r = inverse_rms(s[0], a.H, a.eps), c = s[1] / (float)a.H * r * r;
+        if (!a.ordinary(s)) {
+            // (the row is read again, so that the ordinary row's registers are its own)
+            const TD* dn = static_cast<const TD*>(a.dn) + t * a.lddn;
+            const TT* total = static_cast<const TT*>(a.total) + t * a.ldt;
+            const GradFactors f = grad_rescaled(mean_square(s[0], a.H, a.eps), a.H, a.eps, scratch, [&](float scale) {
+                float q = 0.0f;
+                for (int at = threadIdx.x; at < items; at += blockDim.x) {
+                    float x[8];
+                    load8<TT, kForm>(total, at, a.H, x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) q = fmaf(x[j] * scale, x[j] * scale, q);
+                }
+                return q;
+            }, [&](const Factors& f) {
+                float q = 0.0f;
+                for (int at = threadIdx.x; at < items; at += blockDim.x) {
+                    float y[8], x[8], g[8];
+                    load8<TD, kForm>(dn, at, a.H, y);
+                    load8<TT, kForm>(total, at, a.H, x);
+                    load8<float, kForm>(a.gamma, at, a.H, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) q = fmaf(y[j] * g[j], x[j] * f.first * f.second, q);
+                }
+                return q;
+            });
+#pragma unroll
+            for (int i = 0; i < kNormItems; ++i) {
+                const int at = threadIdx.x + i * blockDim.x;
+                if (at >= items) break;
+                float y[8], x[8], g[8], o[8] = {};
+                load8<TD, kForm>(dn, at, a.H, y);
+                load8<TT, kForm>(total, at, a.H, x);
+                load8<float, kForm>(a.gamma, at, a.H, g);
+                if (a.dtotal) load8<TT, kForm>(static_cast<const TT*>(a.dtotal) + t * a.lddt, at, a.H, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = x[j] * f.f.first * f.f.second;
+                    acc[i][j] = fmaf(y[j], n, acc[i][j]);
+                    o[j] += (y[j] * g[j] - n * f.mean) * f.whole * f.rest;
+                }
+                store8<TT, kForm>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+            }
+            continue;
+        }
+        const float r = inverse_sqrt(mean_square(s[0], a.H, a.eps)), c = s[1] / (float)a.H * r * r;
 #pragma unroll
         for (int i = 0; i < kNormItems; ++i) {
             const int at = threadIdx.x + i * blockDim.x;
@@ -441,22 +559,63 @@ __global__ void __launch_bounds__(kNormThreads, kItems == 2 ? 2 : 1) k_add_rmsno
             for (int j = 0; j < 8; ++j) sum[0] = fmaf(v[j], v[j], sum[0]), sum[1] = fmaf(d[j] * g[j], v[j], sum[1]);
         }
         row_sum<2>(sum, scratch);
-        const float r = inverse_rms(sum[0], a.H, a.eps), c = sum[1] / (float)a.H * r * r;
+        if (a.ordinary(sum)) {
+            const float r = inverse_sqrt(mean_square(sum[0], a.H, a.eps)), c = sum[1] / (float)a.H * r * r;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int at = threadIdx.x + i * blockDim.x;
-            if (at >= items) break;
-            float d[8], v[8], g[8], o[8] = {};
-            load8<TD, kVector>(dn, at, a.H, d);
-            load8<TT, kVector>(total, at, a.H, v);
-            gain8(gain, at, items, g);
-            if (a.dtotal) load8<TT, kVector>(dtotal, at, a.H, o);
+            for (int i = 0; i < kItems; ++i) {
+                const int at = threadIdx.x + i * blockDim.x;
+                if (at >= items) break;
+                float d[8], v[8], g[8], o[8] = {};
+                load8<TD, kVector>(dn, at, a.H, d);
+                load8<TT, kVector>(total, at, a.H, v);
+                gain8(gain, at, items, g);
+                if (a.dtotal) load8<TT, kVector>(dtotal, at, a.H, o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc[i][j] = fmaf(d[j], v[j] * r, acc[i][j]);
-                o[j] += (d[j] * g[j] - v[j] * c) * r;
+                for (int j = 0; j < 8; ++j) {
+                    acc[i][j] = fmaf(d[j], v[j] * r, acc[i][j]);
+                    o[j] += (d[j] * g[j] - v[j] * c) * r;
+                }
+                store8<TT, kVector>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
             }
-            store8<TT, kVector>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+        } else {
+            const GradFactors f = grad_rescaled(mean_square(sum[0], a.H, a.eps), a.H, a.eps, scratch, [&](float scale) {
+                float q = 0.0f;
+                for (int at = threadIdx.x; at < items; at += blockDim.x) {
+                    float v[8];
+                    load8<TT, kVector>(total, at, a.H, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) q = fmaf(v[j] * scale, v[j] * scale, q);
+                }
+                return q;
+            }, [&](const Factors& f) {
+                float q = 0.0f;
+                for (int at = threadIdx.x; at < items; at += blockDim.x) {
+                    float d[8], v[8], g[8];
+                    load8<TD, kVector>(dn, at, a.H, d);
+                    load8<TT, kVector>(total, at, a.H, v);
+                    gain8(gain, at, items, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) q = fmaf(d[j] * g[j], v[j] * f.first * f.second, q);
+                }
+                return q;
+            });
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int at = threadIdx.x + i * blockDim.x;
+                if (at >= items) break;
+                float d[8], v[8], g[8], o[8] = {};
+                load8<TD, kVector>(dn, at, a.H, d);
+                load8<TT, kVector>(total, at, a.H, v);
+                gain8(gain, at, items, g);
+                if (a.dtotal) load8<TT, kVector>(dtotal, at, a.H, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = v[j] * f.f.first * f.f.second;
+                    acc[i][j] = fmaf(d[j], n, acc[i][j]);
+                    o[j] += (d[j] * g[j] - n * f.mean) * f.whole * f.rest;
+                }
+                store8<TT, kVector>(static_cast<TT*>(a.dx) + t * a.lddx, at, a.H, o);
+            }
         }
         bring(s);   // this thread has read its pieces
         if (++s == ring.stages) s = 0;
@@ -594,7 +753,7 @@ extern "C" int moe_add_rmsnorm(int T, int H, int x_type, const void* x, long lon
     if (rc) return rc;
     const bool vec = H % 8 == 0 && vectors(x, ldx, x_type) && vectors(gamma, 0, QBMOE_F32) && vectors(y, y ? ldy : 0, y_type) &&
                      (!residual || (vectors(residual, ldr, res_type) && vectors(total, ldt, res_type)));
-    const NormArgs a{T, H, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, codes, scales};
+    const NormArgs a{T, H, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, codes, scales, range_of(H, eps, kLargest)};
     const dim3 block = row_block(H);
     const unsigned grid = (unsigned)(((long long)T + block.y - 1) / block.y);
     const RingShape rows = ring_of(T, H, H * (size_of(x_type) + (residual ? size_of(res_type) : 0)), 0, 3, vec && (x_type == QBMOE_BF16 || (residual && res_type == QBMOE_BF16)));
@@ -642,7 +801,7 @@ extern "C" int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* d
                      vectors(gamma, 0, QBMOE_F32) && vectors(dtotal, dtotal ? lddt : 0, total_type) &&
                      vectors(dx, lddx, total_type);
     float* parts = dgamma ? static_cast<float*>(workspace) : nullptr;
-    const NormGradArgs a{T, H, dn, lddn, total, ldt, gamma, eps, dtotal, lddt, dx, lddx, parts};
+    const NormGradArgs a{T, H, dn, lddn, total, ldt, gamma, eps, dtotal, lddt, dx, lddx, parts, range_of(H, eps, kLargeMean)};
     const dim3 block = row_block(H);
     const RingShape rows = ring_of(T, H, H * (size_of(dn_type) + size_of(total_type) * (dtotal ? 2 : 1)), H * 4, 2, vec && (dn_type == QBMOE_BF16 || total_type == QBMOE_BF16));
     const int grid = rows.use ? rows.grid : gain_parts(T, H);
