@@ -22,10 +22,11 @@ __global__ void __launch_bounds__(256) k_slab_sum(int slabs, int R, int N, int E
     }
 }
 
-// Scratch of a call: parts of the slabs; or the rows' pieces, their offsets and odd bytes.
+// Scratch of a call: parts of the slabs; or the rows' pieces, their offsets and odd bytes.  It is sized without E: pieces
+// that pay for as many experts as there are rows have their place, also where a call of fewer experts does without.
 constexpr long long kMostPieces = 1LL << 25;   // elements of x that are split: 143 MB of pieces
 struct MatvecScratch {
-    size_t parts = 0, offsets = 0, odd = 0, bytes = 0;
+    size_t offsets = 0, odd = 0, bytes = 0;
     bool pieces;
     MatvecScratch(int R, int N, int K) {
         pieces = qbh::pieces_ok(K) && slabs_of(K) == 1 && (long long)R * K <= kMostPieces &&

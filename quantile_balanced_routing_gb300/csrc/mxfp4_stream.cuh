@@ -702,9 +702,9 @@ int slabs_of(int K, int mode = kStore) {
     return (K / 32 + most - 1) / most;
 }
 
-// Calls f with the shape whose warps hold `per` blocks: the smallest of a few sizes (what is beyond a
-// warp's share is multiplied with zeros).  14 and 28 are K = 7 2^n; two tiles a unit halve what a
-// unit costs besides, where the registers allow them.
+// Calls f with the shape whose warps hold `per` blocks: the smallest of a few sizes (a warp with fewer leaves its loop
+// after its last pair of blocks; a block missing from that pair is multiplied as zeros).  14 and 28 are K = 7 2^n; two
+// tiles a unit halve what a unit costs besides, where the registers allow them.
 template <int kMode, typename F>
 int for_shape(bool boxes, int per, F f) {
     if constexpr (terms_of(kMode) == 2) {
@@ -755,10 +755,10 @@ int stream(StreamArgs a, const uint8_t* codes, const uint8_t* codes2, cudaStream
         const size_t fixed = S::fixed(a.E, kMode == kStore ? 0 : a.R);
         a.stages = (int)((kMaxDynamic - kSlack - fixed) / a.stage_bytes);
         if (a.stages > kMaxStages) a.stages = kMaxStages;
-        // Where groups take turns a stage belongs to one of them, and to one producer (their number being even):
+        // Where groups take turns (2, 4 or 8 of them) a stage belongs to one of them, and to one producer:
         // a warp that waits for a barrier's next phase has then seen the one before, which a parity
         // cannot tell from the one after.
-        if (a.groups > 1) a.stages -= a.stages % (a.groups * (1 + a.groups % 2) * S::kTiles / S::kStaged);
+        if (a.groups > 1) a.stages -= a.stages % (a.groups * S::kTiles / S::kStaged);
         const size_t smem = fixed + (size_t)a.stages * a.stage_bytes + kSlack;   // two stages or more, and over the 32 KB that hist takes
         long long units = 0x7fffffff;
         if (kMode == kStore && !a.offsets) units = (((long long)a.R + kCols - 1) / kCols) * ((a.N + rows - 1) / rows) * a.slabs;
