@@ -409,10 +409,12 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *   for moe_mxfp4_matmul (offsets [E + 1] or NULL; rows that no expert owns are not
  *   written), but x at its own precision: QBMOE_BF16 [R, K], row stride ldx, or
  *   QBMOE_MXFP8 (x the codes, x_scales the scales, ldx = K).  y [R, N] of y_type
- *   (QBMOE_BF16 or QBMOE_F32), row stride ldy.  Each expert's weights are read
- *   once per 8 of its rows, or 24 (below): meant for few rows an expert.
+ *   (QBMOE_BF16 or QBMOE_F32), row stride ldy.  Each expert's weights are read once per 8 of
+ *   its rows, in pieces (below) once per 2, 8, 16 or 24, as many as R / E asks for: meant for few rows
+ *   an expert.
  *   workspace: device, 256-byte aligned, >= qbmoe_mxfp4_matvec_workspace_bytes(R, N, K)
- *   bytes (0, and NULL allowed, for few rows and small weights up to K = 8192).
+ *   bytes (0, and NULL allowed, for few rows and small weights up to K = 8192; it does not know E and
+ *   holds what the largest would need).
  *
  * moe_mxfp4_experts: for T tokens with the experts idx [T, k] (an entry outside
  *   [0, E) stands for no route) and weights w [T, k] of moe_route_qb,
@@ -427,12 +429,12 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  *
  * Both take weights and MXFP8 rows as they are.  Small calls, and depths that are not multiples of 256 or
  * over 8192, take each block of 32 of a bf16 row as fp16 times a power of two: exact for elements
- * down to 2^-29 of the block's largest and within 2^-40 of it below; the SiTU-GLU's fp32 result as two such terms
+ * down to 2^-32 of the block's largest and within 2^-40 of it below; the SiTU-GLU's fp32 result as two such terms
  * (within 2^-22 of the value, or 2^-40 of the block's largest).  All others take bf16 rows, and the SiTU-GLU's result, as sums of eight MXFP4 rows:
  * within 2^-22 of a block's largest (bf16 elements down to 2^-14 of it are exact); rows with
  * infinities or blocks of magnitudes below 2^-100 are multiplied as they are, slowly, and
  * what is below 2^-121 in the SiTU-GLU's result is dropped.  Sums are fp32 in a
- * fixed order: bit-reproducible.  So are a block's products before the weights' scale: where they pass
+ * fixed order: bit-reproducible (in pieces the tensor cores cut partial sums off where fp32 addition would round).  So are a block's products before the weights' scale: where they pass
  * fp32's range the result is infinite.  A row's result does not depend on other rows' elements.
  * 0 <= R <= QBMOE_MAX_ROWS, 1 <= E <= QBMOE_MAX_EXPERTS, 1 <= k <= QBMOE_MAX_TOPK, N a
  * multiple of 8, K, L and M multiples of 32 and at most QBMOE_MATVEC_MAX_K, E N below 2^31.  Pointers

@@ -765,8 +765,9 @@ int piece_product(const PieceProduct& q, cudaStream_t s) {
     p.a2_codes = q.w2_codes;
     p.sums = q.y;
     p.sums_type = q.y_type;
-    // Row tile: the smallest that holds an average expert's pieces, 192 beyond (by 896 experts of 1024 x 3584, five
-    // rows an expert: 326 us with 64, 320 with 128, cold; the experts of 256 tokens 895 and 894).
+    // Row tile, of 2, 8, 16 or 24 rows: the smallest that holds the pieces of an average expert, those without rows among
+    // them, 192 beyond (by 896 experts of 1024 x 3584, five rows an expert: 294 us with 64, 296 with 128; the experts of
+    // 256 tokens 784 and 767).
     const int avg = (m.R + q.E - 1) / q.E;
     if (avg <= 16) return launch<16, true>(m, p, s);
     if (avg <= 64) return launch<64, true>(m, p, s);

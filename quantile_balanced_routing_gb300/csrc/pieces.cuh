@@ -9,7 +9,7 @@
 // (743 cycles a SM for a stage's bytes, 375 for its MMAs at 192).
 //
 // Measured (896 experts of 1024 x 3584, 4096 rows): split 26 us (67 MB of pieces to L2), product 255 us, the weights
-// at 6.8 TB/s; together 290 to 296, where the rows in registers (mxfp4_stream.cuh) take 408.  Experts of 256 tokens:
+// at 6.8 TB/s; together 290 to 296, where the rows in registers (mxfp4_stream.cuh) take 403.  Experts of 256 tokens:
 // split 31, gate and up 450 (6.7 TB/s), SiTU-GLU 21, down 256 (5.8 TB/s, with 59 MB of fp32 rows written), combine 11 to 20.
 #pragma once
 
@@ -20,10 +20,11 @@ namespace qbh {
 constexpr int kPieces = 8;
 
 // Whether pieces pay: by the elements of weights that products of eight rows at a time would read, n matrices
-// of `elements` each and once more per eight rows.  One row by 6144 x K = 7168 (50 M) takes 23 us as it is and
-// 26 in pieces, by 12288 (99 M) 29 and 27; 64 rows by 896 x 7168 (58 M) 25 and 23; 128 rows over 24 matrices of
-// 512 x 1024 (21 M) 17 and 20; the experts (3584 x 1024, three matrices) of a token's 4 routes (50 M) 43 and 46,
-// of 8 (99 M) 57 and 49, of 256 tokens' 16 (15 G) 1325 and 895 with a cold cache.
+// of `elements` each and once more per eight rows.  GPU time in us (a replayed graph, cold caches) as it is and in
+// pieces: one row by 6144 x K = 7168 (44 M) 24 and 22, by 12288 (88 M) 30 and 24; 64 rows by 896 x 7168 (58 M) 26
+// and 20; 128 rows over 24 matrices of 512 x 1024 (21 M) 18 and 16; the experts (3584 x 1024, three matrices) of a
+// token's 4 routes (44 M) 42 and 40, of 6 (66 M) 52 and 44, of 8 (99 M) 50 and 46, of 256 tokens' 16 (15 G) 1439 and 789.
+// Below the bound pieces would save about 2 us of GPU time for one or two launches and a scratch tensor more.
 inline bool pieces_pay(long long n, long long rows, long long elements) { return (n + rows / 8) * elements >= 1LL << 26; }
 inline bool pieces_ok(int K) { return K % 256 == 0; }   // whole words of scales for a warp
 inline size_t piece_code_bytes(long long rows, int K) { return align_up((size_t)rows * kPieces * (K / 2), 256); }

@@ -12,9 +12,9 @@
 // reduction.  Few rows, short rows and rows off 16-byte boundaries go through the kernels without a ring.
 //
 // Measured, 16384 x 7168 bf16 with residual: forward to MXFP8 and its values 173 us (6.1 TB/s, 90% of the copy rate; 238
-// without the ring), backward with dtotal 158 us (5.9 TB/s; 331, and 189 with the gain read from global memory).
+// without the ring), backward with dtotal 161 us (5.8 TB/s; 331, and 189 with the gain read from global memory).
 // HBM bounds both.  Rows of odd widths are read an element at a time and bound by issue: 16384 x 2021 bf16, 141 and
-// 176 us for a floor of 39.
+// 177 us for a floor of 39.
 #include "mxfp4.cuh"
 
 #include <cuda_fp16.h>
@@ -30,13 +30,13 @@ constexpr int kNormItems = 4;            // pieces of 8 elements a thread holds
 constexpr int kNormThreads = 512;        // most threads of a row
 constexpr int kRowWarps = 8;             // rows of a CTA when a warp holds a row
 constexpr int kGainParts = 608;          // most partial sums of the gain's gradient (twice as many CTAs of 64 threads:
-                                         // 16384 x 2021 bf16, 176 us, 289 with 608)
+                                         // 16384 x 2021 bf16, 177 us, 315 with 608)
 constexpr int kRingParts = 1520;         // with rows in a ring
 constexpr int kRingRow = 512;            // shortest row of a ring
 
 // How a piece of 8 elements lies in its row: together, read at once or one by one; or 32 elements apart, a warp's
 // pieces sharing 256 elements, so that the reads of a row off 16-byte boundaries are contiguous over the lanes
-// (16384 x 2021 bf16: 143 us, 176 one by one; 4096 x 7001 fp32 90).
+// (16384 x 2021 bf16: 141 us, 176 one by one; 4096 x 7001 fp32 88).
 enum { kOnes, kVector, kSpread };
 template <int kForm>
 QB_DEV int element(int i, int j) { return kForm == kSpread ? ((i & ~31) << 3) + 32 * j + (i & 31) : 8 * i + j; }
@@ -108,7 +108,8 @@ QB_DEV float inverse_sqrt(float mean) { return __fdiv_rn(1.0f, __fsqrt_rn(mean))
 
 // Rows whose sum of squares left fp32's range or came near its least numbers take it again of elements times a
 // power of two, so that it lies between 2^-118 and 2^126.  The whole row decides alike, by the sum itself.  (The question
-// costs ordinary rows up to 2%: 16384 x 7168 bf16 173.2 us for 172.4 without it, the gradient 160.3 for 157.5.)
+// costs ordinary rows 1 to 4%: 16384 x 7168 bf16 173.2 us for 172.4 without it, the gradient 160.3 for 157.5, 131072 x 512
+// 116.2 for 114.7 and 121.0 for 116.1.)
 struct Range {
     float least, most;
     QB_DEV bool holds(float squares) const { return squares >= least && squares <= most; }
@@ -668,13 +669,14 @@ int gain_parts(int T, int H) {
 
 // Whether the rows go through a ring, and its shape: up to rows of 8192 as many CTAs a SM as 64 registers a thread
 // and `least` rows (and the gain, where it is read twice a row) each in shared memory allow, one beyond.  Measured in us with
-// a ring and without, forward and backward, bf16 (floor: bytes at the copy rate):
-//   310 x 7168 (3)      10, 12    18, 27        65536 x 2048 (158)  170, 203   182, 379
-//   1000 x 7168 (8)     16, 23    25, 39        65536 x 1056 (81)   100, 139   137, 309
-//   8192 x 7168 (69)    80, 111   88, 135       65536 x 1024 (79)    94, 111   100, 129
-//   8192 x 3584 (35)    43, 57    55, 74        131072 x 512 (79)   115, 125   119, 139
-// and not better for 200000 x 256 (94, 125; 129, 121), nor for fp32 alone (8192 x 4096: 88, 86; 96, 88), whose 16-byte reads
-// meet in shared memory's banks, nor with two rows forward (fp32, 8192 x 7168: 154, 143).
+// a ring and without, forward and (with dtotal) backward, bf16, GPU time (floor: bytes at the copy rate):
+//   310 x 7168 (3)       8, 7     13, 21       65536 x 2048 (158)  178, 201   183, 322
+//   1000 x 7168 (8)     12, 12    19, 32       65536 x 1056 (81)   100, 137   138, 228
+//   8192 x 7168 (69)    79, 109   87, 177      65536 x 1024 (79)    92, 108    99, 165
+//   8192 x 3584 (35)    42, 55    53, 91       131072 x 512 (79)   116, 123   121, 178
+// Forward, a ring is no better for fp32 alone (8192 x 4096: 88, 83), whose 16-byte reads meet in shared memory's banks,
+// nor with two rows (fp32, 8192 x 7168: 154, 143).  What the rule leaves: 200000 x 256 (61: 100, 125; 133, 156), and fp32's
+// gradient (8192 x 4096: 97, 106).
 constexpr int kRingBytes = 224 * 1024;     // a SM's
 constexpr int kRingCta = 112 * 1024;
 constexpr int kWide = 8192;

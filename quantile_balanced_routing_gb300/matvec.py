@@ -31,9 +31,11 @@ def _input(what, x, K):
 def mxfp4_matvec(x, w: Mxfp4, offsets=None, out_dtype=None, stream=None):
     """y [R, N] = x w^T for few rows x and MXFP4 weights w [N, K].
 
-    x keeps its precision, where :func:`mxfp4_matmul` takes 4-bit rows: an :class:`Mxfp8`
+    x has 8 or 16 bits, where :func:`mxfp4_matmul` takes 4-bit rows: an :class:`Mxfp8`
     [R, K], or bf16 (rows may be strided).  y is bf16, or fp32 with out_dtype.  Meant for
-    few rows a matrix: its weights are read again for every 8 to 24 rows.
+    few rows a matrix: its weights are read again for every 2 to 24 rows.  Larger calls hold
+    bf16 elements within 2^-22 of the largest of their 32 neighbours, exactly down to 2^-14 of it,
+    smaller calls exactly down to 2^-32.
     Grouped: w [E, N, K] and offsets [E + 1] int32, the rows in expert order;
     rows that no expert owns are left unwritten."""
     import torch
@@ -69,7 +71,8 @@ def mxfp4_experts(x, idx, w, gate: Mxfp4, up: Mxfp4, out: Mxfp4, gamma=None, eps
     index outside [0, E) stands for no route.  gate and up MXFP4 [E, M, L], out [E, L, M].
     Each route's SiTU-GLU(x gate^T, x up^T) goes through out; a token's routes are
     summed by weight, and with gamma [L] fp32 the sum is RMS-normed and scaled: the routed
-    part of :class:`LatentMoE`, with fp32 between its steps.  T k is at most 4096."""
+    part of :class:`LatentMoE`, with fp32 between its steps, of which the down product takes
+    22 bits.  T k is at most 4096."""
     import torch
     if stream is not None:
         with torch.cuda.stream(stream):
