@@ -175,7 +175,8 @@ def test_small_products_hold_elements_down_to_2_32_of_the_largest(loads, N, K):
 
 SIZES = [(1, 1, 1, 32, 32), (1, 16, 40, 512, 256), (5, 2, 3, 96, 64), (9, 4, 2, 1056, 96), (23, 3, 5, 64, 544), (30, 8, 12, 1056, 32),
          (1, 4, 6, 3584, 1024), (3, 2, 4, 64, 8224), (1, 2, 3, 8256, 64), (128, 32, 40, 64, 96), (100, 8, 16, 768, 512),
-         (33, 16, 20, 1024, 768), (2, 16, 16, 2048, 1024), (260, 4, 7, 512, 512)]
+         (33, 16, 20, 1024, 768), (2, 16, 16, 2048, 1024), (260, 4, 7, 512, 512), (2, 2, 3, 64, 2048), (9, 3, 4, 96, 1600), (2, 1, 2, 32, 2080),
+         (11, 3, 3, 64, 320), (3, 2, 2, 32, 4096)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp8"])
