@@ -430,12 +430,13 @@ int moe_add_rmsnorm_backward(int T, int H, int dn_type, const void* dn, long lon
  * Both take weights and MXFP8 rows as they are.  Small calls, and depths that are not multiples of 256 or
  * over 8192, take each block of 32 of a bf16 row as fp16 times a power of two: exact for elements
  * down to 2^-32 of the block's largest and within 2^-40 of it below; the SiTU-GLU's fp32 result as two such terms
- * (within 2^-22 of the value, or 2^-40 of the block's largest).  All others take bf16 rows, and the SiTU-GLU's result, as sums of eight MXFP4 rows:
+ * (within 2^-22 of the value, or 2^-40 of the block's largest).  All others take bf16 rows, and the SiTU-GLU's
+ * result, as sums of eight MXFP4 rows:
  * within 2^-22 of a block's largest (bf16 elements down to 2^-14 of it are exact); rows with
  * infinities or blocks of magnitudes below 2^-100 are multiplied as they are, slowly, and
  * what is below 2^-121 in the SiTU-GLU's result is dropped.  Sums are fp32 in a
- * fixed order: bit-reproducible (in pieces the tensor cores cut partial sums off where fp32 addition would round).  So are a block's products before the weights' scale: where they pass
- * fp32's range the result is infinite.  A row's result does not depend on other rows' elements.
+ * fixed order: bit-reproducible (in pieces the tensor cores cut partial sums off where fp32 addition would
+ * round).  So are a block's products before the weights' scale: where they pass fp32's range the result is infinite.  A row's result does not depend on other rows' elements.
  * 0 <= R <= QBMOE_MAX_ROWS, 1 <= E <= QBMOE_MAX_EXPERTS, 1 <= k <= QBMOE_MAX_TOPK, N a
  * multiple of 8, K, L and M multiples of 32 and at most QBMOE_MATVEC_MAX_K, E N below 2^31.  Pointers
  * 16-byte aligned (idx, w and gamma: 4), ldx a multiple of 8 elements; y aligned to its type.

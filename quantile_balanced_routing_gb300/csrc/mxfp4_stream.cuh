@@ -2,7 +2,8 @@
 // and for depths that pieces.cuh does not take.
 //
 // One kernel brings weights through shared memory and multiplies them with a few rows that
-// stay in registers (more than fit: with over 8 blocks a warp its variants store 12 to 280 bytes a thread on the stack).  A persistent CTA a SM takes a contiguous run of units; a unit is kMT
+// stay in registers (more than fit: with over 8 blocks a warp its variants store 12 to 280 bytes a thread on the
+// stack).  A persistent CTA a SM takes a contiguous run of units; a unit is kMT
 // tiles of 16 weight rows over the whole depth (or one slab of it).  Eight consumer warps of 168 registers
 // form groups that take units in turn, so that one group's fixed work per unit falls into another's products
 // (sixteen warps of 96 registers, one tile a unit: 413 against 408 us by 896 experts of 1024 x 3584, and 4096 rows'
@@ -23,7 +24,8 @@
 //
 // Measured (GPU time, cold caches): one row by 6144 x 7168 24 us (the weights alone take 3.5; 19 with part of them in
 // L2), by 12288 x 7168 30; 13 rows by 896 x 7168 16, 10 from L2 for a floor of 0.5: route lists and barriers, rows to
-// registers and code fetched cold come before the first product.  A large call spends 74 cycles a scheduler on a block and tile (the products' own
+// registers and code fetched cold come before the first product.  A large call spends 74 cycles a scheduler on a block
+// and tile (the products' own
 // instructions take 35, HBM 46): waits, sums and scales of each unit; pieces.cuh has those.
 #pragma once
 
